@@ -363,6 +363,161 @@ int pml_fp8_paged_mqa_logits_noalloc(const uint8_t* q, const uint8_t* kv_fused,
 /* Largest num_ctas pml_fp8_paged_mqa_logits_noalloc accepts (1024). */
 int pml_noalloc_max_ctas(void);
 
+/* ------------------------------------------------------------------------
+ * Serving operators: what feeds the logits above and what reads the positions
+ * they select.  All of them work on pages of 64 tokens: token position p of a
+ * request is slot p % 64 of page block_table[request * bt_stride + p / 64].
+ * ------------------------------------------------------------------------ */
+
+#define PML_DTYPE_FLOAT16 2   /* element type of the serving operators only */
+
+#define PML_STATUS_NO_PAGES 16u  /* pml_pages_fork / _extend: the pool ran out of free pages */
+
+/*
+ * pml_rope -- rotary positions, and their gradient.
+ *
+ *   (a, b) -> mscale * (a cos t - b sin t, b cos t + a sin t),
+ *   t = positions[token] * inv_freq[j]
+ *
+ * for the rot_dim / 2 pairs j of every head: elements rot_offset + j and
+ * rot_offset + rot_dim/2 + j, or (interleaved != 0) rot_offset + 2j and
+ * rot_offset + 2j + 1.  A head's other elements are copied.  gradient != 0
+ * applies the transposed map (t negated): it takes the gradient of the
+ * output to that of the input.  The angle is reduced exactly at any position
+ * (64-bit fixed point); arithmetic is fp32, rounded once.
+ *
+ * x, out      dtype PML_DTYPE_FLOAT32, _BFLOAT16 or _FLOAT16; element (token,
+ *             head, d) at token * token_stride + head * head_stride + d
+ *             (strides in elements, any value; 16-byte aligned pointers and
+ *             strides are fastest).  out may be x with the same strides;
+ *             other overlaps are not allowed
+ * positions   [tokens] int32, or int64 (positions_64 != 0); any sign
+ * inv_freq    [rot_dim/2] fp32, or fp64 (freq_64 != 0), radians per position
+ *             (long-context scalings are choices of inv_freq and mscale);
+ *             infinities, NaN and subnormals count as 0
+ * rot_dim     even, 0 .. head_dim - rot_offset;  head_dim  1 .. 512
+ */
+int pml_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, void* out,
+             int64_t out_token_stride, int64_t out_head_stride, int dtype, const void* positions,
+             int positions_64, const void* inv_freq, int freq_64, int rot_dim, int rot_offset,
+             int interleaved, float mscale, int gradient, int tokens, int heads, int head_dim,
+             void* stream);
+
+/*
+ * pml_rope_append -- a step's q, k and v on their way into attention: q
+ * rotated into q_out, k rotated and v copied into the pages of their caches,
+ * one launch.  The rotation is pml_rope's.
+ *
+ * q, q_out    [tokens, num_heads, head_dim] (num_heads may be 0); k, v
+ *             [tokens, kv_heads, head_dim]: bf16 or fp16 with strides in
+ *             elements as in pml_rope; q_out may be q
+ * k_cache     element (page, slot, head, d) at page * k_page_stride + slot *
+ *             k_slot_stride + head * k_cache_head_stride + d; v_cache alike
+ * requests    int32 [tokens], the token's block-table row.  A negative
+ *             request or position makes the token padding: nothing of it is
+ *             written.  A request at or past num_requests sets
+ *             PML_STATUS_BAD_REQUEST, a position at or past 64 * bt_width or
+ *             a page outside [0, num_pages) PML_STATUS_BAD_BLOCK; that
+ *             token's k and v are then not written
+ * Two tokens of a call must not share a slot.
+ */
+int pml_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, void* q_out,
+                    int64_t q_out_token_stride, int64_t q_out_head_stride, const void* k,
+                    int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                    int64_t v_token_stride, int64_t v_head_stride, int dtype, const void* positions,
+                    int positions_64, const int32_t* requests, int num_requests,
+                    const void* inv_freq, int freq_64, int rot_dim, int rot_offset, int interleaved,
+                    float mscale, void* k_cache, int64_t k_page_stride, int64_t k_slot_stride,
+                    int64_t k_cache_head_stride, void* v_cache, int64_t v_page_stride,
+                    int64_t v_slot_stride, int64_t v_cache_head_stride, int64_t num_pages,
+                    const int32_t* block_table, int64_t bt_stride, int bt_width, int tokens,
+                    int num_heads, int kv_heads, int head_dim, void* stream);
+
+/*
+ * pml_index_quant_append -- the inputs of pml_fp8_paged_mqa_logits from a
+ * step's bf16 rows: r = rotated row, s = max(max |r|, 1e-12) / 448, codes
+ * e4m3(r / s).  A q row's scale goes into its weight, w_out = weights * s *
+ * weight_scale; a key's codes and scale go into its kv_fused block.
+ *
+ * q           bf16 [tokens, num_heads, 128], strides in elements, multiples of
+ *             8, 16-byte aligned; k bf16 [tokens, 128] alike, or NULL (no
+ *             keys are written; requests and kv_fused are not read)
+ * weights     fp32 [tokens, num_heads], contiguous; w_out alike
+ * q_out       e4m3 [tokens, num_heads, 128], contiguous, 16-byte aligned
+ * kv_fused    [num_blocks][8448] as pml_fp8_paged_mqa_logits takes it
+ * rot_dim a multiple of 16, rot_offset of 8; num_heads 1 .. 1024; padding
+ * tokens and bad requests and pages as in pml_rope_append.  A NaN in a row
+ * makes its scale NaN, an infinity makes it infinite (the row's codes are
+ * then 0 or NaN).
+ */
+int pml_index_quant_append(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                           const void* k, int64_t k_token_stride, const float* weights,
+                           float weight_scale, const void* positions, int positions_64,
+                           const int32_t* requests, int num_requests, const void* inv_freq,
+                           int freq_64, int rot_dim, int rot_offset, int interleaved, float mscale,
+                           uint8_t* q_out, float* w_out, uint8_t* kv_fused, int64_t num_blocks,
+                           const int32_t* block_table, int64_t bt_stride, int bt_width, int tokens,
+                           int num_heads, void* stream);
+
+/*
+ * Page bookkeeping.  A pool is ref_counts [num_pages] (how many requests hold
+ * each page; 0: free), block_table [rows, bt_stride] of which bt_width columns
+ * are used, and seq_lens [rows]; a row's first ceil(seq_lens / 64) entries are
+ * its pages.  Pages are taken lowest number first, so results depend on the
+ * pool alone.  All arrays are device int32; rows * (bt_width + 1) < 2^31.
+ *
+ * pml_pages_fork: for i < n, row children[i] becomes a copy of row
+ * parents[i]: full pages are shared (their count rises), a last page that is
+ * part full is replaced by a free page, and (its page, the new page) is added
+ * to copy_src / copy_dst (n entries each, in order of i, -1 past
+ * *copy_count) for pml_pages_copy.  Forks are served in order; one that finds
+ * no free page leaves the child with length 0 and sets PML_STATUS_NO_PAGES.
+ * A row is not both a parent and a child of one call nor twice a child, and a
+ * child holds no pages (free it first).  Rows outside [0, rows) or longer
+ * than the table set PML_STATUS_BAD_REQUEST and are skipped.
+ *
+ * pml_pages_extend: grows every row to new_lens[row] tokens, taking pages in
+ * (row, page) order; shorter lengths change nothing.  A row whose pages are
+ * not all there keeps its length, as does every later row that needs one
+ * (PML_STATUS_NO_PAGES); a length past the table's width is refused
+ * (PML_STATUS_BAD_BLOCK).  new_pages [capacity] receives the pages taken, -1
+ * past *new_count; at most `capacity` pages are taken.
+ *
+ * pml_pages_free: the rows in list (distinct) give back their pages and get
+ * length 0; their table entries stay.
+ *
+ * pml_pages_compact: the L live pages move to numbers 0 .. L-1: the live pages
+ * at or past L, ascending, to the free ones below it, ascending.  remap
+ * [num_pages] says where each page went (-1: it was free), copy_src /
+ * copy_dst [capacity >= num_pages / 2] list the moves for pml_pages_copy, -1
+ * past *copy_count; ref_counts_out and block_table_out (which may be the
+ * inputs) are the new state, entries past a row's length copied as they are.
+ *
+ * pml_pages_copy: for i < min(*copy_count, capacity), page copy_src[i] of
+ * every layer is copied over page copy_dst[i]; layer l, page p starts at byte
+ * l * layer_stride_bytes + p * page_stride_bytes.  No page is a source and a
+ * target of one call, nor a target twice.  Page numbers outside the cache are
+ * skipped (PML_STATUS_BAD_BLOCK).
+ */
+int pml_pages_fork(int32_t* ref_counts, int num_pages, int32_t* block_table, int64_t bt_stride,
+                   int bt_width, int32_t* seq_lens, int rows, const int32_t* parents,
+                   const int32_t* children, int n, int32_t* copy_src, int32_t* copy_dst,
+                   int32_t* copy_count, void* stream);
+int pml_pages_extend(int32_t* ref_counts, int num_pages, int32_t* block_table, int64_t bt_stride,
+                     int bt_width, int32_t* seq_lens, int rows, const int32_t* new_lens,
+                     int32_t* new_pages, int capacity, int32_t* new_count, void* stream);
+int pml_pages_free(int32_t* ref_counts, int num_pages, int32_t* block_table, int64_t bt_stride,
+                   int bt_width, int32_t* seq_lens, int rows, const int32_t* list, int n,
+                   void* stream);
+int pml_pages_compact(int32_t* ref_counts, int num_pages, int32_t* block_table, int64_t bt_stride,
+                      int bt_width, const int32_t* seq_lens, int rows, int32_t* ref_counts_out,
+                      int32_t* block_table_out, int64_t bt_out_stride, int32_t* remap,
+                      int32_t* copy_src, int32_t* copy_dst, int capacity, int32_t* copy_count,
+                      void* stream);
+int pml_pages_copy(void* cache, int layers, int64_t layer_stride_bytes, int num_pages,
+                   int64_t page_stride_bytes, int64_t page_bytes, const int32_t* copy_src,
+                   const int32_t* copy_dst, const int32_t* copy_count, int capacity, void* stream);
+
 /* Read (and, if clear != 0, reset) the current device's sticky status word.
  * Synchronises with the device (waits for all work queued so far). */
 int pml_device_status(unsigned int* status, int clear);

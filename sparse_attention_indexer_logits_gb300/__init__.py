@@ -40,6 +40,8 @@ __all__ = [
     "pml_fp8_paged_mqa_logits_noalloc", "pml_fp8_paged_mqa_logits_wait_test",
     "pml_device_status",
     "pml_default_num_ctas", "pml_min_block_table_width", "pml_padded_seq_len", "pml_schedule_meta_elems",
+    "pml_rope", "pml_rope_append", "pml_index_quant_append", "pml_pages_fork", "pml_pages_extend",
+    "pml_pages_free", "pml_pages_compact", "pml_pages_copy",
     "fp8_paged_mqa_logits", "indexer_scores", "compute_paged_mqa_logits_schedule",
 ]
 
@@ -50,6 +52,7 @@ _lib = None
 STATUS_WAIT_TIMEOUT = 1
 STATUS_BAD_BLOCK = 2
 STATUS_BAD_REQUEST = 4
+STATUS_NO_PAGES = 16
 
 
 class PmlError(RuntimeError):
@@ -107,6 +110,24 @@ def lib() -> ctypes.CDLL:
                                                        i32, i32, i32, P]
         L.pml_fp8_paged_mqa_logits_noalloc.restype = i32
         L.pml_noalloc_max_ctas.restype = i32
+        f32 = ctypes.c_float
+        pool = [P, i32, P, i64, i32, P, i32]
+        for name, types in {
+            "pml_rope": [P, i64, i64, P, i64, i64, i32, P, i32, P, i32, i32, i32, i32, f32, i32, i32,
+                         i32, i32, P],
+            "pml_rope_append": [P, i64, i64, P, i64, i64, P, i64, i64, P, i64, i64, i32, P, i32, P,
+                                i32, P, i32, i32, i32, i32, f32, P, i64, i64, i64, P, i64, i64, i64,
+                                i64, P, i64, i32, i32, i32, i32, i32, P],
+            "pml_index_quant_append": [P, i64, i64, P, i64, P, f32, P, i32, P, i32, P, i32, i32, i32,
+                                       i32, f32, P, P, P, i64, P, i64, i32, i32, i32, P],
+            "pml_pages_fork": pool + [P, P, i32, P, P, P, P],
+            "pml_pages_extend": pool + [P, P, i32, P, P],
+            "pml_pages_free": pool + [P, i32, P],
+            "pml_pages_compact": pool + [P, P, i64, P, P, P, i32, P, P],
+            "pml_pages_copy": [P, i32, i64, i32, i64, i64, P, P, P, i32, P],
+        }.items():
+            getattr(L, name).argtypes = types
+            getattr(L, name).restype = i32
         L.pml_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint), i32]
         L.pml_device_status.restype = i32
         _lib = L
@@ -416,6 +437,276 @@ def pml_fp8_paged_mqa_logits_noalloc(q: torch.Tensor, kv_fused: torch.Tensor,
         _ptr(block_table), block_table.stride(0), num_ctas, _ptr(out), out.stride(0), max_context,
         batch, next_n, q.shape[1], _stream(stream)), "pml_fp8_paged_mqa_logits_noalloc")
     return out
+
+
+# ---------------------------------------------------------------- serving operators
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_IS64 = {torch.int32: 0, torch.int64: 1, torch.float32: 0, torch.float64: 1}
+
+
+def _serving(name: str, *args, stream=None):
+    s = torch.cuda.current_stream() if stream is None else stream
+    rc = getattr(lib(), name)(*args, s.cuda_stream)
+    if rc != 0:
+        raise PmlError(rc, name)
+
+
+def _addr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+def _heads(t: torch.Tensor, name: str, dtype=None):
+    """Checks a ``[tokens, heads, dim]`` tensor with unit last stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
+        raise ValueError(f"{name} must be [tokens, heads, dim] with unit last stride")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}")
+
+
+def _ints(t: torch.Tensor, name: str, count: int | None = None):
+    if not t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA int32 tensor")
+    if count is not None and t.numel() != count:
+        raise ValueError(f"{name} must hold {count} values")
+
+
+def _rotation(positions: torch.Tensor, inv_freq: torch.Tensor, tokens: int):
+    if not positions.is_cuda or positions.dtype not in (torch.int32, torch.int64):
+        raise ValueError("positions must be a CUDA int32 or int64 tensor")
+    if not inv_freq.is_cuda or inv_freq.dtype not in (torch.float32, torch.float64):
+        raise ValueError("inv_freq must be a CUDA float32 or float64 tensor")
+    if not positions.is_contiguous() or not inv_freq.is_contiguous():
+        raise ValueError("positions and inv_freq must be contiguous")
+    if positions.numel() != tokens:
+        raise ValueError("positions must hold one value per token")
+    return _IS64[positions.dtype], _IS64[inv_freq.dtype], 2 * inv_freq.numel()
+
+
+def _table(t: torch.Tensor, name: str = "block_table"):
+    if not t.is_cuda or t.dtype != torch.int32 or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{name} must be a CUDA int32 [rows, width] tensor with unit last stride")
+
+
+def _cache(t: torch.Tensor, name: str, like: torch.Tensor):
+    if not t.is_cuda or t.dim() != 4 or t.shape[1] != 64 or (t.stride(3) != 1 and t.shape[3] > 1):
+        raise ValueError(f"{name} must be a CUDA [pages, 64, heads, dim] tensor with unit last stride")
+    if t.dtype != like.dtype:
+        raise ValueError(f"{name} must be {like.dtype}")
+
+
+def pml_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
+             out: torch.Tensor | None = None, rot_offset: int = 0, interleaved: bool = False,
+             mscale: float = 1.0, gradient: bool = False, stream=None) -> torch.Tensor:
+    """Rotary positions of ``x`` ``[tokens, heads, dim]`` (fp32, bf16 or fp16;
+    any token and head strides): pair ``j`` turned by ``positions[token] *
+    inv_freq[j]`` and multiplied by ``mscale``.
+
+    ``inv_freq`` (fp32 or fp64, ``rot_dim / 2`` values) says how much of each
+    head is rotated, from element ``rot_offset`` on; pairs are ``(j, rot_dim/2
+    + j)``, or ``(2j, 2j+1)`` when ``interleaved``.  ``gradient=True`` takes
+    the output's gradient to the input's.  ``out`` may be ``x``."""
+    _heads(x, "x")
+    if x.dtype not in _DTYPES:
+        raise ValueError("x must be float32, bfloat16 or float16")
+    tokens, heads, dim = x.shape
+    p64, f64, rot = _rotation(positions, inv_freq, tokens)
+    if out is None:
+        out = torch.empty((tokens, heads, dim), dtype=x.dtype, device=x.device)
+    else:
+        _heads(out, "out", x.dtype)
+        if out.shape != x.shape:
+            raise ValueError("out must have x's shape")
+    _serving("pml_rope", x.data_ptr(), x.stride(0), x.stride(1), out.data_ptr(), out.stride(0),
+             out.stride(1), _DTYPES[x.dtype], positions.data_ptr(), p64, inv_freq.data_ptr(), f64,
+             rot, rot_offset, int(interleaved), mscale, int(gradient), tokens, heads, dim,
+             stream=stream)
+    return out
+
+
+def pml_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                    requests: torch.Tensor, inv_freq: torch.Tensor, k_cache: torch.Tensor,
+                    v_cache: torch.Tensor, block_table: torch.Tensor,
+                    q_out: torch.Tensor | None = None, rot_offset: int = 0,
+                    interleaved: bool = False, mscale: float = 1.0, stream=None) -> torch.Tensor:
+    """q rotated into ``q_out`` (returned), k rotated and v copied into slot
+    ``positions[t] % 64`` of page ``block_table[requests[t], positions[t] // 64]``
+    of their caches ``[pages, 64, kv_heads, dim]`` (any strides).  bf16 or
+    fp16; a negative request or position makes the token padding."""
+    _heads(q, "q")
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("q must be bfloat16 or float16")
+    _heads(k, "k", q.dtype)
+    _heads(v, "v", q.dtype)
+    tokens, heads, dim = q.shape
+    kv_heads = k.shape[1]
+    if k.shape != (tokens, kv_heads, dim) or v.shape != k.shape:
+        raise ValueError("k and v must be [tokens, kv_heads, dim] with q's tokens and dim")
+    p64, f64, rot = _rotation(positions, inv_freq, tokens)
+    _ints(requests, "requests", tokens)
+    _table(block_table)
+    _cache(k_cache, "k_cache", q)
+    _cache(v_cache, "v_cache", q)
+    if k_cache.shape != v_cache.shape or k_cache.shape[2:] != k.shape[1:]:
+        raise ValueError("k_cache and v_cache must be [pages, 64, kv_heads, dim]")
+    if q_out is None:
+        q_out = torch.empty((tokens, heads, dim), dtype=q.dtype, device=q.device)
+    else:
+        _heads(q_out, "q_out", q.dtype)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+    _serving("pml_rope_append", q.data_ptr(), q.stride(0), q.stride(1), q_out.data_ptr(),
+             q_out.stride(0), q_out.stride(1), k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(),
+             v.stride(0), v.stride(1), _DTYPES[q.dtype], positions.data_ptr(), p64,
+             requests.data_ptr(), block_table.shape[0], inv_freq.data_ptr(), f64, rot, rot_offset,
+             int(interleaved), mscale, k_cache.data_ptr(), k_cache.stride(0), k_cache.stride(1),
+             k_cache.stride(2), v_cache.data_ptr(), v_cache.stride(0), v_cache.stride(1),
+             v_cache.stride(2), k_cache.shape[0], block_table.data_ptr(), block_table.stride(0),
+             block_table.shape[1], tokens, heads, kv_heads, dim, stream=stream)
+    return q_out
+
+
+def pml_index_quant_append(q: torch.Tensor, k: torch.Tensor | None, weights: torch.Tensor,
+                           positions: torch.Tensor, requests: torch.Tensor | None,
+                           inv_freq: torch.Tensor, kv_fused: torch.Tensor | None,
+                           block_table: torch.Tensor | None, q_out: torch.Tensor | None = None,
+                           w_out: torch.Tensor | None = None, weight_scale: float = 1.0,
+                           rot_offset: int = 0, interleaved: bool = False, mscale: float = 1.0,
+                           stream=None):
+    """The inputs of ``pml_fp8_paged_mqa_logits``: q bf16 ``[tokens, heads,
+    128]`` rotated and quantised to e4m3 ``q_out``, its scales folded into
+    ``w_out = weights * scale * weight_scale``; k bf16 ``[tokens, 128]``
+    rotated, quantised and written with its scale into ``kv_fused`` uint8
+    ``[blocks, 8448]`` (``k=None``: no keys).  Returns ``(q_out, w_out)``."""
+    _heads(q, "q", torch.bfloat16)
+    tokens, heads, dim = q.shape
+    if dim != 128:
+        raise ValueError("q must be bf16 [tokens, heads, 128]")
+    p64, f64, rot = _rotation(positions, inv_freq, tokens)
+    if weights.dtype != torch.float32 or weights.shape != (tokens, heads):
+        raise ValueError("weights must be float32 [tokens, heads]")
+    _cuda(weights, "weights")
+    blocks = rows = width = stride = k_stride = 0
+    if k is not None:
+        if not k.is_cuda or k.dtype != torch.bfloat16 or k.shape != (tokens, 128) or k.stride(1) != 1:
+            raise ValueError("k must be a CUDA bf16 [tokens, 128] tensor with unit last stride")
+        if requests is None or kv_fused is None or block_table is None:
+            raise ValueError("keys need requests, kv_fused and block_table")
+        _ints(requests, "requests", tokens)
+        _table(block_table)
+        _cuda(kv_fused, "kv_fused")
+        if kv_fused.dtype != torch.uint8 or kv_fused.numel() % 8448 != 0:
+            raise ValueError("kv_fused must be uint8 and hold whole 8448-byte blocks")
+        blocks, k_stride = kv_fused.numel() // 8448, k.stride(0)
+        rows, width, stride = block_table.shape[0], block_table.shape[1], block_table.stride(0)
+    if q_out is None:
+        q_out = torch.empty((tokens, heads, 128), dtype=torch.float8_e4m3fn, device=q.device)
+    if w_out is None:
+        w_out = torch.empty((tokens, heads), dtype=torch.float32, device=q.device)
+    if q_out.shape != q.shape or q_out.element_size() != 1 or w_out.shape != weights.shape or \
+            w_out.dtype != torch.float32:
+        raise ValueError("q_out must be 1-byte [tokens, heads, 128], w_out float32 [tokens, heads]")
+    _cuda(q_out, "q_out")
+    _cuda(w_out, "w_out")
+    _serving("pml_index_quant_append", q.data_ptr(), q.stride(0), q.stride(1), _addr(k), k_stride,
+             weights.data_ptr(), weight_scale, positions.data_ptr(), p64, _addr(requests), rows,
+             inv_freq.data_ptr(), f64, rot, rot_offset, int(interleaved), mscale, q_out.data_ptr(),
+             w_out.data_ptr(), _addr(kv_fused), blocks, _addr(block_table), stride, width, tokens,
+             heads, stream=stream)
+    return q_out, w_out
+
+
+def _pool(ref_counts, block_table, seq_lens):
+    _ints(ref_counts, "ref_counts")
+    _table(block_table)
+    _ints(seq_lens, "seq_lens", block_table.shape[0])
+    return (ref_counts.data_ptr(), ref_counts.numel(), block_table.data_ptr(), block_table.stride(0),
+            block_table.shape[1], seq_lens.data_ptr(), block_table.shape[0])
+
+
+def pml_pages_fork(ref_counts: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                   parents: torch.Tensor, children: torch.Tensor, copy_src: torch.Tensor,
+                   copy_dst: torch.Tensor, copy_count: torch.Tensor, stream=None) -> None:
+    """Rows ``children`` become copies of rows ``parents``: full pages shared,
+    a part-full last page replaced by the lowest free page and listed in
+    ``copy_src`` / ``copy_dst`` / ``copy_count`` for ``pml_pages_copy``.  All
+    int32, updated in place."""
+    pool = _pool(ref_counts, block_table, seq_lens)
+    n = parents.numel()
+    _ints(parents, "parents")
+    for t, nm in ((children, "children"), (copy_src, "copy_src"), (copy_dst, "copy_dst")):
+        _ints(t, nm, n)
+    _ints(copy_count, "copy_count", 1)
+    _serving("pml_pages_fork", *pool, parents.data_ptr(), children.data_ptr(), n,
+             copy_src.data_ptr(), copy_dst.data_ptr(), copy_count.data_ptr(), stream=stream)
+
+
+def pml_pages_extend(ref_counts: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                     new_lens: torch.Tensor, new_pages: torch.Tensor, new_count: torch.Tensor,
+                     stream=None) -> None:
+    """Grows every row to ``new_lens`` tokens with the lowest free pages, in
+    (row, page) order; the pages taken are listed in ``new_pages``."""
+    pool = _pool(ref_counts, block_table, seq_lens)
+    _ints(new_lens, "new_lens", seq_lens.numel())
+    _ints(new_pages, "new_pages")
+    _ints(new_count, "new_count", 1)
+    _serving("pml_pages_extend", *pool, new_lens.data_ptr(), new_pages.data_ptr(),
+             new_pages.numel(), new_count.data_ptr(), stream=stream)
+
+
+def pml_pages_free(ref_counts: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                   rows: torch.Tensor, stream=None) -> None:
+    """The listed rows (distinct) give back their pages; their length becomes 0."""
+    pool = _pool(ref_counts, block_table, seq_lens)
+    _ints(rows, "rows")
+    _serving("pml_pages_free", *pool, rows.data_ptr(), rows.numel(), stream=stream)
+
+
+def pml_pages_compact(ref_counts: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                      ref_counts_out: torch.Tensor, block_table_out: torch.Tensor,
+                      remap: torch.Tensor, copy_src: torch.Tensor, copy_dst: torch.Tensor,
+                      copy_count: torch.Tensor, stream=None) -> None:
+    """Moves the live pages to the lowest numbers: new counts and tables (which
+    may be the inputs), ``remap`` of every page, and the moves listed for
+    ``pml_pages_copy`` (``copy_src`` / ``copy_dst`` of ``num_pages // 2`` or
+    more entries)."""
+    pool = _pool(ref_counts, block_table, seq_lens)
+    _ints(ref_counts_out, "ref_counts_out", ref_counts.numel())
+    _ints(remap, "remap", ref_counts.numel())
+    _table(block_table_out, "block_table_out")
+    if block_table_out.shape != block_table.shape:
+        raise ValueError("block_table_out must have block_table's shape")
+    _ints(copy_src, "copy_src")
+    _ints(copy_dst, "copy_dst", copy_src.numel())
+    _ints(copy_count, "copy_count", 1)
+    _serving("pml_pages_compact", *pool, ref_counts_out.data_ptr(), block_table_out.data_ptr(),
+             block_table_out.stride(0), remap.data_ptr(), copy_src.data_ptr(), copy_dst.data_ptr(),
+             copy_src.numel(), copy_count.data_ptr(), stream=stream)
+
+
+def pml_pages_copy(cache: torch.Tensor, copy_src: torch.Tensor, copy_dst: torch.Tensor,
+                   copy_count: torch.Tensor, layers: bool = True, stream=None) -> None:
+    """Copies page ``copy_src[i]`` over page ``copy_dst[i]`` for ``i <
+    copy_count`` in every layer of ``cache`` ``[layers, pages, ...]``
+    (``layers=False``: ``[pages, ...]``); each page is contiguous."""
+    if not cache.is_cuda or cache.dim() < (2 if layers else 1):
+        raise ValueError("cache must be a CUDA tensor [layers, pages, ...] or [pages, ...]")
+    _ints(copy_src, "copy_src")
+    _ints(copy_dst, "copy_dst", copy_src.numel())
+    _ints(copy_count, "copy_count", 1)
+    at = 1 if layers else 0
+    elems = 1
+    for size, step in zip(reversed(cache.shape[at + 1:]), reversed(cache.stride()[at + 1:])):
+        if size > 1 and step != elems:
+            raise ValueError("each page of the cache must be contiguous")
+        elems *= size
+    b = cache.element_size()
+    _serving("pml_pages_copy", cache.data_ptr(), cache.shape[0] if layers else 1,
+             cache.stride(0) * b if layers else 0, cache.shape[at], cache.stride(at) * b, elems * b,
+             copy_src.data_ptr(), copy_dst.data_ptr(), copy_count.data_ptr(), copy_src.numel(),
+             stream=stream)
 
 
 # ---------------------------------------------------------------- pages' keyword style

@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "host.h"
 #include "kernels.h"
 #include "pml.h"
 
@@ -31,21 +32,16 @@ int g_smem_optin[kMaxDevices];
 unsigned int* g_status_ptr[kMaxDevices];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
+}  // namespace
+
+namespace pml {
+
 int cuda_fail(cudaError_t e)
 {
     g_last_cuda_error = static_cast<int>(e);
     return PML_ERR_CUDA;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-struct DeviceInfo {
-    int device, sm_count, smem_optin;
-    unsigned int* status;
-};
-
-// Device properties and the status word's device address, looked up once per
-// device with that device current.
 cudaError_t device_info(DeviceInfo& d)
 {
     cudaError_t e = cudaGetDevice(&d.device);
@@ -71,6 +67,10 @@ cudaError_t device_info(DeviceInfo& d)
     return cudaSuccess;
 }
 
+}  // namespace pml
+
+namespace {
+
 cudaError_t encoder(PFN_cuTensorMapEncodeTiled_v12000& fn)
 {
     std::lock_guard<std::mutex> lock(g_mutex);
@@ -87,7 +87,10 @@ cudaError_t encoder(PFN_cuTensorMapEncodeTiled_v12000& fn)
     return cudaSuccess;
 }
 
-// Tiled map: dims/strides innermost first, strides in bytes for dimensions 1.. .
+}  // namespace
+
+namespace pml {
+
 cudaError_t encode_tiled(CUtensorMap& map, CUtensorMapDataType dtype, int rank, const void* base,
                          const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
                          CUtensorMapSwizzle swizzle)
@@ -95,12 +98,16 @@ cudaError_t encode_tiled(CUtensorMap& map, CUtensorMapDataType dtype, int rank, 
     PFN_cuTensorMapEncodeTiled_v12000 fn;
     cudaError_t e = encoder(fn);
     if (e != cudaSuccess) return e;
-    const uint32_t estr[3] = {1, 1, 1};
+    const uint32_t estr[5] = {1, 1, 1, 1, 1};
     CUresult r = fn(&map, dtype, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
+
+}  // namespace pml
+
+namespace {
 
 // The same with the 128-byte swizzle.
 cudaError_t encode_sw128(CUtensorMap& map, CUtensorMapDataType dtype, int rank, const void* base,
