@@ -460,6 +460,83 @@ int pml_index_quant_append(const void* q, int64_t q_token_stride, int64_t q_head
                            int num_heads, void* stream);
 
 /*
+ * pml_paged_attention -- attention of new tokens over a paged cache: one
+ * token per request, chunks, or any mix.
+ *
+ *   out[t, h] = sum_p softmax_p(softmax_scale * q[t, h] . k_p) v_p,
+ *   lse[t, h] = ln sum_p exp(softmax_scale * q[t, h] . k_p)
+ *
+ * Request b's new tokens are rows cu_q[b] .. cu_q[b+1]-1 of q (cu_q NULL:
+ * tokens / batch rows each) and the last ones of its kv_lens[b] cached
+ * tokens: row i of n stands at position kv_lens[b] - n + i.  It may see
+ * positions p of its request up to its own (causal != 0; else all below
+ * kv_lens[b]) and, for window > 0, past its own - window.  Query head h reads
+ * kv head h / (num_heads / kv_heads).  A row that may see nothing (an empty
+ * cache, a negative position) gives 0 and -inf.  Places a row may not see
+ * never reach it, whatever they hold (infinities and NaN too), nor do slots
+ * past kv_lens[b].
+ *
+ * Scores, softmax and sums are fp32; the probabilities are rounded to the
+ * inputs' type for the second product (half a step each, 2^-8 relative in
+ * bf16, averaged over the keys), the output once.
+ *
+ * q, out       bf16 or fp16 [tokens, num_heads, head_dim], strides in elements,
+ *              multiples of 8 and (q) positive; 16-byte aligned pointers
+ * k_cache      element (page, slot, head, d) at page * k_page_stride + slot *
+ *              k_slot_stride + head * k_head_stride + d; strides positive
+ *              multiples of 8, 16-byte aligned; v_cache alike
+ * kv_lens      int32 [batch], contents trusted; positions at or past 64 *
+ *              bt_width are not there
+ * cu_q         int32 [batch+1], ascending from 0 to tokens, or NULL
+ * head_dim     64 or 128;  num_heads a multiple of kv_heads, at most 128 times
+ * softmax_scale  positive;  batch <= 16384
+ * lse          fp32 [tokens, num_heads] or NULL
+ * workspace    device, 16-byte aligned, pml_attention_workspace_bytes(SM count,
+ *              head_dim) bytes or more; contents do not matter and nothing in
+ *              it outlives the call, but calls that overlap need one each
+ * A page outside [0, num_pages) is replaced by 0 (PML_STATUS_BAD_BLOCK).
+ * Results do not depend on the order in which CTAs run.
+ */
+int pml_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                        const void* k_cache, int64_t k_page_stride, int64_t k_slot_stride,
+                        int64_t k_head_stride, const void* v_cache, int64_t v_page_stride,
+                        int64_t v_slot_stride, int64_t v_head_stride, int dtype, int64_t num_pages,
+                        const int32_t* block_table, int64_t bt_stride, int bt_width,
+                        const int32_t* kv_lens, const int32_t* cu_q, int batch, int tokens,
+                        int num_heads, int kv_heads, int head_dim, float softmax_scale, int causal,
+                        int window, void* out, int64_t out_token_stride, int64_t out_head_stride,
+                        float* lse, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * pml_sparse_attention -- the same over the positions that a list names, as
+ * pml_topk_logits leaves them: token t looks at selected[t, 0..k) of request
+ * requests[t].  Entries below 0 or at or past kv_lens[requests[t]] are not
+ * there; the order does not matter; an entry that is there twice counts
+ * twice.  No causal rule applies beyond the list.  A negative request makes
+ * all of its token's entries absent (out 0, lse -inf), one at or past
+ * num_requests does too and sets PML_STATUS_BAD_REQUEST.
+ *
+ * selected     int32 [tokens, selected_stride], k entries used
+ * Strides of k_cache and v_cache are multiples of head_dim here (rows of one
+ * [rows, head_dim] tensor, fewer than 2^31 of them), else
+ * PML_ERR_UNSUPPORTED.  The rest as in pml_paged_attention.
+ */
+int pml_sparse_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                         const void* k_cache, int64_t k_page_stride, int64_t k_slot_stride,
+                         int64_t k_head_stride, const void* v_cache, int64_t v_page_stride,
+                         int64_t v_slot_stride, int64_t v_head_stride, int dtype, int64_t num_pages,
+                         const int32_t* block_table, int64_t bt_stride, int bt_width,
+                         const int32_t* kv_lens, const int32_t* requests, int num_requests,
+                         const int32_t* selected, int64_t selected_stride, int k, int tokens,
+                         int num_heads, int kv_heads, int head_dim, float softmax_scale, void* out,
+                         int64_t out_token_stride, int64_t out_head_stride, float* lse,
+                         void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace for either attention call; num_ctas is the device's SM
+ * count (pml_default_num_ctas).  0 for a head_dim other than 64 and 128. */
+int64_t pml_attention_workspace_bytes(int num_ctas, int head_dim);
+
+/*
  * Page bookkeeping.  A pool is ref_counts [num_pages] (how many requests hold
  * each page; 0: free), block_table [rows, bt_stride] of which bt_width columns
  * are used, and seq_lens [rows]; a row's first ceil(seq_lens / 64) entries are

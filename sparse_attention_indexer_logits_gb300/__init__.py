@@ -40,7 +40,8 @@ __all__ = [
     "pml_fp8_paged_mqa_logits_noalloc", "pml_fp8_paged_mqa_logits_wait_test",
     "pml_device_status",
     "pml_default_num_ctas", "pml_min_block_table_width", "pml_padded_seq_len", "pml_schedule_meta_elems",
-    "pml_rope", "pml_rope_append", "pml_index_quant_append", "pml_pages_fork", "pml_pages_extend",
+    "pml_rope", "pml_rope_append", "pml_index_quant_append", "pml_paged_attention",
+    "pml_sparse_attention", "pml_attention_workspace", "pml_pages_fork", "pml_pages_extend",
     "pml_pages_free", "pml_pages_compact", "pml_pages_copy",
     "fp8_paged_mqa_logits", "indexer_scores", "compute_paged_mqa_logits_schedule",
 ]
@@ -110,6 +111,8 @@ def lib() -> ctypes.CDLL:
                                                        i32, i32, i32, P]
         L.pml_fp8_paged_mqa_logits_noalloc.restype = i32
         L.pml_noalloc_max_ctas.restype = i32
+        L.pml_attention_workspace_bytes.argtypes = [i32, i32]
+        L.pml_attention_workspace_bytes.restype = i64
         f32 = ctypes.c_float
         pool = [P, i32, P, i64, i32, P, i32]
         for name, types in {
@@ -120,6 +123,12 @@ def lib() -> ctypes.CDLL:
                                 i64, P, i64, i32, i32, i32, i32, i32, P],
             "pml_index_quant_append": [P, i64, i64, P, i64, P, f32, P, i32, P, i32, P, i32, i32, i32,
                                        i32, f32, P, P, P, i64, P, i64, i32, i32, i32, P],
+            "pml_paged_attention": [P, i64, i64, P, i64, i64, i64, P, i64, i64, i64, i32, i64, P, i64, i32,
+                                    P, P, i32, i32, i32, i32, i32, f32, i32, i32, P, i64, i64, P, P,
+                                    i64, P],
+            "pml_sparse_attention": [P, i64, i64, P, i64, i64, i64, P, i64, i64, i64, i32, i64, P, i64,
+                                     i32, P, P, i32, P, i64, i32, i32, i32, i32, i32, f32, P, i64, i64,
+                                     P, P, i64, P],
             "pml_pages_fork": pool + [P, P, i32, P, P, P, P],
             "pml_pages_extend": pool + [P, P, i32, P, P],
             "pml_pages_free": pool + [P, i32, P],
@@ -616,6 +625,104 @@ def pml_index_quant_append(q: torch.Tensor, k: torch.Tensor | None, weights: tor
              w_out.data_ptr(), _addr(kv_fused), blocks, _addr(block_table), stride, width, tokens,
              heads, stream=stream)
     return q_out, w_out
+
+
+def _attention(name, q, k_cache, v_cache, block_table, kv_lens, out, lse, workspace, softmax_scale):
+    """The checks and arguments that both attention calls share."""
+    _heads(q, "q")
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("q must be bfloat16 or float16")
+    tokens, heads, dim = q.shape
+    _cache(k_cache, "k_cache", q)
+    _cache(v_cache, "v_cache", q)
+    if k_cache.shape != v_cache.shape or k_cache.shape[3] != dim:
+        raise ValueError("k_cache and v_cache must be [pages, 64, kv_heads, dim] with q's dim")
+    _table(block_table)
+    _ints(kv_lens, "kv_lens", block_table.shape[0])
+    if out is None:
+        out = torch.empty((tokens, heads, dim), dtype=q.dtype, device=q.device)
+    else:
+        _heads(out, "out", q.dtype)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (tokens, heads)
+                            or not lse.is_contiguous() or not lse.is_cuda):
+        raise ValueError("lse must be a contiguous CUDA float32 [tokens, heads] tensor")
+    if workspace is None:
+        workspace = pml_attention_workspace(dim, q.device)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    if softmax_scale is None:
+        softmax_scale = dim ** -0.5
+    kv = (q.data_ptr(), q.stride(0), q.stride(1), k_cache.data_ptr(), k_cache.stride(0),
+          k_cache.stride(1), k_cache.stride(2), v_cache.data_ptr(), v_cache.stride(0),
+          v_cache.stride(1), v_cache.stride(2), _DTYPES[q.dtype], k_cache.shape[0],
+          block_table.data_ptr(), block_table.stride(0), block_table.shape[1], kv_lens.data_ptr())
+    size = (tokens, heads, k_cache.shape[2], dim, softmax_scale)
+    tail = (out.data_ptr(), out.stride(0), out.stride(1), _addr(lse), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
+    return out, workspace, kv, size, tail
+
+
+def pml_attention_workspace(head_dim: int, device=None) -> torch.Tensor:
+    """A workspace for the attention calls on ``device``: calls that may
+    overlap on the GPU need one each."""
+    d = torch.device("cuda" if device is None else device)
+    index = torch.cuda.current_device() if d.index is None else d.index
+    if index not in _num_ctas:
+        _num_ctas[index] = pml_default_num_ctas(index)
+    n = lib().pml_attention_workspace_bytes(_num_ctas[index], head_dim)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=d)
+
+
+_num_ctas: dict = {}
+
+
+def pml_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                        block_table: torch.Tensor, kv_lens: torch.Tensor,
+                        cu_q: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                        softmax_scale: float | None = None, causal: bool = True, window: int = 0,
+                        lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                        stream=None) -> torch.Tensor:
+    """Attention of new tokens ``q`` ``[tokens, heads, dim]`` over paged caches
+    ``[pages, 64, kv_heads, dim]`` (any page, slot and head strides; bf16 or
+    fp16; dim 64 or 128).
+
+    Request b's rows are ``cu_q[b] .. cu_q[b+1]`` (``None``: equally many
+    each), the last of its ``kv_lens[b]`` tokens, whose keys and values are
+    already in its pages.  ``window > 0``: only keys past position - window.
+    ``lse`` receives the logarithms of the rows' sums.  ``softmax_scale``
+    defaults to ``dim ** -0.5``."""
+    out, workspace, kv, size, tail = _attention("pml_paged_attention", q, k_cache, v_cache, block_table,
+                                                kv_lens, out, lse, workspace, softmax_scale)
+    batch = kv_lens.numel()
+    if cu_q is not None:
+        _ints(cu_q, "cu_q", batch + 1)
+    elif batch == 0 or q.shape[0] % batch != 0:
+        raise ValueError("without cu_q the tokens must divide equally over the requests")
+    _serving("pml_paged_attention", *kv, _addr(cu_q), batch, *size, int(causal), window, *tail,
+             stream=stream)
+    return out
+
+
+def pml_sparse_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                         block_table: torch.Tensor, kv_lens: torch.Tensor, requests: torch.Tensor,
+                         selected: torch.Tensor, out: torch.Tensor | None = None,
+                         softmax_scale: float | None = None, lse: torch.Tensor | None = None,
+                         workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of each token over the positions ``selected[t]`` (int32
+    ``[tokens, k]``, as ``pml_topk_logits`` leaves them; entries below 0 or
+    past the request's length are not there) of request ``requests[t]``."""
+    out, workspace, kv, size, tail = _attention("pml_sparse_attention", q, k_cache, v_cache, block_table,
+                                                kv_lens, out, lse, workspace, softmax_scale)
+    tokens = q.shape[0]
+    _ints(requests, "requests", tokens)
+    _table(selected, "selected")
+    if selected.shape[0] != tokens:
+        raise ValueError("selected must hold a row per token")
+    _serving("pml_sparse_attention", *kv, requests.data_ptr(), block_table.shape[0],
+             selected.data_ptr(), selected.stride(0), selected.shape[1], *size, *tail, stream=stream)
+    return out
 
 
 def _pool(ref_counts, block_table, seq_lens):

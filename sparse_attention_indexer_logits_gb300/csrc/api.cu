@@ -120,7 +120,7 @@ cudaError_t encode_sw128(CUtensorMap& map, CUtensorMapDataType dtype, int rank, 
 
 extern "C" {
 
-int pml_version(void) { return 101; }
+int pml_version(void) { return 102; }
 
 const char* pml_error_string(int code)
 {

@@ -120,6 +120,128 @@ PoolArgs pool(int32_t* ref_counts, int num_pages, int32_t* block_table, int64_t 
     return p;
 }
 
+// Strides of a dimension of one element are never used: any valid one will do.
+int64_t used(int64_t stride, int64_t size, int64_t other) { return size > 1 ? stride : other; }
+
+// The cache as a [rows][head_dim] tensor: row strides of pages, slots and
+// heads, and the number of rows; false if they are not whole rows.
+bool cache_rows(int64_t page, int64_t slot, int64_t head, int64_t pages, int heads, int dim,
+                int& page_rows, int& slot_rows, int& head_rows, int64_t& rows)
+{
+    page = used(page, pages, dim);
+    head = used(head, heads, dim);
+    if (page % dim || slot % dim || head % dim) return false;
+    rows = (pages - 1) * (page / dim) + (kBlockKeys - 1) * (slot / dim) + (heads - 1) * (head / dim) + 1;
+    if (rows > 0x7fffffffLL) return false;
+    page_rows = (int)(page / dim);
+    slot_rows = (int)(slot / dim);
+    head_rows = (int)(head / dim);
+    return true;
+}
+
+// The checks, tensor maps and launches that both attention calls share; `a`
+// comes with what is theirs.
+int attention_call(AttnArgs& a, const void* q, int64_t q_token, int64_t q_head, const void* k_cache,
+                   int64_t k_page, int64_t k_slot, int64_t k_head, const void* v_cache,
+                   int64_t v_page, int64_t v_slot, int64_t v_head, int dtype, int64_t num_pages,
+                   const int32_t* block_table, int64_t bt_stride, int bt_width,
+                   const int32_t* kv_lens, int tokens, int num_heads, int kv_heads, int head_dim,
+                   float softmax_scale, void* out, int64_t out_token, int64_t out_head, float* lse,
+                   void* workspace, int64_t workspace_bytes, void* stream)
+{
+    if (tokens < 0 || num_heads < 1 || kv_heads < 1 || num_heads % kv_heads) return PML_ERR_INVALID_ARG;
+    if (dtype != PML_DTYPE_BFLOAT16 && dtype != PML_DTYPE_FLOAT16) return PML_ERR_UNSUPPORTED;
+    if (head_dim != 64 && head_dim != 128) return PML_ERR_UNSUPPORTED;
+    const int group = num_heads / kv_heads;
+    if (group > kAttnHalfRows) return PML_ERR_UNSUPPORTED;
+    if (!(softmax_scale > 0.0f) || softmax_scale > 1e30f) return PML_ERR_INVALID_ARG;
+    if (tokens == 0) return PML_OK;
+    if (!q || !k_cache || !v_cache || !block_table || !kv_lens || !out || !workspace)
+        return PML_ERR_INVALID_ARG;
+    if (num_pages < 1 || num_pages > 0x7fffffffLL || bt_width < 1 || bt_stride < bt_width)
+        return PML_ERR_INVALID_ARG;
+    if (bt_width > 0x7fffffff / kBlockKeys) return PML_ERR_UNSUPPORTED;
+    const bool select = a.selected != nullptr;
+    // strides in elements, multiples of 16 bytes
+    int64_t qs[2] = {used(q_head, num_heads, head_dim), used(q_token, tokens, head_dim)};
+    int64_t ks[3] = {k_slot, used(k_head, kv_heads, head_dim), used(k_page, num_pages, head_dim)};
+    int64_t vs[3] = {v_slot, used(v_head, kv_heads, head_dim), used(v_page, num_pages, head_dim)};
+    for (int64_t s : {qs[0], qs[1], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2]})
+        if (s <= 0 || s % 8) return PML_ERR_ALIGNMENT;
+    if ((tokens > 1 && out_token % 8) || (num_heads > 1 && out_head % 8)) return PML_ERR_ALIGNMENT;
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+        !aligned(workspace, 16) || !aligned(lse, 4) || !aligned(block_table, 4) ||
+        !aligned(kv_lens, 4) || !aligned(a.cu_q, 4))
+        return PML_ERR_ALIGNMENT;
+    int64_t k_rows = 0, v_rows = 0;
+    if (select && (!cache_rows(k_page, k_slot, k_head, num_pages, kv_heads, head_dim, a.sel_page_rows,
+                               a.sel_slot_rows, a.sel_head_rows, k_rows) ||
+                   !cache_rows(v_page, v_slot, v_head, num_pages, kv_heads, head_dim, a.sel_page_rows_v,
+                               a.sel_slot_rows_v, a.sel_head_rows_v, v_rows)))
+        return PML_ERR_UNSUPPORTED;
+    DeviceInfo dev;
+    cudaError_t e = device_info(dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    const int num_ctas = dev.sm_count;
+    if (workspace_bytes < pml_attention_workspace_bytes(num_ctas, head_dim)) return PML_ERR_INVALID_ARG;
+
+    const int64_t slots = 2LL * num_ctas;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.partial = reinterpret_cast<float*>(ws);
+    ws += slots * kAttnSlotRows * head_dim * 4LL;
+    a.stats = reinterpret_cast<float2*>(ws);
+    ws += slots * kAttnSlotRows * 8;
+    a.pieces = reinterpret_cast<int*>(ws);
+    a.block_table = block_table;
+    a.kv_lens = kv_lens;
+    a.out = out;
+    a.lse = lse;
+    a.status = dev.status;
+    a.bt_stride = bt_stride;
+    a.bt_width = bt_width;
+    a.out_token = out_token;
+    a.out_head = out_head;
+    a.num_pages = num_pages;
+    a.tokens = tokens;
+    a.kv_heads = kv_heads;
+    a.group = group;
+    a.half_tokens = kAttnHalfRows / group;
+    a.scale = softmax_scale;
+    a.scale_log2 = softmax_scale * 1.4426950408889634f;
+
+    const bool fp16 = dtype == PML_DTYPE_FLOAT16;
+    const CUtensorMapDataType type = fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    CUtensorMap qmap, kmap, vmap;
+    {
+        const uint64_t dims[3] = {(uint64_t)head_dim, (uint64_t)num_heads, (uint64_t)tokens};
+        const uint64_t strides[2] = {(uint64_t)qs[0] * 2, (uint64_t)qs[1] * 2};
+        const uint32_t box[3] = {64, (uint32_t)group, (uint32_t)a.half_tokens};
+        e = encode_tiled(qmap, type, 3, q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    for (int i = 0; i < 2; ++i) {
+        const void* cache = i ? v_cache : k_cache;
+        CUtensorMap& map = i ? vmap : kmap;
+        if (select) {
+            const uint64_t dims[2] = {(uint64_t)head_dim, (uint64_t)(i ? v_rows : k_rows)};
+            const uint64_t strides[1] = {(uint64_t)head_dim * 2};
+            const uint32_t box[2] = {64, 1};
+            e = encode_tiled(map, type, 2, cache, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+        } else {
+            const int64_t* s = i ? vs : ks;
+            const uint64_t dims[4] = {(uint64_t)head_dim, (uint64_t)kBlockKeys, (uint64_t)kv_heads,
+                                      (uint64_t)num_pages};
+            const uint64_t strides[3] = {(uint64_t)s[0] * 2, (uint64_t)s[1] * 2, (uint64_t)s[2] * 2};
+            const uint32_t box[4] = {64, (uint32_t)kBlockKeys, 1, 1};
+            e = encode_tiled(map, type, 4, cache, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+        }
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    e = launch_paged_attention(head_dim, fp16, select, qmap, kmap, vmap, a, num_ctas,
+                               static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PML_OK : cuda_fail(e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -365,6 +487,68 @@ int pml_pages_copy(void* cache, int layers, int64_t layer_stride_bytes, int num_
     }
     e = launch_pages_copy(a, dev.sm_count, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PML_OK : cuda_fail(e);
+}
+
+int64_t pml_attention_workspace_bytes(int num_ctas, int head_dim)
+{
+    if (num_ctas < 1 || (head_dim != 64 && head_dim != 128)) return 0;
+    const int64_t slots = 2LL * num_ctas;
+    return slots * kPieceInts * 4 + slots * kAttnSlotRows * 8 + slots * kAttnSlotRows * head_dim * 4LL;
+}
+
+int pml_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                        const void* k_cache, int64_t k_page_stride, int64_t k_slot_stride,
+                        int64_t k_head_stride, const void* v_cache, int64_t v_page_stride,
+                        int64_t v_slot_stride, int64_t v_head_stride, int dtype, int64_t num_pages,
+                        const int32_t* block_table, int64_t bt_stride, int bt_width,
+                        const int32_t* kv_lens, const int32_t* cu_q, int batch, int tokens,
+                        int num_heads, int kv_heads, int head_dim, float softmax_scale, int causal,
+                        int window, void* out, int64_t out_token_stride, int64_t out_head_stride,
+                        float* lse, void* workspace, int64_t workspace_bytes, void* stream)
+{
+    if (batch < 0) return PML_ERR_INVALID_ARG;
+    if (batch > kAttnMaxBatch) return PML_ERR_UNSUPPORTED;
+    if (tokens > 0 && batch == 0) return PML_ERR_INVALID_ARG;
+    if (cu_q == nullptr && batch > 0 && tokens % batch != 0) return PML_ERR_INVALID_ARG;
+    if (window < 0) return PML_ERR_INVALID_ARG;
+    AttnArgs a = {};
+    a.cu_q = cu_q;
+    a.q_per_request = batch > 0 ? tokens / batch : 0;
+    a.batch = batch;
+    a.causal = causal ? 1 : 0;
+    a.window = window;
+    return attention_call(a, q, q_token_stride, q_head_stride, k_cache, k_page_stride, k_slot_stride,
+                          k_head_stride, v_cache, v_page_stride, v_slot_stride, v_head_stride, dtype,
+                          num_pages, block_table, bt_stride, bt_width, kv_lens, tokens, num_heads,
+                          kv_heads, head_dim, softmax_scale, out, out_token_stride, out_head_stride,
+                          lse, workspace, workspace_bytes, stream);
+}
+
+int pml_sparse_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                         const void* k_cache, int64_t k_page_stride, int64_t k_slot_stride,
+                         int64_t k_head_stride, const void* v_cache, int64_t v_page_stride,
+                         int64_t v_slot_stride, int64_t v_head_stride, int dtype, int64_t num_pages,
+                         const int32_t* block_table, int64_t bt_stride, int bt_width,
+                         const int32_t* kv_lens, const int32_t* requests, int num_requests,
+                         const int32_t* selected, int64_t selected_stride, int k, int tokens,
+                         int num_heads, int kv_heads, int head_dim, float softmax_scale, void* out,
+                         int64_t out_token_stride, int64_t out_head_stride, float* lse,
+                         void* workspace, int64_t workspace_bytes, void* stream)
+{
+    if (k < 1 || selected_stride < k || num_requests < 1) return PML_ERR_INVALID_ARG;
+    if (tokens > 0 && (!requests || !selected)) return PML_ERR_INVALID_ARG;
+    if (!aligned(requests, 4) || !aligned(selected, 4)) return PML_ERR_ALIGNMENT;
+    AttnArgs a = {};
+    a.batch = num_requests;
+    a.requests = requests;
+    a.selected = selected;
+    a.sel_stride = selected_stride;
+    a.sel_k = k;
+    return attention_call(a, q, q_token_stride, q_head_stride, k_cache, k_page_stride, k_slot_stride,
+                          k_head_stride, v_cache, v_page_stride, v_slot_stride, v_head_stride, dtype,
+                          num_pages, block_table, bt_stride, bt_width, kv_lens, tokens, num_heads,
+                          kv_heads, head_dim, softmax_scale, out, out_token_stride, out_head_stride,
+                          lse, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,1201 @@
+// Attention of new tokens over a paged cache on sm_103a.
+//
+//   out[t, h] = sum_p softmax_p(scale * q[t, h] . k_p) v_p
+//
+// over the positions p that token t may see: those of its request up to its
+// own (causal), past position - window (window > 0), or the ones a list
+// names.  One pass over the keys with a running maximum m and sum l of
+// exponentials: a tile of 128 keys gives S = Q K^T, P = 2^(c S - c m), O += P V;
+// at the end out = O / l and lse = scale * m + ln l.
+//
+// Work.  The rows of an item are up to 256 (token, head) pairs that share a kv
+// head, its unit of work is one tile of 128 keys.  The units of all items, in
+// order, are cut into one contiguous range per CTA, so a long request's keys
+// are split over many CTAs and short requests share one, whatever the mix.  A
+// range that ends inside an item leaves its (m, l, O) in the workspace and a
+// second kernel joins the pieces.
+//
+// A CTA holds two 128-row accumulator pairs (S and O, 512 TMEM columns).  An
+// item of more than 128 rows gives each its own half of the rows and both see
+// every tile; an item of at most 128 rows gives both the same rows and the
+// tiles in turn, and their two results are joined at its end.  Either way the
+// tensor core works on one half while the other half's softmax runs:
+//
+//   producer warp    walks the range; per item a descriptor and the Q rows,
+//                    per tile the K and V pages (TMA, 128-byte swizzle), or
+//                    the listed rows (gather4), into a ring of stages
+//   MMA warp         S_h = Q_h K^T (both operands in shared memory), then
+//                    O_h += P_h V with P_h read from TMEM, where it replaced
+//                    S_h, and V as the transposed operand
+//   2 softmax groups 128 threads each, a row per thread: S from TMEM, maximum,
+//                    exponentials, sum, P back to TMEM.  O is rescaled only
+//                    when a row's maximum has grown by more than 2^8 in P's
+//                    scale (exact: l and O share the reference), which is
+//                    rare after the first tiles
+//
+// Masked places never reach a result, whatever they hold: scores are replaced
+// by -inf before the maximum; V rows that no row of the item may see are
+// zeroed in shared memory; and where a tile's V rows are visible to some rows
+// and hidden from others (the causal diagonal, a window's edge) and hold an
+// infinity or NaN, the group adds that tile's product row by row itself.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "ptx.cuh"
+#include "serving.h"
+
+namespace pml {
+namespace attn {
+
+constexpr int kThreads = 384;      // three warpgroups: softmax, softmax, MMA and copies
+// Registers per thread: the block is launched with 168, the third warpgroup
+// gives some back and the softmax groups, which hold a row of S, take them
+// (2 * 208 + 88 = 3 * 168).
+constexpr int kLaunchRegs = 168, kHighRegs = 208, kLowRegs = 88;
+constexpr int kMmaWarp = 8;
+constexpr int kLoadWarp = 9;
+constexpr int kItemSlots = 4;
+constexpr int kItemInts = 16;
+
+// item descriptor
+enum { kItN, kItJ0, kItFlags, kItTok0, kItNtok, kItHead, kItPos0, kItKvHi, kItLo, kItHi, kItSlot };
+constexpr int kAlt = 1;      // both halves hold the same rows and take the tiles in turn
+constexpr int kWhole = 2;    // the piece is a whole item: write the output
+constexpr int kEnd = 8;      // no more items
+// piece record in the workspace
+enum { kPcUsed, kPcTok0, kPcNtok, kPcHead, kPcLast, kPcAlt };
+
+// A wait by a whole warp: one result for all lanes, so that a wait that ran
+// out in some lanes only cannot part them before the next warp-wide step.
+// (The slow path is inlined: a kernel that re-splits its registers contains no
+// calls.)
+__device__ __forceinline__ bool warp_wait(uint32_t b, uint32_t parity, volatile int* abort,
+                                          unsigned int* status)
+{
+    return __all_sync(0xffffffffu, mbar_wait<false>(b, parity, abort, status));
+}
+
+template <int D>
+struct Cfg {
+    static constexpr int kBlocks = D / 64;                     // 128-byte column blocks
+    static constexpr int kBlockBytes = 128 * 128;              // 128 rows of 128 bytes
+    static constexpr int kStageBytes = kBlocks * kBlockBytes;  // a K or V tile
+    static constexpr int kHalfBytes = kBlocks * kBlockBytes;   // a Q half
+    static constexpr int kStages = D == 128 ? 5 : 11;
+    static constexpr int kQ = 0;
+    static constexpr int kRing = kQ + 2 * kHalfBytes;
+    static constexpr int kStats = kRing + kStages * kStageBytes;      // float2 [2][128]
+    static constexpr int kBars = kStats + 2 * 128 * 8;
+    // barriers: full, empty per stage; q full, q empty; s full, p ready, pv
+    // done, group sync per half; o empty, alt sync; item full, item empty; the
+    // MMA warp's last commit
+    static constexpr int kNumBars = 2 * kStages + 2 + 8 + 2 + 2 * kItemSlots + 1;
+    static constexpr int kItems = (kBars + kNumBars * 8 + 15) / 16 * 16;
+    static constexpr int kMisc = kItems + kItemSlots * kItemInts * 4;
+    static constexpr int kTotal = kMisc + 128;
+};
+
+constexpr uint32_t kColS = 0;      // S_h at 128 h; P_h over its first 64 columns
+constexpr uint32_t kColO = 256;    // O_h at 256 + 128 h
+
+// MN-major operand (V: keys are the rows, 128 bytes of columns each, 128-byte
+// swizzle): groups of 64 columns lie `lbo` bytes apart, groups of eight keys
+// 1024 bytes.
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t lbo)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int32_t c0, int32_t c1, int32_t c2, int32_t c3)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+// Four rows of a [rows][columns] tensor, 64 columns from c0 on, to four
+// consecutive 128-byte rows of shared memory.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int32_t c0, int4 r)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr)
+{
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r)
+                 : "r"(taddr)
+                 : "memory");
+    return r;
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&v)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+                 "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+// 2^x; -inf gives 0
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool FP16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi)
+{
+    uint32_t r;
+    if constexpr (FP16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <bool FP16>
+__device__ __forceinline__ float2 unpack16(uint32_t w)
+{
+    if constexpr (FP16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    else return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// Whether either 16-bit value of w is an infinity or NaN.
+template <bool FP16>
+__device__ __forceinline__ bool not_finite(uint32_t w)
+{
+    constexpr uint32_t kExp = FP16 ? 0x7c007c00u : 0x7f807f80u;
+    constexpr uint32_t kOne = FP16 ? 0x04000400u : 0x00800080u;
+    return (((w & kExp) + kOne) & 0x80008000u) != 0;
+}
+
+// The tokens and tiles of tile `tile` of a request with nq new tokens of kv.
+struct Span {
+    int t0, ntok;    // tokens of the request
+    int lo, hi;      // keys that some row of the tile may see
+    int j0, n;       // their tiles of 128 keys; at least one
+};
+
+__device__ __forceinline__ Span tile_span(const AttnArgs& a, int nq, int kv, int tile)
+{
+    Span s;
+    const int per = 2 * a.half_tokens;
+    s.t0 = tile * per;
+    s.ntok = min(per, nq - s.t0);
+    const int there = (int)min((long long)kv, (long long)a.bt_width * kBlockKeys);
+    const long long pos0 = (long long)kv - nq + s.t0;      // position of the tile's first token
+    long long hi = there;
+    if (a.causal) hi = min(hi, pos0 + s.ntok);
+    long long lo = 0;
+    if (a.window > 0) lo = max(lo, pos0 - a.window + 1);
+    if (hi <= lo) { hi = 0; lo = 0; }
+    s.lo = (int)lo;
+    s.hi = (int)hi;
+    s.j0 = s.lo / kAttnTileKeys;
+    s.n = max(1, (s.hi + kAttnTileKeys - 1) / kAttnTileKeys - s.j0);
+    return s;
+}
+
+__device__ __forceinline__ int tiles_of(const AttnArgs& a, int nq)
+{
+    const int per = 2 * a.half_tokens;
+    return (nq + per - 1) / per;
+}
+
+__device__ __forceinline__ void request_of(const AttnArgs& a, int b, int& tok0, int& nq, int& kv)
+{
+    if (a.cu_q != nullptr) {
+        const int s = __ldg(a.cu_q + b), e = __ldg(a.cu_q + b + 1);
+        tok0 = min(max(s, 0), a.tokens);
+        nq = min(max(e, tok0), a.tokens) - tok0;
+    } else {
+        tok0 = b * a.q_per_request;
+        nq = a.q_per_request;
+    }
+    kv = max(__ldg(a.kv_lens + b), 0);
+}
+
+// Units (tiles) of one kv head of request b; a warp computes it together.
+__device__ __forceinline__ int head_units(const AttnArgs& a, int nq, int kv, int lane)
+{
+    int u = 0;
+    const int tiles = tiles_of(a, nq);
+    for (int i = lane; i < tiles; i += 32) u += tile_span(a, nq, kv, i).n;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+    return u;
+}
+
+template <int D, bool FP16, bool SEL>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_attention_kernel(const __grid_constant__ CUtensorMap qmap,
+                           const __grid_constant__ CUtensorMap kmap,
+                           const __grid_constant__ CUtensorMap vmap, const AttnArgs a)
+{
+    using C = Cfg<D>;
+    constexpr int S = C::kStages;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t base = smem_addr(smem);
+    if (base & 1023u) {                       // the swizzled tiles need it; never seen
+        if (threadIdx.x == 0) atomicOr(a.status, kStatusWaitTimeout);
+        return;
+    }
+    const uint32_t bar = base + C::kBars;
+    auto full_bar = [&](int s) { return bar + 8u * s; };
+    auto empty_bar = [&](int s) { return bar + 8u * (S + s); };
+    const uint32_t qfull = bar + 8u * (2 * S), qempty = qfull + 8u;
+    const uint32_t sfull0 = qfull + 16u, pready0 = sfull0 + 16u, pvdone0 = pready0 + 16u,
+                   group0 = pvdone0 + 16u, oempty = group0 + 16u, altbar = oempty + 8u,
+                   itfull0 = altbar + 8u, itempty0 = itfull0 + 8u * kItemSlots, drain = itempty0 + 8u * kItemSlots;
+    int* items = reinterpret_cast<int*>(smem + C::kItems);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMisc + 4);
+    volatile int* skip_flag = reinterpret_cast<volatile int*>(smem + C::kMisc + 8);   // [2]
+    volatile int* votes = reinterpret_cast<volatile int*>(smem + C::kMisc + 16);      // [2][2][4]
+    float2* stats = reinterpret_cast<float2*>(smem + C::kStats);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        skip_flag[0] = 0;
+        skip_flag[1] = 0;
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        mbar_init(qfull, 1);
+        mbar_init(qempty, 1);
+        for (int h = 0; h < 2; ++h) {
+            mbar_init(sfull0 + 8u * h, 1);
+            mbar_init(pready0 + 8u * h, 4);
+            mbar_init(pvdone0 + 8u * h, 1);
+            mbar_init(group0 + 8u * h, 4);
+        }
+        mbar_init(drain, 1);
+        mbar_init(oempty, 8);
+        mbar_init(altbar, 8);
+        for (int i = 0; i < kItemSlots; ++i) {
+            mbar_init(itfull0 + 8u * i, 1);
+            mbar_init(itempty0 + 8u * i, 9);
+        }
+        fence_mbar_init();
+        tma_prefetch_map(&qmap);
+        tma_prefetch_map(&kmap);
+        tma_prefetch_map(&vmap);
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_addr(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    // units per request and kv head, in the ring's memory until the copies begin
+    int* units = reinterpret_cast<int*>(smem + C::kRing);
+    if constexpr (!SEL) {
+        for (int b = warp; b < a.batch; b += kThreads / 32) {
+            int tok0, nq, kv;
+            request_of(a, b, tok0, nq, kv);
+            const int u = head_units(a, nq, kv, lane);
+            if (lane == 0) units[b] = u;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp >= kMmaWarp) {
+        regs_dec<kLowRegs>();
+    if (warp == kLoadWarp) {
+        // ------------------------------------------------------------ producer
+        int b = 0, head = 0, tile = 0, j = 0;       // the range's start
+        long long left;                              // units left in the range
+        const int sel_tiles = SEL ? (a.sel_k + kAttnTileKeys - 1) / kAttnTileKeys : 0;
+        if constexpr (SEL) {
+            const long long total = (long long)a.tokens * a.kv_heads * sel_tiles;
+            const long long s0 = range_start(total, gridDim.x, blockIdx.x);
+            left = range_start(total, gridDim.x, blockIdx.x + 1) - s0;
+            const long long item = s0 / sel_tiles;
+            j = (int)(s0 - item * sel_tiles);
+            b = (int)(item / a.kv_heads);           // the token
+            head = (int)(item - (long long)b * a.kv_heads);
+        } else {
+            long long total = 0;
+            for (int i = lane; i < a.batch; i += 32) total += units[i];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+            total *= a.kv_heads;
+            const long long s0 = range_start(total, gridDim.x, blockIdx.x);
+            left = range_start(total, gridDim.x, blockIdx.x + 1) - s0;
+            // the request that holds unit s0
+            long long before = 0, off = 0;
+            bool found = false;
+            for (int c = 0; c < a.batch && !found && left > 0; c += 32) {
+                const long long v = c + lane < a.batch ? (long long)units[c + lane] * a.kv_heads : 0;
+                long long incl = v;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += u;
+                }
+                const bool mine = before + incl - v <= s0 && s0 < before + incl;
+                const unsigned who = __ballot_sync(0xffffffffu, mine);
+                if (who) {
+                    const int l = __ffs(who) - 1;
+                    b = c + l;
+                    off = s0 - __shfl_sync(0xffffffffu, before + incl - v, l);
+                    found = true;
+                }
+                before += __shfl_sync(0xffffffffu, incl, 31);
+            }
+            if (left > 0) {
+                const int per_head = units[b];
+                head = (int)(off / per_head);
+                int rem = (int)(off - (long long)head * per_head);
+                int tok0, nq, kv;
+                request_of(a, b, tok0, nq, kv);
+                const int tiles = tiles_of(a, nq);
+                found = false;
+                for (int c = 0; c < tiles && !found; c += 32) {
+                    const int v = c + lane < tiles ? tile_span(a, nq, kv, c + lane).n : 0;
+                    int incl = v;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int u = __shfl_up_sync(0xffffffffu, incl, o);
+                        if (lane >= o) incl += u;
+                    }
+                    const unsigned who = __ballot_sync(0xffffffffu, incl - v <= rem && rem < incl);
+                    if (who) {
+                        const int l = __ffs(who) - 1;
+                        tile = c + l;
+                        j = rem - __shfl_sync(0xffffffffu, incl - v, l);
+                        found = true;
+                    } else {
+                        rem -= __shfl_sync(0xffffffffu, incl, 31);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        // `units` has been read; the ring's memory is the copies' from here
+        // on (no other warp touches it before a full barrier)
+        fence_proxy_async_smem();
+
+        int* piece = a.pieces + (long long)blockIdx.x * 2 * kPieceInts;
+        if (lane < 2) piece[lane * kPieceInts + kPcUsed] = 0;
+        __syncwarp();
+
+        int pos = 0;                 // stages filled so far
+        int item = 0;
+        bool ok = true;
+        int tok0 = 0, nq = 0, kv = 0, tiles = 0, cur_b = -1;
+        while (left > 0 && ok) {
+            if (!SEL && b >= a.batch) break;     // lengths changed under the call
+            Span sp;
+            int req;
+            if constexpr (SEL) {
+                req = __ldg(a.requests + b);
+                bool fine = req >= 0 && req < a.batch;
+                if (!fine) {
+                    if (req >= a.batch && lane == 0) atomicOr(a.status, kStatusBadRequest);
+                    req = 0;
+                }
+                kv = fine ? max(__ldg(a.kv_lens + req), 0) : 0;
+                kv = (int)min((long long)kv, (long long)a.bt_width * kBlockKeys);
+                sp.t0 = 0;
+                sp.ntok = 1;
+                sp.lo = 0;
+                sp.hi = kv;
+                sp.j0 = 0;
+                sp.n = sel_tiles;
+                tok0 = b;
+            } else {
+                if (b != cur_b) {
+                    request_of(a, b, tok0, nq, kv);
+                    tiles = tiles_of(a, nq);
+                    cur_b = b;
+                    if (tiles == 0) { ++b; head = 0; tile = 0; j = 0; continue; }
+                }
+                req = b;
+                sp = tile_span(a, nq, kv, tile);
+            }
+            const int n = (int)min(left, (long long)(sp.n - j));
+            const bool first = j == 0, last = j + n == sp.n;
+            const bool alt = SEL || sp.ntok <= a.half_tokens;
+            const int slot = first ? 1 : 0;          // workspace slot of a piece
+            // ---- the item's descriptor and Q rows
+            const int is = item % kItemSlots;
+            ok = warp_wait(itempty0 + 8u * is, ((item / kItemSlots) & 1) ^ 1, abort_flag, a.status);
+            if (!ok) break;
+            const int j0 = sp.j0 + j;
+            if (lane == 0) {
+                int* it = items + is * kItemInts;
+                it[kItN] = n;
+                it[kItJ0] = j0;
+                it[kItFlags] = (alt ? kAlt : 0) | (first && last ? kWhole : 0);
+                it[kItTok0] = tok0 + sp.t0;
+                it[kItNtok] = sp.ntok;
+                it[kItHead] = head;
+                it[kItPos0] = kv - nq + sp.t0;
+                it[kItKvHi] = (int)min((long long)kv, (long long)a.bt_width * kBlockKeys);
+                it[kItLo] = sp.lo;
+                it[kItHi] = sp.hi;
+                it[kItSlot] = slot;
+                if (!(first && last)) {
+                    int* p = piece + slot * kPieceInts;
+                    p[kPcUsed] = 1;
+                    p[kPcTok0] = tok0 + sp.t0;
+                    p[kPcNtok] = sp.ntok;
+                    p[kPcHead] = head;
+                    p[kPcLast] = last ? 1 : 0;
+                    p[kPcAlt] = alt ? 1 : 0;
+                }
+                mbar_arrive(itfull0 + 8u * is);
+            }
+            ok = warp_wait(qempty, (item & 1) ^ 1, abort_flag, a.status);
+            if (!ok) break;
+            if (lane == 0) {
+                const int halves = alt ? 1 : 2;
+                mbar_arrive_expect_tx(qfull, (uint32_t)(halves * C::kBlocks * 128 * a.group * a.half_tokens));
+                for (int h = 0; h < halves; ++h)
+                    for (int kb = 0; kb < C::kBlocks; ++kb)
+                        tma_load_3d(base + C::kQ + h * C::kHalfBytes + kb * C::kBlockBytes, &qmap, qfull,
+                                    kb * 64, head * a.group, tok0 + sp.t0 + h * a.half_tokens);
+            }
+            __syncwarp();
+            ++item;
+
+            // ---- K and V tiles: K runs `ahead` tiles before V
+            const int ahead = alt ? 2 : 1;
+            auto begin_stage = [&](uint32_t& dst, uint32_t& fb) {
+                const int s = pos % S;
+                const bool r = warp_wait(empty_bar(s), (uint32_t)((pos / S) & 1) ^ 1u, abort_flag, a.status);
+                dst = base + C::kRing + s * C::kStageBytes;
+                fb = full_bar(s);
+                ++pos;
+                return r;
+            };
+            if constexpr (SEL) {
+                const int32_t* list = a.selected + (long long)b * a.sel_stride;
+                const int32_t* table = a.block_table + (long long)req * a.bt_stride;
+                // the cache rows of this lane's four entries of a tile (as page
+                // and slot); w: none of them is there
+                auto find = [&](int t, int4& pg, int4& sl, bool& any) {
+                    int* pp = &pg.x;
+                    int* ss = &sl.x;
+                    any = false;
+                    bool bad = false;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int at = (j0 + t) * kAttnTileKeys + 4 * lane + e;
+                        const int p = at < a.sel_k ? __ldg(list + at) : -1;
+                        const bool there = p >= 0 && p < kv;
+                        long long page = there ? __ldg(table + (p >> 6)) : 0;
+                        if (page < 0 || page >= a.num_pages) { bad = true; page = 0; }
+                        pp[e] = (int)page;
+                        ss[e] = there ? p & 63 : 0;
+                        any |= there;
+                    }
+                    if (bad) atomicOr(a.status, kStatusBadBlock);
+                };
+                auto rows = [&](int4 pg, int4 sl, bool v) {
+                    const int pr = v ? a.sel_page_rows_v : a.sel_page_rows;
+                    const int sr = v ? a.sel_slot_rows_v : a.sel_slot_rows;
+                    const int h0 = head * (v ? a.sel_head_rows_v : a.sel_head_rows);
+                    return make_int4(pg.x * pr + sl.x * sr + h0, pg.y * pr + sl.y * sr + h0,
+                                     pg.z * pr + sl.z * sr + h0, pg.w * pr + sl.w * sr + h0);
+                };
+                auto load = [&](const CUtensorMap* map, int4 r, bool any) {
+                    uint32_t dst, fb;
+                    if (!begin_stage(dst, fb)) return false;
+                    const int cnt = __popc(__ballot_sync(0xffffffffu, any));
+                    if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)(cnt * 512 * C::kBlocks));
+                    __syncwarp();
+                    if (any)
+                        for (int kb = 0; kb < C::kBlocks; ++kb)
+                            tma_gather4(dst + kb * C::kBlockBytes + lane * 512, map, fb, kb * 64, r);
+                    return true;
+                };
+                int4 p0, s0, p1, s1, p2, s2;
+                bool a0, a1 = false, a2 = false;
+                find(0, p0, s0, a0);
+                p1 = s1 = p2 = s2 = make_int4(0, 0, 0, 0);
+                if (n > 1) find(1, p1, s1, a1);
+                ok = load(&kmap, rows(p0, s0, false), a0);
+                if (ok && n > 1) ok = load(&kmap, rows(p1, s1, false), a1);
+                for (int t = 0; t < n && ok; ++t) {
+                    if (t + 2 < n) find(t + 2, p2, s2, a2);
+                    ok = load(&vmap, rows(p0, s0, true), a0);
+                    if (ok && t + 2 < n) ok = load(&kmap, rows(p2, s2, false), a2);
+                    p0 = p1; s0 = s1; a0 = a1;
+                    p1 = p2; s1 = s2; a1 = a2;
+                }
+            } else {
+                const int32_t* table = a.block_table + (long long)req * a.bt_stride;
+                // pages with visible keys; others are neither looked up nor read
+                const int page_begin = sp.lo / kBlockKeys;
+                const int page_end = (sp.hi + kBlockKeys - 1) / kBlockKeys;
+                int win = -1, entry = 0;       // 32 table entries from page `win` on, one a lane
+                auto pages = [&](int t, int& g0, int& g1, int& want) {
+                    const int p = 2 * (j0 + t);
+                    if (win < 0 || p >= win + 32) {
+                        win = p;
+                        long long g = p + lane >= page_begin && p + lane < page_end ? __ldg(table + p + lane) : 0;
+                        if (g < 0 || g >= a.num_pages) {
+                            atomicOr(a.status, kStatusBadBlock);
+                            g = 0;
+                        }
+                        entry = (int)g;
+                    }
+                    g0 = __shfl_sync(0xffffffffu, entry, p - win);
+                    g1 = __shfl_sync(0xffffffffu, entry, p - win + 1);
+                    want = (p >= page_begin && p < page_end ? 1 : 0) | (p + 1 < page_end ? 2 : 0);
+                };
+                auto load = [&](const CUtensorMap* map, int g0, int g1, int want) {
+                    uint32_t dst, fb;
+                    if (!begin_stage(dst, fb)) return false;
+                    if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)(__popc(want) * C::kBlocks * 8192));
+                    __syncwarp();
+                    const int pg = lane / C::kBlocks, kb = lane - pg * C::kBlocks;
+                    if (pg < 2 && ((want >> pg) & 1)) {
+                        tma_load_4d(dst + kb * C::kBlockBytes + pg * 8192, map, fb, kb * 64, 0, head,
+                                    pg ? g1 : g0);
+                    }
+                    return true;
+                };
+                int x0 = 0, y0 = 0, c0 = 0, x1 = 0, y1 = 0, c1 = 0, x2 = 0, y2 = 0, c2 = 0;
+                pages(0, x0, y0, c0);
+                ok = load(&kmap, x0, y0, c0);
+                if (ahead == 2 && n > 1 && ok) {
+                    pages(1, x1, y1, c1);
+                    ok = load(&kmap, x1, y1, c1);
+                }
+                for (int t = 0; t < n && ok; ++t) {
+                    const bool more = t + ahead < n;
+                    if (more) pages(t + ahead, x2, y2, c2);
+                    ok = load(&vmap, x0, y0, c0);
+                    if (ok && more) ok = load(&kmap, x2, y2, c2);
+                    if (ahead == 2) { x0 = x1; y0 = y1; c0 = c1; x1 = x2; y1 = y2; c1 = c2; }
+                    else { x0 = x2; y0 = y2; c0 = c2; }
+                }
+            }
+            // ---- the next item
+            left -= n;
+            j = 0;
+            if (last) {
+                if constexpr (SEL) {
+                    if (++head == a.kv_heads) { head = 0; ++b; }
+                } else {
+                    if (++tile == tiles) {
+                        tile = 0;
+                        if (++head == a.kv_heads) { head = 0; ++b; }
+                    }
+                }
+            }
+        }
+        if (ok) {
+            const int is = item % kItemSlots;
+            ok = warp_wait(itempty0 + 8u * is, ((item / kItemSlots) & 1) ^ 1, abort_flag, a.status);
+            if (ok && lane == 0) {
+                items[is * kItemInts + kItFlags] = kEnd;
+                mbar_arrive(itfull0 + 8u * is);
+            }
+        }
+        // copies in flight land before the CTA may leave
+        for (int t = pos > S ? pos - S : 0; t < pos; ++t)
+            mbar_wait_drain<false>(full_bar(t % S), (uint32_t)((t / S) & 1));
+        if (item > 0) mbar_wait_drain<false>(qfull, (uint32_t)((item - 1) & 1));
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------ MMA issuer
+        constexpr uint32_t kFmt = FP16 ? 0u : 1u;
+        constexpr uint32_t idesc_s = make_idesc(kFmt, kFmt, 128, 128);
+        constexpr uint32_t idesc_o = make_idesc(kFmt, kFmt, 128, D) | (1u << 16);   // B transposed
+        int pos = 0;
+        uint32_t pcount[2] = {0, 0};
+        bool ok = true;
+        auto wait_stage = [&](uint32_t& addr, int& st) {
+            st = pos % S;
+            const bool r = warp_wait(full_bar(st), (uint32_t)((pos / S) & 1), abort_flag, a.status);
+            addr = base + C::kRing + st * C::kStageBytes;
+            ++pos;
+            return r;
+        };
+        auto issue_s = [&](int h, int qh, uint32_t k_addr) {
+            if (lane == 0) {
+                tc_fence_after();
+                const uint32_t q_addr = base + C::kQ + qh * C::kHalfBytes;
+#pragma unroll
+                for (int kb = 0; kb < C::kBlocks; ++kb) {
+                    const uint64_t ad = smem_desc_sw128(q_addr + kb * C::kBlockBytes);
+                    const uint64_t bd = smem_desc_sw128(k_addr + kb * C::kBlockBytes);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_f16(tmem + kColS + 128u * h, ad + 2u * k, bd + 2u * k, idesc_s,
+                                (kb | k) ? 1u : 0u);
+                }
+                mma_commit(sfull0 + 8u * h);
+            }
+            __syncwarp();
+        };
+        auto issue_pv = [&](int h, uint32_t v_addr, bool acc) {
+            if (lane == 0) {
+                tc_fence_after();
+                if (skip_flag[h]) {
+                    skip_flag[h] = 0;          // the group added this tile itself
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_f16_tmem_a(tmem + kColO + 128u * h, tmem + kColS + 128u * h + 8u * k,
+                                       desc_mn_sw128(v_addr + k * 2048, C::kBlockBytes), idesc_o,
+                                       (acc || k) ? 1u : 0u);
+                }
+                mma_commit(pvdone0 + 8u * h);
+            }
+            __syncwarp();
+        };
+        auto release = [&](uint32_t b) {
+            if (lane == 0) mma_commit(b);
+            __syncwarp();
+        };
+        for (int item = 0; ok; ++item) {
+            const int is = item % kItemSlots;
+            ok = warp_wait(itfull0 + 8u * is, (item / kItemSlots) & 1, abort_flag, a.status);
+            if (!ok) break;
+            const int* it = items + is * kItemInts;
+            const int flags = it[kItFlags], n = it[kItN];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(itempty0 + 8u * is);
+            if (flags & kEnd) break;
+            const bool alt = flags & kAlt;
+            ok = warp_wait(qfull, item & 1, abort_flag, a.status);
+            if (!ok) break;
+            uint32_t k_addr, v_addr;
+            int ks, vs;
+            if (!alt) {
+                ok = wait_stage(k_addr, ks);
+                if (!ok) break;
+                issue_s(0, 0, k_addr);
+                issue_s(1, 1, k_addr);
+                release(empty_bar(ks));
+                if (n == 1) release(qempty);
+                for (int t = 0; t < n && ok; ++t) {
+                    ok = wait_stage(v_addr, vs);
+                    if (!ok) break;
+                    for (int h = 0; h < 2 && ok; ++h) {
+                        ok = warp_wait(pready0 + 8u * h, pcount[h] & 1, abort_flag, a.status);
+                        if (ok && t == 0 && h == 0)
+                            ok = warp_wait(oempty, (uint32_t)(item & 1) ^ 1u, abort_flag, a.status);
+                        if (!ok) break;
+                        ++pcount[h];
+                        issue_pv(h, v_addr, t > 0);
+                        if (h == 1) release(empty_bar(vs));
+                        if (t + 1 < n) {
+                            if (h == 0) ok = wait_stage(k_addr, ks);
+                            if (!ok) break;
+                            issue_s(h, h, k_addr);
+                            if (h == 1) {
+                                release(empty_bar(ks));
+                                if (t + 2 == n) release(qempty);
+                            }
+                        }
+                    }
+                }
+            } else {
+                ok = wait_stage(k_addr, ks);
+                if (!ok) break;
+                issue_s(0, 0, k_addr);
+                release(empty_bar(ks));
+                if (n > 1) {
+                    ok = wait_stage(k_addr, ks);
+                    if (!ok) break;
+                    issue_s(1, 0, k_addr);
+                    release(empty_bar(ks));
+                }
+                if (n <= 2) release(qempty);
+                for (int t = 0; t < n && ok; ++t) {
+                    const int h = t & 1;
+                    ok = wait_stage(v_addr, vs);
+                    if (ok) ok = warp_wait(pready0 + 8u * h, pcount[h] & 1, abort_flag, a.status);
+                    if (ok && t == 0)
+                        ok = warp_wait(oempty, (uint32_t)(item & 1) ^ 1u, abort_flag, a.status);
+                    if (!ok) break;
+                    ++pcount[h];
+                    issue_pv(h, v_addr, t > 1);
+                    release(empty_bar(vs));
+                    if (t + 2 < n) {
+                        ok = wait_stage(k_addr, ks);
+                        if (!ok) break;
+                        issue_s(h, 0, k_addr);
+                        release(empty_bar(ks));
+                        if (t + 3 == n) release(qempty);
+                    }
+                }
+            }
+        }
+        // every MMA and every arrival it owes is through before the CTA leaves
+        release(drain);
+        mbar_wait_drain<false>(drain, 0);
+    }
+    } else {
+        regs_inc<kHighRegs>();
+        // ------------------------------------------------------------ softmax
+        const int h = warp >> 2;                 // half
+        const int quad = warp & 3;
+        const int row = quad * 32 + lane;        // row of the half = TMEM lane
+        const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
+        const uint32_t t_s = lane_addr + kColS + 128u * h;
+        const uint32_t t_o = lane_addr + kColO + 128u * h;
+        const float c = a.scale_log2;
+        const int G = a.group;
+        const int row_tok = row / G;
+        const int row_head = row - row_tok * G;
+        uint32_t scount = 0, pvcount = 0, group_phase = 0, alt_phase = 0;
+        int pos_base = 0;
+        bool ok = true;
+        for (int item = 0; ok; ++item) {
+            const int is = item % kItemSlots;
+            ok = warp_wait(itfull0 + 8u * is, (item / kItemSlots) & 1, abort_flag, a.status);
+            if (!ok) break;
+            const int* it = items + is * kItemInts;
+            const int flags = it[kItFlags], n = it[kItN], j0 = it[kItJ0], tok0 = it[kItTok0],
+                      ntok = it[kItNtok], head = it[kItHead], pos0 = it[kItPos0], kv_hi = it[kItKvHi],
+                      item_lo = it[kItLo], item_hi = it[kItHi], slot = it[kItSlot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(itempty0 + 8u * is);
+            if (flags & kEnd) break;
+            const bool alt = flags & kAlt;
+            const int half_tok0 = alt ? 0 : h * a.half_tokens;
+            const int half_ntok = min(a.half_tokens, ntok - half_tok0);
+            const bool valid = row_tok < half_ntok;
+            // warps without a valid row have nothing to compute
+            const bool active = quad * 32 < half_ntok * G;
+            // keys that this row may see, and the range that all rows see
+            int row_lo = item_lo, row_hi = item_hi, all_lo = item_lo, all_hi = item_hi;
+            if constexpr (!SEL) {
+                const int p_first = pos0 + half_tok0, p_last = p_first + half_ntok - 1;
+                const int p_row = p_first + row_tok;
+                if (a.causal) {
+                    row_hi = min(kv_hi, p_row + 1);
+                    all_hi = min(kv_hi, p_first + 1);
+                }
+                if (a.window > 0) {
+                    row_lo = max(0, p_row - a.window + 1);
+                    all_lo = max(0, p_last - a.window + 1);
+                }
+            }
+            const int tiles_here = alt ? (n + 1 - h) / 2 : n;
+            float m = -INFINITY, l = 0.0f;
+            for (int i = 0; i < tiles_here && ok; ++i) {
+                const int t = alt ? 2 * i + h : i;
+                const int key0 = (j0 + t) * kAttnTileKeys;
+                // selected: which of the 128 entries are there (bit k / 4 of word k % 4)
+                uint32_t there[4] = {0, 0, 0, 0};
+                if constexpr (SEL) {
+                    const int32_t* list = a.selected + (long long)tok0 * a.sel_stride;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int at = key0 + 4 * lane + e;
+                        const int p = at < a.sel_k ? __ldg(list + at) : -1;
+                        there[e] = __ballot_sync(0xffffffffu, p >= 0 && p < item_hi);
+                    }
+                }
+                ok = warp_wait(sfull0 + 8u * h, scount & 1, abort_flag, a.status);
+                if (!ok) break;
+                ++scount;
+                tc_fence_after();
+                bool masked;
+                if constexpr (SEL) masked = (there[0] & there[1] & there[2] & there[3]) != 0xffffffffu;
+                else masked = key0 < all_lo || key0 + kAttnTileKeys > all_hi;
+
+                uint32_t x[128];
+                float top = -INFINITY;
+                if (active) {
+                    {
+                        uint32_t(&x0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&x[0]);
+                        uint32_t(&x1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&x[32]);
+                        uint32_t(&x2)[32] = *reinterpret_cast<uint32_t(*)[32]>(&x[64]);
+                        uint32_t(&x3)[32] = *reinterpret_cast<uint32_t(*)[32]>(&x[96]);
+                        tmem_ld32_async(t_s, x0);
+                        tmem_ld32_async(t_s + 32, x1);
+                        tmem_ld32_async(t_s + 64, x2);
+                        tmem_ld32_async(t_s + 96, x3);
+                        tmem_wait_bind32(x0);
+                        tmem_wait_bind32(x1);
+                        tmem_wait_bind32(x2);
+                        tmem_wait_bind32(x3);
+                    }
+                    if (masked) {
+                        const uint32_t kNone = 0xff800000u;    // -inf
+                        if constexpr (SEL) {
+#pragma unroll
+                            for (int k = 0; k < 128; ++k)
+                                if (!((there[k & 3] >> (k >> 2)) & 1u)) x[k] = kNone;
+                        } else {
+                            const int lo = row_lo - key0, hi = row_hi - key0;
+#pragma unroll
+                            for (int k = 0; k < 128; ++k)
+                                if (k < lo || k >= hi) x[k] = kNone;
+                        }
+                    }
+                    float t0 = __uint_as_float(x[0]), t1 = __uint_as_float(x[1]);
+                    float t2 = __uint_as_float(x[2]), t3 = __uint_as_float(x[3]);
+#pragma unroll
+                    for (int k = 4; k < 124; k += 8) {
+                        t0 = fmaxf(t0, fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
+                        t1 = fmaxf(t1, fmaxf(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])));
+                        t2 = fmaxf(t2, fmaxf(__uint_as_float(x[k + 4]), __uint_as_float(x[k + 5])));
+                        t3 = fmaxf(t3, fmaxf(__uint_as_float(x[k + 6]), __uint_as_float(x[k + 7])));
+                    }
+                    t0 = fmaxf(t0, fmaxf(__uint_as_float(x[124]), __uint_as_float(x[125])));
+                    t1 = fmaxf(t1, fmaxf(__uint_as_float(x[126]), __uint_as_float(x[127])));
+                    top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
+                    // a new reference when the old one is too low by 2^8
+                    const float m_new = fmaxf(m, top);
+                    const bool grow = valid && (m_new - m) * c > 8.0f;   // m = -inf: yes unless m_new is
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float f = grow ? exp2_approx((m - m_new) * c) : 1.0f;
+                        if (grow) m = m_new;
+                        l *= f;
+                        if (i > 0) {
+                            ok = warp_wait(pvdone0 + 8u * h, (pvcount - 1) & 1, abort_flag, a.status);
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int d = 0; d < D; d += 32) {
+                                uint32_t o[32];
+                                tmem_ld32_async(t_o + d, o);
+                                tmem_wait_bind32(o);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st32(t_o + d, o);
+                            }
+                        }
+                    }
+                    // c x - c m in one fused product and sum: c m is rounded
+                    // once, a factor that all of the row shares but the next
+                    // reference and the other pieces do not, 2^-15 for |c m|
+                    // up to 2^10.  Past that the difference is taken first.
+                    float mc = m == -INFINITY ? 0.0f : m * c;
+                    if (__any_sync(0xffffffffu, fabsf(mc) > 1024.0f)) {
+                        const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+                        for (int k = 0; k < 128; ++k)
+                            x[k] = __float_as_uint(__uint_as_float(x[k]) - ref);
+                        mc = 0.0f;
+                    }
+                    const uint64_t cc = pack2(c, c), nm = pack2(-mc, -mc);
+                    uint64_t sum[2] = {0, 0};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int k = q * 32 + 2 * e;
+                            uint64_t v = fma2(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), cc, nm);
+                            float lo, hi;
+                            unpack2(v, lo, hi);
+                            lo = exp2_approx(lo);
+                            hi = exp2_approx(hi);
+                            sum[e & 1] = add2(sum[e & 1], pack2(lo, hi));
+                            p[e] = pack16<FP16>(lo, hi);
+                        }
+                        tmem_st16(t_s + 16 * q, p);
+                    }
+                    l += sum2(add2(sum[0], sum[1]));
+                    tmem_wait_st();
+                }
+                // V rows that must not count
+                if (masked) {
+                    const int vpos = t + min(n, t + (alt ? 2 : 1));
+                    const int vp = pos_base + vpos;
+                    const int vs = vp % S;
+                    ok = warp_wait(full_bar(vs), (uint32_t)((vp / S) & 1), abort_flag, a.status);
+                    if (!ok) break;
+                    uint8_t* vt = smem + C::kRing + vs * C::kStageBytes;
+                    // thread = key of the tile
+                    const int key = key0 + row;
+                    bool none;                  // no row of the item sees it
+                    bool some = false;          // some rows of this half do not
+                    if constexpr (SEL) {
+                        none = !((there[row & 3] >> (row >> 2)) & 1u);
+                    } else {
+                        none = key < item_lo || key >= item_hi;
+                        some = !none && (key < all_lo || key >= all_hi);
+                    }
+                    if (none) {
+#pragma unroll
+                        for (int e = 0; e < 8 * C::kBlocks; ++e)
+                            *reinterpret_cast<uint4*>(vt + (e >> 3) * C::kBlockBytes + row * 128 +
+                                                      (((e + row) & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                    }
+                    if constexpr (!SEL) {
+                        bool bad = false;
+                        if (some) {
+                            for (int e = 0; e < 8 * C::kBlocks; ++e) {
+                                const uint4 w = *reinterpret_cast<const uint4*>(
+                                    vt + (e >> 3) * C::kBlockBytes + row * 128 + (((e + row) & 7) << 4));
+                                bad |= not_finite<FP16>(w.x) || not_finite<FP16>(w.y) ||
+                                       not_finite<FP16>(w.z) || not_finite<FP16>(w.w);
+                            }
+                        }
+                        const bool any_bad = __any_sync(0xffffffffu, bad);
+                        const int par = group_phase & 1;
+                        if (lane == 0) {
+                            votes[(h * 2 + par) * 4 + quad] = any_bad ? 1 : 0;
+                            mbar_arrive(group0 + 8u * h);
+                        }
+                        ok = warp_wait(group0 + 8u * h, group_phase & 1, abort_flag, a.status);
+                        if (!ok) break;
+                        ++group_phase;
+                        const volatile int* v4 = votes + (h * 2 + par) * 4;
+                        if (v4[0] | v4[1] | v4[2] | v4[3]) {
+                            // this tile's product, row by row over the keys it
+                            // may see (P as the tensor core would read it)
+                            if (i > 0) {
+                                ok = warp_wait(pvdone0 + 8u * h, (pvcount - 1) & 1, abort_flag, a.status);
+                                if (!ok) break;
+                                tc_fence_after();
+                            }
+                            if (active) {
+                                const int lo = row_lo - key0, hi = row_hi - key0;
+                                for (int d = 0; d < D; d += 8) {
+                                    float acc[8];
+                                    tmem_ld8(t_o + d, acc);
+                                    if (i == 0)
+#pragma unroll
+                                        for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+                                    const uint8_t* col = vt + (d >> 6) * C::kBlockBytes;
+                                    for (int k = 0; k < 128; k += 2) {
+                                        const float2 p = unpack16<FP16>(tmem_ld1(t_s + (k >> 1)));
+#pragma unroll
+                                        for (int b = 0; b < 2; ++b) {
+                                            const int kk = k + b;
+                                            if (kk < lo || kk >= hi) continue;
+                                            const uint4 w = *reinterpret_cast<const uint4*>(
+                                                col + kk * 128 + ((((d & 63) >> 3) ^ (kk & 7)) << 4));
+                                            const float pk = b ? p.y : p.x;
+                                            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                                            for (int e = 0; e < 4; ++e) {
+                                                const float2 vv = unpack16<FP16>(ww[e]);
+                                                acc[2 * e] += pk * vv.x;
+                                                acc[2 * e + 1] += pk * vv.y;
+                                            }
+                                        }
+                                        __syncwarp();
+                                    }
+                                    tmem_st8(t_o + d, acc);
+                                }
+                                tmem_wait_st();
+                            }
+                            if (row == 0) skip_flag[h] = 1;
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pready0 + 8u * h);
+                ++pvcount;
+            }
+            if (!ok) break;
+            pos_base += 2 * n;
+
+            // ---------------------------------------------------- the item's end
+            if (tiles_here > 0) {
+                ok = warp_wait(pvdone0 + 8u * h, (pvcount - 1) & 1, abort_flag, a.status);
+                if (!ok) break;
+            }
+            tc_fence_after();
+            const int token = tok0 + half_tok0 + row_tok;
+            const bool whole = flags & kWhole;
+            const int qhead = head * G + row_head;
+            const long long ws_row = ((long long)blockIdx.x * 2 + slot) * kAttnSlotRows +
+                                     (alt ? 0 : h * kAttnHalfRows) + row;
+            if (!alt) {
+                if (active) {
+                    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+                    uint16_t* orow = static_cast<uint16_t*>(a.out) + (long long)token * a.out_token +
+                                     (long long)qhead * a.out_head;
+                    float* prow = a.partial + ws_row * D;
+#pragma unroll
+                    for (int d = 0; d < D; d += 32) {
+                        uint32_t o[32];
+                        tmem_ld32_async(t_o + d, o);
+                        tmem_wait_bind32(o);
+                        if (valid) {
+                            if (whole) {
+#pragma unroll
+                                for (int e = 0; e < 32; e += 8) {
+                                    uint32_t w[4];
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k)
+                                        w[k] = pack16<FP16>(__uint_as_float(o[e + 2 * k]) * inv,
+                                                            __uint_as_float(o[e + 2 * k + 1]) * inv);
+                                    *reinterpret_cast<uint4*>(orow + d + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                                }
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 32; e += 4)
+                                    *reinterpret_cast<uint4*>(prow + d + e) =
+                                        make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                            }
+                        }
+                    }
+                    if (valid) {
+                        if (!whole) a.stats[ws_row] = make_float2(m, l);
+                        else if (a.lse != nullptr)
+                            a.lse[(long long)token * a.kv_heads * G + qhead] =
+                                l == 0.0f ? -INFINITY : m * a.scale + logf(l);
+                    }
+                }
+            } else {
+                // both halves hold these rows: group h writes columns h D/2 ..
+                stats[h * 128 + row] = make_float2(m, l);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(altbar);
+                ok = warp_wait(altbar, alt_phase & 1, abort_flag, a.status);
+                if (!ok) break;
+                ++alt_phase;
+                tc_fence_after();
+                if (active) {
+                    const float2 s0 = stats[row], s1 = stats[128 + row];
+                    const float top = fmaxf(s0.x, s1.x);
+                    const float f0 = s0.x == -INFINITY ? 0.0f : exp2_approx((s0.x - top) * c);
+                    const float f1 = s1.x == -INFINITY ? 0.0f : exp2_approx((s1.x - top) * c);
+                    const float sum = s0.y * f0 + s1.y * f1;
+                    const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+                    const float g0 = whole ? f0 * inv : f0, g1 = whole ? f1 * inv : f1;
+                    uint16_t* orow = static_cast<uint16_t*>(a.out) + (long long)token * a.out_token +
+                                     (long long)qhead * a.out_head;
+                    float* prow = a.partial + ws_row * D;
+#pragma unroll
+                    for (int dd = 0; dd < D / 2; dd += 32) {
+                        const int d = h * (D / 2) + dd;
+                        uint32_t o[32], u[32];
+                        tmem_ld32_async(lane_addr + kColO + d, o);
+                        tmem_ld32_async(lane_addr + kColO + 128u + d, u);
+                        tmem_wait_bind32(o);
+                        tmem_wait_bind32(u);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            float v = __uint_as_float(o[e]) * g0;
+                            if (n > 1) v = fmaf(__uint_as_float(u[e]), g1, v);   // half 1 saw a tile
+                            o[e] = __float_as_uint(v);
+                        }
+                        if (valid) {
+                            if (whole) {
+#pragma unroll
+                                for (int e = 0; e < 32; e += 8) {
+                                    uint32_t w[4];
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k)
+                                        w[k] = pack16<FP16>(__uint_as_float(o[e + 2 * k]),
+                                                            __uint_as_float(o[e + 2 * k + 1]));
+                                    *reinterpret_cast<uint4*>(orow + d + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                                }
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 32; e += 4)
+                                    *reinterpret_cast<uint4*>(prow + d + e) =
+                                        make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                            }
+                        }
+                    }
+                    if (valid && h == 0) {
+                        if (!whole) a.stats[ws_row] = make_float2(top, sum);
+                        else if (a.lse != nullptr)
+                            a.lse[(long long)token * a.kv_heads * G + qhead] =
+                                sum == 0.0f ? -INFINITY : top * a.scale + logf(sum);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(oempty);
+        }
+    }
+
+    // ---------------------------------------------------------------- teardown
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D, bool FP16, bool SEL>
+cudaError_t launch_kernel(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                          const AttnArgs& a, int num_ctas, cudaStream_t stream)
+{
+    auto kernel = paged_attention_kernel<D, FP16, SEL>;
+    static int configured_device = -1;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (configured_device != dev) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kTotal);
+        if (e != cudaSuccess) return e;
+        // the warpgroups' shares must fit the block's allocation, else the
+        // softmax groups' setmaxnreg.inc would wait forever
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, kernel);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs != kLaunchRegs || 2 * kHighRegs + kLowRegs > 3 * kLaunchRegs)
+            return cudaErrorInvalidConfiguration;
+        configured_device = dev;
+    }
+    kernel<<<num_ctas, kThreads, Cfg<D>::kTotal, stream>>>(qmap, kmap, vmap, a);
+    return cudaGetLastError();
+}
+
+}  // namespace attn
+}  // namespace pml

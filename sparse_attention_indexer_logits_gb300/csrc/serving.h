@@ -140,6 +140,51 @@ struct CopyPagesArgs {
     int vec;                   // bytes per access: 16, 4 or 1
 };
 
+// Attention of new tokens over pages.  Rows of a tile are (token, head of the
+// kv head's group): row = token * group + head.
+constexpr int kAttnTileKeys = 128;     // keys of a tile: two pages, or 128 list entries
+constexpr int kAttnHalfRows = 128;     // rows of one MMA accumulator
+constexpr int kAttnSlotRows = 2 * kAttnHalfRows;
+constexpr int kAttnMaxBatch = 16384;
+
+struct AttnArgs {
+    const int32_t* block_table;
+    const int32_t* kv_lens;        // per request
+    const int32_t* cu_q;           // batch + 1 token offsets; null: q_per_request each
+    const int32_t* requests;       // selected: one per token
+    const int32_t* selected;       // selected: [tokens][sel_stride] positions
+    void* out;
+    float* lse;                    // [tokens][heads], may be null
+    unsigned int* status;
+    int* pieces;                   // workspace: [num_ctas][2][kPieceInts]
+    float2* stats;                 // workspace: [num_ctas][2][kAttnSlotRows] (maximum, sum)
+    float* partial;                // workspace: [num_ctas][2][kAttnSlotRows][head_dim]
+    long long bt_stride;
+    long long sel_stride;
+    long long out_token, out_head; // elements
+    long long num_pages;
+    int bt_width;
+    int batch;                     // requests (rows of the block table when selected)
+    int tokens;
+    int q_per_request;
+    int kv_heads;
+    int group;                     // query heads per kv head
+    int half_tokens;               // tokens of a 128-row half: 128 / group
+    int sel_k;                     // selected: entries per token
+    int sel_page_rows, sel_slot_rows, sel_head_rows;   // selected: row strides in the cache's
+    int sel_page_rows_v, sel_slot_rows_v, sel_head_rows_v;  // [rows][head_dim] view
+    int causal;
+    int window;                    // > 0: only keys past position - window
+    float scale_log2;              // softmax scale * log2(e)
+    float scale;
+};
+
+constexpr int kPieceInts = 8;
+
+cudaError_t launch_paged_attention(int head_dim, bool fp16, bool select, const CUtensorMap& qmap,
+                                   const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                   const AttnArgs& a, int num_ctas, cudaStream_t stream);
+
 cudaError_t launch_pages_fork(const ForkArgs& a, cudaStream_t stream);
 cudaError_t launch_pages_extend(const ExtendArgs& a, cudaStream_t stream);
 cudaError_t launch_pages_free(const FreeArgs& a, cudaStream_t stream);

@@ -66,9 +66,14 @@ def attention(q, k, v, allowed, scale):
     the sum, and the weighted magnitudes sum_j p_j |v_j| that errors scale with."""
     s = (q.double() @ k.double().T) * scale
     s = s.masked_fill(~allowed, -math.inf)
-    lse = torch.logsumexp(s, dim=1) if s.shape[1] else torch.full((s.shape[0],), -math.inf,
-                                                                  dtype=torch.float64)
-    p = torch.exp(s - lse.clamp(min=-1e300)[:, None])
+    if s.shape[1] == 0:
+        s = torch.full((s.shape[0], 1), -math.inf, dtype=torch.float64)
+        v, allowed = torch.zeros((1, v.shape[1])), torch.zeros((s.shape[0], 1), dtype=torch.bool)
+    top = s.amax(1).clamp(min=-1e300)
+    e = torch.exp(s - top[:, None])
+    total = e.sum(1)
+    lse = top + total.log()
+    p = e / total.clamp(min=1e-300)[:, None]
     vv = torch.where(allowed.any(0)[:, None], v.double(), 0.0)
     # a masked key contributes nothing, whatever its value holds
     bad = ~torch.isfinite(vv)
