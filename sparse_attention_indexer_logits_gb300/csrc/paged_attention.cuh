@@ -79,6 +79,75 @@ __device__ __forceinline__ bool warp_wait(uint32_t b, uint32_t parity, volatile 
     return __all_sync(0xffffffffu, mbar_wait<false>(b, parity, abort, status));
 }
 
+// Waits until the producer has begun to fill a stage for place `pos` of the
+// ring.  A parity alone does not tell place pos from pos - 2 S: a thread that
+// does not wait for every place of the ring (the halves take turns) may look
+// at a stage whose previous copy, the other half's, has not even landed.
+// Once the stage is pos's, its previous copy has been consumed, and the
+// parity of pos means pos.
+__device__ __forceinline__ bool stage_begun(const volatile int* begun, int pos, volatile int* abort,
+                                            unsigned int* status)
+{
+    if (*begun == pos) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t it = 1; *begun != pos; ++it) {
+        if ((it & 31u) == 0) {
+            if (*abort) return false;
+            if (global_timer_ns() - t0 > kWaitLimitNs) {
+                atomicOr(status, kStatusWaitTimeout);
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+    return true;
+}
+
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ void st_release_shared(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// Waits until the four warps of a group have written their part of the
+// group's tile number `count` (each says so in its word); skip: the group has
+// added the tile's product itself (all four say the same).
+__device__ __forceinline__ bool p_written(uint32_t words, uint32_t count, bool& skip,
+                                          volatile int* abort, unsigned int* status)
+{
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        const uint4 w = ld_shared_v4(words);
+        if ((w.x >> 1) == count && (w.y >> 1) == count && (w.z >> 1) == count && (w.w >> 1) == count) {
+            asm volatile("fence.acq_rel.cta;" ::: "memory");
+            skip = w.x & 1u;
+            return true;
+        }
+        if ((it & 255u) == 0) {
+            if (*abort) return false;
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > kWaitLimitNs) {
+                atomicOr(status, kStatusWaitTimeout);
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+
 template <int D>
 struct Cfg {
     static constexpr int kBlocks = D / 64;                     // 128-byte column blocks
@@ -90,13 +159,13 @@ struct Cfg {
     static constexpr int kRing = kQ + 2 * kHalfBytes;
     static constexpr int kStats = kRing + kStages * kStageBytes;      // float2 [2][128]
     static constexpr int kBars = kStats + 2 * 128 * 8;
-    // barriers: full, empty per stage; q full, q empty; s full, p ready, pv
-    // done, group sync per half; o empty, alt sync; item full, item empty; the
-    // MMA warp's last commit
-    static constexpr int kNumBars = 2 * kStages + 2 + 8 + 2 + 2 * kItemSlots + 1;
+    // barriers: full, empty per stage; q full, q empty; s full, pv done, group
+    // sync per half; o empty, alt sync; item full, item empty; the issuer's
+    // last commit
+    static constexpr int kNumBars = 2 * kStages + 2 + 6 + 2 + 2 * kItemSlots + 1;
     static constexpr int kItems = (kBars + kNumBars * 8 + 15) / 16 * 16;
     static constexpr int kMisc = kItems + kItemSlots * kItemInts * 4;
-    static constexpr int kTotal = kMisc + 128;
+    static constexpr int kTotal = kMisc + 192;
 };
 
 constexpr uint32_t kColS = 0;      // S_h at 128 h; P_h over its first 64 columns
@@ -290,14 +359,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto full_bar = [&](int s) { return bar + 8u * s; };
     auto empty_bar = [&](int s) { return bar + 8u * (S + s); };
     const uint32_t qfull = bar + 8u * (2 * S), qempty = qfull + 8u;
-    const uint32_t sfull0 = qfull + 16u, pready0 = sfull0 + 16u, pvdone0 = pready0 + 16u,
+    const uint32_t sfull0 = qfull + 16u, pvdone0 = sfull0 + 16u,
                    group0 = pvdone0 + 16u, oempty = group0 + 16u, altbar = oempty + 8u,
                    itfull0 = altbar + 8u, itempty0 = itfull0 + 8u * kItemSlots, drain = itempty0 + 8u * kItemSlots;
     int* items = reinterpret_cast<int*>(smem + C::kItems);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMisc + 4);
-    volatile int* skip_flag = reinterpret_cast<volatile int*>(smem + C::kMisc + 8);   // [2]
     volatile int* votes = reinterpret_cast<volatile int*>(smem + C::kMisc + 16);      // [2][2][4]
+    // P written by warp w of half h: 2 * tiles, + 1 if this tile's product with V
+    // has been added already
+    const uint32_t ready0 = base + C::kMisc + 128;
+    volatile uint32_t* ready = reinterpret_cast<volatile uint32_t*>(smem + C::kMisc + 128);   // [2][4]
+    volatile int* begun = reinterpret_cast<volatile int*>(smem + C::kMisc + 80);      // [S]
     float2* stats = reinterpret_cast<float2*>(smem + C::kStats);
 
     const int warp = threadIdx.x >> 5;
@@ -305,21 +378,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         *abort_flag = 0;
-        skip_flag[0] = 0;
-        skip_flag[1] = 0;
         for (int s = 0; s < S; ++s) {
+            begun[s] = -1;
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
         }
         mbar_init(qfull, 1);
         mbar_init(qempty, 1);
+        mbar_init(drain, 1);
         for (int h = 0; h < 2; ++h) {
             mbar_init(sfull0 + 8u * h, 1);
-            mbar_init(pready0 + 8u * h, 4);
             mbar_init(pvdone0 + 8u * h, 1);
             mbar_init(group0 + 8u * h, 4);
+            for (int w = 0; w < 4; ++w) ready[4 * h + w] = 0;
         }
-        mbar_init(drain, 1);
         mbar_init(oempty, 8);
         mbar_init(altbar, 8);
         for (int i = 0; i < kItemSlots; ++i) {
@@ -518,6 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool r = warp_wait(empty_bar(s), (uint32_t)((pos / S) & 1) ^ 1u, abort_flag, a.status);
                 dst = base + C::kRing + s * C::kStageBytes;
                 fb = full_bar(s);
+                if (r && lane == 0) begun[s] = pos;
                 ++pos;
                 return r;
             };
@@ -653,134 +726,148 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (item > 0) mbar_wait_drain<false>(qfull, (uint32_t)((item - 1) & 1));
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issuer
-        constexpr uint32_t kFmt = FP16 ? 0u : 1u;
-        constexpr uint32_t idesc_s = make_idesc(kFmt, kFmt, 128, 128);
-        constexpr uint32_t idesc_o = make_idesc(kFmt, kFmt, 128, D) | (1u << 16);   // B transposed
-        int pos = 0;
-        uint32_t pcount[2] = {0, 0};
-        bool ok = true;
-        auto wait_stage = [&](uint32_t& addr, int& st) {
-            st = pos % S;
-            const bool r = warp_wait(full_bar(st), (uint32_t)((pos / S) & 1), abort_flag, a.status);
-            addr = base + C::kRing + st * C::kStageBytes;
-            ++pos;
-            return r;
-        };
-        auto issue_s = [&](int h, int qh, uint32_t k_addr) {
-            if (lane == 0) {
-                tc_fence_after();
-                const uint32_t q_addr = base + C::kQ + qh * C::kHalfBytes;
+        // One thread, and nothing between two products that can be elsewhere:
+        // issuing takes as long as the tensor core does, so whatever the
+        // thread waits for, the tensor core waits for too.  A wait on an
+        // mbarrier costs it some 230 cycles even when the phase is over; so
+        // the stages of the next step are tested while products are being
+        // issued, and P is announced by plain shared-memory words.
+        if (lane == 0) {
+            constexpr uint32_t kFmt = FP16 ? 0u : 1u;
+            constexpr uint32_t idesc_s = make_idesc(kFmt, kFmt, 128, 128);
+            constexpr uint32_t idesc_o = make_idesc(kFmt, kFmt, 128, D) | (1u << 16);   // B transposed
+            const uint64_t q_desc = smem_desc_sw128(base + C::kQ);
+            const uint64_t k_desc = smem_desc_sw128(base + C::kRing);
+            const uint64_t v_desc = desc_mn_sw128(base + C::kRing, C::kBlockBytes);
+            uint32_t stage = 0, phase = 0;       // the next stage to be consumed
+            uint32_t pcount[2] = {0, 0};         // P tiles consumed
+            bool ok = true;
+            auto wait = [&](uint32_t b, uint32_t parity) {
+                return mbar_wait<false>(b, parity, abort_flag, a.status);
+            };
+            // takes the next stage of the ring; its barrier and parity
+            struct Next {
+                uint32_t st, parity;
+                bool there;
+            };
+            auto take = [&]() {
+                Next x = {stage, phase, false};
+                if (++stage == S) { stage = 0; phase ^= 1; }
+                return x;
+            };
+            auto test = [&](Next& x) { x.there = mbar_test(full_bar(x.st), x.parity); };
+            auto landed = [&](const Next& x) { return x.there || wait(full_bar(x.st), x.parity); };
+            auto issue_s = [&](int h, int qh, uint32_t st) {
+                const uint64_t ad = q_desc + (uint32_t)(qh * (C::kHalfBytes >> 4));
+                const uint64_t bd = k_desc + st * (uint32_t)(C::kStageBytes >> 4);
 #pragma unroll
-                for (int kb = 0; kb < C::kBlocks; ++kb) {
-                    const uint64_t ad = smem_desc_sw128(q_addr + kb * C::kBlockBytes);
-                    const uint64_t bd = smem_desc_sw128(k_addr + kb * C::kBlockBytes);
+                for (int kb = 0; kb < C::kBlocks; ++kb)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_f16(tmem + kColS + 128u * h, ad + 2u * k, bd + 2u * k, idesc_s,
+                        mma_f16(tmem + kColS + 128u * h, ad + (uint32_t)(kb * (C::kBlockBytes >> 4) + 2 * k),
+                                bd + (uint32_t)(kb * (C::kBlockBytes >> 4) + 2 * k), idesc_s,
                                 (kb | k) ? 1u : 0u);
-                }
                 mma_commit(sfull0 + 8u * h);
-            }
-            __syncwarp();
-        };
-        auto issue_pv = [&](int h, uint32_t v_addr, bool acc) {
-            if (lane == 0) {
+            };
+            // P of half h's next tile: the group's four warps have written it
+            auto wait_p = [&](int h, bool& skip) {
+                return p_written(ready0 + 16u * h, ++pcount[h], skip, abort_flag, a.status);
+            };
+            auto issue_pv = [&](int h, uint32_t st, bool acc, bool skip) {
                 tc_fence_after();
-                if (skip_flag[h]) {
-                    skip_flag[h] = 0;          // the group added this tile itself
-                } else {
+                if (!skip) {                     // else the group added this tile itself
+                    const uint64_t bd = v_desc + st * (uint32_t)(C::kStageBytes >> 4);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         mma_f16_tmem_a(tmem + kColO + 128u * h, tmem + kColS + 128u * h + 8u * k,
-                                       desc_mn_sw128(v_addr + k * 2048, C::kBlockBytes), idesc_o,
-                                       (acc || k) ? 1u : 0u);
+                                       bd + (uint32_t)(k * (2048 >> 4)), idesc_o, (acc || k) ? 1u : 0u);
                 }
                 mma_commit(pvdone0 + 8u * h);
-            }
-            __syncwarp();
-        };
-        auto release = [&](uint32_t b) {
-            if (lane == 0) mma_commit(b);
-            __syncwarp();
-        };
-        for (int item = 0; ok; ++item) {
-            const int is = item % kItemSlots;
-            ok = warp_wait(itfull0 + 8u * is, (item / kItemSlots) & 1, abort_flag, a.status);
-            if (!ok) break;
-            const int* it = items + is * kItemInts;
-            const int flags = it[kItFlags], n = it[kItN];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(itempty0 + 8u * is);
-            if (flags & kEnd) break;
-            const bool alt = flags & kAlt;
-            ok = warp_wait(qfull, item & 1, abort_flag, a.status);
-            if (!ok) break;
-            uint32_t k_addr, v_addr;
-            int ks, vs;
-            if (!alt) {
-                ok = wait_stage(k_addr, ks);
+            };
+            for (int item = 0; ok; ++item) {
+                const int is = item % kItemSlots;
+                ok = wait(itfull0 + 8u * is, (item / kItemSlots) & 1);
                 if (!ok) break;
-                issue_s(0, 0, k_addr);
-                issue_s(1, 1, k_addr);
-                release(empty_bar(ks));
-                if (n == 1) release(qempty);
-                for (int t = 0; t < n && ok; ++t) {
-                    ok = wait_stage(v_addr, vs);
-                    if (!ok) break;
-                    for (int h = 0; h < 2 && ok; ++h) {
-                        ok = warp_wait(pready0 + 8u * h, pcount[h] & 1, abort_flag, a.status);
-                        if (ok && t == 0 && h == 0)
-                            ok = warp_wait(oempty, (uint32_t)(item & 1) ^ 1u, abort_flag, a.status);
+                const volatile int* it = items + is * kItemInts;
+                const int flags = it[kItFlags], n = it[kItN];
+                mbar_arrive(itempty0 + 8u * is);
+                if (flags & kEnd) break;
+                const bool alt = flags & kAlt;
+                bool skip = false;
+                Next ks = take();
+                ok = wait(qfull, item & 1) && landed(ks);
+                if (!ok) break;
+                tc_fence_after();
+                issue_s(0, 0, ks.st);
+                if (!alt) {
+                    issue_s(1, 1, ks.st);
+                    mma_commit(empty_bar(ks.st));
+                    if (n == 1) mma_commit(qempty);
+                    ok = wait(oempty, (uint32_t)(item & 1) ^ 1u);
+                    Next vs = take();
+                    if (n > 1) ks = take();
+                    for (int t = 0; t < n && ok; ++t) {
+                        const bool more = t + 1 < n;
+                        ok = landed(vs) && (!more || landed(ks)) && wait_p(0, skip);
                         if (!ok) break;
-                        ++pcount[h];
-                        issue_pv(h, v_addr, t > 0);
-                        if (h == 1) release(empty_bar(vs));
+                        issue_pv(0, vs.st, t > 0, skip);
+                        // the next step's stages, in the order they are filled
+                        const uint32_t v0 = vs.st, k0 = ks.st;
+                        if (more) {
+                            vs = take();
+                            test(vs);
+                            if (t + 2 < n) { ks = take(); test(ks); }
+                            issue_s(0, 0, k0);
+                        }
+                        ok = wait_p(1, skip);
+                        if (!ok) break;
+                        issue_pv(1, v0, t > 0, skip);
+                        mma_commit(empty_bar(v0));
+                        if (more) {
+                            issue_s(1, 1, k0);
+                            mma_commit(empty_bar(k0));
+                            if (t + 2 == n) mma_commit(qempty);
+                        }
+                    }
+                } else {
+                    mma_commit(empty_bar(ks.st));
+                    if (n > 1) {
+                        ks = take();
+                        ok = landed(ks);
+                        if (!ok) break;
+                        issue_s(1, 0, ks.st);
+                        mma_commit(empty_bar(ks.st));
+                    }
+                    if (n <= 2) mma_commit(qempty);
+                    ok = wait(oempty, (uint32_t)(item & 1) ^ 1u);
+                    Next vs = take();
+                    if (n > 2) ks = take();
+                    for (int t = 0; t < n && ok; ++t) {
+                        const int h = t & 1;
+                        const bool more = t + 2 < n;
+                        ok = landed(vs) && (!more || landed(ks)) && wait_p(h, skip);
+                        if (!ok) break;
+                        issue_pv(h, vs.st, t > 1, skip);
+                        mma_commit(empty_bar(vs.st));
+                        const uint32_t k0 = ks.st;
                         if (t + 1 < n) {
-                            if (h == 0) ok = wait_stage(k_addr, ks);
-                            if (!ok) break;
-                            issue_s(h, h, k_addr);
-                            if (h == 1) {
-                                release(empty_bar(ks));
-                                if (t + 2 == n) release(qempty);
-                            }
+                            vs = take();
+                            test(vs);
+                            if (t + 3 < n) { ks = take(); test(ks); }
+                        }
+                        if (more) {
+                            issue_s(h, 0, k0);
+                            mma_commit(empty_bar(k0));
+                            if (t + 3 == n) mma_commit(qempty);
                         }
                     }
                 }
-            } else {
-                ok = wait_stage(k_addr, ks);
-                if (!ok) break;
-                issue_s(0, 0, k_addr);
-                release(empty_bar(ks));
-                if (n > 1) {
-                    ok = wait_stage(k_addr, ks);
-                    if (!ok) break;
-                    issue_s(1, 0, k_addr);
-                    release(empty_bar(ks));
-                }
-                if (n <= 2) release(qempty);
-                for (int t = 0; t < n && ok; ++t) {
-                    const int h = t & 1;
-                    ok = wait_stage(v_addr, vs);
-                    if (ok) ok = warp_wait(pready0 + 8u * h, pcount[h] & 1, abort_flag, a.status);
-                    if (ok && t == 0)
-                        ok = warp_wait(oempty, (uint32_t)(item & 1) ^ 1u, abort_flag, a.status);
-                    if (!ok) break;
-                    ++pcount[h];
-                    issue_pv(h, v_addr, t > 1);
-                    release(empty_bar(vs));
-                    if (t + 2 < n) {
-                        ok = wait_stage(k_addr, ks);
-                        if (!ok) break;
-                        issue_s(h, 0, k_addr);
-                        release(empty_bar(ks));
-                        if (t + 3 == n) release(qempty);
-                    }
-                }
             }
+            // every MMA and every arrival it owes is through before the CTA leaves
+            mma_commit(drain);
+            mbar_wait_drain<false>(drain, 0);
         }
-        // every MMA and every arrival it owes is through before the CTA leaves
-        release(drain);
-        mbar_wait_drain<false>(drain, 0);
+        __syncwarp();
     }
     } else {
         regs_inc<kHighRegs>();
@@ -802,23 +889,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int is = item % kItemSlots;
             ok = warp_wait(itfull0 + 8u * is, (item / kItemSlots) & 1, abort_flag, a.status);
             if (!ok) break;
-            const int* it = items + is * kItemInts;
-            const int flags = it[kItFlags], n = it[kItN], j0 = it[kItJ0], tok0 = it[kItTok0],
-                      ntok = it[kItNtok], head = it[kItHead], pos0 = it[kItPos0], kv_hi = it[kItKvHi],
-                      item_lo = it[kItLo], item_hi = it[kItHi], slot = it[kItSlot];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(itempty0 + 8u * is);
-            if (flags & kEnd) break;
-            const bool alt = flags & kAlt;
+            // (read again where they are needed: the slot is released at the
+            // item's end, and the registers are the row of S's)
+            const volatile int* it = items + is * kItemInts;
+            if (it[kItFlags] & kEnd) break;
+            const bool alt = it[kItFlags] & kAlt;
+            const int n = it[kItN], j0 = it[kItJ0];
             const int half_tok0 = alt ? 0 : h * a.half_tokens;
-            const int half_ntok = min(a.half_tokens, ntok - half_tok0);
+            const int half_ntok = min(a.half_tokens, it[kItNtok] - half_tok0);
             const bool valid = row_tok < half_ntok;
             // warps without a valid row have nothing to compute
             const bool active = quad * 32 < half_ntok * G;
             // keys that this row may see, and the range that all rows see
-            int row_lo = item_lo, row_hi = item_hi, all_lo = item_lo, all_hi = item_hi;
+            int row_lo = it[kItLo], row_hi = it[kItHi], all_lo = row_lo, all_hi = row_hi;
             if constexpr (!SEL) {
-                const int p_first = pos0 + half_tok0, p_last = p_first + half_ntok - 1;
+                const int kv_hi = it[kItKvHi];
+                const int p_first = it[kItPos0] + half_tok0, p_last = p_first + half_ntok - 1;
                 const int p_row = p_first + row_tok;
                 if (a.causal) {
                     row_hi = min(kv_hi, p_row + 1);
@@ -837,7 +923,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // selected: which of the 128 entries are there (bit k / 4 of word k % 4)
                 uint32_t there[4] = {0, 0, 0, 0};
                 if constexpr (SEL) {
-                    const int32_t* list = a.selected + (long long)tok0 * a.sel_stride;
+                    const int32_t* list = a.selected + (long long)it[kItTok0] * a.sel_stride;
+                    const int item_hi = it[kItHi];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int at = key0 + 4 * lane + e;
@@ -853,48 +940,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (SEL) masked = (there[0] & there[1] & there[2] & there[3]) != 0xffffffffu;
                 else masked = key0 < all_lo || key0 + kAttnTileKeys > all_hi;
 
-                uint32_t x[128];
-                float top = -INFINITY;
                 if (active) {
-                    {
-                        uint32_t(&x0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&x[0]);
-                        uint32_t(&x1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&x[32]);
-                        uint32_t(&x2)[32] = *reinterpret_cast<uint32_t(*)[32]>(&x[64]);
-                        uint32_t(&x3)[32] = *reinterpret_cast<uint32_t(*)[32]>(&x[96]);
-                        tmem_ld32_async(t_s, x0);
-                        tmem_ld32_async(t_s + 32, x1);
-                        tmem_ld32_async(t_s + 64, x2);
-                        tmem_ld32_async(t_s + 96, x3);
-                        tmem_wait_bind32(x0);
-                        tmem_wait_bind32(x1);
-                        tmem_wait_bind32(x2);
-                        tmem_wait_bind32(x3);
-                    }
+                    uint32_t x[4][32];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_ld32_async(t_s + 32 * q, x[q]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_wait_bind32(x[q]);
                     if (masked) {
                         const uint32_t kNone = 0xff800000u;    // -inf
-                        if constexpr (SEL) {
+                        const int lo = row_lo - key0, hi = row_hi - key0;
 #pragma unroll
-                            for (int k = 0; k < 128; ++k)
-                                if (!((there[k & 3] >> (k >> 2)) & 1u)) x[k] = kNone;
-                        } else {
-                            const int lo = row_lo - key0, hi = row_hi - key0;
-#pragma unroll
-                            for (int k = 0; k < 128; ++k)
-                                if (k < lo || k >= hi) x[k] = kNone;
+                        for (int k = 0; k < 128; ++k) {
+                            if constexpr (SEL) {
+                                if (!((there[k & 3] >> (k >> 2)) & 1u)) x[k >> 5][k & 31] = kNone;
+                            } else {
+                                if (k < lo || k >= hi) x[k >> 5][k & 31] = kNone;
+                            }
                         }
                     }
-                    float t0 = __uint_as_float(x[0]), t1 = __uint_as_float(x[1]);
-                    float t2 = __uint_as_float(x[2]), t3 = __uint_as_float(x[3]);
+                    float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int k = 4; k < 124; k += 8) {
-                        t0 = fmaxf(t0, fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
-                        t1 = fmaxf(t1, fmaxf(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])));
-                        t2 = fmaxf(t2, fmaxf(__uint_as_float(x[k + 4]), __uint_as_float(x[k + 5])));
-                        t3 = fmaxf(t3, fmaxf(__uint_as_float(x[k + 6]), __uint_as_float(x[k + 7])));
-                    }
-                    t0 = fmaxf(t0, fmaxf(__uint_as_float(x[124]), __uint_as_float(x[125])));
-                    t1 = fmaxf(t1, fmaxf(__uint_as_float(x[126]), __uint_as_float(x[127])));
-                    top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
+                    for (int k = 0; k < 128; k += 2)
+                        t[(k >> 1) & 3] = fmaxf(t[(k >> 1) & 3], fmaxf(__uint_as_float(x[k >> 5][k & 31]),
+                                                                       __uint_as_float(x[k >> 5][(k & 31) + 1])));
+                    const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
                     // a new reference when the old one is too low by 2^8
                     const float m_new = fmaxf(m, top);
                     const bool grow = valid && (m_new - m) * c > 8.0f;   // m = -inf: yes unless m_new is
@@ -906,14 +975,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ok = warp_wait(pvdone0 + 8u * h, (pvcount - 1) & 1, abort_flag, a.status);
                             if (!ok) break;
                             tc_fence_after();
+                            // eight columns at a time: the row of S stays in registers
+#pragma unroll 1
+                            for (int d = 0; d < D; d += 8) {
+                                float o[8];
+                                tmem_ld8(t_o + d, o);
 #pragma unroll
-                            for (int d = 0; d < D; d += 32) {
-                                uint32_t o[32];
-                                tmem_ld32_async(t_o + d, o);
-                                tmem_wait_bind32(o);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                tmem_st32(t_o + d, o);
+                                for (int e = 0; e < 8; ++e) o[e] *= f;
+                                tmem_st8(t_o + d, o);
                             }
                         }
                     }
@@ -922,22 +991,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // reference and the other pieces do not, 2^-15 for |c m|
                     // up to 2^10.  Past that the difference is taken first.
                     float mc = m == -INFINITY ? 0.0f : m * c;
+                    const float ref = m == -INFINITY ? 0.0f : m;
                     if (__any_sync(0xffffffffu, fabsf(mc) > 1024.0f)) {
-                        const float ref = m == -INFINITY ? 0.0f : m;
 #pragma unroll
                         for (int k = 0; k < 128; ++k)
-                            x[k] = __float_as_uint(__uint_as_float(x[k]) - ref);
+                            x[k >> 5][k & 31] = __float_as_uint(__uint_as_float(x[k >> 5][k & 31]) - ref);
                         mc = 0.0f;
                     }
                     const uint64_t cc = pack2(c, c), nm = pack2(-mc, -mc);
                     uint64_t sum[2] = {0, 0};
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
+                        uint32_t(&y)[32] = x[q];
                         uint32_t p[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const int k = q * 32 + 2 * e;
-                            uint64_t v = fma2(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), cc, nm);
+                            const uint64_t v =
+                                fma2(pack2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])), cc, nm);
                             float lo, hi;
                             unpack2(v, lo, hi);
                             lo = exp2_approx(lo);
@@ -951,15 +1021,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_wait_st();
                 }
                 // V rows that must not count
+                bool added = false;             // this tile's product is in O already
                 if (masked) {
                     const int vpos = t + min(n, t + (alt ? 2 : 1));
                     const int vp = pos_base + vpos;
                     const int vs = vp % S;
-                    ok = warp_wait(full_bar(vs), (uint32_t)((vp / S) & 1), abort_flag, a.status);
+                    ok = __all_sync(0xffffffffu, stage_begun(begun + vs, vp, abort_flag, a.status)) &&
+                         warp_wait(full_bar(vs), (uint32_t)((vp / S) & 1), abort_flag, a.status);
                     if (!ok) break;
                     uint8_t* vt = smem + C::kRing + vs * C::kStageBytes;
                     // thread = key of the tile
                     const int key = key0 + row;
+                    const int item_lo = it[kItLo], item_hi = it[kItHi];
                     bool none;                  // no row of the item sees it
                     bool some = false;          // some rows of this half do not
                     if constexpr (SEL) {
@@ -1034,15 +1107,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 }
                                 tmem_wait_st();
                             }
-                            if (row == 0) skip_flag[h] = 1;
+                            added = true;
                         }
                     }
                     fence_proxy_async_smem();
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(pready0 + 8u * h);
                 ++pvcount;
+                if (lane == 0) st_release_shared(ready0 + 16u * h + 4u * quad, 2u * pvcount + (added ? 1u : 0u));
             }
             if (!ok) break;
             pos_base += 2 * n;
@@ -1053,10 +1126,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
             }
             tc_fence_after();
-            const int token = tok0 + half_tok0 + row_tok;
-            const bool whole = flags & kWhole;
-            const int qhead = head * G + row_head;
-            const long long ws_row = ((long long)blockIdx.x * 2 + slot) * kAttnSlotRows +
+            const int token = it[kItTok0] + half_tok0 + row_tok;
+            const bool whole = it[kItFlags] & kWhole;
+            const int qhead = it[kItHead] * G + row_head;
+            const long long ws_row = ((long long)blockIdx.x * 2 + it[kItSlot]) * kAttnSlotRows +
                                      (alt ? 0 : h * kAttnHalfRows) + row;
             if (!alt) {
                 if (active) {
@@ -1159,7 +1232,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(oempty);
+            if (lane == 0) {
+                mbar_arrive(oempty);
+                mbar_arrive(itempty0 + 8u * is);
+            }
         }
     }
 
