@@ -58,6 +58,7 @@ constexpr int kThreads = 384;      // three warpgroups: softmax, softmax, MMA an
 constexpr int kLaunchRegs = 168, kHighRegs = 208, kLowRegs = 88;
 constexpr int kMmaWarp = 8;
 constexpr int kLoadWarp = 9;
+constexpr int kLandWarp = 10;
 constexpr int kItemSlots = 4;
 constexpr int kItemInts = 16;
 
@@ -79,41 +80,21 @@ __device__ __forceinline__ bool warp_wait(uint32_t b, uint32_t parity, volatile 
     return __all_sync(0xffffffffu, mbar_wait<false>(b, parity, abort, status));
 }
 
-// Waits until the producer has begun to fill a stage for place `pos` of the
-// ring.  A parity alone does not tell place pos from pos - 2 S: a thread that
-// does not wait for every place of the ring (the halves take turns) may look
-// at a stage whose previous copy, the other half's, has not even landed.
-// Once the stage is pos's, its previous copy has been consumed, and the
-// parity of pos means pos.
-__device__ __forceinline__ bool stage_begun(const volatile int* begun, int pos, volatile int* abort,
-                                            unsigned int* status)
+__device__ __forceinline__ uint32_t ld_acquire_shared(uint32_t addr)
 {
-    if (*begun == pos) return true;
-    const uint64_t t0 = global_timer_ns();
-    for (uint32_t it = 1; *begun != pos; ++it) {
-        if ((it & 31u) == 0) {
-            if (*abort) return false;
-            if (global_timer_ns() - t0 > kWaitLimitNs) {
-                atomicOr(status, kStatusWaitTimeout);
-                *abort = 1;
-                return false;
-            }
-        }
-    }
-    return true;
+    uint32_t v;
+    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
 }
 
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+__device__ __forceinline__ uint4 ld_acquire_shared_v4(uint32_t addr)
 {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
+    uint4 v;
+    asm volatile("ld.acquire.cta.shared::cta.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
 }
 
 __device__ __forceinline__ void st_release_shared(uint32_t addr, uint32_t v)
@@ -121,17 +102,21 @@ __device__ __forceinline__ void st_release_shared(uint32_t addr, uint32_t v)
     asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// Waits until the four warps of a group have written their part of the
-// group's tile number `count` (each says so in its word); skip: the group has
-// added the tile's product itself (all four say the same).
-__device__ __forceinline__ bool p_written(uint32_t words, uint32_t count, bool& skip,
-                                          volatile int* abort, unsigned int* status)
+// Waits until `places` copies have landed and (words != 0) the four warps of
+// a group have written their part of the group's P number `count`, each
+// saying so in its word; skip: the group has added that tile's product itself
+// (all four say the same).
+__device__ __forceinline__ bool words_ready(uint32_t landed, uint32_t places, uint32_t words,
+                                            uint32_t count, bool& skip, volatile int* abort,
+                                            unsigned int* status)
 {
     uint64_t t0 = 0;
     for (uint32_t it = 1;; ++it) {
-        const uint4 w = ld_shared_v4(words);
-        if ((w.x >> 1) == count && (w.y >> 1) == count && (w.z >> 1) == count && (w.w >> 1) == count) {
-            asm volatile("fence.acq_rel.cta;" ::: "memory");
+        uint4 w = make_uint4(2 * count, 2 * count, 2 * count, 2 * count);
+        if (words != 0) w = ld_acquire_shared_v4(words);
+        const uint32_t there = ld_acquire_shared(landed);
+        if (there >= places && (w.x >> 1) == count && (w.y >> 1) == count && (w.z >> 1) == count &&
+            (w.w >> 1) == count) {
             skip = w.x & 1u;
             return true;
         }
@@ -370,7 +355,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // has been added already
     const uint32_t ready0 = base + C::kMisc + 128;
     volatile uint32_t* ready = reinterpret_cast<volatile uint32_t*>(smem + C::kMisc + 128);   // [2][4]
-    volatile int* begun = reinterpret_cast<volatile int*>(smem + C::kMisc + 80);      // [S]
+    // places of the ring whose copies have landed, and (the producer's last
+    // word) how many there will be
+    const uint32_t landed_word = base + C::kMisc + 160;
+    volatile int* total_places = reinterpret_cast<volatile int*>(smem + C::kMisc + 164);
     float2* stats = reinterpret_cast<float2*>(smem + C::kStats);
 
     const int warp = threadIdx.x >> 5;
@@ -378,8 +366,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         *abort_flag = 0;
+        *total_places = -1;
+        st_release_shared(landed_word, 0);
         for (int s = 0; s < S; ++s) {
-            begun[s] = -1;
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
         }
@@ -590,7 +579,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool r = warp_wait(empty_bar(s), (uint32_t)((pos / S) & 1) ^ 1u, abort_flag, a.status);
                 dst = base + C::kRing + s * C::kStageBytes;
                 fb = full_bar(s);
-                if (r && lane == 0) begun[s] = pos;
                 ++pos;
                 return r;
             };
@@ -721,17 +709,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         // copies in flight land before the CTA may leave
+        if (lane == 0) *total_places = pos;
         for (int t = pos > S ? pos - S : 0; t < pos; ++t)
             mbar_wait_drain<false>(full_bar(t % S), (uint32_t)((t / S) & 1));
         if (item > 0) mbar_wait_drain<false>(qfull, (uint32_t)((item - 1) & 1));
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issuer
-        // One thread, and nothing between two products that can be elsewhere:
-        // issuing takes as long as the tensor core does, so whatever the
-        // thread waits for, the tensor core waits for too.  A wait on an
-        // mbarrier costs it some 230 cycles even when the phase is over; so
-        // the stages of the next step are tested while products are being
-        // issued, and P is announced by plain shared-memory words.
+        // One thread, which issues about as fast as the tensor core computes:
+        // whatever else it does, the tensor core waits for.  An mbarrier wait
+        // costs it some 230 cycles even when the phase is over and a commit
+        // 130, so in the loop over tiles there is one commit per product
+        // pair, "scores ready", which covers the products before it (stages
+        // and O are released by the softmax groups when they see it), and
+        // stages and P are announced by plain words in shared memory.
         if (lane == 0) {
             constexpr uint32_t kFmt = FP16 ? 0u : 1u;
             constexpr uint32_t idesc_s = make_idesc(kFmt, kFmt, 128, 128);
@@ -739,24 +729,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t q_desc = smem_desc_sw128(base + C::kQ);
             const uint64_t k_desc = smem_desc_sw128(base + C::kRing);
             const uint64_t v_desc = desc_mn_sw128(base + C::kRing, C::kBlockBytes);
-            uint32_t stage = 0, phase = 0;       // the next stage to be consumed
+            uint32_t stage = 0;                  // of the next place of the ring
+            uint32_t place = 0;                  // places consumed
             uint32_t pcount[2] = {0, 0};         // P tiles consumed
-            bool ok = true;
+            bool ok = true, skip = false;
             auto wait = [&](uint32_t b, uint32_t parity) {
                 return mbar_wait<false>(b, parity, abort_flag, a.status);
             };
-            // takes the next stage of the ring; its barrier and parity
-            struct Next {
-                uint32_t st, parity;
-                bool there;
-            };
             auto take = [&]() {
-                Next x = {stage, phase, false};
-                if (++stage == S) { stage = 0; phase ^= 1; }
-                return x;
+                const uint32_t st = stage;
+                if (++stage == S) stage = 0;
+                ++place;
+                return st;
             };
-            auto test = [&](Next& x) { x.there = mbar_test(full_bar(x.st), x.parity); };
-            auto landed = [&](const Next& x) { return x.there || wait(full_bar(x.st), x.parity); };
             auto issue_s = [&](int h, int qh, uint32_t st) {
                 const uint64_t ad = q_desc + (uint32_t)(qh * (C::kHalfBytes >> 4));
                 const uint64_t bd = k_desc + st * (uint32_t)(C::kStageBytes >> 4);
@@ -769,20 +754,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 (kb | k) ? 1u : 0u);
                 mma_commit(sfull0 + 8u * h);
             };
-            // P of half h's next tile: the group's four warps have written it
-            auto wait_p = [&](int h, bool& skip) {
-                return p_written(ready0 + 16u * h, ++pcount[h], skip, abort_flag, a.status);
-            };
-            auto issue_pv = [&](int h, uint32_t st, bool acc, bool skip) {
+            auto issue_pv = [&](int h, uint32_t st, bool acc) {
                 tc_fence_after();
-                if (!skip) {                     // else the group added this tile itself
-                    const uint64_t bd = v_desc + st * (uint32_t)(C::kStageBytes >> 4);
+                if (skip) return;                // the group has added this tile itself
+                const uint64_t bd = v_desc + st * (uint32_t)(C::kStageBytes >> 4);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma_f16_tmem_a(tmem + kColO + 128u * h, tmem + kColS + 128u * h + 8u * k,
-                                       bd + (uint32_t)(k * (2048 >> 4)), idesc_o, (acc || k) ? 1u : 0u);
-                }
-                mma_commit(pvdone0 + 8u * h);
+                for (int k = 0; k < 8; ++k)
+                    mma_f16_tmem_a(tmem + kColO + 128u * h, tmem + kColS + 128u * h + 8u * k,
+                                   bd + (uint32_t)(k * (2048 >> 4)), idesc_o, (acc || k) ? 1u : 0u);
+            };
+            // places below `place` have landed, and (h >= 0) half h's next P
+            auto wait_words = [&](int h) {
+                return words_ready(landed_word, place, h < 0 ? 0u : ready0 + 16u * h,
+                                   h < 0 ? 0u : ++pcount[h], skip, abort_flag, a.status);
             };
             for (int item = 0; ok; ++item) {
                 const int is = item % kItemSlots;
@@ -792,80 +776,69 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int flags = it[kItFlags], n = it[kItN];
                 mbar_arrive(itempty0 + 8u * is);
                 if (flags & kEnd) break;
-                const bool alt = flags & kAlt;
-                bool skip = false;
-                Next ks = take();
-                ok = wait(qfull, item & 1) && landed(ks);
+                uint32_t ks = take(), vs = 0;
+                ok = wait(qfull, item & 1) && wait_words(-1);
                 if (!ok) break;
                 tc_fence_after();
-                issue_s(0, 0, ks.st);
-                if (!alt) {
-                    issue_s(1, 1, ks.st);
-                    mma_commit(empty_bar(ks.st));
-                    if (n == 1) mma_commit(qempty);
+                issue_s(0, 0, ks);
+                if (!(flags & kAlt)) {
+                    issue_s(1, 1, ks);
                     ok = wait(oempty, (uint32_t)(item & 1) ^ 1u);
-                    Next vs = take();
-                    if (n > 1) ks = take();
                     for (int t = 0; t < n && ok; ++t) {
                         const bool more = t + 1 < n;
-                        ok = landed(vs) && (!more || landed(ks)) && wait_p(0, skip);
+                        vs = take();
+                        if (more) ks = take();
+                        ok = wait_words(0);
                         if (!ok) break;
-                        issue_pv(0, vs.st, t > 0, skip);
-                        // the next step's stages, in the order they are filled
-                        const uint32_t v0 = vs.st, k0 = ks.st;
-                        if (more) {
-                            vs = take();
-                            test(vs);
-                            if (t + 2 < n) { ks = take(); test(ks); }
-                            issue_s(0, 0, k0);
-                        }
-                        ok = wait_p(1, skip);
+                        issue_pv(0, vs, t > 0);
+                        if (more) issue_s(0, 0, ks);
+                        else mma_commit(pvdone0);
+                        ok = wait_words(1);
                         if (!ok) break;
-                        issue_pv(1, v0, t > 0, skip);
-                        mma_commit(empty_bar(v0));
-                        if (more) {
-                            issue_s(1, 1, k0);
-                            mma_commit(empty_bar(k0));
-                            if (t + 2 == n) mma_commit(qempty);
-                        }
+                        issue_pv(1, vs, t > 0);
+                        if (more) issue_s(1, 1, ks);
+                        else mma_commit(pvdone0 + 8u);
                     }
                 } else {
-                    mma_commit(empty_bar(ks.st));
                     if (n > 1) {
                         ks = take();
-                        ok = landed(ks);
+                        ok = wait_words(-1);
                         if (!ok) break;
-                        issue_s(1, 0, ks.st);
-                        mma_commit(empty_bar(ks.st));
+                        issue_s(1, 0, ks);
                     }
-                    if (n <= 2) mma_commit(qempty);
                     ok = wait(oempty, (uint32_t)(item & 1) ^ 1u);
-                    Next vs = take();
-                    if (n > 2) ks = take();
                     for (int t = 0; t < n && ok; ++t) {
                         const int h = t & 1;
                         const bool more = t + 2 < n;
-                        ok = landed(vs) && (!more || landed(ks)) && wait_p(h, skip);
+                        vs = take();
+                        if (more) ks = take();
+                        ok = wait_words(h);
                         if (!ok) break;
-                        issue_pv(h, vs.st, t > 1, skip);
-                        mma_commit(empty_bar(vs.st));
-                        const uint32_t k0 = ks.st;
-                        if (t + 1 < n) {
-                            vs = take();
-                            test(vs);
-                            if (t + 3 < n) { ks = take(); test(ks); }
-                        }
-                        if (more) {
-                            issue_s(h, 0, k0);
-                            mma_commit(empty_bar(k0));
-                            if (t + 3 == n) mma_commit(qempty);
-                        }
+                        issue_pv(h, vs, t > 1);
+                        if (more) issue_s(h, 0, ks);
+                        else mma_commit(pvdone0 + 8u * h);
                     }
                 }
             }
             // every MMA and every arrival it owes is through before the CTA leaves
             mma_commit(drain);
             mbar_wait_drain<false>(drain, 0);
+        }
+        __syncwarp();
+    } else if (warp == kLandWarp) {
+        // ------------------------------------------------------------ landed stages
+        // Counts, in order, the places of the ring whose copies have landed.
+        // It ends with the producer's last place, or with an abort (every
+        // other role's waits are bounded and raise it).
+        if (lane == 0) {
+            for (int pos = 0;; ) {
+                if (mbar_try_wait_suspend(full_bar(pos % S), (uint32_t)((pos / S) & 1), kWaitSuspendNs)) {
+                    ++pos;
+                    st_release_shared(landed_word, (uint32_t)pos);
+                } else if (*total_places == pos || *abort_flag) {
+                    break;
+                }
+            }
         }
         __syncwarp();
     }
@@ -882,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int G = a.group;
         const int row_tok = row / G;
         const int row_head = row - row_tok * G;
-        uint32_t scount = 0, pvcount = 0, group_phase = 0, alt_phase = 0;
+        uint32_t scount = 0, pvcount = 0, done_phase = 0, group_phase = 0, alt_phase = 0;
         int pos_base = 0;
         bool ok = true;
         for (int item = 0; ok; ++item) {
@@ -917,6 +890,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const int tiles_here = alt ? (n + 1 - h) / 2 : n;
             float m = -INFINITY, l = 0.0f;
+            int v_place = 0;                     // of the last tile's V
             for (int i = 0; i < tiles_here && ok; ++i) {
                 const int t = alt ? 2 * i + h : i;
                 const int key0 = (j0 + t) * kAttnTileKeys;
@@ -936,6 +910,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 ++scount;
                 tc_fence_after();
+                // the scores' commit covers every product issued before it:
+                // this tile's K has been read, and the V and P of this half's
+                // last tile (of both halves' where they share it, since half 1
+                // comes second)
+                if ((alt || h == 1) && threadIdx.x % 128 == 96) {
+                    const int kp = pos_base + (t < (alt ? 2 : 1) ? t : 2 * t - (alt ? 1 : 0));
+                    mbar_arrive(empty_bar(kp % S));
+                    if (i > 0) mbar_arrive(empty_bar(v_place % S));
+                    if (t == n - 1) mbar_arrive(qempty);
+                }
+                v_place = pos_base + t + min(n, t + (alt ? 2 : 1));
                 bool masked;
                 if constexpr (SEL) masked = (there[0] & there[1] & there[2] & there[3]) != 0xffffffffu;
                 else masked = key0 < all_lo || key0 + kAttnTileKeys > all_hi;
@@ -972,9 +957,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (grow) m = m_new;
                         l *= f;
                         if (i > 0) {
-                            ok = warp_wait(pvdone0 + 8u * h, (pvcount - 1) & 1, abort_flag, a.status);
-                            if (!ok) break;
-                            tc_fence_after();
                             // eight columns at a time: the row of S stays in registers
 #pragma unroll 1
                             for (int d = 0; d < D; d += 8) {
@@ -1023,11 +1005,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // V rows that must not count
                 bool added = false;             // this tile's product is in O already
                 if (masked) {
-                    const int vpos = t + min(n, t + (alt ? 2 : 1));
-                    const int vp = pos_base + vpos;
-                    const int vs = vp % S;
-                    ok = __all_sync(0xffffffffu, stage_begun(begun + vs, vp, abort_flag, a.status)) &&
-                         warp_wait(full_bar(vs), (uint32_t)((vp / S) & 1), abort_flag, a.status);
+                    const int vs = v_place % S;
+                    // (the parity of v_place cannot be an older one's: these
+                    // scores were issued after place v_place - S was consumed)
+                    ok = warp_wait(full_bar(vs), (uint32_t)((v_place / S) & 1), abort_flag, a.status);
                     if (!ok) break;
                     uint8_t* vt = smem + C::kRing + vs * C::kStageBytes;
                     // thread = key of the tile
@@ -1070,11 +1051,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (v4[0] | v4[1] | v4[2] | v4[3]) {
                             // this tile's product, row by row over the keys it
                             // may see (P as the tensor core would read it)
-                            if (i > 0) {
-                                ok = warp_wait(pvdone0 + 8u * h, (pvcount - 1) & 1, abort_flag, a.status);
-                                if (!ok) break;
-                                tc_fence_after();
-                            }
                             if (active) {
                                 const int lo = row_lo - key0, hi = row_hi - key0;
                                 for (int d = 0; d < D; d += 8) {
@@ -1122,8 +1098,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
             // ---------------------------------------------------- the item's end
             if (tiles_here > 0) {
-                ok = warp_wait(pvdone0 + 8u * h, (pvcount - 1) & 1, abort_flag, a.status);
+                ok = warp_wait(pvdone0 + 8u * h, done_phase, abort_flag, a.status);
                 if (!ok) break;
+                done_phase ^= 1;
+                if ((alt || h == 1) && threadIdx.x % 128 == 96) mbar_arrive(empty_bar(v_place % S));
             }
             tc_fence_after();
             const int token = it[kItTok0] + half_tok0 + row_tok;
