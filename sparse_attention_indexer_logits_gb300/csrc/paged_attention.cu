@@ -23,6 +23,7 @@ constexpr int kJoinSplit = 8;     // CTAs that share one item's rows
 template <int D, bool FP16>
 __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const AttnArgs a, int num_ctas)
 {
+    allow_dependent_launch();
     grid_dependency_wait();
     const int owner = blockIdx.x;
     const int* rec = a.pieces + (owner * 2LL + 1) * kPieceInts;
@@ -99,9 +100,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const A
 template <int D, bool FP16>
 cudaError_t launch_join(const AttnArgs& a, int num_ctas, cudaStream_t stream)
 {
-    attention_join_kernel<D, FP16>
-        <<<dim3((unsigned)num_ctas, kJoinSplit), kJoinWarps * 32, 0, stream>>>(a, num_ctas);
-    return cudaGetLastError();
+    return launch_dependent(attention_join_kernel<D, FP16>, dim3((unsigned)num_ctas, kJoinSplit),
+                            kJoinWarps * 32, 0, stream, a, num_ctas);
 }
 
 }  // namespace

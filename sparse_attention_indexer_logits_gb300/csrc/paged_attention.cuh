@@ -9,9 +9,10 @@
 // at the end out = O / l and lse = scale * m + ln l.
 //
 // Work.  The rows of an item are up to 256 (token, head) pairs that share a kv
-// head, its unit of work is one tile of 128 keys.  The units of all items, in
-// order, are cut into one contiguous range per CTA, so a long request's keys
-// are split over many CTAs and short requests share one, whatever the mix.  A
+// head, its unit of work is one tile of 128 keys (and two units for the item
+// itself).  The units of all items, in order, are cut into one contiguous
+// range per CTA, so a long request's keys are split over many CTAs and short
+// requests share one, whatever the mix.  A
 // range that ends inside an item leaves its (m, l, O) in the workspace and a
 // second kernel joins the pieces.
 //
@@ -144,10 +145,10 @@ struct Cfg {
     static constexpr int kRing = kQ + 2 * kHalfBytes;
     static constexpr int kStats = kRing + kStages * kStageBytes;      // float2 [2][128]
     static constexpr int kBars = kStats + 2 * 128 * 8;
-    // barriers: full, empty per stage; q full, q empty; s full, pv done, group
+    // barriers: full, empty per stage; q full, q empty per half; s full, pv done, group
     // sync per half; o empty, alt sync; item full, item empty; the issuer's
     // last commit
-    static constexpr int kNumBars = 2 * kStages + 2 + 6 + 2 + 2 * kItemSlots + 1;
+    static constexpr int kNumBars = 2 * kStages + 4 + 6 + 2 + 2 * kItemSlots + 1;
     static constexpr int kItems = (kBars + kNumBars * 8 + 15) / 16 * 16;
     static constexpr int kMisc = kItems + kItemSlots * kItemInts * 4;
     static constexpr int kTotal = kMisc + 192;
@@ -315,12 +316,17 @@ __device__ __forceinline__ void request_of(const AttnArgs& a, int b, int& tok0, 
     kv = max(__ldg(a.kv_lens + b), 0);
 }
 
-// Units (tiles) of one kv head of request b; a warp computes it together.
+// What beginning and ending an item costs, in tiles (Q's way in, the first
+// copies, the output): counted into the ranges, so that a CTA with many short
+// items gets fewer tiles.
+constexpr int kItemUnits = 2;
+
+// Units of one kv head of request b; a warp computes it together.
 __device__ __forceinline__ int head_units(const AttnArgs& a, int nq, int kv, int lane)
 {
     int u = 0;
     const int tiles = tiles_of(a, nq);
-    for (int i = lane; i < tiles; i += 32) u += tile_span(a, nq, kv, i).n;
+    for (int i = lane; i < tiles; i += 32) u += tile_span(a, nq, kv, i).n + kItemUnits;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
     return u;
@@ -343,8 +349,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t bar = base + C::kBars;
     auto full_bar = [&](int s) { return bar + 8u * s; };
     auto empty_bar = [&](int s) { return bar + 8u * (S + s); };
-    const uint32_t qfull = bar + 8u * (2 * S), qempty = qfull + 8u;
-    const uint32_t sfull0 = qfull + 16u, pvdone0 = sfull0 + 16u,
+    const uint32_t qfull0 = bar + 8u * (2 * S), qempty0 = qfull0 + 16u;   // per Q half
+    const uint32_t sfull0 = qempty0 + 16u, pvdone0 = sfull0 + 16u,
                    group0 = pvdone0 + 16u, oempty = group0 + 16u, altbar = oempty + 8u,
                    itfull0 = altbar + 8u, itempty0 = itfull0 + 8u * kItemSlots, drain = itempty0 + 8u * kItemSlots;
     int* items = reinterpret_cast<int*>(smem + C::kItems);
@@ -372,10 +378,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
         }
-        mbar_init(qfull, 1);
-        mbar_init(qempty, 1);
         mbar_init(drain, 1);
         for (int h = 0; h < 2; ++h) {
+            mbar_init(qfull0 + 8u * h, 1);
+            mbar_init(qempty0 + 8u * h, 1);
             mbar_init(sfull0 + 8u * h, 1);
             mbar_init(pvdone0 + 8u * h, 1);
             mbar_init(group0 + 8u * h, 4);
@@ -396,6 +402,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(smem_addr(tmem_slot), 512);
         tmem_relinquish();
     }
+    // what follows reads memory that the kernel before this one may have written
+    allow_dependent_launch();
+    grid_dependency_wait();
     // units per request and kv head, in the ring's memory until the copies begin
     int* units = reinterpret_cast<int*>(smem + C::kRing);
     if constexpr (!SEL) {
@@ -415,15 +424,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         regs_dec<kLowRegs>();
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ producer
-        int b = 0, head = 0, tile = 0, j = 0;       // the range's start
+        int b = 0, head = 0, tile = 0;   // the range's start, and the unit of that
+        int at = 0;                      // item where it lies
         long long left;                              // units left in the range
         const int sel_tiles = SEL ? (a.sel_k + kAttnTileKeys - 1) / kAttnTileKeys : 0;
         if constexpr (SEL) {
-            const long long total = (long long)a.tokens * a.kv_heads * sel_tiles;
+            const int per_item = sel_tiles + kItemUnits;
+            const long long total = (long long)a.tokens * a.kv_heads * per_item;
             const long long s0 = range_start(total, gridDim.x, blockIdx.x);
             left = range_start(total, gridDim.x, blockIdx.x + 1) - s0;
-            const long long item = s0 / sel_tiles;
-            j = (int)(s0 - item * sel_tiles);
+            const long long item = s0 / per_item;
+            at = (int)(s0 - item * per_item);
             b = (int)(item / a.kv_heads);           // the token
             head = (int)(item - (long long)b * a.kv_heads);
         } else {
@@ -464,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int tiles = tiles_of(a, nq);
                 found = false;
                 for (int c = 0; c < tiles && !found; c += 32) {
-                    const int v = c + lane < tiles ? tile_span(a, nq, kv, c + lane).n : 0;
+                    const int v = c + lane < tiles ? tile_span(a, nq, kv, c + lane).n + kItemUnits : 0;
                     int incl = v;
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
@@ -475,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (who) {
                         const int l = __ffs(who) - 1;
                         tile = c + l;
-                        j = rem - __shfl_sync(0xffffffffu, incl - v, l);
+                        at = rem - __shfl_sync(0xffffffffu, incl - v, l);
                         found = true;
                     } else {
                         rem -= __shfl_sync(0xffffffffu, incl, 31);
@@ -494,6 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
         int pos = 0;                 // stages filled so far
         int item = 0;
+        uint32_t qcount = 0;         // Q halves filled so far
         bool ok = true;
         int tok0 = 0, nq = 0, kv = 0, tiles = 0, cur_b = -1;
         while (left > 0 && ok) {
@@ -521,12 +533,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     request_of(a, b, tok0, nq, kv);
                     tiles = tiles_of(a, nq);
                     cur_b = b;
-                    if (tiles == 0) { ++b; head = 0; tile = 0; j = 0; continue; }
+                    if (tiles == 0) { ++b; head = 0; tile = 0; at = 0; continue; }
                 }
                 req = b;
                 sp = tile_span(a, nq, kv, tile);
             }
-            const int n = (int)min(left, (long long)(sp.n - j));
+            // the tiles of this range: j .. j + n - 1; none if the range ends
+            // in the item's own units (the next one begins with its first tile)
+            const int j = max(0, at - kItemUnits);
+            const int used = (int)min(left, (long long)(sp.n + kItemUnits - at));
+            const int n = max(0, at + used - kItemUnits) - j;
+            left -= used;
+            if (n == 0) break;
             const bool first = j == 0, last = j + n == sp.n;
             const bool alt = SEL || sp.ntok <= a.half_tokens;
             const int slot = first ? 1 : 0;          // workspace slot of a piece
@@ -559,16 +577,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 mbar_arrive(itfull0 + 8u * is);
             }
-            ok = warp_wait(qempty, (item & 1) ^ 1, abort_flag, a.status);
-            if (!ok) break;
-            if (lane == 0) {
-                const int halves = alt ? 1 : 2;
-                mbar_arrive_expect_tx(qfull, (uint32_t)(halves * C::kBlocks * 128 * a.group * a.half_tokens));
-                for (int h = 0; h < halves; ++h)
+            // an item of one half takes the Q halves in turn, so its rows come
+            // while the item before it is still at work
+            for (int h = 0; h < (alt ? 1 : 2) && ok; ++h, ++qcount) {
+                const uint32_t qs = qcount & 1u;
+                ok = warp_wait(qempty0 + 8u * qs, ((qcount >> 1) & 1u) ^ 1u, abort_flag, a.status);
+                if (ok && lane == 0) {
+                    const uint32_t fb = qfull0 + 8u * qs;
+                    mbar_arrive_expect_tx(fb, (uint32_t)(C::kBlocks * 128 * a.group * a.half_tokens));
                     for (int kb = 0; kb < C::kBlocks; ++kb)
-                        tma_load_3d(base + C::kQ + h * C::kHalfBytes + kb * C::kBlockBytes, &qmap, qfull,
+                        tma_load_3d(base + C::kQ + qs * C::kHalfBytes + kb * C::kBlockBytes, &qmap, fb,
                                     kb * 64, head * a.group, tok0 + sp.t0 + h * a.half_tokens);
+                }
             }
+            if (!ok) break;
             __syncwarp();
             ++item;
 
@@ -585,23 +607,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (SEL) {
                 const int32_t* list = a.selected + (long long)b * a.sel_stride;
                 const int32_t* table = a.block_table + (long long)req * a.bt_stride;
-                // the cache rows of this lane's four entries of a tile (as page
-                // and slot); w: none of them is there
-                auto find = [&](int t, int4& pg, int4& sl, bool& any) {
-                    int* pp = &pg.x;
-                    int* ss = &sl.x;
-                    any = false;
-                    bool bad = false;
+                // This lane's four entries of a tile, in three steps a tile
+                // apart, so that no step waits for a load of its own: the
+                // positions; their pages; the cache rows.  `any`: one of them
+                // is there.
+                auto positions = [&](int t) {
+                    int4 r;
+                    int* pp = &r.x;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int at = (j0 + t) * kAttnTileKeys + 4 * lane + e;
-                        const int p = at < a.sel_k ? __ldg(list + at) : -1;
-                        const bool there = p >= 0 && p < kv;
-                        long long page = there ? __ldg(table + (p >> 6)) : 0;
-                        if (page < 0 || page >= a.num_pages) { bad = true; page = 0; }
-                        pp[e] = (int)page;
-                        ss[e] = there ? p & 63 : 0;
-                        any |= there;
+                        const int i = (j0 + t) * kAttnTileKeys + 4 * lane + e;
+                        const int p = t < n && i < a.sel_k ? __ldg(list + i) : -1;
+                        pp[e] = p < kv ? p : -1;
+                    }
+                    return r;
+                };
+                auto pages = [&](int4 r) {
+                    return make_int4(r.x >= 0 ? __ldg(table + (r.x >> 6)) : 0, r.y >= 0 ? __ldg(table + (r.y >> 6)) : 0,
+                                     r.z >= 0 ? __ldg(table + (r.z >> 6)) : 0, r.w >= 0 ? __ldg(table + (r.w >> 6)) : 0);
+                };
+                // positions become slots; pages that are not there become 0
+                auto settle = [&](int4& pos4, int4& pg, bool& any) {
+                    int* pp = &pos4.x;
+                    int* gg = &pg.x;
+                    bool bad = false;
+                    any = false;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        any |= pp[e] >= 0;
+                        pp[e] = pp[e] >= 0 ? pp[e] & 63 : 0;
+                        if (gg[e] < 0 || gg[e] >= a.num_pages) { bad = true; gg[e] = 0; }
                     }
                     if (bad) atomicOr(a.status, kStatusBadBlock);
                 };
@@ -623,19 +658,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tma_gather4(dst + kb * C::kBlockBytes + lane * 512, map, fb, kb * 64, r);
                     return true;
                 };
-                int4 p0, s0, p1, s1, p2, s2;
-                bool a0, a1 = false, a2 = false;
-                find(0, p0, s0, a0);
-                p1 = s1 = p2 = s2 = make_int4(0, 0, 0, 0);
-                if (n > 1) find(1, p1, s1, a1);
+                int4 s0 = positions(0), s1 = positions(1), s2 = positions(2), s3 = positions(3);
+                int4 p0 = pages(s0), p1 = pages(s1), p2 = pages(s2);
+                bool a0, a1, a2;
+                settle(s0, p0, a0);
+                settle(s1, p1, a1);
                 ok = load(&kmap, rows(p0, s0, false), a0);
                 if (ok && n > 1) ok = load(&kmap, rows(p1, s1, false), a1);
                 for (int t = 0; t < n && ok; ++t) {
-                    if (t + 2 < n) find(t + 2, p2, s2, a2);
+                    const int4 s4 = positions(t + 4), p3 = pages(s3);
                     ok = load(&vmap, rows(p0, s0, true), a0);
+                    settle(s2, p2, a2);
                     if (ok && t + 2 < n) ok = load(&kmap, rows(p2, s2, false), a2);
                     p0 = p1; s0 = s1; a0 = a1;
                     p1 = p2; s1 = s2; a1 = a2;
+                    p2 = p3; s2 = s3; s3 = s4;
                 }
             } else {
                 const int32_t* table = a.block_table + (long long)req * a.bt_stride;
@@ -687,8 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             // ---- the next item
-            left -= n;
-            j = 0;
+            at = 0;
             if (last) {
                 if constexpr (SEL) {
                     if (++head == a.kv_heads) { head = 0; ++b; }
@@ -712,7 +748,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) *total_places = pos;
         for (int t = pos > S ? pos - S : 0; t < pos; ++t)
             mbar_wait_drain<false>(full_bar(t % S), (uint32_t)((t / S) & 1));
-        if (item > 0) mbar_wait_drain<false>(qfull, (uint32_t)((item - 1) & 1));
+        for (uint32_t c = qcount > 2 ? qcount - 2 : 0; c < qcount; ++c)
+            mbar_wait_drain<false>(qfull0 + 8u * (c & 1u), (c >> 1) & 1u);
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issuer
         // One thread, which issues about as fast as the tensor core computes:
@@ -731,6 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t v_desc = desc_mn_sw128(base + C::kRing, C::kBlockBytes);
             uint32_t stage = 0;                  // of the next place of the ring
             uint32_t place = 0;                  // places consumed
+            uint32_t qcount = 0;                 // Q halves used
             uint32_t pcount[2] = {0, 0};         // P tiles consumed
             bool ok = true, skip = false;
             auto wait = [&](uint32_t b, uint32_t parity) {
@@ -777,12 +815,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(itempty0 + 8u * is);
                 if (flags & kEnd) break;
                 uint32_t ks = take(), vs = 0;
-                ok = wait(qfull, item & 1) && wait_words(-1);
+                const int q0 = qcount & 1u, q1 = q0 ^ 1;     // Q halves of this item
+                auto q_landed = [&](uint32_t c) { return wait(qfull0 + 8u * (c & 1u), (c >> 1) & 1u); };
+                ok = q_landed(qcount++) && ((flags & kAlt) || q_landed(qcount++)) && wait_words(-1);
                 if (!ok) break;
                 tc_fence_after();
-                issue_s(0, 0, ks);
+                issue_s(0, q0, ks);
                 if (!(flags & kAlt)) {
-                    issue_s(1, 1, ks);
+                    issue_s(1, q1, ks);
                     ok = wait(oempty, (uint32_t)(item & 1) ^ 1u);
                     for (int t = 0; t < n && ok; ++t) {
                         const bool more = t + 1 < n;
@@ -791,12 +831,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = wait_words(0);
                         if (!ok) break;
                         issue_pv(0, vs, t > 0);
-                        if (more) issue_s(0, 0, ks);
+                        if (more) issue_s(0, q0, ks);
                         else mma_commit(pvdone0);
                         ok = wait_words(1);
                         if (!ok) break;
                         issue_pv(1, vs, t > 0);
-                        if (more) issue_s(1, 1, ks);
+                        if (more) issue_s(1, q1, ks);
                         else mma_commit(pvdone0 + 8u);
                     }
                 } else {
@@ -804,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ks = take();
                         ok = wait_words(-1);
                         if (!ok) break;
-                        issue_s(1, 0, ks);
+                        issue_s(1, q0, ks);
                     }
                     ok = wait(oempty, (uint32_t)(item & 1) ^ 1u);
                     for (int t = 0; t < n && ok; ++t) {
@@ -815,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = wait_words(h);
                         if (!ok) break;
                         issue_pv(h, vs, t > 1);
-                        if (more) issue_s(h, 0, ks);
+                        if (more) issue_s(h, q0, ks);
                         else mma_commit(pvdone0 + 8u * h);
                     }
                 }
@@ -855,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int G = a.group;
         const int row_tok = row / G;
         const int row_head = row - row_tok * G;
-        uint32_t scount = 0, pvcount = 0, done_phase = 0, group_phase = 0, alt_phase = 0;
+        uint32_t qcount = 0, scount = 0, pvcount = 0, done_phase = 0, group_phase = 0, alt_phase = 0;
         int pos_base = 0;
         bool ok = true;
         for (int item = 0; ok; ++item) {
@@ -918,7 +958,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int kp = pos_base + (t < (alt ? 2 : 1) ? t : 2 * t - (alt ? 1 : 0));
                     mbar_arrive(empty_bar(kp % S));
                     if (i > 0) mbar_arrive(empty_bar(v_place % S));
-                    if (t == n - 1) mbar_arrive(qempty);
+                    if (t == n - 1) {
+                        mbar_arrive(qempty0 + 8u * (qcount & 1u));
+                        if (!alt) mbar_arrive(qempty0 + 8u * (~qcount & 1u));
+                    }
                 }
                 v_place = pos_base + t + min(n, t + (alt ? 2 : 1));
                 bool masked;
@@ -1088,13 +1131,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     fence_proxy_async_smem();
                 }
-                tc_fence_before();
+                // (P is in place: its stores were waited for)
                 __syncwarp();
                 ++pvcount;
                 if (lane == 0) st_release_shared(ready0 + 16u * h + 4u * quad, 2u * pvcount + (added ? 1u : 0u));
             }
             if (!ok) break;
             pos_base += 2 * n;
+            qcount += alt ? 1u : 2u;
 
             // ---------------------------------------------------- the item's end
             if (tiles_here > 0) {
@@ -1226,6 +1270,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// A launch that may begin while the kernel before it in the stream ends (both
+// kernels wait in grid_dependency_wait before they touch memory).
+template <class K, class... Args>
+cudaError_t launch_dependent(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                             const Args&... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 template <int D, bool FP16, bool SEL>
 cudaError_t launch_kernel(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
                           const AttnArgs& a, int num_ctas, cudaStream_t stream)
@@ -1247,8 +1311,8 @@ cudaError_t launch_kernel(const CUtensorMap& qmap, const CUtensorMap& kmap, cons
             return cudaErrorInvalidConfiguration;
         configured_device = dev;
     }
-    kernel<<<num_ctas, kThreads, Cfg<D>::kTotal, stream>>>(qmap, kmap, vmap, a);
-    return cudaGetLastError();
+    return launch_dependent(kernel, dim3((unsigned)num_ctas), kThreads, Cfg<D>::kTotal, stream, qmap, kmap,
+                            vmap, a);
 }
 
 }  // namespace attn

@@ -44,7 +44,7 @@ class Model:
         self.full = [Bar(1) for _ in range(stages)]
         self.empty = [Bar(1) for _ in range(stages)]
         self.holds = [None] * stages
-        self.qfull, self.qempty, self.qholds = Bar(1), Bar(1), None
+        self.qfull, self.qempty, self.qholds = [Bar(1), Bar(1)], [Bar(1), Bar(1)], [None, None]
         self.sfull, self.pvdone = [Bar(1), Bar(1)], [Bar(1), Bar(1)]
         self.ready, self.landed, self.total = [0, 0], 0, -1
         self.oempty, self.altbar = Bar(8), Bar(8)
@@ -70,13 +70,15 @@ class Model:
 
     # ---- roles: generators that yield a condition to wait for, or a delay
     def producer(self):
-        place = 0
+        place = q = 0
         for i, (alt, n) in enumerate(self.items):
             yield lambda: self.itempty[i % 4].done(i // 4 & 1 ^ 1)
             self.itfull[i % 4].arrive()
-            yield lambda: self.qempty.done(i & 1 ^ 1)
-            self.qfull.arrive(1)
-            self.at(self.now + self.r.randint(5, 20 * self.slow), self.q_lands, i)
+            for h in (0,) if alt else (0, 1):
+                yield lambda: self.qempty[q & 1].done(q >> 1 & 1 ^ 1)
+                self.qfull[q & 1].arrive(1)
+                self.at(self.now + self.r.randint(5, 20 * self.slow), self.q_lands, q & 1, (i, h))
+                q += 1
             a = self.ahead(alt)
             order = [("K", t) for t in range(min(a, n))]
             for t in range(n):
@@ -102,9 +104,9 @@ class Model:
     def _base(self, item):
         return sum(2 * n for _, n in self.items[:item])
 
-    def q_lands(self, i):
-        self.qholds = i
-        self.qfull.landed()
+    def q_lands(self, s, what):
+        self.qholds[s] = what
+        self.qfull[s].landed()
 
     def stage_lands(self, s, what):
         self.holds[s] = what
@@ -129,8 +131,9 @@ class Model:
     def commit(self, bar):
         self.at(max(self.tensor, self.now + 1), bar.arrive)
 
-    def does_s(self, h, i, t, s):
-        assert self.holds[s] == (i, "K", t) and self.qholds == i, (self.holds[s], i, t)
+    def does_s(self, h, i, t, s, q):
+        want = (i, 0 if self.items[i][0] else h)
+        assert self.holds[s] == (i, "K", t) and self.qholds[q & 1] == want, (self.holds[s], i, t)
         self.S_holds[h] = ("S", i, t)
 
     def does_pv(self, h, i, t, s, first):
@@ -138,7 +141,7 @@ class Model:
         self.O_holds[h] = ([] if first else self.O_holds[h]) + [(i, t)]
 
     def issuer(self):
-        place, count = 0, [0, 0]
+        place, count, q = 0, [0, 0], 0
         for i, (alt, n) in enumerate(self.items + [(False, 0)]):
             yield lambda: self.itfull[i % 4].done(i // 4 & 1)
             self.itempty[i % 4].arrive()
@@ -146,18 +149,19 @@ class Model:
                 return
             k = place % self.S
             place += 1
-            yield lambda: self.qfull.done(i & 1)
+            for u in (q,) if alt else (q, q + 1):
+                yield lambda: self.qfull[u & 1].done(u >> 1 & 1)
             yield lambda: self.landed >= place
-            self.issue(self.does_s, 0, i, 0, k)
+            self.issue(self.does_s, 0, i, 0, k, q)
             self.commit(self.sfull[0])
             if not alt:
-                self.issue(self.does_s, 1, i, 0, k)
+                self.issue(self.does_s, 1, i, 0, k, q + 1)
                 self.commit(self.sfull[1])
             elif n > 1:
                 k = place % self.S
                 place += 1
                 yield lambda: self.landed >= place
-                self.issue(self.does_s, 1, i, 1, k)
+                self.issue(self.does_s, 1, i, 1, k, q)
                 self.commit(self.sfull[1])
             yield lambda: self.oempty.done(i & 1 ^ 1)
             a = self.ahead(alt)
@@ -172,14 +176,15 @@ class Model:
                     yield lambda: self.landed >= place and self.ready[h] == 4 * count[h]
                     self.issue(self.does_pv, h, i, t, v, t < a)
                     if t + a < n:
-                        self.issue(self.does_s, h, i, t + a, k)
+                        self.issue(self.does_s, h, i, t + a, k, q if alt else q + h)
                         self.commit(self.sfull[h])
                     else:
                         self.commit(self.pvdone[h])
                     yield self.r.randint(1, 10)
+            q += a ^ 3
 
     def softmax(self, h):
-        scount = done = turns = 0
+        scount = done = turns = q = 0
         for i, (alt, n) in enumerate(self.items + [(False, 0)]):
             yield lambda: self.itfull[i % 4].done(i // 4 & 1)
             if i == len(self.items):
@@ -198,7 +203,8 @@ class Model:
                     elif j > 0:
                         self.empty[v % self.S].arrive()
                     if t == n - 1:
-                        self.qempty.arrive()
+                        for u in (q,) if alt else (q, q + 1):
+                            self.qempty[u & 1].arrive()
                 v = self.v_place(base, alt, n, t)
                 yield self.r.randint(1, 30)
                 if t == n - 1 or self.r.random() < 0.3:      # a tile with hidden keys
@@ -217,6 +223,7 @@ class Model:
                     self.altbar.arrive()
                 yield lambda: self.altbar.done(turns)
                 turns ^= 1
+            q += 1 if alt else 2
             yield self.r.randint(1, 40)
             for g in (0, 1) if alt else (h,):
                 want = [(i, t) for t in range(n) if not alt or t % 2 == g]
