@@ -321,15 +321,82 @@ __device__ __forceinline__ void request_of(const AttnArgs& a, int b, int& tok0, 
 // items gets fewer tiles.
 constexpr int kItemUnits = 2;
 
-// Units of one kv head of request b; a warp computes it together.
-__device__ __forceinline__ int head_units(const AttnArgs& a, int nq, int kv, int lane)
+// Where a CTA's range begins, and how many units it has.
+struct Start {
+    int b, head, tile;   // selected: b is the token
+    int at;              // unit of the item
+    long long left;
+};
+
+// Executed by one warp.  `units`: shared memory for one int per request.
+__device__ __forceinline__ Start find_start(const AttnArgs& a, int* units, int lane)
 {
-    int u = 0;
-    const int tiles = tiles_of(a, nq);
-    for (int i = lane; i < tiles; i += 32) u += tile_span(a, nq, kv, i).n + kItemUnits;
+    Start s = {0, 0, 0, 0, 0};
+    long long total = 0;
+#pragma unroll 1
+    for (int b = lane; b < a.batch; b += 32) {
+        int tok0, nq, kv, u = 0;
+        request_of(a, b, tok0, nq, kv);
+        const int tiles = tiles_of(a, nq);
+#pragma unroll 1
+        for (int i = 0; i < tiles; ++i) u += tile_span(a, nq, kv, i).n + kItemUnits;
+        units[b] = u;
+        total += u;
+    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-    return u;
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    total *= a.kv_heads;
+    long long rem = range_start(total, gridDim.x, blockIdx.x);
+    s.left = range_start(total, gridDim.x, blockIdx.x + 1) - rem;
+    if (s.left == 0) return s;
+    // the request that holds unit `rem`, 32 at a time
+    int per_head = 0;
+#pragma unroll 1
+    for (int c = 0; c < a.batch; c += 32) {
+        const int v = c + lane < a.batch ? units[c + lane] : 0;
+        long long incl = (long long)v * a.kv_heads;
+        const long long mine = incl;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        const unsigned who = __ballot_sync(0xffffffffu, incl - mine <= rem && rem < incl);
+        if (who) {
+            const int l = __ffs(who) - 1;
+            s.b = c + l;
+            per_head = __shfl_sync(0xffffffffu, v, l);
+            rem -= __shfl_sync(0xffffffffu, incl - mine, l);
+            break;
+        }
+        rem -= __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (per_head == 0) { s.left = 0; return s; }    // never
+    s.head = (int)(rem / per_head);
+    int off = (int)(rem - (long long)s.head * per_head);
+    // the tile of that request's head, 32 at a time
+    int tok0, nq, kv;
+    request_of(a, s.b, tok0, nq, kv);
+    const int tiles = tiles_of(a, nq);
+#pragma unroll 1
+    for (int c = 0; c < tiles; c += 32) {
+        const int v = c + lane < tiles ? tile_span(a, nq, kv, c + lane).n + kItemUnits : 0;
+        int incl = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        const unsigned who = __ballot_sync(0xffffffffu, incl - v <= off && off < incl);
+        if (who) {
+            const int l = __ffs(who) - 1;
+            s.tile = c + l;
+            s.at = off - __shfl_sync(0xffffffffu, incl - v, l);
+            break;
+        }
+        off -= __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return s;
 }
 
 template <int D, bool FP16, bool SEL>
@@ -405,14 +472,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     // what follows reads memory that the kernel before this one may have written
     allow_dependent_launch();
     grid_dependency_wait();
-    // units per request and kv head, in the ring's memory until the copies begin
-    int* units = reinterpret_cast<int*>(smem + C::kRing);
-    if constexpr (!SEL) {
-        for (int b = warp; b < a.batch; b += kThreads / 32) {
-            int tok0, nq, kv;
-            request_of(a, b, tok0, nq, kv);
-            const int u = head_units(a, nq, kv, lane);
-            if (lane == 0) units[b] = u;
+    const int sel_tiles = SEL ? (a.sel_k + kAttnTileKeys - 1) / kAttnTileKeys : 0;
+    Start start = {0, 0, 0, 0, 0};
+    if (warp == kLoadWarp) {
+        if constexpr (SEL) {
+            const int per_item = sel_tiles + kItemUnits;
+            const long long total = (long long)a.tokens * a.kv_heads * per_item;
+            const long long s0 = range_start(total, gridDim.x, blockIdx.x);
+            start.left = range_start(total, gridDim.x, blockIdx.x + 1) - s0;
+            const long long item = s0 / per_item;
+            start.at = (int)(s0 - item * per_item);
+            start.b = (int)(item / a.kv_heads);
+            start.head = (int)(item - (long long)start.b * a.kv_heads);
+        } else {
+            // units per request in the ring's memory, which nobody else
+            // touches before the copies begin
+            start = find_start(a, reinterpret_cast<int*>(smem + C::kRing), lane);
+            __syncwarp();
+            fence_proxy_async_smem();
         }
     }
     tc_fence_before();
@@ -424,81 +501,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         regs_dec<kLowRegs>();
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ producer
-        int b = 0, head = 0, tile = 0;   // the range's start, and the unit of that
-        int at = 0;                      // item where it lies
-        long long left;                              // units left in the range
-        const int sel_tiles = SEL ? (a.sel_k + kAttnTileKeys - 1) / kAttnTileKeys : 0;
-        if constexpr (SEL) {
-            const int per_item = sel_tiles + kItemUnits;
-            const long long total = (long long)a.tokens * a.kv_heads * per_item;
-            const long long s0 = range_start(total, gridDim.x, blockIdx.x);
-            left = range_start(total, gridDim.x, blockIdx.x + 1) - s0;
-            const long long item = s0 / per_item;
-            at = (int)(s0 - item * per_item);
-            b = (int)(item / a.kv_heads);           // the token
-            head = (int)(item - (long long)b * a.kv_heads);
-        } else {
-            long long total = 0;
-            for (int i = lane; i < a.batch; i += 32) total += units[i];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-            total *= a.kv_heads;
-            const long long s0 = range_start(total, gridDim.x, blockIdx.x);
-            left = range_start(total, gridDim.x, blockIdx.x + 1) - s0;
-            // the request that holds unit s0
-            long long before = 0, off = 0;
-            bool found = false;
-            for (int c = 0; c < a.batch && !found && left > 0; c += 32) {
-                const long long v = c + lane < a.batch ? (long long)units[c + lane] * a.kv_heads : 0;
-                long long incl = v;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const long long u = __shfl_up_sync(0xffffffffu, incl, o);
-                    if (lane >= o) incl += u;
-                }
-                const bool mine = before + incl - v <= s0 && s0 < before + incl;
-                const unsigned who = __ballot_sync(0xffffffffu, mine);
-                if (who) {
-                    const int l = __ffs(who) - 1;
-                    b = c + l;
-                    off = s0 - __shfl_sync(0xffffffffu, before + incl - v, l);
-                    found = true;
-                }
-                before += __shfl_sync(0xffffffffu, incl, 31);
-            }
-            if (left > 0) {
-                const int per_head = units[b];
-                head = (int)(off / per_head);
-                int rem = (int)(off - (long long)head * per_head);
-                int tok0, nq, kv;
-                request_of(a, b, tok0, nq, kv);
-                const int tiles = tiles_of(a, nq);
-                found = false;
-                for (int c = 0; c < tiles && !found; c += 32) {
-                    const int v = c + lane < tiles ? tile_span(a, nq, kv, c + lane).n + kItemUnits : 0;
-                    int incl = v;
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const int u = __shfl_up_sync(0xffffffffu, incl, o);
-                        if (lane >= o) incl += u;
-                    }
-                    const unsigned who = __ballot_sync(0xffffffffu, incl - v <= rem && rem < incl);
-                    if (who) {
-                        const int l = __ffs(who) - 1;
-                        tile = c + l;
-                        at = rem - __shfl_sync(0xffffffffu, incl - v, l);
-                        found = true;
-                    } else {
-                        rem -= __shfl_sync(0xffffffffu, incl, 31);
-                    }
-                }
-            }
-        }
-        __syncwarp();
-        // `units` has been read; the ring's memory is the copies' from here
-        // on (no other warp touches it before a full barrier)
-        fence_proxy_async_smem();
-
+        int b = start.b, head = start.head, tile = start.tile, at = start.at;
+        long long left = start.left;                 // units left in the range
         int* piece = a.pieces + (long long)blockIdx.x * 2 * kPieceInts;
         if (lane < 2) piece[lane * kPieceInts + kPcUsed] = 0;
         __syncwarp();
@@ -969,55 +973,64 @@ __global__ void __launch_bounds__(kThreads, 1)
                 else masked = key0 < all_lo || key0 + kAttnTileKeys > all_hi;
 
                 if (active) {
-                    uint32_t x[4][32];
+                    // bit k % 32 of word k / 32 (selected: k / 4 of k % 4): key k is shown
+                    uint32_t shown[4];
+                    if constexpr (SEL) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_ld32_async(t_s + 32 * q, x[q]);
+                        for (int e = 0; e < 4; ++e) shown[e] = there[e];
+                    } else if (masked) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_wait_bind32(x[q]);
-                    if (masked) {
-                        const uint32_t kNone = 0xff800000u;    // -inf
-                        const int lo = row_lo - key0, hi = row_hi - key0;
-#pragma unroll
-                        for (int k = 0; k < 128; ++k) {
-                            if constexpr (SEL) {
-                                if (!((there[k & 3] >> (k >> 2)) & 1u)) x[k >> 5][k & 31] = kNone;
-                            } else {
-                                if (k < lo || k >= hi) x[k >> 5][k & 31] = kNone;
-                            }
+                        for (int e = 0; e < 4; ++e) {
+                            const int lo = min(max(row_lo - key0 - 32 * e, 0), 32);
+                            const int hi = min(max(row_hi - key0 - 32 * e, 0), 32);
+                            shown[e] = lo < hi ? (0xffffffffu >> (32 - hi + lo)) << lo : 0u;
                         }
                     }
+                    uint32_t x[4][32];
+                    auto load = [&]() {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) tmem_ld32_async(t_s + 32 * q, x[q]);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) tmem_wait_bind32(x[q]);
+                        if (masked) {
+#pragma unroll
+                            for (int k = 0; k < 128; ++k) {
+                                const uint32_t w = SEL ? shown[k & 3] >> (k >> 2) : shown[k >> 5] >> (k & 31);
+                                if (!(w & 1u)) x[k >> 5][k & 31] = 0xff800000u;    // -inf
+                            }
+                        }
+                    };
+                    load();
                     float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                     for (int k = 0; k < 128; k += 2)
                         t[(k >> 1) & 3] = fmaxf(t[(k >> 1) & 3], fmaxf(__uint_as_float(x[k >> 5][k & 31]),
                                                                        __uint_as_float(x[k >> 5][(k & 31) + 1])));
-                    const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
                     // a new reference when the old one is too low by 2^8
-                    const float m_new = fmaxf(m, top);
+                    const float m_new = fmaxf(m, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])));
                     const bool grow = valid && (m_new - m) * c > 8.0f;   // m = -inf: yes unless m_new is
                     if (__any_sync(0xffffffffu, grow)) {
                         const float f = grow ? exp2_approx((m - m_new) * c) : 1.0f;
                         if (grow) m = m_new;
                         l *= f;
-                        if (i > 0) {
-                            // eight columns at a time: the row of S stays in registers
+                        // eight columns at a time: the row of S stays in registers
 #pragma unroll 1
-                            for (int d = 0; d < D; d += 8) {
-                                float o[8];
-                                tmem_ld8(t_o + d, o);
+                        for (int d = 0; i > 0 && d < D; d += 8) {
+                            float o[8];
+                            tmem_ld8(t_o + d, o);
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) o[e] *= f;
-                                tmem_st8(t_o + d, o);
-                            }
+                            for (int e = 0; e < 8; ++e) o[e] *= f;
+                            tmem_st8(t_o + d, o);
                         }
                     }
                     // c x - c m in one fused product and sum: c m is rounded
                     // once, a factor that all of the row shares but the next
-                    // reference and the other pieces do not, 2^-15 for |c m|
-                    // up to 2^10.  Past that the difference is taken first.
+                    // reference and the other pieces do not, 2^-15 for |c m| up
+                    // to 2^10.  Past that the difference is taken first, in
+                    // tensor memory.
                     float mc = m == -INFINITY ? 0.0f : m * c;
-                    const float ref = m == -INFINITY ? 0.0f : m;
                     if (__any_sync(0xffffffffu, fabsf(mc) > 1024.0f)) {
+                        const float ref = m == -INFINITY ? 0.0f : m;
 #pragma unroll
                         for (int k = 0; k < 128; ++k)
                             x[k >> 5][k & 31] = __float_as_uint(__uint_as_float(x[k >> 5][k & 31]) - ref);
@@ -1148,50 +1161,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if ((alt || h == 1) && threadIdx.x % 128 == 96) mbar_arrive(empty_bar(v_place % S));
             }
             tc_fence_after();
-            const int token = it[kItTok0] + half_tok0 + row_tok;
             const bool whole = it[kItFlags] & kWhole;
-            const int qhead = it[kItHead] * G + row_head;
-            const long long ws_row = ((long long)blockIdx.x * 2 + it[kItSlot]) * kAttnSlotRows +
-                                     (alt ? 0 : h * kAttnHalfRows) + row;
-            if (!alt) {
-                if (active) {
-                    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-                    uint16_t* orow = static_cast<uint16_t*>(a.out) + (long long)token * a.out_token +
-                                     (long long)qhead * a.out_head;
-                    float* prow = a.partial + ws_row * D;
-#pragma unroll
-                    for (int d = 0; d < D; d += 32) {
-                        uint32_t o[32];
-                        tmem_ld32_async(t_o + d, o);
-                        tmem_wait_bind32(o);
-                        if (valid) {
-                            if (whole) {
-#pragma unroll
-                                for (int e = 0; e < 32; e += 8) {
-                                    uint32_t w[4];
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k)
-                                        w[k] = pack16<FP16>(__uint_as_float(o[e + 2 * k]) * inv,
-                                                            __uint_as_float(o[e + 2 * k + 1]) * inv);
-                                    *reinterpret_cast<uint4*>(orow + d + e) = make_uint4(w[0], w[1], w[2], w[3]);
-                                }
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < 32; e += 4)
-                                    *reinterpret_cast<uint4*>(prow + d + e) =
-                                        make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                            }
-                        }
-                    }
-                    if (valid) {
-                        if (!whole) a.stats[ws_row] = make_float2(m, l);
-                        else if (a.lse != nullptr)
-                            a.lse[(long long)token * a.kv_heads * G + qhead] =
-                                l == 0.0f ? -INFINITY : m * a.scale + logf(l);
-                    }
-                }
-            } else {
-                // both halves hold these rows: group h writes columns h D/2 ..
+            float top = m, sum = l, g0 = 1.0f, g1 = 0.0f;
+            if (alt) {
+                // both halves hold these rows: they join, and group h writes
+                // columns h D / 2 .. of the result
                 stats[h * 128 + row] = make_float2(m, l);
                 tc_fence_before();
                 __syncwarp();
@@ -1200,56 +1174,62 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 ++alt_phase;
                 tc_fence_after();
-                if (active) {
-                    const float2 s0 = stats[row], s1 = stats[128 + row];
-                    const float top = fmaxf(s0.x, s1.x);
-                    const float f0 = s0.x == -INFINITY ? 0.0f : exp2_approx((s0.x - top) * c);
-                    const float f1 = s1.x == -INFINITY ? 0.0f : exp2_approx((s1.x - top) * c);
-                    const float sum = s0.y * f0 + s1.y * f1;
+                const float2 s0 = stats[row], s1 = stats[128 + row];
+                top = fmaxf(s0.x, s1.x);
+                g0 = s0.x == -INFINITY ? 0.0f : exp2_approx((s0.x - top) * c);
+                g1 = s1.x == -INFINITY ? 0.0f : exp2_approx((s1.x - top) * c);
+                sum = s0.y * g0 + s1.y * g1;
+            }
+            if (active) {
+                if (whole) {
                     const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-                    const float g0 = whole ? f0 * inv : f0, g1 = whole ? f1 * inv : f1;
-                    uint16_t* orow = static_cast<uint16_t*>(a.out) + (long long)token * a.out_token +
-                                     (long long)qhead * a.out_head;
-                    float* prow = a.partial + ws_row * D;
+                    g0 *= inv;
+                    g1 *= inv;
+                }
+                const int token = it[kItTok0] + half_tok0 + row_tok;
+                const int qhead = it[kItHead] * G + row_head;
+                const long long ws_row = ((long long)blockIdx.x * 2 + it[kItSlot]) * kAttnSlotRows +
+                                         (alt ? 0 : h * kAttnHalfRows) + row;
+                uint16_t* orow = static_cast<uint16_t*>(a.out) + (long long)token * a.out_token +
+                                 (long long)qhead * a.out_head;
+                float* prow = a.partial + ws_row * D;
+                const bool both = alt && n > 1;          // half 1 saw a tile, too
+                const uint32_t o0 = alt ? lane_addr + kColO : t_o;
+                const int d_end = alt ? (h + 1) * (D / 2) : D;
+#pragma unroll 1
+                for (int d = alt ? h * (D / 2) : 0; d < d_end; d += 16) {
+                    uint32_t o[16], u[16];
+                    tmem_ld16_async(o0 + d, o);
+                    if (both) tmem_ld16_async(lane_addr + kColO + 128u + d, u);
+                    tmem_wait_bind16(o);
 #pragma unroll
-                    for (int dd = 0; dd < D / 2; dd += 32) {
-                        const int d = h * (D / 2) + dd;
-                        uint32_t o[32], u[32];
-                        tmem_ld32_async(lane_addr + kColO + d, o);
-                        tmem_ld32_async(lane_addr + kColO + 128u + d, u);
-                        tmem_wait_bind32(o);
-                        tmem_wait_bind32(u);
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * g0);
+                    if (both) {
+                        tmem_wait_bind16(u);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            float v = __uint_as_float(o[e]) * g0;
-                            if (n > 1) v = fmaf(__uint_as_float(u[e]), g1, v);   // half 1 saw a tile
-                            o[e] = __float_as_uint(v);
-                        }
-                        if (valid) {
-                            if (whole) {
-#pragma unroll
-                                for (int e = 0; e < 32; e += 8) {
-                                    uint32_t w[4];
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k)
-                                        w[k] = pack16<FP16>(__uint_as_float(o[e + 2 * k]),
-                                                            __uint_as_float(o[e + 2 * k + 1]));
-                                    *reinterpret_cast<uint4*>(orow + d + e) = make_uint4(w[0], w[1], w[2], w[3]);
-                                }
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < 32; e += 4)
-                                    *reinterpret_cast<uint4*>(prow + d + e) =
-                                        make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                            }
-                        }
+                        for (int e = 0; e < 16; ++e)
+                            o[e] = __float_as_uint(fmaf(__uint_as_float(u[e]), g1, __uint_as_float(o[e])));
                     }
-                    if (valid && h == 0) {
-                        if (!whole) a.stats[ws_row] = make_float2(top, sum);
-                        else if (a.lse != nullptr)
-                            a.lse[(long long)token * a.kv_heads * G + qhead] =
-                                sum == 0.0f ? -INFINITY : top * a.scale + logf(sum);
+                    if (valid && whole) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            w[e] = pack16<FP16>(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+                        uint4* dst = reinterpret_cast<uint4*>(orow + d);
+                        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    } else if (valid) {
+                        uint4* dst = reinterpret_cast<uint4*>(prow + d);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                     }
+                }
+                if (valid && (h == 0 || !alt)) {
+                    if (!whole) a.stats[ws_row] = make_float2(top, sum);
+                    else if (a.lse != nullptr)
+                        a.lse[(long long)token * a.kv_heads * G + qhead] =
+                            sum == 0.0f ? -INFINITY : top * a.scale + logf(sum);
                 }
             }
             tc_fence_before();
