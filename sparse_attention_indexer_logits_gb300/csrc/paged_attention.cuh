@@ -57,7 +57,10 @@ constexpr int kThreads = 384;      // three warpgroups: softmax, softmax, MMA an
 // gives some back and the softmax groups, which hold a row of S, take them
 // (2 * 208 + 88 = 3 * 168).
 constexpr int kLaunchRegs = 168, kHighRegs = 208, kLowRegs = 88;
-constexpr int kMmaWarp = 8;
+// (a scheduler serves warps w, w + 4, w + 8: the issuer, which polls, is not
+// with the warps that hold the first 32 rows, all the rows of a small call)
+constexpr int kSoftmaxWarps = 8;
+constexpr int kMmaWarp = 11;
 constexpr int kLoadWarp = 9;
 constexpr int kLandWarp = 10;
 constexpr int kItemSlots = 4;
@@ -497,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp >= kMmaWarp) {
+    if (warp >= kSoftmaxWarps) {
         regs_dec<kLowRegs>();
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ producer
