@@ -450,13 +450,24 @@ def pml_fp8_paged_mqa_logits_noalloc(q: torch.Tensor, kv_fused: torch.Tensor,
 
 # ---------------------------------------------------------------- serving operators
 
+# A decode step makes these calls every few microseconds of GPU time, so their
+# checks look at each tensor once and the stream is read without a wrapper.
+
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-_IS64 = {torch.int32: 0, torch.int64: 1, torch.float32: 0, torch.float64: 1}
+_HALVES = (torch.bfloat16, torch.float16)
+_INTS = {torch.int32: 0, torch.int64: 1}
+_FREQS = {torch.float32: 0, torch.float64: 1}
+_serving_calls: dict = {}
 
 
-def _serving(name: str, *args, stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    rc = getattr(lib(), name)(*args, s.cuda_stream)
+def _serving(name: str, stream, *args):
+    call = _serving_calls.get(name)
+    if call is None:
+        call = _serving_calls[name] = getattr(lib(), name)
+    if stream is None:
+        rc = call(*args, torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
+    else:
+        rc = call(*args, stream.cuda_stream)
     if rc != 0:
         raise PmlError(rc, name)
 
@@ -466,44 +477,57 @@ def _addr(t: torch.Tensor | None):
 
 
 def _heads(t: torch.Tensor, name: str, dtype=None):
-    """Checks a ``[tokens, heads, dim]`` tensor with unit last stride."""
+    """Shape, and (address, token stride, head stride) of a ``[tokens, heads,
+    dim]`` tensor with unit last stride."""
+    shape, strides = t.shape, t.stride()
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
+    if len(shape) != 3 or (strides[2] != 1 and shape[2] > 1):
         raise ValueError(f"{name} must be [tokens, heads, dim] with unit last stride")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}")
+    return shape, (t.data_ptr(), strides[0], strides[1])
 
 
 def _ints(t: torch.Tensor, name: str, count: int | None = None):
-    if not t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous():
+    """Address of a contiguous int32 tensor of `count` values."""
+    if t.dtype is not torch.int32 or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA int32 tensor")
     if count is not None and t.numel() != count:
         raise ValueError(f"{name} must hold {count} values")
+    return t.data_ptr()
 
 
 def _rotation(positions: torch.Tensor, inv_freq: torch.Tensor, tokens: int):
-    if not positions.is_cuda or positions.dtype not in (torch.int32, torch.int64):
+    """(address, 64-bit) of the positions and of the frequencies, rotated elements."""
+    p64, f64 = _INTS.get(positions.dtype), _FREQS.get(inv_freq.dtype)
+    if p64 is None or not positions.is_cuda:
         raise ValueError("positions must be a CUDA int32 or int64 tensor")
-    if not inv_freq.is_cuda or inv_freq.dtype not in (torch.float32, torch.float64):
+    if f64 is None or not inv_freq.is_cuda:
         raise ValueError("inv_freq must be a CUDA float32 or float64 tensor")
     if not positions.is_contiguous() or not inv_freq.is_contiguous():
         raise ValueError("positions and inv_freq must be contiguous")
     if positions.numel() != tokens:
         raise ValueError("positions must hold one value per token")
-    return _IS64[positions.dtype], _IS64[inv_freq.dtype], 2 * inv_freq.numel()
+    return positions.data_ptr(), p64, inv_freq.data_ptr(), f64, 2 * inv_freq.numel()
 
 
 def _table(t: torch.Tensor, name: str = "block_table"):
-    if not t.is_cuda or t.dtype != torch.int32 or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+    """Shape, address and row stride of an int32 ``[rows, width]`` tensor."""
+    shape, strides = t.shape, t.stride()
+    if t.dtype is not torch.int32 or not t.is_cuda or len(shape) != 2 or (strides[1] != 1 and shape[1] > 1):
         raise ValueError(f"{name} must be a CUDA int32 [rows, width] tensor with unit last stride")
+    return shape, t.data_ptr(), strides[0]
 
 
-def _cache(t: torch.Tensor, name: str, like: torch.Tensor):
-    if not t.is_cuda or t.dim() != 4 or t.shape[1] != 64 or (t.stride(3) != 1 and t.shape[3] > 1):
+def _cache(t: torch.Tensor, name: str, dtype):
+    """Shape, and (address, page, slot and head strides) of a cache."""
+    shape, strides = t.shape, t.stride()
+    if not t.is_cuda or len(shape) != 4 or shape[1] != 64 or (strides[3] != 1 and shape[3] > 1):
         raise ValueError(f"{name} must be a CUDA [pages, 64, heads, dim] tensor with unit last stride")
-    if t.dtype != like.dtype:
-        raise ValueError(f"{name} must be {like.dtype}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    return shape, (t.data_ptr(), strides[0], strides[1], strides[2])
 
 
 def pml_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
@@ -517,21 +541,19 @@ def pml_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
     head is rotated, from element ``rot_offset`` on; pairs are ``(j, rot_dim/2
     + j)``, or ``(2j, 2j+1)`` when ``interleaved``.  ``gradient=True`` takes
     the output's gradient to the input's.  ``out`` may be ``x``."""
-    _heads(x, "x")
-    if x.dtype not in _DTYPES:
+    shape, src = _heads(x, "x")
+    dtype = _DTYPES.get(x.dtype)
+    if dtype is None:
         raise ValueError("x must be float32, bfloat16 or float16")
-    tokens, heads, dim = x.shape
-    p64, f64, rot = _rotation(positions, inv_freq, tokens)
+    tokens, heads, dim = shape
+    pos, p64, freq, f64, rot = _rotation(positions, inv_freq, tokens)
     if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=x.dtype, device=x.device)
-    else:
-        _heads(out, "out", x.dtype)
-        if out.shape != x.shape:
-            raise ValueError("out must have x's shape")
-    _serving("pml_rope", x.data_ptr(), x.stride(0), x.stride(1), out.data_ptr(), out.stride(0),
-             out.stride(1), _DTYPES[x.dtype], positions.data_ptr(), p64, inv_freq.data_ptr(), f64,
-             rot, rot_offset, int(interleaved), mscale, int(gradient), tokens, heads, dim,
-             stream=stream)
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    out_shape, dst = _heads(out, "out", x.dtype)
+    if out_shape != shape:
+        raise ValueError("out must have x's shape")
+    _serving("pml_rope", stream, *src, *dst, dtype, pos, p64, freq, f64, rot, rot_offset,
+             int(interleaved), mscale, int(gradient), tokens, heads, dim)
     return out
 
 
@@ -544,36 +566,31 @@ def pml_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions
     ``positions[t] % 64`` of page ``block_table[requests[t], positions[t] // 64]``
     of their caches ``[pages, 64, kv_heads, dim]`` (any strides).  bf16 or
     fp16; a negative request or position makes the token padding."""
-    _heads(q, "q")
-    if q.dtype not in (torch.bfloat16, torch.float16):
+    dtype = q.dtype
+    shape, qa = _heads(q, "q")
+    if dtype not in _HALVES:
         raise ValueError("q must be bfloat16 or float16")
-    _heads(k, "k", q.dtype)
-    _heads(v, "v", q.dtype)
-    tokens, heads, dim = q.shape
-    kv_heads = k.shape[1]
-    if k.shape != (tokens, kv_heads, dim) or v.shape != k.shape:
+    k_shape, ka = _heads(k, "k", dtype)
+    v_shape, va = _heads(v, "v", dtype)
+    tokens, heads, dim = shape
+    kv_heads = k_shape[1]
+    if v_shape != k_shape or k_shape[0] != tokens or k_shape[2] != dim:
         raise ValueError("k and v must be [tokens, kv_heads, dim] with q's tokens and dim")
-    p64, f64, rot = _rotation(positions, inv_freq, tokens)
-    _ints(requests, "requests", tokens)
-    _table(block_table)
-    _cache(k_cache, "k_cache", q)
-    _cache(v_cache, "v_cache", q)
-    if k_cache.shape != v_cache.shape or k_cache.shape[2:] != k.shape[1:]:
+    pos, p64, freq, f64, rot = _rotation(positions, inv_freq, tokens)
+    req = _ints(requests, "requests", tokens)
+    (rows, width), table, bt_stride = _table(block_table)
+    c_shape, kc = _cache(k_cache, "k_cache", dtype)
+    vc_shape, vc = _cache(v_cache, "v_cache", dtype)
+    if c_shape != vc_shape or c_shape[2] != kv_heads or c_shape[3] != dim:
         raise ValueError("k_cache and v_cache must be [pages, 64, kv_heads, dim]")
     if q_out is None:
-        q_out = torch.empty((tokens, heads, dim), dtype=q.dtype, device=q.device)
-    else:
-        _heads(q_out, "q_out", q.dtype)
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
-    _serving("pml_rope_append", q.data_ptr(), q.stride(0), q.stride(1), q_out.data_ptr(),
-             q_out.stride(0), q_out.stride(1), k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(),
-             v.stride(0), v.stride(1), _DTYPES[q.dtype], positions.data_ptr(), p64,
-             requests.data_ptr(), block_table.shape[0], inv_freq.data_ptr(), f64, rot, rot_offset,
-             int(interleaved), mscale, k_cache.data_ptr(), k_cache.stride(0), k_cache.stride(1),
-             k_cache.stride(2), v_cache.data_ptr(), v_cache.stride(0), v_cache.stride(1),
-             v_cache.stride(2), k_cache.shape[0], block_table.data_ptr(), block_table.stride(0),
-             block_table.shape[1], tokens, heads, kv_heads, dim, stream=stream)
+        q_out = torch.empty(shape, dtype=dtype, device=q.device)
+    out_shape, qo = _heads(q_out, "q_out", dtype)
+    if out_shape != shape:
+        raise ValueError("q_out must have q's shape")
+    _serving("pml_rope_append", stream, *qa, *qo, *ka, *va, _DTYPES[dtype], pos, p64, req, rows, freq,
+             f64, rot, rot_offset, int(interleaved), mscale, *kc, *vc, c_shape[0], table, bt_stride,
+             width, tokens, heads, kv_heads, dim)
     return q_out
 
 
@@ -589,63 +606,62 @@ def pml_index_quant_append(q: torch.Tensor, k: torch.Tensor | None, weights: tor
     ``w_out = weights * scale * weight_scale``; k bf16 ``[tokens, 128]``
     rotated, quantised and written with its scale into ``kv_fused`` uint8
     ``[blocks, 8448]`` (``k=None``: no keys).  Returns ``(q_out, w_out)``."""
-    _heads(q, "q", torch.bfloat16)
-    tokens, heads, dim = q.shape
+    shape, qa = _heads(q, "q", torch.bfloat16)
+    tokens, heads, dim = shape
     if dim != 128:
         raise ValueError("q must be bf16 [tokens, heads, 128]")
-    p64, f64, rot = _rotation(positions, inv_freq, tokens)
-    if weights.dtype != torch.float32 or weights.shape != (tokens, heads):
+    pos, p64, freq, f64, rot = _rotation(positions, inv_freq, tokens)
+    if weights.dtype is not torch.float32 or weights.shape != (tokens, heads):
         raise ValueError("weights must be float32 [tokens, heads]")
     _cuda(weights, "weights")
-    blocks = rows = width = stride = k_stride = 0
+    blocks = rows = width = bt_stride = k_stride = 0
+    ka = req = kv = table = None
     if k is not None:
-        if not k.is_cuda or k.dtype != torch.bfloat16 or k.shape != (tokens, 128) or k.stride(1) != 1:
+        if not k.is_cuda or k.dtype is not torch.bfloat16 or k.shape != (tokens, 128) or k.stride(1) != 1:
             raise ValueError("k must be a CUDA bf16 [tokens, 128] tensor with unit last stride")
         if requests is None or kv_fused is None or block_table is None:
             raise ValueError("keys need requests, kv_fused and block_table")
-        _ints(requests, "requests", tokens)
-        _table(block_table)
+        req = _ints(requests, "requests", tokens)
+        (rows, width), table, bt_stride = _table(block_table)
         _cuda(kv_fused, "kv_fused")
-        if kv_fused.dtype != torch.uint8 or kv_fused.numel() % 8448 != 0:
+        blocks, rest = divmod(kv_fused.numel(), 8448)
+        if kv_fused.dtype is not torch.uint8 or rest:
             raise ValueError("kv_fused must be uint8 and hold whole 8448-byte blocks")
-        blocks, k_stride = kv_fused.numel() // 8448, k.stride(0)
-        rows, width, stride = block_table.shape[0], block_table.shape[1], block_table.stride(0)
+        ka, k_stride, kv = k.data_ptr(), k.stride(0), kv_fused.data_ptr()
     if q_out is None:
-        q_out = torch.empty((tokens, heads, 128), dtype=torch.float8_e4m3fn, device=q.device)
+        q_out = torch.empty(shape, dtype=torch.float8_e4m3fn, device=q.device)
     if w_out is None:
         w_out = torch.empty((tokens, heads), dtype=torch.float32, device=q.device)
-    if q_out.shape != q.shape or q_out.element_size() != 1 or w_out.shape != weights.shape or \
-            w_out.dtype != torch.float32:
+    if q_out.shape != shape or q_out.element_size() != 1 or w_out.shape != (tokens, heads) or \
+            w_out.dtype is not torch.float32:
         raise ValueError("q_out must be 1-byte [tokens, heads, 128], w_out float32 [tokens, heads]")
     _cuda(q_out, "q_out")
     _cuda(w_out, "w_out")
-    _serving("pml_index_quant_append", q.data_ptr(), q.stride(0), q.stride(1), _addr(k), k_stride,
-             weights.data_ptr(), weight_scale, positions.data_ptr(), p64, _addr(requests), rows,
-             inv_freq.data_ptr(), f64, rot, rot_offset, int(interleaved), mscale, q_out.data_ptr(),
-             w_out.data_ptr(), _addr(kv_fused), blocks, _addr(block_table), stride, width, tokens,
-             heads, stream=stream)
+    _serving("pml_index_quant_append", stream, *qa, ka, k_stride, weights.data_ptr(), weight_scale, pos,
+             p64, req, rows, freq, f64, rot, rot_offset, int(interleaved), mscale, q_out.data_ptr(),
+             w_out.data_ptr(), kv, blocks, table, bt_stride, width, tokens, heads)
     return q_out, w_out
 
 
-def _attention(name, q, k_cache, v_cache, block_table, kv_lens, out, lse, workspace, softmax_scale):
-    """The checks and arguments that both attention calls share."""
-    _heads(q, "q")
-    if q.dtype not in (torch.bfloat16, torch.float16):
+def _attention(q, k_cache, v_cache, block_table, kv_lens, out, lse, workspace, softmax_scale):
+    """The checks that both attention calls share; their arguments in three runs."""
+    dtype = q.dtype
+    shape, qa = _heads(q, "q")
+    if dtype not in _HALVES:
         raise ValueError("q must be bfloat16 or float16")
-    tokens, heads, dim = q.shape
-    _cache(k_cache, "k_cache", q)
-    _cache(v_cache, "v_cache", q)
-    if k_cache.shape != v_cache.shape or k_cache.shape[3] != dim:
+    tokens, heads, dim = shape
+    c_shape, kc = _cache(k_cache, "k_cache", dtype)
+    v_shape, vc = _cache(v_cache, "v_cache", dtype)
+    if c_shape != v_shape or c_shape[3] != dim:
         raise ValueError("k_cache and v_cache must be [pages, 64, kv_heads, dim] with q's dim")
-    _table(block_table)
-    _ints(kv_lens, "kv_lens", block_table.shape[0])
+    (rows, width), table, bt_stride = _table(block_table)
+    lens = _ints(kv_lens, "kv_lens", rows)
     if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=q.dtype, device=q.device)
-    else:
-        _heads(out, "out", q.dtype)
-        if out.shape != q.shape:
-            raise ValueError("out must have q's shape")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (tokens, heads)
+        out = torch.empty(shape, dtype=dtype, device=q.device)
+    out_shape, oa = _heads(out, "out", dtype)
+    if out_shape != shape:
+        raise ValueError("out must have q's shape")
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != shape[:2]
                             or not lse.is_contiguous() or not lse.is_cuda):
         raise ValueError("lse must be a contiguous CUDA float32 [tokens, heads] tensor")
     if workspace is None:
@@ -654,28 +670,27 @@ def _attention(name, q, k_cache, v_cache, block_table, kv_lens, out, lse, worksp
         raise ValueError("workspace must be a contiguous CUDA tensor")
     if softmax_scale is None:
         softmax_scale = dim ** -0.5
-    kv = (q.data_ptr(), q.stride(0), q.stride(1), k_cache.data_ptr(), k_cache.stride(0),
-          k_cache.stride(1), k_cache.stride(2), v_cache.data_ptr(), v_cache.stride(0),
-          v_cache.stride(1), v_cache.stride(2), _DTYPES[q.dtype], k_cache.shape[0],
-          block_table.data_ptr(), block_table.stride(0), block_table.shape[1], kv_lens.data_ptr())
-    size = (tokens, heads, k_cache.shape[2], dim, softmax_scale)
-    tail = (out.data_ptr(), out.stride(0), out.stride(1), _addr(lse), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size())
-    return out, workspace, kv, size, tail
+    # (the workspace may go back to its allocator when the call returns: what
+    # takes its memory next on this stream runs after the kernels)
+    return (out, rows, (*qa, *kc, *vc, _DTYPES[dtype], c_shape[0], table, bt_stride, width, lens),
+            (tokens, heads, c_shape[2], dim, softmax_scale),
+            (*oa, _addr(lse), workspace.data_ptr(), workspace.numel() * workspace.element_size()),
+            workspace)
 
 
 def pml_attention_workspace(head_dim: int, device=None) -> torch.Tensor:
     """A workspace for the attention calls on ``device``: calls that may
     overlap on the GPU need one each."""
     d = torch.device("cuda" if device is None else device)
-    index = torch.cuda.current_device() if d.index is None else d.index
-    if index not in _num_ctas:
-        _num_ctas[index] = pml_default_num_ctas(index)
-    n = lib().pml_attention_workspace_bytes(_num_ctas[index], head_dim)
-    return torch.empty(max(n, 16), dtype=torch.uint8, device=d)
+    key = (torch.cuda.current_device() if d.index is None else d.index, head_dim)
+    size = _workspace_bytes.get(key)
+    if size is None:
+        size = lib().pml_attention_workspace_bytes(pml_default_num_ctas(key[0]), head_dim)
+        _workspace_bytes[key] = size
+    return torch.empty(max(size, 16), dtype=torch.uint8, device=d)
 
 
-_num_ctas: dict = {}
+_workspace_bytes: dict = {}    # by (device, head dimension)
 
 
 def pml_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -693,15 +708,14 @@ def pml_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     already in its pages.  ``window > 0``: only keys past position - window.
     ``lse`` receives the logarithms of the rows' sums.  ``softmax_scale``
     defaults to ``dim ** -0.5``."""
-    out, workspace, kv, size, tail = _attention("pml_paged_attention", q, k_cache, v_cache, block_table,
-                                                kv_lens, out, lse, workspace, softmax_scale)
-    batch = kv_lens.numel()
+    out, batch, kv, size, tail, workspace = _attention(q, k_cache, v_cache, block_table, kv_lens, out, lse,
+                                                       workspace, softmax_scale)
+    starts = None
     if cu_q is not None:
-        _ints(cu_q, "cu_q", batch + 1)
-    elif batch == 0 or q.shape[0] % batch != 0:
+        starts = _ints(cu_q, "cu_q", batch + 1)
+    elif batch == 0 or size[0] % batch != 0:
         raise ValueError("without cu_q the tokens must divide equally over the requests")
-    _serving("pml_paged_attention", *kv, _addr(cu_q), batch, *size, int(causal), window, *tail,
-             stream=stream)
+    _serving("pml_paged_attention", stream, *kv, starts, batch, *size, int(causal), window, *tail)
     return out
 
 
@@ -713,24 +727,20 @@ def pml_sparse_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     """Attention of each token over the positions ``selected[t]`` (int32
     ``[tokens, k]``, as ``pml_topk_logits`` leaves them; entries below 0 or
     past the request's length are not there) of request ``requests[t]``."""
-    out, workspace, kv, size, tail = _attention("pml_sparse_attention", q, k_cache, v_cache, block_table,
-                                                kv_lens, out, lse, workspace, softmax_scale)
-    tokens = q.shape[0]
-    _ints(requests, "requests", tokens)
-    _table(selected, "selected")
-    if selected.shape[0] != tokens:
+    out, rows, kv, size, tail, workspace = _attention(q, k_cache, v_cache, block_table, kv_lens, out, lse,
+                                                      workspace, softmax_scale)
+    req = _ints(requests, "requests", size[0])
+    (tokens, k), sel, sel_stride = _table(selected, "selected")
+    if tokens != size[0]:
         raise ValueError("selected must hold a row per token")
-    _serving("pml_sparse_attention", *kv, requests.data_ptr(), block_table.shape[0],
-             selected.data_ptr(), selected.stride(0), selected.shape[1], *size, *tail, stream=stream)
+    _serving("pml_sparse_attention", stream, *kv, req, rows, sel, sel_stride, k, *size, *tail)
     return out
 
 
 def _pool(ref_counts, block_table, seq_lens):
-    _ints(ref_counts, "ref_counts")
-    _table(block_table)
-    _ints(seq_lens, "seq_lens", block_table.shape[0])
-    return (ref_counts.data_ptr(), ref_counts.numel(), block_table.data_ptr(), block_table.stride(0),
-            block_table.shape[1], seq_lens.data_ptr(), block_table.shape[0])
+    refs = _ints(ref_counts, "ref_counts")
+    (rows, width), table, bt_stride = _table(block_table)
+    return refs, ref_counts.numel(), table, bt_stride, width, _ints(seq_lens, "seq_lens", rows), rows
 
 
 def pml_pages_fork(ref_counts: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -742,12 +752,9 @@ def pml_pages_fork(ref_counts: torch.Tensor, block_table: torch.Tensor, seq_lens
     int32, updated in place."""
     pool = _pool(ref_counts, block_table, seq_lens)
     n = parents.numel()
-    _ints(parents, "parents")
-    for t, nm in ((children, "children"), (copy_src, "copy_src"), (copy_dst, "copy_dst")):
-        _ints(t, nm, n)
-    _ints(copy_count, "copy_count", 1)
-    _serving("pml_pages_fork", *pool, parents.data_ptr(), children.data_ptr(), n,
-             copy_src.data_ptr(), copy_dst.data_ptr(), copy_count.data_ptr(), stream=stream)
+    _serving("pml_pages_fork", stream, *pool, _ints(parents, "parents"), _ints(children, "children", n), n,
+             _ints(copy_src, "copy_src", n), _ints(copy_dst, "copy_dst", n),
+             _ints(copy_count, "copy_count", 1))
 
 
 def pml_pages_extend(ref_counts: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -756,19 +763,15 @@ def pml_pages_extend(ref_counts: torch.Tensor, block_table: torch.Tensor, seq_le
     """Grows every row to ``new_lens`` tokens with the lowest free pages, in
     (row, page) order; the pages taken are listed in ``new_pages``."""
     pool = _pool(ref_counts, block_table, seq_lens)
-    _ints(new_lens, "new_lens", seq_lens.numel())
-    _ints(new_pages, "new_pages")
-    _ints(new_count, "new_count", 1)
-    _serving("pml_pages_extend", *pool, new_lens.data_ptr(), new_pages.data_ptr(),
-             new_pages.numel(), new_count.data_ptr(), stream=stream)
+    _serving("pml_pages_extend", stream, *pool, _ints(new_lens, "new_lens", pool[-1]),
+             _ints(new_pages, "new_pages"), new_pages.numel(), _ints(new_count, "new_count", 1))
 
 
 def pml_pages_free(ref_counts: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
                    rows: torch.Tensor, stream=None) -> None:
     """The listed rows (distinct) give back their pages; their length becomes 0."""
     pool = _pool(ref_counts, block_table, seq_lens)
-    _ints(rows, "rows")
-    _serving("pml_pages_free", *pool, rows.data_ptr(), rows.numel(), stream=stream)
+    _serving("pml_pages_free", stream, *pool, _ints(rows, "rows"), rows.numel())
 
 
 def pml_pages_compact(ref_counts: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -780,17 +783,13 @@ def pml_pages_compact(ref_counts: torch.Tensor, block_table: torch.Tensor, seq_l
     ``pml_pages_copy`` (``copy_src`` / ``copy_dst`` of ``num_pages // 2`` or
     more entries)."""
     pool = _pool(ref_counts, block_table, seq_lens)
-    _ints(ref_counts_out, "ref_counts_out", ref_counts.numel())
-    _ints(remap, "remap", ref_counts.numel())
-    _table(block_table_out, "block_table_out")
-    if block_table_out.shape != block_table.shape:
+    shape, table_out, out_stride = _table(block_table_out, "block_table_out")
+    if shape != block_table.shape:
         raise ValueError("block_table_out must have block_table's shape")
-    _ints(copy_src, "copy_src")
-    _ints(copy_dst, "copy_dst", copy_src.numel())
-    _ints(copy_count, "copy_count", 1)
-    _serving("pml_pages_compact", *pool, ref_counts_out.data_ptr(), block_table_out.data_ptr(),
-             block_table_out.stride(0), remap.data_ptr(), copy_src.data_ptr(), copy_dst.data_ptr(),
-             copy_src.numel(), copy_count.data_ptr(), stream=stream)
+    n = copy_src.numel()
+    _serving("pml_pages_compact", stream, *pool, _ints(ref_counts_out, "ref_counts_out", pool[1]),
+             table_out, out_stride, _ints(remap, "remap", pool[1]), _ints(copy_src, "copy_src"),
+             _ints(copy_dst, "copy_dst", n), n, _ints(copy_count, "copy_count", 1))
 
 
 def pml_pages_copy(cache: torch.Tensor, copy_src: torch.Tensor, copy_dst: torch.Tensor,
@@ -798,22 +797,20 @@ def pml_pages_copy(cache: torch.Tensor, copy_src: torch.Tensor, copy_dst: torch.
     """Copies page ``copy_src[i]`` over page ``copy_dst[i]`` for ``i <
     copy_count`` in every layer of ``cache`` ``[layers, pages, ...]``
     (``layers=False``: ``[pages, ...]``); each page is contiguous."""
-    if not cache.is_cuda or cache.dim() < (2 if layers else 1):
-        raise ValueError("cache must be a CUDA tensor [layers, pages, ...] or [pages, ...]")
-    _ints(copy_src, "copy_src")
-    _ints(copy_dst, "copy_dst", copy_src.numel())
-    _ints(copy_count, "copy_count", 1)
+    shape, strides = cache.shape, cache.stride()
     at = 1 if layers else 0
+    if not cache.is_cuda or len(shape) <= at:
+        raise ValueError("cache must be a CUDA tensor [layers, pages, ...] or [pages, ...]")
     elems = 1
-    for size, step in zip(reversed(cache.shape[at + 1:]), reversed(cache.stride()[at + 1:])):
+    for size, step in zip(shape[:at:-1], strides[:at:-1]):
         if size > 1 and step != elems:
             raise ValueError("each page of the cache must be contiguous")
         elems *= size
     b = cache.element_size()
-    _serving("pml_pages_copy", cache.data_ptr(), cache.shape[0] if layers else 1,
-             cache.stride(0) * b if layers else 0, cache.shape[at], cache.stride(at) * b, elems * b,
-             copy_src.data_ptr(), copy_dst.data_ptr(), copy_count.data_ptr(), copy_src.numel(),
-             stream=stream)
+    n = copy_src.numel()
+    _serving("pml_pages_copy", stream, cache.data_ptr(), shape[0] if layers else 1,
+             strides[0] * b if layers else 0, shape[at], strides[at] * b, elems * b,
+             _ints(copy_src, "copy_src"), _ints(copy_dst, "copy_dst", n), _ints(copy_count, "copy_count", 1), n)
 
 
 # ---------------------------------------------------------------- pages' keyword style
