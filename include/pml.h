@@ -517,9 +517,7 @@ int pml_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
  * num_requests does too and sets PML_STATUS_BAD_REQUEST.
  *
  * selected     int32 [tokens, selected_stride], k entries used
- * Strides of k_cache and v_cache are multiples of head_dim here (rows of one
- * [rows, head_dim] tensor, fewer than 2^31 of them), else
- * PML_ERR_UNSUPPORTED.  The rest as in pml_paged_attention.
+ * The rest as in pml_paged_attention.
  */
 int pml_sparse_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
                          const void* k_cache, int64_t k_page_stride, int64_t k_slot_stride,

@@ -123,22 +123,6 @@ PoolArgs pool(int32_t* ref_counts, int num_pages, int32_t* block_table, int64_t 
 // Strides of a dimension of one element are never used: any valid one will do.
 int64_t used(int64_t stride, int64_t size, int64_t other) { return size > 1 ? stride : other; }
 
-// The cache as a [rows][head_dim] tensor: row strides of pages, slots and
-// heads, and the number of rows; false if they are not whole rows.
-bool cache_rows(int64_t page, int64_t slot, int64_t head, int64_t pages, int heads, int dim,
-                int& page_rows, int& slot_rows, int& head_rows, int64_t& rows)
-{
-    page = used(page, pages, dim);
-    head = used(head, heads, dim);
-    if (page % dim || slot % dim || head % dim) return false;
-    rows = (pages - 1) * (page / dim) + (kBlockKeys - 1) * (slot / dim) + (heads - 1) * (head / dim) + 1;
-    if (rows > 0x7fffffffLL) return false;
-    page_rows = (int)(page / dim);
-    slot_rows = (int)(slot / dim);
-    head_rows = (int)(head / dim);
-    return true;
-}
-
 // The checks, tensor maps and launches that both attention calls share; `a`
 // comes with what is theirs.
 int attention_call(AttnArgs& a, const void* q, int64_t q_token, int64_t q_head, const void* k_cache,
@@ -173,12 +157,6 @@ int attention_call(AttnArgs& a, const void* q, int64_t q_token, int64_t q_head, 
         !aligned(workspace, 16) || !aligned(lse, 4) || !aligned(block_table, 4) ||
         !aligned(kv_lens, 4) || !aligned(a.cu_q, 4))
         return PML_ERR_ALIGNMENT;
-    int64_t k_rows = 0, v_rows = 0;
-    if (select && (!cache_rows(k_page, k_slot, k_head, num_pages, kv_heads, head_dim, a.sel_page_rows,
-                               a.sel_slot_rows, a.sel_head_rows, k_rows) ||
-                   !cache_rows(v_page, v_slot, v_head, num_pages, kv_heads, head_dim, a.sel_page_rows_v,
-                               a.sel_slot_rows_v, a.sel_head_rows_v, v_rows)))
-        return PML_ERR_UNSUPPORTED;
     DeviceInfo dev;
     cudaError_t e = device_info(dev);
     if (e != cudaSuccess) return cuda_fail(e);
@@ -192,6 +170,14 @@ int attention_call(AttnArgs& a, const void* q, int64_t q_token, int64_t q_head, 
     a.stats = reinterpret_cast<float2*>(ws);
     ws += slots * kAttnSlotRows * 8;
     a.pieces = reinterpret_cast<int*>(ws);
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_slot = ks[0];
+    a.k_head = ks[1];
+    a.k_page = ks[2];
+    a.v_slot = vs[0];
+    a.v_head = vs[1];
+    a.v_page = vs[2];
     a.block_table = block_table;
     a.kv_lens = kv_lens;
     a.out = out;
@@ -219,22 +205,15 @@ int attention_call(AttnArgs& a, const void* q, int64_t q_token, int64_t q_head, 
         e = encode_tiled(qmap, type, 3, q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
         if (e != cudaSuccess) return cuda_fail(e);
     }
-    for (int i = 0; i < 2; ++i) {
-        const void* cache = i ? v_cache : k_cache;
-        CUtensorMap& map = i ? vmap : kmap;
-        if (select) {
-            const uint64_t dims[2] = {(uint64_t)head_dim, (uint64_t)(i ? v_rows : k_rows)};
-            const uint64_t strides[1] = {(uint64_t)head_dim * 2};
-            const uint32_t box[2] = {64, 1};
-            e = encode_tiled(map, type, 2, cache, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
-        } else {
-            const int64_t* s = i ? vs : ks;
-            const uint64_t dims[4] = {(uint64_t)head_dim, (uint64_t)kBlockKeys, (uint64_t)kv_heads,
-                                      (uint64_t)num_pages};
-            const uint64_t strides[3] = {(uint64_t)s[0] * 2, (uint64_t)s[1] * 2, (uint64_t)s[2] * 2};
-            const uint32_t box[4] = {64, (uint32_t)kBlockKeys, 1, 1};
-            e = encode_tiled(map, type, 4, cache, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
-        }
+    kmap = vmap = qmap;
+    for (int i = 0; i < 2 && !select; ++i) {
+        const int64_t* s = i ? vs : ks;
+        const uint64_t dims[4] = {(uint64_t)head_dim, (uint64_t)kBlockKeys, (uint64_t)kv_heads,
+                                  (uint64_t)num_pages};
+        const uint64_t strides[3] = {(uint64_t)s[0] * 2, (uint64_t)s[1] * 2, (uint64_t)s[2] * 2};
+        const uint32_t box[4] = {64, (uint32_t)kBlockKeys, 1, 1};
+        e = encode_tiled(i ? vmap : kmap, type, 4, i ? v_cache : k_cache, dims, strides, box,
+                         CU_TENSOR_MAP_SWIZZLE_128B);
         if (e != cudaSuccess) return cuda_fail(e);
     }
     e = launch_paged_attention(head_dim, fp16, select, qmap, kmap, vmap, a, num_ctas,

@@ -14,12 +14,12 @@ namespace {
 using namespace attn;
 
 constexpr int kJoinWarps = 8;
-constexpr int kJoinSplit = 8;     // CTAs that share one item's rows
 
 // A CTA whose range ended inside an item it had begun (slot 1) owns the join:
 // the item's other pieces are slot 0 of the following CTAs, up to the one
-// that holds its end.  A warp takes a row: lanes hold the pieces' maxima and
-// sums, then D / 32 columns each.
+// that holds its end.  A warp takes 32 rows (neighbours in the workspace) and
+// 16 columns; a lane goes over its row's pieces twice, for the maximum and
+// for the weighted sum.
 template <int D, bool FP16>
 __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const AttnArgs a, int num_ctas)
 {
@@ -30,6 +30,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const A
     if (!rec[kPcUsed]) return;
     const int tok0 = rec[kPcTok0], ntok = rec[kPcNtok], head = rec[kPcHead];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = a.group;
+    const int half_rows = a.half_tokens * G;      // rows in use of a half
+    constexpr int kColGroups = D / 16;
+    // groups of 32 rows, four to a half
+    const int unit = blockIdx.y * kJoinWarps + warp;
+    const int cols = unit % kColGroups * 16, row = unit / kColGroups * 32 + lane;
+    const int in_half = row % kAttnHalfRows;
+    const int i = row / kAttnHalfRows * a.half_tokens + in_half / G, g = in_half % G;
+    const bool valid = in_half < half_rows && i < ntok;
+    if (!__any_sync(0xffffffffu, valid)) return;
     int end = owner + 1;              // the CTA that holds the item's end
     for (; end < num_ctas; end += 32) {
         const int cta = end + lane;
@@ -41,66 +51,49 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const A
             break;
         }
     }
-    if (end >= num_ctas) return;      // never: an item's end is in some range
+    if (end >= num_ctas || !valid) return;      // (an item's end is in some range)
     const int pieces = end - owner + 1;
-    const int G = a.group;
-    constexpr int V = D / 32;
-    for (int r = blockIdx.y * kJoinWarps + warp; r < ntok * G; r += gridDim.y * kJoinWarps) {
-        const int i = r / G, g = r - i * G;
-        const int half = i / a.half_tokens;
-        const int row = half * kAttnHalfRows + (i - half * a.half_tokens) * G + g;
-        // piece p: slot 1 of the owner, then slot 0 of its followers
-        auto ws = [&](int p) {
-            return ((owner + p) * 2LL + (p == 0 ? 1 : 0)) * kAttnSlotRows + row;
-        };
-        float top = -INFINITY;
-        for (int p = lane; p < pieces; p += 32) top = fmaxf(top, a.stats[ws(p)].x);
+    // piece p: slot 1 of the owner, then slot 0 of its followers
+    auto stat = [&](int p) {
+        return a.stats[((owner + p) * 2LL + (p == 0 ? 1 : 0)) * kAttnSlotRows + row];
+    };
+    float top = -INFINITY;
+#pragma unroll 4
+    for (int p = 0; p < pieces; ++p) top = fmaxf(top, stat(p).x);
+    float sum = 0.0f, acc[16] = {};
+#pragma unroll 2
+    for (int p = 0; p < pieces; ++p) {
+        const float2 s = stat(p);
+        const float f = s.x == -INFINITY ? 0.0f : exp2_approx((s.x - top) * a.scale_log2);
+        sum += s.y * f;
+        const float* o = a.partial + partial_at<D>(owner + p, p == 0 ? 1 : 0, cols / 4, row);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        float sum = 0.0f, acc[V] = {};
-        for (int p0 = 0; p0 < pieces; p0 += 32) {
-            float f = 0.0f;
-            if (p0 + lane < pieces) {
-                const float2 s = a.stats[ws(p0 + lane)];
-                if (s.x != -INFINITY) f = exp2_approx((s.x - top) * a.scale_log2);
-                sum += s.y * f;
-            }
-            const int here = min(32, pieces - p0);
-            for (int p = 0; p < here; ++p) {
-                const float fp = __shfl_sync(0xffffffffu, f, p);
-                const float* o = a.partial + ws(p0 + p) * D + lane * V;
-                if constexpr (V == 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(o);
-                    acc[0] = fmaf(v.x, fp, acc[0]);
-                    acc[1] = fmaf(v.y, fp, acc[1]);
-                    acc[2] = fmaf(v.z, fp, acc[2]);
-                    acc[3] = fmaf(v.w, fp, acc[3]);
-                } else {
-                    const float2 v = *reinterpret_cast<const float2*>(o);
-                    acc[0] = fmaf(v.x, fp, acc[0]);
-                    acc[1] = fmaf(v.y, fp, acc[1]);
-                }
-            }
+        for (int k = 0; k < 4; ++k) {
+            const float4 v = *reinterpret_cast<const float4*>(o + k * 4 * kAttnSlotRows);
+            acc[4 * k] = fmaf(v.x, f, acc[4 * k]);
+            acc[4 * k + 1] = fmaf(v.y, f, acc[4 * k + 1]);
+            acc[4 * k + 2] = fmaf(v.z, f, acc[4 * k + 2]);
+            acc[4 * k + 3] = fmaf(v.w, f, acc[4 * k + 3]);
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-        const long long token = tok0 + i;
-        const int qhead = head * G + g;
-        uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + token * a.out_token +
-                                                    qhead * a.out_head + lane * V);
-#pragma unroll
-        for (int e = 0; e < V / 2; ++e) out[e] = pack16<FP16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-        if (lane == 0 && a.lse != nullptr)
-            a.lse[token * a.kv_heads * G + qhead] =
-                sum == 0.0f ? -INFINITY : top * a.scale + logf(sum);
     }
+    const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+    const long long token = tok0 + i;
+    const int qhead = head * G + g;
+    uint32_t w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = pack16<FP16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + token * a.out_token +
+                                          qhead * a.out_head + cols);
+    out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    if (cols == 0 && a.lse != nullptr)
+        a.lse[token * a.kv_heads * G + qhead] = sum == 0.0f ? -INFINITY : top * a.scale + logf(sum);
 }
 
 template <int D, bool FP16>
 cudaError_t launch_join(const AttnArgs& a, int num_ctas, cudaStream_t stream)
 {
-    return launch_dependent(attention_join_kernel<D, FP16>, dim3((unsigned)num_ctas, kJoinSplit),
+    return launch_dependent(attention_join_kernel<D, FP16>, dim3((unsigned)num_ctas, kAttnSlotRows / 32 * (D / 16) / kJoinWarps),
                             kJoinWarps * 32, 0, stream, a, num_ctas);
 }
 

@@ -23,8 +23,11 @@
 // tensor core works on one half while the other half's softmax runs:
 //
 //   producer warp    walks the range; per item a descriptor and the Q rows,
-//                    per tile the K and V pages (TMA, 128-byte swizzle), or
-//                    the listed rows (gather4), into a ring of stages
+//                    per tile the K and V pages (TMA, 128-byte swizzle) into
+//                    a ring of stages; listed rows are gathered by it and a
+//                    second warp, 16 bytes a lane (cp.async).  TMA's gather4
+//                    took 6800 cycles for the 512 row pieces of a tile's K
+//                    and V, twice the time of everything else
 //   MMA warp         S_h = Q_h K^T (both operands in shared memory), then
 //                    O_h += P_h V with P_h read from TMEM, where it replaced
 //                    S_h, and V as the transposed operand
@@ -62,6 +65,7 @@ constexpr int kLaunchRegs = 168, kHighRegs = 208, kLowRegs = 88;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kMmaWarp = 11;
 constexpr int kLoadWarp = 9;
+constexpr int kGatherWarp = 8;     // selected: the second half of each tile's rows
 constexpr int kLandWarp = 10;
 constexpr int kItemSlots = 4;
 constexpr int kItemInts = 16;
@@ -137,6 +141,13 @@ __device__ __forceinline__ bool words_ready(uint32_t landed, uint32_t places, ui
     }
 }
 
+// Where columns 4 * col .. 4 * col + 3 of a row of a workspace slot lie.
+template <int D>
+__device__ __forceinline__ long long partial_at(int cta, int slot, int col, int row)
+{
+    return ((((long long)cta * 2 + slot) * (D / 4) + col) * kAttnSlotRows + row) * 4;
+}
+
 template <int D>
 struct Cfg {
     static constexpr int kBlocks = D / 64;                     // 128-byte column blocks
@@ -184,16 +195,24 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-// Four rows of a [rows][columns] tensor, 64 columns from c0 on, to four
-// consecutive 128-byte rows of shared memory.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint32_t bar,
-                                            int32_t c0, int4 r)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src)
 {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src))
+                 : "memory");
+}
+
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w)
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
         : "memory");
+    return ok != 0;
 }
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32])
@@ -445,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         *total_places = -1;
         st_release_shared(landed_word, 0);
         for (int s = 0; s < S; ++s) {
-            mbar_init(full_bar(s), 1);
+            mbar_init(full_bar(s), SEL ? 2 : 1);
             mbar_init(empty_bar(s), 1);
         }
         mbar_init(drain, 1);
@@ -465,8 +484,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_mbar_init();
         tma_prefetch_map(&qmap);
-        tma_prefetch_map(&kmap);
-        tma_prefetch_map(&vmap);
+        if (!SEL) {
+            tma_prefetch_map(&kmap);
+            tma_prefetch_map(&vmap);
+        }
     }
     if (warp == kMmaWarp) {
         tmem_alloc(smem_addr(tmem_slot), 512);
@@ -477,7 +498,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_dependency_wait();
     const int sel_tiles = SEL ? (a.sel_k + kAttnTileKeys - 1) / kAttnTileKeys : 0;
     Start start = {0, 0, 0, 0, 0};
-    if (warp == kLoadWarp) {
+    const bool loads = warp == kLoadWarp || (SEL && warp == kGatherWarp);
+    const bool lead = warp == kLoadWarp;
+    if (loads) {
         if constexpr (SEL) {
             const int per_item = sel_tiles + kItemUnits;
             const long long total = (long long)a.tokens * a.kv_heads * per_item;
@@ -502,15 +525,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp >= kSoftmaxWarps) {
         regs_dec<kLowRegs>();
-    if (warp == kLoadWarp) {
+    if (loads) {
         // ------------------------------------------------------------ producer
         int b = start.b, head = start.head, tile = start.tile, at = start.at;
         long long left = start.left;                 // units left in the range
         int* piece = a.pieces + (long long)blockIdx.x * 2 * kPieceInts;
-        if (lane < 2) piece[lane * kPieceInts + kPcUsed] = 0;
+        if (lead && lane < 2) piece[lane * kPieceInts + kPcUsed] = 0;
         __syncwarp();
 
-        int pos = 0;                 // stages filled so far
+        int pos = 0;                 // places of the ring taken so far
+        int handed = 0;              // selected: those whose copies are complete
         int item = 0;
         uint32_t qcount = 0;         // Q halves filled so far
         bool ok = true;
@@ -557,10 +581,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int slot = first ? 1 : 0;          // workspace slot of a piece
             // ---- the item's descriptor and Q rows
             const int is = item % kItemSlots;
-            ok = warp_wait(itempty0 + 8u * is, ((item / kItemSlots) & 1) ^ 1, abort_flag, a.status);
+            if (lead) ok = warp_wait(itempty0 + 8u * is, ((item / kItemSlots) & 1) ^ 1, abort_flag, a.status);
             if (!ok) break;
             const int j0 = sp.j0 + j;
-            if (lane == 0) {
+            if (lead && lane == 0) {
                 int* it = items + is * kItemInts;
                 it[kItN] = n;
                 it[kItJ0] = j0;
@@ -586,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // an item of one half takes the Q halves in turn, so its rows come
             // while the item before it is still at work
-            for (int h = 0; h < (alt ? 1 : 2) && ok; ++h, ++qcount) {
+            for (int h = 0; lead && h < (alt ? 1 : 2) && ok; ++h, ++qcount) {
                 const uint32_t qs = qcount & 1u;
                 ok = warp_wait(qempty0 + 8u * qs, ((qcount >> 1) & 1u) ^ 1u, abort_flag, a.status);
                 if (ok && lane == 0) {
@@ -603,86 +627,109 @@ __global__ void __launch_bounds__(kThreads, 1)
 
             // ---- K and V tiles: K runs `ahead` tiles before V
             const int ahead = alt ? 2 : 1;
-            auto begin_stage = [&](uint32_t& dst, uint32_t& fb) {
-                const int s = pos % S;
-                const bool r = warp_wait(empty_bar(s), (uint32_t)((pos / S) & 1) ^ 1u, abort_flag, a.status);
-                dst = base + C::kRing + s * C::kStageBytes;
-                fb = full_bar(s);
-                ++pos;
-                return r;
-            };
             if constexpr (SEL) {
                 const int32_t* list = a.selected + (long long)b * a.sel_stride;
                 const int32_t* table = a.block_table + (long long)req * a.bt_stride;
-                // This lane's four entries of a tile, in three steps a tile
-                // apart, so that no step waits for a load of its own: the
-                // positions; their pages; the cache rows.  `any`: one of them
-                // is there.
+                const int row0 = lead ? 0 : 64;
+                // This lane's two rows of a tile (row0 + lane and 32 on), in
+                // three steps a tile apart, so that no step waits for a load
+                // of its own: the positions (-1: not there), their pages, the
+                // rows' offsets in the cache.
                 auto positions = [&](int t) {
-                    int4 r;
-                    int* pp = &r.x;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int i = (j0 + t) * kAttnTileKeys + 4 * lane + e;
-                        const int p = t < n && i < a.sel_k ? __ldg(list + i) : -1;
-                        pp[e] = p < kv ? p : -1;
+                    const int i = (j0 + t) * kAttnTileKeys + row0 + lane;
+                    int x = t < n && i < a.sel_k ? __ldg(list + i) : -1;
+                    int y = t < n && i + 32 < a.sel_k ? __ldg(list + i + 32) : -1;
+                    return make_int2(x < kv ? x : -1, y < kv ? y : -1);
+                };
+                auto pages = [&](int2 p) {
+                    return make_int2(p.x >= 0 ? __ldg(table + (p.x >> 6)) : 0,
+                                     p.y >= 0 ? __ldg(table + (p.y >> 6)) : 0);
+                };
+                auto settle = [&](int2& g) {
+                    const bool bx = g.x < 0 || g.x >= a.num_pages, by = g.y < 0 || g.y >= a.num_pages;
+                    if (bx || by) atomicOr(a.status, kStatusBadBlock);
+                    if (bx) g.x = 0;
+                    if (by) g.y = 0;
+                };
+                // the oldest tile whose copies are under way is handed over
+                auto hand_over = [&]() {
+                    switch (pos - handed - 1) {
+                    case 0: cp_async_wait<0>(); break;
+                    case 1: cp_async_wait<1>(); break;
+                    case 2: cp_async_wait<2>(); break;
+                    default: cp_async_wait<3>(); break;
                     }
-                    return r;
-                };
-                auto pages = [&](int4 r) {
-                    return make_int4(r.x >= 0 ? __ldg(table + (r.x >> 6)) : 0, r.y >= 0 ? __ldg(table + (r.y >> 6)) : 0,
-                                     r.z >= 0 ? __ldg(table + (r.z >> 6)) : 0, r.w >= 0 ? __ldg(table + (r.w >> 6)) : 0);
-                };
-                // positions become slots; pages that are not there become 0
-                auto settle = [&](int4& pos4, int4& pg, bool& any) {
-                    int* pp = &pos4.x;
-                    int* gg = &pg.x;
-                    bool bad = false;
-                    any = false;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        any |= pp[e] >= 0;
-                        pp[e] = pp[e] >= 0 ? pp[e] & 63 : 0;
-                        if (gg[e] < 0 || gg[e] >= a.num_pages) { bad = true; gg[e] = 0; }
-                    }
-                    if (bad) atomicOr(a.status, kStatusBadBlock);
-                };
-                auto rows = [&](int4 pg, int4 sl, bool v) {
-                    const int pr = v ? a.sel_page_rows_v : a.sel_page_rows;
-                    const int sr = v ? a.sel_slot_rows_v : a.sel_slot_rows;
-                    const int h0 = head * (v ? a.sel_head_rows_v : a.sel_head_rows);
-                    return make_int4(pg.x * pr + sl.x * sr + h0, pg.y * pr + sl.y * sr + h0,
-                                     pg.z * pr + sl.z * sr + h0, pg.w * pr + sl.w * sr + h0);
-                };
-                auto load = [&](const CUtensorMap* map, int4 r, bool any) {
-                    uint32_t dst, fb;
-                    if (!begin_stage(dst, fb)) return false;
-                    const int cnt = __popc(__ballot_sync(0xffffffffu, any));
-                    if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)(cnt * 512 * C::kBlocks));
+                    fence_proxy_async_smem();     // the tensor core reads what this lane has copied
                     __syncwarp();
-                    if (any)
-                        for (int kb = 0; kb < C::kBlocks; ++kb)
-                            tma_gather4(dst + kb * C::kBlockBytes + lane * 512, map, fb, kb * 64, r);
+                    if (lane == 0) mbar_arrive(full_bar(handed % S));
+                    ++handed;
+                };
+                auto gather = [&](const void* cache, long long page_stride, long long slot_stride,
+                                  long long head_stride, int2 p, int2 g) {
+                    const int st = pos % S;
+                    const uint32_t parity = (uint32_t)((pos / S) & 1) ^ 1u;
+                    while (!__all_sync(0xffffffffu, mbar_test(empty_bar(st), parity))) {
+                        // (a stage may wait for one that is still under way here)
+                        if (handed < pos) {
+                            hand_over();
+                        } else {
+                            if (!warp_wait(empty_bar(st), parity, abort_flag, a.status)) return false;
+                            break;
+                        }
+                    }
+                    // D / 8 lanes copy a row; a lane's source is the row of one
+                    // of the 32 lanes, whose offset it is told
+                    constexpr int kRowLanes = D / 8;
+                    const int chunk = lane % kRowLanes, first = lane / kRowLanes * kRowLanes;
+                    const uint32_t dst0 = base + C::kRing + st * C::kStageBytes + (chunk >> 3) * C::kBlockBytes;
+                    const uint16_t* src0 = static_cast<const uint16_t*>(cache) + head * head_stride + chunk * 8;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int at = half ? p.y : p.x, page = half ? g.y : g.x;
+                        const long long off = at < 0 ? -1 : page * page_stride + (at & 63) * slot_stride;
+#pragma unroll
+                        for (int i = 0; i < kRowLanes; ++i) {
+                            const long long o = __shfl_sync(0xffffffffu, off, first + i);
+                            const int r = row0 + 32 * half + first + i;
+                            if (o >= 0) cp_async16(dst0 + r * 128 + (((chunk & 7) ^ (r & 7)) << 4), src0 + o);
+                        }
+                    }
+                    cp_async_commit();
+                    ++pos;
+                    if (pos - handed > min(3, S - 2)) hand_over();
                     return true;
                 };
-                int4 s0 = positions(0), s1 = positions(1), s2 = positions(2), s3 = positions(3);
-                int4 p0 = pages(s0), p1 = pages(s1), p2 = pages(s2);
-                bool a0, a1, a2;
-                settle(s0, p0, a0);
-                settle(s1, p1, a1);
-                ok = load(&kmap, rows(p0, s0, false), a0);
-                if (ok && n > 1) ok = load(&kmap, rows(p1, s1, false), a1);
+                auto gather_k = [&](int2 p, int2 g) {
+                    return gather(a.k_cache, a.k_page, a.k_slot, a.k_head, p, g);
+                };
+                int2 p0 = positions(0), p1 = positions(1), p2 = positions(2), p3 = positions(3);
+                int2 g0 = pages(p0), g1 = pages(p1), g2 = pages(p2);
+                settle(g0);
+                settle(g1);
+                ok = gather_k(p0, g0);
+                if (ok && n > 1) ok = gather_k(p1, g1);
+#pragma unroll 1
                 for (int t = 0; t < n && ok; ++t) {
-                    const int4 s4 = positions(t + 4), p3 = pages(s3);
-                    ok = load(&vmap, rows(p0, s0, true), a0);
-                    settle(s2, p2, a2);
-                    if (ok && t + 2 < n) ok = load(&kmap, rows(p2, s2, false), a2);
-                    p0 = p1; s0 = s1; a0 = a1;
-                    p1 = p2; s1 = s2; a1 = a2;
-                    p2 = p3; s2 = s3; s3 = s4;
+                    const int2 p4 = positions(t + 4), g3 = pages(p3);
+                    ok = gather(a.v_cache, a.v_page, a.v_slot, a.v_head, p0, g0);
+                    settle(g2);
+                    if (ok && t + 2 < n) ok = gather_k(p2, g2);
+                    p0 = p1; g0 = g1;
+                    p1 = p2; g1 = g2;
+                    p2 = p3; g2 = g3; p3 = p4;
                 }
+                // (what is under way is handed over with the next item's
+                // first tiles, or at the end)
             } else {
                 const int32_t* table = a.block_table + (long long)req * a.bt_stride;
+                auto begin_stage = [&](uint32_t& dst, uint32_t& fb) {
+                    const int s = pos % S;
+                    const bool r = warp_wait(empty_bar(s), (uint32_t)((pos / S) & 1) ^ 1u, abort_flag, a.status);
+                    dst = base + C::kRing + s * C::kStageBytes;
+                    fb = full_bar(s);
+                    ++pos;
+                    return r;
+                };
                 // pages with visible keys; others are neither looked up nor read
                 const int page_begin = sp.lo / kBlockKeys;
                 const int page_end = (sp.hi + kBlockKeys - 1) / kBlockKeys;
@@ -743,20 +790,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        if (ok) {
-            const int is = item % kItemSlots;
-            ok = warp_wait(itempty0 + 8u * is, ((item / kItemSlots) & 1) ^ 1, abort_flag, a.status);
-            if (ok && lane == 0) {
-                items[is * kItemInts + kItFlags] = kEnd;
-                mbar_arrive(itfull0 + 8u * is);
+        if constexpr (SEL) {
+            for (; handed < pos; ++handed) {
+                cp_async_wait<0>();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full_bar(handed % S));
             }
         }
-        // copies in flight land before the CTA may leave
-        if (lane == 0) *total_places = pos;
-        for (int t = pos > S ? pos - S : 0; t < pos; ++t)
-            mbar_wait_drain<false>(full_bar(t % S), (uint32_t)((t / S) & 1));
-        for (uint32_t c = qcount > 2 ? qcount - 2 : 0; c < qcount; ++c)
-            mbar_wait_drain<false>(qfull0 + 8u * (c & 1u), (c >> 1) & 1u);
+        if (lead) {
+            if (ok) {
+                const int is = item % kItemSlots;
+                ok = warp_wait(itempty0 + 8u * is, ((item / kItemSlots) & 1) ^ 1, abort_flag, a.status);
+                if (ok && lane == 0) {
+                    items[is * kItemInts + kItFlags] = kEnd;
+                    mbar_arrive(itfull0 + 8u * is);
+                }
+            }
+            if (lane == 0) *total_places = pos;
+            // copies in flight land before the CTA may leave
+            for (int t = pos > S ? pos - S : 0; t < pos; ++t)
+                mbar_wait_drain<false>(full_bar(t % S), (uint32_t)((t / S) & 1));
+            for (uint32_t c = qcount > 2 ? qcount - 2 : 0; c < qcount; ++c)
+                mbar_wait_drain<false>(qfull0 + 8u * (c & 1u), (c >> 1) & 1u);
+        }
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issuer
         // One thread, which issues about as fast as the tensor core computes:
@@ -1195,7 +1252,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                          (alt ? 0 : h * kAttnHalfRows) + row;
                 uint16_t* orow = static_cast<uint16_t*>(a.out) + (long long)token * a.out_token +
                                  (long long)qhead * a.out_head;
-                float* prow = a.partial + ws_row * D;
+                // partial results lie column by column (four at a time): the
+                // rows of a warp are neighbours
+                float* prow = a.partial + partial_at<D>(blockIdx.x, it[kItSlot], 0, (alt ? 0 : h * kAttnHalfRows) + row);
                 const bool both = alt && n > 1;          // half 1 saw a tile, too
                 const uint32_t o0 = alt ? lane_addr + kColO : t_o;
                 const int d_end = alt ? (h + 1) * (D / 2) : D;
@@ -1222,10 +1281,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
                         dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
                     } else if (valid) {
-                        uint4* dst = reinterpret_cast<uint4*>(prow + d);
+                        uint4* dst = reinterpret_cast<uint4*>(prow) + (d >> 2) * kAttnSlotRows;
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                            dst[e * kAttnSlotRows] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                     }
                 }
                 if (valid && (h == 0 || !alt)) {

@@ -158,7 +158,11 @@ struct AttnArgs {
     unsigned int* status;
     int* pieces;                   // workspace: [num_ctas][2][kPieceInts]
     float2* stats;                 // workspace: [num_ctas][2][kAttnSlotRows] (maximum, sum)
-    float* partial;                // workspace: [num_ctas][2][kAttnSlotRows][head_dim]
+    float* partial;                // workspace: [num_ctas][2][head_dim / 4][kAttnSlotRows][4]
+    const void* k_cache;           // selected: read row by row
+    const void* v_cache;
+    long long k_page, k_slot, k_head;   // elements
+    long long v_page, v_slot, v_head;
     long long bt_stride;
     long long sel_stride;
     long long out_token, out_head; // elements
@@ -171,8 +175,6 @@ struct AttnArgs {
     int group;                     // query heads per kv head
     int half_tokens;               // tokens of a 128-row half: 128 / group
     int sel_k;                     // selected: entries per token
-    int sel_page_rows, sel_slot_rows, sel_head_rows;   // selected: row strides in the cache's
-    int sel_page_rows_v, sel_slot_rows_v, sel_head_rows_v;  // [rows][head_dim] view
     int causal;
     int window;                    // > 0: only keys past position - window
     float scale_log2;              // softmax scale * log2(e)

@@ -335,10 +335,11 @@ def test_selected_layouts_and_bad_places():
     assert pml.pml_device_status(clear=True) == pml.STATUS_BAD_REQUEST
     assert (out[1] == 0).all()
     # rows of 64 that do not start at multiples of 64
-    with pytest.raises(pml.PmlError) as e:
-        gaps = torch.zeros((k.shape[0], 64, 2, 72), dtype=BF, device="cuda")[..., :64]
-        pml.pml_sparse_attention(q, gaps, gaps, table, lens, req.cuda(), sel.cuda())
-    assert e.value.code == 2
+    gaps = [torch.full((k.shape[0], 64, 2, 72), math.nan, dtype=BF, device="cuda")[..., :64] for _ in range(2)]
+    for dst, c in zip(gaps, (k, v)):
+        dst.copy_(c)
+    out = pml.pml_sparse_attention(q, gaps[0], gaps[1], table, lens, req.cuda(), sel.cuda(), lse=lse)
+    check_selected(p, req, sel, out, lse)
 
 
 def test_selecting_everything_is_dense_attention():

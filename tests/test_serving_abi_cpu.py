@@ -113,8 +113,6 @@ def test_sparse_attention(L):
     attention_refusals(call)
     assert call(k=0) == INVALID and call(sst=63) == INVALID and call(nreq=0) == INVALID
     assert call(req=None) == INVALID and call(sel=None) == INVALID and call(sel=P + 2) == ALIGNMENT
-    assert call(ks=264) == UNSUPPORTED and call(vp=16384 + 8) == UNSUPPORTED       # not whole rows
-    assert call(pages=1 << 30) == UNSUPPORTED                                      # rows past 2^31
 
 
 def test_workspace_bytes(L):
