@@ -195,10 +195,11 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src)
+// Sixteen bytes, or zeros (bytes = 0: src is not read).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(src))
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes)
                  : "memory");
 }
 
@@ -687,11 +688,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int half = 0; half < 2; ++half) {
                         const int at = half ? p.y : p.x, page = half ? g.y : g.x;
                         const long long off = at < 0 ? -1 : page * page_stride + (at & 63) * slot_stride;
+                        // (the offsets first: a shuffle's latency is not paid
+                        // sixteen times over)
+                        long long o[kRowLanes];
+#pragma unroll
+                        for (int i = 0; i < kRowLanes; ++i) o[i] = __shfl_sync(0xffffffffu, off, first + i);
 #pragma unroll
                         for (int i = 0; i < kRowLanes; ++i) {
-                            const long long o = __shfl_sync(0xffffffffu, off, first + i);
                             const int r = row0 + 32 * half + first + i;
-                            if (o >= 0) cp_async16(dst0 + r * 128 + (((chunk & 7) ^ (r & 7)) << 4), src0 + o);
+                            cp_async16(dst0 + r * 128 + (((chunk & 7) ^ (r & 7)) << 4), src0 + max(o[i], 0ll),
+                                       o[i] < 0 ? 0u : 16u);
                         }
                     }
                     cp_async_commit();
