@@ -705,37 +705,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (pos - handed > min(3, S - 2)) hand_over();
                     return true;
                 };
-                auto gather_k = [&](int2 p, int2 g) {
-                    return gather(a.k_cache, a.k_page, a.k_slot, a.k_head, p, g);
-                };
-                int2 p0 = positions(0), p1 = positions(1), p2 = positions(2), p3 = positions(3);
-                int2 g0 = pages(p0), g1 = pages(p1), g2 = pages(p2);
+                // tile nk's rows (settled), the two tiles' after it on their
+                // way, and those of the one or two tiles whose K is in and V
+                // is not
+                int2 p0 = positions(0), p1 = positions(1), p2 = positions(2);
+                int2 g0 = pages(p0), g1 = pages(p1);
+                int2 vp0 = {}, vg0 = {}, vp1 = {}, vg1 = {};
                 settle(g0);
-                settle(g1);
-                ok = gather_k(p0, g0);
-                if (ok && n > 1) ok = gather_k(p1, g1);
 #pragma unroll 1
-                for (int t = 0; t < n && ok; ++t) {
-                    const int2 p4 = positions(t + 4), g3 = pages(p3);
-                    ok = gather(a.v_cache, a.v_page, a.v_slot, a.v_head, p0, g0);
-                    settle(g2);
-                    if (ok && t + 2 < n) ok = gather_k(p2, g2);
-                    p0 = p1; g0 = g1;
-                    p1 = p2; g1 = g2;
-                    p2 = p3; g2 = g3; p3 = p4;
+                for (int nk = 0, nv = 0; nv < n && ok;) {
+                    const bool is_k = nk < n && nk - nv < ahead;
+                    ok = gather(is_k ? a.k_cache : a.v_cache, is_k ? a.k_page : a.v_page,
+                                is_k ? a.k_slot : a.v_slot, is_k ? a.k_head : a.v_head, is_k ? p0 : vp0,
+                                is_k ? g0 : vg0);
+                    if (is_k) {
+                        if (nk == nv) { vp0 = p0; vg0 = g0; }
+                        else { vp1 = p0; vg1 = g0; }
+                        ++nk;
+                        p0 = p1; g0 = g1; settle(g0);
+                        p1 = p2; g1 = pages(p1);
+                        p2 = positions(nk + 2);
+                    } else {
+                        vp0 = vp1; vg0 = vg1;
+                        ++nv;
+                    }
                 }
                 // (what is under way is handed over with the next item's
                 // first tiles, or at the end)
             } else {
                 const int32_t* table = a.block_table + (long long)req * a.bt_stride;
-                auto begin_stage = [&](uint32_t& dst, uint32_t& fb) {
-                    const int s = pos % S;
-                    const bool r = warp_wait(empty_bar(s), (uint32_t)((pos / S) & 1) ^ 1u, abort_flag, a.status);
-                    dst = base + C::kRing + s * C::kStageBytes;
-                    fb = full_bar(s);
-                    ++pos;
-                    return r;
-                };
                 // pages with visible keys; others are neither looked up nor read
                 const int page_begin = sp.lo / kBlockKeys;
                 const int page_end = (sp.hi + kBlockKeys - 1) / kBlockKeys;
@@ -755,32 +753,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                     g1 = __shfl_sync(0xffffffffu, entry, p - win + 1);
                     want = (p >= page_begin && p < page_end ? 1 : 0) | (p + 1 < page_end ? 2 : 0);
                 };
-                auto load = [&](const CUtensorMap* map, int g0, int g1, int want) {
-                    uint32_t dst, fb;
-                    if (!begin_stage(dst, fb)) return false;
-                    if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)(__popc(want) * C::kBlocks * 8192));
+                // pages of tile nk's K, and of the one or two tiles whose K is
+                // in and V is not
+                int x = 0, y = 0, c = 0, x0 = 0, y0 = 0, c0 = 0, x1 = 0, y1 = 0, c1 = 0;
+#pragma unroll 1
+                for (int nk = 0, nv = 0; nv < n && ok;) {
+                    const bool is_k = nk < n && nk - nv < ahead;
+                    if (is_k) {
+                        pages(nk, x, y, c);
+                        if (nk == nv) { x0 = x; y0 = y; c0 = c; }
+                        else { x1 = x; y1 = y; c1 = c; }
+                        ++nk;
+                    } else {
+                        x = x0; y = y0; c = c0;
+                        x0 = x1; y0 = y1; c0 = c1;
+                        ++nv;
+                    }
+                    const int st = pos % S;
+                    ok = warp_wait(empty_bar(st), (uint32_t)((pos / S) & 1) ^ 1u, abort_flag, a.status);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(full_bar(st), (uint32_t)(__popc(c) * C::kBlocks * 8192));
                     __syncwarp();
                     const int pg = lane / C::kBlocks, kb = lane - pg * C::kBlocks;
-                    if (pg < 2 && ((want >> pg) & 1)) {
-                        tma_load_4d(dst + kb * C::kBlockBytes + pg * 8192, map, fb, kb * 64, 0, head,
-                                    pg ? g1 : g0);
-                    }
-                    return true;
-                };
-                int x0 = 0, y0 = 0, c0 = 0, x1 = 0, y1 = 0, c1 = 0, x2 = 0, y2 = 0, c2 = 0;
-                pages(0, x0, y0, c0);
-                ok = load(&kmap, x0, y0, c0);
-                if (ahead == 2 && n > 1 && ok) {
-                    pages(1, x1, y1, c1);
-                    ok = load(&kmap, x1, y1, c1);
-                }
-                for (int t = 0; t < n && ok; ++t) {
-                    const bool more = t + ahead < n;
-                    if (more) pages(t + ahead, x2, y2, c2);
-                    ok = load(&vmap, x0, y0, c0);
-                    if (ok && more) ok = load(&kmap, x2, y2, c2);
-                    if (ahead == 2) { x0 = x1; y0 = y1; c0 = c1; x1 = x2; y1 = y2; c1 = c2; }
-                    else { x0 = x2; y0 = y2; c0 = c2; }
+                    if (pg < 2 && ((c >> pg) & 1))
+                        tma_load_4d(base + C::kRing + st * C::kStageBytes + kb * C::kBlockBytes + pg * 8192,
+                                    is_k ? &kmap : &vmap, full_bar(st), kb * 64, 0, head, pg ? y : x);
+                    ++pos;
                 }
             }
             // ---- the next item
@@ -839,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t stage = 0;                  // of the next place of the ring
             uint32_t place = 0;                  // places consumed
             uint32_t qcount = 0;                 // Q halves used
-            uint32_t pcount[2] = {0, 0};         // P tiles consumed
+            uint32_t pcount0 = 0, pcount1 = 0;   // P tiles consumed of each half
             bool ok = true, skip = false;
             auto wait = [&](uint32_t b, uint32_t parity) {
                 return mbar_wait<false>(b, parity, abort_flag, a.status);
@@ -850,8 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++place;
                 return st;
             };
-            auto issue_s = [&](int h, int qh, uint32_t st) {
-                const uint64_t ad = q_desc + (uint32_t)(qh * (C::kHalfBytes >> 4));
+            auto issue_s = [&](int h, uint64_t ad, uint32_t st) {
                 const uint64_t bd = k_desc + st * (uint32_t)(C::kStageBytes >> 4);
 #pragma unroll
                 for (int kb = 0; kb < C::kBlocks; ++kb)
@@ -871,10 +868,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mma_f16_tmem_a(tmem + kColO + 128u * h, tmem + kColS + 128u * h + 8u * k,
                                    bd + (uint32_t)(k * (2048 >> 4)), idesc_o, (acc || k) ? 1u : 0u);
             };
-            // places below `place` have landed, and (h >= 0) half h's next P
-            auto wait_words = [&](int h) {
-                return words_ready(landed_word, place, h < 0 ? 0u : ready0 + 16u * h,
-                                   h < 0 ? 0u : ++pcount[h], skip, abort_flag, a.status);
+            // places below `place` have landed, and (words != 0) a half's P number `count`
+            auto wait_words = [&](uint32_t words, uint32_t count) {
+                return words_ready(landed_word, place, words, count, skip, abort_flag, a.status);
             };
             for (int item = 0; ok; ++item) {
                 const int is = item % kItemSlots;
@@ -884,49 +880,62 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int flags = it[kItFlags], n = it[kItN];
                 mbar_arrive(itempty0 + 8u * is);
                 if (flags & kEnd) break;
-                uint32_t ks = take(), vs = 0;
-                const int q0 = qcount & 1u, q1 = q0 ^ 1;     // Q halves of this item
-                auto q_landed = [&](uint32_t c) { return wait(qfull0 + 8u * (c & 1u), (c >> 1) & 1u); };
-                ok = q_landed(qcount++) && ((flags & kAlt) || q_landed(qcount++)) && wait_words(-1);
-                if (!ok) break;
-                tc_fence_after();
-                issue_s(0, q0, ks);
-                if (!(flags & kAlt)) {
-                    issue_s(1, q1, ks);
+                const bool alt = flags & kAlt;
+                const uint32_t q0 = qcount & 1u;             // Q halves of this item
+                for (int i = alt ? 1 : 0; i < 2 && ok; ++i, ++qcount)
+                    ok = wait(qfull0 + 8u * (qcount & 1u), (qcount >> 1) & 1u);
+                if (!alt) {
+                    // both halves see every tile; written out, since with
+                    // these items the tensor core's time is what counts
+                    uint32_t ks = take(), vs = 0;
+                    const uint64_t ad0 = q_desc + q0 * (uint32_t)(C::kHalfBytes >> 4);
+                    const uint64_t ad1 = q_desc + (q0 ^ 1u) * (uint32_t)(C::kHalfBytes >> 4);
+                    ok = ok && wait_words(0u, 0u);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_s(0, ad0, ks);
+                    issue_s(1, ad1, ks);
                     ok = wait(oempty, (uint32_t)(item & 1) ^ 1u);
+#pragma unroll 1
                     for (int t = 0; t < n && ok; ++t) {
                         const bool more = t + 1 < n;
                         vs = take();
                         if (more) ks = take();
-                        ok = wait_words(0);
+                        ok = wait_words(ready0, ++pcount0);
                         if (!ok) break;
                         issue_pv(0, vs, t > 0);
-                        if (more) issue_s(0, q0, ks);
+                        if (more) issue_s(0, ad0, ks);
                         else mma_commit(pvdone0);
-                        ok = wait_words(1);
+                        ok = wait_words(ready0 + 16u, ++pcount1);
                         if (!ok) break;
                         issue_pv(1, vs, t > 0);
-                        if (more) issue_s(1, q1, ks);
+                        if (more) issue_s(1, ad1, ks);
                         else mma_commit(pvdone0 + 8u);
                     }
                 } else {
-                    if (n > 1) {
-                        ks = take();
-                        ok = wait_words(-1);
-                        if (!ok) break;
-                        issue_s(1, q0, ks);
-                    }
-                    ok = wait(oempty, (uint32_t)(item & 1) ^ 1u);
-                    for (int t = 0; t < n && ok; ++t) {
+                    // the halves take the tiles in turn; two steps of scores
+                    // alone, then each the product with V of a tile and the
+                    // scores of the half's next (one copy of the code: these
+                    // items are short or wait for memory)
+                    const uint64_t ad = q_desc + q0 * (uint32_t)(C::kHalfBytes >> 4);
+                    uint32_t ks = 0, vs = 0;
+#pragma unroll 1
+                    for (int t = -2; t < n && ok; ++t) {
                         const int h = t & 1;
                         const bool more = t + 2 < n;
-                        vs = take();
+                        if (t >= 0) vs = take();
                         if (more) ks = take();
-                        ok = wait_words(h);
+                        if (t == 0) ok = wait(oempty, (uint32_t)(item & 1) ^ 1u);
+                        if (t >= 0) {
+                            if (h) ++pcount1;
+                            else ++pcount0;
+                        }
+                        ok = ok && (t >= 0 ? wait_words(ready0 + 16u * h, h ? pcount1 : pcount0) : wait_words(0u, 0u));
                         if (!ok) break;
-                        issue_pv(h, vs, t > 1);
-                        if (more) issue_s(h, q0, ks);
-                        else mma_commit(pvdone0 + 8u * h);
+                        tc_fence_after();
+                        if (t >= 0) issue_pv(h, vs, t > 1);
+                        if (more) issue_s(h, ad, ks);
+                        else if (t >= 0) mma_commit(pvdone0 + 8u * h);
                     }
                 }
             }
@@ -1153,6 +1162,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if constexpr (!SEL) {
                         bool bad = false;
                         if (some) {
+#pragma unroll 2
                             for (int e = 0; e < 8 * C::kBlocks; ++e) {
                                 const uint4 w = *reinterpret_cast<const uint4*>(
                                     vt + (e >> 3) * C::kBlockBytes + row * 128 + (((e + row) & 7) << 4));
@@ -1175,6 +1185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             // may see (P as the tensor core would read it)
                             if (active) {
                                 const int lo = row_lo - key0, hi = row_hi - key0;
+#pragma unroll 1
                                 for (int d = 0; d < D; d += 8) {
                                     float acc[8];
                                     tmem_ld8(t_o + d, acc);
@@ -1182,6 +1193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                                         for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
                                     const uint8_t* col = vt + (d >> 6) * C::kBlockBytes;
+#pragma unroll 1
                                     for (int k = 0; k < 128; k += 2) {
                                         const float2 p = unpack16<FP16>(tmem_ld1(t_s + (k >> 1)));
 #pragma unroll
