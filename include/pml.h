@@ -395,7 +395,8 @@ int pml_noalloc_max_ctas(void);
  * inv_freq    [rot_dim/2] fp32, or fp64 (freq_64 != 0), radians per position
  *             (long-context scalings are choices of inv_freq and mscale);
  *             infinities, NaN and subnormals count as 0
- * rot_dim     even, 0 .. head_dim - rot_offset;  head_dim  1 .. 512
+ * rot_dim     even, 0 .. head_dim - rot_offset;  head_dim  1 .. 512;  at most
+ *             32768 heads
  */
 int pml_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, void* out,
              int64_t out_token_stride, int64_t out_head_stride, int dtype, const void* positions,

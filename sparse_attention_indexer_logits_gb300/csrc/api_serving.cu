@@ -13,6 +13,7 @@ namespace {
 using namespace pml;
 
 constexpr int kMaxRopeDim = 512;
+constexpr int kRopeMaxRows = 32768;    // of a token: the kernels divide by it in fp32
 
 int check_rotary(const void* positions, const void* inv_freq, int positions_64, int freq_64,
                  int rot_dim, int rot_offset, int head_dim)
@@ -63,14 +64,17 @@ int rope_vec(const RopeArgs& a)
     return 1;
 }
 
-// Tokens of a CTA: eight units a thread, at most eight tokens, and no more
-// than leaves four CTAs to each SM.
-int tokens_per_cta(int tokens, long long units_per_token, int sm_count)
+int turn_stride_of(int half) { return (half + 1) & ~1; }
+
+// Rows of a CTA that takes `side` at once: `units` times that, fewer if that
+// would leave SMs without work, and no more than lie in max_tokens tokens
+// wherever the first one begins.
+int cta_rows(int units, int side, long long rows_per_token, int max_tokens, long long tokens, int sm_count)
 {
-    long long t = (8 * 256 + units_per_token - 1) / (units_per_token > 0 ? units_per_token : 1);
-    if (t > 8) t = 8;
-    while (t > 1 && tokens / t < 4LL * sm_count) --t;
-    return t < 1 ? 1 : (int)t;
+    while (units > 1 && tokens * rows_per_token < (long long)units * side * 2 * sm_count) --units;
+    const long long most = (max_tokens - 1) * rows_per_token + 1;
+    const long long rows = (long long)units * side;
+    return (int)(rows < most ? rows : most);
 }
 
 int dtype_bytes(int dtype)
@@ -86,9 +90,17 @@ int rope_launch(RopeArgs& a, void* stream)
     if (e != cudaSuccess) return cuda_fail(e);
     a.slot.status = dev.status;
     a.vec = rope_vec(a);
-    const long long heads = a.q.heads + a.k.heads + a.v.heads;
-    const int per_unit = a.vec * (a.rot.interleaved && a.vec > 1 ? 1 : 2);
-    a.tokens_per_cta = tokens_per_cta(a.tokens, heads * a.dim / per_unit + 1, dev.sm_count);
+    // a row's units of two accesses: those that turn, then the rest
+    const int rot = 2 * a.rot.half;
+    const int turn = a.rot.interleaved && a.vec > 1 ? 0 : a.rot.half / a.vec;
+    const int rest = (turn ? a.dim - rot : a.dim) / a.vec;
+    int units = turn + (rest + 1) / 2;
+    if (a.paged && units < (a.dim / a.vec + 1) / 2) units = (a.dim / a.vec + 1) / 2;    // v's rows
+    while ((1 << a.row_lanes_log2) < units && a.row_lanes_log2 < 8) ++a.row_lanes_log2;
+    if ((1 << a.row_lanes_log2) < units) return PML_ERR_UNSUPPORTED;    // never: head_dim <= 512
+    a.turn_stride = turn_stride_of(a.rot.half);
+    a.rows_per_cta = cta_rows(kRopeUnits, kRopeThreads >> a.row_lanes_log2, a.q.heads + a.k.heads + a.v.heads,
+                              kRopeMaxTokens, a.tokens, dev.sm_count);
     e = launch_rope(a, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PML_OK : cuda_fail(e);
 }
@@ -235,7 +247,7 @@ int pml_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, void*
     const int elem = dtype_bytes(dtype);
     if (elem == 0 || head_dim > kMaxRopeDim) return PML_ERR_UNSUPPORTED;
     if (tokens == 0 || heads == 0) return PML_OK;
-    if ((long long)heads * head_dim > 0x7ffffffLL) return PML_ERR_UNSUPPORTED;
+    if (heads > kRopeMaxRows) return PML_ERR_UNSUPPORTED;
     if (!x || !out) return PML_ERR_INVALID_ARG;
     const int rc = check_rotary(positions, inv_freq, positions_64, freq_64, rot_dim, rot_offset, head_dim);
     if (rc != PML_OK) return rc;
@@ -268,7 +280,7 @@ int pml_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_stride
     const int elem = dtype_bytes(dtype);
     if (elem != 2 || head_dim > kMaxRopeDim) return PML_ERR_UNSUPPORTED;
     if (tokens == 0) return PML_OK;
-    if (((long long)num_heads + 2LL * kv_heads) * head_dim > 0x7ffffffLL) return PML_ERR_UNSUPPORTED;
+    if (num_heads + 2LL * kv_heads > kRopeMaxRows) return PML_ERR_UNSUPPORTED;
     if (!k || !v || !k_cache || !v_cache || !requests || !block_table) return PML_ERR_INVALID_ARG;
     if (num_heads > 0 && (!q || !q_out)) return PML_ERR_INVALID_ARG;
     if (num_pages < 1 || num_pages > 0x7fffffffLL || num_requests < 1) return PML_ERR_INVALID_ARG;
@@ -353,7 +365,8 @@ int pml_index_quant_append(const void* q, int64_t q_token_stride, int64_t q_head
     a.weight_scale = weight_scale;
     a.tokens = tokens;
     a.heads = num_heads;
-    a.tokens_per_cta = tokens_per_cta(tokens, (num_heads + 1) * 8LL, dev.sm_count);
+    a.rows_per_cta = cta_rows(kQuantRows, kQuantThreads / 8, num_heads + (k != nullptr ? 1 : 0), kQuantMaxTokens,
+                              tokens, dev.sm_count);
     e = launch_index_quant(a, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PML_OK : cuda_fail(e);
 }

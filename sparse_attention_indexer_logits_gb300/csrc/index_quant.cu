@@ -9,15 +9,18 @@
 //
 // Bound by memory: 256 bytes in, 128 out per row.  Eight lanes hold a row,
 // sixteen elements each, arranged so that both elements of a pair lie in one
-// lane; the row's maximum takes three shuffles.  The maximum is taken over
-// the values' bits, which orders infinities above all numbers and NaNs above
-// those, so a row with a NaN gets a NaN scale instead of a silent one.  The
-// quotient is a product with 448 / max: one rounding more than a division
-// (2^-24 against the code's 2^-4), a tenth of its instructions.
+// lane, and up to four rows a lane; a CTA takes that many rows of the
+// flattened (token, head) list, a token's key after its heads, loads them
+// all, computes its tokens' angles while they are on their way, and works.
+// A row's maximum takes three shuffles; it keeps a NaN, so a row with one
+// gets a NaN scale instead of a silent one.  The quotient is a product with
+// 448 / max, one rounding more than a division (2^-23 against the code's
+// 2^-4) and a tenth of its instructions.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "dependent.cuh"
 #include "rotary.cuh"
 #include "serving.h"
 
@@ -25,7 +28,7 @@ namespace pml {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = kQuantThreads;
 constexpr int kRowLanes = 8;                       // lanes of a row
 constexpr int kRows = kThreads / kRowLanes;        // rows of a CTA's step
 
@@ -55,17 +58,79 @@ __device__ __forceinline__ uint2 pack_e4m3(const float (&x)[8], float inv)
     return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
-template <bool INTER>
-__global__ void __launch_bounds__(kThreads) index_quant_kernel(const IndexQuantArgs a)
+__device__ __forceinline__ float max_nan(float a, float b)
 {
-    extern __shared__ float2 cs[];
-    __shared__ long long page_of[8];
-    __shared__ int slot_of[8];
-    __shared__ int state_of[8];    // 0 padding, 1 q only, 2 q and key
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 
-    const long long token0 = (long long)blockIdx.x * a.tokens_per_cta;
-    const int nt = (int)min((long long)a.tokens_per_cta, (long long)a.tokens - token0);
+template <bool INTER>
+__global__ void __launch_bounds__(kThreads, 3) index_quant_kernel(const IndexQuantArgs a)
+{
+    extern __shared__ __align__(16) float2 cs[];
+    __shared__ long long page_of[kQuantMaxTokens];
+    __shared__ int slot_of[kQuantMaxTokens];
+    __shared__ int state_of[kQuantMaxTokens];    // 0 padding, 1 q only, 2 q and key
+
+    allow_dependent_launch();
+    grid_dependency_wait();
     const int half = a.rot.half, off8 = a.rot.offset >> 3, half8 = half >> 3;
+    const int rows = a.heads + (a.k != nullptr ? 1 : 0);          // of a token
+    const long long row0 = (long long)blockIdx.x * a.rows_per_cta;
+    const int count = (int)min((long long)a.rows_per_cta, (long long)a.tokens * rows - row0);
+    const long long token0 = row0 / rows;
+    const int first = (int)(row0 - token0 * rows);
+    const int nt = (first + count - 1) / rows + 1;
+    const float per_row = 1.0f / (float)rows;
+
+    const int lane = threadIdx.x & (kRowLanes - 1);
+    const unsigned mask = 0xffu << (threadIdx.x & 24);
+    // the two 8-element chunks of this lane: the halves of eight pairs, or
+    // two chunks outside the rotated part, or (interleaved) two neighbours
+    int c0 = 2 * lane, c1 = 2 * lane + 1;
+    // which of the chunks turn, and their first pairs
+    bool turn0 = false, turn1 = false;
+    int pair0 = 0, pair1 = 0;
+    if constexpr (INTER) {
+        turn0 = c0 >= off8 && c0 < off8 + 2 * half8;
+        turn1 = c1 >= off8 && c1 < off8 + 2 * half8;
+        pair0 = turn0 ? 4 * (c0 - off8) : 0;
+        pair1 = turn1 ? 4 * (c1 - off8) : 0;
+    } else if (lane < half8) {
+        c0 = off8 + lane;
+        c1 = c0 + half8;
+        turn0 = true;
+        pair0 = 8 * lane;
+        pair1 = pair0 + 4;
+    } else {
+        c0 = 2 * (lane - half8);
+        c1 = c0 + 1;
+        if (c0 >= off8) c0 += 2 * half8;
+        if (c1 >= off8) c1 += 2 * half8;
+    }
+    // token of the CTA and row of the token, of this group's row b
+    auto place = [&](int b, int& t, int& r) {
+        const int i = (int)threadIdx.x / kRowLanes + b * kRows;
+        r = first + i;
+        t = (int)(((float)r + 0.5f) * per_row);      // r / rows: r is below 2^16
+        r -= t * rows;
+        return i < count;
+    };
+    uint4 v0[kQuantRows], v1[kQuantRows];
+    float weight[kQuantRows];
+#pragma unroll
+    for (int b = 0; b < kQuantRows; ++b) {
+        int t, h;
+        if (!place(b, t, h)) continue;
+        const long long tok = token0 + t;
+        const __nv_bfloat16* src =
+            h == a.heads ? static_cast<const __nv_bfloat16*>(a.k) + tok * a.k_token
+                         : static_cast<const __nv_bfloat16*>(a.q) + tok * a.q_token + h * a.q_head;
+        v0[b] = __ldg(reinterpret_cast<const uint4*>(src) + c0);
+        v1[b] = __ldg(reinterpret_cast<const uint4*>(src) + c1);
+        weight[b] = lane == 0 && h < a.heads ? __ldg(a.weights + tok * a.heads + h) : 0.0f;
+    }
 
     fill_turns(a.rot, cs, token0, nt);
     if ((int)threadIdx.x < nt) {
@@ -82,80 +147,56 @@ __global__ void __launch_bounds__(kThreads) index_quant_kernel(const IndexQuantA
     }
     __syncthreads();
 
-    const int lane = threadIdx.x & (kRowLanes - 1);
-    const unsigned mask = 0xffu << (threadIdx.x & 24);
-    // the two 8-element chunks of this lane: the halves of eight pairs, or
-    // two chunks outside the rotated part, or (interleaved) two neighbours
-    int c0 = 2 * lane, c1 = 2 * lane + 1;
-    bool turned_pair = false;
-    if constexpr (!INTER) {
-        if (lane < half8) {
-            c0 = off8 + lane;
-            c1 = c0 + half8;
-            turned_pair = true;
-        } else {
-            c0 = 2 * (lane - half8);
-            c1 = c0 + 1;
-            if (c0 >= off8) c0 += 2 * half8;
-            if (c1 >= off8) c1 += 2 * half8;
-        }
-    }
-    const int rows_per_token = a.heads + (a.k != nullptr ? 1 : 0);
-    for (int r = (int)threadIdx.x / kRowLanes; r < nt * rows_per_token; r += kRows) {
-        const int t = r / rows_per_token;
-        const int h = r - t * rows_per_token;
+#pragma unroll
+    for (int b = 0; b < kQuantRows; ++b) {
+        int t, h;
+        if (!place(b, t, h)) continue;                 // (eight lanes together)
         const bool is_k = h == a.heads;
-        const int st = state_of[t];
-        if (st == 0 || (is_k && st == 1)) continue;     // whole rows together
-        const long long tok = token0 + t;
-        const __nv_bfloat16* src =
-            is_k ? static_cast<const __nv_bfloat16*>(a.k) + tok * a.k_token
-                 : static_cast<const __nv_bfloat16*>(a.q) + tok * a.q_token + h * a.q_head;
-        const uint4 v0 = __ldg(reinterpret_cast<const uint4*>(src) + c0);
-        const uint4 v1 = __ldg(reinterpret_cast<const uint4*>(src) + c1);
+        if (state_of[t] < (is_k ? 2 : 1)) continue;
         float x[8], y[8];
-        unpack8(v0, x);
-        unpack8(v1, y);
-        const float2* c = cs + t * half;
+        unpack8(v0[b], x);
+        unpack8(v1[b], y);
+        const float2* c = cs + t * turn_stride(half);
         if constexpr (INTER) {
+            if (turn0) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int ch = (b == 0 ? c0 : c1) - off8;
-                if (ch >= 0 && ch < 2 * half8) {
-                    float(&z)[8] = b == 0 ? x : y;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 w = c[4 * ch + e];
-                        const float p = z[2 * e], q = z[2 * e + 1];
-                        z[2 * e] = p * w.x - q * w.y;
-                        z[2 * e + 1] = q * w.x + p * w.y;
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const float2 w = c[pair0 + e];
+                    const float p = x[2 * e], q = x[2 * e + 1];
+                    x[2 * e] = p * w.x - q * w.y;
+                    x[2 * e + 1] = q * w.x + p * w.y;
                 }
             }
-        } else if (turned_pair) {
+            if (turn1) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float2 w = c[8 * lane + e];
-                const float p = x[e], q = y[e];
+                for (int e = 0; e < 4; ++e) {
+                    const float2 w = c[pair1 + e];
+                    const float p = y[2 * e], q = y[2 * e + 1];
+                    y[2 * e] = p * w.x - q * w.y;
+                    y[2 * e + 1] = q * w.x + p * w.y;
+                }
+            }
+        } else if (turn0) {
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                const float4 w = *reinterpret_cast<const float4*>(c + pair0 + e);
+                const float p = x[e], q = y[e], r = x[e + 1], s = y[e + 1];
                 x[e] = p * w.x - q * w.y;
                 y[e] = q * w.x + p * w.y;
+                x[e + 1] = r * w.z - s * w.w;
+                y[e + 1] = s * w.z + r * w.w;
             }
         }
-        uint32_t top = 0;
+        float amax = 1e-12f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
-            top = max(top, __float_as_uint(y[e]) & 0x7fffffffu);
-        }
+        for (int e = 0; e < 8; ++e) amax = max_nan(amax, max_nan(fabsf(x[e]), fabsf(y[e])));
 #pragma unroll
-        for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(mask, top, o));
-        // as bits: a NaN maximum stays one
-        const float amax = __uint_as_float(max(top, __float_as_uint(1e-12f)));
-        const float scale = amax / 448.0f;
-        const float inv = 448.0f / amax;
+        for (int o = 4; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(mask, amax, o));
+        const float inv = __fdividef(448.0f, amax);
+        const float scale = amax * (1.0f / 448.0f);
         const uint2 p0 = pack_e4m3(x, inv), p1 = pack_e4m3(y, inv);
         uint8_t* dst = is_k ? a.kv_fused + page_of[t] * kFp8BlockBytes + slot_of[t] * kHeadDim
-                            : a.q_out + (tok * a.heads + h) * kHeadDim;
+                            : a.q_out + ((token0 + t) * a.heads + h) * kHeadDim;
         if constexpr (INTER) {
             reinterpret_cast<uint4*>(dst)[lane] = make_uint4(p0.x, p0.y, p1.x, p1.y);
         } else {
@@ -167,8 +208,7 @@ __global__ void __launch_bounds__(kThreads) index_quant_kernel(const IndexQuantA
                 reinterpret_cast<float*>(a.kv_fused + page_of[t] * kFp8BlockBytes +
                                          kFp8BlockKeyBytes)[slot_of[t]] = scale;
             else
-                a.w_out[tok * a.heads + h] =
-                    __ldg(a.weights + tok * a.heads + h) * scale * a.weight_scale;
+                a.w_out[(token0 + t) * a.heads + h] = weight[b] * scale * a.weight_scale;
         }
     }
 }
@@ -177,11 +217,12 @@ __global__ void __launch_bounds__(kThreads) index_quant_kernel(const IndexQuantA
 
 cudaError_t launch_index_quant(const IndexQuantArgs& a, cudaStream_t stream)
 {
-    const unsigned grid = (unsigned)((a.tokens + a.tokens_per_cta - 1) / a.tokens_per_cta);
-    const size_t smem = (size_t)a.tokens_per_cta * a.rot.half * sizeof(float2);
-    if (a.rot.interleaved) index_quant_kernel<true><<<grid, kThreads, smem, stream>>>(a);
-    else index_quant_kernel<false><<<grid, kThreads, smem, stream>>>(a);
-    return cudaGetLastError();
+    const long long rows = (long long)a.tokens * (a.heads + (a.k != nullptr ? 1 : 0));
+    const unsigned grid = (unsigned)((rows + a.rows_per_cta - 1) / a.rows_per_cta);
+    const size_t smem = (size_t)kQuantMaxTokens * turn_stride(a.rot.half) * sizeof(float2);
+    return a.rot.interleaved
+               ? launch_dependent(index_quant_kernel<true>, dim3(grid), kThreads, smem, stream, a)
+               : launch_dependent(index_quant_kernel<false>, dim3(grid), kThreads, smem, stream, a);
 }
 
 }  // namespace pml

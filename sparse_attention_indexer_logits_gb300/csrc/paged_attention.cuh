@@ -49,6 +49,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "dependent.cuh"
 #include "ptx.cuh"
 #include "serving.h"
 
@@ -1328,26 +1329,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
-}
-
-// A launch that may begin while the kernel before it in the stream ends (both
-// kernels wait in grid_dependency_wait before they touch memory).
-template <class K, class... Args>
-cudaError_t launch_dependent(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream,
-                             const Args&... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int D, bool FP16, bool SEL>

@@ -9,16 +9,22 @@
 // the key cache and copies v into those of the value cache.
 //
 // Bound by memory: every element is read once and written once, about three
-// operations each.  A CTA takes a few tokens: their cosines and sines are
-// computed once into shared memory (an angle serves every head), then the
-// threads walk the tokens' (head, unit) pairs, a unit being one 16-byte
-// access that holds whole pairs, or two accesses that hold the two halves of
-// eight (four in fp32) pairs.  Narrower accesses serve sizes and strides that
-// 16 bytes do not divide.
+// operations each.  A row (one head of one token) is cut into units of two
+// 16-byte accesses: the two halves of eight (four in fp32) pairs, two
+// neighbours of whole pairs, or two that only pass through.  A power of two
+// of neighbouring threads takes a row, a thread a unit of up to four rows, and
+// a CTA that many rows of the flattened (token, head) list: it loads all it
+// will ever load, computes its tokens' cosines and sines into shared memory
+// while that is on its way (an angle serves every head), turns and stores.
+// Sixteen-bit values are unpacked and packed two to a word: converted one by
+// one they take a quarter-rate instruction each, and the kernel's time was
+// its instructions'.  Narrower accesses serve sizes and strides that 16 bytes
+// do not divide.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "dependent.cuh"
 #include "rotary.cuh"
 #include "serving.h"
 
@@ -26,7 +32,7 @@ namespace pml {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = kRopeThreads;
 
 template <int BYTES>
 struct Raw;
@@ -48,19 +54,12 @@ template <typename T, int VEC>
 union Vec {
     typename Raw<VEC * sizeof(T)>::type raw;
     T e[VEC];
+    uint32_t w[(VEC * sizeof(T) + 3) / 4];
     __device__ Vec() {}
 };
 
 template <typename T, int VEC>
 __device__ __forceinline__ void load_vec(Vec<T, VEC>& v, const T* p)
-{
-    using R = typename Raw<VEC * sizeof(T)>::type;
-    v.raw = __ldg(reinterpret_cast<const R*>(p));
-}
-// in place the other threads' stores may share this launch's memory: no
-// read-only path
-template <typename T, int VEC>
-__device__ __forceinline__ void load_vec_rw(Vec<T, VEC>& v, const T* p)
 {
     using R = typename Raw<VEC * sizeof(T)>::type;
     v.raw = *reinterpret_cast<const R*>(p);
@@ -72,20 +71,148 @@ __device__ __forceinline__ void store_vec(T* p, const Vec<T, VEC>& v)
     *reinterpret_cast<R*>(p) = v.raw;
 }
 
-// MODE 0: pairs in two halves, VEC pairs per unit; 1: interleaved pairs, VEC
-// elements (VEC / 2 pairs) per unit; 2: interleaved pairs read element by
-// element (VEC 1).
-template <typename T, int VEC, int MODE, bool PAGED>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a)
+// Two neighbouring 16-bit values of a word.
+__device__ __forceinline__ float2 unpack(uint32_t w, __half)
 {
-    extern __shared__ float2 cs[];
-    __shared__ long long page_of[8];
-    __shared__ int slot_of[8];
-    __shared__ int state_of[8];    // 0 padding, 1 q only, 2 q, k and v
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+__device__ __forceinline__ float2 unpack(uint32_t w, __nv_bfloat16)
+{
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t pack(float lo, float hi, __half)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack(float lo, float hi, __nv_bfloat16)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 
-    const long long token0 = (long long)blockIdx.x * a.tokens_per_cta;
-    const int nt = (int)min((long long)a.tokens_per_cta, (long long)a.tokens - token0);
+// (p, q) turned by the angle of c = (cosine, sine)
+__device__ __forceinline__ float2 turn(float p, float q, float cosine, float sine)
+{
+    return make_float2(p * cosine - q * sine, q * cosine + p * sine);
+}
+
+// Pair i is (x[i], y[i]), its angle c[i].
+template <typename T, int VEC>
+__device__ __forceinline__ void turn_across(Vec<T, VEC>& x, Vec<T, VEC>& y, const float2* c)
+{
+    if constexpr (sizeof(T) == 2 && VEC >= 2) {
+#pragma unroll
+        for (int k = 0; k < VEC / 2; ++k) {
+            const float2 a = unpack(x.w[k], T()), b = unpack(y.w[k], T());
+            const float4 cc = *reinterpret_cast<const float4*>(c + 2 * k);
+            const float2 u = turn(a.x, b.x, cc.x, cc.y), v = turn(a.y, b.y, cc.z, cc.w);
+            x.w[k] = pack(u.x, v.x, T());
+            y.w[k] = pack(u.y, v.y, T());
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+            const float2 u = turn(to_float(x.e[k]), to_float(y.e[k]), c[k].x, c[k].y);
+            x.e[k] = from_float<T>(u.x);
+            y.e[k] = from_float<T>(u.y);
+        }
+    }
+}
+
+// Pair i is (v[2i], v[2i + 1]).
+template <typename T, int VEC>
+__device__ __forceinline__ void turn_along(Vec<T, VEC>& v, const float2* c)
+{
+#pragma unroll
+    for (int k = 0; k < VEC / 2; ++k) {
+        if constexpr (sizeof(T) == 2) {
+            const float2 a = unpack(v.w[k], T());
+            const float2 u = turn(a.x, a.y, c[k].x, c[k].y);
+            v.w[k] = pack(u.x, u.y, T());
+        } else {
+            const float2 u = turn(v.e[2 * k], v.e[2 * k + 1], c[k].x, c[k].y);
+            v.e[2 * k] = u.x;
+            v.e[2 * k + 1] = u.y;
+        }
+    }
+}
+
+// MODE 0: pairs in two halves, VEC pairs per unit; 1: interleaved pairs, two
+// neighbouring accesses per unit; 2: interleaved pairs, two elements per unit
+// (VEC 1).
+template <typename T, int VEC, int MODE, bool PAGED>
+__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs a)
+{
+    extern __shared__ __align__(16) float2 cs[];
+    __shared__ long long page_of[kRopeMaxTokens];
+    __shared__ int slot_of[kRopeMaxTokens];
+    __shared__ int state_of[kRopeMaxTokens];    // 0 padding, 1 q only, 2 q, k and v
+
+    allow_dependent_launch();
+    grid_dependency_wait();
     const int half = a.rot.half, rot = 2 * half, off = a.rot.offset;
+    const int rows = a.q.heads + (PAGED ? a.k.heads + a.v.heads : 0);    // of a token
+    // the CTA's rows of all tokens' rows, and its tokens
+    const long long row0 = (long long)blockIdx.x * a.rows_per_cta;
+    const int count = (int)min((long long)a.rows_per_cta, (long long)a.tokens * rows - row0);
+    const long long token0 = row0 / rows;
+    const int first = (int)(row0 - token0 * rows);         // row of the first token
+    const int nt = (first + count - 1) / rows + 1;
+    const int u = threadIdx.x & ((1 << a.row_lanes_log2) - 1);
+    const int rows_step = kThreads >> a.row_lanes_log2;
+    const float per_row = 1.0f / (float)rows;
+
+    // this thread's unit: two accesses of a row, at e0 and e1 (< 0: none); of
+    // a row that turns, and of one that does not (v)
+    const int turn_units = MODE != 1 ? half / VEC : 0;
+    const bool turns = u < turn_units;
+    int e0, e1, v0 = -1, v1 = -1;
+    if (turns) {
+        e0 = MODE == 2 ? off + 2 * u : off + u * VEC;
+        e1 = MODE == 2 ? e0 + 1 : e0 + half;
+    } else {
+        const int k = 2 * (u - turn_units), rest = (a.dim - (MODE == 1 ? 0 : rot)) / VEC;
+        e0 = k < rest ? k * VEC : -1;
+        e1 = k + 1 < rest ? (k + 1) * VEC : -1;
+        if (MODE != 1) {
+            if (e0 >= off) e0 += rot;
+            if (e1 >= off) e1 += rot;
+        }
+    }
+    if constexpr (PAGED) {
+        if (2 * u < a.dim / VEC) v0 = 2 * u * VEC;
+        if (2 * u + 1 < a.dim / VEC) v1 = (2 * u + 1) * VEC;
+    }
+    // (MODE 1) an access turns if it lies in the rotated part
+    const bool in0 = MODE == 1 && e0 >= off && e0 < off + rot;
+    const bool in1 = MODE == 1 && e1 >= off && e1 < off + rot;
+    // q in place: what does not turn stays
+    const int q0 = a.skip_rest && !turns && !in0 ? -1 : e0, q1 = a.skip_rest && !turns && !in1 ? -1 : e1;
+
+    Vec<T, VEC> x[kRopeUnits], y[kRopeUnits];
+    // token of the CTA and row of the token, of unit b
+    auto place = [&](int b, int& t, int& r) {
+        const int i = (int)(threadIdx.x >> a.row_lanes_log2) + b * rows_step;
+        r = first + i;
+        t = (int)(((float)r + 0.5f) * per_row);      // r / rows: r is below 2^16
+        r -= t * rows;
+        return i < count;
+    };
+#pragma unroll
+    for (int b = 0; b < kRopeUnits; ++b) {
+        int t, r;
+        if (!place(b, t, r)) continue;
+        const bool is_q = !PAGED || r < a.q.heads, is_v = PAGED && r >= a.q.heads + a.k.heads;
+        const RopeRows& set = is_q ? a.q : is_v ? a.v : a.k;
+        const int head = is_q ? r : is_v ? r - a.q.heads - a.k.heads : r - a.q.heads;
+        const T* src = static_cast<const T*>(set.src) + (token0 + t) * set.src_token + head * set.src_head;
+        const int f0 = is_q ? q0 : is_v ? v0 : e0, f1 = is_q ? q1 : is_v ? v1 : e1;
+        if (f0 >= 0) load_vec(x[b], src + f0);
+        if (f1 >= 0) load_vec(y[b], src + f1);
+    }
 
     fill_turns(a.rot, cs, token0, nt);
     if constexpr (PAGED) {
@@ -103,96 +230,43 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a)
     }
     __syncthreads();
 
-    // units of a rotated row, and those that only pass through
-    const int turn_units = MODE == 1 ? rot / VEC : half / VEC;
-    const int rest_units = a.skip_rest ? 0 : (a.dim - rot) / VEC;
-    const int q_row = turn_units + rest_units;
-    const int k_row = turn_units + (a.dim - rot) / VEC;
-    const int v_row = a.dim / VEC;
-    const int q_units = a.q.heads * q_row;
-    const int k_units = PAGED ? a.k.heads * k_row : 0;
-    const int units = q_units + k_units + (PAGED ? a.v.heads * v_row : 0);
-
-    for (int i = threadIdx.x; i < nt * units; i += kThreads) {
-        const int t = i / units;
-        int u = i - t * units;
-        const T* src;
-        T* dst;
-        bool rotated = true;
+#pragma unroll
+    for (int b = 0; b < kRopeUnits; ++b) {
+        int t, r;
+        if (!place(b, t, r)) continue;
+        const bool is_q = !PAGED || r < a.q.heads, is_v = PAGED && r >= a.q.heads + a.k.heads;
+        const RopeRows& set = is_q ? a.q : is_v ? a.v : a.k;
+        const int head = is_q ? r : is_v ? r - a.q.heads - a.k.heads : r - a.q.heads;
+        T* dst = static_cast<T*>(set.dst) + head * set.dst_head;
         if constexpr (PAGED) {
-            const int st = state_of[t];
-            if (st == 0 || (st == 1 && u >= q_units)) continue;
-        }
-        if (!PAGED || u < q_units) {
-            const int h = u / q_row;
-            u -= h * q_row;
-            src = static_cast<const T*>(a.q.src) + (token0 + t) * a.q.src_token + h * a.q.src_head;
-            dst = static_cast<T*>(a.q.dst) + (token0 + t) * a.q.dst_token + h * a.q.dst_head;
+            if (state_of[t] < (is_q ? 1 : 2)) continue;
+            dst += is_q ? (token0 + t) * set.dst_token : page_of[t] * set.dst_page + slot_of[t] * set.dst_token;
         } else {
-            const bool is_k = u < q_units + k_units;
-            u -= is_k ? q_units : q_units + k_units;
-            const int row = is_k ? k_row : v_row;
-            const RopeRows& r = is_k ? a.k : a.v;
-            const int h = u / row;
-            u -= h * row;
-            rotated = is_k;
-            src = static_cast<const T*>(r.src) + (token0 + t) * r.src_token + h * r.src_head;
-            dst = static_cast<T*>(r.dst) + page_of[t] * r.dst_page + slot_of[t] * r.dst_token +
-                  h * r.dst_head;
+            dst += (token0 + t) * set.dst_token;
         }
-        if (rotated && u < turn_units) {
-            const float2* c = cs + t * half;
-            if constexpr (MODE == 0) {
-                const int j = u * VEC;
-                Vec<T, VEC> x, y;
-                load_vec_rw(x, src + off + j);
-                load_vec_rw(y, src + off + half + j);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float2 w = c[j + e];
-                    const float p = to_float(x.e[e]), q = to_float(y.e[e]);
-                    x.e[e] = from_float<T>(p * w.x - q * w.y);
-                    y.e[e] = from_float<T>(q * w.x + p * w.y);
-                }
-                store_vec(dst + off + j, x);
-                store_vec(dst + off + half + j, y);
-            } else if constexpr (MODE == 1) {
-                const int j = u * VEC;
-                Vec<T, VEC> x;
-                load_vec_rw(x, src + off + j);
-#pragma unroll
-                for (int e = 0; e < VEC; e += 2) {
-                    const float2 w = c[(j + e) >> 1];
-                    const float p = to_float(x.e[e]), q = to_float(x.e[e + 1]);
-                    x.e[e] = from_float<T>(p * w.x - q * w.y);
-                    x.e[e + 1] = from_float<T>(q * w.x + p * w.y);
-                }
-                store_vec(dst + off + j, x);
+        const int f0 = is_q ? q0 : is_v ? v0 : e0, f1 = is_q ? q1 : is_v ? v1 : e1;
+        if (!is_v) {
+            const float2* c = cs + t * a.turn_stride;
+            if constexpr (MODE == 1) {
+                if (in0) turn_along(x[b], c + ((e0 - off) >> 1));
+                if (in1) turn_along(y[b], c + ((e1 - off) >> 1));
             } else {
-                const float2 w = c[u];
-                const float p = to_float(src[off + 2 * u]), q = to_float(src[off + 2 * u + 1]);
-                dst[off + 2 * u] = from_float<T>(p * w.x - q * w.y);
-                dst[off + 2 * u + 1] = from_float<T>(q * w.x + p * w.y);
+                if (turns) turn_across(x[b], y[b], c + u * VEC);
             }
-        } else {
-            // an element outside the rotated part, or of v
-            int e = rotated ? (u - turn_units) * VEC : u * VEC;
-            if (rotated && e >= off) e += rot;
-            Vec<T, VEC> x;
-            load_vec_rw(x, src + e);
-            store_vec(dst + e, x);
         }
+        if (f0 >= 0) store_vec(dst + f0, x[b]);
+        if (f1 >= 0) store_vec(dst + f1, y[b]);
     }
 }
 
 template <typename T, int VEC, int MODE>
 cudaError_t launch_mode(const RopeArgs& a, cudaStream_t stream)
 {
-    const unsigned grid = (unsigned)((a.tokens + a.tokens_per_cta - 1) / a.tokens_per_cta);
-    const size_t smem = (size_t)a.tokens_per_cta * a.rot.half * sizeof(float2);
-    if (a.paged) rope_kernel<T, VEC, MODE, true><<<grid, kThreads, smem, stream>>>(a);
-    else rope_kernel<T, VEC, MODE, false><<<grid, kThreads, smem, stream>>>(a);
-    return cudaGetLastError();
+    const long long rows = (long long)a.tokens * (a.q.heads + a.k.heads + a.v.heads);
+    const dim3 grid((unsigned)((rows + a.rows_per_cta - 1) / a.rows_per_cta));
+    const size_t smem = (size_t)kRopeMaxTokens * a.turn_stride * sizeof(float2);
+    return a.paged ? launch_dependent(rope_kernel<T, VEC, MODE, true>, grid, kThreads, smem, stream, a)
+                   : launch_dependent(rope_kernel<T, VEC, MODE, false>, grid, kThreads, smem, stream, a);
 }
 
 template <typename T>

@@ -66,7 +66,12 @@ __device__ __forceinline__ float2 turned(uint64_t step, long long position, floa
     return make_float2(c * mscale, s * mscale * sign);
 }
 
-// Fills cs[t * half + j] for the CTA's tokens; every thread of the CTA calls.
+// Values of a token in the table below: an even number, so that two of them
+// can be read at once.
+__host__ __device__ __forceinline__ int turn_stride(int half) { return (half + 1) & ~1; }
+
+// Fills cs[t * turn_stride(half) + j] for the CTA's tokens; every thread of
+// the CTA calls.
 __device__ __forceinline__ void fill_turns(const RotaryArgs& r, float2* cs, long long token0,
                                            int tokens)
 {
@@ -79,7 +84,7 @@ __device__ __forceinline__ void fill_turns(const RotaryArgs& r, float2* cs, long
         for (int j = (int)threadIdx.x - g * half; j < half; j += blockDim.x) {
             const uint64_t step = load_step(r, j);
             for (int t = g; t < tokens; t += lanes)
-                cs[t * half + j] = turned(step, load_position(r, token0 + t), r.mscale, r.sign);
+                cs[t * turn_stride(half) + j] = turned(step, load_position(r, token0 + t), r.mscale, r.sign);
         }
     }
 }

@@ -55,8 +55,14 @@ struct RopeArgs {
     int elem;                      // bytes of an element: 2 or 4
     int fp16;                      // 2-byte elements: 1 fp16, 0 bf16
     int vec;                       // elements per access: a power of two up to 16 bytes
-    int tokens_per_cta;
+    int rows_per_cta;
+    int row_lanes_log2;            // threads of a row: a power of two, at most 256
+    int turn_stride;
 };
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeUnits = 4;      // rows of a thread
+constexpr int kRopeMaxTokens = 8;  // of a CTA, in part
 
 // The indexer's inputs: q rows [tokens][heads][128] and key rows [tokens][128].
 struct IndexQuantArgs {
@@ -73,8 +79,12 @@ struct IndexQuantArgs {
     float weight_scale;
     int tokens;
     int heads;
-    int tokens_per_cta;
+    int rows_per_cta;              // of the tokens' heads + 1 rows each (no keys: heads)
 };
+
+constexpr int kQuantThreads = 256;
+constexpr int kQuantRows = 4;      // rows of a group of eight lanes
+constexpr int kQuantMaxTokens = 8; // of a CTA, in part
 
 // A pool of pages: ref_counts[page] requests hold the page (0: free), and the
 // first ceil(seq_lens[row] / 64) entries of a row's block table are its pages.
