@@ -64,8 +64,6 @@ int rope_vec(const RopeArgs& a)
     return 1;
 }
 
-int turn_stride_of(int half) { return (half + 1) & ~1; }
-
 // Rows of a CTA that takes `side` at once: `units` times that, fewer if that
 // would leave SMs without work, and no more than lie in max_tokens tokens
 // wherever the first one begins.
@@ -98,7 +96,6 @@ int rope_launch(RopeArgs& a, void* stream)
     if (a.paged && units < (a.dim / a.vec + 1) / 2) units = (a.dim / a.vec + 1) / 2;    // v's rows
     while ((1 << a.row_lanes_log2) < units && a.row_lanes_log2 < 8) ++a.row_lanes_log2;
     if ((1 << a.row_lanes_log2) < units) return PML_ERR_UNSUPPORTED;    // never: head_dim <= 512
-    a.turn_stride = turn_stride_of(a.rot.half);
     a.rows_per_cta = cta_rows(kRopeUnits, kRopeThreads >> a.row_lanes_log2, a.q.heads + a.k.heads + a.v.heads,
                               kRopeMaxTokens, a.tokens, dev.sm_count);
     e = launch_rope(a, static_cast<cudaStream_t>(stream));

@@ -89,20 +89,15 @@ __global__ void __launch_bounds__(kThreads, 3) index_quant_kernel(const IndexQua
     // the two 8-element chunks of this lane: the halves of eight pairs, or
     // two chunks outside the rotated part, or (interleaved) two neighbours
     int c0 = 2 * lane, c1 = 2 * lane + 1;
-    // which of the chunks turn, and their first pairs
+    // which of the chunks turn
     bool turn0 = false, turn1 = false;
-    int pair0 = 0, pair1 = 0;
     if constexpr (INTER) {
         turn0 = c0 >= off8 && c0 < off8 + 2 * half8;
         turn1 = c1 >= off8 && c1 < off8 + 2 * half8;
-        pair0 = turn0 ? 4 * (c0 - off8) : 0;
-        pair1 = turn1 ? 4 * (c1 - off8) : 0;
     } else if (lane < half8) {
         c0 = off8 + lane;
         c1 = c0 + half8;
         turn0 = true;
-        pair0 = 8 * lane;
-        pair1 = pair0 + 4;
     } else {
         c0 = 2 * (lane - half8);
         c1 = c0 + 1;
@@ -132,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, 3) index_quant_kernel(const IndexQua
         weight[b] = lane == 0 && h < a.heads ? __ldg(a.weights + tok * a.heads + h) : 0.0f;
     }
 
-    fill_turns(a.rot, cs, token0, nt);
+    fill_turns<INTER ? 4 : 8, INTER>(a.rot, cs, token0, nt);
     if ((int)threadIdx.x < nt) {
         const int t = threadIdx.x;
         bool pad = false;
@@ -157,35 +152,29 @@ __global__ void __launch_bounds__(kThreads, 3) index_quant_kernel(const IndexQua
         unpack8(v0[b], x);
         unpack8(v1[b], y);
         const float2* c = cs + t * turn_stride(half);
+        // two pairs' angles at a time
+        auto turn2 = [](float& p0, float& q0, float& p1, float& q1, float4 w) {
+            const float a0 = p0, b0 = q0, a1 = p1, b1 = q1;
+            p0 = a0 * w.x - b0 * w.y;
+            q0 = b0 * w.x + a0 * w.y;
+            p1 = a1 * w.z - b1 * w.w;
+            q1 = b1 * w.z + a1 * w.w;
+        };
         if constexpr (INTER) {
-            if (turn0) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 w = c[pair0 + e];
-                    const float p = x[2 * e], q = x[2 * e + 1];
-                    x[2 * e] = p * w.x - q * w.y;
-                    x[2 * e + 1] = q * w.x + p * w.y;
-                }
-            }
-            if (turn1) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 w = c[pair1 + e];
-                    const float p = y[2 * e], q = y[2 * e + 1];
-                    y[2 * e] = p * w.x - q * w.y;
-                    y[2 * e + 1] = q * w.x + p * w.y;
-                }
+            for (int e = 0; e < 4; e += 2) {
+                if (turn0)
+                    turn2(x[2 * e], x[2 * e + 1], x[2 * e + 2], x[2 * e + 3],
+                          *reinterpret_cast<const float4*>(c + turn_place<4, true>(half, 4 * (c0 - off8) + e)));
+                if (turn1)
+                    turn2(y[2 * e], y[2 * e + 1], y[2 * e + 2], y[2 * e + 3],
+                          *reinterpret_cast<const float4*>(c + turn_place<4, true>(half, 4 * (c1 - off8) + e)));
             }
         } else if (turn0) {
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                const float4 w = *reinterpret_cast<const float4*>(c + pair0 + e);
-                const float p = x[e], q = y[e], r = x[e + 1], s = y[e + 1];
-                x[e] = p * w.x - q * w.y;
-                y[e] = q * w.x + p * w.y;
-                x[e + 1] = r * w.z - s * w.w;
-                y[e + 1] = s * w.z + r * w.w;
-            }
+            for (int e = 0; e < 8; e += 2)
+                turn2(x[e], y[e], x[e + 1], y[e + 1],
+                      *reinterpret_cast<const float4*>(c + turn_place<8, false>(half, 8 * lane + e)));
         }
         float amax = 1e-12f;
 #pragma unroll

@@ -99,43 +99,67 @@ __device__ __forceinline__ float2 turn(float p, float q, float cosine, float sin
     return make_float2(p * cosine - q * sine, q * cosine + p * sine);
 }
 
-// Pair i is (x[i], y[i]), its angle c[i].
+// Pair i is (x[i], y[i]); c: the token's angles, this unit's the u-th run.
 template <typename T, int VEC>
-__device__ __forceinline__ void turn_across(Vec<T, VEC>& x, Vec<T, VEC>& y, const float2* c)
+__device__ __forceinline__ void turn_across(Vec<T, VEC>& x, Vec<T, VEC>& y, const float2* c, int half, int u)
 {
-    if constexpr (sizeof(T) == 2 && VEC >= 2) {
-#pragma unroll
-        for (int k = 0; k < VEC / 2; ++k) {
-            const float2 a = unpack(x.w[k], T()), b = unpack(y.w[k], T());
-            const float4 cc = *reinterpret_cast<const float4*>(c + 2 * k);
-            const float2 u = turn(a.x, b.x, cc.x, cc.y), v = turn(a.y, b.y, cc.z, cc.w);
-            x.w[k] = pack(u.x, v.x, T());
-            y.w[k] = pack(u.y, v.y, T());
-        }
+    if constexpr (VEC == 1) {
+        const float2 v = turn(to_float(x.e[0]), to_float(y.e[0]), c[u].x, c[u].y);
+        x.e[0] = from_float<T>(v.x);
+        y.e[0] = from_float<T>(v.y);
     } else {
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-            const float2 u = turn(to_float(x.e[k]), to_float(y.e[k]), c[k].x, c[k].y);
-            x.e[k] = from_float<T>(u.x);
-            y.e[k] = from_float<T>(u.y);
+        for (int k = 0; k < VEC / 2; ++k) {
+            const float4 w = *reinterpret_cast<const float4*>(c + turn_place<VEC, false>(half, u * VEC + 2 * k));
+            if constexpr (sizeof(T) == 2) {
+                const float2 a = unpack(x.w[k], T()), b = unpack(y.w[k], T());
+                const float2 p = turn(a.x, b.x, w.x, w.y), q = turn(a.y, b.y, w.z, w.w);
+                x.w[k] = pack(p.x, q.x, T());
+                y.w[k] = pack(p.y, q.y, T());
+            } else {
+                const float2 p = turn(x.e[2 * k], y.e[2 * k], w.x, w.y);
+                const float2 q = turn(x.e[2 * k + 1], y.e[2 * k + 1], w.z, w.w);
+                x.e[2 * k] = p.x;
+                y.e[2 * k] = p.y;
+                x.e[2 * k + 1] = q.x;
+                y.e[2 * k + 1] = q.y;
+            }
         }
     }
 }
 
-// Pair i is (v[2i], v[2i + 1]).
+// Pair i is (v[2i], v[2i + 1]); its angles are the run-th run of the token's.
 template <typename T, int VEC>
-__device__ __forceinline__ void turn_along(Vec<T, VEC>& v, const float2* c)
+__device__ __forceinline__ void turn_along(Vec<T, VEC>& v, const float2* c, int half, int run)
 {
-#pragma unroll
-    for (int k = 0; k < VEC / 2; ++k) {
+    constexpr int kPairs = VEC / 2;
+    if constexpr (kPairs == 1) {
+        const float2 w = c[run];
         if constexpr (sizeof(T) == 2) {
-            const float2 a = unpack(v.w[k], T());
-            const float2 u = turn(a.x, a.y, c[k].x, c[k].y);
-            v.w[k] = pack(u.x, u.y, T());
+            const float2 a = unpack(v.w[0], T()), p = turn(a.x, a.y, w.x, w.y);
+            v.w[0] = pack(p.x, p.y, T());
         } else {
-            const float2 u = turn(v.e[2 * k], v.e[2 * k + 1], c[k].x, c[k].y);
-            v.e[2 * k] = u.x;
-            v.e[2 * k + 1] = u.y;
+            const float2 p = turn(v.e[0], v.e[1], w.x, w.y);
+            v.e[0] = p.x;
+            v.e[1] = p.y;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kPairs; k += 2) {
+            const float4 w = *reinterpret_cast<const float4*>(c + turn_place<kPairs, true>(half, run * kPairs + k));
+            if constexpr (sizeof(T) == 2) {
+                const float2 a = unpack(v.w[k], T()), b = unpack(v.w[k + 1], T());
+                const float2 p = turn(a.x, a.y, w.x, w.y), q = turn(b.x, b.y, w.z, w.w);
+                v.w[k] = pack(p.x, p.y, T());
+                v.w[k + 1] = pack(q.x, q.y, T());
+            } else {
+                const float2 p = turn(v.e[2 * k], v.e[2 * k + 1], w.x, w.y);
+                const float2 q = turn(v.e[2 * k + 2], v.e[2 * k + 3], w.z, w.w);
+                v.e[2 * k] = p.x;
+                v.e[2 * k + 1] = p.y;
+                v.e[2 * k + 2] = q.x;
+                v.e[2 * k + 3] = q.y;
+            }
         }
     }
 }
@@ -214,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs a)
         if (f1 >= 0) load_vec(y[b], src + f1);
     }
 
-    fill_turns(a.rot, cs, token0, nt);
+    fill_turns<MODE == 1 ? VEC / 2 : VEC, MODE == 1>(a.rot, cs, token0, nt);
     if constexpr (PAGED) {
         if ((int)threadIdx.x < nt) {
             const int t = threadIdx.x;
@@ -246,12 +270,12 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs a)
         }
         const int f0 = is_q ? q0 : is_v ? v0 : e0, f1 = is_q ? q1 : is_v ? v1 : e1;
         if (!is_v) {
-            const float2* c = cs + t * a.turn_stride;
+            const float2* c = cs + t * turn_stride(half);
             if constexpr (MODE == 1) {
-                if (in0) turn_along(x[b], c + ((e0 - off) >> 1));
-                if (in1) turn_along(y[b], c + ((e1 - off) >> 1));
+                if (in0) turn_along(x[b], c, half, (e0 - off) / VEC);
+                if (in1) turn_along(y[b], c, half, (e1 - off) / VEC);
             } else {
-                if (turns) turn_across(x[b], y[b], c + u * VEC);
+                if (turns) turn_across(x[b], y[b], c, half, u);
             }
         }
         if (f0 >= 0) store_vec(dst + f0, x[b]);
@@ -264,7 +288,7 @@ cudaError_t launch_mode(const RopeArgs& a, cudaStream_t stream)
 {
     const long long rows = (long long)a.tokens * (a.q.heads + a.k.heads + a.v.heads);
     const dim3 grid((unsigned)((rows + a.rows_per_cta - 1) / a.rows_per_cta));
-    const size_t smem = (size_t)kRopeMaxTokens * a.turn_stride * sizeof(float2);
+    const size_t smem = (size_t)kRopeMaxTokens * turn_stride(a.rot.half) * sizeof(float2);
     return a.paged ? launch_dependent(rope_kernel<T, VEC, MODE, true>, grid, kThreads, smem, stream, a)
                    : launch_dependent(rope_kernel<T, VEC, MODE, false>, grid, kThreads, smem, stream, a);
 }

@@ -66,12 +66,30 @@ __device__ __forceinline__ float2 turned(uint64_t step, long long position, floa
     return make_float2(c * mscale, s * mscale * sign);
 }
 
-// Values of a token in the table below: an even number, so that two of them
-// can be read at once.
-__host__ __device__ __forceinline__ int turn_stride(int half) { return (half + 1) & ~1; }
+// Where pair j lies in a token's part of the table below.  Neighbouring
+// threads take neighbouring runs of `run` pairs and read them two at a time:
+// the first two of every run, then the next two, so that these reads are
+// contiguous.  With kTwin a thread takes two runs, whose first ones precede
+// the second ones.
+template <int kRun, bool kTwin>
+__device__ __forceinline__ int turn_place(int half, int j)
+{
+    if constexpr (kRun < 2) {
+        return j;
+    } else {
+        const int run = j / kRun, k = j % kRun;
+        if constexpr (!kTwin) return 2 * ((k >> 1) * (half / kRun) + run) + (k & 1);
+        const int runs = (half / kRun + 1) >> 1;
+        return 2 * (((run & 1) * (kRun / 2) + (k >> 1)) * runs + (run >> 1)) + (k & 1);
+    }
+}
 
-// Fills cs[t * turn_stride(half) + j] for the CTA's tokens; every thread of
-// the CTA calls.
+// Values of a token in the table: room for an odd run out, and an even number.
+__host__ __device__ __forceinline__ int turn_stride(int half) { return (half + 5) & ~1; }
+
+// Fills cs[t * turn_stride(half) + turn_place(j)] for the CTA's tokens; every
+// thread of the CTA calls.
+template <int kRun, bool kTwin>
 __device__ __forceinline__ void fill_turns(const RotaryArgs& r, float2* cs, long long token0,
                                            int tokens)
 {
@@ -83,8 +101,9 @@ __device__ __forceinline__ void fill_turns(const RotaryArgs& r, float2* cs, long
     if (g < lanes) {
         for (int j = (int)threadIdx.x - g * half; j < half; j += blockDim.x) {
             const uint64_t step = load_step(r, j);
+            const int at = turn_place<kRun, kTwin>(half, j);
             for (int t = g; t < tokens; t += lanes)
-                cs[t * turn_stride(half) + j] = turned(step, load_position(r, token0 + t), r.mscale, r.sign);
+                cs[t * turn_stride(half) + at] = turned(step, load_position(r, token0 + t), r.mscale, r.sign);
         }
     }
 }

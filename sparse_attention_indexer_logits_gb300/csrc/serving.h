@@ -57,7 +57,6 @@ struct RopeArgs {
     int vec;                       // elements per access: a power of two up to 16 bytes
     int rows_per_cta;
     int row_lanes_log2;            // threads of a row: a power of two, at most 256
-    int turn_stride;
 };
 
 constexpr int kRopeThreads = 256;
