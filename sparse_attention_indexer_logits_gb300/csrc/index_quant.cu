@@ -9,7 +9,7 @@
 //
 // Bound by memory: 256 bytes in, 128 out per row.  Eight lanes hold a row,
 // sixteen elements each, arranged so that both elements of a pair lie in one
-// lane, and up to four rows a lane; a CTA takes that many rows of the
+// lane, and up to three rows a lane; a CTA takes that many rows of the
 // flattened (token, head) list, a token's key after its heads, loads them
 // all, computes its tokens' angles while they are on their way, and works.
 // A row's maximum takes three shuffles; it keeps a NaN, so a row with one
@@ -66,7 +66,7 @@ __device__ __forceinline__ float max_nan(float a, float b)
 }
 
 template <bool INTER>
-__global__ void __launch_bounds__(kThreads, 3) index_quant_kernel(const IndexQuantArgs a)
+__global__ void __launch_bounds__(kThreads, 4) index_quant_kernel(const IndexQuantArgs a)
 {
     extern __shared__ __align__(16) float2 cs[];
     __shared__ long long page_of[kQuantMaxTokens];
@@ -104,27 +104,29 @@ __global__ void __launch_bounds__(kThreads, 3) index_quant_kernel(const IndexQua
         if (c0 >= off8) c0 += 2 * half8;
         if (c1 >= off8) c1 += 2 * half8;
     }
-    // token of the CTA and row of the token, of this group's row b
-    auto place = [&](int b, int& t, int& r) {
-        const int i = (int)threadIdx.x / kRowLanes + b * kRows;
-        r = first + i;
-        t = (int)(((float)r + 0.5f) * per_row);      // r / rows: r is below 2^16
-        r -= t * rows;
-        return i < count;
+    // token of the CTA and row of the token, of this group's next row
+    const int i0 = (int)threadIdx.x / kRowLanes;
+    const int t0 = (int)(((float)(first + i0) + 0.5f) * per_row);     // (first + i0) / rows: below 2^16
+    const int h0 = first + i0 - t0 * rows;
+    auto next = [&](int& t, int& h) {
+        h += kRows;
+        while (h >= rows) { h -= rows; ++t; }
     };
     uint4 v0[kQuantRows], v1[kQuantRows];
     float weight[kQuantRows];
+    {
+        int t = t0, h = h0;
 #pragma unroll
-    for (int b = 0; b < kQuantRows; ++b) {
-        int t, h;
-        if (!place(b, t, h)) continue;
-        const long long tok = token0 + t;
-        const __nv_bfloat16* src =
-            h == a.heads ? static_cast<const __nv_bfloat16*>(a.k) + tok * a.k_token
-                         : static_cast<const __nv_bfloat16*>(a.q) + tok * a.q_token + h * a.q_head;
-        v0[b] = __ldg(reinterpret_cast<const uint4*>(src) + c0);
-        v1[b] = __ldg(reinterpret_cast<const uint4*>(src) + c1);
-        weight[b] = lane == 0 && h < a.heads ? __ldg(a.weights + tok * a.heads + h) : 0.0f;
+        for (int b = 0; b < kQuantRows; ++b, next(t, h)) {
+            if (i0 + b * kRows >= count) continue;
+            const long long tok = token0 + t;
+            const __nv_bfloat16* src =
+                h == a.heads ? static_cast<const __nv_bfloat16*>(a.k) + tok * a.k_token
+                             : static_cast<const __nv_bfloat16*>(a.q) + tok * a.q_token + h * a.q_head;
+            v0[b] = __ldg(reinterpret_cast<const uint4*>(src) + c0);
+            v1[b] = __ldg(reinterpret_cast<const uint4*>(src) + c1);
+            weight[b] = lane == 0 && h < a.heads ? __ldg(a.weights + tok * a.heads + h) : 0.0f;
+        }
     }
 
     fill_turns<INTER ? 4 : 8, INTER>(a.rot, cs, token0, nt);
@@ -142,10 +144,10 @@ __global__ void __launch_bounds__(kThreads, 3) index_quant_kernel(const IndexQua
     }
     __syncthreads();
 
+    int t = t0, h = h0;
 #pragma unroll
-    for (int b = 0; b < kQuantRows; ++b) {
-        int t, h;
-        if (!place(b, t, h)) continue;                 // (eight lanes together)
+    for (int b = 0; b < kQuantRows; ++b, next(t, h)) {
+        if (i0 + b * kRows >= count) continue;         // (eight lanes together)
         const bool is_k = h == a.heads;
         if (state_of[t] < (is_k ? 2 : 1)) continue;
         float x[8], y[8];

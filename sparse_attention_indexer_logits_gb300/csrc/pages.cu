@@ -18,6 +18,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "dependent.cuh"
 #include "serving.h"
 
 namespace pml {
@@ -124,6 +125,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     __shared__ int buf[kWarps];
     __shared__ int ranks[kThreads];
     __shared__ int xfree;
+    allow_dependent_launch();
+    grid_dependency_wait();
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank();
     const PoolArgs& P = a.pool;
@@ -221,6 +224,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     __shared__ int buf[kWarps];
     __shared__ int ranks[kThreads];
     __shared__ int xfree;
+    allow_dependent_launch();
+    grid_dependency_wait();
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank();
     const PoolArgs& P = a.pool;
@@ -302,6 +307,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
 
 __global__ void __launch_bounds__(256) pages_free_kernel(const FreeArgs a)
 {
+    allow_dependent_launch();
+    grid_dependency_wait();
     const PoolArgs& P = a.pool;
     const int lane = threadIdx.x & 31;
     const int i = (int)((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
@@ -336,6 +343,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
 {
     __shared__ int buf[kWarps];
     __shared__ int xlive, xmove, xhole;
+    allow_dependent_launch();
+    grid_dependency_wait();
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank();
     const PoolArgs& P = a.pool;
@@ -421,6 +430,8 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const CopyPage
 {
     using W = typename Word<VEC>::type;
     constexpr int kPiece = kCopyThreads * kCopyUnroll;
+    allow_dependent_launch();
+    grid_dependency_wait();
     const long long n = min(max(*a.count, 0), a.capacity);
     const long long items = n * a.layers * pieces;
     for (long long it = blockIdx.x; it < items; it += gridDim.x) {
@@ -454,35 +465,31 @@ cudaError_t launch_copy(const CopyPagesArgs& a, int sm_count, cudaStream_t strea
     if (pieces > 0x7fffffffLL) return cudaErrorInvalidValue;
     long long grid = (long long)a.capacity * a.layers * pieces;
     if (grid > (long long)sm_count * 8) grid = (long long)sm_count * 8;
-    pages_copy_kernel<VEC><<<(unsigned)grid, kCopyThreads, 0, stream>>>(a, words, (int)pieces);
-    return cudaGetLastError();
+    return launch_dependent(pages_copy_kernel<VEC>, dim3((unsigned)grid), kCopyThreads, 0, stream, a, words,
+                            (int)pieces);
 }
 
 }  // namespace
 
 cudaError_t launch_pages_fork(const ForkArgs& a, cudaStream_t stream)
 {
-    pages_fork_kernel<<<kCtas, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(pages_fork_kernel, dim3(kCtas), kThreads, 0, stream, a);
 }
 
 cudaError_t launch_pages_extend(const ExtendArgs& a, cudaStream_t stream)
 {
-    pages_extend_kernel<<<kCtas, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(pages_extend_kernel, dim3(kCtas), kThreads, 0, stream, a);
 }
 
 cudaError_t launch_pages_free(const FreeArgs& a, cudaStream_t stream)
 {
     const unsigned blocks = ((unsigned)a.n + 7) / 8;
-    pages_free_kernel<<<blocks, 256, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(pages_free_kernel, dim3(blocks), 256, 0, stream, a);
 }
 
 cudaError_t launch_pages_compact(const CompactArgs& a, cudaStream_t stream)
 {
-    pages_compact_kernel<<<kCtas, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(pages_compact_kernel, dim3(kCtas), kThreads, 0, stream, a);
 }
 
 cudaError_t launch_pages_copy(const CopyPagesArgs& a, int sm_count, cudaStream_t stream)

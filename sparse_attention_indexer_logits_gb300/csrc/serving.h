@@ -82,7 +82,7 @@ struct IndexQuantArgs {
 };
 
 constexpr int kQuantThreads = 256;
-constexpr int kQuantRows = 4;      // rows of a group of eight lanes
+constexpr int kQuantRows = 3;      // rows of a group of eight lanes
 constexpr int kQuantMaxTokens = 8; // of a CTA, in part
 
 // A pool of pages: ref_counts[page] requests hold the page (0: free), and the
