@@ -17,66 +17,96 @@ constexpr int kJoinWarps = 8;
 
 // A CTA whose range ended inside an item it had begun (slot 1) owns the join:
 // the item's other pieces are slot 0 of the following CTAs, up to the one
-// that holds its end.  A warp takes 32 rows (neighbours in the workspace) and
-// 16 columns; a lane goes over its row's pieces twice, for the maximum and
-// for the weighted sum.
+// that holds its end.  A CTA here takes 16 columns of an item's rows; a warp
+// 32 rows (neighbours in the workspace), and where the rows leave warps over
+// (a single token's few rows in many pieces) each a part of the pieces, in
+// the order of their numbers, joined through shared memory.  Bound by the
+// latency of dependent loads: the records of the owner and of the CTAs after
+// it, then maxima, sums and values at once (one pass with a running maximum).
 template <int D, bool FP16>
 __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const AttnArgs a, int num_ctas)
 {
+    __shared__ float part[kJoinWarps][18][32];
     allow_dependent_launch();
     grid_dependency_wait();
     const int owner = blockIdx.x;
-    const int* rec = a.pieces + (owner * 2LL + 1) * kPieceInts;
-    if (!rec[kPcUsed]) return;
-    const int tok0 = rec[kPcTok0], ntok = rec[kPcNtok], head = rec[kPcHead];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int G = a.group;
-    const int half_rows = a.half_tokens * G;      // rows in use of a half
-    constexpr int kColGroups = D / 16;
-    // groups of 32 rows, four to a half
-    const int unit = blockIdx.y * kJoinWarps + warp;
-    const int cols = unit % kColGroups * 16, row = unit / kColGroups * 32 + lane;
-    const int in_half = row % kAttnHalfRows;
-    const int i = row / kAttnHalfRows * a.half_tokens + in_half / G, g = in_half % G;
-    const bool valid = in_half < half_rows && i < ntok;
-    if (!__any_sync(0xffffffffu, valid)) return;
-    int end = owner + 1;              // the CTA that holds the item's end
-    for (; end < num_ctas; end += 32) {
-        const int cta = end + lane;
-        const bool here = cta < num_ctas && a.pieces[cta * 2LL * kPieceInts + kPcLast] &&
-                          a.pieces[cta * 2LL * kPieceInts + kPcUsed];
-        const unsigned who = __ballot_sync(0xffffffffu, here);
-        if (who) {
-            end += __ffs(who) - 1;
-            break;
-        }
-    }
-    if (end >= num_ctas || !valid) return;      // (an item's end is in some range)
-    const int pieces = end - owner + 1;
-    // piece p: slot 1 of the owner, then slot 0 of its followers
-    auto stat = [&](int p) {
-        return a.stats[((owner + p) * 2LL + (p == 0 ? 1 : 0)) * kAttnSlotRows + row];
+    const int4* rec = reinterpret_cast<const int4*>(a.pieces + (owner * 2LL + 1) * kPieceInts);
+    const int4 r0 = rec[0];                       // used, first token, tokens, kv head
+    // the first CTA after the owner that holds the item's end
+    auto ends = [&](int cta) {
+        if (cta >= num_ctas) return false;
+        const int* p = a.pieces + cta * 2LL * kPieceInts;
+        return p[kPcUsed] && p[kPcLast];
     };
-    float top = -INFINITY;
-#pragma unroll 4
-    for (int p = 0; p < pieces; ++p) top = fmaxf(top, stat(p).x);
-    float sum = 0.0f, acc[16] = {};
-#pragma unroll 2
-    for (int p = 0; p < pieces; ++p) {
-        const float2 s = stat(p);
-        const float f = s.x == -INFINITY ? 0.0f : exp2_approx((s.x - top) * a.scale_log2);
-        sum += s.y * f;
-        const float* o = a.partial + partial_at<D>(owner + p, p == 0 ? 1 : 0, cols / 4, row);
+    unsigned who = __ballot_sync(0xffffffffu, ends(owner + 1 + lane));
+    if (!r0.x) return;
+    int end = owner + 1;
+    while (!who && end + 32 < num_ctas) {
+        end += 32;
+        who = __ballot_sync(0xffffffffu, ends(end + lane));
+    }
+    if (!who) return;                             // never: an item's end is in some range
+    end += __ffs(who) - 1;
+    const int pieces = end - owner + 1;
+    const int tok0 = r0.y, ntok = r0.z, head = r0.w;
+    const int G = a.group;
+    // groups of 32 rows, first half 0's, then half 1's; the pieces' parts
+    const int rows0 = min(ntok, a.half_tokens) * G, rows1 = max(ntok - a.half_tokens, 0) * G;
+    const int groups0 = (rows0 + 31) >> 5, groups = groups0 + ((rows1 + 31) >> 5);
+    const int groups_log2 = groups <= 1 ? 0 : 32 - __clz(groups - 1);
+    const int grp = warp & ((1 << groups_log2) - 1), split = warp >> groups_log2;
+    const int splits = kJoinWarps >> groups_log2;
+    const int half = grp >= groups0 ? 1 : 0;
+    const int in_half = (grp - half * groups0) * 32 + lane;
+    const bool valid = grp < groups && in_half < (half ? rows1 : rows0);
+    const int row = half * kAttnHalfRows + in_half;
+    const int cols = blockIdx.y * 16;
+    const int p0 = pieces * split / splits, p1 = pieces * (split + 1) / splits;
+    float top = -INFINITY, sum = 0.0f, acc[16] = {};
+    auto add = [&](float m, float l, const float (&v)[16]) {
+        const float next = fmaxf(top, m);
+        const float f = top == -INFINITY ? 0.0f : exp2_approx((top - next) * a.scale_log2);
+        const float g = m == -INFINITY ? 0.0f : exp2_approx((m - next) * a.scale_log2);
+        top = next;
+        sum = sum * f + l * g;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float4 v = *reinterpret_cast<const float4*>(o + k * 4 * kAttnSlotRows);
-            acc[4 * k] = fmaf(v.x, f, acc[4 * k]);
-            acc[4 * k + 1] = fmaf(v.y, f, acc[4 * k + 1]);
-            acc[4 * k + 2] = fmaf(v.z, f, acc[4 * k + 2]);
-            acc[4 * k + 3] = fmaf(v.w, f, acc[4 * k + 3]);
+        for (int k = 0; k < 16; ++k) acc[k] = fmaf(v[k], g, acc[k] * f);
+    };
+    if (valid) {
+#pragma unroll 2
+        for (int p = p0; p < p1; ++p) {
+            // piece p: slot 1 of the owner, then slot 0 of its followers
+            const int slot = p == 0 ? 1 : 0;
+            const float2 st = a.stats[((owner + p) * 2LL + slot) * kAttnSlotRows + row];
+            const float* o = a.partial + partial_at<D>(owner + p, slot, cols / 4, row);
+            float v[16];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                *reinterpret_cast<float4*>(v + 4 * k) = *reinterpret_cast<const float4*>(o + k * 4 * kAttnSlotRows);
+            add(st.x, st.y, v);
         }
     }
+    if (splits > 1) {
+        if (split > 0) {
+            part[warp][16][lane] = top;
+            part[warp][17][lane] = sum;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) part[warp][k][lane] = acc[k];
+        }
+        __syncthreads();
+        if (split > 0) return;
+        for (int q = 1; q < splits; ++q) {
+            const int w = (q << groups_log2) + grp;
+            float v[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = part[w][k][lane];
+            add(part[w][16][lane], part[w][17][lane], v);
+        }
+    }
+    if (!valid) return;
     const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+    const int i = half * a.half_tokens + in_half / G, g = in_half % G;
     const long long token = tok0 + i;
     const int qhead = head * G + g;
     uint32_t w[8];
@@ -93,7 +123,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const A
 template <int D, bool FP16>
 cudaError_t launch_join(const AttnArgs& a, int num_ctas, cudaStream_t stream)
 {
-    return launch_dependent(attention_join_kernel<D, FP16>, dim3((unsigned)num_ctas, kAttnSlotRows / 32 * (D / 16) / kJoinWarps),
+    return launch_dependent(attention_join_kernel<D, FP16>, dim3((unsigned)num_ctas, D / 16),
                             kJoinWarps * 32, 0, stream, a, num_ctas);
 }
 
