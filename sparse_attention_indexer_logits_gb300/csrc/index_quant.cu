@@ -130,8 +130,8 @@ __global__ void __launch_bounds__(kThreads, 4) index_quant_kernel(const IndexQua
     }
 
     fill_turns<INTER ? 4 : 8, INTER>(a.rot, cs, token0, nt);
-    if ((int)threadIdx.x < nt) {
-        const int t = threadIdx.x;
+    // (by the last warp: the first ones have the angles)
+    if (const int t = (int)threadIdx.x - (kThreads - 32); t >= 0 && t < nt) {
         bool pad = false;
         long long page = 0;
         int slot = 0;

@@ -240,8 +240,9 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs a)
 
     fill_turns<MODE == 1 ? VEC / 2 : VEC, MODE == 1>(a.rot, cs, token0, nt);
     if constexpr (PAGED) {
-        if ((int)threadIdx.x < nt) {
-            const int t = threadIdx.x;
+        // (by the last warp: the first ones have the angles)
+        const int t = (int)threadIdx.x - (kThreads - 32);
+        if (t >= 0 && t < nt) {
             bool pad;
             long long page;
             int slot;

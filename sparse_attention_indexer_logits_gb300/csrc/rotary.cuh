@@ -98,12 +98,15 @@ __device__ __forceinline__ void fill_turns(const RotaryArgs& r, float2* cs, long
     // thread = (pair, token lane): one step per thread while pairs <= threads
     const int lanes = max(1, (int)blockDim.x / half);
     const int g = (int)threadIdx.x / half;
-    if (g < lanes) {
+    if (g < lanes && g < tokens) {
+        // (both loads on their way before either is used)
+        const long long first = load_position(r, token0 + g);
         for (int j = (int)threadIdx.x - g * half; j < half; j += blockDim.x) {
             const uint64_t step = load_step(r, j);
             const int at = turn_place<kRun, kTwin>(half, j);
             for (int t = g; t < tokens; t += lanes)
-                cs[t * turn_stride(half) + at] = turned(step, load_position(r, token0 + t), r.mscale, r.sign);
+                cs[t * turn_stride(half) + at] =
+                    turned(step, t == g ? first : load_position(r, token0 + t), r.mscale, r.sign);
         }
     }
 }
