@@ -362,7 +362,7 @@ int pml_index_quant_append(const void* q, int64_t q_token_stride, int64_t q_head
     a.weight_scale = weight_scale;
     a.tokens = tokens;
     a.heads = num_heads;
-    a.rows_per_cta = cta_rows(kQuantRows, kQuantThreads / 8, num_heads + (k != nullptr ? 1 : 0), kQuantMaxTokens,
+    a.rows_per_cta = cta_rows(kQuantRows, kQuantThreads / kQuantLanes, num_heads + (k != nullptr ? 1 : 0), kQuantMaxTokens,
                               tokens, dev.sm_count);
     e = launch_index_quant(a, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PML_OK : cuda_fail(e);

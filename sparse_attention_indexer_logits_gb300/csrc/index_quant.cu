@@ -7,13 +7,14 @@
 // next to it in its page (the s_p of the logits), so the logits are those of
 // the unquantised rows up to the codes' rounding (half a step, 2^-4).
 //
-// Bound by memory: 256 bytes in, 128 out per row.  Eight lanes hold a row,
-// sixteen elements each, arranged so that both elements of a pair lie in one
-// lane, and up to three rows a lane; a CTA takes that many rows of the
+// Bound by memory: 256 bytes in, 128 out per row.  Four lanes hold a row,
+// two units of sixteen elements each, a unit arranged so that both elements
+// of a pair lie in it (where half of the row turns, every lane has one unit
+// that does and one that does not); a CTA takes a few rows a lane of the
 // flattened (token, head) list, a token's key after its heads, loads them
 // all, computes its tokens' angles while they are on their way, and works.
-// A row's maximum takes three shuffles; it keeps a NaN, so a row with one
-// gets a NaN scale instead of a silent one.  The quotient is a product with
+// A row's maximum takes two shuffles; it keeps a NaN, so a row with one gets
+// a NaN scale instead of a silent one.  The quotient is a product with
 // 448 / max, one rounding more than a division (2^-23 against the code's
 // 2^-4) and a tenth of its instructions.
 #include <cuda_bf16.h>
@@ -29,7 +30,7 @@ namespace pml {
 namespace {
 
 constexpr int kThreads = kQuantThreads;
-constexpr int kRowLanes = 8;                       // lanes of a row
+constexpr int kRowLanes = kQuantLanes;                       // lanes of a row
 constexpr int kRows = kThreads / kRowLanes;        // rows of a CTA's step
 
 __device__ __forceinline__ void unpack8(uint4 v, float (&x)[8])
@@ -66,7 +67,7 @@ __device__ __forceinline__ float max_nan(float a, float b)
 }
 
 template <bool INTER>
-__global__ void __launch_bounds__(kThreads, 4) index_quant_kernel(const IndexQuantArgs a)
+__global__ void __launch_bounds__(kThreads, 3) index_quant_kernel(const IndexQuantArgs a)
 {
     extern __shared__ __align__(16) float2 cs[];
     __shared__ long long page_of[kQuantMaxTokens];
@@ -85,24 +86,27 @@ __global__ void __launch_bounds__(kThreads, 4) index_quant_kernel(const IndexQua
     const float per_row = 1.0f / (float)rows;
 
     const int lane = threadIdx.x & (kRowLanes - 1);
-    const unsigned mask = 0xffu << (threadIdx.x & 24);
-    // the two 8-element chunks of this lane: the halves of eight pairs, or
-    // two chunks outside the rotated part, or (interleaved) two neighbours
-    int c0 = 2 * lane, c1 = 2 * lane + 1;
-    // which of the chunks turn
-    bool turn0 = false, turn1 = false;
-    if constexpr (INTER) {
-        turn0 = c0 >= off8 && c0 < off8 + 2 * half8;
-        turn1 = c1 >= off8 && c1 < off8 + 2 * half8;
-    } else if (lane < half8) {
-        c0 = off8 + lane;
-        c1 = c0 + half8;
-        turn0 = true;
-    } else {
-        c0 = 2 * (lane - half8);
-        c1 = c0 + 1;
-        if (c0 >= off8) c0 += 2 * half8;
-        if (c1 >= off8) c1 += 2 * half8;
+    const unsigned mask = 0xfu << (threadIdx.x & 28);
+    // the two 8-element chunks of each of this lane's units, lane and lane +
+    // 4: the halves of eight pairs, or two chunks outside the rotated part,
+    // or (interleaved) two neighbours
+    int c0[2], c1[2];
+    bool turn0[2], turn1[2];       // which of the chunks turn
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int u = lane + kRowLanes * i;
+        if (INTER || u >= half8) {
+            c0[i] = 2 * (INTER ? u : u - half8);
+            c1[i] = c0[i] + 1;
+            if (!INTER && c0[i] >= off8) c0[i] += 2 * half8;
+            if (!INTER && c1[i] >= off8) c1[i] += 2 * half8;
+            turn0[i] = INTER && c0[i] >= off8 && c0[i] < off8 + 2 * half8;
+            turn1[i] = INTER && c1[i] >= off8 && c1[i] < off8 + 2 * half8;
+        } else {
+            c0[i] = off8 + u;
+            c1[i] = c0[i] + half8;
+            turn0[i] = turn1[i] = true;
+        }
     }
     // token of the CTA and row of the token, of this group's next row
     const int i0 = (int)threadIdx.x / kRowLanes;
@@ -112,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 4) index_quant_kernel(const IndexQua
         h += kRows;
         while (h >= rows) { h -= rows; ++t; }
     };
-    uint4 v0[kQuantRows], v1[kQuantRows];
+    uint4 v0[kQuantRows][2], v1[kQuantRows][2];
     float weight[kQuantRows];
     {
         int t = t0, h = h0;
@@ -123,8 +127,11 @@ __global__ void __launch_bounds__(kThreads, 4) index_quant_kernel(const IndexQua
             const __nv_bfloat16* src =
                 h == a.heads ? static_cast<const __nv_bfloat16*>(a.k) + tok * a.k_token
                              : static_cast<const __nv_bfloat16*>(a.q) + tok * a.q_token + h * a.q_head;
-            v0[b] = __ldg(reinterpret_cast<const uint4*>(src) + c0);
-            v1[b] = __ldg(reinterpret_cast<const uint4*>(src) + c1);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                v0[b][i] = __ldg(reinterpret_cast<const uint4*>(src) + c0[i]);
+                v1[b][i] = __ldg(reinterpret_cast<const uint4*>(src) + c1[i]);
+            }
             weight[b] = lane == 0 && h < a.heads ? __ldg(a.weights + tok * a.heads + h) : 0.0f;
         }
     }
@@ -147,12 +154,10 @@ __global__ void __launch_bounds__(kThreads, 4) index_quant_kernel(const IndexQua
     int t = t0, h = h0;
 #pragma unroll
     for (int b = 0; b < kQuantRows; ++b, next(t, h)) {
-        if (i0 + b * kRows >= count) continue;         // (eight lanes together)
+        if (i0 + b * kRows >= count) continue;         // (the lanes of a row together)
         const bool is_k = h == a.heads;
         if (state_of[t] < (is_k ? 2 : 1)) continue;
-        float x[8], y[8];
-        unpack8(v0[b], x);
-        unpack8(v1[b], y);
+        float x[2][8], y[2][8];
         const float2* c = cs + t * turn_stride(half);
         // two pairs' angles at a time
         auto turn2 = [](float& p0, float& q0, float& p1, float& q1, float4 w) {
@@ -162,37 +167,46 @@ __global__ void __launch_bounds__(kThreads, 4) index_quant_kernel(const IndexQua
             p1 = a1 * w.z - b1 * w.w;
             q1 = b1 * w.z + a1 * w.w;
         };
-        if constexpr (INTER) {
-#pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-                if (turn0)
-                    turn2(x[2 * e], x[2 * e + 1], x[2 * e + 2], x[2 * e + 3],
-                          *reinterpret_cast<const float4*>(c + turn_place<4, true>(half, 4 * (c0 - off8) + e)));
-                if (turn1)
-                    turn2(y[2 * e], y[2 * e + 1], y[2 * e + 2], y[2 * e + 3],
-                          *reinterpret_cast<const float4*>(c + turn_place<4, true>(half, 4 * (c1 - off8) + e)));
-            }
-        } else if (turn0) {
-#pragma unroll
-            for (int e = 0; e < 8; e += 2)
-                turn2(x[e], y[e], x[e + 1], y[e + 1],
-                      *reinterpret_cast<const float4*>(c + turn_place<8, false>(half, 8 * lane + e)));
-        }
         float amax = 1e-12f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) amax = max_nan(amax, max_nan(fabsf(x[e]), fabsf(y[e])));
+        for (int i = 0; i < 2; ++i) {
+            unpack8(v0[b][i], x[i]);
+            unpack8(v1[b][i], y[i]);
+            if constexpr (INTER) {
 #pragma unroll
-        for (int o = 4; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(mask, amax, o));
+                for (int e = 0; e < 4; e += 2) {
+                    if (turn0[i])
+                        turn2(x[i][2 * e], x[i][2 * e + 1], x[i][2 * e + 2], x[i][2 * e + 3],
+                              *reinterpret_cast<const float4*>(c + turn_place<4, true>(half, 4 * (c0[i] - off8) + e)));
+                    if (turn1[i])
+                        turn2(y[i][2 * e], y[i][2 * e + 1], y[i][2 * e + 2], y[i][2 * e + 3],
+                              *reinterpret_cast<const float4*>(c + turn_place<4, true>(half, 4 * (c1[i] - off8) + e)));
+                }
+            } else if (turn0[i]) {
+#pragma unroll
+                for (int e = 0; e < 8; e += 2)
+                    turn2(x[i][e], y[i][e], x[i][e + 1], y[i][e + 1],
+                          *reinterpret_cast<const float4*>(
+                              c + turn_place<8, false>(half, 8 * (lane + kRowLanes * i) + e)));
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) amax = max_nan(amax, max_nan(fabsf(x[i][e]), fabsf(y[i][e])));
+        }
+#pragma unroll
+        for (int o = kRowLanes / 2; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(mask, amax, o));
         const float inv = __fdividef(448.0f, amax);
         const float scale = amax * (1.0f / 448.0f);
-        const uint2 p0 = pack_e4m3(x, inv), p1 = pack_e4m3(y, inv);
         uint8_t* dst = is_k ? a.kv_fused + page_of[t] * kFp8BlockBytes + slot_of[t] * kHeadDim
                             : a.q_out + ((token0 + t) * a.heads + h) * kHeadDim;
-        if constexpr (INTER) {
-            reinterpret_cast<uint4*>(dst)[lane] = make_uint4(p0.x, p0.y, p1.x, p1.y);
-        } else {
-            reinterpret_cast<uint2*>(dst)[c0] = p0;
-            reinterpret_cast<uint2*>(dst)[c1] = p1;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint2 p0 = pack_e4m3(x[i], inv), p1 = pack_e4m3(y[i], inv);
+            if constexpr (INTER) {
+                reinterpret_cast<uint4*>(dst)[lane + kRowLanes * i] = make_uint4(p0.x, p0.y, p1.x, p1.y);
+            } else {
+                reinterpret_cast<uint2*>(dst)[c0[i]] = p0;
+                reinterpret_cast<uint2*>(dst)[c1[i]] = p1;
+            }
         }
         if (lane == 0) {
             if (is_k)

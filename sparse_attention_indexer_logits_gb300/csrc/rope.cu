@@ -168,7 +168,7 @@ __device__ __forceinline__ void turn_along(Vec<T, VEC>& v, const float2* c, int 
 // neighbouring accesses per unit; 2: interleaved pairs, two elements per unit
 // (VEC 1).
 template <typename T, int VEC, int MODE, bool PAGED>
-__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs a)
+__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeArgs a)
 {
     extern __shared__ __align__(16) float2 cs[];
     __shared__ long long page_of[kRopeMaxTokens];

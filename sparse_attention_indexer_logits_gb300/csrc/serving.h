@@ -82,7 +82,8 @@ struct IndexQuantArgs {
 };
 
 constexpr int kQuantThreads = 256;
-constexpr int kQuantRows = 3;      // rows of a group of eight lanes
+constexpr int kQuantLanes = 4;     // of a row
+constexpr int kQuantRows = 2;      // rows of a lane
 constexpr int kQuantMaxTokens = 8; // of a CTA, in part
 
 // A pool of pages: ref_counts[page] requests hold the page (0: free), and the
