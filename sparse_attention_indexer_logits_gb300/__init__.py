@@ -472,6 +472,15 @@ def _serving(name: str, stream, *args):
         raise PmlError(rc, name)
 
 
+def _new(shape, dtype, device, stream):
+    """Memory for a call on `stream`: its own allocations, so that what is
+    freed when the call returns is not used again before the call has run."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _addr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
@@ -548,7 +557,7 @@ def pml_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
     tokens, heads, dim = shape
     pos, p64, freq, f64, rot = _rotation(positions, inv_freq, tokens)
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        out = _new(shape, x.dtype, x.device, stream)
     out_shape, dst = _heads(out, "out", x.dtype)
     if out_shape != shape:
         raise ValueError("out must have x's shape")
@@ -584,7 +593,7 @@ def pml_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions
     if c_shape != vc_shape or c_shape[2] != kv_heads or c_shape[3] != dim:
         raise ValueError("k_cache and v_cache must be [pages, 64, kv_heads, dim]")
     if q_out is None:
-        q_out = torch.empty(shape, dtype=dtype, device=q.device)
+        q_out = _new(shape, dtype, q.device, stream)
     out_shape, qo = _heads(q_out, "q_out", dtype)
     if out_shape != shape:
         raise ValueError("q_out must have q's shape")
@@ -629,9 +638,9 @@ def pml_index_quant_append(q: torch.Tensor, k: torch.Tensor | None, weights: tor
             raise ValueError("kv_fused must be uint8 and hold whole 8448-byte blocks")
         ka, k_stride, kv = k.data_ptr(), k.stride(0), kv_fused.data_ptr()
     if q_out is None:
-        q_out = torch.empty(shape, dtype=torch.float8_e4m3fn, device=q.device)
+        q_out = _new(shape, torch.float8_e4m3fn, q.device, stream)
     if w_out is None:
-        w_out = torch.empty((tokens, heads), dtype=torch.float32, device=q.device)
+        w_out = _new((tokens, heads), torch.float32, q.device, stream)
     if q_out.shape != shape or q_out.element_size() != 1 or w_out.shape != (tokens, heads) or \
             w_out.dtype is not torch.float32:
         raise ValueError("q_out must be 1-byte [tokens, heads, 128], w_out float32 [tokens, heads]")
@@ -643,7 +652,7 @@ def pml_index_quant_append(q: torch.Tensor, k: torch.Tensor | None, weights: tor
     return q_out, w_out
 
 
-def _attention(q, k_cache, v_cache, block_table, kv_lens, out, lse, workspace, softmax_scale):
+def _attention(q, k_cache, v_cache, block_table, kv_lens, out, lse, workspace, softmax_scale, stream):
     """The checks that both attention calls share; their arguments in three runs."""
     dtype = q.dtype
     shape, qa = _heads(q, "q")
@@ -657,7 +666,7 @@ def _attention(q, k_cache, v_cache, block_table, kv_lens, out, lse, workspace, s
     (rows, width), table, bt_stride = _table(block_table)
     lens = _ints(kv_lens, "kv_lens", rows)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=q.device)
+        out = _new(shape, dtype, q.device, stream)
     out_shape, oa = _heads(out, "out", dtype)
     if out_shape != shape:
         raise ValueError("out must have q's shape")
@@ -665,20 +674,20 @@ def _attention(q, k_cache, v_cache, block_table, kv_lens, out, lse, workspace, s
                             or not lse.is_contiguous() or not lse.is_cuda):
         raise ValueError("lse must be a contiguous CUDA float32 [tokens, heads] tensor")
     if workspace is None:
-        workspace = pml_attention_workspace(dim, q.device)
+        workspace = pml_attention_workspace(dim, q.device, stream)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     if softmax_scale is None:
         softmax_scale = dim ** -0.5
-    # (the workspace may go back to its allocator when the call returns: what
-    # takes its memory next on this stream runs after the kernels)
+    # (a workspace of the call's own goes back to its allocator when the call
+    # returns: what takes its memory next on the stream runs after the kernels)
     return (out, rows, (*qa, *kc, *vc, _DTYPES[dtype], c_shape[0], table, bt_stride, width, lens),
             (tokens, heads, c_shape[2], dim, softmax_scale),
             (*oa, _addr(lse), workspace.data_ptr(), workspace.numel() * workspace.element_size()),
             workspace)
 
 
-def pml_attention_workspace(head_dim: int, device=None) -> torch.Tensor:
+def pml_attention_workspace(head_dim: int, device=None, stream=None) -> torch.Tensor:
     """A workspace for the attention calls on ``device``: calls that may
     overlap on the GPU need one each."""
     d = torch.device("cuda" if device is None else device)
@@ -687,7 +696,7 @@ def pml_attention_workspace(head_dim: int, device=None) -> torch.Tensor:
     if size is None:
         size = lib().pml_attention_workspace_bytes(pml_default_num_ctas(key[0]), head_dim)
         _workspace_bytes[key] = size
-    return torch.empty(max(size, 16), dtype=torch.uint8, device=d)
+    return _new((max(size, 16),), torch.uint8, d, stream)
 
 
 _workspace_bytes: dict = {}    # by (device, head dimension)
@@ -709,7 +718,7 @@ def pml_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     ``lse`` receives the logarithms of the rows' sums.  ``softmax_scale``
     defaults to ``dim ** -0.5``."""
     out, batch, kv, size, tail, workspace = _attention(q, k_cache, v_cache, block_table, kv_lens, out, lse,
-                                                       workspace, softmax_scale)
+                                                       workspace, softmax_scale, stream)
     starts = None
     if cu_q is not None:
         starts = _ints(cu_q, "cu_q", batch + 1)
@@ -728,7 +737,7 @@ def pml_sparse_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     ``[tokens, k]``, as ``pml_topk_logits`` leaves them; entries below 0 or
     past the request's length are not there) of request ``requests[t]``."""
     out, rows, kv, size, tail, workspace = _attention(q, k_cache, v_cache, block_table, kv_lens, out, lse,
-                                                      workspace, softmax_scale)
+                                                      workspace, softmax_scale, stream)
     req = _ints(requests, "requests", size[0])
     (tokens, k), sel, sel_stride = _table(selected, "selected")
     if tokens != size[0]:

@@ -13,6 +13,7 @@ namespace {
 using namespace pml;
 
 constexpr int kMaxRopeDim = 512;
+constexpr int kNoWindow = 1 << 30;     // a window past every position; positions plus it fit an int
 constexpr int kRopeMaxRows = 32768;    // of a token: the kernels divide by it in fp32
 
 int check_rotary(const void* positions, const void* inv_freq, int positions_64, int freq_64,
@@ -96,8 +97,10 @@ int rope_launch(RopeArgs& a, void* stream)
     if (a.paged && units < (a.dim / a.vec + 1) / 2) units = (a.dim / a.vec + 1) / 2;    // v's rows
     while ((1 << a.row_lanes_log2) < units && a.row_lanes_log2 < 8) ++a.row_lanes_log2;
     if ((1 << a.row_lanes_log2) < units) return PML_ERR_UNSUPPORTED;    // never: head_dim <= 512
-    a.rows_per_cta = cta_rows(kRopeUnits, kRopeThreads >> a.row_lanes_log2, a.q.heads + a.k.heads + a.v.heads,
-                              kRopeMaxTokens, a.tokens, dev.sm_count);
+    const long long rows = a.q.heads + a.k.heads + a.v.heads;
+    a.rows_per_cta = cta_rows(kRopeUnits, kRopeThreads >> a.row_lanes_log2, rows, kRopeMaxTokens, a.tokens,
+                              dev.sm_count);
+    if (a.tokens * rows / a.rows_per_cta >= 0x7fffffffLL) return PML_ERR_UNSUPPORTED;    // CTAs
     e = launch_rope(a, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PML_OK : cuda_fail(e);
 }
@@ -362,8 +365,9 @@ int pml_index_quant_append(const void* q, int64_t q_token_stride, int64_t q_head
     a.weight_scale = weight_scale;
     a.tokens = tokens;
     a.heads = num_heads;
-    a.rows_per_cta = cta_rows(kQuantRows, kQuantThreads / kQuantLanes, num_heads + (k != nullptr ? 1 : 0), kQuantMaxTokens,
-                              tokens, dev.sm_count);
+    const long long rows = num_heads + (k != nullptr ? 1 : 0);
+    a.rows_per_cta = cta_rows(kQuantRows, kQuantThreads / kQuantLanes, rows, kQuantMaxTokens, tokens, dev.sm_count);
+    if (tokens * rows / a.rows_per_cta >= 0x7fffffffLL) return PML_ERR_UNSUPPORTED;    // CTAs
     e = launch_index_quant(a, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PML_OK : cuda_fail(e);
 }
@@ -505,7 +509,7 @@ int pml_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
     a.q_per_request = batch > 0 ? tokens / batch : 0;
     a.batch = batch;
     a.causal = causal ? 1 : 0;
-    a.window = window;
+    a.window = window < kNoWindow ? window : kNoWindow;
     return attention_call(a, q, q_token_stride, q_head_stride, k_cache, k_page_stride, k_slot_stride,
                           k_head_stride, v_cache, v_page_stride, v_slot_stride, v_head_stride, dtype,
                           num_pages, block_table, bt_stride, bt_width, kv_lens, tokens, num_heads,

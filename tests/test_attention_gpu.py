@@ -382,6 +382,34 @@ def test_same_result_every_time_and_captured():
     assert torch.equal(out, pml.pml_paged_attention(q, k, v, table, lens, cu))
 
 
+def test_memory_of_a_call_on_another_stream():
+    """The workspace and output that a call on another stream makes for itself
+    are not handed to the current stream's allocations while it runs."""
+    p = Problem([1] * 40, [3000] * 40, 8, 2, 128, BF, seed=21)
+    q, k, v, table, lens = p.device()
+    want = pml.pml_paged_attention(q, k, v, table, lens)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    with torch.cuda.stream(side):
+        big = torch.randn((6000, 6000), device="cuda")
+        for _ in range(5):
+            big = big @ big * 1e-3           # the call waits behind this
+    got = pml.pml_paged_attention(q, k, v, table, lens, stream=side)
+    size = pml.pml_attention_workspace(128).numel()
+    junk = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and len(junk) == 4
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 30, 5000])
+def test_windows_past_every_position(window):
+    p = Problem([30, 3], [20, 300], 4, 1, 64, BF, seed=22).stale()
+    out, lse = p.run(window=window)
+    check(p, out, lse)
+
+
 def test_no_tokens():
     p = Problem([0, 0], [10, 0], 4, 2, 64, BF, seed=13)
     out, _ = p.run()
