@@ -78,12 +78,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const A
         for (int p = p0; p < p1; ++p) {
             // piece p: slot 1 of the owner, then slot 0 of its followers
             const int slot = p == 0 ? 1 : 0;
-            const float2 st = a.stats[((owner + p) * 2LL + slot) * kAttnSlotRows + row];
+            // (a range without a tile's first unit left none)
+            const bool used = a.pieces[((owner + p) * 2LL + slot) * kPieceInts + kPcUsed];
+            float2 st = a.stats[((owner + p) * 2LL + slot) * kAttnSlotRows + row];
             const float* o = a.partial + partial_at<D>(owner + p, slot, cols / 4, row);
             float v[16];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 *reinterpret_cast<float4*>(v + 4 * k) = *reinterpret_cast<const float4*>(o + k * 4 * kAttnSlotRows);
+            if (!used) {
+                st = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] = 0.0f;
+            }
             add(st.x, st.y, v);
         }
     }

@@ -9,11 +9,11 @@
 // at the end out = O / l and lse = scale * m + ln l.
 //
 // Work.  The rows of an item are up to 256 (token, head) pairs that share a kv
-// head, its unit of work is one tile of 128 keys (and two units for the item
-// itself).  The units of all items, in order, are cut into one contiguous
-// range per CTA, so a long request's keys are split over many CTAs and short
-// requests share one, whatever the mix.  A range that ends inside an item
-// leaves its (m, l, O) in the workspace and a second kernel joins the pieces.
+// head; a tile of 128 keys is one or two units of work, the item itself three.
+// The units of all items, in order, are cut into one contiguous range per CTA,
+// so a long request's keys are split over many CTAs and short requests share
+// one, whatever the mix.  A range that ends inside an item leaves its (m, l, O)
+// in the workspace and a second kernel joins the pieces.
 //
 // A CTA holds two 128-row accumulator pairs (S and O, 512 TMEM columns).  An
 // item of more than 128 rows gives each its own half of the rows and both see
@@ -53,7 +53,7 @@
 //       chain (scores, softmax, P V) is hidden behind the other's except for
 //       its hand-overs, and the board is at its power limit
 //   24 requests of 1 .. 500 tokens over up to 8000 keys, window 1500, fp16, 64
-//       56 us: a floor of 7; the way into and out of an item and its first
+//       52 us: a floor of 7; the way into and out of an item and its first
 //       tiles, with a cold instruction cache and ranges of a few tiles
 //   64 tokens x 2048 listed positions, 64 heads over 1, bf16
 //       27 us: a floor of 10; a fixed part of 12 us (prologue, first lookups,
@@ -234,20 +234,6 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
     return ok != 0;
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32])
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-        "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-}
-
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr)
 {
     uint32_t r;
@@ -316,6 +302,7 @@ struct Span {
     int t0, ntok;    // tokens of the request
     int lo, hi;      // keys that some row of the tile may see
     int j0, n;       // their tiles of 128 keys; at least one
+    int cost;        // units of a tile
 };
 
 __device__ __forceinline__ Span tile_span(const AttnArgs& a, int nq, int kv, int tile)
@@ -335,6 +322,7 @@ __device__ __forceinline__ Span tile_span(const AttnArgs& a, int nq, int kv, int
     s.hi = (int)hi;
     s.j0 = s.lo / kAttnTileKeys;
     s.n = max(1, (s.hi + kAttnTileKeys - 1) / kAttnTileKeys - s.j0);
+    s.cost = s.ntok <= a.half_tokens ? 1 : 2;
     return s;
 }
 
@@ -357,10 +345,19 @@ __device__ __forceinline__ void request_of(const AttnArgs& a, int b, int& tok0, 
     kv = max(__ldg(a.kv_lens + b), 0);
 }
 
-// What beginning and ending an item costs, in tiles (Q's way in, the first
-// copies, the output): counted into the ranges, so that a CTA with many short
-// items gets fewer tiles.
-constexpr int kItemUnits = 2;
+// Units of work.  A tile is one where the halves take the tiles in turn and two
+// where both see it (1800 and 3600 cycles), and beginning and ending an item
+// (Q's way in, the first copies, the output) is three.  A mixed batch of 24
+// requests takes 51.7 us, with two or six units an item 54.5 or 52.3; 64 tokens
+// of 2048 listed positions 26.5 us, with two, four or six 26.4, 28.8 or 30.0.
+// A range has the tiles whose first unit lies in it.
+constexpr int kItemUnits = 3;
+__device__ __forceinline__ int units_of(const Span& s) { return s.n * s.cost + kItemUnits; }
+__device__ __forceinline__ int tiles_before(const Span& s, int unit)
+{
+    const int u = max(0, unit - kItemUnits);
+    return s.cost == 1 ? u : (u + 1) >> 1;
+}
 
 // Where a CTA's range begins, and how many units it has.
 struct Start {
@@ -380,7 +377,7 @@ __device__ __forceinline__ Start find_start(const AttnArgs& a, int* units, int l
         request_of(a, b, tok0, nq, kv);
         const int tiles = tiles_of(a, nq);
 #pragma unroll 1
-        for (int i = 0; i < tiles; ++i) u += tile_span(a, nq, kv, i).n + kItemUnits;
+        for (int i = 0; i < tiles; ++i) u += units_of(tile_span(a, nq, kv, i));
         units[b] = u;
         total += u;
     }
@@ -421,7 +418,7 @@ __device__ __forceinline__ Start find_start(const AttnArgs& a, int* units, int l
     const int tiles = tiles_of(a, nq);
 #pragma unroll 1
     for (int c = 0; c < tiles; c += 32) {
-        const int v = c + lane < tiles ? tile_span(a, nq, kv, c + lane).n + kItemUnits : 0;
+        const int v = c + lane < tiles ? units_of(tile_span(a, nq, kv, c + lane)) : 0;
         int incl = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -558,6 +555,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t qcount = 0;         // Q halves filled so far
         bool ok = true;
         int tok0 = 0, nq = 0, kv = 0, tiles = 0, cur_b = -1;
+        auto next_item = [&]() {
+            at = 0;
+            if constexpr (SEL) {
+                if (++head == a.kv_heads) { head = 0; ++b; }
+            } else {
+                if (++tile == tiles) {
+                    tile = 0;
+                    if (++head == a.kv_heads) { head = 0; ++b; }
+                }
+            }
+        };
         while (left > 0 && ok) {
             if (!SEL && b >= a.batch) break;     // lengths changed under the call
             Span sp;
@@ -577,6 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sp.hi = kv;
                 sp.j0 = 0;
                 sp.n = sel_tiles;
+                sp.cost = 1;
                 tok0 = b;
             } else {
                 if (b != cur_b) {
@@ -588,14 +597,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 req = b;
                 sp = tile_span(a, nq, kv, tile);
             }
-            // the tiles of this range: j .. j + n - 1; none if the range ends
-            // in the item's own units (the next one begins with its first tile)
-            const int j = max(0, at - kItemUnits);
-            const int used = (int)min(left, (long long)(sp.n + kItemUnits - at));
-            const int n = max(0, at + used - kItemUnits) - j;
+            // the tiles of this range: j .. j + n - 1
+            const int j = tiles_before(sp, at);
+            const int used = (int)min(left, (long long)(units_of(sp) - at));
+            const int n = tiles_before(sp, at + used) - j;
             left -= used;
-            if (n == 0) break;
             const bool first = j == 0, last = j + n == sp.n;
+            if (n == 0) {
+                if (!last) break;                // the range ends in the item's own units
+                next_item();
+                continue;
+            }
             const bool alt = SEL || sp.ntok <= a.half_tokens;
             const int slot = first ? 1 : 0;          // workspace slot of a piece
             // ---- the item's descriptor and Q rows
@@ -801,18 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++pos;
                 }
             }
-            // ---- the next item
-            at = 0;
-            if (last) {
-                if constexpr (SEL) {
-                    if (++head == a.kv_heads) { head = 0; ++b; }
-                } else {
-                    if (++tile == tiles) {
-                        tile = 0;
-                        if (++head == a.kv_heads) { head = 0; ++b; }
-                    }
-                }
-            }
+            if (last) next_item();
         }
         if constexpr (SEL) {
             for (; handed < pos; ++handed) {
@@ -1089,9 +1090,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int q = 0; q < 4; ++q) tmem_wait_bind32(x[q]);
                         if (masked) {
 #pragma unroll
-                            for (int k = 0; k < 128; ++k) {
-                                const uint32_t w = SEL ? shown[k & 3] >> (k >> 2) : shown[k >> 5] >> (k & 31);
-                                if (!(w & 1u)) x[k >> 5][k & 31] = 0xff800000u;    // -inf
+                            for (int q = 0; q < 4; ++q) {
+                                if (!SEL && __all_sync(0xffffffffu, shown[q] == 0xffffffffu)) continue;
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) {
+                                    const uint32_t w = SEL ? shown[k & 3] >> (8 * q + (k >> 2)) : shown[q] >> k;
+                                    if (!(w & 1u)) x[q][k] = 0xff800000u;    // -inf
+                                }
                             }
                         }
                     };
@@ -1153,9 +1158,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l += sum2(add2(sum[0], sum[1]));
                     tmem_wait_st();
                 }
-                // V rows that must not count
+                // V rows that must not count (selected ones came as zeros)
                 bool added = false;             // this tile's product is in O already
-                if (masked) {
+                if (!SEL && masked) {
                     const int vs = v_place % S;
                     // (the parity of v_place cannot be an older one's: these
                     // scores were issued after place v_place - S was consumed)
@@ -1165,21 +1170,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // thread = key of the tile
                     const int key = key0 + row;
                     const int item_lo = it[kItLo], item_hi = it[kItHi];
-                    bool none;                  // no row of the item sees it
-                    bool some = false;          // some rows of this half do not
-                    if constexpr (SEL) {
-                        none = !((there[row & 3] >> (row >> 2)) & 1u);
-                    } else {
-                        none = key < item_lo || key >= item_hi;
-                        some = !none && (key < all_lo || key >= all_hi);
-                    }
+                    const bool none = key < item_lo || key >= item_hi;    // no row of the item sees it
+                    const bool some = !none && (key < all_lo || key >= all_hi);    // some rows of this half do not
                     if (none) {
 #pragma unroll
                         for (int e = 0; e < 8 * C::kBlocks; ++e)
                             *reinterpret_cast<uint4*>(vt + (e >> 3) * C::kBlockBytes + row * 128 +
                                                       (((e + row) & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                        fence_proxy_async_smem();     // the tensor core reads it
                     }
-                    if constexpr (!SEL) {
+                    // (a tile with such keys, the same for all of the half)
+                    if (max(key0, item_lo) < all_lo || min(key0 + kAttnTileKeys, item_hi) > all_hi) {
                         bool bad = false;
                         if (some) {
 #pragma unroll 2
@@ -1240,7 +1241,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                             added = true;
                         }
                     }
-                    fence_proxy_async_smem();
                 }
                 // (P is in place: its stores were waited for)
                 __syncwarp();
