@@ -49,14 +49,15 @@
 //   64 single tokens over U[1024, 32768] keys, 8 kv heads of 128, bf16
 //       687 us, 4.71 GB: bound by HBM, 101 % of the copy
 //   4096 tokens that end 32768 keys, 32 heads over 4, bf16
-//       1535 us, 2.06 TFLOP: 1.34 PFLOP/s, 70 % of the product's.  One half's
-//       chain (scores, softmax, P V) is hidden behind the other's except for
-//       its hand-overs, and the board is at its power limit
+//       1500-1550 us, 2.06 TFLOP: 1.33-1.37 PFLOP/s, 70-72 % of the
+//       product's.  One half's chain (scores, softmax, P V) is hidden behind
+//       the other's except for its hand-overs, and the board is at its power
+//       limit
 //   24 requests of 1 .. 500 tokens over up to 8000 keys, window 1500, fp16, 64
-//       52 us: a floor of 7; the way into and out of an item and its first
-//       tiles, with a cold instruction cache and ranges of a few tiles
+//       53 us: a floor of 7; a tile's chain of 3600 cycles, 17 tiles a CTA,
+//       and the way into and out of two or three items
 //   64 tokens x 2048 listed positions, 64 heads over 1, bf16
-//       27 us: a floor of 10; a fixed part of 12 us (prologue, first lookups,
+//       29 us: a floor of 10; a fixed part of 12 us (prologue, first lookups,
 //       join), then the row copies.  (Sixteen lanes a row took 36 us: an
 //       offset to shuffle for every copy)
 #pragma once
@@ -348,10 +349,11 @@ __device__ __forceinline__ void request_of(const AttnArgs& a, int b, int& tok0, 
 // Units of work.  A tile is one where the halves take the tiles in turn and two
 // where both see it (1800 and 3600 cycles), and beginning and ending an item
 // (Q's way in, the first copies, the output) is three.  A mixed batch of 24
-// requests takes 51.7 us, with two or six units an item 54.5 or 52.3; 64 tokens
-// of 2048 listed positions 26.5 us, with two, four or six 26.4, 28.8 or 30.0.
-// A range has the tiles whose first unit lies in it.
+// requests takes 51.7 us (captured in a graph), with two or six units an item
+// 54.5 or 52.3; 64 tokens of 2048 listed positions 26.5 us, with two, four or
+// six 26.4, 28.8 or 30.0.  A range has the tiles whose first unit lies in it.
 constexpr int kItemUnits = 3;
+
 __device__ __forceinline__ int units_of(const Span& s) { return s.n * s.cost + kItemUnits; }
 __device__ __forceinline__ int tiles_before(const Span& s, int unit)
 {
