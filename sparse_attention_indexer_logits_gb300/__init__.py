@@ -1,10 +1,10 @@
 """Paged MQA logits for the sparse-attention indexer, GB300-native (sm_103a).
 
-Thin Python binding over the C ABI of ``libpml.so`` (``include/pml.h``):
-argument marshalling only -- every step of the computation runs in the
-library's CUDA kernels.  PyTorch supplies device memory and the current
-stream.  There is no CPU fallback: if the library is missing or cannot be
-loaded, every call raises.
+Thin Python binding over the C ABI of ``libpml.so`` (``include/pml.h``; the
+serving operators through the compiled module ``_calls``): argument
+marshalling only -- every step of the computation runs in the library's CUDA
+kernels.  PyTorch supplies device memory and the current stream.  There is no
+CPU fallback: if the library is missing or cannot be loaded, every call raises.
 
 Entry points (same names as the C ABI):
 
@@ -58,7 +58,7 @@ __all__ = [
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libpml.so")
-_lib = None
+_lib = _serving_calls = None
 
 STATUS_WAIT_TIMEOUT = 1
 STATUS_BAD_BLOCK = 2
@@ -78,7 +78,7 @@ class PmlError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """The loaded library (built by ``__graft_entry__.build()`` or
     ``sparse_attention_indexer_logits_gb300._build.build()``)."""
-    global _lib
+    global _lib, _serving_calls
     if _lib is None:
         if not os.path.exists(library_path):
             raise RuntimeError(
@@ -149,7 +149,13 @@ def lib() -> ctypes.CDLL:
             getattr(L, name).restype = i32
         L.pml_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint), i32]
         L.pml_device_status.restype = i32
-        _lib = L
+        try:
+            from . import _calls
+        except ImportError as e:
+            raise RuntimeError(f"{_HERE}/_calls.so cannot be loaded: build it again "
+                               "(python -c 'import __graft_entry__ as g; g.build()')") from e
+        _calls.bind(L._handle)
+        _lib, _serving_calls = L, _calls
     return _lib
 
 
@@ -460,26 +466,16 @@ def pml_fp8_paged_mqa_logits_noalloc(q: torch.Tensor, kv_fused: torch.Tensor,
 
 # ---------------------------------------------------------------- serving operators
 
-# A decode step makes these calls every few microseconds of GPU time, so their
-# checks look at each tensor once and the stream is read without a wrapper.
-
-_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-_HALVES = (torch.bfloat16, torch.float16)
-_INTS = {torch.int32: 0, torch.int64: 1}
-_FREQS = {torch.float32: 0, torch.float64: 1}
-_serving_calls: dict = {}
+# (their checks are in csrc/binding.cpp: a decode step makes these calls every
+# few microseconds of GPU time)
 
 
-def _serving(name: str, stream, *args):
-    call = _serving_calls.get(name)
-    if call is None:
-        call = _serving_calls[name] = getattr(lib(), name)
-    if stream is None:
-        rc = call(*args, torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
-    else:
-        rc = call(*args, stream.cuda_stream)
+def _serving(name: str, *args) -> None:
+    if _lib is None:
+        lib()
+    rc = getattr(_serving_calls, name)(*args)
     if rc != 0:
-        raise PmlError(rc, name)
+        raise PmlError(rc, "pml_" + name)
 
 
 def _new(shape, dtype, device, stream):
@@ -489,64 +485,6 @@ def _new(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _addr(t: torch.Tensor | None):
-    return None if t is None else t.data_ptr()
-
-
-def _heads(t: torch.Tensor, name: str, dtype=None):
-    """Shape, and (address, token stride, head stride) of a ``[tokens, heads,
-    dim]`` tensor with unit last stride."""
-    shape, strides = t.shape, t.stride()
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if len(shape) != 3 or (strides[2] != 1 and shape[2] > 1):
-        raise ValueError(f"{name} must be [tokens, heads, dim] with unit last stride")
-    if dtype is not None and t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}")
-    return shape, (t.data_ptr(), strides[0], strides[1])
-
-
-def _ints(t: torch.Tensor, name: str, count: int | None = None):
-    """Address of a contiguous int32 tensor of `count` values."""
-    if t.dtype is not torch.int32 or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA int32 tensor")
-    if count is not None and t.numel() != count:
-        raise ValueError(f"{name} must hold {count} values")
-    return t.data_ptr()
-
-
-def _rotation(positions: torch.Tensor, inv_freq: torch.Tensor, tokens: int):
-    """(address, 64-bit) of the positions and of the frequencies, rotated elements."""
-    p64, f64 = _INTS.get(positions.dtype), _FREQS.get(inv_freq.dtype)
-    if p64 is None or not positions.is_cuda:
-        raise ValueError("positions must be a CUDA int32 or int64 tensor")
-    if f64 is None or not inv_freq.is_cuda:
-        raise ValueError("inv_freq must be a CUDA float32 or float64 tensor")
-    if not positions.is_contiguous() or not inv_freq.is_contiguous():
-        raise ValueError("positions and inv_freq must be contiguous")
-    if positions.numel() != tokens:
-        raise ValueError("positions must hold one value per token")
-    return positions.data_ptr(), p64, inv_freq.data_ptr(), f64, 2 * inv_freq.numel()
-
-
-def _table(t: torch.Tensor, name: str = "block_table"):
-    """Shape, address and row stride of an int32 ``[rows, width]`` tensor."""
-    shape, strides = t.shape, t.stride()
-    if t.dtype is not torch.int32 or not t.is_cuda or len(shape) != 2 or (strides[1] != 1 and shape[1] > 1):
-        raise ValueError(f"{name} must be a CUDA int32 [rows, width] tensor with unit last stride")
-    return shape, t.data_ptr(), strides[0]
-
-
-def _cache(t: torch.Tensor, name: str, dtype):
-    """Shape, and (address, page, slot and head strides) of a cache."""
-    shape, strides = t.shape, t.stride()
-    if not t.is_cuda or len(shape) != 4 or shape[1] != 64 or (strides[3] != 1 and shape[3] > 1):
-        raise ValueError(f"{name} must be a CUDA [pages, 64, heads, dim] tensor with unit last stride")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}")
-    return shape, (t.data_ptr(), strides[0], strides[1], strides[2])
 
 
 def pml_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
@@ -560,19 +498,9 @@ def pml_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
     head is rotated, from element ``rot_offset`` on; pairs are ``(j, rot_dim/2
     + j)``, or ``(2j, 2j+1)`` when ``interleaved``.  ``gradient=True`` takes
     the output's gradient to the input's.  ``out`` may be ``x``."""
-    shape, src = _heads(x, "x")
-    dtype = _DTYPES.get(x.dtype)
-    if dtype is None:
-        raise ValueError("x must be float32, bfloat16 or float16")
-    tokens, heads, dim = shape
-    pos, p64, freq, f64, rot = _rotation(positions, inv_freq, tokens)
     if out is None:
-        out = _new(shape, x.dtype, x.device, stream)
-    out_shape, dst = _heads(out, "out", x.dtype)
-    if out_shape != shape:
-        raise ValueError("out must have x's shape")
-    _serving("pml_rope", stream, *src, *dst, dtype, pos, p64, freq, f64, rot, rot_offset,
-             int(interleaved), mscale, int(gradient), tokens, heads, dim)
+        out = _new(x.shape, x.dtype, x.device, stream)
+    _serving("rope", x, positions, inv_freq, out, rot_offset, interleaved, mscale, gradient, stream)
     return out
 
 
@@ -585,31 +513,10 @@ def pml_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions
     ``positions[t] % 64`` of page ``block_table[requests[t], positions[t] // 64]``
     of their caches ``[pages, 64, kv_heads, dim]`` (any strides).  bf16 or
     fp16; a negative request or position makes the token padding."""
-    dtype = q.dtype
-    shape, qa = _heads(q, "q")
-    if dtype not in _HALVES:
-        raise ValueError("q must be bfloat16 or float16")
-    k_shape, ka = _heads(k, "k", dtype)
-    v_shape, va = _heads(v, "v", dtype)
-    tokens, heads, dim = shape
-    kv_heads = k_shape[1]
-    if v_shape != k_shape or k_shape[0] != tokens or k_shape[2] != dim:
-        raise ValueError("k and v must be [tokens, kv_heads, dim] with q's tokens and dim")
-    pos, p64, freq, f64, rot = _rotation(positions, inv_freq, tokens)
-    req = _ints(requests, "requests", tokens)
-    (rows, width), table, bt_stride = _table(block_table)
-    c_shape, kc = _cache(k_cache, "k_cache", dtype)
-    vc_shape, vc = _cache(v_cache, "v_cache", dtype)
-    if c_shape != vc_shape or c_shape[2] != kv_heads or c_shape[3] != dim:
-        raise ValueError("k_cache and v_cache must be [pages, 64, kv_heads, dim]")
     if q_out is None:
-        q_out = _new(shape, dtype, q.device, stream)
-    out_shape, qo = _heads(q_out, "q_out", dtype)
-    if out_shape != shape:
-        raise ValueError("q_out must have q's shape")
-    _serving("pml_rope_append", stream, *qa, *qo, *ka, *va, _DTYPES[dtype], pos, p64, req, rows, freq,
-             f64, rot, rot_offset, int(interleaved), mscale, *kc, *vc, c_shape[0], table, bt_stride,
-             width, tokens, heads, kv_heads, dim)
+        q_out = _new(q.shape, q.dtype, q.device, stream)
+    _serving("rope_append", q, k, v, positions, requests, inv_freq, k_cache, v_cache, block_table, q_out,
+             rot_offset, interleaved, mscale, stream)
     return q_out
 
 
@@ -625,76 +532,13 @@ def pml_index_quant_append(q: torch.Tensor, k: torch.Tensor | None, weights: tor
     ``w_out = weights * scale * weight_scale``; k bf16 ``[tokens, 128]``
     rotated, quantised and written with its scale into ``kv_fused`` uint8
     ``[blocks, 8448]`` (``k=None``: no keys).  Returns ``(q_out, w_out)``."""
-    shape, qa = _heads(q, "q", torch.bfloat16)
-    tokens, heads, dim = shape
-    if dim != 128:
-        raise ValueError("q must be bf16 [tokens, heads, 128]")
-    pos, p64, freq, f64, rot = _rotation(positions, inv_freq, tokens)
-    if weights.dtype is not torch.float32 or weights.shape != (tokens, heads):
-        raise ValueError("weights must be float32 [tokens, heads]")
-    _cuda(weights, "weights")
-    blocks = rows = width = bt_stride = k_stride = 0
-    ka = req = kv = table = None
-    if k is not None:
-        if not k.is_cuda or k.dtype is not torch.bfloat16 or k.shape != (tokens, 128) or k.stride(1) != 1:
-            raise ValueError("k must be a CUDA bf16 [tokens, 128] tensor with unit last stride")
-        if requests is None or kv_fused is None or block_table is None:
-            raise ValueError("keys need requests, kv_fused and block_table")
-        req = _ints(requests, "requests", tokens)
-        (rows, width), table, bt_stride = _table(block_table)
-        _cuda(kv_fused, "kv_fused")
-        blocks, rest = divmod(kv_fused.numel(), 8448)
-        if kv_fused.dtype is not torch.uint8 or rest:
-            raise ValueError("kv_fused must be uint8 and hold whole 8448-byte blocks")
-        ka, k_stride, kv = k.data_ptr(), k.stride(0), kv_fused.data_ptr()
     if q_out is None:
-        q_out = _new(shape, torch.float8_e4m3fn, q.device, stream)
+        q_out = _new(q.shape, torch.float8_e4m3fn, q.device, stream)
     if w_out is None:
-        w_out = _new((tokens, heads), torch.float32, q.device, stream)
-    if q_out.shape != shape or q_out.element_size() != 1 or w_out.shape != (tokens, heads) or \
-            w_out.dtype is not torch.float32:
-        raise ValueError("q_out must be 1-byte [tokens, heads, 128], w_out float32 [tokens, heads]")
-    _cuda(q_out, "q_out")
-    _cuda(w_out, "w_out")
-    _serving("pml_index_quant_append", stream, *qa, ka, k_stride, weights.data_ptr(), weight_scale, pos,
-             p64, req, rows, freq, f64, rot, rot_offset, int(interleaved), mscale, q_out.data_ptr(),
-             w_out.data_ptr(), kv, blocks, table, bt_stride, width, tokens, heads)
+        w_out = _new(q.shape[:2], torch.float32, q.device, stream)
+    _serving("index_quant_append", q, k, weights, positions, requests, inv_freq, kv_fused, block_table,
+             q_out, w_out, weight_scale, rot_offset, interleaved, mscale, stream)
     return q_out, w_out
-
-
-def _attention(q, k_cache, v_cache, block_table, kv_lens, out, lse, workspace, softmax_scale, stream):
-    """The checks that both attention calls share; their arguments in three runs."""
-    dtype = q.dtype
-    shape, qa = _heads(q, "q")
-    if dtype not in _HALVES:
-        raise ValueError("q must be bfloat16 or float16")
-    tokens, heads, dim = shape
-    c_shape, kc = _cache(k_cache, "k_cache", dtype)
-    v_shape, vc = _cache(v_cache, "v_cache", dtype)
-    if c_shape != v_shape or c_shape[3] != dim:
-        raise ValueError("k_cache and v_cache must be [pages, 64, kv_heads, dim] with q's dim")
-    (rows, width), table, bt_stride = _table(block_table)
-    lens = _ints(kv_lens, "kv_lens", rows)
-    if out is None:
-        out = _new(shape, dtype, q.device, stream)
-    out_shape, oa = _heads(out, "out", dtype)
-    if out_shape != shape:
-        raise ValueError("out must have q's shape")
-    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != shape[:2]
-                            or not lse.is_contiguous() or not lse.is_cuda):
-        raise ValueError("lse must be a contiguous CUDA float32 [tokens, heads] tensor")
-    if workspace is None:
-        workspace = pml_attention_workspace(dim, q.device, stream)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
-    if softmax_scale is None:
-        softmax_scale = dim ** -0.5
-    # (a workspace of the call's own goes back to its allocator when the call
-    # returns: what takes its memory next on the stream runs after the kernels)
-    return (out, rows, (*qa, *kc, *vc, _DTYPES[dtype], c_shape[0], table, bt_stride, width, lens),
-            (tokens, heads, c_shape[2], dim, softmax_scale),
-            (*oa, _addr(lse), workspace.data_ptr(), workspace.numel() * workspace.element_size()),
-            workspace)
 
 
 def pml_attention_workspace(head_dim: int, device=None, stream=None) -> torch.Tensor:
@@ -727,14 +571,10 @@ def pml_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     already in its pages.  ``window > 0``: only keys past position - window.
     ``lse`` receives the logarithms of the rows' sums.  ``softmax_scale``
     defaults to ``dim ** -0.5``."""
-    out, batch, kv, size, tail, workspace = _attention(q, k_cache, v_cache, block_table, kv_lens, out, lse,
-                                                       workspace, softmax_scale, stream)
-    starts = None
-    if cu_q is not None:
-        starts = _ints(cu_q, "cu_q", batch + 1)
-    elif batch == 0 or size[0] % batch != 0:
-        raise ValueError("without cu_q the tokens must divide equally over the requests")
-    _serving("pml_paged_attention", stream, *kv, starts, batch, *size, int(causal), window, *tail)
+    if out is None:
+        out = _new(q.shape, q.dtype, q.device, stream)
+    _serving("paged_attention", q, k_cache, v_cache, block_table, kv_lens, cu_q, out, softmax_scale, causal,
+             window, lse, workspace, stream)
     return out
 
 
@@ -746,20 +586,11 @@ def pml_sparse_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     """Attention of each token over the positions ``selected[t]`` (int32
     ``[tokens, k]``, as ``pml_topk_logits`` leaves them; entries below 0 or
     past the request's length are not there) of request ``requests[t]``."""
-    out, rows, kv, size, tail, workspace = _attention(q, k_cache, v_cache, block_table, kv_lens, out, lse,
-                                                      workspace, softmax_scale, stream)
-    req = _ints(requests, "requests", size[0])
-    (tokens, k), sel, sel_stride = _table(selected, "selected")
-    if tokens != size[0]:
-        raise ValueError("selected must hold a row per token")
-    _serving("pml_sparse_attention", stream, *kv, req, rows, sel, sel_stride, k, *size, *tail)
+    if out is None:
+        out = _new(q.shape, q.dtype, q.device, stream)
+    _serving("sparse_attention", q, k_cache, v_cache, block_table, kv_lens, requests, selected, out,
+             softmax_scale, lse, workspace, stream)
     return out
-
-
-def _pool(ref_counts, block_table, seq_lens):
-    refs = _ints(ref_counts, "ref_counts")
-    (rows, width), table, bt_stride = _table(block_table)
-    return refs, ref_counts.numel(), table, bt_stride, width, _ints(seq_lens, "seq_lens", rows), rows
 
 
 def pml_pages_fork(ref_counts: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -769,11 +600,8 @@ def pml_pages_fork(ref_counts: torch.Tensor, block_table: torch.Tensor, seq_lens
     a part-full last page replaced by the lowest free page and listed in
     ``copy_src`` / ``copy_dst`` / ``copy_count`` for ``pml_pages_copy``.  All
     int32, updated in place."""
-    pool = _pool(ref_counts, block_table, seq_lens)
-    n = parents.numel()
-    _serving("pml_pages_fork", stream, *pool, _ints(parents, "parents"), _ints(children, "children", n), n,
-             _ints(copy_src, "copy_src", n), _ints(copy_dst, "copy_dst", n),
-             _ints(copy_count, "copy_count", 1))
+    _serving("pages_fork", ref_counts, block_table, seq_lens, parents, children, copy_src, copy_dst,
+             copy_count, stream)
 
 
 def pml_pages_extend(ref_counts: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -781,16 +609,13 @@ def pml_pages_extend(ref_counts: torch.Tensor, block_table: torch.Tensor, seq_le
                      stream=None) -> None:
     """Grows every row to ``new_lens`` tokens with the lowest free pages, in
     (row, page) order; the pages taken are listed in ``new_pages``."""
-    pool = _pool(ref_counts, block_table, seq_lens)
-    _serving("pml_pages_extend", stream, *pool, _ints(new_lens, "new_lens", pool[-1]),
-             _ints(new_pages, "new_pages"), new_pages.numel(), _ints(new_count, "new_count", 1))
+    _serving("pages_extend", ref_counts, block_table, seq_lens, new_lens, new_pages, new_count, stream)
 
 
 def pml_pages_free(ref_counts: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
                    rows: torch.Tensor, stream=None) -> None:
     """The listed rows (distinct) give back their pages; their length becomes 0."""
-    pool = _pool(ref_counts, block_table, seq_lens)
-    _serving("pml_pages_free", stream, *pool, _ints(rows, "rows"), rows.numel())
+    _serving("pages_free", ref_counts, block_table, seq_lens, rows, stream)
 
 
 def pml_pages_compact(ref_counts: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -801,14 +626,8 @@ def pml_pages_compact(ref_counts: torch.Tensor, block_table: torch.Tensor, seq_l
     may be the inputs), ``remap`` of every page, and the moves listed for
     ``pml_pages_copy`` (``copy_src`` / ``copy_dst`` of ``num_pages // 2`` or
     more entries)."""
-    pool = _pool(ref_counts, block_table, seq_lens)
-    shape, table_out, out_stride = _table(block_table_out, "block_table_out")
-    if shape != block_table.shape:
-        raise ValueError("block_table_out must have block_table's shape")
-    n = copy_src.numel()
-    _serving("pml_pages_compact", stream, *pool, _ints(ref_counts_out, "ref_counts_out", pool[1]),
-             table_out, out_stride, _ints(remap, "remap", pool[1]), _ints(copy_src, "copy_src"),
-             _ints(copy_dst, "copy_dst", n), n, _ints(copy_count, "copy_count", 1))
+    _serving("pages_compact", ref_counts, block_table, seq_lens, ref_counts_out, block_table_out, remap,
+             copy_src, copy_dst, copy_count, stream)
 
 
 def pml_pages_copy(cache: torch.Tensor, copy_src: torch.Tensor, copy_dst: torch.Tensor,
@@ -816,20 +635,7 @@ def pml_pages_copy(cache: torch.Tensor, copy_src: torch.Tensor, copy_dst: torch.
     """Copies page ``copy_src[i]`` over page ``copy_dst[i]`` for ``i <
     copy_count`` in every layer of ``cache`` ``[layers, pages, ...]``
     (``layers=False``: ``[pages, ...]``); each page is contiguous."""
-    shape, strides = cache.shape, cache.stride()
-    at = 1 if layers else 0
-    if not cache.is_cuda or len(shape) <= at:
-        raise ValueError("cache must be a CUDA tensor [layers, pages, ...] or [pages, ...]")
-    elems = 1
-    for size, step in zip(shape[:at:-1], strides[:at:-1]):
-        if size > 1 and step != elems:
-            raise ValueError("each page of the cache must be contiguous")
-        elems *= size
-    b = cache.element_size()
-    n = copy_src.numel()
-    _serving("pml_pages_copy", stream, cache.data_ptr(), shape[0] if layers else 1,
-             strides[0] * b if layers else 0, shape[at], strides[at] * b, elems * b,
-             _ints(copy_src, "copy_src"), _ints(copy_dst, "copy_dst", n), _ints(copy_count, "copy_count", 1), n)
+    _serving("pages_copy", cache, copy_src, copy_dst, copy_count, layers, stream)
 
 
 # ---------------------------------------------------------------- pages' keyword style

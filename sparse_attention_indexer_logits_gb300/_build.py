@@ -1,12 +1,18 @@
 """Build libpml.so in-tree: every CUDA translation unit under csrc/ compiled
 for sm_103a in parallel, then linked into one shared library next to this
-file.  Rebuilds only when a source, header or flag changed."""
+file; beside them the Python module _calls (csrc/binding.cpp), against this
+interpreter's PyTorch.  Rebuilds only when a source, header, flag or one of
+the two changed."""
 from __future__ import annotations
 
 import hashlib
 import os
+import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
+
+import torch
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -14,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libpml.so")
+CALLS_PATH = os.path.join(PKG, "_calls.so")
 
 SOURCES = ["api.cu", "schedule.cu", "fp8_logits.cu", "fp8_logits_h8.cu", "fp8_logits_h16.cu",
            "fp8_logits_h32.cu", "fp8_logits_h64.cu", "bf16_scores.cu", "nvfp4_scores.cu",
@@ -37,11 +44,28 @@ def _fingerprint(extra_flags) -> str:
     h = hashlib.sha256()
     for d in (CSRC, INCLUDE):
         for name in sorted(os.listdir(d)):
-            if name.endswith((".cu", ".cuh", ".h")):
+            if name.endswith((".cu", ".cuh", ".h", ".cpp")):
                 with open(os.path.join(d, name), "rb") as f:
                     h.update(name.encode() + f.read())
     h.update(" ".join(NVCC_FLAGS + list(extra_flags)).encode())
+    h.update(f"{sysconfig.get_config_var('SOABI')} {torch.__version__}".encode())
     return h.hexdigest()
+
+
+def _build_calls(nvcc: str) -> None:
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(nvcc) or nvcc)))
+    tmp = CALLS_PATH + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-I", INCLUDE,
+           "-isystem", sysconfig.get_path("include"), "-isystem", os.path.join(home, "include"),
+           "-isystem", os.path.join(cuda, "include"), "-L", os.path.join(home, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS_PATH)
 
 
 def build(force: bool = False, extra_flags=(), verbose: bool = False) -> str:
@@ -49,7 +73,7 @@ def build(force: bool = False, extra_flags=(), verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     stamp = os.path.join(BUILD_DIR, "stamp")
     fp = _fingerprint(extra_flags)
-    if not force and os.path.exists(LIB_PATH) and os.path.exists(stamp):
+    if not force and os.path.exists(LIB_PATH) and os.path.exists(CALLS_PATH) and os.path.exists(stamp):
         with open(stamp) as f:
             if f.read().strip() == fp:
                 return LIB_PATH
@@ -68,8 +92,10 @@ def build(force: bool = False, extra_flags=(), verbose: bool = False) -> str:
             print(r.stdout + r.stderr, flush=True)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        calls = ex.submit(_build_calls, nvcc)
         objs = list(ex.map(compile_one, SOURCES))
+        calls.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [nvcc, "-shared", "-gencode", "arch=compute_103a,code=sm_103a", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
