@@ -15,9 +15,10 @@
 // longer scan per pass.  The page copies are bound by memory and run on the
 // whole GPU.
 //
-// Measured: forking 160 requests of up to 8192 tokens 12 us, freeing them 9 us
-// (each alone); the compaction plan of 64 requests' pages 18 us; copying 544 MB of pages
-// 166 us, 6.55 TB/s of read and write, 97 % of a plain copy's 6776 GB/s.
+// Measured: forking 160 requests of up to 8192 tokens 10.5 us, freeing them 4.3
+// (a warp per request: 9); the compaction plan of 64 requests' pages 14 us (its
+// tables a warp per row: 19); copying 544 MB of pages 166 us, 6.55 TB/s of read
+// and write, 97 % of a plain copy's 6776 GB/s.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -34,6 +35,7 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCtas = 8;
+constexpr int kAhead = 4;     // table entries that a lane loads at once
 constexpr unsigned int kStatusNoPages = 16u;     // PML_STATUS_NO_PAGES
 
 // Exclusive prefix of v over the CTA, and the total; two barriers.
@@ -200,12 +202,6 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
                 if (lane == 0) P.seq_lens[child] = 0;
                 continue;
             }
-            for (int c = lane; c < full; c += 32) {
-                const int p = from[c];
-                to[c] = p;
-                if (p >= 0 && p < P.num_pages) atomicAdd(P.ref_counts + p, 1);
-                else atomicOr(P.status, kStatusBadBlock);
-            }
             if (lane == 0) {
                 if (own_page) {
                     const int p = a.dst[r];
@@ -214,6 +210,19 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
                     P.ref_counts[p] = 1;
                 }
                 P.seq_lens[child] = max(len, 0);
+            }
+            // (several loads on their way at once: each takes longer than the rest)
+            for (int c0 = lane; c0 < full; c0 += 32 * kAhead) {
+                int p[kAhead];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) p[k] = c0 + 32 * k < full ? from[c0 + 32 * k] : -1;
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    if (c0 + 32 * k >= full) break;
+                    to[c0 + 32 * k] = p[k];
+                    if (p[k] >= 0 && p[k] < P.num_pages) atomicAdd(P.ref_counts + p[k], 1);
+                    else atomicOr(P.status, kStatusBadBlock);
+                }
             }
         }
         __syncthreads();
@@ -309,25 +318,26 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
 
 // ------------------------------------------------------------------ free
 
-__global__ void __launch_bounds__(256) pages_free_kernel(const FreeArgs a)
+constexpr int kFreeThreads = 128;
+
+// A CTA per request, a thread per page: one load and one atomic deep up to
+// 128 pages.
+__global__ void __launch_bounds__(kFreeThreads) pages_free_kernel(const FreeArgs a)
 {
     allow_dependent_launch();
     grid_dependency_wait();
     const PoolArgs& P = a.pool;
-    const int lane = threadIdx.x & 31;
-    const int i = (int)((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
-    if (i >= a.n) return;
-    const int row = __ldg(a.list + i);
+    const int row = __ldg(a.list + blockIdx.x);
     if (row < 0 || row >= P.rows) {
-        if (lane == 0) atomicOr(P.status, kStatusBadRequest);
+        if (threadIdx.x == 0) atomicOr(P.status, kStatusBadRequest);
         return;
     }
     int n = pages_of(P.seq_lens[row]);
     if (n > P.bt_width) {
-        if (lane == 0) atomicOr(P.status, kStatusBadBlock);
+        if (threadIdx.x == 0) atomicOr(P.status, kStatusBadBlock);
         n = P.bt_width;
     }
-    for (int c = lane; c < n; c += 32) {
+    for (int c = threadIdx.x; c < n; c += kFreeThreads) {
         const int p = P.block_table[(long long)row * P.bt_stride + c];
         bool bad = p < 0 || p >= P.num_pages;
         if (!bad && atomicSub(P.ref_counts + p, 1) <= 0) {   // nobody held it: put it back
@@ -336,8 +346,8 @@ __global__ void __launch_bounds__(256) pages_free_kernel(const FreeArgs a)
         }
         if (bad) atomicOr(P.status, kStatusBadBlock);
     }
-    __syncwarp();
-    if (lane == 0) P.seq_lens[row] = 0;
+    __syncthreads();
+    if (threadIdx.x == 0) P.seq_lens[row] = 0;
 }
 
 // ------------------------------------------------------------------ compact
@@ -396,20 +406,31 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     }
     __threadfence();
     cl.sync();
-    // the tables, a warp per row
-    const int lane = threadIdx.x & 31;
-    for (int row = cluster_thread >> 5; row < P.rows; row += kStride >> 5) {
-        const int n = min(pages_of(P.seq_lens[row]), P.bt_width);
-        const int32_t* from = P.block_table + (long long)row * P.bt_stride;
-        int32_t* to = a.block_table_out + (long long)row * a.bt_out_stride;
-        for (int c = lane; c < P.bt_width; c += 32) {
-            int p = from[c];
-            if (c < n) {
-                if (p >= 0 && p < P.num_pages) p = a.remap[p];
-                else atomicOr(P.status, kStatusBadBlock);
-            }
-            to[c] = p;
+    // the tables, an entry per thread, a few on their way at once
+    const long long entries = (long long)P.rows * P.bt_width;
+    for (long long e0 = cluster_thread; e0 < entries; e0 += (long long)kStride * kAhead) {
+        int p[kAhead], at[kAhead], row[kAhead];
+        bool used[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            used[k] = false;
+            if (e0 + (long long)k * kStride >= entries) continue;
+            const int e = (int)(e0 + (long long)k * kStride);
+            row[k] = e / P.bt_width;
+            at[k] = e - row[k] * P.bt_width;
+            p[k] = P.block_table[row[k] * P.bt_stride + at[k]];
+            used[k] = at[k] < pages_of(P.seq_lens[row[k]]);
         }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const bool there = p[k] >= 0 && p[k] < P.num_pages;
+            if (used[k] && there) p[k] = a.remap[p[k]];
+            else if (used[k]) atomicOr(P.status, kStatusBadBlock);
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (e0 + (long long)k * kStride < entries)
+                a.block_table_out[row[k] * a.bt_out_stride + at[k]] = p[k];
     }
 }
 
@@ -487,8 +508,7 @@ cudaError_t launch_pages_extend(const ExtendArgs& a, cudaStream_t stream)
 
 cudaError_t launch_pages_free(const FreeArgs& a, cudaStream_t stream)
 {
-    const unsigned blocks = ((unsigned)a.n + 7) / 8;
-    return launch_dependent(pages_free_kernel, dim3(blocks), 256, 0, stream, a);
+    return launch_dependent(pages_free_kernel, dim3((unsigned)a.n), kFreeThreads, 0, stream, a);
 }
 
 cudaError_t launch_pages_compact(const CompactArgs& a, cudaStream_t stream)
