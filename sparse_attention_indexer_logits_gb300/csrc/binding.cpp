@@ -20,6 +20,7 @@
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "pml.h"
@@ -34,7 +35,9 @@ namespace {
     X(pml_pages_fork) X(pml_pages_extend) X(pml_pages_free) X(pml_pages_compact) X(pml_pages_copy)
 
 #define PML_MEMBER(name) decltype(&::name) name = nullptr;
-struct Library { PML_CALLS(PML_MEMBER) } pml;
+struct Library {
+    PML_CALLS(PML_MEMBER)
+} pml;
 
 // ------------------------------------------------------------------ arguments
 
@@ -555,8 +558,9 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n)
         return F(args);
     } catch (const Refused&) {
         return nullptr;
-    } catch (const std::exception& e) {
-        return PyErr_Format(PyExc_RuntimeError, "%s", e.what());
+    } catch (const std::exception&) {    // (the allocator's, with PyTorch's own types)
+        torch::translate_exception_to_python(std::current_exception());
+        return nullptr;
     }
 }
 
