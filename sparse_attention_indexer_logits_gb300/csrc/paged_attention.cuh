@@ -1266,7 +1266,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (alt) {
                 // both halves hold these rows: they join, and group h writes
                 // columns h D / 2 .. of the result
-                stats[h * 128 + row] = make_float2(m, l);
+                // (A group without a tile, h = 1 where n = 1, leaves nothing: it may
+                // be here while the other one still reads what it left for the item
+                // before.  One that had a tile has seen its product end, which
+                // began after both groups' ends of that item.)
+                if (tiles_here > 0) stats[h * 128 + row] = make_float2(m, l);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(altbar);
@@ -1274,7 +1278,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 ++alt_phase;
                 tc_fence_after();
-                const float2 s0 = stats[row], s1 = stats[128 + row];
+                const float2 s0 = stats[row];
+                const float2 s1 = n > 1 ? stats[128 + row] : make_float2(-INFINITY, 0.0f);
                 top = fmaxf(s0.x, s1.x);
                 g0 = s0.x == -INFINITY ? 0.0f : exp2_approx((s0.x - top) * c);
                 g1 = s1.x == -INFINITY ? 0.0f : exp2_approx((s1.x - top) * c);

@@ -1,0 +1,56 @@
+"""Attention over pages where the items of a CTA's range follow each other in
+ways that its groups have to keep apart."""
+import pytest
+import torch
+
+import sparse_attention_indexer_logits_gb300 as pml
+from tests import serving_ref as R
+from tests.test_attention_gpu import BF, FP, Problem, check, check_selected
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _build():
+    import __graft_entry__
+    __graft_entry__.build()
+    pml.pml_device_status(clear=True)
+    yield
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, BF), (128, FP)])
+def test_items_of_one_tile_after_longer_ones(dim, dtype):
+    """One tile leaves a half without work: it comes to that item's end while
+    the other half may be at the end of the item before."""
+    g = R.gen(31)
+    short, longer = torch.randint(1, 129, (700,), generator=g), torch.randint(129, 600, (700,), generator=g)
+    kvn = torch.stack([longer, short], 1).flatten().tolist()
+    p = Problem([1] * len(kvn), kvn, 4, 2, dim, dtype, seed=32).stale()
+    out, lse = p.run(cu=False)
+    check(p, out, lse, requests=range(0, len(kvn), 61))
+    q, k, v, table, lens = p.device()
+    for _ in range(20):
+        again = torch.full_like(lse, 77.0)
+        assert torch.equal(pml.pml_paged_attention(q, k, v, table, lens, lse=again), out)
+        assert torch.equal(again, lse)
+
+
+@pytest.mark.parametrize("k", [100, 300])
+def test_lists_of_a_prompt(k):
+    """A list for every token of a prompt: several items a CTA, of one tile and
+    of more, some cut between CTAs."""
+    g = R.gen(k)
+    kvn, tokens = [900, 260], 900
+    p = Problem([1, 1], kvn, 64, 1, 64, BF, seed=33).stale()
+    p.q = (torch.randn((tokens, 64, 64), generator=g) * 1.5).to(BF)
+    req = torch.randint(0, 2, (tokens,), generator=g, dtype=torch.int32)
+    sel = torch.randint(-50, 900, (tokens, k), generator=g, dtype=torch.int32)
+    q, kc, vc, table, lens = p.device()
+    lse = torch.empty((tokens, 64), device="cuda")
+    out = pml.pml_sparse_attention(q, kc, vc, table, lens, req.cuda(), sel.cuda(), lse=lse)
+    assert pml.pml_device_status(clear=True) == 0
+    at = list(range(0, tokens, 37))
+    p.q = p.q[at]
+    check_selected(p, req[at], sel[at], out[at], lse[at])
+    for _ in range(10):
+        assert torch.equal(pml.pml_sparse_attention(q, kc, vc, table, lens, req.cuda(), sel.cuda()), out)
