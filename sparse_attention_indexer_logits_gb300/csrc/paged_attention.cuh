@@ -1205,7 +1205,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const volatile int* v4 = votes + (h * 2 + par) * 4;
                         if (v4[0] | v4[1] | v4[2] | v4[3]) {
                             // this tile's product, row by row over the keys it
-                            // may see (P as the tensor core would read it)
+                            // may see (P as the tensor core would read it).  O
+                            // is this item's once both groups have read the
+                            // last one's, which the issuer waits for before its
+                            // own first product
+                            if (i == 0) {
+                                ok = warp_wait(oempty, (uint32_t)(item & 1) ^ 1u, abort_flag, a.status);
+                                if (!ok) break;
+                                tc_fence_after();
+                            }
                             if (active) {
                                 const int lo = row_lo - key0, hi = row_hi - key0;
 #pragma unroll 1

@@ -1,5 +1,7 @@
 """Attention over pages where the items of a CTA's range follow each other in
 ways that its groups have to keep apart."""
+import math
+
 import pytest
 import torch
 
@@ -54,3 +56,21 @@ def test_lists_of_a_prompt(k):
     check_selected(p, req[at], sel[at], out[at], lse[at])
     for _ in range(10):
         assert torch.equal(pml.pml_sparse_attention(q, kc, vc, table, lens, req.cuda(), sel.cuda()), out)
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, FP), (128, BF)])
+def test_infinities_in_the_first_tile_of_every_item(dim, dtype):
+    """Two new tokens, the last one's values infinite: the first token must not
+    see them, so each item's product is added row by row, right after the item
+    before has ended."""
+    g = R.gen(34)
+    kvn = torch.randint(2, 260, (900,), generator=g).tolist()
+    p = Problem([2] * len(kvn), kvn, 4, 2, dim, dtype, seed=35).stale()
+    for b, n in enumerate(kvn):
+        p.v[p.table[b, (n - 1) // 64].long(), (n - 1) % 64, :, b % dim] = math.inf
+    out, lse = p.run(cu=False)
+    check(p, out, lse, requests=range(0, len(kvn), 71))
+    assert torch.isfinite(out[::2]).all()
+    q, k, v, table, lens = p.device()
+    for _ in range(20):
+        assert torch.equal(pml.pml_paged_attention(q, k, v, table, lens), out)
