@@ -66,6 +66,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "attention_work.cuh"
 #include "common.cuh"
 #include "dependent.cuh"
 #include "ptx.cuh"
@@ -298,41 +299,6 @@ __device__ __forceinline__ bool not_finite(uint32_t w)
     return (((w & kExp) + kOne) & 0x80008000u) != 0;
 }
 
-// The tokens and tiles of tile `tile` of a request with nq new tokens of kv.
-struct Span {
-    int t0, ntok;    // tokens of the request
-    int lo, hi;      // keys that some row of the tile may see
-    int j0, n;       // their tiles of 128 keys; at least one
-    int cost;        // units of a tile
-};
-
-__device__ __forceinline__ Span tile_span(const AttnArgs& a, int nq, int kv, int tile)
-{
-    Span s;
-    const int per = 2 * a.half_tokens;
-    s.t0 = tile * per;
-    s.ntok = min(per, nq - s.t0);
-    const int there = (int)min((long long)kv, (long long)a.bt_width * kBlockKeys);
-    const long long pos0 = (long long)kv - nq + s.t0;      // position of the tile's first token
-    long long hi = there;
-    if (a.causal) hi = min(hi, pos0 + s.ntok);
-    long long lo = 0;
-    if (a.window > 0) lo = max(lo, pos0 - a.window + 1);
-    if (hi <= lo) { hi = 0; lo = 0; }
-    s.lo = (int)lo;
-    s.hi = (int)hi;
-    s.j0 = s.lo / kAttnTileKeys;
-    s.n = max(1, (s.hi + kAttnTileKeys - 1) / kAttnTileKeys - s.j0);
-    s.cost = s.ntok <= a.half_tokens ? 1 : 2;
-    return s;
-}
-
-__device__ __forceinline__ int tiles_of(const AttnArgs& a, int nq)
-{
-    const int per = 2 * a.half_tokens;
-    return (nq + per - 1) / per;
-}
-
 __device__ __forceinline__ void request_of(const AttnArgs& a, int b, int& tok0, int& nq, int& kv)
 {
     if (a.cu_q != nullptr) {
@@ -346,21 +312,6 @@ __device__ __forceinline__ void request_of(const AttnArgs& a, int b, int& tok0, 
     kv = max(__ldg(a.kv_lens + b), 0);
 }
 
-// Units of work.  A tile is one where the halves take the tiles in turn and two
-// where both see it (1800 and 3600 cycles), and beginning and ending an item
-// (Q's way in, the first copies, the output) is three.  A mixed batch of 24
-// requests takes 51.7 us (captured in a graph), with two or six units an item
-// 54.5 or 52.3; 64 tokens of 2048 listed positions 26.5 us, with two, four or
-// six 26.4, 28.8 or 30.0.  A range has the tiles whose first unit lies in it.
-constexpr int kItemUnits = 3;
-
-__device__ __forceinline__ int units_of(const Span& s) { return s.n * s.cost + kItemUnits; }
-__device__ __forceinline__ int tiles_before(const Span& s, int unit)
-{
-    const int u = max(0, unit - kItemUnits);
-    return s.cost == 1 ? u : (u + 1) >> 1;
-}
-
 // Where a CTA's range begins, and how many units it has.
 struct Start {
     int b, head, tile;   // selected: b is the token
@@ -368,20 +319,17 @@ struct Start {
     long long left;
 };
 
-// Executed by one warp.  `units`: shared memory for one int per request.
-__device__ __forceinline__ Start find_start(const AttnArgs& a, int* units, int lane)
+// Executed by one warp.  `units`: shared memory for one number per request.
+__device__ __forceinline__ Start find_start(const AttnArgs& a, long long* units, int lane)
 {
     Start s = {0, 0, 0, 0, 0};
     long long total = 0;
 #pragma unroll 1
     for (int b = lane; b < a.batch; b += 32) {
-        int tok0, nq, kv, u = 0;
+        int tok0, nq, kv;
         request_of(a, b, tok0, nq, kv);
-        const int tiles = tiles_of(a, nq);
-#pragma unroll 1
-        for (int i = 0; i < tiles; ++i) u += units_of(tile_span(a, nq, kv, i));
-        units[b] = u;
-        total += u;
+        units[b] = units_of_request(a, nq, kv);
+        total += units[b];
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -390,11 +338,11 @@ __device__ __forceinline__ Start find_start(const AttnArgs& a, int* units, int l
     s.left = range_start(total, gridDim.x, blockIdx.x + 1) - rem;
     if (s.left == 0) return s;
     // the request that holds unit `rem`, 32 at a time
-    int per_head = 0;
+    long long per_head = 0;
 #pragma unroll 1
     for (int c = 0; c < a.batch; c += 32) {
-        const int v = c + lane < a.batch ? units[c + lane] : 0;
-        long long incl = (long long)v * a.kv_heads;
+        const long long v = c + lane < a.batch ? units[c + lane] : 0;
+        long long incl = v * a.kv_heads;
         const long long mine = incl;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -413,7 +361,7 @@ __device__ __forceinline__ Start find_start(const AttnArgs& a, int* units, int l
     }
     if (per_head == 0) { s.left = 0; return s; }    // never
     s.head = (int)(rem / per_head);
-    int off = (int)(rem - (long long)s.head * per_head);
+    long long off = rem - s.head * per_head;
     // the tile of that request's head, 32 at a time
     int tok0, nq, kv;
     request_of(a, s.b, tok0, nq, kv);
@@ -431,7 +379,7 @@ __device__ __forceinline__ Start find_start(const AttnArgs& a, int* units, int l
         if (who) {
             const int l = __ffs(who) - 1;
             s.tile = c + l;
-            s.at = off - __shfl_sync(0xffffffffu, incl - v, l);
+            s.at = (int)(off - __shfl_sync(0xffffffffu, incl - v, l));
             break;
         }
         off -= __shfl_sync(0xffffffffu, incl, 31);
@@ -531,7 +479,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
             // units per request in the ring's memory, which nobody else
             // touches before the copies begin
-            start = find_start(a, reinterpret_cast<int*>(smem + C::kRing), lane);
+            static_assert(kAttnMaxBatch * 8 <= C::kStages * C::kStageBytes, "a number per request fits the ring");
+            start = find_start(a, reinterpret_cast<long long*>(smem + C::kRing), lane);
             __syncwarp();
             fence_proxy_async_smem();
         }
