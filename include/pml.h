@@ -517,7 +517,8 @@ int pml_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
  * all of its token's entries absent (out 0, lse -inf), one at or past
  * num_requests does too and sets PML_STATUS_BAD_REQUEST.
  *
- * selected     int32 [tokens, selected_stride], k entries used
+ * selected     int32 [tokens, selected_stride], k entries used (at most 2^31 -
+ *              256)
  * The rest as in pml_paged_attention.
  */
 int pml_sparse_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,

@@ -13,7 +13,7 @@ namespace {
 using namespace pml;
 
 constexpr int kMaxRopeDim = 512;
-constexpr int kNoWindow = 1 << 30;     // a window past every position; positions plus it fit an int
+constexpr int kMaxListed = 0x7fffff00; // entries of a list, so that their tiles' ends fit an int
 constexpr int kRopeMaxRows = 32768;    // of a token: the kernels divide by it in fp32
 
 int check_rotary(const void* positions, const void* inv_freq, int positions_64, int freq_64,
@@ -509,7 +509,7 @@ int pml_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
     a.q_per_request = batch > 0 ? tokens / batch : 0;
     a.batch = batch;
     a.causal = causal ? 1 : 0;
-    a.window = window < kNoWindow ? window : kNoWindow;
+    a.window = window;
     return attention_call(a, q, q_token_stride, q_head_stride, k_cache, k_page_stride, k_slot_stride,
                           k_head_stride, v_cache, v_page_stride, v_slot_stride, v_head_stride, dtype,
                           num_pages, block_table, bt_stride, bt_width, kv_lens, tokens, num_heads,
@@ -529,6 +529,7 @@ int pml_sparse_attention(const void* q, int64_t q_token_stride, int64_t q_head_s
                          void* workspace, int64_t workspace_bytes, void* stream)
 {
     if (k < 1 || selected_stride < k || num_requests < 1) return PML_ERR_INVALID_ARG;
+    if (k > kMaxListed) return PML_ERR_UNSUPPORTED;
     if (tokens > 0 && (!requests || !selected)) return PML_ERR_INVALID_ARG;
     if (!aligned(requests, 4) || !aligned(selected, 4)) return PML_ERR_ALIGNMENT;
     AttnArgs a = {};

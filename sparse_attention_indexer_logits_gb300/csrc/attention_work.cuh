@@ -33,7 +33,7 @@ __host__ __device__ __forceinline__ Span tile_span(const AttnArgs& a, int nq, in
     s.lo = (int)lo;
     s.hi = (int)hi;
     s.j0 = s.lo / kAttnTileKeys;
-    s.n = max(1, (s.hi + kAttnTileKeys - 1) / kAttnTileKeys - s.j0);
+    s.n = s.hi > 0 ? (s.hi - 1) / kAttnTileKeys + 1 - s.j0 : 1;     // (hi + 127 may pass an int)
     s.cost = s.ntok <= a.half_tokens ? 1 : 2;
     return s;
 }

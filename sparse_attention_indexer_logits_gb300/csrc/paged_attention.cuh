@@ -975,8 +975,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     all_hi = min(kv_hi, p_first + 1);
                 }
                 if (a.window > 0) {
-                    row_lo = max(0, p_row - a.window + 1);
-                    all_lo = max(0, p_last - a.window + 1);
+                    row_lo = p_row < a.window ? 0 : p_row - a.window + 1;
+                    all_lo = p_last < a.window ? 0 : p_last - a.window + 1;
                 }
             }
             const int tiles_here = alt ? (n + 1 - h) / 2 : n;
@@ -1017,7 +1017,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 v_place = pos_base + t + min(n, t + (alt ? 2 : 1));
                 bool masked;
                 if constexpr (SEL) masked = (there[0] & there[1] & there[2] & there[3]) != 0xffffffffu;
-                else masked = key0 < all_lo || key0 + kAttnTileKeys > all_hi;
+                else masked = key0 < all_lo || all_hi - key0 < kAttnTileKeys;
 
                 if (active) {
                     // bit k % 32 of word k / 32 (selected: k / 4 of k % 4): key k is shown
@@ -1131,7 +1131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         fence_proxy_async_smem();     // the tensor core reads it
                     }
                     // (a tile with such keys, the same for all of the half)
-                    if (max(key0, item_lo) < all_lo || min(key0 + kAttnTileKeys, item_hi) > all_hi) {
+                    if (max(key0, item_lo) < all_lo || (item_hi > all_hi && all_hi - key0 < kAttnTileKeys)) {
                         bool bad = false;
                         if (some) {
 #pragma unroll 2

@@ -7,7 +7,7 @@ import torch
 
 import sparse_attention_indexer_logits_gb300 as pml
 from tests import serving_ref as R
-from tests.test_attention_gpu import BF, FP, Problem, check, check_selected
+from tests.test_attention_gpu import BF, FP, Problem, check, check_selected, compare
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +74,37 @@ def test_infinities_in_the_first_tile_of_every_item(dim, dtype):
     q, k, v, table, lens = p.device()
     for _ in range(20):
         assert torch.equal(pml.pml_paged_attention(q, k, v, table, lens), out)
+
+
+def far_away(window, pages):
+    """One token at the last position that a table can hold, its table all
+    pages in turn."""
+    g = R.gen(36)
+    width, kv = 2 ** 25 - 1, 2 ** 31 - 64
+    table = (torch.arange(width, device="cuda", dtype=torch.int32) % pages)[None]
+    q = torch.randn((1, 2, 64), generator=g).to(BF)
+    k, v = (torch.randn((pages, 64, 1, 64), generator=g).to(BF) for _ in range(2))
+    lse = torch.empty((1, 2), device="cuda")
+    out = pml.pml_paged_attention(q.cuda(), k.cuda(), v.cuda(), table, torch.tensor([kv], dtype=torch.int32).cuda(),
+                                  window=window, lse=lse)
+    assert pml.pml_device_status(clear=True) == 0
+    at = (torch.arange(max(0, kv - window), kv) if window <= 1000 else torch.arange(64 * pages)) % (64 * pages)
+    k, v = (c.reshape(-1, 64)[at] for c in (k, v))
+    return [(out[:, h], lse[:, h]) + R.attention(q[:, h], k, v, torch.ones((1, len(at)), dtype=torch.bool), 0.125)
+            for h in range(2)]
+
+
+@pytest.mark.parametrize("window", [1, 64, 100, 200, 1000])
+def test_the_farthest_position(window):
+    for got, lse, want, want_lse, mag in far_away(window, 7):
+        compare(got, lse, want, want_lse, mag, BF)
+
+
+def test_a_window_past_2_to_the_30():
+    """Every key of 2^31 counts: one page, 2^25 - 1 times, changes the sum and
+    not the average.  A CTA adds up 1.1e5 tiles, each sum rounded in fp32
+    (2^-24 each of the running one; in tensor memory eight steps a tile, cut
+    off rather than rounded, 2^-23 each)."""
+    for got, lse, want, want_lse, mag in far_away(2 ** 31 - 1, 1):
+        assert abs(lse.item() - want_lse.item() - math.log(2 ** 25 - 1)) <= 1.2e5 * 2.0 ** -24 + 1e-4
+        assert ((got.cpu().double() - want).abs() <= (1e6 * 2.0 ** -23 + 2.0 ** -7) * mag).all()

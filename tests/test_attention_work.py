@@ -80,3 +80,19 @@ def test_ranges_have_every_tile_once(W):
                     seen += [(i, t) for t in range(W.before(n, c, a), W.before(n, c, b))]
                 base += u
         assert seen == [(i, t) for i, (n, _) in enumerate(items) for t in range(n)]
+
+
+@pytest.mark.parametrize("back", [64, 65, 100, 128, 191, 192, 300])
+@pytest.mark.parametrize("causal", [0, 1])
+@pytest.mark.parametrize("window", [0, 1, 200, 1 << 30, (1 << 30) + 5, 2 ** 31 - 1])
+def test_spans_at_the_farthest_positions(W, back, causal, window):
+    """Lengths up to the last position that a table can hold, 2^31 - 65, and
+    windows past 2^30."""
+    width, kv, nq = (1 << 25) - 1, 2 ** 31 - back, 3
+    out = (ctypes.c_int * 7)()
+    W.span(8, width, causal, window, nq, kv, 0, out)
+    t0, ntok, lo, hi, j0, n, cost = out
+    there = min(kv, 64 * width)
+    want_lo = max(0, kv - nq - window + 1) if window else 0
+    assert (t0, ntok, lo, hi, cost) == (0, 3, want_lo, there, 1)
+    assert j0 == want_lo // 128 and n == -(-there // 128) - want_lo // 128
