@@ -200,7 +200,8 @@ __global__ void __launch_bounds__(kThreads, 3) index_quant_kernel(const IndexQua
         }
 #pragma unroll
         for (int o = kRowLanes / 2; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(mask, amax, o));
-        const float inv = __fdividef(448.0f, amax);
+        // (a quarter of both: the intrinsic gives 0 for divisors past 2^126)
+        const float inv = __fdividef(112.0f, 0.25f * amax);
         const float scale = amax * (1.0f / 448.0f);
         uint8_t* dst = is_k ? a.kv_fused + page_of[t] * kFp8BlockBytes + slot_of[t] * kHeadDim
                             : a.q_out + ((token0 + t) * a.heads + h) * kHeadDim;
