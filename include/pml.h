@@ -447,7 +447,8 @@ int pml_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_stride
  * q_out       e4m3 [tokens, num_heads, 128], contiguous, 16-byte aligned
  * kv_fused    [num_blocks][8448] as pml_fp8_paged_mqa_logits takes it
  * rot_dim a multiple of 16, rot_offset of 8; num_heads 1 .. 1024; padding
- * tokens and bad requests and pages as in pml_rope_append.  A NaN in a row
+ * tokens and bad requests and pages as in pml_rope_append (without keys a
+ * negative position alone makes the token padding).  A NaN in a row
  * makes its scale NaN, an infinity makes it infinite (the row's codes are
  * then 0 or NaN).
  */

@@ -57,3 +57,30 @@ def test_small_rows_keep_their_codes():
     qo, wo = pml.pml_index_quant_append(q.cuda(), None, torch.ones((4, 1)).cuda(), torch.arange(4).cuda(), None,
                                         freqs(0).cuda(), None, None)
     check_codes(qo.cpu().double(), wo.cpu().double(), q.double(), q.double().abs())
+
+
+@pytest.mark.parametrize("keys", [False, True])
+def test_padding_tokens(keys):
+    """Nothing of a token with a negative position (or, with keys, request) is
+    written."""
+    g = R.gen(5)
+    n, heads = 40, 5
+    q, k = torch.randn((n, heads, 128), generator=g).bfloat16(), torch.randn((n, 128), generator=g).bfloat16()
+    pos = torch.arange(n)
+    pos[[0, 7, 39]] = torch.tensor([-1, -2 ** 40, -64])
+    req = torch.zeros(n, dtype=torch.int32)
+    real = pos >= 0
+    if keys:
+        req[3], real[3] = -1, False
+    kv = torch.full((1, 8448), 9, dtype=torch.uint8, device="cuda")
+    qo = torch.full((n, heads, 128), 7, dtype=torch.uint8, device="cuda")
+    wo = torch.full((n, heads), 5.0, device="cuda")
+    w = torch.ones((n, heads)).cuda()
+    more = (k.cuda(), req.cuda(), kv, torch.zeros((1, 1), dtype=torch.int32, device="cuda")) if keys else (None,) * 4
+    pml.pml_index_quant_append(q.cuda(), more[0], w, pos.cuda(), more[1], freqs(64).cuda(), more[2], more[3], qo, wo)
+    assert pml.pml_device_status(clear=True) == 0
+    want, size = R.rope(q, pos, freqs(64))
+    codes = qo.cpu().view(torch.float8_e4m3fn).double()
+    check_codes(codes[real], wo.cpu().double()[real], want[real], size[real])
+    assert (qo.cpu()[~real] == 7).all() and (wo.cpu()[~real] == 5.0).all()
+    assert ((kv[0, :8192].reshape(64, 128) != 9).any(1).sum() == real.sum()) if keys else (kv == 9).all()
