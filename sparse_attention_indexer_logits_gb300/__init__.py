@@ -78,7 +78,7 @@ class PmlError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """The loaded library (built by ``__graft_entry__.build()`` or
     ``sparse_attention_indexer_logits_gb300._build.build()``)."""
-    global _lib, _serving_calls
+    global _lib
     if _lib is None:
         if not os.path.exists(library_path):
             raise RuntimeError(
@@ -149,14 +149,24 @@ def lib() -> ctypes.CDLL:
             getattr(L, name).restype = i32
         L.pml_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint), i32]
         L.pml_device_status.restype = i32
+        _lib = L
+    return _lib
+
+
+def _serving_module():
+    """The compiled module of the serving operators' calls, bound to the library.
+    Loaded at their first call: the others need the library alone."""
+    global _serving_calls
+    if _serving_calls is None:
+        L = lib()
         try:
             from . import _calls
         except ImportError as e:
             raise RuntimeError(f"{_HERE}/_calls.so cannot be loaded: build it again "
                                "(python -c 'import __graft_entry__ as g; g.build()')") from e
         _calls.bind(L._handle)
-        _lib, _serving_calls = L, _calls
-    return _lib
+        _serving_calls = _calls
+    return _serving_calls
 
 
 def _ptr(t: torch.Tensor | None):
@@ -471,9 +481,7 @@ def pml_fp8_paged_mqa_logits_noalloc(q: torch.Tensor, kv_fused: torch.Tensor,
 
 
 def _serving(name: str, *args) -> None:
-    if _lib is None:
-        lib()
-    rc = getattr(_serving_calls, name)(*args)
+    rc = getattr(_serving_calls or _serving_module(), name)(*args)
     if rc != 0:
         raise PmlError(rc, "pml_" + name)
 

@@ -1,8 +1,9 @@
 """Build libpml.so in-tree: every CUDA translation unit under csrc/ compiled
 for sm_103a in parallel, then linked into one shared library next to this
-file; beside them the Python module _calls (csrc/binding.cpp), against this
-interpreter's PyTorch.  Rebuilds only when a source, header, flag or one of
-the two changed."""
+file; beside it the Python module _calls (csrc/binding.cpp), against this
+interpreter's PyTorch, which the serving operators' calls need and the library
+does not.  Rebuilds each only when a source, header, flag or (for _calls) the
+interpreter or PyTorch changed."""
 from __future__ import annotations
 
 import hashlib
@@ -11,8 +12,6 @@ import shutil
 import subprocess
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
-
-import torch
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -48,11 +47,28 @@ def _fingerprint(extra_flags) -> str:
                 with open(os.path.join(d, name), "rb") as f:
                     h.update(name.encode() + f.read())
     h.update(" ".join(NVCC_FLAGS + list(extra_flags)).encode())
-    h.update(f"{sysconfig.get_config_var('SOABI')} {torch.__version__}".encode())
     return h.hexdigest()
 
 
-def _build_calls(nvcc: str) -> None:
+def _stamped(stamp: str, made: str, fp: str) -> bool:
+    """Whether `made` is there and was made from what `fp` says."""
+    if not (os.path.exists(made) and os.path.exists(stamp)):
+        return False
+    with open(stamp) as f:
+        return f.read().strip() == fp
+
+
+def _write(stamp: str, fp: str) -> None:
+    with open(stamp, "w") as f:
+        f.write(fp)
+
+
+def _build_calls(nvcc: str, fp: str, force: bool) -> None:
+    import torch
+    stamp = os.path.join(BUILD_DIR, "stamp_calls")
+    fp += f" {sysconfig.get_config_var('SOABI')} {torch.__version__}"
+    if not force and _stamped(stamp, CALLS_PATH, fp):
+        return
     home = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(nvcc) or nvcc)))
     tmp = CALLS_PATH + f".tmp{os.getpid()}"
@@ -66,17 +82,15 @@ def _build_calls(nvcc: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CALLS_PATH)
+    _write(stamp, fp)
 
 
 def build(force: bool = False, extra_flags=(), verbose: bool = False) -> str:
-    """Compile and link libpml.so; returns its path."""
+    """Compile and link libpml.so and _calls; returns the library's path.  A
+    failure of _calls is raised with the library in place."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     stamp = os.path.join(BUILD_DIR, "stamp")
     fp = _fingerprint(extra_flags)
-    if not force and os.path.exists(LIB_PATH) and os.path.exists(CALLS_PATH) and os.path.exists(stamp):
-        with open(stamp) as f:
-            if f.read().strip() == fp:
-                return LIB_PATH
     nvcc = _nvcc()
 
     def compile_one(src: str) -> str:
@@ -93,17 +107,17 @@ def build(force: bool = False, extra_flags=(), verbose: bool = False) -> str:
         return obj
 
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        calls = ex.submit(_build_calls, nvcc)
-        objs = list(ex.map(compile_one, SOURCES))
+        calls = ex.submit(_build_calls, nvcc, fp, force)
+        if force or not _stamped(stamp, LIB_PATH, fp):
+            objs = list(ex.map(compile_one, SOURCES))
+            tmp = LIB_PATH + f".tmp{os.getpid()}"
+            cmd = [nvcc, "-shared", "-gencode", "arch=compute_103a,code=sm_103a", *objs, "-o", tmp]
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+            os.replace(tmp, LIB_PATH)
+            _write(stamp, fp)
         calls.result()
-    tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [nvcc, "-shared", "-gencode", "arch=compute_103a,code=sm_103a", *objs, "-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB_PATH)
-    with open(stamp, "w") as f:
-        f.write(fp)
     return LIB_PATH
 
 
