@@ -52,13 +52,22 @@ struct Refused {};    // a Python error is set
     throw Refused();
 }
 
+// The device of the call's tensors (-1: none seen yet).
+thread_local int call_device = -1;
+
 const at::Tensor& tensor(PyObject* o, const char* name)
 {
     if (!THPVariable_Check(o)) {
         PyErr_Format(PyExc_TypeError, "%s must be a tensor", name);
         throw Refused();
     }
-    return THPVariable_Unpack(o);
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (t.is_cuda()) {
+        const int device = (int)t.get_device();
+        if (call_device < 0) call_device = device;
+        else if (device != call_device) refuse("%s must be on the device of the other tensors", name);
+    }
+    return t;
 }
 
 int narrow(int64_t v, const char* name)
@@ -88,9 +97,23 @@ int truth(PyObject* o)
     return v;
 }
 
+// The call's stream, once its tensors have been seen: all of them, and the
+// stream, belong to the current device (its properties, status word and
+// workspace are what the library uses).
 cudaStream_t stream_of(PyObject* o)
 {
+    const int current = c10::cuda::current_device();
+    if (call_device >= 0 && call_device != current) refuse("the tensors must be on the current device");
     if (o == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
+    PyObject* index = PyObject_GetAttrString(o, "device_index");
+    if (index) {
+        const long long device = PyLong_AsLongLong(index);
+        Py_DECREF(index);
+        if (device == -1 && PyErr_Occurred()) throw Refused();
+        if (device != current) refuse("stream must be of the current device");
+    } else {
+        PyErr_Clear();                            // a stand-in that has the handle alone
+    }
     PyObject* raw = PyObject_GetAttrString(o, "cuda_stream");
     if (!raw) throw Refused();
     void* s = PyLong_AsVoidPtr(raw);
@@ -554,6 +577,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n)
 {
     if (n != N) return PyErr_Format(PyExc_TypeError, "%d arguments expected, not %zd", N, n);
     if (!pml.pml_rope) return PyErr_Format(PyExc_RuntimeError, "the library is not bound");
+    call_device = -1;
     try {
         return F(args);
     } catch (const Refused&) {
