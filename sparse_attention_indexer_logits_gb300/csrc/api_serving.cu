@@ -528,7 +528,7 @@ int pml_sparse_attention(const void* q, int64_t q_token_stride, int64_t q_head_s
                          int64_t out_token_stride, int64_t out_head_stride, float* lse,
                          void* workspace, int64_t workspace_bytes, void* stream)
 {
-    if (k < 1 || selected_stride < k || num_requests < 1) return PML_ERR_INVALID_ARG;
+    if (k < 1 || selected_stride < k || num_requests < (tokens > 0 ? 1 : 0)) return PML_ERR_INVALID_ARG;
     if (k > kMaxListed) return PML_ERR_UNSUPPORTED;
     if (tokens > 0 && (!requests || !selected)) return PML_ERR_INVALID_ARG;
     if (!aligned(requests, 4) || !aligned(selected, 4)) return PML_ERR_ALIGNMENT;

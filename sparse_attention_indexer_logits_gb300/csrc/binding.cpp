@@ -430,7 +430,7 @@ PyObject* paged_attention(PyObject* const* p)
     const int batch = a.table.rows;
     const int32_t* cu_q = nullptr;
     if (p[5] != Py_None) cu_q = ints(p[5], "cu_q", batch + 1LL);
-    else if (batch == 0 || a.q.tokens % batch)
+    else if (batch == 0 ? a.q.tokens != 0 : a.q.tokens % batch != 0)
         refuse("without cu_q the tokens must divide equally over the requests");
     const int causal = truth(p[8]), window = integer(p[9], "window");
     const cudaStream_t s = stream_of(p[12]);
