@@ -479,8 +479,9 @@ int pml_index_quant_append(const void* q, int64_t q_token_stride, int64_t q_head
  * past kv_lens[b].
  *
  * Scores, softmax and sums are fp32; the probabilities are rounded to the
- * inputs' type for the second product (half a step each, 2^-8 relative in
- * bf16, averaged over the keys), the output once.
+ * inputs' type for the second product (half a step each, averaged over the
+ * keys: 2^-8 relative in bf16; 2^-11 in fp16, or 2^-32 of the row's largest
+ * probability where that is more), the output once.
  *
  * q, out       bf16 or fp16 [tokens, num_heads, head_dim], strides in elements,
  *              multiples of 8 and (q) positive; 16-byte aligned pointers

@@ -46,7 +46,10 @@ struct Joined {
         add(part[0][lane], part[1][lane], v, scale_log2);
     }
     __device__ float inverse() const { return sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f; }
-    __device__ float log_sum(float scale) const { return sum == 0.0f ? -INFINITY : top * scale + logf(sum); }
+    __device__ float log_sum(float scale, float sum_scale) const
+    {
+        return sum == 0.0f ? -INFINITY : top * scale + logf(sum * sum_scale);
+    }
 
     // Pieces p0 .. p1 - 1 of an item: slot 1 of its owner, then slot 0 of the
     // following CTAs (a range without a tile's first unit left none), from
@@ -135,7 +138,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const A
         const int qhead = head * G + g;
         *reinterpret_cast<uint2*>(out + token * a.out_token + qhead * a.out_head + 4 * at) =
             make_uint2(pack16<FP16>(x.acc[0] * inv, x.acc[1] * inv), pack16<FP16>(x.acc[2] * inv, x.acc[3] * inv));
-        if (cols + at == 0 && a.lse != nullptr) a.lse[token * a.kv_heads * G + qhead] = x.log_sum(a.scale);
+        if (cols + at == 0 && a.lse != nullptr) a.lse[token * a.kv_heads * G + qhead] = x.log_sum(a.scale, PScale<FP16>::kInverse);
         return;
     }
     // groups of 32 rows, first half 0's, then half 1's; the pieces' parts
@@ -168,7 +171,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const A
     uint4* dst = reinterpret_cast<uint4*>(out + token * a.out_token + qhead * a.out_head);
     dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
     dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    if (cols == 0 && a.lse != nullptr) a.lse[token * a.kv_heads * G + qhead] = x.log_sum(a.scale);
+    if (cols == 0 && a.lse != nullptr) a.lse[token * a.kv_heads * G + qhead] = x.log_sum(a.scale, PScale<FP16>::kInverse);
 }
 
 template <int D, bool FP16>

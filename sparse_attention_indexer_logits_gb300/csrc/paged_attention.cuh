@@ -5,7 +5,8 @@
 // over the positions p that token t may see: those of its request up to its
 // own (causal), past position - window (window > 0), or the ones a list
 // names.  One pass over the keys with a running maximum m and sum l of
-// exponentials: a tile of 128 keys gives S = Q K^T, P = 2^(c S - c m), O += P V;
+// exponentials: a tile of 128 keys gives S = Q K^T, P = 2^(c S - c m), O += P V
+// (fp16: 2^7 times as much, see PScale);
 // at the end out = O / l and lse = scale * m + ln l.
 //
 // Work.  The rows of an item are up to 256 (token, head) pairs that share a kv
@@ -160,6 +161,17 @@ __device__ __forceinline__ bool words_ready(uint32_t landed, uint32_t places, ui
         }
     }
 }
+
+// P, and so l and O, are 2^kLog2 times the weights: fp16 has half steps of
+// 2^-25 below 2^-14, and a long row's many small weights, each under half a
+// step, would be lost beside one large one.  With 2^7, and a reference that may
+// be too low by 2^8, P stays below 2^15, and weights from 2^-21 of the largest
+// on keep fp16's 11 bits.
+template <bool FP16>
+struct PScale {
+    static constexpr float kLog2 = FP16 ? 7.0f : 0.0f;
+    static constexpr float kInverse = FP16 ? 0x1p-7f : 1.0f;     // of a sum, before its logarithm
+};
 
 // Where columns 4 * col .. 4 * col + 3 of a row of a workspace slot lie.
 template <int D>
@@ -1087,7 +1099,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             x[k >> 5][k & 31] = __float_as_uint(__uint_as_float(x[k >> 5][k & 31]) - ref);
                         mc = 0.0f;
                     }
-                    const uint64_t cc = pack2(c, c), nm = pack2(-mc, -mc);
+                    const float shift = PScale<FP16>::kLog2 - mc;
+                    const uint64_t cc = pack2(c, c), nm = pack2(shift, shift);
                     uint64_t sum[2] = {0, 0};
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -1293,7 +1306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!whole) a.stats[ws_row] = make_float2(top, sum);
                     else if (a.lse != nullptr)
                         a.lse[(long long)token * a.kv_heads * G + qhead] =
-                            sum == 0.0f ? -INFINITY : top * a.scale + logf(sum);
+                            sum == 0.0f ? -INFINITY : top * a.scale + logf(sum * PScale<FP16>::kInverse);
                 }
             }
             tc_fence_before();

@@ -85,3 +85,28 @@ def test_all_keys_far_away(dtype, dim, offset):
     out, lse = p.run()
     assert judge(p, out, lse, dim ** -0.5) == 44 * 4
     assert ((lse.cpu() / offset - 1).abs() < 0.2).all()
+
+
+def test_a_long_tail_below_one_large_weight():
+    """One key's weight is 2^25 times each of 2^20 others', whose sum is 2.7 %
+    of all: fp16 weights must not lose them.  A weight below 2^-21 of the
+    largest is off by 2^-32 of it at most (half a step of fp16's subnormals
+    under a largest of 2^7)."""
+    n, tokens = 2 ** 20, 152 * 256
+    k = torch.zeros((n // 64, 64, 1, 64), dtype=FP, device="cuda")
+    v = torch.ones_like(k)
+    k[0, 0, 0, 0], v[0, 0] = 17.4375, 0.0
+    q = torch.zeros((tokens, 1, 64), dtype=FP, device="cuda")
+    q[..., 0] = 8.0                             # scores are the keys' first elements
+    table = torch.arange(n // 64, dtype=torch.int32, device="cuda")[None]
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    lse = torch.empty((tokens, 1), device="cuda")
+    out = pml.pml_paged_attention(q, k, v, table, lens, causal=False, lse=lse)
+    tail = (n - 1) * math.exp(-17.4375)
+    want = tail / (1 + tail)
+    # sums of 4096 tiles' sums in fp32: 2^-24 each, cut off by eight steps a
+    # tile in tensor memory, 2^-23 each
+    rel = 2.0 ** -11 + 2e-4 + 4096 * 8 * 2.0 ** -23
+    assert (out.double() - want).abs().max() <= want * (rel + 2.0 ** -11) + n * 2.0 ** -32
+    assert (lse.double() - 17.4375 - math.log1p(tail)).abs().max() <= 4096 * 2.0 ** -24 + 1e-4
+    assert pml.pml_device_status(clear=True) == 0
