@@ -12,6 +12,8 @@ class Results(Model):
     """`always`: a half without a tile writes its (empty) statistics, too;
     `hasty`: a product is added by hand without a wait for O."""
 
+    by_hand_share = 0.3
+
     def __init__(self, seed, stages, always=False, hasty=False):
         super().__init__(seed, stages)
         self.always, self.hasty = always, hasty
@@ -58,7 +60,7 @@ class Results(Model):
                 v = self.v_place(base, alt, n, t)
                 yield self.r.randint(1, 30)
                 self.S_holds[h] = ("P", i, t)
-                if self.r.random() < 0.3:        # hidden rows of V hold an infinity
+                if self.r.random() < self.by_hand_share:     # hidden rows of V hold an infinity
                     yield lambda: self.full[v % self.S].done(v // self.S & 1)
                     assert self.holds[v % self.S] == (i, "V", t)
                     if j == 0 and not self.hasty:
