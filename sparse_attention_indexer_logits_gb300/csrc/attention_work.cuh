@@ -47,9 +47,9 @@ __host__ __device__ __forceinline__ int tiles_of(const AttnArgs& a, int nq)
 // Units of work.  A tile is one where the halves take the tiles in turn and two
 // where both see it (1800 and 3600 cycles), and beginning and ending an item
 // (Q's way in, the first copies, the output) is three.  A mixed batch of 24
-// requests takes 51.7 us (captured in a graph), with two or six units an item
-// 54.5 or 52.3; 64 tokens of 2048 listed positions 26.5 us, with two, four or
-// six 26.4, 28.8 or 30.0.  A range has the tiles whose first unit lies in it.
+// requests takes 54.9 us, with two, four or six units an item 58.0, 55.1 or
+// 55.6; 64 tokens of 2048 listed positions 29.2 us, with two, four or six 29.2,
+// 31.8 or 32.7.  A range has the tiles whose first unit lies in it.
 constexpr int kItemUnits = 3;
 
 __host__ __device__ __forceinline__ int units_of(const Span& s) { return s.n * s.cost + kItemUnits; }

@@ -149,9 +149,10 @@ __global__ void __launch_bounds__(kThreads, 3) index_quant_kernel(const IndexQua
         long long page = 0;
         int slot = 0;
         bool ok = false;
-        const long long position = load_position(a.rot, token0 + t);
-        if (a.k != nullptr) ok = find_slot(a.slot, token0 + t, position, pad, page, slot);
-        else pad = position < 0;
+        if (a.k != nullptr)
+            ok = find_slot(a.slot, token0 + t, load_position(a.rot, token0 + t), pad, page, slot);
+        else
+            pad = load_position(a.rot, token0 + t) < 0;
         page_of[t] = page;
         slot_of[t] = slot;
         state_of[t] = pad ? 0 : ok ? 2 : 1;
