@@ -50,12 +50,12 @@
 //   64 single tokens over U[1024, 32768] keys, 8 kv heads of 128, bf16
 //       687 us, 4.71 GB: bound by HBM, 101 % of the copy
 //   4096 tokens that end 32768 keys, 32 heads over 4, bf16
-//       1500-1550 us, 2.06 TFLOP: 1.33-1.37 PFLOP/s, 70-72 % of the
+//       1500-1555 us, 2.06 TFLOP: 1.33-1.37 PFLOP/s, 69-72 % of the
 //       product's.  One half's chain (scores, softmax, P V) is hidden behind
 //       the other's except for its hand-overs, and the board is at its power
 //       limit
 //   24 requests of 1 .. 500 tokens over up to 8000 keys, window 1500, fp16, 64
-//       53 us: a floor of 7; a tile's chain of 3600 cycles, 17 tiles a CTA,
+//       55 us: a floor of 7; a tile's chain of 3600 cycles, 17 tiles a CTA,
 //       and the way into and out of two or three items
 //   64 tokens x 2048 listed positions, 64 heads over 1, bf16
 //       29 us: a floor of 10; a fixed part of 12 us (prologue, first lookups,

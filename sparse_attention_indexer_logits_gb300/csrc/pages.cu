@@ -16,7 +16,8 @@
 // whole GPU.
 //
 // Measured: forking 160 requests of up to 8192 tokens 10.5 us, freeing them 4.3
-// (a warp per request: 9); the compaction plan of 64 requests' pages 14 us (its
+// (a warp per request: 9); extending 64 requests by a token 8.0 over 8192 pages
+// and 9.3 over 65536; the compaction plan of 64 requests' pages 14 us (its
 // tables a warp per row: 19); copying 544 MB of pages 166 us, 6.55 TB/s of read
 // and write, 97 % of a plain copy's 6776 GB/s.
 #include <cooperative_groups.h>
