@@ -20,7 +20,7 @@ def _build():
     yield
 
 
-def judge(p, out, lse, scale):
+def compare_rows(p, out, lse, scale):
     """A score is a sum of products that are exact in fp32: each further one
     adds a rounding of 2^-23 of their magnitudes' sum at most (the tensor core
     may cut off), `score` in all.  A weight is 2^(c x - c m): off by the two
@@ -70,7 +70,7 @@ def test_some_keys_far_away(low):
         p.k[page, at % 64] = 0
         p.k[page, at % 64, :, 0] = (low * (0.5 + at / n)).to(BF)[:, None]
     p.stale(torch.finfo(BF).min)
-    assert judge(p, *p.run(), 64 ** -0.5) == 44 * 4
+    assert compare_rows(p, *p.run(), 64 ** -0.5) == 44 * 4
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
@@ -83,7 +83,7 @@ def test_all_keys_far_away(dtype, dim, offset):
     p.q[..., 0] = offset * dim ** 0.5 / 128.0
     p.stale()
     out, lse = p.run()
-    assert judge(p, out, lse, dim ** -0.5) == 44 * 4
+    assert compare_rows(p, out, lse, dim ** -0.5) == 44 * 4
     assert ((lse.cpu() / offset - 1).abs() < 0.2).all()
 
 
