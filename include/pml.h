@@ -534,7 +534,115 @@ int pml_sparse_attention(const void* q, int64_t q_token_stride, int64_t q_head_s
                          int64_t out_token_stride, int64_t out_head_stride, float* lse,
                          void* workspace, int64_t workspace_bytes, void* stream);
 
-/* Bytes of workspace for either attention call; num_ctas is the device's SM
+/*
+ * K/V caches held in 4 bits: a quarter of the memory and traffic of 16 bits.
+ * A row (a token's head of head_dim values, 64 or 128) is head_dim / 2 bytes
+ * of E2M1 codes, element d in byte d / 2, the low nibble the even one, and
+ * head_dim / 16 E4M3 scales, each of sixteen values, as the rows of
+ * pml_indexer_scores_nvfp4; all values of a cache are multiplied by one power
+ * of two besides:
+ *
+ *   value = E2M1(code) * E4M3(scale) * cache.scale
+ *
+ * A NaN scale (0x7F, 0xFF) makes its sixteen values NaN; a negative one negates
+ * them.
+ *
+ * codes    the row of (page, slot, head) at page * page_stride + slot *
+ *          slot_stride + head * head_stride bytes; 16-byte aligned, strides
+ *          positive multiples of 16
+ * scales   alike with its own strides, all aligned to head_dim / 16 bytes
+ * scale    2^-32 .. 2^32, a power of two (else PML_ERR_INVALID_ARG)
+ */
+typedef struct pml_nvfp4_cache {
+    uint8_t* codes;
+    uint8_t* scales;
+    int64_t page_stride, slot_stride, head_stride;
+    int64_t scale_page_stride, scale_slot_stride, scale_head_stride;
+    float scale;
+} pml_nvfp4_cache;
+
+/*
+ * pml_append_nvfp4 -- a step's k and v rows quantised into their pages.  For
+ * each sixteen values x of a row, g the cache's scale:
+ *
+ *   s = e4m3(max |x| / (6 g)), 448 at most, NaN if some x is not finite;
+ *   code = the E2M1 value nearest to x / (s g), ties to the even code, 6 at
+ *          most in magnitude, the sign that of x (0 of -0); 0 where s is 0 or
+ *          NaN
+ *
+ * The codes are those of the exact quotient: equal rows give equal codes.  (k is
+ * stored as it comes; pml_rope rotates it.)
+ *
+ * k, v        bf16 or fp16 [tokens, kv_heads, head_dim], strides in elements,
+ *             multiples of 8, 16-byte aligned
+ * positions, requests, block_table   as in pml_rope_append: padding tokens are
+ *             not written, nor are those of a bad request or page (status)
+ * Two tokens of a call must not share a slot.
+ */
+int pml_append_nvfp4(const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                     int64_t v_token_stride, int64_t v_head_stride, int dtype, const void* positions,
+                     int positions_64, const int32_t* requests, int num_requests,
+                     const pml_nvfp4_cache* k_cache, const pml_nvfp4_cache* v_cache, int64_t num_pages,
+                     const int32_t* block_table, int64_t bt_stride, int bt_width, int tokens,
+                     int kv_heads, int head_dim, void* stream);
+
+/*
+ * pml_read_nvfp4 -- pages read back into 16-bit pages: slot p % 64 of page
+ * out_table[b, p / 64] of k_out and v_out becomes the values of position p of
+ * request b, p < kv_lens[b], rounded once to dtype (exact but where the type's
+ * range ends).  Other slots stay as they were.  A prefill chunk reads its
+ * contexts back once and attends to them with pml_paged_attention, whose
+ * block_table is then out_table.
+ *
+ * k_out, v_out  bf16 or fp16, element (page, slot, head, d) at page *
+ *               k_page_stride + slot * k_slot_stride + head * k_head_stride +
+ *               d; strides positive multiples of 8, 16-byte aligned
+ * width         columns of both tables; positions at or past 64 * width are
+ *               not there
+ * A page outside [0, num_pages) or [0, out_pages) is skipped
+ * (PML_STATUS_BAD_BLOCK).  No two blocks of a call share a page of the outputs.
+ */
+int pml_read_nvfp4(const pml_nvfp4_cache* k_cache, const pml_nvfp4_cache* v_cache, int64_t num_pages,
+                   const int32_t* block_table, int64_t bt_stride, const int32_t* kv_lens, int batch,
+                   int width, void* k_out, int64_t k_page_stride, int64_t k_slot_stride,
+                   int64_t k_head_stride, void* v_out, int64_t v_page_stride, int64_t v_slot_stride,
+                   int64_t v_head_stride, int dtype, int64_t out_pages, const int32_t* out_table,
+                   int64_t ot_stride, int kv_heads, int head_dim, void* stream);
+
+/*
+ * pml_paged_attention_nvfp4 -- pml_paged_attention over caches held in 4 bits:
+ * single tokens and a few drafts per request, or any mix (long chunks are
+ * faster through pml_read_nvfp4).  Arguments, masks, rows without keys, `lse`,
+ * the workspace and the errors are as there, with these differences: the
+ * products take q and the probabilities in fp16 (a bf16 row of q scaled by a
+ * power of two, which keeps its 8 bits for elements down to 2^-17 of its
+ * largest); kv_heads divides num_heads, whose number is at most 8192; a row of
+ * q that is not finite gives a row without meaning.
+ */
+int pml_paged_attention_nvfp4(const void* q, int64_t q_token_stride, int64_t q_head_stride, int dtype,
+                              const pml_nvfp4_cache* k_cache, const pml_nvfp4_cache* v_cache,
+                              int64_t num_pages, const int32_t* block_table, int64_t bt_stride,
+                              int bt_width, const int32_t* kv_lens, const int32_t* cu_q, int batch,
+                              int tokens, int num_heads, int kv_heads, int head_dim,
+                              float softmax_scale, int causal, int window, void* out,
+                              int64_t out_token_stride, int64_t out_head_stride, float* lse,
+                              void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * pml_sparse_attention_nvfp4 -- pml_sparse_attention over caches held in 4
+ * bits, with the differences above.
+ */
+int pml_sparse_attention_nvfp4(const void* q, int64_t q_token_stride, int64_t q_head_stride, int dtype,
+                               const pml_nvfp4_cache* k_cache, const pml_nvfp4_cache* v_cache,
+                               int64_t num_pages, const int32_t* block_table, int64_t bt_stride,
+                               int bt_width, const int32_t* kv_lens, const int32_t* requests,
+                               int num_requests, const int32_t* selected, int64_t selected_stride,
+                               int k, int tokens, int num_heads, int kv_heads, int head_dim,
+                               float softmax_scale, void* out, int64_t out_token_stride,
+                               int64_t out_head_stride, float* lse, void* workspace,
+                               int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace for any attention call; num_ctas is the device's SM
  * count (pml_default_num_ctas).  0 for a head_dim other than 64 and 128. */
 int64_t pml_attention_workspace_bytes(int num_ctas, int head_dim);
 

@@ -28,6 +28,10 @@ Entry points (same names as the C ABI):
 * ``pml_paged_attention`` / ``pml_sparse_attention`` -- softmax attention of
   new tokens over a paged cache: every position they may see, or the listed
   ones (the selection's); ``pml_attention_workspace`` makes their workspace.
+* ``pml_append_nvfp4`` / ``pml_read_nvfp4`` -- K/V caches held in 4 bits: rows
+  quantised into their pages as they are written, and pages read back;
+  ``pml_paged_attention_nvfp4`` / ``pml_sparse_attention_nvfp4`` attend over
+  them; ``pml_nvfp4_pages`` makes such caches.
 * ``pml_pages_fork`` / ``pml_pages_extend`` / ``pml_pages_free`` /
   ``pml_pages_compact`` / ``pml_pages_copy`` -- the pool behind the caches:
   reference counts, block tables, and the page copies that changes ask for.
@@ -52,7 +56,8 @@ __all__ = [
     "pml_default_num_ctas", "pml_min_block_table_width", "pml_padded_seq_len", "pml_schedule_meta_elems",
     "pml_rope", "pml_rope_append", "pml_index_quant_append", "pml_paged_attention",
     "pml_sparse_attention", "pml_attention_workspace", "pml_pages_fork", "pml_pages_extend",
-    "pml_pages_free", "pml_pages_compact", "pml_pages_copy",
+    "pml_pages_free", "pml_pages_compact", "pml_pages_copy", "pml_nvfp4_pages", "pml_append_nvfp4",
+    "pml_read_nvfp4", "pml_paged_attention_nvfp4", "pml_sparse_attention_nvfp4",
     "fp8_paged_mqa_logits", "indexer_scores", "compute_paged_mqa_logits_schedule",
 ]
 
@@ -144,6 +149,14 @@ def lib() -> ctypes.CDLL:
             "pml_pages_free": pool + [P, i32, P],
             "pml_pages_compact": pool + [P, P, i64, P, P, P, i32, P, P],
             "pml_pages_copy": [P, i32, i64, i32, i64, i64, P, P, P, i32, P],
+            "pml_append_nvfp4": [P, i64, i64, P, i64, i64, i32, P, i32, P, i32, P, P, i64, P, i64, i32, i32,
+                                 i32, i32, P],
+            "pml_read_nvfp4": [P, P, i64, P, i64, P, i32, i32, P, i64, i64, i64, P, i64, i64, i64, i32, i64,
+                               P, i64, i32, i32, P],
+            "pml_paged_attention_nvfp4": [P, i64, i64, i32, P, P, i64, P, i64, i32, P, P, i32, i32, i32, i32,
+                                          i32, f32, i32, i32, P, i64, i64, P, P, i64, P],
+            "pml_sparse_attention_nvfp4": [P, i64, i64, i32, P, P, i64, P, i64, i32, P, P, i32, P, i64, i32,
+                                           i32, i32, i32, i32, f32, P, i64, i64, P, P, i64, P],
         }.items():
             getattr(L, name).argtypes = types
             getattr(L, name).restype = i32
@@ -603,6 +616,85 @@ def pml_sparse_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
         out = _new(q.shape, q.dtype, q.device, stream)
     _serving("sparse_attention", q, k_cache, v_cache, block_table, kv_lens, requests, selected, out,
              softmax_scale, lse, workspace, stream)
+    return out
+
+
+def pml_nvfp4_pages(num_pages: int, kv_heads: int, head_dim: int, layers: int | None = None, device=None):
+    """Zeroed caches held in 4 bits: ``(buffer, k_codes, k_scales, v_codes,
+    v_scales)``, the last four views of the first, uint8 ``[num_pages, page
+    bytes]`` (``layers`` of them in front, if given), which ``pml_pages_copy``
+    takes.  A page holds its heads one after another, 64 slots each: k's codes,
+    k's scales, v's codes, v's scales."""
+    if head_dim not in (64, 128):
+        raise ValueError("head_dim must be 64 or 128")
+    lead = (num_pages,) if layers is None else (layers, num_pages)
+    widths = (head_dim // 2, head_dim // 16)
+    rows = kv_heads * 64
+    buffer = torch.zeros((*lead, 2 * rows * sum(widths)), dtype=torch.uint8,
+                         device="cuda" if device is None else device)
+    parts, at = [], 0
+    for width in widths * 2:
+        part = buffer[..., at:at + rows * width].unflatten(-1, (kv_heads, 64, width))
+        parts.append(part.transpose(-3, -2))
+        at += rows * width
+    return (buffer, *parts)
+
+
+def pml_append_nvfp4(k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, requests: torch.Tensor,
+                     k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
+                     v_scales: torch.Tensor, block_table: torch.Tensor, k_scale: float = 1.0,
+                     v_scale: float = 1.0, stream=None) -> None:
+    """k and v ``[tokens, kv_heads, dim]`` (bf16 or fp16; dim 64 or 128)
+    quantised into slot ``positions[t] % 64`` of page ``block_table[requests[t],
+    positions[t] // 64]`` of caches held in 4 bits: codes uint8 ``[pages, 64,
+    kv_heads, dim / 2]`` and scales uint8 or float8_e4m3fn ``[pages, 64,
+    kv_heads, dim / 16]`` (any strides that are multiples of 16 bytes, and of
+    dim / 16).  ``k_scale`` and ``v_scale``: a power of two for all of a cache.
+    A negative request or position makes the token padding."""
+    _serving("append_nvfp4", k, v, positions, requests, k_codes, k_scales, v_codes, v_scales, block_table,
+             k_scale, v_scale, stream)
+
+
+def pml_read_nvfp4(k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
+                   v_scales: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                   k_out: torch.Tensor, v_out: torch.Tensor, out_table: torch.Tensor, k_scale: float = 1.0,
+                   v_scale: float = 1.0, stream=None) -> None:
+    """The first ``kv_lens[b]`` positions of every request read back into the
+    16-bit pages ``out_table[b]`` of ``k_out`` and ``v_out`` ``[pages, 64,
+    kv_heads, dim]`` (any strides); their other slots stay as they are.  A
+    prefill chunk then attends to those pages with ``pml_paged_attention``."""
+    _serving("read_nvfp4", k_codes, k_scales, v_codes, v_scales, block_table, kv_lens, k_out, v_out, out_table,
+             k_scale, v_scale, stream)
+
+
+def pml_paged_attention_nvfp4(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tensor,
+                              v_codes: torch.Tensor, v_scales: torch.Tensor, block_table: torch.Tensor,
+                              kv_lens: torch.Tensor, cu_q: torch.Tensor | None = None,
+                              out: torch.Tensor | None = None, softmax_scale: float | None = None,
+                              causal: bool = True, window: int = 0, k_scale: float = 1.0,
+                              v_scale: float = 1.0, lse: torch.Tensor | None = None,
+                              workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """``pml_paged_attention`` over caches held in 4 bits (as
+    ``pml_append_nvfp4`` writes them): single tokens and a few drafts per
+    request, or any mix; long chunks are faster through ``pml_read_nvfp4``."""
+    if out is None:
+        out = _new(q.shape, q.dtype, q.device, stream)
+    _serving("paged_attention_nvfp4", q, k_codes, k_scales, v_codes, v_scales, block_table, kv_lens, cu_q, out,
+             softmax_scale, causal, window, k_scale, v_scale, lse, workspace, stream)
+    return out
+
+
+def pml_sparse_attention_nvfp4(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tensor,
+                               v_codes: torch.Tensor, v_scales: torch.Tensor, block_table: torch.Tensor,
+                               kv_lens: torch.Tensor, requests: torch.Tensor, selected: torch.Tensor,
+                               out: torch.Tensor | None = None, softmax_scale: float | None = None,
+                               k_scale: float = 1.0, v_scale: float = 1.0, lse: torch.Tensor | None = None,
+                               workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """``pml_sparse_attention`` over caches held in 4 bits."""
+    if out is None:
+        out = _new(q.shape, q.dtype, q.device, stream)
+    _serving("sparse_attention_nvfp4", q, k_codes, k_scales, v_codes, v_scales, block_table, kv_lens, requests,
+             selected, out, softmax_scale, k_scale, v_scale, lse, workspace, stream)
     return out
 
 

@@ -32,7 +32,8 @@ namespace {
 #define PML_CALLS(X) \
     X(pml_rope) X(pml_rope_append) X(pml_index_quant_append) X(pml_paged_attention) \
     X(pml_sparse_attention) X(pml_attention_workspace_bytes) X(pml_default_num_ctas) \
-    X(pml_pages_fork) X(pml_pages_extend) X(pml_pages_free) X(pml_pages_compact) X(pml_pages_copy)
+    X(pml_pages_fork) X(pml_pages_extend) X(pml_pages_free) X(pml_pages_compact) X(pml_pages_copy) \
+    X(pml_append_nvfp4) X(pml_read_nvfp4) X(pml_paged_attention_nvfp4) X(pml_sparse_attention_nvfp4)
 
 #define PML_MEMBER(name) decltype(&::name) name = nullptr;
 struct Library {
@@ -232,6 +233,51 @@ Caches caches_of(PyObject* k_cache, PyObject* v_cache, const Rows& like)
     return c;
 }
 
+// The two caches of a call in 4 bits, from k's codes and scales and v's and the
+// two scales of all values.
+struct Nvfp4Caches {
+    pml_nvfp4_cache k, v;
+    int64_t pages;
+    int heads, dim;
+
+    Nvfp4Caches(PyObject* const* p, PyObject* k_scale, PyObject* v_scale)
+    {
+        one(p[0], "k_codes", p[1], "k_scales", k_scale, k, true);
+        one(p[2], "v_codes", p[3], "v_scales", v_scale, v, false);
+    }
+
+private:
+    void one(PyObject* codes, const char* codes_name, PyObject* scales, const char* scales_name, PyObject* scale,
+             pml_nvfp4_cache& c, bool first)
+    {
+        const at::Tensor& t = tensor(codes, codes_name);
+        if (!t.is_cuda() || t.dim() != 4 || t.size(1) != 64 || t.scalar_type() != at::kByte || t.stride(3) != 1)
+            refuse("%s must be a CUDA uint8 [pages, 64, kv_heads, dim / 2] tensor with unit last stride", codes_name);
+        if (first) {
+            pages = t.size(0);
+            heads = narrow(t.size(2), codes_name);
+            dim = narrow(2 * t.size(3), codes_name);
+        } else if (t.size(0) != pages || t.size(2) != heads || 2 * t.size(3) != dim) {
+            refuse("%s must have k_codes' shape", codes_name);
+        }
+        const at::Tensor& s = tensor(scales, scales_name);
+        if (!s.is_cuda() || s.dim() != 4 || s.size(0) != pages || s.size(1) != 64 || s.size(2) != heads ||
+            16 * s.size(3) != dim || (s.scalar_type() != at::kByte && s.scalar_type() != at::kFloat8_e4m3fn) ||
+            (s.stride(3) != 1 && s.size(3) > 1))
+            refuse("%s must be a CUDA uint8 or float8_e4m3fn [pages, 64, kv_heads, dim / 16] tensor with unit last "
+                   "stride", scales_name);
+        c.codes = static_cast<uint8_t*>(t.data_ptr());
+        c.scales = static_cast<uint8_t*>(s.data_ptr());
+        c.page_stride = t.stride(0);
+        c.slot_stride = t.stride(1);
+        c.head_stride = t.stride(2);
+        c.scale_page_stride = s.stride(0);
+        c.scale_slot_stride = s.stride(1);
+        c.scale_head_stride = s.stride(2);
+        c.scale = real(scale);
+    }
+};
+
 struct Rotation {
     const void* positions;
     const void* freq;
@@ -394,21 +440,19 @@ PyObject* index_quant_append(PyObject* const* p)
     });
 }
 
-// The checks that both attention calls share.
-struct Attention {
+// The checks that all attention calls share.
+struct Attending {
     Rows q, out;
-    Caches c;
     Table table;
     const int32_t* lens;
     float scale;
     float* lse = nullptr;
 
-    Attention(PyObject* q_, PyObject* k_cache, PyObject* v_cache, PyObject* block_table, PyObject* kv_lens,
-              PyObject* out_, PyObject* softmax_scale, PyObject* lse_)
+    Attending(PyObject* q_, PyObject* block_table, PyObject* kv_lens, PyObject* out_, PyObject* softmax_scale,
+              PyObject* lse_)
         : q(rows_of(q_, "q"))
     {
         need_half(q);
-        c = caches_of(k_cache, v_cache, q);
         table = table_of(block_table, "block_table");
         lens = ints(kv_lens, "kv_lens", table.rows);
         out = output_of(out_, "out", q, "q");
@@ -422,16 +466,33 @@ struct Attention {
             lse = static_cast<float*>(t.data_ptr());
         }
     }
+
+    // The tokens' offsets, or null: equally many of each request.
+    const int32_t* offsets(PyObject* cu_q) const
+    {
+        const int batch = table.rows;
+        if (cu_q != Py_None) return ints(cu_q, "cu_q", batch + 1LL);
+        if (batch == 0 ? q.tokens != 0 : q.tokens % batch != 0)
+            refuse("without cu_q the tokens must divide equally over the requests");
+        return nullptr;
+    }
+};
+
+struct Attention : Attending {
+    Caches c;
+
+    Attention(PyObject* q_, PyObject* k_cache, PyObject* v_cache, PyObject* block_table, PyObject* kv_lens,
+              PyObject* out_, PyObject* softmax_scale, PyObject* lse_)
+        : Attending(q_, block_table, kv_lens, out_, softmax_scale, lse_), c(caches_of(k_cache, v_cache, q))
+    {
+    }
 };
 
 PyObject* paged_attention(PyObject* const* p)
 {
     const Attention a(p[0], p[1], p[2], p[3], p[4], p[6], p[7], p[10]);
     const int batch = a.table.rows;
-    const int32_t* cu_q = nullptr;
-    if (p[5] != Py_None) cu_q = ints(p[5], "cu_q", batch + 1LL);
-    else if (batch == 0 ? a.q.tokens != 0 : a.q.tokens % batch != 0)
-        refuse("without cu_q the tokens must divide equally over the requests");
+    const int32_t* cu_q = a.offsets(p[5]);
     const int causal = truth(p[8]), window = integer(p[9], "window");
     const cudaStream_t s = stream_of(p[12]);
     const Workspace w(p[11], a.q.dim, s);
@@ -461,6 +522,93 @@ PyObject* sparse_attention(PyObject* const* p)
                                         selected.stride, selected.width, a.q.tokens, a.q.heads,
                                         a.c.k.heads, a.q.dim, a.scale, a.out.data, a.out.token,
                                         a.out.head, a.lse, w.data, w.bytes, s);
+    });
+}
+
+PyObject* append_nvfp4(PyObject* const* p)
+{
+    const Rows k = rows_of(p[0], "k");
+    if (k.type != at::kBFloat16 && k.type != at::kHalf) refuse("k must be bfloat16 or float16");
+    const Rows v = rows_of(p[1], "v", k);
+    if (!v.same_shape(k)) refuse("v must have k's shape");
+    const at::Tensor& pos = tensor(p[2], "positions");
+    if ((pos.scalar_type() != at::kInt && pos.scalar_type() != at::kLong) || !pos.is_cuda() || !pos.is_contiguous())
+        refuse("positions must be a contiguous CUDA int32 or int64 tensor");
+    if (pos.numel() != k.tokens) refuse("positions must hold one value per token");
+    const int32_t* requests = ints(p[3], "requests", k.tokens);
+    const Nvfp4Caches c(p + 4, p[9], p[10]);
+    if (c.heads != k.heads || c.dim != k.dim) refuse("the caches must have k's heads and dim");
+    const Table table = table_of(p[8], "block_table");
+    const cudaStream_t s = stream_of(p[11]);
+    return run([&] {
+        return pml.pml_append_nvfp4(k.data, k.token, k.head, v.data, v.token, v.head, dtype_code(k.type),
+                                    pos.data_ptr(), pos.scalar_type() == at::kLong, requests, table.rows, &c.k, &c.v,
+                                    c.pages, table.data, table.stride, table.width, k.tokens, k.heads, k.dim, s);
+    });
+}
+
+PyObject* read_nvfp4(PyObject* const* p)
+{
+    const Nvfp4Caches c(p, p[9], p[10]);
+    const Table table = table_of(p[4], "block_table"), to = table_of(p[8], "out_table");
+    if (to.rows != table.rows || to.width != table.width) refuse("out_table must have block_table's shape");
+    const int32_t* lens = ints(p[5], "kv_lens", table.rows);
+    const at::Tensor& first = tensor(p[6], "k_out");
+    if (first.scalar_type() != at::kBFloat16 && first.scalar_type() != at::kHalf)
+        refuse("k_out must be bfloat16 or float16");
+    Rows like = {};
+    like.type = first.scalar_type();
+    const Cache k = cache_of(p[6], "k_out", like), v = cache_of(p[7], "v_out", like);
+    if (k.pages != v.pages || k.heads != c.heads || v.heads != c.heads || k.dim != c.dim || v.dim != c.dim)
+        refuse("k_out and v_out must be [pages, 64, kv_heads, dim] with the caches' heads and dim");
+    const cudaStream_t s = stream_of(p[11]);
+    return run([&] {
+        return pml.pml_read_nvfp4(&c.k, &c.v, c.pages, table.data, table.stride, lens, table.rows, table.width, k.data,
+                                  k.page, k.slot, k.head, v.data, v.page, v.slot, v.head, dtype_code(like.type),
+                                  k.pages, to.data, to.stride, c.heads, c.dim, s);
+    });
+}
+
+struct AttentionNvfp4 : Attending {
+    Nvfp4Caches c;
+
+    AttentionNvfp4(PyObject* q_, PyObject* const* parts, PyObject* block_table, PyObject* kv_lens, PyObject* out_,
+                   PyObject* softmax_scale, PyObject* lse_, PyObject* k_scale, PyObject* v_scale)
+        : Attending(q_, block_table, kv_lens, out_, softmax_scale, lse_), c(parts, k_scale, v_scale)
+    {
+        if (c.dim != q.dim) refuse("the caches must have q's dim");
+    }
+};
+
+PyObject* paged_attention_nvfp4(PyObject* const* p)
+{
+    const AttentionNvfp4 a(p[0], p + 1, p[5], p[6], p[8], p[9], p[14], p[12], p[13]);
+    const int32_t* cu_q = a.offsets(p[7]);
+    const int causal = truth(p[10]), window = integer(p[11], "window");
+    const cudaStream_t s = stream_of(p[16]);
+    const Workspace w(p[15], a.q.dim, s);
+    return run([&] {
+        return pml.pml_paged_attention_nvfp4(a.q.data, a.q.token, a.q.head, dtype_code(a.q.type), &a.c.k, &a.c.v,
+                                             a.c.pages, a.table.data, a.table.stride, a.table.width, a.lens, cu_q,
+                                             a.table.rows, a.q.tokens, a.q.heads, a.c.heads, a.q.dim, a.scale, causal,
+                                             window, a.out.data, a.out.token, a.out.head, a.lse, w.data, w.bytes, s);
+    });
+}
+
+PyObject* sparse_attention_nvfp4(PyObject* const* p)
+{
+    const AttentionNvfp4 a(p[0], p + 1, p[5], p[6], p[9], p[10], p[13], p[11], p[12]);
+    const int32_t* requests = ints(p[7], "requests", a.q.tokens);
+    const Table selected = table_of(p[8], "selected");
+    if (selected.rows != a.q.tokens) refuse("selected must hold a row per token");
+    const cudaStream_t s = stream_of(p[15]);
+    const Workspace w(p[14], a.q.dim, s);
+    return run([&] {
+        return pml.pml_sparse_attention_nvfp4(a.q.data, a.q.token, a.q.head, dtype_code(a.q.type), &a.c.k, &a.c.v,
+                                              a.c.pages, a.table.data, a.table.stride, a.table.width, a.lens,
+                                              requests, a.table.rows, selected.data, selected.stride, selected.width,
+                                              a.q.tokens, a.q.heads, a.c.heads, a.q.dim, a.scale, a.out.data,
+                                              a.out.token, a.out.head, a.lse, w.data, w.bytes, s);
     });
 }
 
@@ -603,6 +751,10 @@ PyMethodDef methods[] = {
     PML_ENTRY(pages_free, 5),
     PML_ENTRY(pages_compact, 10),
     PML_ENTRY(pages_copy, 6),
+    PML_ENTRY(append_nvfp4, 12),
+    PML_ENTRY(read_nvfp4, 12),
+    PML_ENTRY(paged_attention_nvfp4, 17),
+    PML_ENTRY(sparse_attention_nvfp4, 16),
     {nullptr, nullptr, 0, nullptr},
 };
 

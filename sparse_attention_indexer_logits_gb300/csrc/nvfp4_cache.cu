@@ -1,0 +1,299 @@
+// K/V caches held in 4 bits on sm_103a: rows quantised into their pages as they
+// are written, and pages read back in 16 bits.
+//
+// A row is E2M1 codes, two to a byte, and one E4M3 scale s for sixteen values
+// x; with the cache's power of two g
+//
+//   s = e4m3(max |x| / (6 g)),   code = e2m1(x / (s g)),   value = code s g.
+//
+// The codes are those of the exact quotient, ties to the even one: x has at
+// most 11 significant bits and s g four, so a quotient that is not on a border
+// between two codes is 2^-12 or more away from it, and one that is comes out
+// exact from a product with 1 / (s g) and one step of Newton's.  A value read
+// has at most six significant bits: exact in both types within their range.
+//
+// Both are bound by memory: 2 bytes of a value on one side, 9/16 on the other.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "dependent.cuh"
+#include "nvfp4_cache.h"
+#include "rotary.cuh"
+
+namespace pml {
+
+namespace {
+
+constexpr uint32_t kNanScale = 0x7f;
+
+template <bool FP16>
+__device__ __forceinline__ float2 unpack16(uint32_t w)
+{
+    if constexpr (FP16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    else return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+template <bool FP16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi)
+{
+    uint32_t r;
+    if constexpr (FP16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t e4m3_of(float x)
+{
+    uint16_t p;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(p) : "f"(0.0f), "f"(x));
+    return p & 0xffu;
+}
+
+__device__ __forceinline__ float e4m3_value(uint32_t code)
+{
+    const uint32_t h = e4m3_to_f16x2_dup(code);
+    return __half2float(__ushort_as_half((unsigned short)(h & 0xffffu)));
+}
+
+// Two values to a byte of codes, the first in the low nibble.
+__device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}"
+        : "=r"(r)
+        : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Sixteen values to their codes and scale.
+template <bool FP16>
+__device__ __forceinline__ uint2 quantise16(const uint4 (&v)[2], float g, uint32_t& scale)
+{
+    const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+    // magnitudes compare like their bits, infinities and NaN above all others
+    uint32_t top2 = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top2 = __vmaxu2(top2, w[i] & 0x7fff7fffu);
+    const uint32_t top = max(top2 & 0xffffu, top2 >> 16);
+    if (top >= (FP16 ? 0x7c00u : 0x7f80u)) {
+        scale = kNanScale;
+        return make_uint2(0u, 0u);
+    }
+    const float amax = unpack16<FP16>(top).x;
+    scale = e4m3_of(__fdiv_rn(amax, 6.0f * g));
+    const float d = e4m3_value(scale) * g;
+    if (d == 0.0f) return make_uint2(0u, 0u);
+    const float rc = __fdiv_rn(1.0f, d);
+    const float cut = 8.0f * d;
+    const bool beyond = amax > cut;          // past the largest scale: a quotient might be infinite
+    uint32_t b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float2 x = unpack16<FP16>(w[i]);
+        if (beyond) {
+            x.x = fminf(fmaxf(x.x, -cut), cut);
+            x.y = fminf(fmaxf(x.y, -cut), cut);
+        }
+        const float p = x.x * rc, q = x.y * rc;
+        b[i] = e2m1_pair(fmaf(fmaf(-p, d, x.x), rc, p), fmaf(fmaf(-q, d, x.y), rc, q));
+    }
+    return make_uint2(b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24),
+                      b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24));
+}
+
+// A thread takes a group of sixteen, `lanes` threads a row, a CTA a few rows a
+// thread of the flattened (token, k heads then v heads) list; the rows are on
+// their way while the tokens' slots are looked up.
+template <int D, bool FP16>
+__global__ void __launch_bounds__(kNvAppendThreads) nvfp4_append_kernel(const NvAppendArgs a)
+{
+    constexpr int kLanes = D / kNvGroup;
+    constexpr int kRows = kNvAppendThreads / kLanes;
+    __shared__ long long page_of[kNvAppendMaxTokens];     // -1: nothing is written
+    __shared__ int slot_of[kNvAppendMaxTokens];
+    allow_dependent_launch();
+    grid_dependency_wait();
+    const int rows = 2 * a.heads;
+    const long long row0 = (long long)blockIdx.x * a.rows_per_cta;
+    const int count = (int)min((long long)a.rows_per_cta, (long long)a.tokens * rows - row0);
+    const long long token0 = row0 / rows;
+    const int first = (int)(row0 - token0 * rows);
+    const int nt = (first + count - 1) / rows + 1;
+    const int g = threadIdx.x % kLanes, i0 = threadIdx.x / kLanes;
+    uint4 v[kNvAppendUnits][2];
+    int tok[kNvAppendUnits], head[kNvAppendUnits];
+#pragma unroll
+    for (int u = 0; u < kNvAppendUnits; ++u) {
+        const int i = i0 + u * kRows;
+        tok[u] = (first + i) / rows;
+        head[u] = first + i - tok[u] * rows;
+        if (i >= count) continue;
+        const bool is_v = head[u] >= a.heads;
+        const int h = is_v ? head[u] - a.heads : head[u];
+        const long long at = is_v ? (token0 + tok[u]) * a.v_token + h * a.v_head
+                                  : (token0 + tok[u]) * a.k_token + h * a.k_head;
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(is_v ? a.v : a.k) + at) + 2 * g;
+        v[u][0] = __ldg(src);
+        v[u][1] = __ldg(src + 1);
+    }
+    for (int t = threadIdx.x; t < nt; t += kNvAppendThreads) {
+        const long long pos = a.pos64 ? __ldg(static_cast<const long long*>(a.positions) + token0 + t)
+                                      : (long long)__ldg(static_cast<const int32_t*>(a.positions) + token0 + t);
+        bool pad;
+        long long page;
+        int slot;
+        const bool ok = find_slot(a.slot, token0 + t, pos, pad, page, slot);
+        page_of[t] = ok ? page : -1;
+        slot_of[t] = slot;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kNvAppendUnits; ++u) {
+        if (i0 + u * kRows >= count) continue;
+        const long long page = page_of[tok[u]];
+        if (page < 0) continue;
+        const int slot = slot_of[tok[u]];
+        const bool is_v = head[u] >= a.heads;
+        const NvCache& c = is_v ? a.vc : a.kc;
+        const int h = is_v ? head[u] - a.heads : head[u];
+        uint32_t scale;
+        const uint2 codes = quantise16<FP16>(v[u], c.scale, scale);
+        *reinterpret_cast<uint2*>(c.codes + page * c.page + slot * c.slot + h * c.head + g * 8) = codes;
+        c.scales[page * c.s_page + slot * c.s_slot + h * c.s_head + g] = (uint8_t)scale;
+    }
+}
+
+constexpr int kReadThreads = 256;
+
+// Blocks of request b that are there.
+__device__ __forceinline__ int blocks_there(const NvReadArgs& a, int b)
+{
+    return min(blocks_of(__ldg(a.kv_lens + b)), a.width);
+}
+
+// The pages of all requests, each in strips (a head's keys, a head's values), in
+// order, cut into one contiguous range per CTA.  A thread turns eight values,
+// four bytes of codes, into sixteen bytes.
+template <int D, bool FP16>
+__global__ void __launch_bounds__(kReadThreads) nvfp4_read_kernel(const NvReadArgs a)
+{
+    __shared__ int start[2];               // request, block
+    __shared__ long long first_left[2];    // strip within the block, strips of the range
+    allow_dependent_launch();
+    grid_dependency_wait();
+    const int strips = 2 * a.heads;
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        long long total = 0;
+        for (int b = lane; b < a.batch; b += 32) total += blocks_there(a, b);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        const long long s0 = range_start(total * strips, gridDim.x, blockIdx.x);
+        const long long s1 = range_start(total * strips, gridDim.x, blockIdx.x + 1);
+        if (lane == 0) {
+            first_left[0] = s0 % strips;
+            first_left[1] = s1 - s0;
+        }
+        long long rem = s0 / strips;
+        if (s0 < s1) {
+            for (int c = 0; c < a.batch; c += 32) {
+                const long long n = c + lane < a.batch ? blocks_there(a, c + lane) : 0;
+                long long incl = n;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += u;
+                }
+                if (incl - n <= rem && rem < incl) {
+                    start[0] = c + lane;
+                    start[1] = (int)(rem - (incl - n));
+                }
+                const long long all = __shfl_sync(0xffffffffu, incl, 31);
+                if (rem < all) break;
+                rem -= all;
+            }
+        }
+    }
+    __syncthreads();
+    long long left = first_left[1];
+    if (left == 0) return;
+    int b = start[0], j = start[1], strip = (int)first_left[0];
+    const int unit = threadIdx.x % (D / 8), row0 = threadIdx.x / (D / 8);
+    constexpr int kStep = kReadThreads / (D / 8);
+    for (; left > 0; --left) {
+        const int len = __ldg(a.kv_lens + b);
+        const long long page = __ldg(a.block_table + b * a.bt_stride + j);
+        const long long to = __ldg(a.out_table + b * a.ot_stride + j);
+        if (page < 0 || page >= a.num_pages || to < 0 || to >= a.out_pages) {
+            if (threadIdx.x == 0) atomicOr(a.status, kStatusBadBlock);
+        } else {
+            const bool is_v = strip >= a.heads;
+            const int h = is_v ? strip - a.heads : strip;
+            const NvCache& c = is_v ? a.vc : a.kc;
+            const int rows = min(len - j * kBlockKeys, kBlockKeys);
+            const uint8_t* codes = c.codes + page * c.page + h * c.head + unit * 4;
+            const uint8_t* scales = c.scales + page * c.s_page + h * c.s_head + unit / 2;
+            uint16_t* out = static_cast<uint16_t*>(is_v ? a.v_out : a.k_out) +
+                            (is_v ? to * a.v_page + h * a.v_head : to * a.k_page + h * a.k_head) + unit * 8;
+            const long long slot = is_v ? a.v_slot : a.k_slot;
+            uint32_t w[kBlockKeys / kStep], s[kBlockKeys / kStep];
+#pragma unroll
+            for (int i = 0; i < kBlockKeys / kStep; ++i) {
+                const int r = row0 + i * kStep;
+                if (r >= rows) continue;
+                w[i] = __ldg(reinterpret_cast<const uint32_t*>(codes + r * c.slot));
+                s[i] = __ldg(scales + r * c.s_slot);
+            }
+#pragma unroll
+            for (int i = 0; i < kBlockKeys / kStep; ++i) {
+                const int r = row0 + i * kStep;
+                if (r >= rows) continue;
+                uint32_t x[4], y[4];
+                e2m1x8_to_f16x2x4(w[i], x);
+                const uint32_t sc = e4m3_to_f16x2_dup(s[i]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = unpack16<true>(mul_f16x2(x[e], sc));
+                    y[e] = pack16<FP16>(f.x * c.scale, f.y * c.scale);
+                }
+                *reinterpret_cast<uint4*>(out + r * slot) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+        }
+        if (++strip == strips) {
+            strip = 0;
+            if (++j >= blocks_there(a, b)) {
+                j = 0;
+                ++b;
+                while (b < a.batch && blocks_there(a, b) == 0) ++b;
+                if (b >= a.batch) return;
+            }
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_nvfp4_append(const NvAppendArgs& a, cudaStream_t stream)
+{
+    const long long rows = 2LL * a.tokens * a.heads;
+    const dim3 grid((unsigned)((rows + a.rows_per_cta - 1) / a.rows_per_cta));
+    if (a.dim == 128)
+        return a.fp16 ? launch_dependent(nvfp4_append_kernel<128, true>, grid, kNvAppendThreads, 0, stream, a)
+                      : launch_dependent(nvfp4_append_kernel<128, false>, grid, kNvAppendThreads, 0, stream, a);
+    return a.fp16 ? launch_dependent(nvfp4_append_kernel<64, true>, grid, kNvAppendThreads, 0, stream, a)
+                  : launch_dependent(nvfp4_append_kernel<64, false>, grid, kNvAppendThreads, 0, stream, a);
+}
+
+cudaError_t launch_nvfp4_read(const NvReadArgs& a, int sm_count, cudaStream_t stream)
+{
+    const dim3 grid((unsigned)(sm_count * 8));
+    if (a.dim == 128)
+        return a.fp16 ? launch_dependent(nvfp4_read_kernel<128, true>, grid, kReadThreads, 0, stream, a)
+                      : launch_dependent(nvfp4_read_kernel<128, false>, grid, kReadThreads, 0, stream, a);
+    return a.fp16 ? launch_dependent(nvfp4_read_kernel<64, true>, grid, kReadThreads, 0, stream, a)
+                  : launch_dependent(nvfp4_read_kernel<64, false>, grid, kReadThreads, 0, stream, a);
+}
+
+}  // namespace pml

@@ -1,0 +1,95 @@
+// Host-side launch records of the operators over K/V caches held in 4 bits.
+// Internal to the library: the public C ABI is include/pml.h.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "serving.h"
+
+namespace pml {
+
+constexpr int kNvGroup = 16;       // values of a scale
+
+// One of the two caches: a row's codes and its scales.  Strides in bytes.
+struct NvCache {
+    uint8_t* codes;
+    uint8_t* scales;
+    long long page, slot, head;
+    long long s_page, s_slot, s_head;
+    float scale;                   // of all values, a power of two
+};
+
+struct NvAppendArgs {
+    SlotArgs slot;
+    const void* positions;         // int32 or int64, one per token
+    const void* k;
+    const void* v;
+    long long k_token, k_head;     // elements
+    long long v_token, v_head;
+    NvCache kc, vc;
+    int pos64;
+    int fp16;                      // 1 fp16, 0 bf16
+    int tokens;
+    int heads;
+    int dim;
+    int rows_per_cta;              // of the tokens' 2 * heads rows each
+};
+
+constexpr int kNvAppendThreads = 256;
+constexpr int kNvAppendUnits = 4;      // groups of a thread
+constexpr int kNvAppendMaxTokens = 128; // of a CTA, in part
+
+struct NvReadArgs {
+    NvCache kc, vc;
+    const int32_t* block_table;
+    const int32_t* out_table;
+    const int32_t* kv_lens;
+    unsigned int* status;
+    void* k_out;
+    void* v_out;
+    long long k_page, k_slot, k_head;   // elements, of the outputs
+    long long v_page, v_slot, v_head;
+    long long bt_stride, ot_stride;
+    long long num_pages, out_pages;
+    int width;                     // columns that both tables have
+    int batch;
+    int heads;
+    int dim;
+    int fp16;
+};
+
+struct NvAttnArgs {
+    NvCache kc, vc;
+    const void* q;
+    void* out;
+    float* lse;                    // [tokens][heads], may be null
+    const int32_t* block_table;
+    const int32_t* kv_lens;        // per request
+    const int32_t* cu_q;           // batch + 1 token offsets; null: q_per_request each
+    const int32_t* requests;       // selected: one per token
+    const int32_t* selected;       // selected: [tokens][sel_stride] positions
+    unsigned int* status;
+    long long q_token, q_head;     // elements
+    long long out_token, out_head;
+    long long bt_stride;
+    long long sel_stride;
+    long long num_pages;
+    int bt_width;
+    int batch;                     // requests (rows of the block table)
+    int tokens;
+    int q_per_request;
+    int kv_heads;
+    int group;                     // query heads per kv head
+    int sel_k;                     // selected: entries per token
+    int causal;
+    int window;                    // > 0: only keys past position - window
+    float scale;                   // softmax scale times the keys' scale
+    float scale_log2;              // the same times log2(e)
+};
+
+cudaError_t launch_nvfp4_append(const NvAppendArgs& a, cudaStream_t stream);
+cudaError_t launch_nvfp4_read(const NvReadArgs& a, int sm_count, cudaStream_t stream);
+cudaError_t launch_nvfp4_attention(int head_dim, bool fp16, const NvAttnArgs& a, cudaStream_t stream);
+
+}  // namespace pml
