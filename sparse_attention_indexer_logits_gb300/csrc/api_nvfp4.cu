@@ -97,7 +97,8 @@ int attention_call(NvAttnArgs& a, const void* q, int64_t q_token, int64_t q_head
     a.group = num_heads / kv_heads;
     a.scale = softmax_scale * a.kc.scale;
     a.scale_log2 = a.scale * 1.4426950408889634f;
-    e = launch_nvfp4_attention(head_dim, dtype == PML_DTYPE_FLOAT16, a, static_cast<cudaStream_t>(stream));
+    e = launch_nvfp4_attention(head_dim, dtype == PML_DTYPE_FLOAT16, a, dev.sm_count, workspace, workspace_bytes,
+                               static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PML_OK : cuda_fail(e);
 }
 

@@ -1,160 +1,138 @@
-// Attention of new tokens over K/V caches held in 4 bits.
-//
-//   out[t, h] = sum_p softmax_p(scale * q[t, h] . k_p) v_p
-//
-// over values code * s * g (codes E2M1, s the E4M3 scale of sixteen values, g
-// the cache's power of two) and the positions p that token t may see.  One CTA
-// per (token, head): each warp takes every fourth key, a lane the same few
-// elements of each row, with a running maximum and sum; the warps' results are
-// joined at the end.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_runtime.h>
-
-#include "common.cuh"
-#include "dependent.cuh"
-#include "nvfp4_cache.h"
-#include "ptx.cuh"
+// Dispatch of the attention over caches held in 4 bits, and the kernel that
+// joins the pieces of items that several CTAs shared.
+#include "nvfp4_attention.cuh"
 
 namespace pml {
 
+template <int D>
+cudaError_t launch_nvfp4_attention_dim(bool fp16, int tiles, const NvAttnArgs& a, const nvattn::Pieces& wp,
+                                       const nvattn::Pieces& cp, int num_ctas, cudaStream_t stream);
+extern template cudaError_t launch_nvfp4_attention_dim<64>(bool, int, const NvAttnArgs&, const nvattn::Pieces&,
+                                                           const nvattn::Pieces&, int, cudaStream_t);
+extern template cudaError_t launch_nvfp4_attention_dim<128>(bool, int, const NvAttnArgs&, const nvattn::Pieces&,
+                                                            const nvattn::Pieces&, int, cudaStream_t);
+
 namespace {
 
-constexpr int kWarps = 4;
+using namespace nvattn;
 
-template <bool FP16>
-__device__ __forceinline__ float load16(const void* p, long long at)
-{
-    if constexpr (FP16) return __half2float(static_cast<const __half*>(p)[at]);
-    else return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]);
-}
+constexpr int kJoinWarps = 8;
 
-template <int D, bool FP16>
-__global__ void __launch_bounds__(kWarps * 32) nvfp4_attention_kernel(const NvAttnArgs a)
+// A CTA whose pieces ended with an item that it had begun (slot 1) owns the
+// join: the item's other pieces are slot 0 of the following CTAs, up to the one
+// that holds its end.  A CTA here takes one row; each warp a part of the pieces,
+// in the order of their numbers, a lane two or four columns.
+template <int D, bool FP16, int NT>
+__global__ void __launch_bounds__(kJoinWarps * 32) nvfp4_join_kernel(const NvAttnArgs a, const Pieces cp, int num_ctas)
 {
-    constexpr int E = D / 32;              // elements of a lane
-    __shared__ float part[kWarps][D + 2];
+    constexpr int N = D / 32, kRows = 8 * NT;
+    __shared__ float part[kJoinWarps][N + 2][32];
     allow_dependent_launch();
     grid_dependency_wait();
-    const long long t = blockIdx.x;
-    const int head = blockIdx.y, kvh = head / a.group;
+    const int owner = blockIdx.x, row = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int req, kv, lo = 0, hi;
-    if (a.selected) {
-        req = __ldg(a.requests + t);
-        if (req >= a.batch && threadIdx.x == 0) atomicOr(a.status, kStatusBadRequest);
-        const bool fine = req >= 0 && req < a.batch;
-        kv = fine ? max(__ldg(a.kv_lens + req), 0) : 0;
-        req = fine ? req : 0;
-        hi = a.sel_k;
-    } else {
-        int start, end;
-        if (a.cu_q) {
-            int l = 0, r = a.batch;        // the last request that begins at or before t
-            while (r - l > 1) {
-                const int m = (l + r) >> 1;
-                if (__ldg(a.cu_q + m) <= t) l = m;
-                else r = m;
-            }
-            req = l;
-            start = __ldg(a.cu_q + l);
-            end = __ldg(a.cu_q + l + 1);
-            if (t < start || t >= end) return;
-        } else {
-            req = (int)(t / a.q_per_request);
-            start = req * a.q_per_request;
-            end = start + a.q_per_request;
+    const int* rec = cp.rec + (owner * 2LL + 1) * kPcInts;
+    // the first CTA after the owner that holds the item's end
+    auto ends = [&](int cta) {
+        if (cta >= num_ctas) return false;
+        const int* p = cp.rec + cta * 2LL * kPcInts;
+        return p[kPcUsed] && p[kPcLast];
+    };
+    unsigned who = __ballot_sync(0xffffffffu, ends(owner + 1 + lane));
+    if (!rec[kPcUsed] || row >= rec[kPcNtok] * rec[kPcHeads]) return;
+    int end = owner + 1;
+    while (!who && end + 32 < num_ctas) {
+        end += 32;
+        who = __ballot_sync(0xffffffffu, ends(end + lane));
+    }
+    if (!who) return;                             // never: an item's end is in some range
+    end += __ffs(who) - 1;
+    const int pieces = end - owner + 1;
+    Joined<N> x;
+    const int last = pieces * (warp + 1) / kJoinWarps;
+#pragma unroll 4
+    for (int p = pieces * warp / kJoinWarps; p < last; ++p) {
+        const int slot = p == 0 ? 1 : 0;
+        const long long at = (owner + p) * 2LL + slot;
+        const bool used = cp.rec[at * kPcInts + kPcUsed];      // (a range without a step left none)
+        float2 st = cp.stats[at * kRows + row];
+        float v[N];
+        load_cols<N>(cp.part + (at * kRows + row) * D + lane * N, v);
+        if (!used) {
+            st = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] = 0.0f;
         }
-        kv = max(__ldg(a.kv_lens + req), 0);
-        const long long pos = (long long)kv - (end - t);
-        hi = kv;
-        if (a.causal) hi = (int)max(min((long long)hi, pos + 1), 0ll);
-        if (a.window > 0) lo = (int)max(pos - a.window + 1, 0ll);
+        x.add(st.x, st.y, v);
     }
-    const long long there = (long long)a.bt_width * kBlockKeys;
-    kv = (int)min((long long)kv, there);
-    if (!a.selected) hi = min(hi, kv);
-    float q[E], acc[E], m = -INFINITY, l = 0.0f;
+    part[warp][0][lane] = x.top;
+    part[warp][1][lane] = x.sum;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        q[e] = load16<FP16>(a.q, t * a.q_token + head * a.q_head + lane * E + e);
-        acc[e] = 0.0f;
-    }
-    for (int i = lo + warp; i < hi; i += kWarps) {
-        int p = i;
-        if (a.selected) {
-            p = __ldg(a.selected + t * a.sel_stride + i);
-            if (p < 0 || p >= kv) continue;
-        }
-        long long page = __ldg(a.block_table + req * a.bt_stride + (p >> 6));
-        if (page < 0 || page >= a.num_pages) {
-            if (lane == 0) atomicOr(a.status, kStatusBadBlock);
-            page = 0;
-        }
-        auto row = [&](const NvCache& c, float (&x)[E]) {
-            const uint8_t* codes = c.codes + page * c.page + (p & 63) * c.slot + kvh * c.head + lane * (E / 2);
-            const uint32_t s = e4m3_to_f16x2_dup(__ldg(c.scales + page * c.s_page + (p & 63) * c.s_slot +
-                                                       kvh * c.s_head + lane * E / kNvGroup));
-#pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                const uint32_t h = mul_f16x2(e2m1x2_to_f16x2(__ldg(codes + e / 2)), s);
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-                x[e] = f.x;
-                x[e + 1] = f.y;
-            }
-        };
-        float k[E], v[E], dot = 0.0f;
-        row(a.kc, k);
-        row(a.vc, v);
-#pragma unroll
-        for (int e = 0; e < E; ++e) dot = fmaf(q[e], k[e], dot);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        const float z = dot * a.scale, next = fmaxf(m, z);
-        const float f = m == -INFINITY ? 0.0f : expf(m - next), w = z == -INFINITY ? 0.0f : expf(z - next);
-        m = next;
-        l = l * f + w;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = acc[e] * f + w * v[e];
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) part[warp][lane * E + e] = acc[e];
-    if (lane == 0) {
-        part[warp][D] = m;
-        part[warp][D + 1] = l;
-    }
+    for (int k = 0; k < N; ++k) part[warp][2 + k][lane] = x.acc[k];
     __syncthreads();
-    if (warp != 0) return;
-    float top = -INFINITY, sum = 0.0f;
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part[w][D]);
+    if (warp > 0) return;
+    Joined<N> y;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-    for (int w = 0; w < kWarps; ++w) {
-        const float f = part[w][D] == -INFINITY ? 0.0f : expf(part[w][D] - top);
-        sum += part[w][D + 1] * f;
+    for (int q = 0; q < kJoinWarps; ++q) {
+        float v[N];
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += part[w][lane * E + e] * f;
+        for (int k = 0; k < N; ++k) v[k] = part[q][2 + k][lane];
+        y.add(part[q][0][lane], part[q][1][lane], v);
     }
-    const float inv = sum > 0.0f || sum != sum ? a.vc.scale / sum : 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const long long at = t * a.out_token + head * a.out_head + lane * E + e;
-        if constexpr (FP16) static_cast<__half*>(a.out)[at] = __float2half_rn(acc[e] * inv);
-        else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(acc[e] * inv);
-    }
-    if (lane == 0 && a.lse) a.lse[t * a.kv_heads * a.group + head] = sum == 0.0f ? -INFINITY : top + logf(sum);
+    write_joined<FP16, N>(a, y, rec[kPcTok0], rec[kPcHead], rec[kPcHeads], row, lane * N);
+}
+
+template <int D, bool FP16, int NT>
+cudaError_t launch_join(const NvAttnArgs& a, const Pieces& cp, int num_ctas, cudaStream_t stream)
+{
+    return launch_dependent(nvfp4_join_kernel<D, FP16, NT>, dim3((unsigned)num_ctas, 8 * NT), kJoinWarps * 32, 0,
+                            stream, a, cp, num_ctas);
+}
+
+template <int D>
+cudaError_t launch_join_dim(bool fp16, int tiles, const NvAttnArgs& a, const Pieces& cp, int num_ctas,
+                            cudaStream_t stream)
+{
+    if (tiles == 1)
+        return fp16 ? launch_join<D, true, 1>(a, cp, num_ctas, stream) : launch_join<D, false, 1>(a, cp, num_ctas, stream);
+    return fp16 ? launch_join<D, true, 2>(a, cp, num_ctas, stream) : launch_join<D, false, 2>(a, cp, num_ctas, stream);
+}
+
+// `n` pieces of two slots from `at` on.
+Pieces take(uint8_t*& at, int64_t n, int rows, int dim)
+{
+    Pieces p;
+    p.part = reinterpret_cast<float*>(at);
+    at += n * 2 * rows * dim * 4;
+    p.stats = reinterpret_cast<float2*>(at);
+    at += n * 2 * rows * 8;
+    p.rec = reinterpret_cast<int*>(at);
+    at += n * 2 * kPcInts * 4;
+    return p;
 }
 
 }  // namespace
 
-cudaError_t launch_nvfp4_attention(int head_dim, bool fp16, const NvAttnArgs& a, cudaStream_t stream)
+cudaError_t launch_nvfp4_attention(int head_dim, bool fp16, NvAttnArgs& a, int num_ctas, void* workspace,
+                                   int64_t workspace_bytes, cudaStream_t stream)
 {
-    const dim3 grid((unsigned)a.tokens, (unsigned)(a.kv_heads * a.group));
-    if (head_dim == 128)
-        return fp16 ? launch_dependent(nvfp4_attention_kernel<128, true>, grid, kWarps * 32, 0, stream, a)
-                    : launch_dependent(nvfp4_attention_kernel<128, false>, grid, kWarps * 32, 0, stream, a);
-    return fp16 ? launch_dependent(nvfp4_attention_kernel<64, true>, grid, kWarps * 32, 0, stream, a)
-                : launch_dependent(nvfp4_attention_kernel<64, false>, grid, kWarps * 32, 0, stream, a);
+    // Items of 8 or of 16 rows: the larger ones where a request's tokens fill them.
+    const long long per_request = a.selected ? 1 : (a.tokens + a.batch - 1) / a.batch;
+    const int tiles = per_request * a.group > 8 ? 2 : 1, rows = 8 * tiles;
+    a.head_blocks = (a.group + rows - 1) / rows;
+    a.block_heads = (a.group + a.head_blocks - 1) / a.head_blocks;
+    a.tile_tokens = a.selected || a.group > rows ? 1 : rows / a.group;
+    const int warps = head_dim == 128 ? (tiles == 1 ? Cfg<128, 1>::kWarps : Cfg<128, 2>::kWarps)
+                                      : (tiles == 1 ? Cfg<64, 1>::kWarps : Cfg<64, 2>::kWarps);
+    uint8_t* at = static_cast<uint8_t*>(workspace);
+    const Pieces wp = take(at, (int64_t)num_ctas * warps, rows, head_dim);
+    const Pieces cp = take(at, num_ctas, rows, head_dim);
+    if (at - static_cast<uint8_t*>(workspace) > workspace_bytes) return cudaErrorInvalidValue;    // never
+    cudaError_t e = head_dim == 128 ? launch_nvfp4_attention_dim<128>(fp16, tiles, a, wp, cp, num_ctas, stream)
+                                    : launch_nvfp4_attention_dim<64>(fp16, tiles, a, wp, cp, num_ctas, stream);
+    if (e != cudaSuccess) return e;
+    return head_dim == 128 ? launch_join_dim<128>(fp16, tiles, a, cp, num_ctas, stream)
+                           : launch_join_dim<64>(fp16, tiles, a, cp, num_ctas, stream);
 }
 
 }  // namespace pml

@@ -1,0 +1,961 @@
+// Attention of new tokens over K/V caches held in 4 bits, on sm_103a.
+//
+//   out[t, h] = sum_p softmax_p(scale * q[t, h] . k_p) v_p
+//
+// over values code * s * g (codes E2M1, s the E4M3 scale of sixteen values, g
+// the cache's power of two) and the positions p that token t may see: those of
+// its request up to its own (causal), past position - window (window > 0), or
+// the ones a list names.  code * s has at most six significant bits and lies
+// between 2^-10 and 2688: exact in fp16, the type of both products.  One pass
+// with a running maximum m and sum l: P = 2^(c S - m + 7), O += P V, rescaled
+// only when a row's maximum has grown by more than 2^8.
+//
+// What it is bound by.  A row of 128 values is 72 bytes, read once for 8 or 16
+// query rows: at HBM's rate an SM gets a key and its value every 6.5 cycles.
+// The tensor work is a fiftieth of what the tensor core could do in that time;
+// turning codes into fp16 is what takes instructions, so the codes go straight
+// from shared memory into the operand registers of the warp's own matrix
+// instructions.  (Operands of the larger tensor-core instruction lie in shared
+// memory: its tiles would have to be written there and read again, four times
+// the bytes of the codes, with a hand-over for each tile.)
+//
+// Warps work alone.  An item is 8 or 16 rows ((token, head) pairs that share a
+// kv head) and the keys they see, in steps of 32.  The steps of all items, in
+// order, are cut into one contiguous range per warp.  A warp copies its keys'
+// codes and scales into a ring of its own (cp.async, a few steps ahead) and
+// waits for nobody.  Pieces of items that several warps of a CTA shared are
+// joined at the CTA's end, those of several CTAs by a second kernel; all in a
+// fixed order.
+//
+// Operands (m16n8k16; g = lane / 4, t = lane % 4):
+//   S = Q K^T   Q's rows are A.  The order of the summed elements is free, so
+//               lane t takes elements (D/4) t .. of every row: of a key 16 (8)
+//               bytes in one load, two (one) scales
+//   O^T = V^T P^T   V^T is A: its rows are elements, lane g takes (D/8) g .. of
+//               a value, one scale; its columns are keys, two to a register:
+//               the nibbles of two keys are interleaved into bytes before they
+//               are converted.  P^T is B, which is how S leaves its product
+// A score's column c of eight is key (c / 2) + 4 (c & 1): with K's rows stored
+// in that order and V's 16-byte chunks swapped in every other pair of rows all
+// loads are free of bank conflicts.
+//
+// Masked places never reach a result, whatever they hold: their scores are
+// -inf; rows outside the item's keys are zeros in shared memory; and where a
+// value under a NaN scale is visible to some rows and hidden from others, that
+// step's product is made row by row.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "dependent.cuh"
+#include "nvfp4_cache.h"
+#include "ptx.cuh"
+
+namespace pml {
+namespace nvattn {
+
+constexpr int kStepKeys = 32;
+// Units of work: a step is one, beginning and ending an item two.
+constexpr int kItemUnits = 2;
+constexpr float kPLog2 = 7.0f;         // P is 2^7 times the weights: fp16 keeps the small ones' bits
+constexpr float kGrow = 8.0f;          // a reference may be too low by 2^8: P stays below 2^15
+
+template <int D, int NT>
+struct Cfg {
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kWarps = NT == 1 ? 16 : 12;       // 128 or 168 registers a thread
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kCode = D / 2, kScale = D / 16;   // bytes of a row
+    static constexpr int kStageBytes = 2 * kStepKeys * (kCode + kScale);
+    static constexpr int kStages = D == 128 ? (NT == 1 ? 3 : 4) : (NT == 1 ? 4 : 5);
+    static constexpr int kRing = kStages * kStageBytes;    // of a warp
+    static constexpr int kMasks = kWarps * kRing;          // uint32 [kWarps][8]
+    static constexpr int kSums = kMasks + kWarps * 32;     // long long [kWarps]
+    static constexpr int kRecs = kSums + kWarps * 8;       // pieces of the CTA
+    static constexpr int kTotal = kRecs + kWarps * 2 * 4;
+    static_assert(kTotal <= 232448, "shared memory of a CTA");
+    static_assert(kAttnMaxBatch * 8 <= kWarps * kRing, "a number per request fits the ring");
+};
+
+// piece record in the workspace
+enum { kPcUsed, kPcTok0, kPcNtok, kPcHead, kPcHeads, kPcLast };
+constexpr int kPcInts = 8;
+
+// Where rows of a piece lie.
+struct Pieces {
+    int* rec;          // [n][2][kPcInts]
+    float2* stats;     // [n][2][rows] (maximum, sum)
+    float* part;       // [n][2][rows][D]
+};
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <bool FP16>
+__device__ __forceinline__ uint32_t pack_out(float lo, float hi)
+{
+    uint32_t r;
+    if constexpr (FP16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// c += A B, A 16 x 16 and B 16 x 8 in fp16
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                    uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Bytes, or zeros (bytes = 0: src is not read).
+template <int N>
+__device__ __forceinline__ void cp_async_zfill(uint32_t dst, const void* src, uint32_t bytes)
+{
+    if constexpr (N == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+                     "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes)
+                     : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst),
+                     "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "n"(N)
+                     : "memory");
+}
+
+__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// Two E4M3 codes (low byte -> low half) to f16x2, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes)
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
+    return h;
+}
+
+__device__ __forceinline__ bool f16x2_has_nan(uint32_t h)
+{
+    return (h & 0x7fffu) > 0x7c00u || ((h >> 16) & 0x7fffu) > 0x7c00u;
+}
+
+// ------------------------------------------------------------------ items
+
+__device__ __forceinline__ void request_of(const NvAttnArgs& a, int b, int& tok0, int& nq, int& kv)
+{
+    if (a.cu_q != nullptr) {
+        const int s = __ldg(a.cu_q + b), e = __ldg(a.cu_q + b + 1);
+        tok0 = min(max(s, 0), a.tokens);
+        nq = min(max(e, tok0), a.tokens) - tok0;
+    } else {
+        tok0 = b * a.q_per_request;
+        nq = a.q_per_request;
+    }
+    kv = max(__ldg(a.kv_lens + b), 0);
+}
+
+// The tokens of tile `tile` of a request with nq new tokens of kv, and the keys
+// that some of them may see.
+struct Span {
+    int t0, ntok;
+    int lo, hi;
+    int j0, n;       // steps
+};
+
+__device__ __forceinline__ Span span_of(const NvAttnArgs& a, int nq, int kv, int tile)
+{
+    Span s;
+    s.t0 = tile * a.tile_tokens;
+    s.ntok = min(a.tile_tokens, nq - s.t0);
+    const long long there = min((long long)kv, (long long)a.bt_width * kBlockKeys);
+    const long long pos0 = (long long)kv - nq + s.t0;      // position of the tile's first token
+    long long hi = there, lo = 0;
+    if (a.causal) hi = min(hi, pos0 + s.ntok);
+    if (a.window > 0) lo = max(lo, pos0 - a.window + 1);
+    if (hi <= lo) { hi = 0; lo = 0; }
+    s.lo = (int)lo;
+    s.hi = (int)hi;
+    s.j0 = s.lo / kStepKeys;
+    s.n = s.hi > 0 ? (s.hi - 1) / kStepKeys + 1 - s.j0 : 0;
+    return s;
+}
+
+__device__ __forceinline__ int tiles_of(const NvAttnArgs& a, int nq)
+{
+    return (nq + a.tile_tokens - 1) / a.tile_tokens;
+}
+
+// Where a warp's range begins, and how many units it has.
+struct Start {
+    int b, tile, head;   // selected: b is the token; head: of kv_heads * head_blocks
+    int at;              // unit of the item
+    long long left;
+};
+
+template <int D, int NT>
+__device__ __forceinline__ Start find_start(const NvAttnArgs& a, uint8_t* smem)
+{
+    using C = Cfg<D, NT>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int heads = a.kv_heads * a.head_blocks;
+    long long* units = reinterpret_cast<long long*>(smem);
+    long long* sums = reinterpret_cast<long long*>(smem + C::kSums);
+    long long total = 0;
+    for (int b0 = warp * 32; b0 < a.batch; b0 += C::kThreads) {
+        const int b = b0 + lane;
+        int tok0 = 0, nq = 0, kv = 0;
+        if (b < a.batch) request_of(a, b, tok0, nq, kv);
+        const int tiles = tiles_of(a, nq);
+        long long u = 0;
+        if (tiles <= 4)
+            for (int i = 0; i < tiles; ++i) u += kItemUnits + span_of(a, nq, kv, i).n;
+        // long ones by the whole warp
+        for (unsigned who = __ballot_sync(0xffffffffu, tiles > 4); who; who &= who - 1) {
+            const int l = __ffs(who) - 1;
+            const int n = __shfl_sync(0xffffffffu, nq, l), k = __shfl_sync(0xffffffffu, kv, l);
+            long long v = 0;
+            for (int i = lane; i < tiles_of(a, n); i += 32) v += kItemUnits + span_of(a, n, k, i).n;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            if (lane == l) u = v;
+        }
+        if (b < a.batch) units[b] = u;
+        total += u;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (lane == 0) sums[warp] = total;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < C::kWarps; ++w) total += sums[w];
+    total *= heads;
+    Start s = {0, 0, 0, 0, 0};
+    const int workers = gridDim.x * C::kWarps, me = blockIdx.x * C::kWarps + warp;
+    long long rem = range_start(total, workers, me);
+    s.left = range_start(total, workers, me + 1) - rem;
+    if (s.left == 0) return s;
+    // the request that holds unit `rem`, 32 at a time
+    bool found = false;
+    for (int c = 0; c < a.batch; c += 32) {
+        long long incl = c + lane < a.batch ? units[c + lane] * heads : 0;
+        const long long mine = incl;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        const unsigned who = __ballot_sync(0xffffffffu, incl - mine <= rem && rem < incl);
+        if (who) {
+            const int l = __ffs(who) - 1;
+            s.b = c + l;
+            rem -= __shfl_sync(0xffffffffu, incl - mine, l);
+            found = true;
+            break;
+        }
+        rem -= __shfl_sync(0xffffffffu, incl, 31);
+    }
+    // its tile, 32 at a time
+    int tok0, nq, kv;
+    request_of(a, s.b, tok0, nq, kv);
+    const int tiles = tiles_of(a, nq);
+    for (int c = 0; found && c < tiles; c += 32) {
+        const int per = c + lane < tiles ? kItemUnits + span_of(a, nq, kv, c + lane).n : 0;
+        long long incl = (long long)per * heads;
+        const long long mine = incl;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        const unsigned who = __ballot_sync(0xffffffffu, incl - mine <= rem && rem < incl);
+        if (who) {
+            const int l = __ffs(who) - 1;
+            s.tile = c + l;
+            const int n = __shfl_sync(0xffffffffu, per, l);
+            rem -= __shfl_sync(0xffffffffu, incl - mine, l);
+            s.head = (int)(rem / n);
+            s.at = (int)(rem - (long long)s.head * n);
+            return s;
+        }
+        rem -= __shfl_sync(0xffffffffu, incl, 31);
+    }
+    s.left = 0;            // never
+    return s;
+}
+
+// ------------------------------------------------------------------ pieces joined
+
+// Parts of a row joined in turn: N of its columns under a running maximum.
+template <int N>
+struct Joined {
+    float top = -INFINITY, sum = 0.0f, acc[N] = {};
+
+    __device__ void add(float m, float l, const float (&v)[N])
+    {
+        const float next = fmaxf(top, m);
+        const float f = top == -INFINITY ? 0.0f : exp2_approx(top - next);
+        const float g = m == -INFINITY ? 0.0f : exp2_approx(m - next);
+        top = next;
+        sum = sum * f + l * g;
+#pragma unroll
+        for (int k = 0; k < N; ++k) acc[k] = fmaf(v[k], g, acc[k] * f);
+    }
+};
+
+template <int N>
+__device__ __forceinline__ void load_cols(const float* p, float (&v)[N])
+{
+    static_assert(N == 2 || N == 4, "columns");
+    if constexpr (N == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(p);
+        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    } else {
+        const float2 x = *reinterpret_cast<const float2*>(p);
+        v[0] = x.x; v[1] = x.y;
+    }
+}
+
+// A row's scaled output and log-sum from its sums (2^7 times their size).
+__device__ __forceinline__ float inverse_of(float sum, float v_scale)
+{
+    return sum > 0.0f || sum != sum ? v_scale / sum : 0.0f;
+}
+
+__device__ __forceinline__ float log_sum_of(float top, float sum)
+{
+    return sum == 0.0f ? -INFINITY : (top - kPLog2) * 0.6931471805599453f + logf(sum);
+}
+
+// N columns of row `row` of an item, joined.
+template <bool FP16, int N>
+__device__ __forceinline__ void write_joined(const NvAttnArgs& a, const Joined<N>& x, int tok0, int head0, int heads,
+                                             int row, int col)
+{
+    const float inv = inverse_of(x.sum, a.vc.scale);
+    const long long token = tok0 + row / heads;
+    const int head = head0 + row % heads;
+    uint16_t* out = static_cast<uint16_t*>(a.out) + token * a.out_token + head * a.out_head + col;
+    if constexpr (N == 4)
+        *reinterpret_cast<uint2*>(out) = make_uint2(pack_out<FP16>(x.acc[0] * inv, x.acc[1] * inv),
+                                                    pack_out<FP16>(x.acc[2] * inv, x.acc[3] * inv));
+    else
+        *reinterpret_cast<uint32_t*>(out) = pack_out<FP16>(x.acc[0] * inv, x.acc[1] * inv);
+    if (col == 0 && a.lse != nullptr)
+        a.lse[token * a.kv_heads * a.group + head] = log_sum_of(x.top, x.sum);
+}
+
+// ------------------------------------------------------------------ the kernel
+
+template <int D, bool FP16, bool SEL, int NT>
+__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
+    nvfp4_attention_kernel(const NvAttnArgs a, const Pieces wp, const Pieces cp)
+{
+    using C = Cfg<D, NT>;
+    constexpr int S = C::kStages;
+    constexpr int KS = D / 16;             // 16-element steps of a score, 16-element blocks of an output
+    constexpr int CB = C::kCode, SB = C::kScale;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    allow_dependent_launch();
+    grid_dependency_wait();
+
+    Start start;
+    const int sel_n = SEL ? (a.sel_k + kStepKeys - 1) / kStepKeys : 0;
+    const int heads = a.kv_heads * a.head_blocks;
+    if constexpr (SEL) {
+        const int per = sel_n + kItemUnits;
+        const int workers = gridDim.x * C::kWarps, me = blockIdx.x * C::kWarps + warp;
+        const long long total = (long long)a.tokens * heads * per;
+        const long long s0 = range_start(total, workers, me);
+        start.left = range_start(total, workers, me + 1) - s0;
+        const long long item = s0 / per;
+        start.at = (int)(s0 - item * per);
+        start.b = (int)(item / heads);
+        start.head = (int)(item - (long long)start.b * heads);
+        start.tile = 0;
+    } else {
+        start = find_start<D, NT>(a, smem);
+        __syncthreads();                   // (the numbers lie in the ring)
+    }
+
+    const uint32_t ring = smem_addr(smem) + warp * C::kRing;
+    volatile uint32_t* masks = reinterpret_cast<volatile uint32_t*>(smem + C::kMasks) + warp * 8;
+    constexpr int kKC = 0, kVC = kStepKeys * CB, kKS = 2 * kStepKeys * CB, kVS = kKS + kStepKeys * SB;
+    const long long worker = (long long)blockIdx.x * C::kWarps + warp;
+    int* rec = wp.rec + worker * 2 * kPcInts;
+    uint8_t* used = smem + C::kRecs + warp * 8;           // [2] used, [2] last
+    if (lane < 8) used[lane] = 0;
+
+    // copies: this lane's row and 16-byte chunk of 8 (16) rows of codes
+    constexpr int kRowLanes = CB / 16, kInstRows = 32 / kRowLanes;
+    const int sub = lane / kRowLanes, chunk = lane % kRowLanes;
+    auto column = [](int r) { return (r & ~7) | ((r & 3) << 1) | ((r >> 2) & 1); };
+    const uint32_t k_to = kKC + column(sub) * CB + chunk * 16;
+    const uint32_t v_to = kVC + sub * CB + (D == 128 ? (chunk ^ (((sub >> 1) & 1) << 1)) : chunk) * 16;
+    const uint32_t ks_to = kKS + column(lane) * SB, vs_to = kVS + lane * SB;
+
+    int b = start.b, tile = start.tile, head = start.head, at = start.at;
+    long long left = start.left;
+    int cur_b = -1, tok0 = 0, nq = 0, kv = 0, tiles = 0;
+    while (left > 0) {
+        Span sp;
+        int req, token;
+        if constexpr (SEL) {
+            req = __ldg(a.requests + b);
+            if (req >= a.batch && lane == 0) atomicOr(a.status, kStatusBadRequest);
+            const bool fine = req >= 0 && req < a.batch;
+            kv = fine ? max(__ldg(a.kv_lens + req), 0) : 0;
+            kv = (int)min((long long)kv, (long long)a.bt_width * kBlockKeys);
+            req = fine ? req : 0;
+            sp = {0, 1, 0, kv, 0, sel_n};
+            token = b;
+        } else {
+            if (b >= a.batch) break;       // lengths changed under the call
+            if (b != cur_b) {
+                request_of(a, b, tok0, nq, kv);
+                tiles = tiles_of(a, nq);
+                cur_b = b;
+                if (tiles == 0) { ++b; tile = 0; head = 0; at = 0; continue; }
+            }
+            req = b;
+            sp = span_of(a, nq, kv, tile);
+            token = tok0 + sp.t0;
+        }
+        const int kvh = head / a.head_blocks, hb = head - kvh * a.head_blocks;
+        const int head0 = kvh * a.group + hb * a.block_heads;
+        const int nh = min(a.block_heads, a.group - hb * a.block_heads);
+        // the steps of this range: j .. j + n - 1
+        const int take = (int)min(left, (long long)(kItemUnits + sp.n - at));
+        const int j = max(at - kItemUnits, 0), n = max(at + take - kItemUnits, 0) - j;
+        const bool whole = n == sp.n;
+        const bool nothing = at == 0 && sp.n == 0;        // rows that see no key
+        left -= take;
+        const bool done = at + take == kItemUnits + sp.n;
+        const bool first = j == 0;
+        at = 0;
+        if (done) {
+            if (++head == heads) {
+                head = 0;
+                if (SEL || ++tile == tiles) { tile = 0; ++b; }
+            }
+        }
+        if (n == 0 && !nothing) continue;
+
+        // ---- the rows: scaled to fp16, their factors and what they see
+        const int rows = sp.ntok * nh;
+        uint32_t qa[KS][2 * NT];
+        float f[NT], off[NT], ref[NT], l[NT];
+        int see_lo[NT], see_hi[NT];
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+            const int r = g + 8 * x;
+            uint4 w[KS / 2];
+#pragma unroll
+            for (int i = 0; i < KS / 2; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
+            const int i = r / nh;
+            if (r < rows) {
+                const uint4* src = reinterpret_cast<const uint4*>(
+                    static_cast<const uint16_t*>(a.q) + (long long)(token + i) * a.q_token +
+                    (long long)(head0 + r - i * nh) * a.q_head + t * (D / 4));
+#pragma unroll
+                for (int c = 0; c < KS / 2; ++c) w[c] = __ldg(src + c);
+            }
+            float scale = a.scale_log2;
+            if constexpr (!FP16) {
+                // the row's largest exponent, which becomes 0
+                uint32_t top = 0;
+#pragma unroll
+                for (int c = 0; c < KS / 2; ++c) {
+                    const uint32_t m = 0x7fff7fffu;
+                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[c].x & m, w[c].y & m), __vmaxu2(w[c].z & m, w[c].w & m)));
+                }
+                top = max(top & 0xffffu, top >> 16) >> 7;
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                top = min(max(top, 1u), 253u);
+                scale *= __uint_as_float(top << 23);
+                const float inv = __uint_as_float((254u - top) << 23);
+                auto half = [&](uint32_t v) {
+                    return pack_f16(__uint_as_float(v << 16) * inv, __uint_as_float(v & 0xffff0000u) * inv);
+                };
+#pragma unroll
+                for (int c = 0; c < KS / 2; ++c)
+                    w[c] = make_uint4(half(w[c].x), half(w[c].y), half(w[c].z), half(w[c].w));
+            }
+#pragma unroll
+            for (int c = 0; c < KS / 2; ++c) {
+                qa[2 * c][x] = w[c].x;
+                qa[2 * c][NT + x] = w[c].y;
+                qa[2 * c + 1][x] = w[c].z;
+                qa[2 * c + 1][NT + x] = w[c].w;
+            }
+            f[x] = fmaxf(scale, 1.2e-38f);         // (times -inf it stays -inf)
+            ref[x] = -INFINITY;
+            off[x] = kPLog2;
+            l[x] = 0.0f;
+            const long long pos = SEL ? 0 : (long long)kv - nq + sp.t0 + min(i, sp.ntok - 1);
+            see_lo[x] = SEL || a.window == 0 ? 0 : (int)max(pos - a.window + 1, 0ll);
+            see_hi[x] = SEL ? 0 : a.causal ? min((int)max(pos + 1, 0ll), sp.hi) : sp.hi;
+        }
+        // steps that every row sees all of lie in [all_lo, all_hi)
+        int all_lo = 0, all_hi = 0;
+        if constexpr (!SEL) {
+            const long long pos = (long long)kv - nq + sp.t0;
+            all_lo = a.window > 0 ? (int)max(pos + sp.ntok - a.window, 0ll) : 0;
+            all_hi = a.causal ? (int)min(max(pos + 1, 0ll), (long long)sp.hi) : sp.hi;
+        }
+        float o[NT][KS][4];
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[x][i][e] = 0.0f;
+
+        // ---- copies, a few steps ahead
+        const int32_t* table = a.block_table + (long long)req * a.bt_stride;
+        const int32_t* list = SEL ? a.selected + (long long)token * a.sel_stride : nullptr;
+        const uint8_t* k_from = a.kc.codes + kvh * a.kc.head + chunk * 16;
+        const uint8_t* v_from = a.vc.codes + kvh * a.vc.head + chunk * 16;
+        const uint8_t* ks_from = a.kc.scales + kvh * a.kc.s_head;
+        const uint8_t* vs_from = a.vc.scales + kvh * a.vc.s_head;
+        const int j0 = sp.j0 + j;
+        // dense: 32 table entries from page `win` on, one a lane
+        int win = -1, entry = 0;
+        // selected: this lane's position and page of the next step to copy, the
+        // page of the one after it on its way, the position of the third
+        int p0 = -1, p1 = -1, p2 = -1, g0 = 0, g1 = 0;
+        auto position = [&](int s) {
+            const int i = (j0 + s) * kStepKeys + lane;
+            const int p = s < n && i < a.sel_k ? __ldg(list + i) : -1;
+            return p < kv ? p : -1;
+        };
+        auto page_at = [&](int p) { return p >= 0 ? __ldg(table + (p >> 6)) : 0; };
+        if constexpr (SEL) {
+            p0 = position(0);
+            p1 = position(1);
+            p2 = position(2);
+            g0 = page_at(p0);
+            g1 = page_at(p1);
+        }
+        auto copy = [&](int s, int st) {
+            const uint32_t to = ring + st * C::kStageBytes;
+            if constexpr (SEL) {
+                if (g0 < 0 || g0 >= a.num_pages) {
+                    atomicOr(a.status, kStatusBadBlock);
+                    g0 = 0;
+                }
+                const unsigned valid = __ballot_sync(0xffffffffu, p0 >= 0);
+                if (lane == 0) masks[st] = valid;
+                const int slot = p0 & 63;
+#pragma unroll
+                for (int i = 0; i < kStepKeys / kInstRows; ++i) {
+                    const int r = i * kInstRows + sub;
+                    const long long page = __shfl_sync(0xffffffffu, g0, r);
+                    const int sl = __shfl_sync(0xffffffffu, slot, r);
+                    const uint32_t bytes = (valid >> r) & 1 ? 16u : 0u;
+                    cp_async_zfill<16>(to + k_to + i * kInstRows * CB, k_from + page * a.kc.page + sl * a.kc.slot, bytes);
+                    cp_async_zfill<16>(to + v_to + i * kInstRows * CB, v_from + page * a.vc.page + sl * a.vc.slot, bytes);
+                }
+                const uint32_t bytes = p0 >= 0 ? SB : 0u;
+                cp_async_zfill<SB>(to + ks_to, ks_from + g0 * a.kc.s_page + slot * a.kc.s_slot, bytes);
+                cp_async_zfill<SB>(to + vs_to, vs_from + g0 * a.vc.s_page + slot * a.vc.s_slot, bytes);
+                p0 = p1;
+                g0 = g1;
+                p1 = p2;
+                g1 = page_at(p1);
+                p2 = position(s + 3);
+            } else {
+                const int key0 = (j0 + s) * kStepKeys, pg = key0 >> 6;
+                if (win < 0 || pg >= win + 32) {
+                    win = pg;
+                    entry = pg + lane <= (sp.hi - 1) >> 6 ? __ldg(table + pg + lane) : 0;
+                    if (entry < 0 || entry >= a.num_pages) {
+                        atomicOr(a.status, kStatusBadBlock);
+                        entry = 0;
+                    }
+                }
+                const long long page = __shfl_sync(0xffffffffu, entry, pg - win);
+                const int slot0 = key0 & 63;
+                const uint8_t* kp = k_from + page * a.kc.page + (slot0 + sub) * a.kc.slot;
+                const uint8_t* vp = v_from + page * a.vc.page + (slot0 + sub) * a.vc.slot;
+                const uint8_t* ksp = ks_from + page * a.kc.s_page + (slot0 + lane) * a.kc.s_slot;
+                const uint8_t* vsp = vs_from + page * a.vc.s_page + (slot0 + lane) * a.vc.s_slot;
+                // (rows outside the item's keys become zeros)
+                auto there = [&](int r) { return key0 + r >= sp.lo && key0 + r < sp.hi; };
+#pragma unroll
+                for (int i = 0; i < kStepKeys / kInstRows; ++i) {
+                    const uint32_t bytes = there(i * kInstRows + sub) ? 16u : 0u;
+                    cp_async_zfill<16>(to + k_to + i * kInstRows * CB, kp + (long long)i * kInstRows * a.kc.slot, bytes);
+                    cp_async_zfill<16>(to + v_to + i * kInstRows * CB, vp + (long long)i * kInstRows * a.vc.slot, bytes);
+                }
+                const uint32_t bytes = there(lane) ? SB : 0u;
+                cp_async_zfill<SB>(to + ks_to, ksp, bytes);
+                cp_async_zfill<SB>(to + vs_to, vsp, bytes);
+            }
+        };
+
+        // ---- one step's keys in stage `st`
+        auto compute = [&](int s, int st) {
+            const uint32_t from = ring + st * C::kStageBytes;
+            float sc[4][4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                uint32_t w[KS / 2], h0, h1;
+                const uint32_t row = from + kKC + (8 * x + g) * CB + t * (CB / 4);
+                if constexpr (D == 128) {
+                    const uint4 v = ld_shared_v4(row);
+                    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+                    const uint32_t h = e4m3x2_to_f16x2(ld_shared_u16(from + kKS + (8 * x + g) * SB + 2 * t));
+                    h0 = __byte_perm(h, h, 0x1010);
+                    h1 = __byte_perm(h, h, 0x3232);
+                } else {
+                    const uint2 v = ld_shared_v2_u32(row);
+                    w[0] = v.x; w[1] = v.y;
+                    h0 = h1 = e4m3_to_f16x2_dup(ld_shared_u8(from + kKS + (8 * x + g) * SB + t));
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[x][e] = 0.0f;
+#pragma unroll
+                for (int c = 0; c < KS / 2; ++c) {
+                    uint32_t h[4];
+                    e2m1x8_to_f16x2x4(w[c], h);
+                    const uint32_t m = 2 * c < KS / 2 ? h0 : h1;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        mma(sc[x], qa[2 * c + e][0], NT == 2 ? qa[2 * c + e][NT - 1] : 0u, qa[2 * c + e][NT],
+                            NT == 2 ? qa[2 * c + e][2 * NT - 1] : 0u, mul_f16x2(h[2 * e], m),
+                            mul_f16x2(h[2 * e + 1], m));
+                }
+            }
+            // scores: element 2 r + c of sc[x] is row g + 8 r, key 8 x + t + 4 c
+            const int key0 = (j0 + s) * kStepKeys;
+            bool parted = false;
+            if constexpr (SEL) {
+                const uint32_t valid = masks[st];
+                if (valid != 0xffffffffu) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+#pragma unroll
+                        for (int e = 0; e < 2 * NT; ++e)
+                            if (!((valid >> (8 * x + t + 4 * (e & 1))) & 1)) sc[x][e] = -INFINITY;
+                }
+            } else {
+                parted = key0 < all_lo || key0 + kStepKeys > all_hi;
+                if (parted) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+#pragma unroll
+                        for (int e = 0; e < 2 * NT; ++e) {
+                            const int key = key0 + 8 * x + t + 4 * (e & 1);
+                            if (key < see_lo[e >> 1] || key >= see_hi[e >> 1]) sc[x][e] = -INFINITY;
+                        }
+                }
+            }
+            bool grown = false;
+            float top[NT];
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+                float m = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(sc[i][2 * x], sc[i][2 * x + 1]));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                top[x] = m * f[x];
+                grown = grown || top[x] > ref[x] + kGrow;
+            }
+            if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+                for (int x = 0; x < NT; ++x) {
+                    const float next = fmaxf(ref[x], top[x]);
+                    const float down = ref[x] == -INFINITY ? 0.0f : exp2_approx(ref[x] - next);
+                    ref[x] = next;
+                    off[x] = next == -INFINITY ? kPLog2 : kPLog2 - next;
+                    l[x] *= down;
+                    // O's columns are rows 2 t and 2 t + 1
+                    const float d0 = __shfl_sync(0xffffffffu, down, 8 * t), d1 = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) {
+                        o[x][i][0] *= d0;
+                        o[x][i][1] *= d1;
+                        o[x][i][2] *= d0;
+                        o[x][i][3] *= d1;
+                    }
+                }
+            }
+            uint32_t pb[NT][4];
+#pragma unroll
+            for (int x = 0; x < NT; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float u = exp2_approx(fmaf(sc[i][2 * x], f[x], off[x]));
+                    const float v = exp2_approx(fmaf(sc[i][2 * x + 1], f[x], off[x]));
+                    l[x] += u + v;
+                    pb[x][i] = pack_f16(u, v);
+                }
+            // values: keys k + {0, 4, 8, 12}, k = 16 y + t, elements (D / 8) g ..
+            auto scales_at = [&](int y, uint32_t& sa, uint32_t& sb) {
+                const uint32_t vs = from + kVS + (16 * y + t) * SB + (D == 128 ? g : g >> 1);
+                sa = e4m3x2_to_f16x2(ld_shared_u8(vs) | (ld_shared_u8(vs + 4 * SB) << 8));
+                sb = e4m3x2_to_f16x2(ld_shared_u8(vs + 8 * SB) | (ld_shared_u8(vs + 12 * SB) << 8));
+            };
+            auto words_at = [&](int y, int e, uint32_t (&w)[KS / 4]) {
+                if constexpr (D == 128) {
+                    const uint2 v = ld_shared_v2_u32(from + kVC + (16 * y + t + 4 * e) * CB +
+                                                     (((g >> 1) ^ (((t >> 1) & 1) << 1)) << 4) + (g & 1) * 8);
+                    w[0] = v.x; w[1] = v.y;
+                } else {
+                    w[0] = ld_shared_u32(from + kVC + (16 * y + t + 4 * e) * CB + g * 4);
+                }
+            };
+            // two keys' words: bytes of (first, second) codes of even and of odd elements
+            auto pairs_of = [](uint32_t u, uint32_t v, uint32_t m, uint32_t (&even)[4], uint32_t (&odd)[4]) {
+                e2m1x8_to_f16x2x4((u & 0x0f0f0f0fu) | ((v << 4) & 0xf0f0f0f0u), even);
+                e2m1x8_to_f16x2x4(((u >> 4) & 0x0f0f0f0fu) | (v & 0xf0f0f0f0u), odd);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    even[e] = mul_f16x2(even[e], m);
+                    odd[e] = mul_f16x2(odd[e], m);
+                }
+            };
+            if (parted) {
+                uint32_t sa, sb, ta, tb;
+                scales_at(0, sa, sb);
+                scales_at(1, ta, tb);
+                const bool nan = f16x2_has_nan(sa) || f16x2_has_nan(sb) || f16x2_has_nan(ta) || f16x2_has_nan(tb);
+                if (__any_sync(0xffffffffu, nan)) {
+                    // row by row, the others' keys at 0
+#pragma unroll
+                    for (int x = 0; x < NT; ++x)
+#pragma unroll 1
+                        for (int r = 0; r < 8; ++r) {
+                            const int lo = __shfl_sync(0xffffffffu, see_lo[x], 4 * r);
+                            const int hi = __shfl_sync(0xffffffffu, see_hi[x], 4 * r);
+                            // halves of a register whose key the row sees
+                            auto seen = [&](int k) {
+                                const int u = key0 + k, v = u + 4;
+                                return (u >= lo && u < hi ? 0xffffu : 0u) | (v >= lo && v < hi ? 0xffff0000u : 0u);
+                            };
+#pragma unroll
+                            for (int c = 0; c < KS / 4; ++c) {
+                                float d[4][4] = {};
+#pragma unroll
+                                for (int y = 0; y < 2; ++y) {
+                                    uint32_t wd[4][KS / 4], ea[4], oa[4], eb[4], ob[4], su, sv;
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) words_at(y, e, wd[e]);
+                                    scales_at(y, su, sv);
+                                    pairs_of(wd[0][c], wd[1][c], su, ea, oa);
+                                    pairs_of(wd[2][c], wd[3][c], sv, eb, ob);
+                                    const uint32_t ma = seen(16 * y + t), mb = seen(16 * y + 8 + t);
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e)
+                                        mma(d[e], ea[e] & ma, oa[e] & ma, eb[e] & mb, ob[e] & mb, pb[x][2 * y],
+                                            pb[x][2 * y + 1]);
+                                }
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    if (r == 2 * t) { o[x][4 * c + e][0] += d[e][0]; o[x][4 * c + e][2] += d[e][2]; }
+                                    if (r == 2 * t + 1) { o[x][4 * c + e][1] += d[e][1]; o[x][4 * c + e][3] += d[e][3]; }
+                                }
+                            }
+                        }
+                    return;
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                uint32_t w[4][KS / 4], sa, sb;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) words_at(y, e, w[e]);
+                scales_at(y, sa, sb);
+#pragma unroll
+                for (int c = 0; c < KS / 4; ++c) {
+                    uint32_t ea[4], oa[4], eb[4], ob[4];
+                    pairs_of(w[0][c], w[1][c], sa, ea, oa);
+                    pairs_of(w[2][c], w[3][c], sb, eb, ob);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int x = 0; x < NT; ++x)
+                            mma(o[x][4 * c + e], ea[e], oa[e], eb[e], ob[e], pb[x][2 * y], pb[x][2 * y + 1]);
+                }
+            }
+        };
+
+        // ---- the steps
+        {
+            int put = 0, got = 0;          // stages
+#pragma unroll 1
+            for (int s = 0; s < S - 1; ++s) {
+                if (s < n) copy(s, put);
+                cp_async_commit();
+                ++put;
+            }
+#pragma unroll 1
+            for (int s = 0; s < n; ++s) {
+                cp_async_wait<S - 2>();
+                __syncwarp();              // step s is there, and step s - 1's stage is free
+                if (s + S - 1 < n) copy(s + S - 1, put);
+                cp_async_commit();
+                if (++put == S) put = 0;
+                compute(s, got);
+                if (++got == S) got = 0;
+            }
+            __syncwarp();
+        }
+
+        // ---- the rows' results, or a piece of them.  Lane (g, t) has elements
+        // (D / 8) g .. of rows 2 t and 2 t + 1
+        constexpr int E = D / 8;
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+            l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+            l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+        }
+        if (whole) {
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+                const float inv = inverse_of(l[x], a.vc.scale);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float m = __shfl_sync(0xffffffffu, inv, 8 * t + 4 * c);
+                    const int r = 8 * x + 2 * t + c;
+                    if (r >= rows) continue;
+                    const int i = r / nh;
+                    uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
+                                                          (long long)(token + i) * a.out_token +
+                                                          (long long)(head0 + r - i * nh) * a.out_head + g * E);
+#pragma unroll
+                    for (int v = 0; v < E / 8; ++v) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = pack_out<FP16>(o[x][4 * v + e][c] * m, o[x][4 * v + e][2 + c] * m);
+                        out[v] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                const int r = g + 8 * x, i = r / nh;
+                if (t == 0 && r < rows && a.lse != nullptr)
+                    a.lse[(long long)(token + i) * a.kv_heads * a.group + head0 + r - i * nh] = log_sum_of(ref[x], l[x]);
+            }
+        } else {
+            const int slot = first ? 1 : 0;
+            const long long at_piece = (worker * 2 + slot) * C::kRows;
+            if (lane == 0) {
+                int* p = rec + slot * kPcInts;
+                p[kPcTok0] = token;
+                p[kPcNtok] = sp.ntok;
+                p[kPcHead] = head0;
+                p[kPcHeads] = nh;
+                used[slot] = 1;
+                used[2 + slot] = j + n == sp.n;
+            }
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+                if (t == 0) wp.stats[at_piece + g + 8 * x] = make_float2(ref[x], l[x]);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float4* out = reinterpret_cast<float4*>(wp.part + (at_piece + 8 * x + 2 * t + c) * D + g * E);
+#pragma unroll
+                    for (int v = 0; v < E / 4; ++v)
+                        out[v] = make_float4(o[x][2 * v][c], o[x][2 * v][2 + c], o[x][2 * v + 1][c], o[x][2 * v + 1][2 + c]);
+                }
+            }
+        }
+    }
+
+    // ---- the CTA's pieces, in order: an item's begin with slot 1 of a warp and
+    // go on with slot 0 of the warps after it
+    __syncthreads();
+    constexpr int N = D / 32;
+    const uint8_t* all = smem + C::kRecs;
+    int* crec = cp.rec + blockIdx.x * 2LL * kPcInts;
+    if (threadIdx.x < 2) crec[threadIdx.x * kPcInts + kPcUsed] = 0;
+    int w = 0, slot = 0;
+    while (w < C::kWarps) {
+        if (!all[w * 8 + slot]) {
+            if (++slot == 2) { slot = 0; ++w; }
+            continue;
+        }
+        // a chain: from (w, slot) to the piece that ends the item, or the last one here
+        const int w0 = w, slot0 = slot;
+        bool ends = all[w * 8 + 2 + slot];
+        int count = 1, last_w = w;
+        for (int v = w + 1; v < C::kWarps && !ends; ++v)
+            if (all[v * 8]) {
+                ends = all[v * 8 + 2];
+                ++count;
+                last_w = v;
+            }
+        const bool complete = slot0 == 1 && ends;
+        const int* p = wp.rec + ((blockIdx.x * (long long)C::kWarps + w0) * 2 + slot0) * kPcInts;
+        const int c_tok0 = p[kPcTok0], c_ntok = p[kPcNtok], c_head = p[kPcHead], c_heads = p[kPcHeads];
+        for (int i = threadIdx.x; i < C::kRows * 32; i += C::kThreads) {
+            const int row = i >> 5, col = (i & 31) * N;
+            if (row >= c_ntok * c_heads) continue;
+            Joined<N> x;
+#pragma unroll 4
+            for (int v = w0; v <= last_w; ++v) {
+                const int sl = v == w0 ? slot0 : 0;
+                const long long q = ((blockIdx.x * (long long)C::kWarps + v) * 2 + sl) * C::kRows + row;
+                float2 st = wp.stats[q];
+                float y[N];
+                load_cols<N>(wp.part + q * D + col, y);
+                if (!all[v * 8 + sl]) {
+                    st = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+                    for (int e = 0; e < N; ++e) y[e] = 0.0f;
+                }
+                x.add(st.x, st.y, y);
+            }
+            if (complete) {
+                write_joined<FP16, N>(a, x, c_tok0, c_head, c_heads, row, col);
+            } else {
+                const long long q = (blockIdx.x * 2LL + slot0) * C::kRows + row;
+                if (col == 0) cp.stats[q] = make_float2(x.top, x.sum);
+#pragma unroll
+                for (int e = 0; e < N; ++e) cp.part[q * D + col + e] = x.acc[e];
+            }
+        }
+        if (!complete && threadIdx.x == 0) {
+            int* r = crec + slot0 * kPcInts;
+            r[kPcTok0] = c_tok0;
+            r[kPcNtok] = c_ntok;
+            r[kPcHead] = c_head;
+            r[kPcHeads] = c_heads;
+            r[kPcLast] = ends;
+        }
+        if (!complete) {
+            __syncthreads();               // (the record's first word was cleared above)
+            if (threadIdx.x == 0) crec[slot0 * kPcInts + kPcUsed] = 1;
+        }
+        // on to what follows the chain
+        w = last_w;
+        slot = count == 1 ? slot0 : 0;
+        if (++slot == 2) { slot = 0; ++w; }
+    }
+}
+
+}  // namespace nvattn
+}  // namespace pml

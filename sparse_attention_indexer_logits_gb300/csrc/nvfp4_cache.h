@@ -81,6 +81,9 @@ struct NvAttnArgs {
     int q_per_request;
     int kv_heads;
     int group;                     // query heads per kv head
+    int tile_tokens;               // tokens of an item
+    int head_blocks;               // items that share a kv head's query heads
+    int block_heads;               // query heads of one
     int sel_k;                     // selected: entries per token
     int causal;
     int window;                    // > 0: only keys past position - window
@@ -90,6 +93,8 @@ struct NvAttnArgs {
 
 cudaError_t launch_nvfp4_append(const NvAppendArgs& a, cudaStream_t stream);
 cudaError_t launch_nvfp4_read(const NvReadArgs& a, int sm_count, cudaStream_t stream);
-cudaError_t launch_nvfp4_attention(int head_dim, bool fp16, const NvAttnArgs& a, cudaStream_t stream);
+// Fills in the items' shape.  `workspace` holds pml_attention_workspace_bytes.
+cudaError_t launch_nvfp4_attention(int head_dim, bool fp16, NvAttnArgs& a, int num_ctas, void* workspace,
+                                   int64_t workspace_bytes, cudaStream_t stream);
 
 }  // namespace pml

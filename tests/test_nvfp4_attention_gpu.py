@@ -441,8 +441,8 @@ def test_same_result_every_time_and_captured():
     args[-1][0] = 1800                     # the graph reads the lengths when it runs
     graph.replay()
     torch.cuda.synchronize()
-    assert torch.equal(out[1:], want[1:]) and not torch.equal(out[0], want[0])
-    p.kvn[0] = 1800
+    assert not torch.equal(out[0], want[0])
+    p.kvn[0] = 1800                        # (how the keys are shared out depends on all lengths)
     lse = torch.empty((92, 8), device="cuda")
     check(p, pml.pml_paged_attention_nvfp4(*args, cu, lse=lse), lse)
     assert torch.equal(out, pml.pml_paged_attention_nvfp4(*args, cu))
