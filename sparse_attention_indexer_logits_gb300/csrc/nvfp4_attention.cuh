@@ -27,22 +27,24 @@
 // joined at the CTA's end, those of several CTAs by a second kernel; all in a
 // fixed order.
 //
-// Operands (m16n8k16; g = lane / 4, t = lane % 4):
-//   S = Q K^T   Q's rows are A.  The order of the summed elements is free, so
+// Operands (m16n8k16; g = lane / 4, t = lane % 4), eight rows of Q at a time:
+//   S^T = K Q^T   K is A, 16 keys.  The order of the summed elements is free, so
 //               lane t takes elements (D/4) t .. of every row: of a key 16 (8)
 //               bytes in one load, two (one) scales
 //   O^T = V^T P^T   V^T is A: its rows are elements, lane g takes (D/8) g .. of
 //               a value, one scale; its columns are keys, two to a register:
 //               the nibbles of two keys are interleaved into bytes before they
-//               are converted.  P^T is B, which is how S leaves its product
-// A score's column c of eight is key (c / 2) + 4 (c & 1): with K's rows stored
-// in that order and V's 16-byte chunks swapped in every other pair of rows all
-// loads are free of bank conflicts.
+//               are converted.  P^T is B: S^T's fragments, transposed between
+//               lanes (movmatrix)
+// Key c of eight is row (c / 2) + 4 (c & 1): with K's rows stored in that order
+// and V's 16-byte chunks swapped in every other pair of rows all loads are free
+// of bank conflicts.  (Q as A, which leaves P as B without the transposition,
+// takes twice the instructions for eight rows: 16 of Q's are not there.)
 //
 // Masked places never reach a result, whatever they hold: their scores are
-// -inf; rows outside the item's keys are zeros in shared memory; and where a
-// value under a NaN scale is visible to some rows and hidden from others, that
-// step's product is made row by row.
+// -inf; rows outside the item's keys are zeros in shared memory; and in a step
+// that some rows see in part, values under a NaN scale are taken out of the
+// product and put into the rows that see them.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -60,8 +62,10 @@ namespace nvattn {
 constexpr int kStepKeys = 32;
 // Units of work: a step is one, beginning and ending an item two.
 constexpr int kItemUnits = 2;
-constexpr float kPLog2 = 7.0f;         // P is 2^7 times the weights: fp16 keeps the small ones' bits
-constexpr float kGrow = 8.0f;          // a reference may be too low by 2^8: P stays below 2^15
+// P = 2^(c S + off): 2^7 times the weights, so that fp16 keeps the small ones'
+// bits, up to 2^15 before a larger maximum moves `off`.
+constexpr float kPLog2 = 7.0f, kPMost = 15.0f;
+constexpr float kFresh = 1e30f;        // `off` of a row that has seen no key
 
 template <int D, int NT>
 struct Cfg {
@@ -138,6 +142,32 @@ __device__ __forceinline__ void cp_async_zfill(uint32_t dst, const void* src, ui
                      : "memory");
 }
 
+// The same with c = 0 before.
+__device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+// An 8 x 8 matrix of 16-bit elements, lane (g, t) holding row g's elements 2 t
+// and 2 t + 1, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 __device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr)
 {
     uint32_t v;
@@ -151,11 +181,6 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes)
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
     return h;
-}
-
-__device__ __forceinline__ bool f16x2_has_nan(uint32_t h)
-{
-    return (h & 0x7fffu) > 0x7c00u || ((h >> 16) & 0x7fffu) > 0x7c00u;
 }
 
 // ------------------------------------------------------------------ items
@@ -334,7 +359,7 @@ __device__ __forceinline__ void load_cols(const float* p, float (&v)[N])
     }
 }
 
-// A row's scaled output and log-sum from its sums (2^7 times their size).
+// A row's scaled output and log-sum: `top` is the exponent that its sums lack.
 __device__ __forceinline__ float inverse_of(float sum, float v_scale)
 {
     return sum > 0.0f || sum != sum ? v_scale / sum : 0.0f;
@@ -342,7 +367,7 @@ __device__ __forceinline__ float inverse_of(float sum, float v_scale)
 
 __device__ __forceinline__ float log_sum_of(float top, float sum)
 {
-    return sum == 0.0f ? -INFINITY : (top - kPLog2) * 0.6931471805599453f + logf(sum);
+    return sum == 0.0f ? -INFINITY : top * 0.6931471805599453f + logf(sum);
 }
 
 // N columns of row `row` of an item, joined.
@@ -461,19 +486,19 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         }
         if (n == 0 && !nothing) continue;
 
-        // ---- the rows: scaled to fp16, their factors and what they see
+        // ---- the rows: scaled to fp16 (lane (g, t) holds part of row g of eight),
+        // and of rows 2 t and 2 t + 1 the factor, the exponent, the sum and the keys
         const int rows = sp.ntok * nh;
-        uint32_t qa[KS][2 * NT];
-        float f[NT], off[NT], ref[NT], l[NT];
-        int see_lo[NT], see_hi[NT];
+        uint32_t qb[NT][KS][2];
+        float f[NT][2], off[NT][2], l[NT][2];
+        int see_lo[NT][2], see_hi[NT][2];
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
-            const int r = g + 8 * x;
             uint4 w[KS / 2];
 #pragma unroll
-            for (int i = 0; i < KS / 2; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
-            const int i = r / nh;
-            if (r < rows) {
+            for (int c = 0; c < KS / 2; ++c) w[c] = make_uint4(0u, 0u, 0u, 0u);
+            if (const int r = g + 8 * x; r < rows) {
+                const int i = r / nh;
                 const uint4* src = reinterpret_cast<const uint4*>(
                     static_cast<const uint16_t*>(a.q) + (long long)(token + i) * a.q_token +
                     (long long)(head0 + r - i * nh) * a.q_head + t * (D / 4));
@@ -504,18 +529,22 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             }
 #pragma unroll
             for (int c = 0; c < KS / 2; ++c) {
-                qa[2 * c][x] = w[c].x;
-                qa[2 * c][NT + x] = w[c].y;
-                qa[2 * c + 1][x] = w[c].z;
-                qa[2 * c + 1][NT + x] = w[c].w;
+                qb[x][2 * c][0] = w[c].x;
+                qb[x][2 * c][1] = w[c].y;
+                qb[x][2 * c + 1][0] = w[c].z;
+                qb[x][2 * c + 1][1] = w[c].w;
             }
-            f[x] = fmaxf(scale, 1.2e-38f);         // (times -inf it stays -inf)
-            ref[x] = -INFINITY;
-            off[x] = kPLog2;
-            l[x] = 0.0f;
-            const long long pos = SEL ? 0 : (long long)kv - nq + sp.t0 + min(i, sp.ntok - 1);
-            see_lo[x] = SEL || a.window == 0 ? 0 : (int)max(pos - a.window + 1, 0ll);
-            see_hi[x] = SEL ? 0 : a.causal ? min((int)max(pos + 1, 0ll), sp.hi) : sp.hi;
+            scale = fmaxf(scale, 1.2e-38f);        // (times -inf it stays -inf)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                f[x][c] = __shfl_sync(0xffffffffu, scale, 8 * t + 4 * c);
+                off[x][c] = kFresh;
+                l[x][c] = 0.0f;
+                const int i = min((8 * x + 2 * t + c) / nh, sp.ntok - 1);
+                const long long pos = SEL ? 0 : (long long)kv - nq + sp.t0 + i;
+                see_lo[x][c] = SEL || a.window == 0 ? 0 : (int)max(pos - a.window + 1, 0ll);
+                see_hi[x][c] = SEL ? 0 : a.causal ? min((int)max(pos + 1, 0ll), sp.hi) : sp.hi;
+            }
         }
         // steps that every row sees all of lie in [all_lo, all_hi)
         int all_lo = 0, all_hi = 0;
@@ -618,101 +647,127 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         // ---- one step's keys in stage `st`
         auto compute = [&](int s, int st) {
             const uint32_t from = ring + st * C::kStageBytes;
-            float sc[4][4];
+            // element 2 h + c of sc[x][y] is key 16 y + 8 h + (g / 2) + 4 (g & 1),
+            // row 8 x + 2 t + c
+            float sc[NT][2][4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                uint32_t w[KS / 2], h0, h1;
-                const uint32_t row = from + kKC + (8 * x + g) * CB + t * (CB / 4);
-                if constexpr (D == 128) {
-                    const uint4 v = ld_shared_v4(row);
-                    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-                    const uint32_t h = e4m3x2_to_f16x2(ld_shared_u16(from + kKS + (8 * x + g) * SB + 2 * t));
-                    h0 = __byte_perm(h, h, 0x1010);
-                    h1 = __byte_perm(h, h, 0x3232);
-                } else {
-                    const uint2 v = ld_shared_v2_u32(row);
-                    w[0] = v.x; w[1] = v.y;
-                    h0 = h1 = e4m3_to_f16x2_dup(ld_shared_u8(from + kKS + (8 * x + g) * SB + t));
+            for (int y = 0; y < 2; ++y) {
+                uint32_t w[2][KS / 2], m[2][2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = 16 * y + 8 * h + g;
+                    if constexpr (D == 128) {
+                        const uint4 v = ld_shared_v4(from + kKC + row * CB + t * (CB / 4));
+                        w[h][0] = v.x; w[h][1] = v.y; w[h][2] = v.z; w[h][3] = v.w;
+                        const uint32_t s2 = e4m3x2_to_f16x2(ld_shared_u16(from + kKS + row * SB + 2 * t));
+                        m[h][0] = __byte_perm(s2, s2, 0x1010);
+                        m[h][1] = __byte_perm(s2, s2, 0x3232);
+                    } else {
+                        const uint2 v = ld_shared_v2_u32(from + kKC + row * CB + t * (CB / 4));
+                        w[h][0] = v.x; w[h][1] = v.y;
+                        m[h][0] = m[h][1] = e4m3_to_f16x2_dup(ld_shared_u8(from + kKS + row * SB + t));
+                    }
                 }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sc[x][e] = 0.0f;
 #pragma unroll
                 for (int c = 0; c < KS / 2; ++c) {
-                    uint32_t h[4];
-                    e2m1x8_to_f16x2x4(w[c], h);
-                    const uint32_t m = 2 * c < KS / 2 ? h0 : h1;
+                    uint32_t u[4], v[4];
+                    e2m1x8_to_f16x2x4(w[0][c], u);
+                    e2m1x8_to_f16x2x4(w[1][c], v);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        mma(sc[x], qa[2 * c + e][0], NT == 2 ? qa[2 * c + e][NT - 1] : 0u, qa[2 * c + e][NT],
-                            NT == 2 ? qa[2 * c + e][2 * NT - 1] : 0u, mul_f16x2(h[2 * e], m),
-                            mul_f16x2(h[2 * e + 1], m));
+                    for (int e = 0; e < 4; ++e) {
+                        u[e] = mul_f16x2(u[e], m[0][2 * c < KS / 2 ? 0 : 1]);
+                        v[e] = mul_f16x2(v[e], m[1][2 * c < KS / 2 ? 0 : 1]);
+                    }
+#pragma unroll
+                    for (int x = 0; x < NT; ++x)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t b0 = qb[x][2 * c + e][0], b1 = qb[x][2 * c + e][1];
+                            if (c + e == 0) mma_first(sc[x][y], u[0], v[0], u[1], v[1], b0, b1);
+                            else mma(sc[x][y], u[2 * e], v[2 * e], u[2 * e + 1], v[2 * e + 1], b0, b1);
+                        }
                 }
             }
-            // scores: element 2 r + c of sc[x] is row g + 8 r, key 8 x + t + 4 c
             const int key0 = (j0 + s) * kStepKeys;
             bool parted = false;
             if constexpr (SEL) {
-                const uint32_t valid = masks[st];
-                if (valid != 0xffffffffu) {
+                const uint32_t valid = masks[st] >> ((g >> 1) + 4 * (g & 1));
+                if (valid != 0xffffffffu >> ((g >> 1) + 4 * (g & 1))) {
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
+                    for (int y = 0; y < 2; ++y)
 #pragma unroll
-                        for (int e = 0; e < 2 * NT; ++e)
-                            if (!((valid >> (8 * x + t + 4 * (e & 1))) & 1)) sc[x][e] = -INFINITY;
+                        for (int h = 0; h < 2; ++h)
+                            if (!((valid >> (16 * y + 8 * h)) & 1))
+#pragma unroll
+                                for (int x = 0; x < NT; ++x) sc[x][y][2 * h] = sc[x][y][2 * h + 1] = -INFINITY;
                 }
             } else {
                 parted = key0 < all_lo || key0 + kStepKeys > all_hi;
                 if (parted) {
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
+                    for (int y = 0; y < 2; ++y)
 #pragma unroll
-                        for (int e = 0; e < 2 * NT; ++e) {
-                            const int key = key0 + 8 * x + t + 4 * (e & 1);
-                            if (key < see_lo[e >> 1] || key >= see_hi[e >> 1]) sc[x][e] = -INFINITY;
+                        for (int h = 0; h < 2; ++h) {
+                            const int key = key0 + 16 * y + 8 * h + (g >> 1) + 4 * (g & 1);
+#pragma unroll
+                            for (int x = 0; x < NT; ++x)
+#pragma unroll
+                                for (int c = 0; c < 2; ++c)
+                                    if (key < see_lo[x][c] || key >= see_hi[x][c]) sc[x][y][2 * h + c] = -INFINITY;
                         }
                 }
             }
-            bool grown = false;
-            float top[NT];
-#pragma unroll
-            for (int x = 0; x < NT; ++x) {
-                float m = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(sc[i][2 * x], sc[i][2 * x + 1]));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                top[x] = m * f[x];
-                grown = grown || top[x] > ref[x] + kGrow;
-            }
-            if (__any_sync(0xffffffffu, grown)) {
-#pragma unroll
-                for (int x = 0; x < NT; ++x) {
-                    const float next = fmaxf(ref[x], top[x]);
-                    const float down = ref[x] == -INFINITY ? 0.0f : exp2_approx(ref[x] - next);
-                    ref[x] = next;
-                    off[x] = next == -INFINITY ? kPLog2 : kPLog2 - next;
-                    l[x] *= down;
-                    // O's columns are rows 2 t and 2 t + 1
-                    const float d0 = __shfl_sync(0xffffffffu, down, 8 * t), d1 = __shfl_sync(0xffffffffu, down, 8 * t + 4);
-#pragma unroll
-                    for (int i = 0; i < KS; ++i) {
-                        o[x][i][0] *= d0;
-                        o[x][i][1] *= d1;
-                        o[x][i][2] *= d0;
-                        o[x][i][3] *= d1;
-                    }
-                }
-            }
-            uint32_t pb[NT][4];
+            // exponents of P, unless one is too large
+            float most = -INFINITY;
+            float z[NT][2][4];
 #pragma unroll
             for (int x = 0; x < NT; ++x)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float u = exp2_approx(fmaf(sc[i][2 * x], f[x], off[x]));
-                    const float v = exp2_approx(fmaf(sc[i][2 * x + 1], f[x], off[x]));
-                    l[x] += u + v;
-                    pb[x][i] = pack_f16(u, v);
+                for (int y = 0; y < 2; ++y) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z[x][y][e] = fmaf(sc[x][y][e], f[x][e & 1], off[x][e & 1]);
+                    most = max3(most, z[x][y][0], z[x][y][1]);
+                    most = max3(most, z[x][y][2], z[x][y][3]);
                 }
+            if (__any_sync(0xffffffffu, most > kPMost)) {
+#pragma unroll
+                for (int x = 0; x < NT; ++x) {
+                    float down[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float m = fmaxf(fmaxf(sc[x][0][c], sc[x][0][2 + c]), fmaxf(sc[x][1][c], sc[x][1][2 + c]));
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+                        const float next = m == -INFINITY ? off[x][c] : fminf(off[x][c], fmaf(-m, f[x][c], kPLog2));
+                        down[c] = off[x][c] == kFresh ? 0.0f : exp2_approx(next - off[x][c]);
+                        off[x][c] = next;
+                        l[x][c] *= down[c];
+                    }
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) {
+                        o[x][i][0] *= down[0];
+                        o[x][i][1] *= down[1];
+                        o[x][i][2] *= down[0];
+                        o[x][i][3] *= down[1];
+                    }
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) z[x][y][e] = fmaf(sc[x][y][e], f[x][e & 1], off[x][e & 1]);
+                }
+            }
+            uint32_t pb[NT][2][2];
+#pragma unroll
+            for (int x = 0; x < NT; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float u = exp2_approx(z[x][y][2 * h]), v = exp2_approx(z[x][y][2 * h + 1]);
+                        l[x][0] += u;
+                        l[x][1] += v;
+                        pb[x][y][h] = transpose8(pack_f16(u, v));
+                    }
             // values: keys k + {0, 4, 8, 12}, k = 16 y + t, elements (D / 8) g ..
             auto scales_at = [&](int y, uint32_t& sa, uint32_t& sb) {
                 const uint32_t vs = from + kVS + (16 * y + t) * SB + (D == 128 ? g : g >> 1);
@@ -739,48 +794,33 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                 }
             };
             if (parted) {
-                uint32_t sa, sb, ta, tb;
-                scales_at(0, sa, sb);
-                scales_at(1, ta, tb);
-                const bool nan = f16x2_has_nan(sa) || f16x2_has_nan(sb) || f16x2_has_nan(ta) || f16x2_has_nan(tb);
-                if (__any_sync(0xffffffffu, nan)) {
-                    // row by row, the others' keys at 0
+                // NaN scales: the rows that see their keys become NaN where they
+                // stand, and the scales 0 for the product
+                const uint32_t mine = from + kVS + lane * SB;
+                uint32_t s0 = ld_shared_u32(mine), s1 = SB == 8 ? ld_shared_u32(mine + SB - 4) : 0u;
+                auto clean = [](uint32_t v) { return v & ~__vcmpeq4(v & 0x7f7f7f7fu, 0x7f7f7f7fu); };
+                if (__any_sync(0xffffffffu, clean(s0) != s0 || clean(s1) != s1)) {
 #pragma unroll
-                    for (int x = 0; x < NT; ++x)
+                    for (int x = 0; x < NT; ++x) {
+                        float n0 = 0.0f, n1 = 0.0f;
 #pragma unroll 1
-                        for (int r = 0; r < 8; ++r) {
-                            const int lo = __shfl_sync(0xffffffffu, see_lo[x], 4 * r);
-                            const int hi = __shfl_sync(0xffffffffu, see_hi[x], 4 * r);
-                            // halves of a register whose key the row sees
-                            auto seen = [&](int k) {
-                                const int u = key0 + k, v = u + 4;
-                                return (u >= lo && u < hi ? 0xffffu : 0u) | (v >= lo && v < hi ? 0xffff0000u : 0u);
-                            };
-#pragma unroll
-                            for (int c = 0; c < KS / 4; ++c) {
-                                float d[4][4] = {};
-#pragma unroll
-                                for (int y = 0; y < 2; ++y) {
-                                    uint32_t wd[4][KS / 4], ea[4], oa[4], eb[4], ob[4], su, sv;
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e) words_at(y, e, wd[e]);
-                                    scales_at(y, su, sv);
-                                    pairs_of(wd[0][c], wd[1][c], su, ea, oa);
-                                    pairs_of(wd[2][c], wd[3][c], sv, eb, ob);
-                                    const uint32_t ma = seen(16 * y + t), mb = seen(16 * y + 8 + t);
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e)
-                                        mma(d[e], ea[e] & ma, oa[e] & ma, eb[e] & mb, ob[e] & mb, pb[x][2 * y],
-                                            pb[x][2 * y + 1]);
-                                }
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    if (r == 2 * t) { o[x][4 * c + e][0] += d[e][0]; o[x][4 * c + e][2] += d[e][2]; }
-                                    if (r == 2 * t + 1) { o[x][4 * c + e][1] += d[e][1]; o[x][4 * c + e][3] += d[e][3]; }
-                                }
-                            }
+                        for (int k = 0; k < kStepKeys; ++k) {
+                            if ((ld_shared_u8(from + kVS + k * SB + (D == 128 ? g : g >> 1)) & 0x7fu) != 0x7fu) continue;
+                            if (key0 + k >= see_lo[x][0] && key0 + k < see_hi[x][0]) n0 = NAN;
+                            if (key0 + k >= see_lo[x][1] && key0 + k < see_hi[x][1]) n1 = NAN;
                         }
-                    return;
+#pragma unroll
+                        for (int i = 0; i < KS; ++i) {
+                            o[x][i][0] += n0;
+                            o[x][i][1] += n1;
+                            o[x][i][2] += n0;
+                            o[x][i][3] += n1;
+                        }
+                    }
+                    __syncwarp();
+                    st_shared_u32(mine, clean(s0));
+                    if (SB == 8) st_shared_u32(mine + SB - 4, clean(s1));
+                    __syncwarp();
                 }
             }
 #pragma unroll
@@ -798,7 +838,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                     for (int e = 0; e < 4; ++e)
 #pragma unroll
                         for (int x = 0; x < NT; ++x)
-                            mma(o[x][4 * c + e], ea[e], oa[e], eb[e], ob[e], pb[x][2 * y], pb[x][2 * y + 1]);
+                            mma(o[x][4 * c + e], ea[e], oa[e], eb[e], ob[e], pb[x][y][0], pb[x][y][1]);
                 }
             }
         };
@@ -829,19 +869,19 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         // (D / 8) g .. of rows 2 t and 2 t + 1
         constexpr int E = D / 8;
 #pragma unroll
-        for (int x = 0; x < NT; ++x) {
-            l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-            l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-        }
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[x][c] += __shfl_xor_sync(0xffffffffu, l[x][c], d);
         if (whole) {
 #pragma unroll
-            for (int x = 0; x < NT; ++x) {
-                const float inv = inverse_of(l[x], a.vc.scale);
+            for (int x = 0; x < NT; ++x)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float m = __shfl_sync(0xffffffffu, inv, 8 * t + 4 * c);
                     const int r = 8 * x + 2 * t + c;
                     if (r >= rows) continue;
+                    const float m = inverse_of(l[x][c], a.vc.scale);
                     const int i = r / nh;
                     uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
                                                           (long long)(token + i) * a.out_token +
@@ -854,11 +894,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                             w[e] = pack_out<FP16>(o[x][4 * v + e][c] * m, o[x][4 * v + e][2 + c] * m);
                         out[v] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
+                    if (g == 0 && a.lse != nullptr)
+                        a.lse[(long long)(token + i) * a.kv_heads * a.group + head0 + r - i * nh] =
+                            log_sum_of(-off[x][c], l[x][c]);
                 }
-                const int r = g + 8 * x, i = r / nh;
-                if (t == 0 && r < rows && a.lse != nullptr)
-                    a.lse[(long long)(token + i) * a.kv_heads * a.group + head0 + r - i * nh] = log_sum_of(ref[x], l[x]);
-            }
         } else {
             const int slot = first ? 1 : 0;
             const long long at_piece = (worker * 2 + slot) * C::kRows;
@@ -873,9 +912,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             }
 #pragma unroll
             for (int x = 0; x < NT; ++x) {
-                if (t == 0) wp.stats[at_piece + g + 8 * x] = make_float2(ref[x], l[x]);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
+                    if (g == 0)
+                        wp.stats[at_piece + 8 * x + 2 * t + c] =
+                            make_float2(off[x][c] == kFresh ? -INFINITY : -off[x][c], l[x][c]);
                     float4* out = reinterpret_cast<float4*>(wp.part + (at_piece + 8 * x + 2 * t + c) * D + g * E);
 #pragma unroll
                     for (int v = 0; v < E / 4; ++v)
