@@ -568,6 +568,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         const uint8_t* v_from = a.vc.codes + kvh * a.vc.head + chunk * 16;
         const uint8_t* ks_from = a.kc.scales + kvh * a.kc.s_head;
         const uint8_t* vs_from = a.vc.scales + kvh * a.vc.s_head;
+        if constexpr (!SEL) {              // this lane's rows of a page's first step
+            k_from += sub * a.kc.slot;
+            v_from += sub * a.vc.slot;
+            ks_from += lane * a.kc.s_slot;
+            vs_from += lane * a.vc.s_slot;
+        }
         const int j0 = sp.j0 + j;
         // dense: 32 table entries from page `win` on, one a lane
         int win = -1, entry = 0;
@@ -624,23 +630,34 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                         entry = 0;
                     }
                 }
-                const long long page = __shfl_sync(0xffffffffu, entry, pg - win);
-                const int slot0 = key0 & 63;
-                const uint8_t* kp = k_from + page * a.kc.page + (slot0 + sub) * a.kc.slot;
-                const uint8_t* vp = v_from + page * a.vc.page + (slot0 + sub) * a.vc.slot;
-                const uint8_t* ksp = ks_from + page * a.kc.s_page + (slot0 + lane) * a.kc.s_slot;
-                const uint8_t* vsp = vs_from + page * a.vc.s_page + (slot0 + lane) * a.vc.s_slot;
-                // (rows outside the item's keys become zeros)
-                auto there = [&](int r) { return key0 + r >= sp.lo && key0 + r < sp.hi; };
-#pragma unroll
-                for (int i = 0; i < kStepKeys / kInstRows; ++i) {
-                    const uint32_t bytes = there(i * kInstRows + sub) ? 16u : 0u;
-                    cp_async_zfill<16>(to + k_to + i * kInstRows * CB, kp + (long long)i * kInstRows * a.kc.slot, bytes);
-                    cp_async_zfill<16>(to + v_to + i * kInstRows * CB, vp + (long long)i * kInstRows * a.vc.slot, bytes);
+                const int page = __shfl_sync(0xffffffffu, entry, pg - win);
+                const uint8_t* kp = k_from + page * a.kc.page;
+                const uint8_t* vp = v_from + page * a.vc.page;
+                const uint8_t* ksp = ks_from + page * a.kc.s_page;
+                const uint8_t* vsp = vs_from + page * a.vc.s_page;
+                if (key0 & kStepKeys) {    // the page's second step
+                    kp += kStepKeys * a.kc.slot;
+                    vp += kStepKeys * a.vc.slot;
+                    ksp += kStepKeys * a.kc.s_slot;
+                    vsp += kStepKeys * a.vc.s_slot;
                 }
-                const uint32_t bytes = there(lane) ? SB : 0u;
-                cp_async_zfill<SB>(to + ks_to, ksp, bytes);
-                cp_async_zfill<SB>(to + vs_to, vsp, bytes);
+                auto rows_in = [&](auto bytes_of) {
+#pragma unroll
+                    for (int i = 0; i < kStepKeys / kInstRows; ++i) {
+                        const uint32_t bytes = bytes_of(i * kInstRows + sub, 16);
+                        cp_async_zfill<16>(to + k_to + i * kInstRows * CB, kp, bytes);
+                        cp_async_zfill<16>(to + v_to + i * kInstRows * CB, vp, bytes);
+                        kp += kInstRows * a.kc.slot;
+                        vp += kInstRows * a.vc.slot;
+                    }
+                    const uint32_t bytes = bytes_of(lane, SB);
+                    cp_async_zfill<SB>(to + ks_to, ksp, bytes);
+                    cp_async_zfill<SB>(to + vs_to, vsp, bytes);
+                };
+                if (key0 >= sp.lo && key0 + kStepKeys <= sp.hi)
+                    rows_in([](int, int bytes) { return bytes; });
+                else                       // (rows outside the item's keys become zeros)
+                    rows_in([&](int r, int bytes) { return key0 + r >= sp.lo && key0 + r < sp.hi ? bytes : 0; });
             }
         };
 
