@@ -439,6 +439,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     const uint32_t v_to = kVC + sub * CB + (D == 128 ? (chunk ^ (((sub >> 1) & 1) << 1)) : chunk) * 16;
     const uint32_t ks_to = kKS + column(lane) * SB, vs_to = kVS + lane * SB;
 
+    const bool same = a.kc.page == a.vc.page && a.kc.slot == a.vc.slot;
+
     int b = start.b, tile = start.tile, head = start.head, at = start.at;
     long long left = start.left;
     int cur_b = -1, tok0 = 0, nq = 0, kv = 0, tiles = 0;
@@ -486,81 +488,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         }
         if (n == 0 && !nothing) continue;
 
-        // ---- the rows: scaled to fp16 (lane (g, t) holds part of row g of eight),
-        // and of rows 2 t and 2 t + 1 the factor, the exponent, the sum and the keys
-        const int rows = sp.ntok * nh;
-        uint32_t qb[NT][KS][2];
-        float f[NT][2], off[NT][2], l[NT][2];
-        int see_lo[NT][2], see_hi[NT][2];
-#pragma unroll
-        for (int x = 0; x < NT; ++x) {
-            uint4 w[KS / 2];
-#pragma unroll
-            for (int c = 0; c < KS / 2; ++c) w[c] = make_uint4(0u, 0u, 0u, 0u);
-            if (const int r = g + 8 * x; r < rows) {
-                const int i = r / nh;
-                const uint4* src = reinterpret_cast<const uint4*>(
-                    static_cast<const uint16_t*>(a.q) + (long long)(token + i) * a.q_token +
-                    (long long)(head0 + r - i * nh) * a.q_head + t * (D / 4));
-#pragma unroll
-                for (int c = 0; c < KS / 2; ++c) w[c] = __ldg(src + c);
-            }
-            float scale = a.scale_log2;
-            if constexpr (!FP16) {
-                // the row's largest exponent, which becomes 0
-                uint32_t top = 0;
-#pragma unroll
-                for (int c = 0; c < KS / 2; ++c) {
-                    const uint32_t m = 0x7fff7fffu;
-                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[c].x & m, w[c].y & m), __vmaxu2(w[c].z & m, w[c].w & m)));
-                }
-                top = max(top & 0xffffu, top >> 16) >> 7;
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                top = min(max(top, 1u), 253u);
-                scale *= __uint_as_float(top << 23);
-                const float inv = __uint_as_float((254u - top) << 23);
-                auto half = [&](uint32_t v) {
-                    return pack_f16(__uint_as_float(v << 16) * inv, __uint_as_float(v & 0xffff0000u) * inv);
-                };
-#pragma unroll
-                for (int c = 0; c < KS / 2; ++c)
-                    w[c] = make_uint4(half(w[c].x), half(w[c].y), half(w[c].z), half(w[c].w));
-            }
-#pragma unroll
-            for (int c = 0; c < KS / 2; ++c) {
-                qb[x][2 * c][0] = w[c].x;
-                qb[x][2 * c][1] = w[c].y;
-                qb[x][2 * c + 1][0] = w[c].z;
-                qb[x][2 * c + 1][1] = w[c].w;
-            }
-            scale = fmaxf(scale, 1.2e-38f);        // (times -inf it stays -inf)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                f[x][c] = __shfl_sync(0xffffffffu, scale, 8 * t + 4 * c);
-                off[x][c] = kFresh;
-                l[x][c] = 0.0f;
-                const int i = min((8 * x + 2 * t + c) / nh, sp.ntok - 1);
-                const long long pos = SEL ? 0 : (long long)kv - nq + sp.t0 + i;
-                see_lo[x][c] = SEL || a.window == 0 ? 0 : (int)max(pos - a.window + 1, 0ll);
-                see_hi[x][c] = SEL ? 0 : a.causal ? min((int)max(pos + 1, 0ll), sp.hi) : sp.hi;
-            }
-        }
-        // steps that every row sees all of lie in [all_lo, all_hi)
-        int all_lo = 0, all_hi = 0;
-        if constexpr (!SEL) {
-            const long long pos = (long long)kv - nq + sp.t0;
-            all_lo = a.window > 0 ? (int)max(pos + sp.ntok - a.window, 0ll) : 0;
-            all_hi = a.causal ? (int)min(max(pos + 1, 0ll), (long long)sp.hi) : sp.hi;
-        }
-        float o[NT][KS][4];
-#pragma unroll
-        for (int x = 0; x < NT; ++x)
-#pragma unroll
-            for (int i = 0; i < KS; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[x][i][e] = 0.0f;
-
         // ---- copies, a few steps ahead
         const int32_t* table = a.block_table + (long long)req * a.bt_stride;
         const int32_t* list = SEL ? a.selected + (long long)token * a.sel_stride : nullptr;
@@ -590,6 +517,25 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             p0 = position(0);
             p1 = position(1);
             p2 = position(2);
+        }
+        // ---- Q's rows on their way: lane (g, t) takes part of row g of each eight
+        const int rows = sp.ntok * nh;
+        uint4 qw[NT][KS / 2];
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+#pragma unroll
+            for (int c = 0; c < KS / 2; ++c) qw[x][c] = make_uint4(0u, 0u, 0u, 0u);
+            if (const int r = g + 8 * x; r < rows) {
+                const int i = r / nh;
+                const uint4* src = reinterpret_cast<const uint4*>(
+                    static_cast<const uint16_t*>(a.q) + (long long)(token + i) * a.q_token +
+                    (long long)(head0 + r - i * nh) * a.q_head + t * (D / 4));
+#pragma unroll
+                for (int c = 0; c < KS / 2; ++c) qw[x][c] = __ldg(src + c);
+            }
+        }
+
+        if constexpr (SEL) {
             g0 = page_at(p0);
             g1 = page_at(p1);
         }
@@ -603,14 +549,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                 const unsigned valid = __ballot_sync(0xffffffffu, p0 >= 0);
                 if (lane == 0) masks[st] = valid;
                 const int slot = p0 & 63;
+                const long long k_off = g0 * a.kc.page + slot * a.kc.slot, v_off = g0 * a.vc.page + slot * a.vc.slot;
 #pragma unroll
                 for (int i = 0; i < kStepKeys / kInstRows; ++i) {
                     const int r = i * kInstRows + sub;
-                    const long long page = __shfl_sync(0xffffffffu, g0, r);
-                    const int sl = __shfl_sync(0xffffffffu, slot, r);
                     const uint32_t bytes = (valid >> r) & 1 ? 16u : 0u;
-                    cp_async_zfill<16>(to + k_to + i * kInstRows * CB, k_from + page * a.kc.page + sl * a.kc.slot, bytes);
-                    cp_async_zfill<16>(to + v_to + i * kInstRows * CB, v_from + page * a.vc.page + sl * a.vc.slot, bytes);
+                    const long long ko = __shfl_sync(0xffffffffu, k_off, r);
+                    const long long vo = same ? ko : __shfl_sync(0xffffffffu, v_off, r);
+                    cp_async_zfill<16>(to + k_to + i * kInstRows * CB, k_from + ko, bytes);
+                    cp_async_zfill<16>(to + v_to + i * kInstRows * CB, v_from + vo, bytes);
                 }
                 const uint32_t bytes = p0 >= 0 ? SB : 0u;
                 cp_async_zfill<SB>(to + ks_to, ks_from + g0 * a.kc.s_page + slot * a.kc.s_slot, bytes);
@@ -661,39 +608,113 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             }
         };
 
+        // the first copies, and what the steps work on while those are under way
+#pragma unroll 1
+        for (int s = 0; s < S - 1; ++s) {
+            if (s < n) copy(s, s);
+            cp_async_commit();
+        }
+
+        // ---- the rows scaled to fp16, and of rows 2 t and 2 t + 1 the factor, the exponent, the sum and the keys
+        uint32_t qb[NT][KS][2];
+        float f[NT][2], off[NT][2], l[NT][2];
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+            uint4 (&w)[KS / 2] = qw[x];
+            float scale = a.scale_log2;
+            if constexpr (!FP16) {
+                // the row's largest exponent, which becomes 0
+                uint32_t top = 0;
+#pragma unroll
+                for (int c = 0; c < KS / 2; ++c) {
+                    const uint32_t m = 0x7fff7fffu;
+                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[c].x & m, w[c].y & m), __vmaxu2(w[c].z & m, w[c].w & m)));
+                }
+                top = max(top & 0xffffu, top >> 16) >> 7;
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                top = min(max(top, 1u), 253u);
+                scale *= __uint_as_float(top << 23);
+                const float inv = __uint_as_float((254u - top) << 23);
+                auto half = [&](uint32_t v) {
+                    return pack_f16(__uint_as_float(v << 16) * inv, __uint_as_float(v & 0xffff0000u) * inv);
+                };
+#pragma unroll
+                for (int c = 0; c < KS / 2; ++c)
+                    w[c] = make_uint4(half(w[c].x), half(w[c].y), half(w[c].z), half(w[c].w));
+            }
+#pragma unroll
+            for (int c = 0; c < KS / 2; ++c) {
+                qb[x][2 * c][0] = w[c].x;
+                qb[x][2 * c][1] = w[c].y;
+                qb[x][2 * c + 1][0] = w[c].z;
+                qb[x][2 * c + 1][1] = w[c].w;
+            }
+            scale = fmaxf(scale, 1.2e-38f);        // (times -inf it stays -inf)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                f[x][c] = __shfl_sync(0xffffffffu, scale, 8 * t + 4 * c);
+                off[x][c] = kFresh;
+                l[x][c] = 0.0f;
+            }
+        }
+        // the keys that row 8 x + 2 t + c sees: [x, y)
+        auto sees = [&](int x, int c) {
+            const int pos = kv - nq + sp.t0 + min((8 * x + 2 * t + c) / nh, sp.ntok - 1);
+            return make_int2(a.window > 0 ? (int)max((long long)pos - a.window + 1, 0ll) : 0,
+                             a.causal ? min(max(pos + 1, 0), sp.hi) : sp.hi);
+        };
+        // steps that every row sees all of lie in [all_lo, all_hi)
+        int all_lo = 0, all_hi = 0;
+        if constexpr (!SEL) {
+            const long long pos = (long long)kv - nq + sp.t0;
+            all_lo = a.window > 0 ? (int)max(pos + sp.ntok - a.window, 0ll) : 0;
+            all_hi = a.causal ? (int)min(max(pos + 1, 0ll), (long long)sp.hi) : sp.hi;
+        }
+        float o[NT][KS][4];
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[x][i][e] = 0.0f;
+
         // ---- one step's keys in stage `st`
         auto compute = [&](int s, int st) {
             const uint32_t from = ring + st * C::kStageBytes;
             // element 2 h + c of sc[x][y] is key 16 y + 8 h + (g / 2) + 4 (g & 1),
             // row 8 x + 2 t + c
             float sc[NT][2][4];
+            uint32_t w[2][2][KS / 2], m[2][2][2];
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                uint32_t w[2][KS / 2], m[2][2];
+            for (int y = 0; y < 2; ++y)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int row = 16 * y + 8 * h + g;
                     if constexpr (D == 128) {
                         const uint4 v = ld_shared_v4(from + kKC + row * CB + t * (CB / 4));
-                        w[h][0] = v.x; w[h][1] = v.y; w[h][2] = v.z; w[h][3] = v.w;
+                        w[y][h][0] = v.x; w[y][h][1] = v.y; w[y][h][2] = v.z; w[y][h][3] = v.w;
                         const uint32_t s2 = e4m3x2_to_f16x2(ld_shared_u16(from + kKS + row * SB + 2 * t));
-                        m[h][0] = __byte_perm(s2, s2, 0x1010);
-                        m[h][1] = __byte_perm(s2, s2, 0x3232);
+                        m[y][h][0] = __byte_perm(s2, s2, 0x1010);
+                        m[y][h][1] = __byte_perm(s2, s2, 0x3232);
                     } else {
                         const uint2 v = ld_shared_v2_u32(from + kKC + row * CB + t * (CB / 4));
-                        w[h][0] = v.x; w[h][1] = v.y;
-                        m[h][0] = m[h][1] = e4m3_to_f16x2_dup(ld_shared_u8(from + kKS + row * SB + t));
+                        w[y][h][0] = v.x; w[y][h][1] = v.y;
+                        m[y][h][0] = m[y][h][1] = e4m3_to_f16x2_dup(ld_shared_u8(from + kKS + row * SB + t));
                     }
                 }
+            // (the two blocks of keys in turn: neither waits for its own sums)
 #pragma unroll
-                for (int c = 0; c < KS / 2; ++c) {
+            for (int c = 0; c < KS / 2; ++c)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
                     uint32_t u[4], v[4];
-                    e2m1x8_to_f16x2x4(w[0][c], u);
-                    e2m1x8_to_f16x2x4(w[1][c], v);
+                    e2m1x8_to_f16x2x4(w[y][0][c], u);
+                    e2m1x8_to_f16x2x4(w[y][1][c], v);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        u[e] = mul_f16x2(u[e], m[0][2 * c < KS / 2 ? 0 : 1]);
-                        v[e] = mul_f16x2(v[e], m[1][2 * c < KS / 2 ? 0 : 1]);
+                        u[e] = mul_f16x2(u[e], m[y][0][2 * c < KS / 2 ? 0 : 1]);
+                        v[e] = mul_f16x2(v[e], m[y][1][2 * c < KS / 2 ? 0 : 1]);
                     }
 #pragma unroll
                     for (int x = 0; x < NT; ++x)
@@ -704,7 +725,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                             else mma(sc[x][y], u[2 * e], v[2 * e], u[2 * e + 1], v[2 * e + 1], b0, b1);
                         }
                 }
-            }
             const int key0 = (j0 + s) * kStepKeys;
             bool parted = false;
             if constexpr (SEL) {
@@ -722,15 +742,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                 parted = key0 < all_lo || key0 + kStepKeys > all_hi;
                 if (parted) {
 #pragma unroll
-                    for (int y = 0; y < 2; ++y)
+                    for (int x = 0; x < NT; ++x)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int key = key0 + 16 * y + 8 * h + (g >> 1) + 4 * (g & 1);
+                        for (int c = 0; c < 2; ++c) {
+                            const int2 see = sees(x, c);
 #pragma unroll
-                            for (int x = 0; x < NT; ++x)
-#pragma unroll
-                                for (int c = 0; c < 2; ++c)
-                                    if (key < see_lo[x][c] || key >= see_hi[x][c]) sc[x][y][2 * h + c] = -INFINITY;
+                            for (int i = 0; i < 4; ++i) {
+                                const int key = key0 + 8 * i + (g >> 1) + 4 * (g & 1);
+                                if (key < see.x || key >= see.y) sc[x][i >> 1][2 * (i & 1) + c] = -INFINITY;
+                            }
                         }
                 }
             }
@@ -819,12 +839,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                 if (__any_sync(0xffffffffu, clean(s0) != s0 || clean(s1) != s1)) {
 #pragma unroll
                     for (int x = 0; x < NT; ++x) {
+                        const int2 see0 = sees(x, 0), see1 = sees(x, 1);
                         float n0 = 0.0f, n1 = 0.0f;
 #pragma unroll 1
                         for (int k = 0; k < kStepKeys; ++k) {
                             if ((ld_shared_u8(from + kVS + k * SB + (D == 128 ? g : g >> 1)) & 0x7fu) != 0x7fu) continue;
-                            if (key0 + k >= see_lo[x][0] && key0 + k < see_hi[x][0]) n0 = NAN;
-                            if (key0 + k >= see_lo[x][1] && key0 + k < see_hi[x][1]) n1 = NAN;
+                            if (key0 + k >= see0.x && key0 + k < see0.y) n0 = NAN;
+                            if (key0 + k >= see1.x && key0 + k < see1.y) n1 = NAN;
                         }
 #pragma unroll
                         for (int i = 0; i < KS; ++i) {
@@ -862,13 +883,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 
         // ---- the steps
         {
-            int put = 0, got = 0;          // stages
-#pragma unroll 1
-            for (int s = 0; s < S - 1; ++s) {
-                if (s < n) copy(s, put);
-                cp_async_commit();
-                ++put;
-            }
+            int put = S - 1, got = 0;      // stages
 #pragma unroll 1
             for (int s = 0; s < n; ++s) {
                 cp_async_wait<S - 2>();
@@ -916,25 +931,29 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                             log_sum_of(-off[x][c], l[x][c]);
                 }
         } else {
+            // The last piece stays in the ring, which nothing else needs any more.
             const int slot = first ? 1 : 0;
             const long long at_piece = (worker * 2 + slot) * C::kRows;
+            const bool here = left == 0;
+            float* part = here ? reinterpret_cast<float*>(smem + warp * C::kRing) : wp.part + at_piece * D;
+            float2* stats = here ? reinterpret_cast<float2*>(smem + warp * C::kRing + C::kRows * D * 4)
+                                 : wp.stats + at_piece;
             if (lane == 0) {
                 int* p = rec + slot * kPcInts;
                 p[kPcTok0] = token;
                 p[kPcNtok] = sp.ntok;
                 p[kPcHead] = head0;
                 p[kPcHeads] = nh;
-                used[slot] = 1;
+                used[slot] = here ? 2 : 1;
                 used[2 + slot] = j + n == sp.n;
             }
 #pragma unroll
             for (int x = 0; x < NT; ++x) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    if (g == 0)
-                        wp.stats[at_piece + 8 * x + 2 * t + c] =
-                            make_float2(off[x][c] == kFresh ? -INFINITY : -off[x][c], l[x][c]);
-                    float4* out = reinterpret_cast<float4*>(wp.part + (at_piece + 8 * x + 2 * t + c) * D + g * E);
+                    const int r = 8 * x + 2 * t + c;
+                    if (g == 0) stats[r] = make_float2(off[x][c] == kFresh ? -INFINITY : -off[x][c], l[x][c]);
+                    float4* out = reinterpret_cast<float4*>(part + r * D + g * E);
 #pragma unroll
                     for (int v = 0; v < E / 4; ++v)
                         out[v] = make_float4(o[x][2 * v][c], o[x][2 * v][2 + c], o[x][2 * v + 1][c], o[x][2 * v + 1][2 + c]);
@@ -947,71 +966,66 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     // go on with slot 0 of the warps after it
     __syncthreads();
     constexpr int N = D / 32;
-    const uint8_t* all = smem + C::kRecs;
+    const uint32_t flags = lane < C::kWarps ? *reinterpret_cast<const uint32_t*>(smem + C::kRecs + lane * 8) : 0u;
+    const unsigned begin = __ballot_sync(0xffffffffu, flags & 0xff00u), go = __ballot_sync(0xffffffffu, flags & 0xffu),
+                   end = __ballot_sync(0xffffffffu, flags & 0xff0000u),
+                   kept = __ballot_sync(0xffffffffu, (flags & 0xffu) == 2u);
+    // pieces that go on an item begun before this CTA: from the first warp on
+    const bool lead = go != 0 && (begin == 0 || __ffs(go) <= __ffs(begin));
+    const int chains = __popc(begin) + (lead ? 1 : 0);
     int* crec = cp.rec + blockIdx.x * 2LL * kPcInts;
-    if (threadIdx.x < 2) crec[threadIdx.x * kPcInts + kPcUsed] = 0;
-    int w = 0, slot = 0;
-    while (w < C::kWarps) {
-        if (!all[w * 8 + slot]) {
-            if (++slot == 2) { slot = 0; ++w; }
-            continue;
+    if (threadIdx.x < 2) {
+        // slot 0: the item from before; slot 1: the last one, if it does not end here
+        const bool mine = threadIdx.x == 0 ? lead
+                                           : begin != 0 && !(go & end & ~((2u << (31 - __clz(begin))) - 1u));
+        const int w = threadIdx.x == 0 ? __ffs(go) - 1 : 31 - __clz(begin);
+        int* r = crec + threadIdx.x * kPcInts;
+        r[kPcUsed] = mine;
+        if (mine) {
+            const int* p = wp.rec + ((blockIdx.x * (long long)C::kWarps + w) * 2 + threadIdx.x) * kPcInts;
+            r[kPcTok0] = p[kPcTok0];
+            r[kPcNtok] = p[kPcNtok];
+            r[kPcHead] = p[kPcHead];
+            r[kPcHeads] = p[kPcHeads];
+            r[kPcLast] = threadIdx.x == 0 && (go & end) != 0;
         }
-        // a chain: from (w, slot) to the piece that ends the item, or the last one here
-        const int w0 = w, slot0 = slot;
-        bool ends = all[w * 8 + 2 + slot];
-        int count = 1, last_w = w;
-        for (int v = w + 1; v < C::kWarps && !ends; ++v)
-            if (all[v * 8]) {
-                ends = all[v * 8 + 2];
-                ++count;
-                last_w = v;
-            }
-        const bool complete = slot0 == 1 && ends;
-        const int* p = wp.rec + ((blockIdx.x * (long long)C::kWarps + w0) * 2 + slot0) * kPcInts;
-        const int c_tok0 = p[kPcTok0], c_ntok = p[kPcNtok], c_head = p[kPcHead], c_heads = p[kPcHeads];
-        for (int i = threadIdx.x; i < C::kRows * 32; i += C::kThreads) {
-            const int row = i >> 5, col = (i & 31) * N;
-            if (row >= c_ntok * c_heads) continue;
-            Joined<N> x;
-#pragma unroll 4
-            for (int v = w0; v <= last_w; ++v) {
-                const int sl = v == w0 ? slot0 : 0;
-                const long long q = ((blockIdx.x * (long long)C::kWarps + v) * 2 + sl) * C::kRows + row;
-                float2 st = wp.stats[q];
-                float y[N];
-                load_cols<N>(wp.part + q * D + col, y);
-                if (!all[v * 8 + sl]) {
-                    st = make_float2(-INFINITY, 0.0f);
+    }
+    for (int i = threadIdx.x; i < chains * C::kRows * 32; i += C::kThreads) {
+        const int chain = i / (C::kRows * 32), row = (i >> 5) % C::kRows, col = (i & 31) * N;
+        const bool led = lead && chain == 0;
+        unsigned b0 = begin;                   // its first warp is the lowest bit left
+        for (int k = lead ? 1 : 0; k < chain; ++k) b0 &= b0 - 1;
+        const int w0 = __ffs(led ? go : b0) - 1;
+        unsigned members = led ? go : go & ~((2u << w0) - 1u);
+        const unsigned ends = members & end;
+        if (ends) members &= ((ends & (0u - ends)) << 1) - 1u;
+        const int* p = wp.rec + ((blockIdx.x * (long long)C::kWarps + w0) * 2 + (led ? 0 : 1)) * kPcInts;
+        const int c_heads = p[kPcHeads];
+        if (row >= p[kPcNtok] * c_heads) continue;
+        Joined<N> x;
+        auto add = [&](int w, int slot, bool here) {
+            const long long q = ((blockIdx.x * (long long)C::kWarps + w) * 2 + slot) * C::kRows;
+            const float* part = here ? reinterpret_cast<const float*>(smem + w * C::kRing) : wp.part + q * D;
+            const float2* stats = here ? reinterpret_cast<const float2*>(smem + w * C::kRing + C::kRows * D * 4)
+                                       : wp.stats + q;
+            const float2 st = stats[row];
+            float y[N];
+            load_cols<N>(part + row * D + col, y);
+            x.add(st.x, st.y, y);
+        };
+        if (!led) add(w0, 1, true);            // (what an item begins with is its warp's last piece)
+        for (; members; members &= members - 1) {
+            const int w = __ffs(members) - 1;
+            add(w, 0, (kept >> w) & 1);
+        }
+        if (!led && ends) {
+            write_joined<FP16, N>(a, x, p[kPcTok0], p[kPcHead], c_heads, row, col);
+        } else {
+            const long long q = (blockIdx.x * 2LL + (led ? 0 : 1)) * C::kRows + row;
+            if (col == 0) cp.stats[q] = make_float2(x.top, x.sum);
 #pragma unroll
-                    for (int e = 0; e < N; ++e) y[e] = 0.0f;
-                }
-                x.add(st.x, st.y, y);
-            }
-            if (complete) {
-                write_joined<FP16, N>(a, x, c_tok0, c_head, c_heads, row, col);
-            } else {
-                const long long q = (blockIdx.x * 2LL + slot0) * C::kRows + row;
-                if (col == 0) cp.stats[q] = make_float2(x.top, x.sum);
-#pragma unroll
-                for (int e = 0; e < N; ++e) cp.part[q * D + col + e] = x.acc[e];
-            }
+            for (int e = 0; e < N; ++e) cp.part[q * D + col + e] = x.acc[e];
         }
-        if (!complete && threadIdx.x == 0) {
-            int* r = crec + slot0 * kPcInts;
-            r[kPcTok0] = c_tok0;
-            r[kPcNtok] = c_ntok;
-            r[kPcHead] = c_head;
-            r[kPcHeads] = c_heads;
-            r[kPcLast] = ends;
-        }
-        if (!complete) {
-            __syncthreads();               // (the record's first word was cleared above)
-            if (threadIdx.x == 0) crec[slot0 * kPcInts + kPcUsed] = 1;
-        }
-        // on to what follows the chain
-        w = last_w;
-        slot = count == 1 ? slot0 : 0;
-        if (++slot == 2) { slot = 0; ++w; }
     }
 }
 
