@@ -26,7 +26,8 @@ SOURCES = ["api.cu", "schedule.cu", "fp8_logits.cu", "fp8_logits_h8.cu", "fp8_lo
            "topk.cu", "mxfp4_logits.cu", "noalloc.cu", "api_serving.cu", "rope.cu",
            "index_quant.cu", "pages.cu", "paged_attention.cu", "paged_attention_d64.cu",
            "paged_attention_d128.cu", "api_nvfp4.cu", "nvfp4_cache.cu", "nvfp4_attention.cu",
-           "nvfp4_attention_d64.cu", "nvfp4_attention_d128.cu"]
+           "nvfp4_attention_d64.cu", "nvfp4_attention_d128.cu", "paged_attention_nvfp4_d64.cu",
+           "paged_attention_nvfp4_d128.cu"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
     "-O3", "-lineinfo", "-std=c++17",

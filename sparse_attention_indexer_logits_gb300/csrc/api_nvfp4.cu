@@ -16,6 +16,12 @@ using namespace pml;
 constexpr int kMaxListed = 0x7fffff00; // entries of a list, so that their tiles' ends fit an int
 constexpr int kMaxHeads = 8192;
 constexpr int kMaxScaleExponent = 32;
+// Rows ((token, head) pairs of a kv head) up to which a request's attention is
+// left to warps alone.
+#ifndef NVROWS
+#define NVROWS 16
+#endif
+constexpr int kNvWarpRows = NVROWS;
 
 // Strides of a dimension of one element are never used: any valid one will do.
 int64_t used(int64_t stride, int64_t size, int64_t other) { return size > 1 ? stride : other; }
@@ -70,8 +76,9 @@ int attention_call(NvAttnArgs& a, const void* q, int64_t q_token, int64_t q_head
     int rc = take_cache(k_cache, num_pages, kv_heads, head_dim, a.kc);
     if (rc == PML_OK) rc = take_cache(v_cache, num_pages, kv_heads, head_dim, a.vc);
     if (rc != PML_OK) return rc;
-    if ((tokens > 1 && (q_token % 8 || out_token % 8)) || (num_heads > 1 && (q_head % 8 || out_head % 8)))
-        return PML_ERR_ALIGNMENT;
+    const int64_t qs[2] = {used(q_head, num_heads, head_dim), used(q_token, tokens, head_dim)};
+    if (qs[0] <= 0 || qs[0] % 8 || qs[1] <= 0 || qs[1] % 8) return PML_ERR_ALIGNMENT;
+    if ((tokens > 1 && out_token % 8) || (num_heads > 1 && out_head % 8)) return PML_ERR_ALIGNMENT;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) || !aligned(lse, 4) ||
         !aligned(block_table, 4) || !aligned(kv_lens, 4) || !aligned(a.cu_q, 4))
         return PML_ERR_ALIGNMENT;
@@ -79,6 +86,52 @@ int attention_call(NvAttnArgs& a, const void* q, int64_t q_token, int64_t q_head
     cudaError_t e = device_info(dev);
     if (e != cudaSuccess) return cuda_fail(e);
     if (workspace_bytes < pml_attention_workspace_bytes(dev.sm_count, head_dim)) return PML_ERR_INVALID_ARG;
+    const int group = num_heads / kv_heads;
+    const bool fp16 = dtype == PML_DTYPE_FLOAT16;
+    const float scale = softmax_scale * a.kc.scale;
+    const long long per_request = a.selected ? 1 : (tokens + a.batch - 1) / a.batch;
+    if (per_request * group > kNvWarpRows && group <= kAttnHalfRows) {
+        AttnArgs w = {};
+        attention_workspace(w, workspace, dev.sm_count, head_dim);
+        w.kc4 = a.kc;
+        w.vc4 = a.vc;
+        w.out_scale = a.vc.scale;
+        w.block_table = block_table;
+        w.bt_stride = bt_stride;
+        w.bt_width = bt_width;
+        w.kv_lens = kv_lens;
+        w.cu_q = a.cu_q;
+        w.requests = a.requests;
+        w.selected = a.selected;
+        w.sel_stride = a.sel_stride;
+        w.sel_k = a.sel_k;
+        w.out = out;
+        w.out_token = out_token;
+        w.out_head = out_head;
+        w.lse = lse;
+        w.status = dev.status;
+        w.num_pages = num_pages;
+        w.batch = a.batch;
+        w.tokens = tokens;
+        w.q_per_request = a.q_per_request;
+        w.kv_heads = kv_heads;
+        w.group = group;
+        w.half_tokens = kAttnHalfRows / group;
+        w.causal = a.causal;
+        w.window = a.window;
+        w.scale = scale;
+        w.scale_log2 = scale * 1.4426950408889634f;
+        CUtensorMap qmap;
+        const uint64_t dims[3] = {(uint64_t)head_dim, (uint64_t)num_heads, (uint64_t)tokens};
+        const uint64_t strides[2] = {(uint64_t)qs[0] * 2, (uint64_t)qs[1] * 2};
+        const uint32_t box[3] = {64, (uint32_t)group, (uint32_t)w.half_tokens};
+        e = encode_tiled(qmap, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, dims,
+                         strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+        if (e != cudaSuccess) return cuda_fail(e);
+        e = launch_paged_attention_nvfp4(head_dim, fp16, a.selected != nullptr, qmap, w, dev.sm_count,
+                                         static_cast<cudaStream_t>(stream));
+        return e == cudaSuccess ? PML_OK : cuda_fail(e);
+    }
     a.q = q;
     a.q_token = q_token;
     a.q_head = q_head;
@@ -94,10 +147,10 @@ int attention_call(NvAttnArgs& a, const void* q, int64_t q_token, int64_t q_head
     a.num_pages = num_pages;
     a.tokens = tokens;
     a.kv_heads = kv_heads;
-    a.group = num_heads / kv_heads;
-    a.scale = softmax_scale * a.kc.scale;
-    a.scale_log2 = a.scale * 1.4426950408889634f;
-    e = launch_nvfp4_attention(head_dim, dtype == PML_DTYPE_FLOAT16, a, dev.sm_count, workspace, workspace_bytes,
+    a.group = group;
+    a.scale = scale;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    e = launch_nvfp4_attention(head_dim, fp16, a, dev.sm_count, workspace, workspace_bytes,
                                static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PML_OK : cuda_fail(e);
 }

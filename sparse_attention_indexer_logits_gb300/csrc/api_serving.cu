@@ -175,13 +175,7 @@ int attention_call(AttnArgs& a, const void* q, int64_t q_token, int64_t q_head, 
     const int num_ctas = dev.sm_count;
     if (workspace_bytes < pml_attention_workspace_bytes(num_ctas, head_dim)) return PML_ERR_INVALID_ARG;
 
-    const int64_t slots = 2LL * num_ctas;
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    a.partial = reinterpret_cast<float*>(ws);
-    ws += slots * kAttnSlotRows * head_dim * 4LL;
-    a.stats = reinterpret_cast<float2*>(ws);
-    ws += slots * kAttnSlotRows * 8;
-    a.pieces = reinterpret_cast<int*>(ws);
+    attention_workspace(a, workspace, num_ctas, head_dim);
     a.k_cache = k_cache;
     a.v_cache = v_cache;
     a.k_slot = ks[0];
@@ -205,6 +199,7 @@ int attention_call(AttnArgs& a, const void* q, int64_t q_token, int64_t q_head, 
     a.group = group;
     a.half_tokens = kAttnHalfRows / group;
     a.scale = softmax_scale;
+    a.out_scale = 1.0f;
     a.scale_log2 = softmax_scale * 1.4426950408889634f;
 
     const bool fp16 = dtype == PML_DTYPE_FLOAT16;

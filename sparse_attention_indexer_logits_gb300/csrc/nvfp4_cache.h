@@ -9,17 +9,6 @@
 
 namespace pml {
 
-constexpr int kNvGroup = 16;       // values of a scale
-
-// One of the two caches: a row's codes and its scales.  Strides in bytes.
-struct NvCache {
-    uint8_t* codes;
-    uint8_t* scales;
-    long long page, slot, head;
-    long long s_page, s_slot, s_head;
-    float scale;                   // of all values, a power of two
-};
-
 struct NvAppendArgs {
     SlotArgs slot;
     const void* positions;         // int32 or int64, one per token

@@ -9,6 +9,9 @@ cudaError_t launch_attention_d64(bool, bool, const CUtensorMap&, const CUtensorM
 cudaError_t launch_attention_d128(bool, bool, const CUtensorMap&, const CUtensorMap&,
                                   const CUtensorMap&, const AttnArgs&, int, cudaStream_t);
 
+cudaError_t launch_attention_nvfp4_d64(bool, bool, const CUtensorMap&, const AttnArgs&, int, cudaStream_t);
+cudaError_t launch_attention_nvfp4_d128(bool, bool, const CUtensorMap&, const AttnArgs&, int, cudaStream_t);
+
 namespace {
 
 using namespace attn;
@@ -45,7 +48,7 @@ struct Joined {
         for (int k = 0; k < N; ++k) v[k] = part[2 + k][lane];
         add(part[0][lane], part[1][lane], v, scale_log2);
     }
-    __device__ float inverse() const { return sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f; }
+    __device__ float inverse(float scale) const { return sum > 0.0f || sum != sum ? scale / sum : 0.0f; }
     __device__ float log_sum(float scale, float sum_scale) const
     {
         return sum == 0.0f ? -INFINITY : top * scale + logf(sum * sum_scale);
@@ -132,7 +135,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const A
         if (warp > 0) return;
         for (int q = 1; q < kJoinWarps; ++q) x.take(part[q], lane, a.scale_log2);
         if (!valid) return;
-        const float inv = x.inverse();
+        const float inv = x.inverse(a.out_scale);
         const int i = row / G, g = row % G;
         const long long token = tok0 + i;
         const int qhead = head * G + g;
@@ -161,7 +164,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const A
         for (int q = 1; q < splits; ++q) x.take(part[(q << groups_log2) + grp], lane, a.scale_log2);
     }
     if (!valid) return;
-    const float inv = x.inverse();
+    const float inv = x.inverse(a.out_scale);
     const int i = half * a.half_tokens + in_half / G, g = in_half % G;
     const long long token = tok0 + i;
     const int qhead = head * G + g;
@@ -181,19 +184,31 @@ cudaError_t launch_join(const AttnArgs& a, int num_ctas, cudaStream_t stream)
                             kJoinWarps * 32, 0, stream, a, num_ctas);
 }
 
+cudaError_t join(int head_dim, bool fp16, const AttnArgs& a, int num_ctas, cudaStream_t stream)
+{
+    if (head_dim == 128)
+        return fp16 ? launch_join<128, true>(a, num_ctas, stream) : launch_join<128, false>(a, num_ctas, stream);
+    return fp16 ? launch_join<64, true>(a, num_ctas, stream) : launch_join<64, false>(a, num_ctas, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_paged_attention(int head_dim, bool fp16, bool select, const CUtensorMap& qmap,
                                    const CUtensorMap& kmap, const CUtensorMap& vmap,
                                    const AttnArgs& a, int num_ctas, cudaStream_t stream)
 {
-    cudaError_t e = head_dim == 128
-                        ? launch_attention_d128(fp16, select, qmap, kmap, vmap, a, num_ctas, stream)
-                        : launch_attention_d64(fp16, select, qmap, kmap, vmap, a, num_ctas, stream);
-    if (e != cudaSuccess) return e;
-    if (head_dim == 128)
-        return fp16 ? launch_join<128, true>(a, num_ctas, stream) : launch_join<128, false>(a, num_ctas, stream);
-    return fp16 ? launch_join<64, true>(a, num_ctas, stream) : launch_join<64, false>(a, num_ctas, stream);
+    const cudaError_t e = head_dim == 128
+                              ? launch_attention_d128(fp16, select, qmap, kmap, vmap, a, num_ctas, stream)
+                              : launch_attention_d64(fp16, select, qmap, kmap, vmap, a, num_ctas, stream);
+    return e != cudaSuccess ? e : join(head_dim, fp16, a, num_ctas, stream);
+}
+
+cudaError_t launch_paged_attention_nvfp4(int head_dim, bool fp16, bool select, const CUtensorMap& qmap,
+                                         const AttnArgs& a, int num_ctas, cudaStream_t stream)
+{
+    const cudaError_t e = head_dim == 128 ? launch_attention_nvfp4_d128(fp16, select, qmap, a, num_ctas, stream)
+                                          : launch_attention_nvfp4_d64(fp16, select, qmap, a, num_ctas, stream);
+    return e != cudaSuccess ? e : join(head_dim, fp16, a, num_ctas, stream);
 }
 
 }  // namespace pml

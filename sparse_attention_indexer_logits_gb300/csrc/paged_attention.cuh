@@ -81,6 +81,7 @@ constexpr int kThreads = 384;      // three warpgroups: softmax, softmax, MMA an
 // gives some back and the softmax groups, which hold a row of S, take them
 // (2 * 208 + 88 = 3 * 168).
 constexpr int kLaunchRegs = 168, kHighRegs = 208, kLowRegs = 88;
+constexpr int kFp4HighRegs = 200, kFp4LowRegs = 104;    // caches in 4 bits: the copying warps hold a tile's codes
 // (a scheduler serves warps w, w + 4, w + 8: the issuer, which polls, is not
 // with the warps that hold the first 32 rows, all the rows of a small call)
 constexpr int kSoftmaxWarps = 8;
@@ -399,7 +400,7 @@ __device__ __forceinline__ Start find_start(const AttnArgs& a, long long* units,
     return s;
 }
 
-template <int D, bool FP16, bool SEL>
+template <int D, bool FP16, bool SEL, bool FP4 = false>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap qmap,
                            const __grid_constant__ CUtensorMap kmap,
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         *total_places = -1;
         st_release_shared(landed_word, 0);
         for (int s = 0; s < S; ++s) {
-            mbar_init(full_bar(s), SEL ? 2 : 1);
+            mbar_init(full_bar(s), SEL || FP4 ? 2 : 1);
             mbar_init(empty_bar(s), 1);
         }
         mbar_init(drain, 1);
@@ -462,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_mbar_init();
         tma_prefetch_map(&qmap);
-        if (!SEL) {
+        if (!SEL && !FP4) {
             tma_prefetch_map(&kmap);
             tma_prefetch_map(&vmap);
         }
@@ -476,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_dependency_wait();
     const int sel_tiles = SEL ? (a.sel_k + kAttnTileKeys - 1) / kAttnTileKeys : 0;
     Start start = {0, 0, 0, 0, 0};
-    const bool loads = warp == kLoadWarp || (SEL && warp == kGatherWarp);
+    const bool loads = warp == kLoadWarp || ((SEL || FP4) && warp == kGatherWarp);
     const bool lead = warp == kLoadWarp;
     if (loads) {
         if constexpr (SEL) {
@@ -503,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
 
     if (warp >= kSoftmaxWarps) {
-        regs_dec<kLowRegs>();
+        regs_dec<FP4 ? kFp4LowRegs : kLowRegs>();
     if (loads) {
         // ------------------------------------------------------------ producer
         int b = start.b, head = start.head, tile = start.tile, at = start.at;
@@ -620,7 +621,166 @@ __global__ void __launch_bounds__(kThreads, 1)
 
             // ---- K and V tiles: K runs `ahead` tiles before V
             const int ahead = alt ? 2 : 1;
-            if constexpr (SEL) {
+            if constexpr (FP4) {
+                // Codes to 16-bit tiles: each of the two warps has half of a
+                // tile's rows.  A lane takes sixteen bytes of a row (eight lanes
+                // side by side the same bytes of eight rows, whose chunks the
+                // swizzle puts into different banks), turns them into 64, and
+                // loads the next tile's as it goes, so that they are there when
+                // the next stage is free.
+                constexpr int CB = D / 2, kRowLanes = CB / 16, kInst = 32 / kRowLanes, kIter = 64 / kInst;
+                const int r_in = (lane & 7) + 8 * (lane / (8 * kRowLanes)), chunk = (lane >> 3) % kRowLanes;
+                const int row0 = lead ? 0 : 64;
+                const int32_t* table = a.block_table + (long long)req * a.bt_stride;
+                auto checked = [&](int page) {
+                    const bool bad = page < 0 || page >= a.num_pages;
+                    if (bad) atomicOr(a.status, kStatusBadBlock);
+                    return bad ? 0 : page;
+                };
+                // what `fetch` reads
+                const uint8_t *src = nullptr, *ssrc = nullptr;
+                long long step = 0, sstep = 0;         // dense: of kInst rows
+                int row_lo = 0, row_hi = 0;            // dense: the page's rows that are there
+                long long at0 = -1, at1 = -1, sat0 = 0, sat1 = 0;   // selected: places of rows lane and lane + 32
+                // dense: 32 table entries from page `win` on, one a lane; pages of
+                // the one or two tiles whose K is in and V is not
+                const int page_begin = sp.lo / kBlockKeys, page_end = sp.hi > 0 ? (sp.hi - 1) / kBlockKeys + 1 : 0;
+                int win = -1, entry = 0, pg0 = 0, pg1 = 0;
+                // selected: positions of the next tiles, and pages of the nearer ones
+                const int32_t* list = SEL ? a.selected + (long long)b * a.sel_stride : nullptr;
+                auto positions = [&](int t) {
+                    const int i = (j0 + t) * kAttnTileKeys + row0 + lane;
+                    const int x = t < n && i < a.sel_k ? __ldg(list + i) : -1;
+                    const int y = t < n && i + 32 < a.sel_k ? __ldg(list + i + 32) : -1;
+                    return make_int2(x < kv ? x : -1, y < kv ? y : -1);
+                };
+                auto pages = [&](int2 p) {
+                    return make_int2(p.x >= 0 ? __ldg(table + (p.x >> 6)) : 0, p.y >= 0 ? __ldg(table + (p.y >> 6)) : 0);
+                };
+                int2 p0 = {}, p1 = {}, p2 = {}, g0 = {}, g1 = {}, vp0 = {}, vg0 = {}, vp1 = {}, vg1 = {};
+                if constexpr (SEL) {
+                    p0 = positions(0);
+                    p1 = positions(1);
+                    p2 = positions(2);
+                    g0 = pages(p0);
+                    g1 = pages(p1);
+                }
+                int nk = 0, nv = 0;
+                // The next tile in order, K `ahead` tiles before V; false: none is left.
+                auto pick = [&]() {
+                    if (nv >= n) return false;
+                    const bool is_k = nk < n && nk - nv < ahead;
+                    const NvCache& c = is_k ? a.kc4 : a.vc4;
+                    src = c.codes + head * c.head + chunk * 16;
+                    ssrc = c.scales + head * c.s_head + chunk * 2;
+                    if constexpr (SEL) {
+                        int2 p = vp0, g = vg0;
+                        if (is_k) {
+                            g0.x = checked(g0.x);
+                            g0.y = checked(g0.y);
+                            p = p0;
+                            g = g0;
+                            if (nk == nv) { vp0 = p0; vg0 = g0; }
+                            else { vp1 = p0; vg1 = g0; }
+                            ++nk;
+                            p0 = p1; g0 = g1;
+                            p1 = p2; g1 = pages(p1);
+                            p2 = positions(nk + 2);
+                        } else {
+                            vp0 = vp1; vg0 = vg1;
+                            ++nv;
+                        }
+                        at0 = p.x < 0 ? -1 : g.x * c.page + (p.x & 63) * c.slot;
+                        at1 = p.y < 0 ? -1 : g.y * c.page + (p.y & 63) * c.slot;
+                        sat0 = g.x * c.s_page + (p.x & 63) * c.s_slot;
+                        sat1 = g.y * c.s_page + (p.y & 63) * c.s_slot;
+                    } else {
+                        int page = pg0, tile_at = nv;
+                        if (is_k) {
+                            const int pg = 2 * (j0 + nk) + (lead ? 0 : 1);
+                            if (win < 0 || pg >= win + 32) {
+                                win = pg;
+                                entry = pg + lane >= page_begin && pg + lane < page_end
+                                            ? checked(__ldg(table + pg + lane)) : 0;
+                            }
+                            page = __shfl_sync(0xffffffffu, entry, pg - win);
+                            if (nk == nv) pg0 = page;
+                            else pg1 = page;
+                            tile_at = nk++;
+                        } else {
+                            pg0 = pg1;
+                            ++nv;
+                        }
+                        const int first_key = (j0 + tile_at) * kAttnTileKeys + row0;
+                        row_lo = sp.lo - first_key;
+                        row_hi = sp.hi - first_key;
+                        src += page * c.page + r_in * c.slot;
+                        ssrc += page * c.s_page + r_in * c.s_slot;
+                        step = kInst * c.slot;
+                        sstep = kInst * c.s_slot;
+                    }
+                    return true;
+                };
+                uint4 codes[kIter];
+                uint32_t scales[kIter];
+                auto fetch = [&](int i) {
+                    codes[i] = make_uint4(0u, 0u, 0u, 0u);
+                    scales[i] = 0;
+                    if constexpr (SEL) {
+                        const int r = (i * kInst + r_in) & 31;
+                        const long long o = __shfl_sync(0xffffffffu, i * kInst < 32 ? at0 : at1, r);
+                        const long long so = __shfl_sync(0xffffffffu, i * kInst < 32 ? sat0 : sat1, r);
+                        if (o >= 0) {
+                            codes[i] = __ldg(reinterpret_cast<const uint4*>(src + o));
+                            scales[i] = __ldg(reinterpret_cast<const uint16_t*>(ssrc + so));
+                        }
+                    } else if (const int r = i * kInst + r_in; r >= row_lo && r < row_hi) {
+                        codes[i] = __ldg(reinterpret_cast<const uint4*>(src + i * step));
+                        scales[i] = __ldg(reinterpret_cast<const uint16_t*>(ssrc + i * sstep));
+                    }
+                };
+                bool more = pick();
+                if (more)
+#pragma unroll
+                    for (int i = 0; i < kIter; ++i) fetch(i);
+#pragma unroll 1
+                while (more && ok) {
+                    const int st = pos % S;
+                    ok = warp_wait(empty_bar(st), (uint32_t)((pos / S) & 1) ^ 1u, abort_flag, a.status);
+                    if (!ok) break;
+                    more = pick();
+                    const uint32_t dst = base + C::kRing + st * C::kStageBytes + (chunk >> 1) * C::kBlockBytes +
+                                         (row0 + r_in) * 128;
+#pragma unroll
+                    for (int i = 0; i < kIter; ++i) {
+                        const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+                        uint32_t m2;
+                        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(m2) : "h"((uint16_t)scales[i]));
+                        const uint32_t m[2] = {__byte_perm(m2, m2, 0x1010), __byte_perm(m2, m2, 0x3232)};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t x[4];
+                            e2m1x8_to_f16x2x4(w[q], x);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                x[e] = mul_f16x2(x[e], m[q >> 1]);
+                                if constexpr (!FP16) {
+                                    const float2 f = unpack16<true>(x[e]);
+                                    x[e] = pack16<false>(f.x, f.y);
+                                }
+                            }
+                            st_shared_v4(dst + i * kInst * 128 + ((((chunk & 1) * 4 + q) ^ (lane & 7)) << 4), x[0], x[1],
+                                         x[2], x[3]);
+                        }
+                        if (more) fetch(i);
+                    }
+                    fence_proxy_async_smem();     // the tensor core reads what this lane has written
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full_bar(st));
+                    ++pos;
+                }
+                handed = pos;
+            } else if constexpr (SEL) {
                 const int32_t* list = a.selected + (long long)b * a.sel_stride;
                 const int32_t* table = a.block_table + (long long)req * a.bt_stride;
                 const int row0 = lead ? 0 : 64;
@@ -946,7 +1106,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     }
     } else {
-        regs_inc<kHighRegs>();
+        regs_inc<FP4 ? kFp4HighRegs : kHighRegs>();
         // ------------------------------------------------------------ softmax
         const int h = warp >> 2;                 // half
         const int quad = warp & 3;
@@ -1257,7 +1417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (active) {
                 if (whole) {
-                    const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+                    const float inv = sum > 0.0f || sum != sum ? (FP4 ? a.out_scale : 1.0f) / sum : 0.0f;
                     g0 *= inv;
                     g1 *= inv;
                 }
@@ -1327,11 +1487,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D, bool FP16, bool SEL>
+template <int D, bool FP16, bool SEL, bool FP4 = false>
 cudaError_t launch_kernel(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
                           const AttnArgs& a, int num_ctas, cudaStream_t stream)
 {
-    auto kernel = paged_attention_kernel<D, FP16, SEL>;
+    auto kernel = paged_attention_kernel<D, FP16, SEL, FP4>;
     static int configured_device = -1;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1344,7 +1504,8 @@ cudaError_t launch_kernel(const CUtensorMap& qmap, const CUtensorMap& kmap, cons
         cudaFuncAttributes fa;
         e = cudaFuncGetAttributes(&fa, kernel);
         if (e != cudaSuccess) return e;
-        if (fa.numRegs != kLaunchRegs || 2 * kHighRegs + kLowRegs > 3 * kLaunchRegs)
+        constexpr int high = FP4 ? kFp4HighRegs : kHighRegs, low = FP4 ? kFp4LowRegs : kLowRegs;
+        if (fa.numRegs != kLaunchRegs || 2 * high + low > 3 * kLaunchRegs)
             return cudaErrorInvalidConfiguration;
         configured_device = dev;
     }

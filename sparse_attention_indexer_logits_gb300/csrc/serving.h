@@ -157,6 +157,18 @@ constexpr int kAttnHalfRows = 128;     // rows of one MMA accumulator
 constexpr int kAttnSlotRows = 2 * kAttnHalfRows;
 constexpr int kAttnMaxBatch = 16384;
 
+// A K or V cache held in 4 bits: a row's E2M1 codes and its E4M3 scales, one of
+// sixteen values.  Strides in bytes.
+struct NvCache {
+    uint8_t* codes;
+    uint8_t* scales;
+    long long page, slot, head;
+    long long s_page, s_slot, s_head;
+    float scale;                   // of all values, a power of two
+};
+
+constexpr int kNvGroup = 16;       // values of a scale
+
 struct AttnArgs {
     const int32_t* block_table;
     const int32_t* kv_lens;        // per request
@@ -189,13 +201,31 @@ struct AttnArgs {
     int window;                    // > 0: only keys past position - window
     float scale_log2;              // softmax scale * log2(e)
     float scale;
+    float out_scale;               // of the output: 1, or that of the values in 4 bits
+    NvCache kc4, vc4;              // caches held in 4 bits
 };
 
 constexpr int kPieceInts = 8;
 
+// Lays the attention's workspace out.
+inline void attention_workspace(AttnArgs& a, void* workspace, int num_ctas, int head_dim)
+{
+    const long long slots = 2LL * num_ctas;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.partial = reinterpret_cast<float*>(ws);
+    ws += slots * kAttnSlotRows * head_dim * 4LL;
+    a.stats = reinterpret_cast<float2*>(ws);
+    ws += slots * kAttnSlotRows * 8;
+    a.pieces = reinterpret_cast<int*>(ws);
+}
+
 cudaError_t launch_paged_attention(int head_dim, bool fp16, bool select, const CUtensorMap& qmap,
                                    const CUtensorMap& kmap, const CUtensorMap& vmap,
                                    const AttnArgs& a, int num_ctas, cudaStream_t stream);
+
+// The same over a.kc4 and a.vc4.
+cudaError_t launch_paged_attention_nvfp4(int head_dim, bool fp16, bool select, const CUtensorMap& qmap,
+                                         const AttnArgs& a, int num_ctas, cudaStream_t stream);
 
 cudaError_t launch_pages_fork(const ForkArgs& a, cudaStream_t stream);
 cudaError_t launch_pages_extend(const ExtendArgs& a, cudaStream_t stream);
