@@ -203,14 +203,10 @@ int pml_append_nvfp4(const void* k, int64_t k_token_stride, int64_t k_head_strid
     a.tokens = tokens;
     a.heads = kv_heads;
     a.dim = head_dim;
-    // rows of a CTA: fewer where that would leave SMs without work, and no more
-    // than lie in kNvAppendMaxTokens tokens wherever the first one begins
-    const long long rows = 2LL * kv_heads, side = kNvAppendThreads / (head_dim / kNvGroup);
-    int units = kNvAppendUnits;
-    while (units > 1 && tokens * rows < units * side * 2 * dev.sm_count) --units;
-    const long long most = (kNvAppendMaxTokens - 1) * rows + 1;
-    a.rows_per_cta = (int)(units * side < most ? units * side : most);
-    if (tokens * rows / a.rows_per_cta >= 0x7fffffffLL) return PML_ERR_UNSUPPORTED;    // CTAs
+    // fewer groups a thread where more would leave SMs without work
+    const long long groups = 2LL * tokens * kv_heads * (head_dim / kNvGroup);
+    a.units = kNvAppendUnits;
+    while (a.units > 1 && groups < (long long)a.units * kNvAppendThreads * 2 * dev.sm_count) --a.units;
     e = launch_nvfp4_append(a, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PML_OK : cuda_fail(e);
 }

@@ -16,21 +16,23 @@ namespace {
 
 using namespace nvattn;
 
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 8, kJoinRows = 4;
 
 // A CTA whose pieces ended with an item that it had begun (slot 1) owns the
 // join: the item's other pieces are slot 0 of the following CTAs, up to the one
-// that holds its end.  A CTA here takes one row; each warp a part of the pieces,
-// in the order of their numbers, a lane two or four columns.
+// that holds its end.  A CTA here takes four rows, two warps each, which take
+// half of the pieces each in the order of their numbers, a lane two or four
+// columns.
 template <int D, bool FP16, int NT>
 __global__ void __launch_bounds__(kJoinWarps * 32) nvfp4_join_kernel(const NvAttnArgs a, const Pieces cp, int num_ctas)
 {
     constexpr int N = D / 32, kRows = 8 * NT;
-    __shared__ float part[kJoinWarps][N + 2][32];
+    __shared__ float part[kJoinRows][N + 2][32];
     allow_dependent_launch();
     grid_dependency_wait();
-    const int owner = blockIdx.x, row = blockIdx.y;
+    const int owner = blockIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row = blockIdx.y * kJoinRows + (warp >> 1), half = warp & 1;
     const int* rec = cp.rec + (owner * 2LL + 1) * kPcInts;
     // the first CTA after the owner that holds the item's end
     auto ends = [&](int cta) {
@@ -39,7 +41,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) nvfp4_join_kernel(const NvAtt
         return p[kPcUsed] && p[kPcLast];
     };
     unsigned who = __ballot_sync(0xffffffffu, ends(owner + 1 + lane));
-    if (!rec[kPcUsed] || row >= rec[kPcNtok] * rec[kPcHeads]) return;
+    const int rows = rec[kPcNtok] * rec[kPcHeads];
+    if (!rec[kPcUsed] || (int)blockIdx.y * kJoinRows >= rows) return;
     int end = owner + 1;
     while (!who && end + 32 < num_ctas) {
         end += 32;
@@ -49,43 +52,43 @@ __global__ void __launch_bounds__(kJoinWarps * 32) nvfp4_join_kernel(const NvAtt
     end += __ffs(who) - 1;
     const int pieces = end - owner + 1;
     Joined<N> x;
-    const int last = pieces * (warp + 1) / kJoinWarps;
+    if (row < rows) {
+        const int last = half ? pieces : pieces / 2;
 #pragma unroll 4
-    for (int p = pieces * warp / kJoinWarps; p < last; ++p) {
-        const int slot = p == 0 ? 1 : 0;
-        const long long at = (owner + p) * 2LL + slot;
-        const bool used = cp.rec[at * kPcInts + kPcUsed];      // (a range without a step left none)
-        float2 st = cp.stats[at * kRows + row];
-        float v[N];
-        load_cols<N>(cp.part + (at * kRows + row) * D + lane * N, v);
-        if (!used) {
-            st = make_float2(-INFINITY, 0.0f);
+        for (int p = half ? pieces / 2 : 0; p < last; ++p) {
+            const int slot = p == 0 ? 1 : 0;
+            const long long at = (owner + p) * 2LL + slot;
+            const bool used = cp.rec[at * kPcInts + kPcUsed];      // (a range without a step left none)
+            float2 st = cp.stats[at * kRows + row];
+            float v[N];
+            load_cols<N>(cp.part + (at * kRows + row) * D + lane * N, v);
+            if (!used) {
+                st = make_float2(-INFINITY, 0.0f);
 #pragma unroll
-            for (int k = 0; k < N; ++k) v[k] = 0.0f;
+                for (int k = 0; k < N; ++k) v[k] = 0.0f;
+            }
+            x.add(st.x, st.y, v);
         }
-        x.add(st.x, st.y, v);
     }
-    part[warp][0][lane] = x.top;
-    part[warp][1][lane] = x.sum;
+    if (half) {
+        part[warp >> 1][0][lane] = x.top;
+        part[warp >> 1][1][lane] = x.sum;
 #pragma unroll
-    for (int k = 0; k < N; ++k) part[warp][2 + k][lane] = x.acc[k];
+        for (int k = 0; k < N; ++k) part[warp >> 1][2 + k][lane] = x.acc[k];
+    }
     __syncthreads();
-    if (warp > 0) return;
-    Joined<N> y;
+    if (half || row >= rows) return;
+    float v[N];
 #pragma unroll
-    for (int q = 0; q < kJoinWarps; ++q) {
-        float v[N];
-#pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = part[q][2 + k][lane];
-        y.add(part[q][0][lane], part[q][1][lane], v);
-    }
-    write_joined<FP16, N>(a, y, rec[kPcTok0], rec[kPcHead], rec[kPcHeads], row, lane * N);
+    for (int k = 0; k < N; ++k) v[k] = part[warp >> 1][2 + k][lane];
+    x.add(part[warp >> 1][0][lane], part[warp >> 1][1][lane], v);
+    write_joined<FP16, N>(a, x, rec[kPcTok0], rec[kPcHead], rec[kPcHeads], row, lane * N);
 }
 
 template <int D, bool FP16, int NT>
 cudaError_t launch_join(const NvAttnArgs& a, const Pieces& cp, int num_ctas, cudaStream_t stream)
 {
-    return launch_dependent(nvfp4_join_kernel<D, FP16, NT>, dim3((unsigned)num_ctas, 8 * NT), kJoinWarps * 32, 0,
+    return launch_dependent(nvfp4_join_kernel<D, FP16, NT>, dim3((unsigned)num_ctas, 8 * NT / kJoinRows), kJoinWarps * 32, 0,
                             stream, a, cp, num_ctas);
 }
 
@@ -95,17 +98,19 @@ cudaError_t launch_join_dim(bool fp16, int tiles, const NvAttnArgs& a, const Pie
 {
     if (tiles == 1)
         return fp16 ? launch_join<D, true, 1>(a, cp, num_ctas, stream) : launch_join<D, false, 1>(a, cp, num_ctas, stream);
-    return fp16 ? launch_join<D, true, 2>(a, cp, num_ctas, stream) : launch_join<D, false, 2>(a, cp, num_ctas, stream);
+    if (tiles == 2)
+        return fp16 ? launch_join<D, true, 2>(a, cp, num_ctas, stream) : launch_join<D, false, 2>(a, cp, num_ctas, stream);
+    return fp16 ? launch_join<D, true, 4>(a, cp, num_ctas, stream) : launch_join<D, false, 4>(a, cp, num_ctas, stream);
 }
 
-// `n` pieces of two slots from `at` on.
-Pieces take(uint8_t*& at, int64_t n, int rows, int dim)
+// `n` pieces from `at` on, the rows of `slots` of their two slots.
+Pieces take(uint8_t*& at, int64_t n, int slots, int rows, int dim)
 {
     Pieces p;
     p.part = reinterpret_cast<float*>(at);
-    at += n * 2 * rows * dim * 4;
+    at += n * slots * rows * dim * 4;
     p.stats = reinterpret_cast<float2*>(at);
-    at += n * 2 * rows * 8;
+    at += n * slots * rows * 8;
     p.rec = reinterpret_cast<int*>(at);
     at += n * 2 * kPcInts * 4;
     return p;
@@ -116,17 +121,20 @@ Pieces take(uint8_t*& at, int64_t n, int rows, int dim)
 cudaError_t launch_nvfp4_attention(int head_dim, bool fp16, NvAttnArgs& a, int num_ctas, void* workspace,
                                    int64_t workspace_bytes, cudaStream_t stream)
 {
-    // Items of 8 or of 16 rows: the larger ones where a request's tokens fill them.
+    // Items of 8, 16 or 32 rows: the larger ones where a request's tokens fill them.
     const long long per_request = a.selected ? 1 : (a.tokens + a.batch - 1) / a.batch;
-    const int tiles = per_request * a.group > 8 ? 2 : 1, rows = 8 * tiles;
+#ifndef R2
+#define R2 16
+#endif
+    const int tiles = per_request * a.group > R2 ? 4 : per_request * a.group > 8 ? 2 : 1, rows = 8 * tiles;
     a.head_blocks = (a.group + rows - 1) / rows;
     a.block_heads = (a.group + a.head_blocks - 1) / a.head_blocks;
     a.tile_tokens = a.selected || a.group > rows ? 1 : rows / a.group;
-    const int warps = head_dim == 128 ? (tiles == 1 ? Cfg<128, 1>::kWarps : Cfg<128, 2>::kWarps)
-                                      : (tiles == 1 ? Cfg<64, 1>::kWarps : Cfg<64, 2>::kWarps);
+    const int warps = tiles == 1 ? Cfg<128, 1>::kWarps : tiles == 2 ? Cfg<128, 2>::kWarps
+                      : head_dim == 128 ? Cfg<128, 4>::kWarps : Cfg<64, 4>::kWarps;
     uint8_t* at = static_cast<uint8_t*>(workspace);
-    const Pieces wp = take(at, (int64_t)num_ctas * warps, rows, head_dim);
-    const Pieces cp = take(at, num_ctas, rows, head_dim);
+    const Pieces wp = take(at, (int64_t)num_ctas * warps, 1, rows, head_dim);
+    const Pieces cp = take(at, num_ctas, 2, rows, head_dim);
     if (at - static_cast<uint8_t*>(workspace) > workspace_bytes) return cudaErrorInvalidValue;    // never
     cudaError_t e = head_dim == 128 ? launch_nvfp4_attention_dim<128>(fp16, tiles, a, wp, cp, num_ctas, stream)
                                     : launch_nvfp4_attention_dim<64>(fp16, tiles, a, wp, cp, num_ctas, stream);

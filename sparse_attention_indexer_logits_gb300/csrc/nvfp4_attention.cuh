@@ -67,32 +67,49 @@ constexpr int kItemUnits = 2;
 constexpr float kPLog2 = 7.0f, kPMost = 15.0f;
 constexpr float kFresh = 1e30f;        // `off` of a row that has seen no key
 
+#ifndef W2
+#define W2 12
+#endif
+#ifndef S2
+#define S2 3
+#endif
+#ifndef W4
+#define W4 8
+#endif
+#ifndef S4
+#define S4 4
+#endif
+// NT: groups of eight rows in an item.  More than one: Q lies in shared memory.
 template <int D, int NT>
 struct Cfg {
     static constexpr int kRows = 8 * NT;
-    static constexpr int kWarps = NT == 1 ? 16 : 12;       // 128 or 168 registers a thread
+    static constexpr int kWarps = NT == 1 ? 16 : NT == 2 || D == 64 ? W2 : W4;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kCode = D / 2, kScale = D / 16;   // bytes of a row
     static constexpr int kStageBytes = 2 * kStepKeys * (kCode + kScale);
-    static constexpr int kStages = D == 128 ? (NT == 1 ? 3 : 4) : (NT == 1 ? 4 : 5);
+    static constexpr int kStages = D == 128 ? (NT == 4 ? S4 : NT == 2 ? S2 : 3) : 5;
     static constexpr int kRing = kStages * kStageBytes;    // of a warp
-    static constexpr int kMasks = kWarps * kRing;          // uint32 [kWarps][8]
+    static constexpr int kQ = kWarps * kRing;
+    static constexpr int kQBytes = NT == 1 ? 0 : kRows * D * 2;    // of a warp
+    static constexpr int kMasks = kQ + kWarps * kQBytes;   // uint32 [kWarps][8]
     static constexpr int kSums = kMasks + kWarps * 32;     // long long [kWarps]
     static constexpr int kRecs = kSums + kWarps * 8;       // pieces of the CTA
     static constexpr int kTotal = kRecs + kWarps * 2 * 4;
     static_assert(kTotal <= 232448, "shared memory of a CTA");
-    static_assert(kAttnMaxBatch * 8 <= kWarps * kRing, "a number per request fits the ring");
+    static_assert(kAttnMaxBatch * 8 <= kMasks, "a number per request fits the ring and Q");
+    static_assert(kRows * (D * 4 + 8) <= kRing, "a piece fits the ring");
 };
 
 // piece record in the workspace
 enum { kPcUsed, kPcTok0, kPcNtok, kPcHead, kPcHeads, kPcLast };
 constexpr int kPcInts = 8;
 
-// Where rows of a piece lie.
+// Where pieces lie: those of warps (slot 0 alone has rows here: slot 1, and the
+// last piece of a warp, stay in shared memory) and those of CTAs.
 struct Pieces {
     int* rec;          // [n][2][kPcInts]
-    float2* stats;     // [n][2][rows] (maximum, sum)
-    float* part;       // [n][2][rows][D]
+    float2* stats;     // [n][slots][rows] (maximum, sum)
+    float* part;       // [n][slots][rows][D]
 };
 
 __device__ __forceinline__ float exp2_approx(float x)
@@ -616,7 +633,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         }
 
         // ---- the rows scaled to fp16, and of rows 2 t and 2 t + 1 the factor, the exponent, the sum and the keys
-        uint32_t qb[NT][KS][2];
+        uint32_t qb[KS][2];                    // (of eight rows)
+        const uint32_t q_at = smem_addr(smem) + C::kQ + warp * C::kQBytes + lane * 16;
         float f[NT][2], off[NT][2], l[NT][2];
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
@@ -645,10 +663,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             }
 #pragma unroll
             for (int c = 0; c < KS / 2; ++c) {
-                qb[x][2 * c][0] = w[c].x;
-                qb[x][2 * c][1] = w[c].y;
-                qb[x][2 * c + 1][0] = w[c].z;
-                qb[x][2 * c + 1][1] = w[c].w;
+                if constexpr (NT == 1) {
+                    qb[2 * c][0] = w[c].x;
+                    qb[2 * c][1] = w[c].y;
+                    qb[2 * c + 1][0] = w[c].z;
+                    qb[2 * c + 1][1] = w[c].w;
+                } else {                           // (a lane reads what it has written)
+                    st_shared_v4(q_at + (x * (KS / 2) + c) * 512, w[c].x, w[c].y, w[c].z, w[c].w);
+                }
             }
             scale = fmaxf(scale, 1.2e-38f);        // (times -inf it stays -inf)
 #pragma unroll
@@ -705,7 +727,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                 }
             // (the two blocks of keys in turn: neither waits for its own sums)
 #pragma unroll
-            for (int c = 0; c < KS / 2; ++c)
+            for (int c = 0; c < KS / 2; ++c) {
+                uint4 q[NT];
+#pragma unroll
+                for (int x = 0; x < NT; ++x) {
+                    if constexpr (NT == 1) q[x] = make_uint4(qb[2 * c][0], qb[2 * c][1], qb[2 * c + 1][0], qb[2 * c + 1][1]);
+                    else q[x] = ld_shared_v4(q_at + (x * (KS / 2) + c) * 512);
+                }
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     uint32_t u[4], v[4];
@@ -717,14 +745,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                         v[e] = mul_f16x2(v[e], m[y][1][2 * c < KS / 2 ? 0 : 1]);
                     }
 #pragma unroll
-                    for (int x = 0; x < NT; ++x)
+                    for (int x = 0; x < NT; ++x) {
+                        if (c == 0) mma_first(sc[x][y], u[0], v[0], u[1], v[1], q[x].x, q[x].y);
+                        else mma(sc[x][y], u[0], v[0], u[1], v[1], q[x].x, q[x].y);
+                    }
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint32_t b0 = qb[x][2 * c + e][0], b1 = qb[x][2 * c + e][1];
-                            if (c + e == 0) mma_first(sc[x][y], u[0], v[0], u[1], v[1], b0, b1);
-                            else mma(sc[x][y], u[2 * e], v[2 * e], u[2 * e + 1], v[2 * e + 1], b0, b1);
-                        }
+                    for (int x = 0; x < NT; ++x) mma(sc[x][y], u[2], v[2], u[3], v[3], q[x].z, q[x].w);
                 }
+            }
             const int key0 = (j0 + s) * kStepKeys;
             bool parted = false;
             if constexpr (SEL) {
@@ -933,7 +961,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         } else {
             // The last piece stays in the ring, which nothing else needs any more.
             const int slot = first ? 1 : 0;
-            const long long at_piece = (worker * 2 + slot) * C::kRows;
+            const long long at_piece = worker * C::kRows;
             const bool here = left == 0;
             float* part = here ? reinterpret_cast<float*>(smem + warp * C::kRing) : wp.part + at_piece * D;
             float2* stats = here ? reinterpret_cast<float2*>(smem + warp * C::kRing + C::kRows * D * 4)
@@ -1003,8 +1031,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         const int c_heads = p[kPcHeads];
         if (row >= p[kPcNtok] * c_heads) continue;
         Joined<N> x;
-        auto add = [&](int w, int slot, bool here) {
-            const long long q = ((blockIdx.x * (long long)C::kWarps + w) * 2 + slot) * C::kRows;
+        auto add = [&](int w, bool here) {
+            const long long q = (blockIdx.x * (long long)C::kWarps + w) * C::kRows;
             const float* part = here ? reinterpret_cast<const float*>(smem + w * C::kRing) : wp.part + q * D;
             const float2* stats = here ? reinterpret_cast<const float2*>(smem + w * C::kRing + C::kRows * D * 4)
                                        : wp.stats + q;
@@ -1013,10 +1041,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             load_cols<N>(part + row * D + col, y);
             x.add(st.x, st.y, y);
         };
-        if (!led) add(w0, 1, true);            // (what an item begins with is its warp's last piece)
+        if (!led) add(w0, true);            // (what an item begins with is its warp's last piece)
         for (; members; members &= members - 1) {
             const int w = __ffs(members) - 1;
-            add(w, 0, (kept >> w) & 1);
+            add(w, (kept >> w) & 1);
         }
         if (!led && ends) {
             write_joined<FP16, N>(a, x, p[kPcTok0], p[kPcHead], c_heads, row, col);

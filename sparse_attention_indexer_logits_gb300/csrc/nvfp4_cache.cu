@@ -103,61 +103,59 @@ __device__ __forceinline__ uint2 quantise16(const uint4 (&v)[2], float g, uint32
                       b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24));
 }
 
-// A thread takes a group of sixteen, `lanes` threads a row, a CTA a few rows a
-// thread of the flattened (token, k heads then v heads) list; the rows are on
-// their way while the tokens' slots are looked up.
+// A thread takes a group of sixteen, eight (four) threads a row; a CTA sixteen
+// tokens and a few of their rows (k's heads, then v's).  Neighbouring rows of
+// threads are neighbouring tokens of one head: what a warp writes is 256 bytes
+// of codes and a whole sector of scales in a page that holds its heads one after
+// another.  The rows are on their way while the tokens' slots are looked up.
 template <int D, bool FP16>
-__global__ void __launch_bounds__(kNvAppendThreads) nvfp4_append_kernel(const NvAppendArgs a)
+__global__ void __launch_bounds__(kNvAppendThreads, 4) nvfp4_append_kernel(const NvAppendArgs a)
 {
     constexpr int kLanes = D / kNvGroup;
-    constexpr int kRows = kNvAppendThreads / kLanes;
-    __shared__ long long page_of[kNvAppendMaxTokens];     // -1: nothing is written
-    __shared__ int slot_of[kNvAppendMaxTokens];
+    constexpr int kRows = kNvAppendThreads / kLanes;       // (token, head) rows of a unit
+    __shared__ long long page_of[kNvAppendTokens];         // -1: nothing is written
+    __shared__ int slot_of[kNvAppendTokens];
     allow_dependent_launch();
     grid_dependency_wait();
-    const int rows = 2 * a.heads;
-    const long long row0 = (long long)blockIdx.x * a.rows_per_cta;
-    const int count = (int)min((long long)a.rows_per_cta, (long long)a.tokens * rows - row0);
-    const long long token0 = row0 / rows;
-    const int first = (int)(row0 - token0 * rows);
-    const int nt = (first + count - 1) / rows + 1;
+    const long long token0 = (long long)blockIdx.x * kNvAppendTokens;
+    const int nt = (int)min((long long)kNvAppendTokens, a.tokens - token0);
+    const int head0 = blockIdx.y * a.units * (kRows / kNvAppendTokens);
     const int g = threadIdx.x % kLanes, i0 = threadIdx.x / kLanes;
+    const int t = i0 % kNvAppendTokens;
     uint4 v[kNvAppendUnits][2];
-    int tok[kNvAppendUnits], head[kNvAppendUnits];
+    auto head_of = [&](int u) { return head0 + u * (kRows / kNvAppendTokens) + i0 / kNvAppendTokens; };
 #pragma unroll
     for (int u = 0; u < kNvAppendUnits; ++u) {
-        const int i = i0 + u * kRows;
-        tok[u] = (first + i) / rows;
-        head[u] = first + i - tok[u] * rows;
-        if (i >= count) continue;
-        const bool is_v = head[u] >= a.heads;
-        const int h = is_v ? head[u] - a.heads : head[u];
-        const long long at = is_v ? (token0 + tok[u]) * a.v_token + h * a.v_head
-                                  : (token0 + tok[u]) * a.k_token + h * a.k_head;
+        const int head = head_of(u);
+        if (u >= a.units || t >= nt || head >= 2 * a.heads) continue;
+        const bool is_v = head >= a.heads;
+        const int h = is_v ? head - a.heads : head;
+        const long long at = is_v ? (token0 + t) * a.v_token + h * a.v_head : (token0 + t) * a.k_token + h * a.k_head;
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(is_v ? a.v : a.k) + at) + 2 * g;
         v[u][0] = __ldg(src);
         v[u][1] = __ldg(src + 1);
     }
-    for (int t = threadIdx.x; t < nt; t += kNvAppendThreads) {
-        const long long pos = a.pos64 ? __ldg(static_cast<const long long*>(a.positions) + token0 + t)
-                                      : (long long)__ldg(static_cast<const int32_t*>(a.positions) + token0 + t);
+    if (const int i = threadIdx.x; i < nt) {
+        const long long pos = a.pos64 ? __ldg(static_cast<const long long*>(a.positions) + token0 + i)
+                                      : (long long)__ldg(static_cast<const int32_t*>(a.positions) + token0 + i);
         bool pad;
         long long page;
         int slot;
-        const bool ok = find_slot(a.slot, token0 + t, pos, pad, page, slot);
-        page_of[t] = ok ? page : -1;
-        slot_of[t] = slot;
+        const bool ok = find_slot(a.slot, token0 + i, pos, pad, page, slot);
+        page_of[i] = ok ? page : -1;
+        slot_of[i] = slot;
     }
     __syncthreads();
+    if (t >= nt || page_of[t] < 0) return;
+    const long long page = page_of[t];
+    const int slot = slot_of[t];
 #pragma unroll
     for (int u = 0; u < kNvAppendUnits; ++u) {
-        if (i0 + u * kRows >= count) continue;
-        const long long page = page_of[tok[u]];
-        if (page < 0) continue;
-        const int slot = slot_of[tok[u]];
-        const bool is_v = head[u] >= a.heads;
+        const int head = head_of(u);
+        if (u >= a.units || head >= 2 * a.heads) continue;
+        const bool is_v = head >= a.heads;
         const NvCache& c = is_v ? a.vc : a.kc;
-        const int h = is_v ? head[u] - a.heads : head[u];
+        const int h = is_v ? head - a.heads : head;
         uint32_t scale;
         const uint2 codes = quantise16<FP16>(v[u], c.scale, scale);
         *reinterpret_cast<uint2*>(c.codes + page * c.page + slot * c.slot + h * c.head + g * 8) = codes;
@@ -173,9 +171,9 @@ __device__ __forceinline__ int blocks_there(const NvReadArgs& a, int b)
     return min(blocks_of(__ldg(a.kv_lens + b)), a.width);
 }
 
-// The pages of all requests, each in strips (a head's keys, a head's values), in
-// order, cut into one contiguous range per CTA.  A thread turns eight values,
-// four bytes of codes, into sixteen bytes.
+// The pages of all requests, each in strips (a head's keys and values), in order,
+// cut into one contiguous range per CTA.  A thread turns eight values, four bytes
+// of codes, into sixteen bytes, several rows at a time.
 template <int D, bool FP16>
 __global__ void __launch_bounds__(kReadThreads) nvfp4_read_kernel(const NvReadArgs a)
 {
@@ -183,7 +181,7 @@ __global__ void __launch_bounds__(kReadThreads) nvfp4_read_kernel(const NvReadAr
     __shared__ long long first_left[2];    // strip within the block, strips of the range
     allow_dependent_launch();
     grid_dependency_wait();
-    const int strips = 2 * a.heads;
+    const int strips = a.heads;
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
         long long total = 0;
@@ -221,44 +219,49 @@ __global__ void __launch_bounds__(kReadThreads) nvfp4_read_kernel(const NvReadAr
     if (left == 0) return;
     int b = start[0], j = start[1], strip = (int)first_left[0];
     const int unit = threadIdx.x % (D / 8), row0 = threadIdx.x / (D / 8);
-    constexpr int kStep = kReadThreads / (D / 8);
+    constexpr int kStep = kReadThreads / (D / 8), kUnits = kBlockKeys / kStep;
     for (; left > 0; --left) {
-        const int len = __ldg(a.kv_lens + b);
+        const int rows = min(__ldg(a.kv_lens + b) - j * kBlockKeys, kBlockKeys);
         const long long page = __ldg(a.block_table + b * a.bt_stride + j);
         const long long to = __ldg(a.out_table + b * a.ot_stride + j);
         if (page < 0 || page >= a.num_pages || to < 0 || to >= a.out_pages) {
             if (threadIdx.x == 0) atomicOr(a.status, kStatusBadBlock);
         } else {
-            const bool is_v = strip >= a.heads;
-            const int h = is_v ? strip - a.heads : strip;
-            const NvCache& c = is_v ? a.vc : a.kc;
-            const int rows = min(len - j * kBlockKeys, kBlockKeys);
-            const uint8_t* codes = c.codes + page * c.page + h * c.head + unit * 4;
-            const uint8_t* scales = c.scales + page * c.s_page + h * c.s_head + unit / 2;
-            uint16_t* out = static_cast<uint16_t*>(is_v ? a.v_out : a.k_out) +
-                            (is_v ? to * a.v_page + h * a.v_head : to * a.k_page + h * a.k_head) + unit * 8;
-            const long long slot = is_v ? a.v_slot : a.k_slot;
-            uint32_t w[kBlockKeys / kStep], s[kBlockKeys / kStep];
+            const long long slots[2] = {a.k_slot, a.v_slot};
+            uint16_t* const out[2] = {static_cast<uint16_t*>(a.k_out) + to * a.k_page + strip * a.k_head + unit * 8,
+                                      static_cast<uint16_t*>(a.v_out) + to * a.v_page + strip * a.v_head + unit * 8};
+            uint32_t w[2][kUnits], s[2][kUnits];
 #pragma unroll
-            for (int i = 0; i < kBlockKeys / kStep; ++i) {
-                const int r = row0 + i * kStep;
-                if (r >= rows) continue;
-                w[i] = __ldg(reinterpret_cast<const uint32_t*>(codes + r * c.slot));
-                s[i] = __ldg(scales + r * c.s_slot);
+            for (int x = 0; x < 2; ++x) {
+                const NvCache& c = x ? a.vc : a.kc;
+                const uint8_t* codes = c.codes + page * c.page + strip * c.head + unit * 4;
+                const uint8_t* scales = c.scales + page * c.s_page + strip * c.s_head + unit / 2;
+#pragma unroll
+                for (int i = 0; i < kUnits; ++i) {
+                    const int r = row0 + i * kStep;
+                    if (r >= rows) continue;
+                    w[x][i] = __ldg(reinterpret_cast<const uint32_t*>(codes + r * c.slot));
+                    s[x][i] = __ldg(scales + r * c.s_slot);
+                }
             }
 #pragma unroll
-            for (int i = 0; i < kBlockKeys / kStep; ++i) {
-                const int r = row0 + i * kStep;
-                if (r >= rows) continue;
-                uint32_t x[4], y[4];
-                e2m1x8_to_f16x2x4(w[i], x);
-                const uint32_t sc = e4m3_to_f16x2_dup(s[i]);
+            for (int x = 0; x < 2; ++x) {
+                const float g = x ? a.vc.scale : a.kc.scale;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 f = unpack16<true>(mul_f16x2(x[e], sc));
-                    y[e] = pack16<FP16>(f.x * c.scale, f.y * c.scale);
+                for (int i = 0; i < kUnits; ++i) {
+                    const int r = row0 + i * kStep;
+                    if (r >= rows) continue;
+                    uint32_t v[4], y[4];
+                    e2m1x8_to_f16x2x4(w[x][i], v);
+                    const uint32_t sc = e4m3_to_f16x2_dup(s[x][i]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = unpack16<true>(mul_f16x2(v[e], sc));
+                        y[e] = pack16<FP16>(f.x * g, f.y * g);
+                    }
+                    uint4* to_row = reinterpret_cast<uint4*>(out[x] + r * slots[x]);
+                    __stcs(to_row, make_uint4(y[0], y[1], y[2], y[3]));    // (written once, four fifths of the traffic)
                 }
-                *reinterpret_cast<uint4*>(out + r * slot) = make_uint4(y[0], y[1], y[2], y[3]);
             }
         }
         if (++strip == strips) {
@@ -277,8 +280,9 @@ __global__ void __launch_bounds__(kReadThreads) nvfp4_read_kernel(const NvReadAr
 
 cudaError_t launch_nvfp4_append(const NvAppendArgs& a, cudaStream_t stream)
 {
-    const long long rows = 2LL * a.tokens * a.heads;
-    const dim3 grid((unsigned)((rows + a.rows_per_cta - 1) / a.rows_per_cta));
+    const int heads_per_cta = a.units * (kNvAppendThreads / (a.dim / kNvGroup) / kNvAppendTokens);
+    const dim3 grid((unsigned)((a.tokens + kNvAppendTokens - 1) / kNvAppendTokens),
+                    (unsigned)((2 * a.heads + heads_per_cta - 1) / heads_per_cta));
     if (a.dim == 128)
         return a.fp16 ? launch_dependent(nvfp4_append_kernel<128, true>, grid, kNvAppendThreads, 0, stream, a)
                       : launch_dependent(nvfp4_append_kernel<128, false>, grid, kNvAppendThreads, 0, stream, a);

@@ -22,12 +22,12 @@ struct NvAppendArgs {
     int tokens;
     int heads;
     int dim;
-    int rows_per_cta;              // of the tokens' 2 * heads rows each
+    int units;                     // groups of a thread, at most kNvAppendUnits
 };
 
 constexpr int kNvAppendThreads = 256;
-constexpr int kNvAppendUnits = 4;      // groups of a thread
-constexpr int kNvAppendMaxTokens = 128; // of a CTA, in part
+constexpr int kNvAppendUnits = 4;
+constexpr int kNvAppendTokens = 16;    // of a CTA
 
 struct NvReadArgs {
     NvCache kc, vc;
