@@ -57,25 +57,68 @@ __device__ __forceinline__ float e4m3_value(uint32_t code)
     return __half2float(__ushort_as_half((unsigned short)(h & 0xffffu)));
 }
 
-// Two values to a byte of codes, the first in the low nibble.
-__device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi)
+// Eight values to eight codes, four bytes, the first in the lowest nibble.
+__device__ __forceinline__ uint32_t e2m1x8_of(const float (&x)[8])
 {
     uint32_t r;
-    asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}"
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
         : "=r"(r)
-        : "f"(hi), "f"(lo));
+        : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
     return r;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Eight values' codes under the scale d, rc = 1 / d.
+template <bool FP16>
+__device__ __forceinline__ uint32_t codes_of(const uint32_t (&w)[4], float d, float rc)
+{
+    const uint64_t nd = pack2(-d, -d), rr = pack2(rc, rc);
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack16<FP16>(w[i]);
+        const uint64_t v = pack2(f.x, f.y), p = mul2(v, rr), q = fma2(fma2(p, nd, v), rr, p);
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(x[2 * i]), "=f"(x[2 * i + 1]) : "l"(q));
+    }
+    return e2m1x8_of(x);
+}
+
+// The same past the largest scale, where a quotient might be infinite.
+template <bool FP16>
+__device__ __noinline__ uint32_t codes_beyond(uint32_t a, uint32_t b, uint32_t c, uint32_t e, float d, float rc)
+{
+    const uint32_t w[4] = {a, b, c, e};
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack16<FP16>(w[i]);
+        const float u = fminf(fmaxf(f.x, -8.0f * d), 8.0f * d), v = fminf(fmaxf(f.y, -8.0f * d), 8.0f * d);
+        x[2 * i] = fmaf(fmaf(-u * rc, d, u), rc, u * rc);
+        x[2 * i + 1] = fmaf(fmaf(-v * rc, d, v), rc, v * rc);
+    }
+    return e2m1x8_of(x);
 }
 
 // Sixteen values to their codes and scale.
 template <bool FP16>
 __device__ __forceinline__ uint2 quantise16(const uint4 (&v)[2], float g, uint32_t& scale)
 {
-    const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+    const uint32_t w[2][4] = {{v[0].x, v[0].y, v[0].z, v[0].w}, {v[1].x, v[1].y, v[1].z, v[1].w}};
     // magnitudes compare like their bits, infinities and NaN above all others
     uint32_t top2 = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top2 = __vmaxu2(top2, w[i] & 0x7fff7fffu);
+    for (int i = 0; i < 8; ++i) top2 = __vmaxu2(top2, w[i / 4][i % 4] & 0x7fff7fffu);
     const uint32_t top = max(top2 & 0xffffu, top2 >> 16);
     if (top >= (FP16 ? 0x7c00u : 0x7f80u)) {
         scale = kNanScale;
@@ -85,22 +128,11 @@ __device__ __forceinline__ uint2 quantise16(const uint4 (&v)[2], float g, uint32
     scale = e4m3_of(__fdiv_rn(amax, 6.0f * g));
     const float d = e4m3_value(scale) * g;
     if (d == 0.0f) return make_uint2(0u, 0u);
-    const float rc = __fdiv_rn(1.0f, d);
-    const float cut = 8.0f * d;
-    const bool beyond = amax > cut;          // past the largest scale: a quotient might be infinite
-    uint32_t b[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float2 x = unpack16<FP16>(w[i]);
-        if (beyond) {
-            x.x = fminf(fmaxf(x.x, -cut), cut);
-            x.y = fminf(fmaxf(x.y, -cut), cut);
-        }
-        const float p = x.x * rc, q = x.y * rc;
-        b[i] = e2m1_pair(fmaf(fmaf(-p, d, x.x), rc, p), fmaf(fmaf(-q, d, x.y), rc, q));
-    }
-    return make_uint2(b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24),
-                      b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24));
+    const float rc = __frcp_rn(d);
+    if (amax > 8.0f * d)
+        return make_uint2(codes_beyond<FP16>(w[0][0], w[0][1], w[0][2], w[0][3], d, rc),
+                          codes_beyond<FP16>(w[1][0], w[1][1], w[1][2], w[1][3], d, rc));
+    return make_uint2(codes_of<FP16>(w[0], d, rc), codes_of<FP16>(w[1], d, rc));
 }
 
 // A thread takes a group of sixteen, eight (four) threads a row; a CTA sixteen
@@ -220,6 +252,9 @@ __global__ void __launch_bounds__(kReadThreads) nvfp4_read_kernel(const NvReadAr
     int b = start[0], j = start[1], strip = (int)first_left[0];
     const int unit = threadIdx.x % (D / 8), row0 = threadIdx.x / (D / 8);
     constexpr int kStep = kReadThreads / (D / 8), kUnits = kBlockKeys / kStep;
+    // the caches' scales, where fp16 holds them
+    const bool plain[2] = {a.kc.scale >= 0x1p-14f && a.kc.scale <= 0x1p15f, a.vc.scale >= 0x1p-14f && a.vc.scale <= 0x1p15f};
+    const uint32_t g16[2] = {pack16<true>(a.kc.scale, a.kc.scale), pack16<true>(a.vc.scale, a.vc.scale)};
     for (; left > 0; --left) {
         const int rows = min(__ldg(a.kv_lens + b) - j * kBlockKeys, kBlockKeys);
         const long long page = __ldg(a.block_table + b * a.bt_stride + j);
@@ -254,10 +289,18 @@ __global__ void __launch_bounds__(kReadThreads) nvfp4_read_kernel(const NvReadAr
                     uint32_t v[4], y[4];
                     e2m1x8_to_f16x2x4(w[x][i], v);
                     const uint32_t sc = e4m3_to_f16x2_dup(s[x][i]);
+                    // (in fp16 a product with a power of two rounds as one in fp32 would)
+                    if (FP16 && plain[x]) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 f = unpack16<true>(mul_f16x2(v[e], sc));
-                        y[e] = pack16<FP16>(f.x * g, f.y * g);
+                        for (int e = 0; e < 4; ++e) y[e] = mul_f16x2(mul_f16x2(v[e], sc), g16[x]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 f = unpack16<true>(mul_f16x2(v[e], sc));
+                            float lo, hi;
+                            asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(mul2(pack2(f.x, f.y), pack2(g, g))));
+                            y[e] = pack16<FP16>(lo, hi);
+                        }
                     }
                     uint4* to_row = reinterpret_cast<uint4*>(out[x] + r * slots[x]);
                     __stcs(to_row, make_uint4(y[0], y[1], y[2], y[3]));    // (written once, four fifths of the traffic)
