@@ -88,7 +88,8 @@ struct Joined {
 // the order of their numbers, joined through shared memory.  Bound by the
 // latency of dependent loads: the records of the owner and of the CTAs after
 // it, then maxima, sums and values at once (one pass with a running maximum).
-template <int D, bool FP16>
+// (P16: P was fp16, whatever the output's type.)
+template <int D, bool FP16, bool P16>
 __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const AttnArgs a, int num_ctas)
 {
     __shared__ float part[kJoinWarps][18][32];
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const A
         const int qhead = head * G + g;
         *reinterpret_cast<uint2*>(out + token * a.out_token + qhead * a.out_head + 4 * at) =
             make_uint2(pack16<FP16>(x.acc[0] * inv, x.acc[1] * inv), pack16<FP16>(x.acc[2] * inv, x.acc[3] * inv));
-        if (cols + at == 0 && a.lse != nullptr) a.lse[token * a.kv_heads * G + qhead] = x.log_sum(a.scale, PScale<FP16>::kInverse);
+        if (cols + at == 0 && a.lse != nullptr) a.lse[token * a.kv_heads * G + qhead] = x.log_sum(a.scale, PScale<P16>::kInverse);
         return;
     }
     // groups of 32 rows, first half 0's, then half 1's; the pieces' parts
@@ -174,21 +175,22 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const A
     uint4* dst = reinterpret_cast<uint4*>(out + token * a.out_token + qhead * a.out_head);
     dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
     dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    if (cols == 0 && a.lse != nullptr) a.lse[token * a.kv_heads * G + qhead] = x.log_sum(a.scale, PScale<FP16>::kInverse);
+    if (cols == 0 && a.lse != nullptr) a.lse[token * a.kv_heads * G + qhead] = x.log_sum(a.scale, PScale<P16>::kInverse);
 }
 
-template <int D, bool FP16>
+template <int D, bool FP16, bool P16>
 cudaError_t launch_join(const AttnArgs& a, int num_ctas, cudaStream_t stream)
 {
-    return launch_dependent(attention_join_kernel<D, FP16>, dim3((unsigned)num_ctas, D / 16),
+    return launch_dependent(attention_join_kernel<D, FP16, P16>, dim3((unsigned)num_ctas, D / 16),
                             kJoinWarps * 32, 0, stream, a, num_ctas);
 }
 
-cudaError_t join(int head_dim, bool fp16, const AttnArgs& a, int num_ctas, cudaStream_t stream)
+template <int D>
+cudaError_t join(bool fp16, bool p16, const AttnArgs& a, int num_ctas, cudaStream_t stream)
 {
-    if (head_dim == 128)
-        return fp16 ? launch_join<128, true>(a, num_ctas, stream) : launch_join<128, false>(a, num_ctas, stream);
-    return fp16 ? launch_join<64, true>(a, num_ctas, stream) : launch_join<64, false>(a, num_ctas, stream);
+    return fp16 ? launch_join<D, true, true>(a, num_ctas, stream)
+           : p16 ? launch_join<D, false, true>(a, num_ctas, stream)
+                 : launch_join<D, false, false>(a, num_ctas, stream);
 }
 
 }  // namespace
@@ -200,7 +202,8 @@ cudaError_t launch_paged_attention(int head_dim, bool fp16, bool select, const C
     const cudaError_t e = head_dim == 128
                               ? launch_attention_d128(fp16, select, qmap, kmap, vmap, a, num_ctas, stream)
                               : launch_attention_d64(fp16, select, qmap, kmap, vmap, a, num_ctas, stream);
-    return e != cudaSuccess ? e : join(head_dim, fp16, a, num_ctas, stream);
+    if (e != cudaSuccess) return e;
+    return head_dim == 128 ? join<128>(fp16, fp16, a, num_ctas, stream) : join<64>(fp16, fp16, a, num_ctas, stream);
 }
 
 cudaError_t launch_paged_attention_nvfp4(int head_dim, bool fp16, bool select, const CUtensorMap& qmap,
@@ -208,7 +211,8 @@ cudaError_t launch_paged_attention_nvfp4(int head_dim, bool fp16, bool select, c
 {
     const cudaError_t e = head_dim == 128 ? launch_attention_nvfp4_d128(fp16, select, qmap, a, num_ctas, stream)
                                           : launch_attention_nvfp4_d64(fp16, select, qmap, a, num_ctas, stream);
-    return e != cudaSuccess ? e : join(head_dim, fp16, a, num_ctas, stream);
+    if (e != cudaSuccess) return e;
+    return head_dim == 128 ? join<128>(fp16, true, a, num_ctas, stream) : join<64>(fp16, true, a, num_ctas, stream);
 }
 
 }  // namespace pml

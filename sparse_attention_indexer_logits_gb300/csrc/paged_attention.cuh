@@ -81,7 +81,6 @@ constexpr int kThreads = 384;      // three warpgroups: softmax, softmax, MMA an
 // gives some back and the softmax groups, which hold a row of S, take them
 // (2 * 208 + 88 = 3 * 168).
 constexpr int kLaunchRegs = 168, kHighRegs = 208, kLowRegs = 88;
-constexpr int kFp4HighRegs = 200, kFp4LowRegs = 104;    // caches in 4 bits: the copying warps hold a tile's codes
 // (a scheduler serves warps w, w + 4, w + 8: the issuer, which polls, is not
 // with the warps that hold the first 32 rows, all the rows of a small call)
 constexpr int kSoftmaxWarps = 8;
@@ -181,24 +180,30 @@ __device__ __forceinline__ long long partial_at(int cta, int slot, int col, int 
     return ((((long long)cta * 2 + slot) * (D / 4) + col) * kAttnSlotRows + row) * 4;
 }
 
-template <int D>
+template <int D, bool FP4 = false>
 struct Cfg {
     static constexpr int kBlocks = D / 64;                     // 128-byte column blocks
     static constexpr int kBlockBytes = 128 * 128;              // 128 rows of 128 bytes
     static constexpr int kStageBytes = kBlocks * kBlockBytes;  // a K or V tile
     static constexpr int kHalfBytes = kBlocks * kBlockBytes;   // a Q half
-    static constexpr int kStages = D == 128 ? 5 : 11;
+    static constexpr int kStages = FP4 ? (D == 128 ? 4 : 9) : D == 128 ? 5 : 11;
+    // 4 bits: half a tile's codes and scales, kRawTiles of them for each of two warps
+    static constexpr int kRawTiles = 3;
+    static constexpr int kRawBytes = 64 * (D / 2 + D / kNvGroup);
     static constexpr int kQ = 0;
     static constexpr int kRing = kQ + 2 * kHalfBytes;
-    static constexpr int kStats = kRing + kStages * kStageBytes;      // float2 [2][128]
-    static constexpr int kBars = kStats + 2 * 128 * 8;
+    static constexpr int kRaw = kRing + kStages * kStageBytes;
+    static constexpr int kStats = kRaw + (FP4 ? 2 * kRawTiles * kRawBytes : 0);    // float2 [2][128]
+    static constexpr int kFactors = kStats + 2 * 128 * 8;             // 4 bits: float [2][128]
+    static constexpr int kBars = kFactors + (FP4 ? 2 * 128 * 4 : 0);
     // barriers: full, empty per stage; q full, q empty per half; s full, pv done, group
     // sync per half; o empty, alt sync; item full, item empty; the issuer's
-    // last commit
-    static constexpr int kNumBars = 2 * kStages + 4 + 6 + 2 + 2 * kItemSlots + 1;
+    // last commit; 4 bits: q turned per half
+    static constexpr int kNumBars = 2 * kStages + 4 + 6 + 2 + 2 * kItemSlots + 1 + (FP4 ? 2 : 0);
     static constexpr int kItems = (kBars + kNumBars * 8 + 15) / 16 * 16;
     static constexpr int kMisc = kItems + kItemSlots * kItemInts * 4;
     static constexpr int kTotal = kMisc + 192;
+    static_assert(kTotal <= 232448, "shared memory of a CTA");
 };
 
 constexpr uint32_t kColS = 0;      // S_h at 128 h; P_h over its first 64 columns
@@ -226,6 +231,15 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
         : "memory");
+}
+
+// N bytes, or zeros (bytes = 0: src is not read).
+template <int N>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, uint32_t bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "n"(N)
+                 : "memory");
 }
 
 // Sixteen bytes, or zeros (bytes = 0: src is not read).
@@ -400,13 +414,17 @@ __device__ __forceinline__ Start find_start(const AttnArgs& a, long long* units,
     return s;
 }
 
-template <int D, bool FP16, bool SEL, bool FP4 = false>
+// FP4: the caches are held in 4 bits.  The two copying warps turn their codes into
+// tiles; both products are in fp16 (FP16), q and the output of another type
+// (OUT16 = false: bf16) or the same.
+template <int D, bool FP16, bool SEL, bool FP4 = false, bool OUT16 = FP16>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap qmap,
                            const __grid_constant__ CUtensorMap kmap,
                            const __grid_constant__ CUtensorMap vmap, const AttnArgs a)
 {
-    using C = Cfg<D>;
+    using C = Cfg<D, FP4>;
+    constexpr bool TURN_Q = FP16 != OUT16;
     constexpr int S = C::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_addr(smem);
@@ -420,7 +438,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t qfull0 = bar + 8u * (2 * S), qempty0 = qfull0 + 16u;   // per Q half
     const uint32_t sfull0 = qempty0 + 16u, pvdone0 = sfull0 + 16u,
                    group0 = pvdone0 + 16u, oempty = group0 + 16u, altbar = oempty + 8u,
-                   itfull0 = altbar + 8u, itempty0 = itfull0 + 8u * kItemSlots, drain = itempty0 + 8u * kItemSlots;
+                   itfull0 = altbar + 8u, itempty0 = itfull0 + 8u * kItemSlots, drain = itempty0 + 8u * kItemSlots,
+                   qready0 = drain + 8u;
     int* items = reinterpret_cast<int*>(smem + C::kItems);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMisc + 4);
@@ -450,6 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int h = 0; h < 2; ++h) {
             mbar_init(qfull0 + 8u * h, 1);
             mbar_init(qempty0 + 8u * h, 1);
+            if (TURN_Q) mbar_init(qready0 + 8u * h, 4);
             mbar_init(sfull0 + 8u * h, 1);
             mbar_init(pvdone0 + 8u * h, 1);
             mbar_init(group0 + 8u * h, 4);
@@ -504,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
 
     if (warp >= kSoftmaxWarps) {
-        regs_dec<FP4 ? kFp4LowRegs : kLowRegs>();
+        regs_dec<kLowRegs>();
     if (loads) {
         // ------------------------------------------------------------ producer
         int b = start.b, head = start.head, tile = start.tile, at = start.at;
@@ -622,31 +642,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---- K and V tiles: K runs `ahead` tiles before V
             const int ahead = alt ? 2 : 1;
             if constexpr (FP4) {
-                // Codes to 16-bit tiles: each of the two warps has half of a
-                // tile's rows.  A lane takes sixteen bytes of a row (eight lanes
-                // side by side the same bytes of eight rows, whose chunks the
-                // swizzle puts into different banks), turns them into 64, and
-                // loads the next tile's as it goes, so that they are there when
-                // the next stage is free.
-                constexpr int CB = D / 2, kRowLanes = CB / 16, kInst = 32 / kRowLanes, kIter = 64 / kInst;
+                // Codes to fp16 tiles: each of the two warps has half of a tile's
+                // rows.  It copies them as they are (cp.async, two tiles ahead)
+                // into its own memory; then a lane takes sixteen bytes of a row
+                // (eight lanes side by side the same bytes of eight rows, whose
+                // chunks the swizzle puts into different banks) and turns them
+                // into 64 in the stage.
+                constexpr int CB = D / 2, SB = D / kNvGroup, kRowLanes = CB / 16, kInst = 32 / kRowLanes,
+                              kIter = 64 / kInst;
                 const int r_in = (lane & 7) + 8 * (lane / (8 * kRowLanes)), chunk = (lane >> 3) % kRowLanes;
                 const int row0 = lead ? 0 : 64;
+                const uint32_t raw0 = base + C::kRaw + (lead ? 0 : C::kRawTiles * C::kRawBytes);
                 const int32_t* table = a.block_table + (long long)req * a.bt_stride;
                 auto checked = [&](int page) {
                     const bool bad = page < 0 || page >= a.num_pages;
                     if (bad) atomicOr(a.status, kStatusBadBlock);
                     return bad ? 0 : page;
                 };
-                // what `fetch` reads
-                const uint8_t *src = nullptr, *ssrc = nullptr;
-                long long step = 0, sstep = 0;         // dense: of kInst rows
-                int row_lo = 0, row_hi = 0;            // dense: the page's rows that are there
-                long long at0 = -1, at1 = -1, sat0 = 0, sat1 = 0;   // selected: places of rows lane and lane + 32
                 // dense: 32 table entries from page `win` on, one a lane; pages of
                 // the one or two tiles whose K is in and V is not
                 const int page_begin = sp.lo / kBlockKeys, page_end = sp.hi > 0 ? (sp.hi - 1) / kBlockKeys + 1 : 0;
                 int win = -1, entry = 0, pg0 = 0, pg1 = 0;
-                // selected: positions of the next tiles, and pages of the nearer ones
+                // selected: positions of this lane's two rows in the next tiles, and
+                // pages of the nearer ones
                 const int32_t* list = SEL ? a.selected + (long long)b * a.sel_stride : nullptr;
                 auto positions = [&](int t) {
                     const int i = (j0 + t) * kAttnTileKeys + row0 + lane;
@@ -665,120 +683,119 @@ __global__ void __launch_bounds__(kThreads, 1)
                     g0 = pages(p0);
                     g1 = pages(p1);
                 }
-                int nk = 0, nv = 0;
-                // The next tile in order, K `ahead` tiles before V; false: none is left.
-                auto pick = [&]() {
-                    if (nv >= n) return false;
-                    const bool is_k = nk < n && nk - nv < ahead;
-                    const NvCache& c = is_k ? a.kc4 : a.vc4;
-                    src = c.codes + head * c.head + chunk * 16;
-                    ssrc = c.scales + head * c.s_head + chunk * 2;
-                    if constexpr (SEL) {
-                        int2 p = vp0, g = vg0;
-                        if (is_k) {
-                            g0.x = checked(g0.x);
-                            g0.y = checked(g0.y);
-                            p = p0;
-                            g = g0;
-                            if (nk == nv) { vp0 = p0; vg0 = g0; }
-                            else { vp1 = p0; vg1 = g0; }
-                            ++nk;
-                            p0 = p1; g0 = g1;
-                            p1 = p2; g1 = pages(p1);
-                            p2 = positions(nk + 2);
-                        } else {
-                            vp0 = vp1; vg0 = vg1;
-                            ++nv;
-                        }
-                        at0 = p.x < 0 ? -1 : g.x * c.page + (p.x & 63) * c.slot;
-                        at1 = p.y < 0 ? -1 : g.y * c.page + (p.y & 63) * c.slot;
-                        sat0 = g.x * c.s_page + (p.x & 63) * c.s_slot;
-                        sat1 = g.y * c.s_page + (p.y & 63) * c.s_slot;
-                    } else {
-                        int page = pg0, tile_at = nv;
-                        if (is_k) {
-                            const int pg = 2 * (j0 + nk) + (lead ? 0 : 1);
-                            if (win < 0 || pg >= win + 32) {
-                                win = pg;
-                                entry = pg + lane >= page_begin && pg + lane < page_end
-                                            ? checked(__ldg(table + pg + lane)) : 0;
+                int nk = 0, nv = 0, put = 0;
+                // Copies the next tile in order, K `ahead` tiles before V; nothing
+                // when none is left.
+                auto copy = [&]() {
+                    if (nv < n) {
+                        const bool is_k = nk < n && nk - nv < ahead;
+                        const NvCache& c = is_k ? a.kc4 : a.vc4;
+                        const uint8_t* src = c.codes + head * c.head + chunk * 16;
+                        const uint8_t* ssrc = c.scales + head * c.s_head;
+                        const uint32_t to = raw0 + put * C::kRawBytes;
+                        if constexpr (SEL) {
+                            int2 p = vp0, g = vg0;
+                            if (is_k) {
+                                p = p0;
+                                g = make_int2(checked(g0.x), checked(g0.y));
+                                if (nk == nv) { vp0 = p; vg0 = g; }
+                                else { vp1 = p; vg1 = g; }
+                                ++nk;
+                                p0 = p1; g0 = g1;
+                                p1 = p2; g1 = pages(p1);
+                                p2 = positions(nk + 2);
+                            } else {
+                                vp0 = vp1; vg0 = vg1;
+                                ++nv;
                             }
-                            page = __shfl_sync(0xffffffffu, entry, pg - win);
-                            if (nk == nv) pg0 = page;
-                            else pg1 = page;
-                            tile_at = nk++;
-                        } else {
-                            pg0 = pg1;
-                            ++nv;
-                        }
-                        const int first_key = (j0 + tile_at) * kAttnTileKeys + row0;
-                        row_lo = sp.lo - first_key;
-                        row_hi = sp.hi - first_key;
-                        src += page * c.page + r_in * c.slot;
-                        ssrc += page * c.s_page + r_in * c.s_slot;
-                        step = kInst * c.slot;
-                        sstep = kInst * c.s_slot;
-                    }
-                    return true;
-                };
-                uint4 codes[kIter];
-                uint32_t scales[kIter];
-                auto fetch = [&](int i) {
-                    codes[i] = make_uint4(0u, 0u, 0u, 0u);
-                    scales[i] = 0;
-                    if constexpr (SEL) {
-                        const int r = (i * kInst + r_in) & 31;
-                        const long long o = __shfl_sync(0xffffffffu, i * kInst < 32 ? at0 : at1, r);
-                        const long long so = __shfl_sync(0xffffffffu, i * kInst < 32 ? sat0 : sat1, r);
-                        if (o >= 0) {
-                            codes[i] = __ldg(reinterpret_cast<const uint4*>(src + o));
-                            scales[i] = __ldg(reinterpret_cast<const uint16_t*>(ssrc + so));
-                        }
-                    } else if (const int r = i * kInst + r_in; r >= row_lo && r < row_hi) {
-                        codes[i] = __ldg(reinterpret_cast<const uint4*>(src + i * step));
-                        scales[i] = __ldg(reinterpret_cast<const uint16_t*>(ssrc + i * sstep));
-                    }
-                };
-                bool more = pick();
-                if (more)
+                            const long long at[2] = {p.x < 0 ? -1 : g.x * c.page + (p.x & 63) * c.slot,
+                                                     p.y < 0 ? -1 : g.y * c.page + (p.y & 63) * c.slot};
 #pragma unroll
-                    for (int i = 0; i < kIter; ++i) fetch(i);
+                            for (int i = 0; i < kIter; ++i) {
+                                const long long o = __shfl_sync(0xffffffffu, at[i * kInst / 32], (i * kInst + r_in) & 31);
+                                cp_async16(to + (i * kInst + r_in) * CB + chunk * 16, src + max(o, 0ll), o < 0 ? 0u : 16u);
+                            }
+                            cp_async_small<SB>(to + 64 * CB + lane * SB, ssrc + g.x * c.s_page + (p.x & 63) * c.s_slot,
+                                               p.x < 0 ? 0u : SB);
+                            cp_async_small<SB>(to + 64 * CB + (lane + 32) * SB, ssrc + g.y * c.s_page + (p.y & 63) * c.s_slot,
+                                               p.y < 0 ? 0u : SB);
+                        } else {
+                            int page = pg0, tile_at = nv;
+                            if (is_k) {
+                                const int pg = 2 * (j0 + nk) + (lead ? 0 : 1);
+                                if (win < 0 || pg >= win + 32) {
+                                    win = pg;
+                                    entry = pg + lane >= page_begin && pg + lane < page_end
+                                                ? checked(__ldg(table + pg + lane)) : 0;
+                                }
+                                page = __shfl_sync(0xffffffffu, entry, pg - win);
+                                if (nk == nv) pg0 = page;
+                                else pg1 = page;
+                                tile_at = nk++;
+                            } else {
+                                pg0 = pg1;
+                                ++nv;
+                            }
+                            // the page's rows that some row of the item may see
+                            const int first_key = (j0 + tile_at) * kAttnTileKeys + row0;
+                            auto there = [&](int r, uint32_t bytes) {
+                                return r >= sp.lo - first_key && r < sp.hi - first_key ? bytes : 0u;
+                            };
+                            src += page * c.page + r_in * c.slot;
+                            ssrc += page * c.s_page + lane * c.s_slot;
+#pragma unroll
+                            for (int i = 0; i < kIter; ++i) {
+                                cp_async16(to + (i * kInst + r_in) * CB + chunk * 16, src, there(i * kInst + r_in, 16u));
+                                src += kInst * c.slot;
+                            }
+                            cp_async_small<SB>(to + 64 * CB + lane * SB, ssrc, there(lane, SB));
+                            cp_async_small<SB>(to + 64 * CB + (lane + 32) * SB, ssrc + 32 * c.s_slot, there(lane + 32, SB));
+                        }
+                        if (++put == C::kRawTiles) put = 0;
+                    }
+                    cp_async_commit();
+                };
 #pragma unroll 1
-                while (more && ok) {
+                for (int i = 0; i < C::kRawTiles - 1; ++i) copy();
+                int got = 0;
+#pragma unroll 1
+                for (int tile_op = 0; tile_op < 2 * n && ok; ++tile_op) {
                     const int st = pos % S;
+                    copy();
+                    cp_async_wait<C::kRawTiles - 1>();
+                    __syncwarp();
                     ok = warp_wait(empty_bar(st), (uint32_t)((pos / S) & 1) ^ 1u, abort_flag, a.status);
                     if (!ok) break;
-                    more = pick();
+                    const uint32_t raw = raw0 + got * C::kRawBytes;
+                    if (++got == C::kRawTiles) got = 0;
                     const uint32_t dst = base + C::kRing + st * C::kStageBytes + (chunk >> 1) * C::kBlockBytes +
                                          (row0 + r_in) * 128;
 #pragma unroll
                     for (int i = 0; i < kIter; ++i) {
-                        const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+                        const int r = i * kInst + r_in;
+                        const uint4 v = ld_shared_v4(raw + r * CB + chunk * 16);
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                         uint32_t m2;
-                        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(m2) : "h"((uint16_t)scales[i]));
+                        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(m2)
+                            : "h"((uint16_t)ld_shared_u16(raw + 64 * CB + r * SB + chunk * 2)));
                         const uint32_t m[2] = {__byte_perm(m2, m2, 0x1010), __byte_perm(m2, m2, 0x3232)};
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             uint32_t x[4];
                             e2m1x8_to_f16x2x4(w[q], x);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                x[e] = mul_f16x2(x[e], m[q >> 1]);
-                                if constexpr (!FP16) {
-                                    const float2 f = unpack16<true>(x[e]);
-                                    x[e] = pack16<false>(f.x, f.y);
-                                }
-                            }
+                            for (int e = 0; e < 4; ++e) x[e] = mul_f16x2(x[e], m[q >> 1]);
                             st_shared_v4(dst + i * kInst * 128 + ((((chunk & 1) * 4 + q) ^ (lane & 7)) << 4), x[0], x[1],
                                          x[2], x[3]);
                         }
-                        if (more) fetch(i);
                     }
                     fence_proxy_async_smem();     // the tensor core reads what this lane has written
-                    __syncwarp();
+                    __syncwarp();                 // (and the codes' place is free)
                     if (lane == 0) mbar_arrive(full_bar(st));
                     ++pos;
                 }
+                cp_async_wait<0>();
+                __syncwarp();
                 handed = pos;
             } else if constexpr (SEL) {
                 const int32_t* list = a.selected + (long long)b * a.sel_stride;
@@ -1027,7 +1044,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool alt = flags & kAlt;
                 const uint32_t q0 = qcount & 1u;             // Q halves of this item
                 for (int i = alt ? 1 : 0; i < 2 && ok; ++i, ++qcount)
-                    ok = wait(qfull0 + 8u * (qcount & 1u), (qcount >> 1) & 1u);
+                    ok = wait((TURN_Q ? qready0 : qfull0) + 8u * (qcount & 1u), (qcount >> 1) & 1u);
                 if (!alt) {
                     // both halves see every tile; written out, since with
                     // these items the tensor core's time is what counts
@@ -1106,7 +1123,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     }
     } else {
-        regs_inc<FP4 ? kFp4HighRegs : kHighRegs>();
+        regs_inc<kHighRegs>();
         // ------------------------------------------------------------ softmax
         const int h = warp >> 2;                 // half
         const int quad = warp & 3;
@@ -1114,7 +1131,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
         const uint32_t t_s = lane_addr + kColS + 128u * h;
         const uint32_t t_o = lane_addr + kColO + 128u * h;
-        const float c = a.scale_log2;
+        float c = a.scale_log2;              // of S (4 bits: the row's own)
+        float factor = 1.0f;
+        float* const factors = reinterpret_cast<float*>(smem + C::kFactors);
         const int G = a.group;
         const int row_tok = row / G;
         const int row_head = row - row_tok * G;
@@ -1152,6 +1171,44 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             const int tiles_here = alt ? (n + 1 - h) / 2 : n;
+            const uint32_t q_slot = (qcount + (alt ? 0u : (uint32_t)h)) & 1u;
+            auto take_factor = [&]() {
+                factor = factors[q_slot * 128 + row];
+                c = fmaxf(a.scale_log2 * factor, 1.2e-38f);      // (times -inf it stays -inf)
+            };
+            if constexpr (TURN_Q) {
+                // Q's rows to fp16, each times a power of two that makes its
+                // largest element 1 to 2: bf16's 8 bits stay for those down to
+                // 2^-17 of it.  A half's group does it, half 0's where both
+                // halves hold the same rows.
+                if (!alt || h == 0) {
+                    ok = warp_wait(qfull0 + 8u * q_slot, ((qcount + (alt ? 0u : (uint32_t)h)) >> 1) & 1u, abort_flag,
+                                   a.status);
+                    if (!ok) break;
+                    uint8_t* qrow = smem + C::kQ + q_slot * C::kHalfBytes + row * 128;
+                    uint4 w[8 * C::kBlocks];
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int e = 0; e < 8 * C::kBlocks; ++e) {
+                        w[e] = *reinterpret_cast<const uint4*>(qrow + (e >> 3) * C::kBlockBytes + (((e + row) & 7) << 4));
+                        constexpr uint32_t k = 0x7fff7fffu;
+                        top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[e].x & k, w[e].y & k), __vmaxu2(w[e].z & k, w[e].w & k)));
+                    }
+                    top = min(max(max(top & 0xffffu, top >> 16) >> 7, 64u), 253u);
+                    const float inv = __uint_as_float((254u - top) << 23);
+                    auto half = [&](uint32_t v) {
+                        return pack16<true>(__uint_as_float(v << 16) * inv, __uint_as_float(v & 0xffff0000u) * inv);
+                    };
+#pragma unroll
+                    for (int e = 0; e < 8 * C::kBlocks; ++e)
+                        *reinterpret_cast<uint4*>(qrow + (e >> 3) * C::kBlockBytes + (((e + row) & 7) << 4)) =
+                            make_uint4(half(w[e].x), half(w[e].y), half(w[e].z), half(w[e].w));
+                    factors[q_slot * 128 + row] = __uint_as_float(top << 23);
+                    fence_proxy_async_smem();     // the tensor core reads it
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(qready0 + 8u * q_slot);
+                }
+            }
             float m = -INFINITY, l = 0.0f;
             int v_place = 0;                     // of the last tile's V
             for (int i = 0; i < tiles_here && ok; ++i) {
@@ -1173,6 +1230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 ++scount;
                 tc_fence_after();
+                if (TURN_Q && i == 0) take_factor();
                 // the scores' commit covers every product issued before it:
                 // this tile's K has been read, and the V and P of this half's
                 // last tile (of both halves' where they share it, since half 1
@@ -1408,6 +1466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 ++alt_phase;
                 tc_fence_after();
+                if (TURN_Q && tiles_here == 0) take_factor();
                 const float2 s0 = stats[row];
                 const float2 s1 = n > 1 ? stats[128 + row] : make_float2(-INFINITY, 0.0f);
                 top = fmaxf(s0.x, s1.x);
@@ -1451,7 +1510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint32_t w[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            w[e] = pack16<FP16>(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+                            w[e] = pack16<OUT16>(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
                         uint4* dst = reinterpret_cast<uint4*>(orow + d);
                         dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
                         dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
@@ -1463,10 +1522,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (valid && (h == 0 || !alt)) {
-                    if (!whole) a.stats[ws_row] = make_float2(top, sum);
+                    if (!whole) a.stats[ws_row] = make_float2(TURN_Q ? top * factor : top, sum);
                     else if (a.lse != nullptr)
                         a.lse[(long long)token * a.kv_heads * G + qhead] =
-                            sum == 0.0f ? -INFINITY : top * a.scale + logf(sum * PScale<FP16>::kInverse);
+                            sum == 0.0f ? -INFINITY
+                                        : (TURN_Q ? top * factor : top) * a.scale + logf(sum * PScale<FP16>::kInverse);
                 }
             }
             tc_fence_before();
@@ -1487,29 +1547,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D, bool FP16, bool SEL, bool FP4 = false>
+template <int D, bool FP16, bool SEL, bool FP4 = false, bool OUT16 = FP16>
 cudaError_t launch_kernel(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
                           const AttnArgs& a, int num_ctas, cudaStream_t stream)
 {
-    auto kernel = paged_attention_kernel<D, FP16, SEL, FP4>;
+    auto kernel = paged_attention_kernel<D, FP16, SEL, FP4, OUT16>;
     static int configured_device = -1;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (configured_device != dev) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kTotal);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, FP4>::kTotal);
         if (e != cudaSuccess) return e;
         // the warpgroups' shares must fit the block's allocation, else the
         // softmax groups' setmaxnreg.inc would wait forever
         cudaFuncAttributes fa;
         e = cudaFuncGetAttributes(&fa, kernel);
         if (e != cudaSuccess) return e;
-        constexpr int high = FP4 ? kFp4HighRegs : kHighRegs, low = FP4 ? kFp4LowRegs : kLowRegs;
-        if (fa.numRegs != kLaunchRegs || 2 * high + low > 3 * kLaunchRegs)
+        if (fa.numRegs != kLaunchRegs || 2 * kHighRegs + kLowRegs > 3 * kLaunchRegs)
             return cudaErrorInvalidConfiguration;
         configured_device = dev;
     }
-    return launch_dependent(kernel, dim3((unsigned)num_ctas), kThreads, Cfg<D>::kTotal, stream, qmap, kmap,
+    return launch_dependent(kernel, dim3((unsigned)num_ctas), kThreads, Cfg<D, FP4>::kTotal, stream, qmap, kmap,
                             vmap, a);
 }
 

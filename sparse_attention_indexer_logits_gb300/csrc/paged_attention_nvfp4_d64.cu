@@ -9,8 +9,8 @@ cudaError_t launch_attention_nvfp4_d64(bool fp16, bool select, const CUtensorMap
     if (fp16)
         return select ? attn::launch_kernel<64, true, true, true>(qmap, qmap, qmap, a, num_ctas, stream)
                       : attn::launch_kernel<64, true, false, true>(qmap, qmap, qmap, a, num_ctas, stream);
-    return select ? attn::launch_kernel<64, false, true, true>(qmap, qmap, qmap, a, num_ctas, stream)
-                  : attn::launch_kernel<64, false, false, true>(qmap, qmap, qmap, a, num_ctas, stream);
+    return select ? attn::launch_kernel<64, true, true, true, false>(qmap, qmap, qmap, a, num_ctas, stream)
+                  : attn::launch_kernel<64, true, false, true, false>(qmap, qmap, qmap, a, num_ctas, stream);
 }
 
 }  // namespace pml

@@ -42,11 +42,6 @@ class Problem:
         self.cu = torch.tensor([0] + list(torch.tensor(qn).cumsum(0)), dtype=torch.int32)
         self.kv_lens = torch.tensor(kvn, dtype=torch.int32)
 
-    @property
-    def many(self):
-        """More than sixteen rows of a request to a kv head, on average."""
-        return self.q.dtype == BF and -(-len(self.q) // len(self.qn)) * self.hq // self.hkv > 16
-
     def stale(self):
         """Slots past each request's end hold arbitrary codes under NaN scales."""
         for b, n in enumerate(self.kvn):
@@ -83,12 +78,10 @@ def judge(p, q, k, v, allowed, scale, got, got_lse, where):
     weight is off by that, by the rounding of its exponent (2^-14 where that is
     below 1024, else fp32's half step of it) under either of two references, and
     by the approximate power's 2^-20: `rel` of it.  Numerator and denominator are
-    off by as much; P is rounded once: to fp16, 2^-11 or, for small ones, 2^-32 of
-    the largest weight, and where a request has more than sixteen rows to a kv head
-    to the inputs' type, 2^-8 in bf16; the output once.  The log-sum is off by
-    `rel` and three roundings of its size."""
+    off by as much; P is rounded to fp16 once, 2^-11 or, for small ones, 2^-32 of
+    the largest weight; the output once.  The log-sum is off by `rel` and three
+    roundings of its size."""
     half = torch.finfo(p.dtype).eps / 2
-    half_p = half if p.many else 2.0 ** -11
     want, want_lse, mag = R.attention(q, k, v, allowed, scale)
     qd, kd = q.double(), torch.nan_to_num(k.double(), nan=0.0)
     size = qd.abs() @ kd.abs().T
@@ -102,7 +95,7 @@ def judge(p, q, k, v, allowed, scale, got, got_lse, where):
     assert torch.equal(torch.isfinite(got), fine), where
     seen = torch.where(allowed.any(0)[:, None], torch.nan_to_num(v.double().abs(), nan=0.0), 0.0)
     tiny = 2.0 ** -32 * seen.sum(0) if len(seen) else 0.0
-    bound = mag * (half_p + 2 * rel[:, None]) + tiny + half * want.abs() + torch.finfo(p.dtype).tiny
+    bound = mag * (2.0 ** -11 + 2 * rel[:, None]) + tiny + half * want.abs() + torch.finfo(p.dtype).tiny
     err = (got - want).abs()
     assert (err <= bound)[fine].all(), f"{where}: off by {(err / bound)[fine].max():.3g} bounds"
     none = torch.isneginf(want_lse)
