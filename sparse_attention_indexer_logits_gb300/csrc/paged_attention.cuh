@@ -651,6 +651,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 constexpr int CB = D / 2, SB = D / kNvGroup, kRowLanes = CB / 16, kInst = 32 / kRowLanes,
                               kIter = 64 / kInst;
                 const int r_in = (lane & 7) + 8 * (lane / (8 * kRowLanes)), chunk = (lane >> 3) % kRowLanes;
+                // (where a row's chunk lies: the same chunk of eight rows in eight places)
+                const int place = (D == 128 ? chunk ^ ((lane >> 1) & 3) : chunk ^ ((lane >> 2) & 1)) * 16;
                 const int row0 = lead ? 0 : 64;
                 const uint32_t raw0 = base + C::kRaw + (lead ? 0 : C::kRawTiles * C::kRawBytes);
                 const int32_t* table = a.block_table + (long long)req * a.bt_stride;
@@ -713,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int i = 0; i < kIter; ++i) {
                                 const long long o = __shfl_sync(0xffffffffu, at[i * kInst / 32], (i * kInst + r_in) & 31);
-                                cp_async16(to + (i * kInst + r_in) * CB + chunk * 16, src + max(o, 0ll), o < 0 ? 0u : 16u);
+                                cp_async16(to + (i * kInst + r_in) * CB + place, src + max(o, 0ll), o < 0 ? 0u : 16u);
                             }
                             cp_async_small<SB>(to + 64 * CB + lane * SB, ssrc + g.x * c.s_page + (p.x & 63) * c.s_slot,
                                                p.x < 0 ? 0u : SB);
@@ -745,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ssrc += page * c.s_page + lane * c.s_slot;
 #pragma unroll
                             for (int i = 0; i < kIter; ++i) {
-                                cp_async16(to + (i * kInst + r_in) * CB + chunk * 16, src, there(i * kInst + r_in, 16u));
+                                cp_async16(to + (i * kInst + r_in) * CB + place, src, there(i * kInst + r_in, 16u));
                                 src += kInst * c.slot;
                             }
                             cp_async_small<SB>(to + 64 * CB + lane * SB, ssrc, there(lane, SB));
@@ -770,23 +772,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (++got == C::kRawTiles) got = 0;
                     const uint32_t dst = base + C::kRing + st * C::kStageBytes + (chunk >> 1) * C::kBlockBytes +
                                          (row0 + r_in) * 128;
+                    // (loads before the first store: nothing tells the compiler that
+                    // they lie apart)
 #pragma unroll
-                    for (int i = 0; i < kIter; ++i) {
-                        const int r = i * kInst + r_in;
-                        const uint4 v = ld_shared_v4(raw + r * CB + chunk * 16);
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                        uint32_t m2;
-                        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(m2)
-                            : "h"((uint16_t)ld_shared_u16(raw + 64 * CB + r * SB + chunk * 2)));
-                        const uint32_t m[2] = {__byte_perm(m2, m2, 0x1010), __byte_perm(m2, m2, 0x3232)};
+                    for (int i0 = 0; i0 < kIter; i0 += 4) {
+                        uint4 v[4];
+                        uint32_t s2[4];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t x[4];
-                            e2m1x8_to_f16x2x4(w[q], x);
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = (i0 + i) * kInst + r_in;
+                            v[i] = ld_shared_v4(raw + r * CB + place);
+                            s2[i] = ld_shared_u16(raw + 64 * CB + r * SB + chunk * 2);
+                        }
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) x[e] = mul_f16x2(x[e], m[q >> 1]);
-                            st_shared_v4(dst + i * kInst * 128 + ((((chunk & 1) * 4 + q) ^ (lane & 7)) << 4), x[0], x[1],
-                                         x[2], x[3]);
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                            uint32_t m2;
+                            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(m2) : "h"((uint16_t)s2[i]));
+                            const uint32_t m[2] = {__byte_perm(m2, m2, 0x1010), __byte_perm(m2, m2, 0x3232)};
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                uint32_t x[4];
+                                e2m1x8_to_f16x2x4(w[q], x);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) x[e] = mul_f16x2(x[e], m[q >> 1]);
+                                st_shared_v4(dst + (i0 + i) * kInst * 128 +
+                                                 ((((chunk & 1) * 4 + q) ^ (lane & 7)) << 4), x[0], x[1], x[2], x[3]);
+                            }
                         }
                     }
                     fence_proxy_async_smem();     // the tensor core reads what this lane has written
