@@ -16,12 +16,11 @@ using namespace pml;
 constexpr int kMaxListed = 0x7fffff00; // entries of a list, so that their tiles' ends fit an int
 constexpr int kMaxHeads = 8192;
 constexpr int kMaxScaleExponent = 32;
-// Rows ((token, head) pairs of a kv head) up to which a request's attention is
-// left to warps alone.
-#ifndef NVROWS
-#define NVROWS 16
-#endif
-constexpr int kNvWarpRows = NVROWS;
+// Rows ((token, head) pairs of a kv head) of a request up to which its attention
+// is left to warps alone.  128 request-heads of 8500 keys, heads of 128: 48 rows
+// take 123 us that way and 139 by tiles, 64 rows 157 and 141, 256 rows 568 and
+// 187.
+constexpr int kNvWarpRows = 48;
 
 // Strides of a dimension of one element are never used: any valid one will do.
 int64_t used(int64_t stride, int64_t size, int64_t other) { return size > 1 ? stride : other; }

@@ -98,9 +98,7 @@ cudaError_t launch_join_dim(bool fp16, int tiles, const NvAttnArgs& a, const Pie
 {
     if (tiles == 1)
         return fp16 ? launch_join<D, true, 1>(a, cp, num_ctas, stream) : launch_join<D, false, 1>(a, cp, num_ctas, stream);
-    if (tiles == 2)
-        return fp16 ? launch_join<D, true, 2>(a, cp, num_ctas, stream) : launch_join<D, false, 2>(a, cp, num_ctas, stream);
-    return fp16 ? launch_join<D, true, 4>(a, cp, num_ctas, stream) : launch_join<D, false, 4>(a, cp, num_ctas, stream);
+    return fp16 ? launch_join<D, true, 2>(a, cp, num_ctas, stream) : launch_join<D, false, 2>(a, cp, num_ctas, stream);
 }
 
 // `n` pieces from `at` on, the rows of `slots` of their two slots.
@@ -121,17 +119,13 @@ Pieces take(uint8_t*& at, int64_t n, int slots, int rows, int dim)
 cudaError_t launch_nvfp4_attention(int head_dim, bool fp16, NvAttnArgs& a, int num_ctas, void* workspace,
                                    int64_t workspace_bytes, cudaStream_t stream)
 {
-    // Items of 8, 16 or 32 rows: the larger ones where a request's tokens fill them.
+    // Items of 8 or of 16 rows: the larger ones where a request's tokens fill them.
     const long long per_request = a.selected ? 1 : (a.tokens + a.batch - 1) / a.batch;
-#ifndef R2
-#define R2 16
-#endif
-    const int tiles = per_request * a.group > R2 ? 4 : per_request * a.group > 8 ? 2 : 1, rows = 8 * tiles;
+    const int tiles = per_request * a.group > 8 ? 2 : 1, rows = 8 * tiles;
     a.head_blocks = (a.group + rows - 1) / rows;
     a.block_heads = (a.group + a.head_blocks - 1) / a.head_blocks;
     a.tile_tokens = a.selected || a.group > rows ? 1 : rows / a.group;
-    const int warps = tiles == 1 ? Cfg<128, 1>::kWarps : tiles == 2 ? Cfg<128, 2>::kWarps
-                      : head_dim == 128 ? Cfg<128, 4>::kWarps : Cfg<64, 4>::kWarps;
+    const int warps = tiles == 1 ? Cfg<128, 1>::kWarps : Cfg<128, 2>::kWarps;
     uint8_t* at = static_cast<uint8_t*>(workspace);
     const Pieces wp = take(at, (int64_t)num_ctas * warps, 1, rows, head_dim);
     const Pieces cp = take(at, num_ctas, 2, rows, head_dim);

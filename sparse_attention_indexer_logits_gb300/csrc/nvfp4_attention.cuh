@@ -60,34 +60,23 @@ namespace pml {
 namespace nvattn {
 
 constexpr int kStepKeys = 32;
-// Units of work: a step is one, beginning and ending an item two.
-constexpr int kItemUnits = 2;
+// Units of work: a step is one, beginning and ending an item three.
+constexpr int kItemUnits = 3;
 // P = 2^(c S + off): 2^7 times the weights, so that fp16 keeps the small ones'
 // bits, up to 2^15 before a larger maximum moves `off`.
 constexpr float kPLog2 = 7.0f, kPMost = 15.0f;
 constexpr float kFresh = 1e30f;        // `off` of a row that has seen no key
 
-#ifndef W2
-#define W2 12
-#endif
-#ifndef S2
-#define S2 3
-#endif
-#ifndef W4
-#define W4 8
-#endif
-#ifndef S4
-#define S4 4
-#endif
-// NT: groups of eight rows in an item.  More than one: Q lies in shared memory.
+// NT: groups of eight rows in an item, one or two.  With two, Q lies in shared
+// memory.
 template <int D, int NT>
 struct Cfg {
     static constexpr int kRows = 8 * NT;
-    static constexpr int kWarps = NT == 1 ? 16 : NT == 2 || D == 64 ? W2 : W4;
+    static constexpr int kWarps = NT == 1 ? 16 : 12;       // 128 or 168 registers a thread
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kCode = D / 2, kScale = D / 16;   // bytes of a row
     static constexpr int kStageBytes = 2 * kStepKeys * (kCode + kScale);
-    static constexpr int kStages = D == 128 ? (NT == 4 ? S4 : NT == 2 ? S2 : 3) : 5;
+    static constexpr int kStages = D == 128 ? (NT == 1 ? 3 : 2) : 5;
     static constexpr int kRing = kStages * kStageBytes;    // of a warp
     static constexpr int kQ = kWarps * kRing;
     static constexpr int kQBytes = NT == 1 ? 0 : kRows * D * 2;    // of a warp

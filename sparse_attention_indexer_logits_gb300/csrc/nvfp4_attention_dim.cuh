@@ -21,17 +21,11 @@ template <int D, bool FP16>
 cudaError_t launch_nvfp4_type(int tiles, const NvAttnArgs& a, const nvattn::Pieces& wp, const nvattn::Pieces& cp,
                               int num_ctas, cudaStream_t stream)
 {
-    switch (tiles) {
-    case 1:
-        return a.selected ? launch_nvfp4_one<D, FP16, true, 1>(a, wp, cp, num_ctas, stream)
-                          : launch_nvfp4_one<D, FP16, false, 1>(a, wp, cp, num_ctas, stream);
-    case 2:
-        return a.selected ? launch_nvfp4_one<D, FP16, true, 2>(a, wp, cp, num_ctas, stream)
-                          : launch_nvfp4_one<D, FP16, false, 2>(a, wp, cp, num_ctas, stream);
-    default:
-        return a.selected ? launch_nvfp4_one<D, FP16, true, 4>(a, wp, cp, num_ctas, stream)
-                          : launch_nvfp4_one<D, FP16, false, 4>(a, wp, cp, num_ctas, stream);
-    }
+    if (a.selected)
+        return tiles == 1 ? launch_nvfp4_one<D, FP16, true, 1>(a, wp, cp, num_ctas, stream)
+                          : launch_nvfp4_one<D, FP16, true, 2>(a, wp, cp, num_ctas, stream);
+    return tiles == 1 ? launch_nvfp4_one<D, FP16, false, 1>(a, wp, cp, num_ctas, stream)
+                      : launch_nvfp4_one<D, FP16, false, 2>(a, wp, cp, num_ctas, stream);
 }
 
 template <int D>
