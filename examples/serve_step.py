@@ -13,9 +13,15 @@ Per layer and step the calls are
     pml_paged_attention     (prefill)
     pml_fp8_paged_mqa_logits, pml_topk_logits, pml_sparse_attention   (decode)
 
-and, between steps, pml_pages_extend / _fork / _copy / _free / _compact.
+and, between steps, pml_pages_extend / _fork / _copy / _free / _compact.  With
+the K/V caches held in 4 bits (``kv_bits=4``) the first and the last of a step's
+calls become
 
-    python examples/serve_step.py
+    pml_rope, pml_append_nvfp4              q and k rotated, k and v quantised into their pages
+    pml_read_nvfp4, pml_paged_attention     (prefill: the contexts read back once a layer)
+    pml_sparse_attention_nvfp4              (decode)
+
+    python examples/serve_step.py [4]
 """
 from __future__ import annotations
 
@@ -33,7 +39,7 @@ PAGE = 64
 
 class Server:
     def __init__(self, layers=2, hidden=512, heads=8, kv_heads=2, dim=128, index_heads=16, rot=64, k=256,
-                 rows=16, pages=256, max_context=2048, seed=0):
+                 rows=16, pages=256, max_context=2048, kv_bits=16, seed=0):
         g = torch.Generator(device="cuda").manual_seed(seed)
         rand = lambda *s: torch.randn(s, generator=g, device="cuda", dtype=torch.bfloat16)  # noqa: E731
         self.layers, self.heads, self.kv_heads, self.dim = layers, heads, kv_heads, dim
@@ -43,8 +49,17 @@ class Server:
         self.w_out = [rand(heads * dim, hidden) * (heads * dim) ** -0.5 for _ in range(layers)]
         self.inv_freq = torch.pow(10000.0, -torch.arange(rot // 2, device="cuda", dtype=torch.float64) * 2 / rot)
         # the caches of all layers, and the pool that hands out their pages
-        self.kv = [torch.zeros((layers, pages, PAGE, kv_heads, dim), device="cuda", dtype=torch.bfloat16)
-                   for _ in range(2)]
+        self.kv_bits = kv_bits
+        cache16 = lambda *s: torch.zeros((*s, PAGE, kv_heads, dim), device="cuda", dtype=torch.bfloat16)  # noqa: E731
+        if kv_bits == 4:
+            buffer, *self.kv4 = pml.pml_nvfp4_pages(pages, kv_heads, dim, layers=layers)
+            self.kv = [buffer]
+            # a step's contexts in 16 bits, of one layer at a time
+            width = max_context // PAGE
+            self.kv16 = [cache16(rows * width) for _ in range(2)]
+            self.table16 = torch.arange(rows * width, device="cuda", dtype=torch.int32).view(rows, width)
+        else:
+            self.kv = [cache16(layers, pages) for _ in range(2)]
         self.index = torch.zeros((layers, pages, 8448), device="cuda", dtype=torch.uint8)
         i32 = lambda *s: torch.zeros(s, device="cuda", dtype=torch.int32)  # noqa: E731
         self.refs, self.lens = i32(pages), i32(rows)
@@ -104,8 +119,14 @@ class Server:
             y = x @ self.w_in[layer]
             q, k, v, qi, ki, w = y.split([h * d, kv * d, kv * d, ih * 128, 128, ih], dim=1)
             q, k, v = (t.unflatten(1, (-1, d)) for t in (q, k, v))
-            kc, vc = self.kv[0][layer], self.kv[1][layer]
-            q = pml.pml_rope_append(q, k, v, position, request, self.inv_freq, kc, vc, table)
+            if self.kv_bits == 4:
+                parts = [p[layer] for p in self.kv4]
+                qk = y[:, :(h + kv) * d].unflatten(1, (-1, d))
+                pml.pml_rope(qk, position, self.inv_freq, qk)
+                pml.pml_append_nvfp4(k, v, position, request, *parts, table)
+            else:
+                kc, vc = self.kv[0][layer], self.kv[1][layer]
+                q = pml.pml_rope_append(q, k, v, position, request, self.inv_freq, kc, vc, table)
             qi, w = pml.pml_index_quant_append(qi.unflatten(1, (ih, 128)), ki, w.float().contiguous(), position,
                                                request, self.inv_freq, self.index[layer], table,
                                                weight_scale=(128 * ih) ** -0.5, interleaved=True)
@@ -113,16 +134,23 @@ class Server:
                 logits = self.logits[:len(rows)]
                 pml.pml_fp8_paged_mqa_logits(qi, self.index[layer], w, lens, table, logits, self.max_context, 1)
                 best, _ = pml.pml_topk_logits(logits, lens, 1, self.max_context, self.k)
-                o = pml.pml_sparse_attention(q, kc, vc, table, lens, request, best, workspace=self.workspace)
+                if self.kv_bits == 4:
+                    o = pml.pml_sparse_attention_nvfp4(q, *parts, table, lens, request, best, workspace=self.workspace)
+                else:
+                    o = pml.pml_sparse_attention(q, kc, vc, table, lens, request, best, workspace=self.workspace)
             else:
-                o = pml.pml_paged_attention(q, kc, vc, table, lens, starts, workspace=self.workspace)
+                at_pages = table
+                if self.kv_bits == 4:
+                    kc, vc, at_pages = *self.kv16, self.table16[:len(rows)]
+                    pml.pml_read_nvfp4(*parts, table, lens, kc, vc, at_pages)
+                o = pml.pml_paged_attention(q, kc, vc, at_pages, lens, starts, workspace=self.workspace)
             x = x + o.flatten(1) @ self.w_out[layer]
         return x
 
 
-def main():
+def main(kv_bits=16):
     torch.manual_seed(0)
-    s = Server()
+    s = Server(kv_bits=kv_bits)
     prompts = {0: 700, 1: 130, 2: 1}
     hidden = s.w_in[0].shape[0]
     inputs = {r: torch.randn((n, hidden), device="cuda", dtype=torch.bfloat16) for r, n in prompts.items()}
@@ -151,4 +179,4 @@ def main():
 
 
 if __name__ == "__main__":
-    main()
+    main(int(sys.argv[1]) if len(sys.argv) > 1 else 16)

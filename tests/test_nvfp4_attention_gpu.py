@@ -2,7 +2,9 @@
 the definitions in 64 bits over the values that the caches stand for: single
 tokens, drafts, chunks and mixed batches; head groups from 1 to 300; causal,
 windows, neither; empty requests and rows without a key; layouts; stale slots
-and NaN scales in masked places; large logits; bad pages, requests and lists."""
+and NaN scales in masked places; large logits; bad pages, requests and lists.
+Up to 48 rows ((token, head) pairs of a kv head) to a request on average run
+warp by warp, more by tiles: both ways are tested throughout."""
 import math
 
 import pytest
@@ -158,14 +160,46 @@ def test_mixed_batches(dtype, window, causal):
 
 @pytest.mark.parametrize("k_scale,v_scale", [(0.25, 2.0 ** -6), (2.0 ** 5, 8.0), (2.0 ** -32, 2.0 ** 10)])
 @pytest.mark.parametrize("dtype", [BF, FP])
-def test_scales_of_all_values(k_scale, v_scale, dtype):
+@pytest.mark.parametrize("hq", [6, 42])
+def test_scales_of_all_values(k_scale, v_scale, dtype, hq):
     if dtype == FP and k_scale < 1e-3:
         k_scale = 2.0 ** -8                        # q grows by as much
-    p = Problem([1, 5], [300, 90], 6, 2, 64, dtype, seed=3, k_scale=k_scale, v_scale=v_scale).stale()
+    p = Problem([1, 5], [300, 90], hq, 2, 64, dtype, seed=3, k_scale=k_scale, v_scale=v_scale).stale()
     check(p, *p.run())
 
 
-def test_rows_without_a_key():
+@pytest.mark.parametrize("hq", [4, 64])
+def test_rows_of_very_different_sizes(hq):
+    """bf16 rows of q from 2^-90 to 2^20, a row of zeros and elements far below
+    their row's largest."""
+    p = Problem([1, 2], [300, 170], hq, 1, 128, BF, seed=19).stale()
+    size = torch.exp2(torch.linspace(-90, 3, hq).round())[:, None]
+    p.q = (p.q.float() * size).to(BF)
+    p.q[0, 1] = 0
+    p.q[1, :, ::3] *= 2.0 ** -12
+    p.q[2, -1] *= 2.0 ** 17
+    check(p, *p.run())
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("hq", [3, 6, 20])
+@pytest.mark.parametrize("window", [0, 1, 31, 33, 64, 130])
+@pytest.mark.parametrize("causal", [True, False])
+def test_mixed_batches_of_few_tokens(dim, hq, window, causal):
+    qn, kvn = [1, 0, 6, 3, 1, 5, 0, 4, 2], [900, 50, 6, 700, 1, 64, 0, 421, 97]
+    p = Problem(qn, kvn, hq, 1, dim, FP if hq == 3 else BF, seed=window).stale()
+    check(p, *p.run(causal=causal, window=window), causal=causal, window=window)
+
+
+def test_a_long_chunk_among_single_tokens():
+    """More tiles of tokens to a request than a lane counts by itself, few on average."""
+    qn = [1] * 60 + [200] + [1] * 20
+    kvn = [30 + 7 * i for i in range(60)] + [450] + [90] * 20
+    p = Problem(qn, kvn, 6, 2, 64, BF, seed=17).stale()
+    check(p, *p.run(), requests=list(range(0, 60, 9)) + [60, 61, 80])
+
+
+def test_rows_without_a_key_of_many():
     qn, kvn = [4, 100, 3, 1, 40, 2], [0, 30, 1, 0, 39, -5]
     p = Problem(qn, kvn, 8, 2, 128, BF, seed=1).stale()
     out, lse = p.run()
@@ -174,11 +208,21 @@ def test_rows_without_a_key():
     assert (out[148:] == 0).all() and torch.isneginf(lse[148:]).all()
 
 
-def test_rows_of_no_request_stay():
-    p = Problem([2, 3], [40, 100], 4, 1, 64, BF, seed=2)
+def test_rows_without_a_key():
+    qn, kvn = [4, 5, 3, 1, 6, 2], [0, 2, 1, 0, 4, -5]
+    p = Problem(qn, kvn, 8, 2, 128, BF, seed=1).stale()
+    out, lse = p.run()
+    check(p, out, lse, requests=range(5))
+    assert (out[:4] == 0).all() and torch.isneginf(lse[:4]).all() and (out[4:7] == 0).all()
+    assert (out[19:] == 0).all() and torch.isneginf(lse[19:]).all()
+
+
+@pytest.mark.parametrize("hq", [4, 24])
+def test_rows_of_no_request_stay(hq):
+    p = Problem([2, 3], [40, 100], hq, 1, 64, BF, seed=2)
     p.q = torch.cat([p.q, p.q])
     args = p.device()
-    out, lse = torch.full_like(args[0], 9.0), torch.full((10, 4), 9.0, device="cuda")
+    out, lse = torch.full_like(args[0], 9.0), torch.full((10, hq), 9.0, device="cuda")
     pml.pml_paged_attention_nvfp4(*args, p.cu.cuda(), out, lse=lse)
     check(p, out[:5], lse[:5])
     assert (out[5:] == 9.0).all() and (lse[5:] == 9.0).all()
@@ -209,8 +253,10 @@ def test_one_long_request():
 
 @pytest.mark.parametrize("layout", ["pages", "gaps"])
 @pytest.mark.parametrize("dim", [64, 128])
-def test_layouts_strides_and_given_outputs(layout, dim):
-    p = Problem([5, 60], [70, 200], 6, 3, dim, FP, seed=4).stale()
+@pytest.mark.parametrize("qn", [[5, 60], [4, 3]])
+def test_layouts_strides_and_given_outputs(layout, dim, qn):
+    n = sum(qn)
+    p = Problem(qn, [70, 200], 6, 3, dim, FP, seed=4).stale()
     q, kc, ks, vc, vs, table, lens = p.device()
     if layout == "pages":
         _, *parts = pml.pml_nvfp4_pages(kc.shape[0], 3, dim)
@@ -220,19 +266,19 @@ def test_layouts_strides_and_given_outputs(layout, dim):
     for dst, src in zip(parts, (kc, ks, vc, vs)):
         dst.copy_(src)
     parts[1], parts[3] = parts[1].view(torch.float8_e4m3fn), parts[3]
-    wide = torch.zeros((65, 10, 136), dtype=FP, device="cuda")
+    wide = torch.zeros((n, 10, 136), dtype=FP, device="cuda")
     wide[:, 2:8, :dim] = q
     tw = torch.full((2, table.shape[1] + 3), -7, dtype=torch.int32, device="cuda")
     tw[:, :table.shape[1]] = table
-    out = torch.full((65, 6, 160), 9.0, dtype=FP, device="cuda")[:, :, :dim]
-    lse = torch.empty((65, 6), device="cuda")
+    out = torch.full((n, 6, 160), 9.0, dtype=FP, device="cuda")[:, :, :dim]
+    lse = torch.empty((n, 6), device="cuda")
     ws = pml.pml_attention_workspace(dim)
     ws.fill_(255)
     got = pml.pml_paged_attention_nvfp4(wide[:, 2:8, :dim], *parts, tw[:, :table.shape[1]], lens, p.cu.cuda(), out,
                                         lse=lse, workspace=ws, softmax_scale=0.3)
     assert got is out
     check(p, out, lse, scale=0.3)
-    assert (out.as_strided((65, 6, 160 - dim), out.stride(), dim) == 9.0).all()
+    assert (out.as_strided((n, 6, 160 - dim), out.stride(), dim) == 9.0).all()
 
 
 @pytest.mark.parametrize("dim", [64, 128])
@@ -253,6 +299,22 @@ def test_masked_places_never_reach_a_row(dim, hq):
     check(p, out, lse, window=64)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("hq", [3, 8])
+def test_masked_places_of_few_tokens(dim, hq):
+    p = Problem([6, 4, 1], [70, 200, 100], hq, 1, dim, BF, seed=18).stale()
+    last = dim // 16 - 1
+    for b, pos, group in ((0, 67, 1), (0, 64, 0), (1, 198, last), (1, 150, 2)):
+        p.set_scale("v", b, pos, 0, group, NAN_SCALE)
+    out, lse = p.run()
+    check(p, out, lse)
+    got = out.cpu()
+    assert torch.isnan(got[3:6, :, 16:32]).all() and torch.isfinite(got[:3, :, 16:32]).all()
+    assert torch.isfinite(got[6:8, :, 16 * last:]).all() or last == 2
+    out, lse = p.run(window=40)
+    check(p, out, lse, window=40)
+
+
 def test_masked_keys_of_nan():
     p = Problem([40], [200], 2, 1, 64, BF, seed=7).stale()
     p.set_scale("k", 0, 199, 0, 2, NAN_SCALE | 128)       # the last token's key
@@ -266,12 +328,13 @@ def test_masked_keys_of_nan():
 
 @pytest.mark.parametrize("factor", [10.0, 300.0, 3e4])
 @pytest.mark.parametrize("dtype", [BF, FP])
-def test_large_logits(factor, dtype):
+@pytest.mark.parametrize("qn", [[3, 40, 1], [3, 9, 1]])
+def test_large_logits(factor, dtype, qn):
     """Scores in the hundreds and thousands that grow along the cache, so that
     the running maximum moves in most tiles."""
     if dtype == FP and factor > 1e4:
         factor = 1e4
-    p = Problem([3, 40, 1], [150, 333, 20000], 4, 1, 64, dtype, seed=8).stale()
+    p = Problem(qn, [150, 333, 20000], 4, 1, 64, dtype, seed=8).stale()
     p.q = (torch.randn(p.q.shape, generator=R.gen(9)) * factor).to(dtype)
     # one group of the keys grows with the position
     for b, n in enumerate(p.kvn):
@@ -282,9 +345,10 @@ def test_large_logits(factor, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
-def test_small_weights_beside_a_large_one(dtype):
+@pytest.mark.parametrize("hq", [2, 64])
+def test_small_weights_beside_a_large_one(dtype, hq):
     """30000 keys whose weights are e^-8 of the best one's."""
-    p = Problem([1], [30000], 2, 1, 64, dtype, seed=10).stale()
+    p = Problem([1], [30000], hq, 1, 64, dtype, seed=10).stale()
     p.q.zero_()
     p.q[..., 0] = 8.0
     p.parts[0][:] = 0
@@ -292,11 +356,12 @@ def test_small_weights_beside_a_large_one(dtype):
     p.parts[1][:] = 0x38 + 24                            # s = 8: scores -8 of 0.125 * 8 * 8
     best = p.table[0, 200].long()
     p.parts[0][best, 5, :, 0] = 0
-    check(p, *p.run())
+    check(p, *p.run(), heads=range(0, hq, 1 if hq == 2 else 21))
 
 
-def test_pages_out_of_range_are_flagged():
-    p = Problem([1, 2], [200, 100], 4, 1, 64, BF, seed=8)
+@pytest.mark.parametrize("hq", [4, 64])
+def test_pages_out_of_range_are_flagged(hq):
+    p = Problem([1, 2], [200, 100], hq, 1, 64, BF, seed=8)
     good = p.table.clone()
     p.table[0, 1] = 9999
     p.table[1, 0] = -1
@@ -310,25 +375,27 @@ def test_pages_out_of_range_are_flagged():
     check(p, out, lse, window=50)
 
 
-def test_lengths_past_the_table():
-    p = Problem([1, 3], [128, 100], 4, 1, 64, BF, seed=9)
+@pytest.mark.parametrize("hq", [4, 64])
+def test_lengths_past_the_table(hq):
+    p = Problem([1, 3], [128, 100], hq, 1, 64, BF, seed=9)
     args = p.device()
     args[-1] = torch.tensor([5000, 100], dtype=torch.int32, device="cuda")
-    lse = torch.empty((4, 4), device="cuda")
+    lse = torch.empty((4, hq), device="cuda")
     out = pml.pml_paged_attention_nvfp4(*args, p.cu.cuda(), lse=lse, causal=False)
     check(p, out, lse, causal=False)
 
 
-def test_cache_past_32_bits():
+@pytest.mark.parametrize("hq", [16, 64])
+def test_cache_past_32_bits(hq):
     pages, used = 70000, [0, 3, 69998, 69999, 40000]
-    p = Problem([7], [300], 16, 8, 128, BF, seed=9, spare=0)
+    p = Problem([7], [300], hq, 8, 128, BF, seed=9, spare=0)
     q, *small, _, lens = p.device()
     _, *parts = pml.pml_nvfp4_pages(pages, 8, 128)
     for i, u in enumerate(used):
         for dst, src in zip(parts, small):
             dst[u] = src[p.table[0, i].long()]
     table = torch.tensor([used], dtype=torch.int32, device="cuda")
-    lse = torch.empty((7, 16), device="cuda")
+    lse = torch.empty((7, hq), device="cuda")
     out = pml.pml_paged_attention_nvfp4(q, *parts, table, lens, p.cu.cuda(), lse=lse)
     check(p, out, lse, heads=(0, 9))
     sel = torch.arange(299, -1, -1, dtype=torch.int32).repeat(7, 1).cuda()
@@ -391,9 +458,27 @@ def test_lists_of_a_prompt():
         assert torch.equal(pml.pml_sparse_attention_nvfp4(*args, req.cuda(), sel.cuda()), out)
 
 
-def test_selected_bad_places_and_nan():
+def test_selected_past_32_bits():
+    """More rows to a kv head than warps take alone, over rows far into the cache."""
+    p = Problem([1], [300], 64, 1, 128, BF, seed=9, spare=0)
+    q, *small, _, lens = p.device()
+    pages, used = 600000, [0, 3, 599998, 599999, 40000]
+    _, *parts = pml.pml_nvfp4_pages(pages, 1, 128)
+    for i, u in enumerate(used):
+        for dst, src in zip(parts, small):
+            dst[u] = src[p.table[0, i].long()]
+    table = torch.tensor([used], dtype=torch.int32, device="cuda")
+    sel = torch.arange(299, -1, -1, dtype=torch.int32)[None]
+    lse = torch.empty((1, 64), device="cuda")
+    out = pml.pml_sparse_attention_nvfp4(q, *parts, table, lens, torch.zeros(1, dtype=torch.int32, device="cuda"),
+                                         sel.cuda(), lse=lse)
+    check_selected(p, torch.tensor([0]), sel, out, lse, heads=(0, 63))
+
+
+@pytest.mark.parametrize("hq", [6, 100])
+def test_selected_bad_places_and_nan(hq):
     g = R.gen(3)
-    p = Problem([1, 1], [500, 400], 6, 2, 64, BF, seed=3).stale()
+    p = Problem([1, 1], [500, 400], hq, 2, 64, BF, seed=3).stale()
     sel = torch.stack([torch.randperm(500, generator=g)[:200], torch.randperm(400, generator=g)[:200]]).int()
     q, *parts, table, lens = p.device()
     req = torch.tensor([0, 1], dtype=torch.int32)
@@ -409,20 +494,21 @@ def test_selected_bad_places_and_nan():
     pos = int(sel[0, 17])
     p.set_scale("v", 0, pos, 0, 1, NAN_SCALE)
     q, *parts, table, lens = p.device()
-    lse = torch.empty((2, 6), device="cuda")
+    lse = torch.empty((2, hq), device="cuda")
     out = pml.pml_sparse_attention_nvfp4(q, *parts, table, lens, req.cuda(), sel.cuda(), lse=lse)
-    check_selected(p, req, sel, out, lse)
-    assert torch.isnan(out[0, :3, 16:32]).all()
+    check_selected(p, req, sel, out, lse, heads=range(0, hq, max(1, hq // 9)))
+    assert torch.isnan(out[0, :hq // 2, 16:32]).all()
     sel[0, 17] = -1
     out = pml.pml_sparse_attention_nvfp4(q, *parts, table, lens, req.cuda(), sel.cuda(), lse=lse)
-    check_selected(p, req, sel, out, lse)
+    check_selected(p, req, sel, out, lse, heads=range(0, hq, max(1, hq // 9)))
     assert torch.isfinite(out).all()
 
 
 # ------------------------------------------------------------------ as they are used
 
-def test_same_result_every_time_and_captured():
-    p = Problem([1, 90, 1], [2500, 700, 40], 8, 2, 128, BF, seed=12).stale()
+@pytest.mark.parametrize("chunk", [90, 3])
+def test_same_result_every_time_and_captured(chunk):
+    p = Problem([1, chunk, 1], [2500, 700, 40], 8, 2, 128, BF, seed=12).stale()
     args = p.device()
     cu, ws = p.cu.cuda(), pml.pml_attention_workspace(128)
     out = torch.empty_like(args[0])
@@ -443,7 +529,7 @@ def test_same_result_every_time_and_captured():
     torch.cuda.synchronize()
     assert not torch.equal(out[0], want[0])
     p.kvn[0] = 1800                        # (how the keys are shared out depends on all lengths)
-    lse = torch.empty((92, 8), device="cuda")
+    lse = torch.empty((chunk + 2, 8), device="cuda")
     check(p, pml.pml_paged_attention_nvfp4(*args, cu, lse=lse), lse)
     assert torch.equal(out, pml.pml_paged_attention_nvfp4(*args, cu))
 
@@ -468,8 +554,9 @@ def test_memory_of_a_call_on_another_stream():
 
 
 @pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 30, 5000])
-def test_windows_past_every_position(window):
-    p = Problem([30, 3], [20, 300], 4, 1, 64, BF, seed=22).stale()
+@pytest.mark.parametrize("qn", [[30, 3], [7, 3]])
+def test_windows_past_every_position(window, qn):
+    p = Problem(qn, [20, 300], 4, 1, 64, BF, seed=22).stale()
     out, lse = p.run(window=window)
     check(p, out, lse)
 
@@ -478,6 +565,50 @@ def test_no_tokens():
     p = Problem([0, 0], [10, 0], 4, 2, 64, BF, seed=13)
     out, _ = p.run()
     assert out.shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("hq", [4, 32])
+def test_positions_up_to_the_last(dim, hq):
+    """A table as wide as positions go, one page behind all its entries, and a
+    window that leaves the end of it."""
+    width = (2 ** 31 - 1) // 64
+    p = Problem([2], [200], hq, 1, dim, BF, seed=20, spare=0)
+    q, *parts, table, _ = p.device()
+    wide = table[:, :1].expand(1, width).contiguous()
+    lens = torch.tensor([64 * width], dtype=torch.int32, device="cuda")
+    lse = torch.empty((2, hq), device="cuda")
+    out = pml.pml_paged_attention_nvfp4(q, *parts, wide, lens, lse=lse, window=150)
+    assert pml.pml_device_status(clear=True) == 0
+    page = p.table[0, 0].long()
+    for i in range(2):
+        at = torch.arange(64 * width - 2 + i - 149, 64 * width - 1 + i) % 64
+        k, v = (N.values(p.parts[c][page, at], p.parts[c + 1][page, at], 1.0) for c in (0, 2))
+        for h in range(hq):
+            judge(p, p.q[i:i + 1, h], k[:, 0], v[:, 0], torch.ones((1, 150), dtype=torch.bool), dim ** -0.5,
+                  out[i:i + 1, h], lse[i:i + 1, h], f"token {i}")
+
+
+def test_two_captured_graphs_share_a_workspace():
+    """Replayed one after the other, whatever the other has left there."""
+    few, many = Problem([1] * 9, [700] * 9, 8, 1, 128, BF, seed=23), Problem([30], [900], 8, 1, 128, BF, seed=24)
+    ws = pml.pml_attention_workspace(128)
+    graphs, outs, want = [], [], []
+    for p in (few, many):
+        args, cu = p.device(), p.cu.cuda()
+        want.append(pml.pml_paged_attention_nvfp4(*args, cu))
+        out = torch.zeros_like(args[0])
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            pml.pml_paged_attention_nvfp4(*args, cu, out, workspace=ws)
+        graphs.append((graph, args, cu))
+        outs.append(out)
+    for order in ((0, 1), (1, 0, 1, 0)):
+        for i in order:
+            graphs[i][0].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
