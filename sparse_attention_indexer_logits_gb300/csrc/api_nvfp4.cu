@@ -21,6 +21,10 @@ constexpr int kMaxScaleExponent = 32;
 // take 123 us that way and 139 by tiles, 64 rows 157 and 141, 256 rows 568 and
 // 187.
 constexpr int kNvWarpRows = 48;
+// Lists are, whatever the rows, while a warp has no more than so many steps: 64
+// heads over 1, 64 tokens of 64 positions 9.2 us that way and 13.9 by tiles, of 500
+// 17.9 and 20.8, of 2048 34.3 and 34.9; 200 tokens of 2048 132 and 83.
+constexpr int kNvWarpSteps = 8;
 
 // Strides of a dimension of one element are never used: any valid one will do.
 int64_t used(int64_t stride, int64_t size, int64_t other) { return size > 1 ? stride : other; }
@@ -89,7 +93,10 @@ int attention_call(NvAttnArgs& a, const void* q, int64_t q_token, int64_t q_head
     const bool fp16 = dtype == PML_DTYPE_FLOAT16;
     const float scale = softmax_scale * a.kc.scale;
     const long long per_request = a.selected ? 1 : (tokens + a.batch - 1) / a.batch;
-    if (per_request * group > kNvWarpRows && group <= kAttnHalfRows) {
+    bool by_tiles = per_request * group > kNvWarpRows && group <= kAttnHalfRows;
+    if (by_tiles && a.selected)
+        by_tiles = nvfp4_list_steps(a.sel_k, group, (long long)tokens * kv_heads) > (long long)kNvWarpSteps * nvfp4_list_warps(dev.sm_count);
+    if (by_tiles) {
         AttnArgs w = {};
         attention_workspace(w, workspace, dev.sm_count, head_dim);
         w.kc4 = a.kc;

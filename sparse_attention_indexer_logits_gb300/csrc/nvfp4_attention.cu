@@ -17,6 +17,7 @@ namespace {
 using namespace nvattn;
 
 constexpr int kJoinWarps = 8, kJoinRows = 4;
+constexpr int kJoinSteps = 3;     // the join's time in steps of a warp
 
 // A CTA whose pieces ended with an item that it had begun (slot 1) owns the
 // join: the item's other pieces are slot 0 of the following CTAs, up to the one
@@ -116,6 +117,14 @@ Pieces take(uint8_t*& at, int64_t n, int slots, int rows, int dim)
 
 }  // namespace
 
+long long nvfp4_list_steps(int k, int group, long long lists)
+{
+    constexpr int rows = Cfg<128, 2>::kRows;
+    return lists * ((group + rows - 1) / rows) * ((k + kStepKeys - 1) / kStepKeys);
+}
+
+int nvfp4_list_warps(int num_ctas) { return num_ctas * Cfg<128, 2>::kWarps; }
+
 cudaError_t launch_nvfp4_attention(int head_dim, bool fp16, NvAttnArgs& a, int num_ctas, void* workspace,
                                    int64_t workspace_bytes, cudaStream_t stream)
 {
@@ -126,13 +135,22 @@ cudaError_t launch_nvfp4_attention(int head_dim, bool fp16, NvAttnArgs& a, int n
     a.block_heads = (a.group + a.head_blocks - 1) / a.head_blocks;
     a.tile_tokens = a.selected || a.group > rows ? 1 : rows / a.group;
     const int warps = tiles == 1 ? Cfg<128, 1>::kWarps : Cfg<128, 2>::kWarps;
+    if (a.selected) {
+        // Items of the same number of steps: where leaving them whole costs a warp no
+        // more than kJoinSteps further steps, no CTA shares one and nothing is left
+        // to join.
+        const long long items = (long long)a.tokens * a.kv_heads * a.head_blocks;
+        const long long steps = (a.sel_k + kStepKeys - 1) / kStepKeys + kItemUnits;
+        const long long whole = (items + num_ctas - 1) / num_ctas * steps / warps;
+        a.whole_items = whole <= items * steps / ((long long)num_ctas * warps) + kJoinSteps;
+    }
     uint8_t* at = static_cast<uint8_t*>(workspace);
     const Pieces wp = take(at, (int64_t)num_ctas * warps, 1, rows, head_dim);
     const Pieces cp = take(at, num_ctas, 2, rows, head_dim);
     if (at - static_cast<uint8_t*>(workspace) > workspace_bytes) return cudaErrorInvalidValue;    // never
     cudaError_t e = head_dim == 128 ? launch_nvfp4_attention_dim<128>(fp16, tiles, a, wp, cp, num_ctas, stream)
                                     : launch_nvfp4_attention_dim<64>(fp16, tiles, a, wp, cp, num_ctas, stream);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || a.whole_items) return e;
     return head_dim == 128 ? launch_join_dim<128>(fp16, tiles, a, cp, num_ctas, stream)
                            : launch_join_dim<64>(fp16, tiles, a, cp, num_ctas, stream);
 }

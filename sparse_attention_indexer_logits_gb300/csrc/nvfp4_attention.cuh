@@ -415,10 +415,19 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     const int heads = a.kv_heads * a.head_blocks;
     if constexpr (SEL) {
         const int per = sel_n + kItemUnits;
-        const int workers = gridDim.x * C::kWarps, me = blockIdx.x * C::kWarps + warp;
-        const long long total = (long long)a.tokens * heads * per;
-        const long long s0 = range_start(total, workers, me);
-        start.left = range_start(total, workers, me + 1) - s0;
+        const long long items = (long long)a.tokens * heads;
+        long long s0, s1;
+        if (a.whole_items) {               // a CTA's items, shared out over its warps
+            const long long i0 = range_start(items, gridDim.x, blockIdx.x);
+            const long long units = (range_start(items, gridDim.x, blockIdx.x + 1) - i0) * per;
+            s0 = i0 * per + range_start(units, C::kWarps, warp);
+            s1 = i0 * per + range_start(units, C::kWarps, warp + 1);
+        } else {
+            const int workers = gridDim.x * C::kWarps, me = blockIdx.x * C::kWarps + warp;
+            s0 = range_start(items * per, workers, me);
+            s1 = range_start(items * per, workers, me + 1);
+        }
+        start.left = s1 - s0;
         const long long item = s0 / per;
         start.at = (int)(s0 - item * per);
         start.b = (int)(item / heads);

@@ -74,6 +74,7 @@ struct NvAttnArgs {
     int head_blocks;               // items that share a kv head's query heads
     int block_heads;               // query heads of one
     int sel_k;                     // selected: entries per token
+    int whole_items;               // selected: no item is split between CTAs
     int causal;
     int window;                    // > 0: only keys past position - window
     float scale;                   // softmax scale times the keys' scale
@@ -82,6 +83,11 @@ struct NvAttnArgs {
 
 cudaError_t launch_nvfp4_append(const NvAppendArgs& a, cudaStream_t stream);
 cudaError_t launch_nvfp4_read(const NvReadArgs& a, int sm_count, cudaStream_t stream);
+// Lists of k positions for groups of more than eight heads: steps of all warps,
+// and the warps.
+long long nvfp4_list_steps(int k, int group, long long lists);
+int nvfp4_list_warps(int num_ctas);
+
 // Fills in the items' shape.  `workspace` holds pml_attention_workspace_bytes.
 cudaError_t launch_nvfp4_attention(int head_dim, bool fp16, NvAttnArgs& a, int num_ctas, void* workspace,
                                    int64_t workspace_bytes, cudaStream_t stream);

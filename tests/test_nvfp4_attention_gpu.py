@@ -458,7 +458,30 @@ def test_lists_of_a_prompt():
         assert torch.equal(pml.pml_sparse_attention_nvfp4(*args, req.cuda(), sel.cuda()), out)
 
 
-def test_selected_past_32_bits():
+@pytest.mark.parametrize("dim", [128, 64])
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("k", [129, 700])
+def test_selected_by_many_tokens(dim, dtype, k):
+    """Enough tokens of 64 heads that their lists go by tiles."""
+    g = R.gen(k + 1)
+    kvn, tokens = [1000, 65, 1, 0, 300], 1200
+    p = Problem([1] * 5, kvn, 64, 1, dim, dtype, seed=k, k_scale=0.5, v_scale=2.0).stale()
+    req = torch.tensor([0, 1, 4, 2, 0, 3, 1, -1], dtype=torch.int32).repeat(tokens // 8)
+    p.q = (torch.randn((tokens, 64, dim), generator=g) * 3.0).to(dtype)
+    sel = torch.randint(-200, 1200, (tokens, k + 3), generator=g, dtype=torch.int32)
+    sel[2::8, ::2] = -1
+    sel[6::8] = -1
+    q, *rest = p.device()
+    lse = torch.empty((tokens, 64), device="cuda")
+    out = pml.pml_sparse_attention_nvfp4(q, *rest, req.cuda(), sel.cuda()[:, :k], lse=lse, k_scale=0.5, v_scale=2.0)
+    assert pml.pml_device_status(clear=True) == 0
+    at = [*range(8), *range(403, 1200, 97), 1199]
+    p.q = p.q[at]
+    check_selected(p, req[at], sel[at][:, :k], out[at], lse[at], heads=(0, 21, 63))
+
+
+@pytest.mark.parametrize("tokens", [1, 900])
+def test_selected_past_32_bits(tokens):
     """More rows to a kv head than warps take alone, over rows far into the cache."""
     p = Problem([1], [300], 64, 1, 128, BF, seed=9, spare=0)
     q, *small, _, lens = p.device()
@@ -468,39 +491,50 @@ def test_selected_past_32_bits():
         for dst, src in zip(parts, small):
             dst[u] = src[p.table[0, i].long()]
     table = torch.tensor([used], dtype=torch.int32, device="cuda")
-    sel = torch.arange(299, -1, -1, dtype=torch.int32)[None]
-    lse = torch.empty((1, 64), device="cuda")
-    out = pml.pml_sparse_attention_nvfp4(q, *parts, table, lens, torch.zeros(1, dtype=torch.int32, device="cuda"),
-                                         sel.cuda(), lse=lse)
-    check_selected(p, torch.tensor([0]), sel, out, lse, heads=(0, 63))
+    sel = torch.arange(299, -1, -1, dtype=torch.int32).repeat(tokens, 1)
+    lse = torch.empty((tokens, 64), device="cuda")
+    out = pml.pml_sparse_attention_nvfp4(q.repeat(tokens, 1, 1), *parts, table, lens,
+                                         torch.zeros(tokens, dtype=torch.int32, device="cuda"), sel.cuda(), lse=lse)
+    for t in {0, tokens // 2, tokens - 1}:
+        check_selected(p, torch.tensor([0]), sel[:1], out[t:t + 1], lse[t:t + 1], heads=(0, 63))
 
 
-@pytest.mark.parametrize("hq", [6, 100])
-def test_selected_bad_places_and_nan(hq):
+@pytest.mark.parametrize("hq,copies", [(6, 1), (100, 1), (100, 400)])
+def test_selected_bad_places_and_nan(hq, copies):
     g = R.gen(3)
     p = Problem([1, 1], [500, 400], hq, 2, 64, BF, seed=3).stale()
     sel = torch.stack([torch.randperm(500, generator=g)[:200], torch.randperm(400, generator=g)[:200]]).int()
-    q, *parts, table, lens = p.device()
     req = torch.tensor([0, 1], dtype=torch.int32)
-    bad = table.clone()
+    heads = range(0, hq, max(1, hq // 9))
+
+    def run(table=None, req=req):
+        q, *parts, good, lens = p.device()
+        many = lambda t: t.cuda().repeat(copies, *[1] * (t.dim() - 1))  # noqa: E731
+        lse = torch.empty((2 * copies, hq), device="cuda")
+        out = pml.pml_sparse_attention_nvfp4(many(q), *parts, good if table is None else table, lens, many(req), many(sel),
+                                             lse=lse)
+        return out, lse
+
+    def judge_all(out, lse):
+        for i in {0, 2 * (copies // 2), 2 * copies - 2}:
+            check_selected(p, req, sel, out[i:i + 2], lse[i:i + 2], heads=heads)
+
+    bad = p.table.clone()
     bad[0, 2] = 100000
-    pml.pml_sparse_attention_nvfp4(q, *parts, bad, lens, req.cuda(), sel.cuda())
+    run(table=bad.cuda())
     assert pml.pml_device_status(clear=True) == pml.STATUS_BAD_BLOCK
-    out = pml.pml_sparse_attention_nvfp4(q, *parts, table, lens, torch.tensor([0, 2], dtype=torch.int32).cuda(),
-                                         sel.cuda())
+    out, _ = run(req=torch.tensor([0, 2], dtype=torch.int32))
     assert pml.pml_device_status(clear=True) == pml.STATUS_BAD_REQUEST
-    assert (out[1] == 0).all()
+    assert (out[1::2] == 0).all()
     # a listed NaN reaches the row, one that is not listed does not
     pos = int(sel[0, 17])
     p.set_scale("v", 0, pos, 0, 1, NAN_SCALE)
-    q, *parts, table, lens = p.device()
-    lse = torch.empty((2, hq), device="cuda")
-    out = pml.pml_sparse_attention_nvfp4(q, *parts, table, lens, req.cuda(), sel.cuda(), lse=lse)
-    check_selected(p, req, sel, out, lse, heads=range(0, hq, max(1, hq // 9)))
-    assert torch.isnan(out[0, :hq // 2, 16:32]).all()
+    out, lse = run()
+    judge_all(out, lse)
+    assert torch.isnan(out[::2, :hq // 2, 16:32]).all()
     sel[0, 17] = -1
-    out = pml.pml_sparse_attention_nvfp4(q, *parts, table, lens, req.cuda(), sel.cuda(), lse=lse)
-    check_selected(p, req, sel, out, lse, heads=range(0, hq, max(1, hq // 9)))
+    out, lse = run()
+    judge_all(out, lse)
     assert torch.isfinite(out).all()
 
 
