@@ -72,7 +72,7 @@ constexpr float kFresh = 1e30f;        // `off` of a row that has seen no key
 template <int D, int NT>
 struct Cfg {
     static constexpr int kRows = 8 * NT;
-    static constexpr int kWarps = NT == 1 ? 16 : 12;       // 128 or 168 registers a thread
+        static constexpr int kWarps = NT == 1 ? 16 : 12;       // 128 or 168 registers a thread
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kCode = D / 2, kScale = D / 16;   // bytes of a row
     static constexpr int kStageBytes = 2 * kStepKeys * (kCode + kScale);
@@ -705,42 +705,39 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             // element 2 h + c of sc[x][y] is key 16 y + 8 h + (g / 2) + 4 (g & 1),
             // row 8 x + 2 t + c
             float sc[NT][2][4];
-            uint32_t w[2][2][KS / 2], m[2][2][2];
 #pragma unroll
-            for (int y = 0; y < 2; ++y)
+            for (int y = 0; y < 2; ++y) {
+                uint32_t w[2][KS / 2], m[2][2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int row = 16 * y + 8 * h + g;
                     if constexpr (D == 128) {
                         const uint4 v = ld_shared_v4(from + kKC + row * CB + t * (CB / 4));
-                        w[y][h][0] = v.x; w[y][h][1] = v.y; w[y][h][2] = v.z; w[y][h][3] = v.w;
+                        w[h][0] = v.x; w[h][1] = v.y; w[h][2] = v.z; w[h][3] = v.w;
                         const uint32_t s2 = e4m3x2_to_f16x2(ld_shared_u16(from + kKS + row * SB + 2 * t));
-                        m[y][h][0] = __byte_perm(s2, s2, 0x1010);
-                        m[y][h][1] = __byte_perm(s2, s2, 0x3232);
+                        m[h][0] = __byte_perm(s2, s2, 0x1010);
+                        m[h][1] = __byte_perm(s2, s2, 0x3232);
                     } else {
                         const uint2 v = ld_shared_v2_u32(from + kKC + row * CB + t * (CB / 4));
-                        w[y][h][0] = v.x; w[y][h][1] = v.y;
-                        m[y][h][0] = m[y][h][1] = e4m3_to_f16x2_dup(ld_shared_u8(from + kKS + row * SB + t));
+                        w[h][0] = v.x; w[h][1] = v.y;
+                        m[h][0] = m[h][1] = e4m3_to_f16x2_dup(ld_shared_u8(from + kKS + row * SB + t));
                     }
                 }
-            // (the two blocks of keys in turn: neither waits for its own sums)
 #pragma unroll
-            for (int c = 0; c < KS / 2; ++c) {
-                uint4 q[NT];
+                for (int c = 0; c < KS / 2; ++c) {
+                    uint4 q[NT];
 #pragma unroll
-                for (int x = 0; x < NT; ++x) {
-                    if constexpr (NT == 1) q[x] = make_uint4(qb[2 * c][0], qb[2 * c][1], qb[2 * c + 1][0], qb[2 * c + 1][1]);
-                    else q[x] = ld_shared_v4(q_at + (x * (KS / 2) + c) * 512);
-                }
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
+                    for (int x = 0; x < NT; ++x) {
+                        if constexpr (NT == 1) q[x] = make_uint4(qb[2 * c][0], qb[2 * c][1], qb[2 * c + 1][0], qb[2 * c + 1][1]);
+                        else q[x] = ld_shared_v4(q_at + (x * (KS / 2) + c) * 512);
+                    }
                     uint32_t u[4], v[4];
-                    e2m1x8_to_f16x2x4(w[y][0][c], u);
-                    e2m1x8_to_f16x2x4(w[y][1][c], v);
+                    e2m1x8_to_f16x2x4(w[0][c], u);
+                    e2m1x8_to_f16x2x4(w[1][c], v);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        u[e] = mul_f16x2(u[e], m[y][0][2 * c < KS / 2 ? 0 : 1]);
-                        v[e] = mul_f16x2(v[e], m[y][1][2 * c < KS / 2 ? 0 : 1]);
+                        u[e] = mul_f16x2(u[e], m[0][2 * c < KS / 2 ? 0 : 1]);
+                        v[e] = mul_f16x2(v[e], m[1][2 * c < KS / 2 ? 0 : 1]);
                     }
 #pragma unroll
                     for (int x = 0; x < NT; ++x) {
