@@ -79,6 +79,9 @@ int attention_call(NvAttnArgs& a, const void* q, int64_t q_token, int64_t q_head
     int rc = take_cache(k_cache, num_pages, kv_heads, head_dim, a.kc);
     if (rc == PML_OK) rc = take_cache(v_cache, num_pages, kv_heads, head_dim, a.vc);
     if (rc != PML_OK) return rc;
+    // (c as a normal number, and its quotients too)
+    const float scale = softmax_scale * a.kc.scale;
+    if (!(scale >= 1e-30f && scale <= 1e30f)) return PML_ERR_INVALID_ARG;
     const int64_t qs[2] = {used(q_head, num_heads, head_dim), used(q_token, tokens, head_dim)};
     if (qs[0] <= 0 || qs[0] % 8 || qs[1] <= 0 || qs[1] % 8) return PML_ERR_ALIGNMENT;
     if ((tokens > 1 && out_token % 8) || (num_heads > 1 && out_head % 8)) return PML_ERR_ALIGNMENT;
@@ -91,7 +94,6 @@ int attention_call(NvAttnArgs& a, const void* q, int64_t q_token, int64_t q_head
     if (workspace_bytes < pml_attention_workspace_bytes(dev.sm_count, head_dim)) return PML_ERR_INVALID_ARG;
     const int group = num_heads / kv_heads;
     const bool fp16 = dtype == PML_DTYPE_FLOAT16;
-    const float scale = softmax_scale * a.kc.scale;
     const long long per_request = a.selected ? 1 : (tokens + a.batch - 1) / a.batch;
     bool by_tiles = per_request * group > kNvWarpRows && group <= kAttnHalfRows;
     if (by_tiles && a.selected)

@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) nvfp4_join_kernel(const NvAtt
 #pragma unroll
                 for (int k = 0; k < N; ++k) v[k] = 0.0f;
             }
-            x.add(st.x, st.y, v);
+            x.add(st.x, st.y, v, a.scale_log2);
         }
     }
     if (half) {
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) nvfp4_join_kernel(const NvAtt
     float v[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) v[k] = part[warp >> 1][2 + k][lane];
-    x.add(part[warp >> 1][0][lane], part[warp >> 1][1][lane], v);
+    x.add(part[warp >> 1][0][lane], part[warp >> 1][1][lane], v, a.scale_log2);
     write_joined<FP16, N>(a, x, rec[kPcTok0], rec[kPcHead], rec[kPcHeads], row, lane * N);
 }
 

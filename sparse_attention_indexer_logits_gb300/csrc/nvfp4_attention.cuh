@@ -62,10 +62,13 @@ namespace nvattn {
 constexpr int kStepKeys = 32;
 // Units of work: a step is one, beginning and ending an item three.
 constexpr int kItemUnits = 3;
-// P = 2^(c S + off): 2^7 times the weights, so that fp16 keeps the small ones'
-// bits, up to 2^15 before a larger maximum moves `off`.
+// P = 2^(c (S - m) + 7): 2^7 times the weights, so that fp16 keeps the small ones'
+// bits, up to 2^15 before a larger maximum moves m.
 constexpr float kPLog2 = 7.0f, kPMost = 15.0f;
-constexpr float kFresh = 1e30f;        // `off` of a row that has seen no key
+// c S - c m is one fused product and sum while |c m| is below this (c m is
+// rounded once, to 2^-14); past it the difference is taken first.
+constexpr float kFar = 1024.0f;
+constexpr float kFresh = 3e38f;        // 7 - c m of a row that has seen no key: any score is too large
 
 // NT: groups of eight rows in an item, one or two.  With two, Q lies in shared
 // memory.
@@ -340,11 +343,12 @@ template <int N>
 struct Joined {
     float top = -INFINITY, sum = 0.0f, acc[N] = {};
 
-    __device__ void add(float m, float l, const float (&v)[N])
+    // (maxima are scores; times scale_log2 they are exponents)
+    __device__ void add(float m, float l, const float (&v)[N], float scale_log2)
     {
         const float next = fmaxf(top, m);
-        const float f = top == -INFINITY ? 0.0f : exp2_approx(top - next);
-        const float g = m == -INFINITY ? 0.0f : exp2_approx(m - next);
+        const float f = top == -INFINITY ? 0.0f : exp2_approx((top - next) * scale_log2);
+        const float g = m == -INFINITY ? 0.0f : exp2_approx((m - next) * scale_log2);
         top = next;
         sum = sum * f + l * g;
 #pragma unroll
@@ -365,7 +369,8 @@ __device__ __forceinline__ void load_cols(const float* p, float (&v)[N])
     }
 }
 
-// A row's scaled output and log-sum: `top` is the exponent that its sums lack.
+// A row's scaled output and log-sum from its sums, which are 2^7 2^-top times too
+// large.
 __device__ __forceinline__ float inverse_of(float sum, float v_scale)
 {
     return sum > 0.0f || sum != sum ? v_scale / sum : 0.0f;
@@ -373,7 +378,7 @@ __device__ __forceinline__ float inverse_of(float sum, float v_scale)
 
 __device__ __forceinline__ float log_sum_of(float top, float sum)
 {
-    return sum == 0.0f ? -INFINITY : top * 0.6931471805599453f + logf(sum);
+    return sum == 0.0f ? -INFINITY : (top - kPLog2) * 0.6931471805599453f + logf(sum);
 }
 
 // N columns of row `row` of an item, joined.
@@ -391,7 +396,7 @@ __device__ __forceinline__ void write_joined(const NvAttnArgs& a, const Joined<N
     else
         *reinterpret_cast<uint32_t*>(out) = pack_out<FP16>(x.acc[0] * inv, x.acc[1] * inv);
     if (col == 0 && a.lse != nullptr)
-        a.lse[token * a.kv_heads * a.group + head] = log_sum_of(x.top, x.sum);
+        a.lse[token * a.kv_heads * a.group + head] = log_sum_of(x.top * a.scale_log2, x.sum);
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -630,10 +635,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             cp_async_commit();
         }
 
-        // ---- the rows scaled to fp16, and of rows 2 t and 2 t + 1 the factor, the exponent, the sum and the keys
+        // ---- the rows scaled to fp16, and of rows 2 t and 2 t + 1 the factor, the reference and the sum
         uint32_t qb[KS][2];                    // (of eight rows)
         const uint32_t q_at = smem_addr(smem) + C::kQ + warp * C::kQBytes + lane * 16;
-        float f[NT][2], off[NT][2], l[NT][2];
+        float f[NT][2], ref[NT][2], l[NT][2];
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
             uint4 (&w)[KS / 2] = qw[x];
@@ -674,7 +679,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 f[x][c] = __shfl_sync(0xffffffffu, scale, 8 * t + 4 * c);
-                off[x][c] = kFresh;
+                ref[x][c] = -INFINITY;
                 l[x][c] = 0.0f;
             }
         }
@@ -779,28 +784,38 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             }
             // exponents of P, unless one is too large
             float most = -INFINITY;
+            bool far = false;
             float z[NT][2][4];
 #pragma unroll
-            for (int x = 0; x < NT; ++x)
+            for (int x = 0; x < NT; ++x) {
+                float off[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    off[c] = ref[x][c] == -INFINITY ? kFresh : fmaf(-ref[x][c], f[x][c], kPLog2);
+                    far = far || fabsf(off[c]) > kFar;
+                }
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) z[x][y][e] = fmaf(sc[x][y][e], f[x][e & 1], off[x][e & 1]);
+                    for (int e = 0; e < 4; ++e) z[x][y][e] = fmaf(sc[x][y][e], f[x][e & 1], off[e & 1]);
                     most = max3(most, z[x][y][0], z[x][y][1]);
                     most = max3(most, z[x][y][2], z[x][y][3]);
                 }
-            if (__any_sync(0xffffffffu, most > kPMost)) {
+            }
+            if (__any_sync(0xffffffffu, far || most > kPMost)) {
 #pragma unroll
                 for (int x = 0; x < NT; ++x) {
-                    float down[2];
+                    float down[2], from_ref[2];
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         float m = fmaxf(fmaxf(sc[x][0][c], sc[x][0][2 + c]), fmaxf(sc[x][1][c], sc[x][1][2 + c]));
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-                        const float next = m == -INFINITY ? off[x][c] : fminf(off[x][c], fmaf(-m, f[x][c], kPLog2));
-                        down[c] = off[x][c] == kFresh ? 0.0f : exp2_approx(next - off[x][c]);
-                        off[x][c] = next;
+                        // (from -inf on: yes unless m is)
+                        const float next = (m - ref[x][c]) * f[x][c] > kPMost - kPLog2 ? m : ref[x][c];
+                        down[c] = ref[x][c] == -INFINITY ? 0.0f : exp2_approx((ref[x][c] - next) * f[x][c]);
+                        ref[x][c] = next;
+                        from_ref[c] = next == -INFINITY ? 0.0f : next;
                         l[x][c] *= down[c];
                     }
 #pragma unroll
@@ -813,7 +828,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 #pragma unroll
                     for (int y = 0; y < 2; ++y)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) z[x][y][e] = fmaf(sc[x][y][e], f[x][e & 1], off[x][e & 1]);
+                        for (int e = 0; e < 4; ++e)
+                            z[x][y][e] = fmaf(sc[x][y][e] - from_ref[e & 1], f[x][e & 1], kPLog2);
                 }
             }
             uint32_t pb[NT][2][2];
@@ -951,7 +967,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                     }
                     if (g == 0 && a.lse != nullptr)
                         a.lse[(long long)(token + i) * a.kv_heads * a.group + head0 + r - i * nh] =
-                            log_sum_of(-off[x][c], l[x][c]);
+                            log_sum_of(ref[x][c] * f[x][c], l[x][c]);
                 }
         } else {
             // The last piece stays in the ring, which nothing else needs any more.
@@ -975,7 +991,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const int r = 8 * x + 2 * t + c;
-                    if (g == 0) stats[r] = make_float2(off[x][c] == kFresh ? -INFINITY : -off[x][c], l[x][c]);
+                    // (the reference as a score of q itself: its own power of two undone)
+                    if (g == 0) stats[r] = make_float2(ref[x][c] * (f[x][c] / a.scale_log2), l[x][c]);
                     float4* out = reinterpret_cast<float4*>(part + r * D + g * E);
 #pragma unroll
                     for (int v = 0; v < E / 4; ++v)
@@ -1034,7 +1051,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             const float2 st = stats[row];
             float y[N];
             load_cols<N>(part + row * D + col, y);
-            x.add(st.x, st.y, y);
+            x.add(st.x, st.y, y, a.scale_log2);
         };
         if (!led) add(w0, true);            // (what an item begins with is its warp's last piece)
         for (; members; members &= members - 1) {

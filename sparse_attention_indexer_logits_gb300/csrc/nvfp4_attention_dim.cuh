@@ -12,8 +12,15 @@ cudaError_t launch_nvfp4_one(const NvAttnArgs& a, const nvattn::Pieces& wp, cons
 {
     using C = nvattn::Cfg<D, NT>;
     auto kernel = nvattn::nvfp4_attention_kernel<D, FP16, SEL, NT>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kTotal);
+    static int configured_device = -1;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (configured_device != dev) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kTotal);
+        if (e != cudaSuccess) return e;
+        configured_device = dev;
+    }
     return launch_dependent(kernel, dim3((unsigned)num_ctas), C::kThreads, C::kTotal, stream, a, wp, cp);
 }
 

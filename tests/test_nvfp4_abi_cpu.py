@@ -80,6 +80,8 @@ def attention_refusals(call):
     assert call(dtype=F32) == UNSUPPORTED and call(dim=96) == UNSUPPORTED and call(heads=8194) == UNSUPPORTED
     for bad in (0.0, -1.0, float("nan"), float("inf")):
         assert call(scale=bad) == INVALID
+    tiny, huge = cache(scale=2.0 ** -32), cache(scale=2.0 ** 32)
+    assert call(kc=tiny[0], scale=1e-22) == INVALID and call(kc=huge[0], scale=1e22) == INVALID
     for name in ("q", "bt", "lens", "out", "ws"):
         assert call(**{name: None}) == INVALID, name
     assert call(pages=0) == INVALID and call(btw=0) == INVALID and call(bts=3) == INVALID

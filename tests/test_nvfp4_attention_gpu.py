@@ -344,6 +344,42 @@ def test_large_logits(factor, dtype, qn):
     check(p, *p.run())
 
 
+@pytest.mark.parametrize("size", [1e4, 1e20, -1e20, 1e34, -1e34])
+@pytest.mark.parametrize("hq", [2, 64])
+def test_equal_logits_far_from_zero(size, hq):
+    """Every key's score is the same number, however large: the output is the mean of
+    the values, to P's and the output's roundings."""
+    p = Problem([1, 1], [300, 4000], hq, 1, 64, BF, seed=11).stale()
+    p.q.fill_(size)
+    for b, n in enumerate(p.kvn):
+        at = torch.arange(n)
+        page = p.table[b].long()[at // 64]
+        p.parts[0][page, at % 64] = 0x22                # 1 s
+        p.parts[1][page, at % 64] = 0x38                # s = 1
+    out, lse = p.run()
+    for b, n in enumerate(p.kvn):
+        _, v = p.rows(b, torch.arange(n))
+        want, mag = v[:, 0].mean(0), v[:, 0].abs().mean(0)
+        assert ((out[b].cpu().double() - want).abs() <= 2.0 ** -10 * mag + 2.0 ** -8 * want.abs()).all()
+        logit = 64 * 0.125 * float(p.q[0, 0, 0])
+        assert (lse[b].cpu().double() - logit - math.log(n)).abs().max() <= 2.0 ** -22 * abs(logit) + 1e-5
+    assert pml.pml_device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(4, 2), (24, 1)])
+def test_long_lists_of_few_tokens(dim, hq, hkv):
+    """Lists long enough to be split between CTAs."""
+    g = R.gen(hq)
+    p = Problem([1, 1], [5000, 3000], hq, hkv, dim, FP, seed=12).stale()
+    sel = torch.randint(-100, 5000, (2, 4000), generator=g, dtype=torch.int32)
+    req = torch.tensor([0, 1], dtype=torch.int32)
+    lse = torch.empty((2, hq), device="cuda")
+    out = pml.pml_sparse_attention_nvfp4(*p.device(), req.cuda(), sel.cuda(), lse=lse)
+    assert pml.pml_device_status(clear=True) == 0
+    check_selected(p, req, sel, out, lse, heads=range(0, hq, 3))
+
+
 @pytest.mark.parametrize("dtype", [BF, FP])
 @pytest.mark.parametrize("hq", [2, 64])
 def test_small_weights_beside_a_large_one(dtype, hq):
