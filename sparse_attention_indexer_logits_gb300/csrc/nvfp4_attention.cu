@@ -23,7 +23,8 @@ constexpr int kJoinSteps = 3;     // the join's time in steps of a warp
 // join: the item's other pieces are slot 0 of the following CTAs, up to the one
 // that holds its end.  A CTA here takes four rows, two warps each, which take
 // half of the pieces each in the order of their numbers, a lane two or four
-// columns.
+// columns.  Bound by the latency of three dependent loads and its launch: about
+// 4 us of a call's time, whatever the lengths.
 template <int D, bool FP16, int NT>
 __global__ void __launch_bounds__(kJoinWarps * 32) nvfp4_join_kernel(const NvAttnArgs a, const Pieces cp, int num_ctas)
 {

@@ -61,6 +61,23 @@
 //       29 us: a floor of 10; a fixed part of 12 us (prologue, first lookups,
 //       join), then the row copies.  (Sixteen lanes a row took 36 us: an
 //       offset to shuffle for every copy)
+//
+// Pages held in 4 bits (FP4): for calls of many rows to a kv head, where a key's
+// codes are turned into fp16 once for up to 256 rows.  The load and the gather
+// warp copy codes and scales as they are, two tiles ahead, and turn them into
+// the stage's tile; nothing else changes but Q, which the softmax groups turn to
+// fp16 (bf16 tiles take twice the conversions: 290 us against 159).
+//   16 requests x 8 kv heads of 128 over 8500 keys each
+//       64 rows of q to a head 141 us, 128 145, 256 187; 21 for the bytes alone.
+//       Bound by the two warps that turn codes: 81 us without that, 69 without
+//       the copies too.  (Six warps, of a block of 512 threads: the softmax has
+//       fewer registers and reads its scores twice; 64 rows 134, 256 rows 218.
+//       Codes held in registers ahead of the stage: spills, 391)
+//   48 requests of 0 .. 40 tokens over up to 8000 keys, 20 / 4 heads of 64, a
+//   window of 1500, fp16: 41 us, bound as the 16-bit pages' mixed batch is
+//   4096 tokens that end 32768 keys, 32 heads over 4: 2270 us, against 1500
+//       where the pages are first read into 16-bit ones (27 us) and attended to
+//       there, as the codes are turned once for each 256 rows
 #pragma once
 
 #include <cuda_bf16.h>
