@@ -111,8 +111,11 @@ Pieces take(uint8_t*& at, int64_t n, int slots, int rows, int dim)
     at += n * slots * rows * dim * 4;
     p.stats = reinterpret_cast<float2*>(at);
     at += n * slots * rows * 8;
-    p.rec = reinterpret_cast<int*>(at);
-    at += n * 2 * kPcInts * 4;
+    p.rec = nullptr;
+    if (slots == 2) {                // (those of one are the CTA's own matter)
+        p.rec = reinterpret_cast<int*>(at);
+        at += n * 2 * kPcInts * 4;
+    }
     return p;
 }
 

@@ -91,6 +91,10 @@ constexpr float kPLog2 = 7.0f, kPMost = 15.0f;
 constexpr float kFar = 1024.0f;
 constexpr float kFresh = 3e38f;        // 7 - c m of a row that has seen no key: any score is too large
 
+// a piece's record
+enum { kPcUsed, kPcTok0, kPcNtok, kPcHead, kPcHeads, kPcLast };
+constexpr int kPcInts = 8;
+
 // NT: groups of eight rows in an item, one or two.  With two, Q lies in shared
 // memory.
 template <int D, int NT>
@@ -107,20 +111,17 @@ struct Cfg {
     static constexpr int kMasks = kQ + kWarps * kQBytes;   // uint32 [kWarps][8]
     static constexpr int kSums = kMasks + kWarps * 32;     // long long [kWarps]
     static constexpr int kRecs = kSums + kWarps * 8;       // pieces of the CTA
-    static constexpr int kTotal = kRecs + kWarps * 2 * 4;
+    static constexpr int kPieces = kRecs + kWarps * 8;     // int [kWarps][2][kPcInts]
+    static constexpr int kTotal = kPieces + kWarps * 2 * kPcInts * 4;
     static_assert(kTotal <= 232448, "shared memory of a CTA");
     static_assert(kAttnMaxBatch * 8 <= kMasks, "a number per request fits the ring and Q");
     static_assert(kRows * (D * 4 + 8) <= kRing, "a piece fits the ring");
 };
 
-// piece record in the workspace
-enum { kPcUsed, kPcTok0, kPcNtok, kPcHead, kPcHeads, kPcLast };
-constexpr int kPcInts = 8;
-
 // Where pieces lie: those of warps (slot 0 alone has rows here: slot 1, and the
 // last piece of a warp, stay in shared memory) and those of CTAs.
 struct Pieces {
-    int* rec;          // [n][2][kPcInts]
+    int* rec;          // [n][2][kPcInts], of CTAs' pieces
     float2* stats;     // [n][slots][rows] (maximum, sum)
     float* part;       // [n][slots][rows][D]
 };
@@ -468,7 +469,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     volatile uint32_t* masks = reinterpret_cast<volatile uint32_t*>(smem + C::kMasks) + warp * 8;
     constexpr int kKC = 0, kVC = kStepKeys * CB, kKS = 2 * kStepKeys * CB, kVS = kKS + kStepKeys * SB;
     const long long worker = (long long)blockIdx.x * C::kWarps + warp;
-    int* rec = wp.rec + worker * 2 * kPcInts;
+    int* rec = reinterpret_cast<int*>(smem + C::kPieces) + warp * 2 * kPcInts;
     uint8_t* used = smem + C::kRecs + warp * 8;           // [2] used, [2] last
     if (lane < 8) used[lane] = 0;
 
@@ -1043,7 +1044,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         int* r = crec + threadIdx.x * kPcInts;
         r[kPcUsed] = mine;
         if (mine) {
-            const int* p = wp.rec + ((blockIdx.x * (long long)C::kWarps + w) * 2 + threadIdx.x) * kPcInts;
+            const int* p = reinterpret_cast<const int*>(smem + C::kPieces) + (w * 2 + threadIdx.x) * kPcInts;
             r[kPcTok0] = p[kPcTok0];
             r[kPcNtok] = p[kPcNtok];
             r[kPcHead] = p[kPcHead];
@@ -1060,7 +1061,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         unsigned members = led ? go : go & ~((2u << w0) - 1u);
         const unsigned ends = members & end;
         if (ends) members &= ((ends & (0u - ends)) << 1) - 1u;
-        const int* p = wp.rec + ((blockIdx.x * (long long)C::kWarps + w0) * 2 + (led ? 0 : 1)) * kPcInts;
+        const int* p = reinterpret_cast<const int*>(smem + C::kPieces) + (w0 * 2 + (led ? 0 : 1)) * kPcInts;
         const int c_heads = p[kPcHeads];
         if (row >= p[kPcNtok] * c_heads) continue;
         Joined<N> x;
