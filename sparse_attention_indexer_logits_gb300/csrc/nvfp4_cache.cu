@@ -177,6 +177,14 @@ __global__ void __launch_bounds__(kNvAppendThreads, 4) nvfp4_append_kernel(const
         page_of[i] = ok ? page : -1;
         slot_of[i] = slot;
     }
+    uint2 codes[kNvAppendUnits];
+    uint32_t scale[kNvAppendUnits];
+#pragma unroll
+    for (int u = 0; u < kNvAppendUnits; ++u) {
+        const int head = head_of(u);
+        if (u >= a.units || t >= nt || head >= 2 * a.heads) continue;
+        codes[u] = quantise16<FP16>(v[u], head >= a.heads ? a.vc.scale : a.kc.scale, scale[u]);
+    }
     __syncthreads();
     if (t >= nt || page_of[t] < 0) return;
     const long long page = page_of[t];
@@ -188,14 +196,12 @@ __global__ void __launch_bounds__(kNvAppendThreads, 4) nvfp4_append_kernel(const
         const bool is_v = head >= a.heads;
         const NvCache& c = is_v ? a.vc : a.kc;
         const int h = is_v ? head - a.heads : head;
-        uint32_t scale;
-        const uint2 codes = quantise16<FP16>(v[u], c.scale, scale);
-        *reinterpret_cast<uint2*>(c.codes + page * c.page + slot * c.slot + h * c.head + g * 8) = codes;
-        c.scales[page * c.s_page + slot * c.s_slot + h * c.s_head + g] = (uint8_t)scale;
+        *reinterpret_cast<uint2*>(c.codes + page * c.page + slot * c.slot + h * c.head + g * 8) = codes[u];
+        c.scales[page * c.s_page + slot * c.s_slot + h * c.s_head + g] = (uint8_t)scale[u];
     }
 }
 
-constexpr int kReadThreads = 256;
+constexpr int kReadThreads = 256, kReadCtas = 4;
 
 // Blocks of request b that are there.
 __device__ __forceinline__ int blocks_there(const NvReadArgs& a, int b)
@@ -207,7 +213,7 @@ __device__ __forceinline__ int blocks_there(const NvReadArgs& a, int b)
 // cut into one contiguous range per CTA.  A thread turns eight values, four bytes
 // of codes, into sixteen bytes, several rows at a time.
 template <int D, bool FP16>
-__global__ void __launch_bounds__(kReadThreads) nvfp4_read_kernel(const NvReadArgs a)
+__global__ void __launch_bounds__(kReadThreads, kReadCtas) nvfp4_read_kernel(const NvReadArgs a)
 {
     __shared__ int start[2];               // request, block
     __shared__ long long first_left[2];    // strip within the block, strips of the range
@@ -335,7 +341,7 @@ cudaError_t launch_nvfp4_append(const NvAppendArgs& a, cudaStream_t stream)
 
 cudaError_t launch_nvfp4_read(const NvReadArgs& a, int sm_count, cudaStream_t stream)
 {
-    const dim3 grid((unsigned)(sm_count * 8));
+    const dim3 grid((unsigned)(sm_count * kReadCtas));
     if (a.dim == 128)
         return a.fp16 ? launch_dependent(nvfp4_read_kernel<128, true>, grid, kReadThreads, 0, stream, a)
                       : launch_dependent(nvfp4_read_kernel<128, false>, grid, kReadThreads, 0, stream, a);
