@@ -211,10 +211,6 @@ int pml_append_nvfp4(const void* k, int64_t k_token_stride, int64_t k_head_strid
     a.tokens = tokens;
     a.heads = kv_heads;
     a.dim = head_dim;
-    // fewer groups a thread where more would leave SMs without work
-    const long long groups = 2LL * tokens * kv_heads * (head_dim / kNvGroup);
-    a.units = kNvAppendUnits;
-    while (a.units > 1 && groups < (long long)a.units * kNvAppendThreads * 2 * dev.sm_count) --a.units;
     e = launch_nvfp4_append(a, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PML_OK : cuda_fail(e);
 }

@@ -13,6 +13,16 @@
 // has at most six significant bits: exact in both types within their range.
 //
 // Both are bound by memory: 2 bytes of a value on one side, 9/16 on the other.
+// Measured (a copy reaches 6794 GB/s; inputs that are not in L2):
+//   7 contexts of 9000 .. 32768 keys read, 4 heads of 64, bf16
+//       29.6 us, 138 MB: 69 % of the copy; about 5 us of it are a launch and the
+//       lookups before the first codes.  (A strip's codes loaded while the one
+//       before is turned: no faster; three CTAs an SM 30.9, five 30.1; stores that
+//       stay in L2 30.7 against 26.9 where the pages read are there)
+//   8190 tokens written, 8 heads of 128, fp16, and their contexts read
+//       22.0 us, 86 MB in two launches: a floor of 12.7
+//   64 tokens written and contexts of up to 160 read: 11.7 us, a floor of 3.9: two
+//       launches, each a chain of three loads
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -136,69 +146,41 @@ __device__ __forceinline__ uint2 quantise16(const uint4 (&v)[2], float g, uint32
 }
 
 // A thread takes a group of sixteen, eight (four) threads a row; a CTA sixteen
-// tokens and a few of their rows (k's heads, then v's).  Neighbouring rows of
+// tokens and two (four) of their rows (k's heads, then v's).  Neighbouring rows of
 // threads are neighbouring tokens of one head: what a warp writes is 256 bytes
 // of codes and a whole sector of scales in a page that holds its heads one after
-// another.  The rows are on their way while the tokens' slots are looked up.
+// another.  Every thread looks up its token's slot, while its values are on their
+// way.  (Four groups a thread, a token's slot looked up once and shared: 25.8 us
+// for a chunk of 8190 tokens written and read back, 23.5 with the lookup beside the
+// quantising, 22.0 so: the full number of threads an SM, and no barrier.)
 template <int D, bool FP16>
-__global__ void __launch_bounds__(kNvAppendThreads, 4) nvfp4_append_kernel(const NvAppendArgs a)
+__global__ void __launch_bounds__(kNvAppendThreads, 8) nvfp4_append_kernel(const NvAppendArgs a)
 {
     constexpr int kLanes = D / kNvGroup;
-    constexpr int kRows = kNvAppendThreads / kLanes;       // (token, head) rows of a unit
-    __shared__ long long page_of[kNvAppendTokens];         // -1: nothing is written
-    __shared__ int slot_of[kNvAppendTokens];
     allow_dependent_launch();
     grid_dependency_wait();
-    const long long token0 = (long long)blockIdx.x * kNvAppendTokens;
-    const int nt = (int)min((long long)kNvAppendTokens, a.tokens - token0);
-    const int head0 = blockIdx.y * a.units * (kRows / kNvAppendTokens);
-    const int g = threadIdx.x % kLanes, i0 = threadIdx.x / kLanes;
-    const int t = i0 % kNvAppendTokens;
-    uint4 v[kNvAppendUnits][2];
-    auto head_of = [&](int u) { return head0 + u * (kRows / kNvAppendTokens) + i0 / kNvAppendTokens; };
-#pragma unroll
-    for (int u = 0; u < kNvAppendUnits; ++u) {
-        const int head = head_of(u);
-        if (u >= a.units || t >= nt || head >= 2 * a.heads) continue;
-        const bool is_v = head >= a.heads;
-        const int h = is_v ? head - a.heads : head;
-        const long long at = is_v ? (token0 + t) * a.v_token + h * a.v_head : (token0 + t) * a.k_token + h * a.k_head;
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(is_v ? a.v : a.k) + at) + 2 * g;
-        v[u][0] = __ldg(src);
-        v[u][1] = __ldg(src + 1);
-    }
-    if (const int i = threadIdx.x; i < nt) {
-        const long long pos = a.pos64 ? __ldg(static_cast<const long long*>(a.positions) + token0 + i)
-                                      : (long long)__ldg(static_cast<const int32_t*>(a.positions) + token0 + i);
-        bool pad;
-        long long page;
-        int slot;
-        const bool ok = find_slot(a.slot, token0 + i, pos, pad, page, slot);
-        page_of[i] = ok ? page : -1;
-        slot_of[i] = slot;
-    }
-    uint2 codes[kNvAppendUnits];
-    uint32_t scale[kNvAppendUnits];
-#pragma unroll
-    for (int u = 0; u < kNvAppendUnits; ++u) {
-        const int head = head_of(u);
-        if (u >= a.units || t >= nt || head >= 2 * a.heads) continue;
-        codes[u] = quantise16<FP16>(v[u], head >= a.heads ? a.vc.scale : a.kc.scale, scale[u]);
-    }
-    __syncthreads();
-    if (t >= nt || page_of[t] < 0) return;
-    const long long page = page_of[t];
-    const int slot = slot_of[t];
-#pragma unroll
-    for (int u = 0; u < kNvAppendUnits; ++u) {
-        const int head = head_of(u);
-        if (u >= a.units || head >= 2 * a.heads) continue;
-        const bool is_v = head >= a.heads;
-        const NvCache& c = is_v ? a.vc : a.kc;
-        const int h = is_v ? head - a.heads : head;
-        *reinterpret_cast<uint2*>(c.codes + page * c.page + slot * c.slot + h * c.head + g * 8) = codes[u];
-        c.scales[page * c.s_page + slot * c.s_slot + h * c.s_head + g] = (uint8_t)scale[u];
-    }
+    const int i = threadIdx.x / kLanes, g = threadIdx.x % kLanes;
+    const long long token = (long long)blockIdx.x * kNvAppendTokens + i % kNvAppendTokens;
+    const int head = blockIdx.y * (kNvAppendThreads / kLanes / kNvAppendTokens) + i / kNvAppendTokens;
+    if (token >= a.tokens || head >= 2 * a.heads) return;
+    const bool is_v = head >= a.heads;
+    const int h = is_v ? head - a.heads : head;
+    const uint16_t* row = is_v ? static_cast<const uint16_t*>(a.v) + token * a.v_token + h * a.v_head
+                               : static_cast<const uint16_t*>(a.k) + token * a.k_token + h * a.k_head;
+    const uint4* src = reinterpret_cast<const uint4*>(row) + 2 * g;
+    const uint4 v[2] = {__ldg(src), __ldg(src + 1)};
+    const long long pos = a.pos64 ? __ldg(static_cast<const long long*>(a.positions) + token)
+                                  : (long long)__ldg(static_cast<const int32_t*>(a.positions) + token);
+    bool pad;
+    long long page;
+    int slot;
+    const bool ok = find_slot(a.slot, token, pos, pad, page, slot);
+    const NvCache& c = is_v ? a.vc : a.kc;
+    uint32_t scale;
+    const uint2 codes = quantise16<FP16>(v, c.scale, scale);
+    if (!ok) return;
+    *reinterpret_cast<uint2*>(c.codes + page * c.page + slot * c.slot + h * c.head + g * 8) = codes;
+    c.scales[page * c.s_page + slot * c.s_slot + h * c.s_head + g] = (uint8_t)scale;
 }
 
 constexpr int kReadThreads = 256, kReadCtas = 4;
@@ -329,7 +311,7 @@ __global__ void __launch_bounds__(kReadThreads, kReadCtas) nvfp4_read_kernel(con
 
 cudaError_t launch_nvfp4_append(const NvAppendArgs& a, cudaStream_t stream)
 {
-    const int heads_per_cta = a.units * (kNvAppendThreads / (a.dim / kNvGroup) / kNvAppendTokens);
+    const int heads_per_cta = kNvAppendThreads / (a.dim / kNvGroup) / kNvAppendTokens;
     const dim3 grid((unsigned)((a.tokens + kNvAppendTokens - 1) / kNvAppendTokens),
                     (unsigned)((2 * a.heads + heads_per_cta - 1) / heads_per_cta));
     if (a.dim == 128)

@@ -22,11 +22,9 @@ struct NvAppendArgs {
     int tokens;
     int heads;
     int dim;
-    int units;                     // groups of a thread, at most kNvAppendUnits
 };
 
 constexpr int kNvAppendThreads = 256;
-constexpr int kNvAppendUnits = 4;
 constexpr int kNvAppendTokens = 16;    // of a CTA
 
 struct NvReadArgs {
