@@ -18,8 +18,8 @@ constexpr int kMaxHeads = 8192;
 constexpr int kMaxScaleExponent = 32;
 // Rows ((token, head) pairs of a kv head) of a request up to which its attention
 // is left to warps alone.  128 request-heads of 8500 keys, heads of 128: 48 rows
-// take 123 us that way and 139 by tiles, 64 rows 157 and 141, 256 rows 568 and
-// 187.
+// take 123 us that way and 124 by tiles, 64 rows 157 and 125, 256 rows 568 and
+// 145.
 constexpr int kNvWarpRows = 48;
 // Lists are, whatever the rows, while a warp has no more than so many steps: 64
 // heads over 1, 64 tokens of 64 positions 9.2 us that way and 13.9 by tiles, of 500
@@ -129,14 +129,25 @@ int attention_call(NvAttnArgs& a, const void* q, int64_t q_token, int64_t q_head
         w.window = a.window;
         w.scale = scale;
         w.scale_log2 = scale * 1.4426950408889634f;
-        CUtensorMap qmap;
+        CUtensorMap qmap, kmap, vmap;
         const uint64_t dims[3] = {(uint64_t)head_dim, (uint64_t)num_heads, (uint64_t)tokens};
         const uint64_t strides[2] = {(uint64_t)qs[0] * 2, (uint64_t)qs[1] * 2};
         const uint32_t box[3] = {64, (uint32_t)group, (uint32_t)w.half_tokens};
         e = encode_tiled(qmap, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, dims,
                          strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
         if (e != cudaSuccess) return cuda_fail(e);
-        e = launch_paged_attention_nvfp4(head_dim, fp16, a.selected != nullptr, qmap, w, dev.sm_count,
+        kmap = vmap = qmap;
+        for (int i = 0; i < 2 && !a.selected && head_dim == 128; ++i) {      // the codes of a page's head
+            const NvCache& c = i ? a.vc : a.kc;
+            const uint64_t bytes = head_dim / 2;
+            const uint64_t cdims[4] = {bytes, (uint64_t)kBlockKeys, (uint64_t)kv_heads, (uint64_t)num_pages};
+            const uint64_t cstrides[3] = {(uint64_t)c.slot, (uint64_t)c.head, (uint64_t)c.page};
+            const uint32_t cbox[4] = {(uint32_t)bytes, (uint32_t)kBlockKeys, 1, 1};
+            e = encode_tiled(i ? vmap : kmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, c.codes, cdims, cstrides, cbox,
+                             CU_TENSOR_MAP_SWIZZLE_64B);
+            if (e != cudaSuccess) return cuda_fail(e);
+        }
+        e = launch_paged_attention_nvfp4(head_dim, fp16, a.selected != nullptr, qmap, kmap, vmap, w, dev.sm_count,
                                          static_cast<cudaStream_t>(stream));
         return e == cudaSuccess ? PML_OK : cuda_fail(e);
     }

@@ -9,8 +9,8 @@ cudaError_t launch_attention_d64(bool, bool, const CUtensorMap&, const CUtensorM
 cudaError_t launch_attention_d128(bool, bool, const CUtensorMap&, const CUtensorMap&,
                                   const CUtensorMap&, const AttnArgs&, int, cudaStream_t);
 
-cudaError_t launch_attention_nvfp4_d64(bool, bool, const CUtensorMap&, const AttnArgs&, int, cudaStream_t);
-cudaError_t launch_attention_nvfp4_d128(bool, bool, const CUtensorMap&, const AttnArgs&, int, cudaStream_t);
+cudaError_t launch_attention_nvfp4_d64(bool, bool, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const AttnArgs&, int, cudaStream_t);
+cudaError_t launch_attention_nvfp4_d128(bool, bool, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const AttnArgs&, int, cudaStream_t);
 
 namespace {
 
@@ -207,10 +207,12 @@ cudaError_t launch_paged_attention(int head_dim, bool fp16, bool select, const C
 }
 
 cudaError_t launch_paged_attention_nvfp4(int head_dim, bool fp16, bool select, const CUtensorMap& qmap,
-                                         const AttnArgs& a, int num_ctas, cudaStream_t stream)
+                                         const CUtensorMap& kmap, const CUtensorMap& vmap, const AttnArgs& a,
+                                         int num_ctas, cudaStream_t stream)
 {
-    const cudaError_t e = head_dim == 128 ? launch_attention_nvfp4_d128(fp16, select, qmap, a, num_ctas, stream)
-                                          : launch_attention_nvfp4_d64(fp16, select, qmap, a, num_ctas, stream);
+    const cudaError_t e = head_dim == 128
+                              ? launch_attention_nvfp4_d128(fp16, select, qmap, kmap, vmap, a, num_ctas, stream)
+                              : launch_attention_nvfp4_d64(fp16, select, qmap, kmap, vmap, a, num_ctas, stream);
     if (e != cudaSuccess) return e;
     return head_dim == 128 ? join<128>(fp16, true, a, num_ctas, stream) : join<64>(fp16, true, a, num_ctas, stream);
 }

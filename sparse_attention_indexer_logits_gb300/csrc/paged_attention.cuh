@@ -68,11 +68,13 @@
 // the stage's tile; nothing else changes but Q, which the softmax groups turn to
 // fp16 (bf16 tiles take twice the conversions: 290 us against 159).
 //   16 requests x 8 kv heads of 128 over 8500 keys each
-//       64 rows of q to a head 141 us, 128 145, 256 187; 21 for the bytes alone.
-//       Bound by the two warps that turn codes: 81 us without that, 69 without
-//       the copies too.  (Six warps, of a block of 512 threads: the softmax has
-//       fewer registers and reads its scores twice; 64 rows 134, 256 rows 218.
-//       Codes held in registers ahead of the stage: spills, 391)
+//       64 rows of q to a head 125 us, 128 129, 256 145; 21 for the bytes alone.
+//       Bound by the two warps that turn codes, 1900 cycles for a half tile of K
+//       or V: 1000 to turn it, 450 to ask for the one after next, 200 of waits;
+//       69 us without all that.  (Six warps, of a block of 512 threads: the
+//       softmax has fewer registers and reads its scores twice; 64 rows 134, 256
+//       rows 218 when two warps took 141 and 187.  The next rows' codes held in
+//       registers: spills, 134 and 151)
 //   48 requests of 0 .. 40 tokens over up to 8000 keys, 20 / 4 heads of 64, a
 //   window of 1500, fp16: 41 us, bound as the 16-bit pages' mixed batch is
 //   4096 tokens that end 32768 keys, 32 heads over 4: 2270 us, against 1500
@@ -215,8 +217,8 @@ struct Cfg {
     static constexpr int kBars = kFactors + (FP4 ? 2 * 128 * 4 : 0);
     // barriers: full, empty per stage; q full, q empty per half; s full, pv done, group
     // sync per half; o empty, alt sync; item full, item empty; the issuer's
-    // last commit; 4 bits: q turned per half
-    static constexpr int kNumBars = 2 * kStages + 4 + 6 + 2 + 2 * kItemSlots + 1 + (FP4 ? 2 : 0);
+    // last commit; 4 bits: q turned per half, codes there per raw tile of each warp
+    static constexpr int kNumBars = 2 * kStages + 4 + 6 + 2 + 2 * kItemSlots + 1 + (FP4 ? 2 + 2 * kRawTiles : 0);
     static constexpr int kItems = (kBars + kNumBars * 8 + 15) / 16 * 16;
     static constexpr int kMisc = kItems + kItemSlots * kItemInts * 4;
     static constexpr int kTotal = kMisc + 192;
@@ -456,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sfull0 = qempty0 + 16u, pvdone0 = sfull0 + 16u,
                    group0 = pvdone0 + 16u, oempty = group0 + 16u, altbar = oempty + 8u,
                    itfull0 = altbar + 8u, itempty0 = itfull0 + 8u * kItemSlots, drain = itempty0 + 8u * kItemSlots,
-                   qready0 = drain + 8u;
+                   qready0 = drain + 8u, rawfull0 = qready0 + 16u;
     int* items = reinterpret_cast<int*>(smem + C::kItems);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMisc + 4);
@@ -483,6 +485,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(empty_bar(s), 1);
         }
         mbar_init(drain, 1);
+        if (FP4)
+            for (int i = 0; i < 2 * C::kRawTiles; ++i) mbar_init(rawfull0 + 8u * i, 1);
         for (int h = 0; h < 2; ++h) {
             mbar_init(qfull0 + 8u * h, 1);
             mbar_init(qempty0 + 8u * h, 1);
@@ -500,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_mbar_init();
         tma_prefetch_map(&qmap);
-        if (!SEL && !FP4) {
+        if (!SEL) {
             tma_prefetch_map(&kmap);
             tma_prefetch_map(&vmap);
         }
@@ -554,6 +558,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int handed = 0;              // selected: those whose copies are complete
         int item = 0;
         uint32_t qcount = 0;         // Q halves filled so far
+        uint32_t raw_put = 0, raw_got = 0;       // 4 bits: this warp's raw tiles asked for and taken
+        const uint32_t raw_bar = rawfull0 + (lead ? 0u : 8u * C::kRawTiles);
         bool ok = true;
         int tok0 = 0, nq = 0, kv = 0, tiles = 0, cur_b = -1;
         auto next_item = [&]() {
@@ -660,15 +666,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int ahead = alt ? 2 : 1;
             if constexpr (FP4) {
                 // Codes to fp16 tiles: each of the two warps has half of a tile's
-                // rows.  It copies them as they are (cp.async, two tiles ahead)
-                // into its own memory; then a lane takes sixteen bytes of a row
-                // (eight lanes side by side the same bytes of eight rows, whose
-                // chunks the swizzle puts into different banks) and turns them
-                // into 64 in the stage.
+                // rows, whose codes and scales it copies as they are, two tiles
+                // ahead, into its own memory; then a lane takes sixteen bytes of
+                // a row (eight lanes side by side the same bytes of eight rows,
+                // whose chunks the swizzle puts into different banks) and turns
+                // them into 64 in the stage.  Rows that no row of the item may
+                // see have scales of zero.  Pages' codes come by TMA where rows
+                // are of 64 bytes (64 rows of q: 125 us against 135 with eight
+                // copies a lane); of 32 bytes it takes as long as the copies, and
+                // longer with 256 rows (131 against 122).
                 constexpr int CB = D / 2, SB = D / kNvGroup, kRowLanes = CB / 16, kInst = 32 / kRowLanes,
                               kIter = 64 / kInst;
+                constexpr bool kByTma = !SEL && D == 128;
                 const int r_in = (lane & 7) + 8 * (lane / (8 * kRowLanes)), chunk = (lane >> 3) % kRowLanes;
-                // (where a row's chunk lies: the same chunk of eight rows in eight places)
+                // (where a row's chunk lies: the same chunk of eight rows in eight places,
+                // which is TMA's 64-byte swizzle for rows of 64)
                 const int place = (D == 128 ? chunk ^ ((lane >> 1) & 3) : chunk ^ ((lane >> 2) & 1)) * 16;
                 const int row0 = lead ? 0 : 64;
                 const uint32_t raw0 = base + C::kRaw + (lead ? 0 : C::kRawTiles * C::kRawBytes);
@@ -702,17 +714,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                     g0 = pages(p0);
                     g1 = pages(p1);
                 }
-                int nk = 0, nv = 0, put = 0;
+                int nk = 0, nv = 0;
+                // dense: a tile's codes and scales from a page, K or V
+                const long long row_k = head * a.kc4.s_head + lane * a.kc4.s_slot,
+                                row_v = head * a.vc4.s_head + lane * a.vc4.s_slot,
+                                code_k = head * a.kc4.head + r_in * a.kc4.slot + chunk * 16,
+                                code_v = head * a.vc4.head + r_in * a.vc4.slot + chunk * 16;
+                auto copy_page = [&](const NvCache& c, const CUtensorMap* map, long long row, long long code, int tile_at, int page) {
+                    const uint32_t slot = raw_put % C::kRawTiles, to = raw0 + slot * C::kRawBytes;
+                    if constexpr (kByTma) {
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(raw_bar + 8u * slot, 64 * CB);
+                            tma_load_4d(to, map, raw_bar + 8u * slot, 0, 0, head, page);
+                        }
+                    } else {
+                        const uint8_t* from = c.codes + page * c.page + code;
+#pragma unroll
+                        for (int i = 0; i < kIter; ++i) {
+                            cp_async16(to + (i * kInst + r_in) * CB + place, from, 16u);
+                            from += kInst * c.slot;
+                        }
+                    }
+                    // the page's rows that some row of the item may see
+                    const int first_key = (j0 + tile_at) * kAttnTileKeys + row0;
+                    const int lo = sp.lo - first_key, hi = sp.hi - first_key;
+                    uint32_t bytes0 = SB, bytes1 = SB;
+                    if (lo > 0 || hi < 64) {
+                        bytes0 = lane >= lo && lane < hi ? SB : 0;
+                        bytes1 = lane + 32 >= lo && lane + 32 < hi ? SB : 0;
+                    }
+                    const uint8_t* src = c.scales + page * c.s_page + row;
+                    cp_async_small<SB>(to + 64 * CB + lane * SB, src, bytes0);
+                    cp_async_small<SB>(to + 64 * CB + (lane + 32) * SB, src + 32 * c.s_slot, bytes1);
+                };
                 // Copies the next tile in order, K `ahead` tiles before V; nothing
                 // when none is left.
                 auto copy = [&]() {
                     if (nv < n) {
                         const bool is_k = nk < n && nk - nv < ahead;
-                        const NvCache& c = is_k ? a.kc4 : a.vc4;
-                        const uint8_t* src = c.codes + head * c.head + chunk * 16;
-                        const uint8_t* ssrc = c.scales + head * c.s_head;
-                        const uint32_t to = raw0 + put * C::kRawBytes;
                         if constexpr (SEL) {
+                            const NvCache& c = is_k ? a.kc4 : a.vc4;
+                            const uint8_t* ssrc = c.scales + head * c.s_head;
+                            const uint32_t to = raw0 + raw_put % C::kRawTiles * C::kRawBytes;
                             int2 p = vp0, g = vg0;
                             if (is_k) {
                                 p = p0;
@@ -727,6 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 vp0 = vp1; vg0 = vg1;
                                 ++nv;
                             }
+                            const uint8_t* src = c.codes + head * c.head + chunk * 16;
                             const long long at[2] = {p.x < 0 ? -1 : g.x * c.page + (p.x & 63) * c.slot,
                                                      p.y < 0 ? -1 : g.y * c.page + (p.y & 63) * c.slot};
 #pragma unroll
@@ -738,85 +782,82 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                p.x < 0 ? 0u : SB);
                             cp_async_small<SB>(to + 64 * CB + (lane + 32) * SB, ssrc + g.y * c.s_page + (p.y & 63) * c.s_slot,
                                                p.y < 0 ? 0u : SB);
+                        } else if (is_k) {
+                            const int pg = 2 * (j0 + nk) + (lead ? 0 : 1);
+                            if (win < 0 || pg >= win + 32) {
+                                win = pg;
+                                entry = pg + lane >= page_begin && pg + lane < page_end
+                                            ? checked(__ldg(table + pg + lane)) : 0;
+                            }
+                            const int page = __shfl_sync(0xffffffffu, entry, pg - win);
+                            if (nk == nv) pg0 = page;
+                            else pg1 = page;
+                            copy_page(a.kc4, &kmap, row_k, code_k, nk, page);
+                            ++nk;
                         } else {
-                            int page = pg0, tile_at = nv;
-                            if (is_k) {
-                                const int pg = 2 * (j0 + nk) + (lead ? 0 : 1);
-                                if (win < 0 || pg >= win + 32) {
-                                    win = pg;
-                                    entry = pg + lane >= page_begin && pg + lane < page_end
-                                                ? checked(__ldg(table + pg + lane)) : 0;
-                                }
-                                page = __shfl_sync(0xffffffffu, entry, pg - win);
-                                if (nk == nv) pg0 = page;
-                                else pg1 = page;
-                                tile_at = nk++;
-                            } else {
-                                pg0 = pg1;
-                                ++nv;
-                            }
-                            // the page's rows that some row of the item may see
-                            const int first_key = (j0 + tile_at) * kAttnTileKeys + row0;
-                            auto there = [&](int r, uint32_t bytes) {
-                                return r >= sp.lo - first_key && r < sp.hi - first_key ? bytes : 0u;
-                            };
-                            src += page * c.page + r_in * c.slot;
-                            ssrc += page * c.s_page + lane * c.s_slot;
-#pragma unroll
-                            for (int i = 0; i < kIter; ++i) {
-                                cp_async16(to + (i * kInst + r_in) * CB + place, src, there(i * kInst + r_in, 16u));
-                                src += kInst * c.slot;
-                            }
-                            cp_async_small<SB>(to + 64 * CB + lane * SB, ssrc, there(lane, SB));
-                            cp_async_small<SB>(to + 64 * CB + (lane + 32) * SB, ssrc + 32 * c.s_slot, there(lane + 32, SB));
+                            copy_page(a.vc4, &vmap, row_v, code_v, nv, pg0);
+                            pg0 = pg1;
+                            ++nv;
                         }
-                        if (++put == C::kRawTiles) put = 0;
+                        ++raw_put;
                     }
                     cp_async_commit();
                 };
 #pragma unroll 1
-                for (int i = 0; i < C::kRawTiles - 1; ++i) copy();
-                int got = 0;
-#pragma unroll 1
-                for (int tile_op = 0; tile_op < 2 * n && ok; ++tile_op) {
-                    const int st = pos % S;
+                for (int tile_op = 1 - C::kRawTiles; tile_op < 2 * n && ok; ++tile_op) {
                     copy();
+                    if (tile_op < 0) continue;
+                    const int st = pos % S;
                     cp_async_wait<C::kRawTiles - 1>();
                     __syncwarp();
-                    ok = warp_wait(empty_bar(st), (uint32_t)((pos / S) & 1) ^ 1u, abort_flag, a.status);
+                    const uint32_t slot = raw_got % C::kRawTiles, raw = raw0 + slot * C::kRawBytes;
+                    const uint32_t raw_parity = (raw_got / C::kRawTiles) & 1u, parity = ((pos / S) & 1) ^ 1u;
+                    if constexpr (SEL) {
+                        ok = warp_wait(empty_bar(st), parity, abort_flag, a.status);
+                    } else {                      // (mostly both are: one vote)
+                        const bool raw_there = !kByTma || mbar_try_wait(raw_bar + 8u * slot, raw_parity);
+                        ok = __all_sync(0xffffffffu, mbar_try_wait(empty_bar(st), parity) && raw_there) ||
+                             ((!kByTma || warp_wait(raw_bar + 8u * slot, raw_parity, abort_flag, a.status)) &&
+                              warp_wait(empty_bar(st), parity, abort_flag, a.status));
+                    }
                     if (!ok) break;
-                    const uint32_t raw = raw0 + got * C::kRawBytes;
-                    if (++got == C::kRawTiles) got = 0;
+                    ++raw_got;
                     const uint32_t dst = base + C::kRing + st * C::kStageBytes + (chunk >> 1) * C::kBlockBytes +
                                          (row0 + r_in) * 128;
-                    // (loads before the first store: nothing tells the compiler that
-                    // they lie apart)
+                    // (a short loop: the softmax's long straight code on the same
+                    // scheduler leaves few instructions where they can be had at
+                    // once.  Unrolled 140 us with 64 rows of q, 179 with 256; two
+                    // rows at a time 125 and 145, one 154 and 172)
+                    constexpr int kRows = 2;
+#pragma unroll 1
+                    for (int i0 = 0; i0 < kIter; i0 += kRows) {
+                        uint32_t w[kRows][4], m[kRows][2];
+                        uint32_t s2[kRows];
 #pragma unroll
-                    for (int i0 = 0; i0 < kIter; i0 += 4) {
-                        uint4 v[4];
-                        uint32_t s2[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < kRows; ++i) {      // (loads before the first store, which might alias)
                             const int r = (i0 + i) * kInst + r_in;
-                            v[i] = ld_shared_v4(raw + r * CB + place);
+                            const uint4 v = ld_shared_v4(raw + r * CB + place);
+                            w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
                             s2[i] = ld_shared_u16(raw + 64 * CB + r * SB + chunk * 2);
                         }
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                        for (int i = 0; i < kRows; ++i) {
                             uint32_t m2;
                             asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(m2) : "h"((uint16_t)s2[i]));
-                            const uint32_t m[2] = {__byte_perm(m2, m2, 0x1010), __byte_perm(m2, m2, 0x3232)};
+                            m[i][0] = __byte_perm(m2, m2, 0x1010);
+                            m[i][1] = __byte_perm(m2, m2, 0x3232);
+                        }
+#pragma unroll
+                        for (int i = 0; i < kRows; ++i)
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
                                 uint32_t x[4];
-                                e2m1x8_to_f16x2x4(w[q], x);
+                                e2m1x8_to_f16x2x4(w[i][q], x);
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) x[e] = mul_f16x2(x[e], m[q >> 1]);
+                                for (int e = 0; e < 4; ++e) x[e] = mul_f16x2(x[e], m[i][q >> 1]);
                                 st_shared_v4(dst + (i0 + i) * kInst * 128 +
                                                  ((((chunk & 1) * 4 + q) ^ (lane & 7)) << 4), x[0], x[1], x[2], x[3]);
                             }
-                        }
                     }
                     fence_proxy_async_smem();     // the tensor core reads what this lane has written
                     __syncwarp();                 // (and the codes' place is free)
@@ -992,6 +1033,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(full_bar(handed % S));
             }
         }
+        if constexpr (FP4 && !SEL && D == 128)              // copies in flight land before the CTA may leave
+            for (; raw_got < raw_put; ++raw_got)
+                mbar_wait_drain<false>(raw_bar + 8u * (raw_got % C::kRawTiles), (raw_got / C::kRawTiles) & 1u);
         if (lead) {
             if (ok) {
                 const int is = item % kItemSlots;

@@ -225,7 +225,8 @@ cudaError_t launch_paged_attention(int head_dim, bool fp16, bool select, const C
 
 // The same over a.kc4 and a.vc4.
 cudaError_t launch_paged_attention_nvfp4(int head_dim, bool fp16, bool select, const CUtensorMap& qmap,
-                                         const AttnArgs& a, int num_ctas, cudaStream_t stream);
+                                         const CUtensorMap& kmap, const CUtensorMap& vmap, const AttnArgs& a,
+                                         int num_ctas, cudaStream_t stream);
 
 cudaError_t launch_pages_fork(const ForkArgs& a, cudaStream_t stream);
 cudaError_t launch_pages_extend(const ExtendArgs& a, cudaStream_t stream);
