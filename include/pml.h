@@ -620,9 +620,9 @@ int pml_read_nvfp4(const pml_nvfp4_cache* k_cache, const pml_nvfp4_cache* v_cach
  * softmax_scale * k_cache->scale is in 1e-30 .. 1e30 (else
  * PML_ERR_INVALID_ARG); a row of q that is not finite, or whose scores fp32
  * does not hold, gives a row without meaning.
- * Up to 48 rows of q to a kv head (tokens of a request, on average, times
- * num_heads / kv_heads) are taken warp by warp, more in tiles of 128, with
- * different roundings.
+ * Up to 32 rows of q to a kv head (tokens of a request, on average, times
+ * num_heads / kv_heads), or 127 in all, are taken warp by warp, more in tiles of
+ * 128, with different roundings.
  */
 int pml_paged_attention_nvfp4(const void* q, int64_t q_token_stride, int64_t q_head_stride, int dtype,
                               const pml_nvfp4_cache* k_cache, const pml_nvfp4_cache* v_cache,

@@ -17,13 +17,18 @@ constexpr int kMaxListed = 0x7fffff00; // entries of a list, so that their tiles
 constexpr int kMaxHeads = 8192;
 constexpr int kMaxScaleExponent = 32;
 // Rows ((token, head) pairs of a kv head) of a request up to which its attention
-// is left to warps alone.  128 request-heads of 8500 keys, heads of 128: 48 rows
-// take 123 us that way and 124 by tiles, 64 rows 157 and 125, 256 rows 568 and
-// 145.
-constexpr int kNvWarpRows = 48;
+// is left to warps alone.  128 request-heads of 8500 keys, heads of 128 (64): 32
+// rows take 91 (61) us that way and 108 (76) by tiles, 40 rows 127 (84) and 107
+// (77), 64 rows 162 (106) and 107 (77), 256 rows 568 and 145.
+constexpr int kNvWarpRows = 32;
+// So is a call of fewer rows in all, of which a warp has no more than a step or
+// two: one request-head of 40 or 64 rows 21 us that way and 31 by tiles, 4 of them
+// 23 and 26, 16 of 40 rows 32 and 28.
+constexpr int kNvTileRows = 128;
 // Lists are, whatever the rows, while a warp has no more than so many steps: 64
 // heads over 1, 64 tokens of 64 positions 9.2 us that way and 13.9 by tiles, of 500
-// 17.9 and 20.8, of 2048 34.3 and 34.9; 200 tokens of 2048 132 and 83.
+// 17.7 and 20.3, of 1500 28.8 and 30.1, of 2048 34.4 and 32.7; 200 tokens of 2048
+// 132 and 83.
 constexpr int kNvWarpSteps = 8;
 
 // Strides of a dimension of one element are never used: any valid one will do.
@@ -96,6 +101,7 @@ int attention_call(NvAttnArgs& a, const void* q, int64_t q_token, int64_t q_head
     const bool fp16 = dtype == PML_DTYPE_FLOAT16;
     const long long per_request = a.selected ? 1 : (tokens + a.batch - 1) / a.batch;
     bool by_tiles = per_request * group > kNvWarpRows && group <= kAttnHalfRows;
+    if (by_tiles && !a.selected) by_tiles = per_request * a.batch * num_heads >= kNvTileRows;
     if (by_tiles && a.selected)
         by_tiles = nvfp4_list_steps(a.sel_k, group, (long long)tokens * kv_heads) > (long long)kNvWarpSteps * nvfp4_list_warps(dev.sm_count);
     if (by_tiles) {
@@ -137,14 +143,14 @@ int attention_call(NvAttnArgs& a, const void* q, int64_t q_token, int64_t q_head
                          strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
         if (e != cudaSuccess) return cuda_fail(e);
         kmap = vmap = qmap;
-        for (int i = 0; i < 2 && !a.selected && head_dim == 128; ++i) {      // the codes of a page's head
+        for (int i = 0; i < 2 && !a.selected; ++i) {      // the codes of a page's head
             const NvCache& c = i ? a.vc : a.kc;
             const uint64_t bytes = head_dim / 2;
             const uint64_t cdims[4] = {bytes, (uint64_t)kBlockKeys, (uint64_t)kv_heads, (uint64_t)num_pages};
             const uint64_t cstrides[3] = {(uint64_t)c.slot, (uint64_t)c.head, (uint64_t)c.page};
             const uint32_t cbox[4] = {(uint32_t)bytes, (uint32_t)kBlockKeys, 1, 1};
             e = encode_tiled(i ? vmap : kmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, c.codes, cdims, cstrides, cbox,
-                             CU_TENSOR_MAP_SWIZZLE_64B);
+                             head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B);
             if (e != cudaSuccess) return cuda_fail(e);
         }
         e = launch_paged_attention_nvfp4(head_dim, fp16, a.selected != nullptr, qmap, kmap, vmap, w, dev.sm_count,

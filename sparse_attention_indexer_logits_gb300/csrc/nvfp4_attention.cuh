@@ -52,14 +52,14 @@
 //       instructions issued in 66 % of the cycles, the ALU busy in 54 %, HBM
 //       5.2 TB/s.  (Q as A 370 us; with spilled registers 310)
 //   16 requests x 8 kv heads over 8500 keys each, 8 rows of q to a head 44 us, 16
-//       rows 54, 24 and 32 rows 88, 48 rows 123 (21 for the bytes alone).  With 16
+//       rows 54, 24 and 32 rows 90 (21 for the bytes alone).  With 16
 //       rows a scheduler has three warps, issues in 46 % of the cycles, and its
 //       matrix unit is as busy: latencies within a step, which more warps (of 128
 //       registers: spills) or items of 32 rows (255 registers, two warps a
-//       scheduler: 88 -> 91, 48 rows 123 -> 158) do not shorten
+//       scheduler: 88 -> 91) do not shorten
 //   31 requests of 4 tokens over up to 16000 keys, 28 / 4 heads: 85 us, a floor of
 //       21, two items of 14 rows to a key.  (Fourteen warps: 114)
-//   64 tokens x 2048 listed positions, 64 heads over 1: 34 us, a floor of 3; nine
+//   64 tokens x 500 listed positions, 64 heads over 1: 17.7 us, a floor of 0.8; two
 //       steps a warp after a fixed part of 10 us
 //   one token, 4000 keys, 32 heads over 8
 //       15 us: a launch, where a range begins 2, first copies and Q 3, joined in

@@ -63,23 +63,27 @@
 //       offset to shuffle for every copy)
 //
 // Pages held in 4 bits (FP4): for calls of many rows to a kv head, where a key's
-// codes are turned into fp16 once for up to 256 rows.  The load and the gather
-// warp copy codes and scales as they are, two tiles ahead, and turn them into
-// the stage's tile; nothing else changes but Q, which the softmax groups turn to
-// fp16 (bf16 tiles take twice the conversions: 290 us against 159).
+// codes are turned into fp16 once for up to 256 rows.  One warp copies codes and
+// scales as they are, two tiles ahead (listed rows: the two warps below, each its
+// own); two warps turn half of a tile's rows each into the stage's tile, and say
+// so in a word each, so that nobody has to count what has landed.  The rest is as
+// for 16 bits, but Q, which the softmax groups turn to fp16 (bf16 tiles take twice
+// the conversions: 290 us against 159).
 //   16 requests x 8 kv heads of 128 over 8500 keys each
-//       64 rows of q to a head 125 us, 128 129, 256 145; 21 for the bytes alone.
-//       Bound by the two warps that turn codes, 1900 cycles for a half tile of K
-//       or V: 1000 to turn it, 450 to ask for the one after next, 200 of waits;
-//       69 us without all that.  (Six warps, of a block of 512 threads: the
-//       softmax has fewer registers and reads its scores twice; 64 rows 134, 256
-//       rows 218 when two warps took 141 and 187.  The next rows' codes held in
-//       registers: spills, 134 and 151)
+//       64 rows of q to a head 102 us, 128 106, 256 145; 21 for the bytes alone.
+//       A half tile of K or V takes 1000 cycles to turn and 300 of waits and
+//       hand-overs, two of them a tile; 69 us without all that, which is the
+//       softmax's chain.  (The turning warps copying for themselves: 450 cycles
+//       more, 125 us.  Six turning warps, of a block of 512 threads: the softmax
+//       has fewer registers and reads its scores twice; 64 rows 134, 256 rows 218
+//       when two warps took 141 and 187.  The next rows' codes held in registers:
+//       spills, 134 when 125)
+//   heads of 64: 74, 76 and 129 us
 //   48 requests of 0 .. 40 tokens over up to 8000 keys, 20 / 4 heads of 64, a
-//   window of 1500, fp16: 41 us, bound as the 16-bit pages' mixed batch is
-//   4096 tokens that end 32768 keys, 32 heads over 4: 2270 us, against 1500
+//   window of 1500, fp16: 40 us, bound as the 16-bit pages' mixed batch is
+//   4096 tokens that end 32768 keys, 32 heads over 4: 1680 us, against 1500
 //       where the pages are first read into 16-bit ones (27 us) and attended to
-//       there, as the codes are turned once for each 256 rows
+//       there: five stages instead of four, and nothing to turn
 #pragma once
 
 #include <cuda_bf16.h>
@@ -106,7 +110,7 @@ constexpr int kSoftmaxWarps = 8;
 constexpr int kMmaWarp = 11;
 constexpr int kLoadWarp = 9;
 constexpr int kGatherWarp = 8;     // selected: the second half of each tile's rows
-constexpr int kLandWarp = 10;
+constexpr int kLandWarp = 10;      // 4 bits: copies pages
 constexpr int kItemSlots = 4;
 constexpr int kItemInts = 16;
 
@@ -154,6 +158,9 @@ __device__ __forceinline__ void st_release_shared(uint32_t addr, uint32_t v)
 // a group have written their part of the group's P number `count`, each
 // saying so in its word; skip: the group has added that tile's product itself
 // (all four say the same).
+// TWO: `landed` and the word 8 bytes on count halves of the places.  (As one load
+// of two words: 104 us against 102.)
+template <bool TWO>
 __device__ __forceinline__ bool words_ready(uint32_t landed, uint32_t places, uint32_t words,
                                             uint32_t count, bool& skip, volatile int* abort,
                                             unsigned int* status)
@@ -162,7 +169,8 @@ __device__ __forceinline__ bool words_ready(uint32_t landed, uint32_t places, ui
     for (uint32_t it = 1;; ++it) {
         uint4 w = make_uint4(2 * count, 2 * count, 2 * count, 2 * count);
         if (words != 0) w = ld_acquire_shared_v4(words);
-        const uint32_t there = ld_acquire_shared(landed);
+        uint32_t there = ld_acquire_shared(landed);
+        if (TWO) there = min(there, ld_acquire_shared(landed + 8));
         if (there >= places && (w.x >> 1) == count && (w.y >> 1) == count && (w.z >> 1) == count &&
             (w.w >> 1) == count) {
             skip = w.x & 1u;
@@ -217,7 +225,7 @@ struct Cfg {
     static constexpr int kBars = kFactors + (FP4 ? 2 * 128 * 4 : 0);
     // barriers: full, empty per stage; q full, q empty per half; s full, pv done, group
     // sync per half; o empty, alt sync; item full, item empty; the issuer's
-    // last commit; 4 bits: q turned per half, codes there per raw tile of each warp
+    // last commit; 4 bits: q turned per half, raw tiles full and empty
     static constexpr int kNumBars = 2 * kStages + 4 + 6 + 2 + 2 * kItemSlots + 1 + (FP4 ? 2 + 2 * kRawTiles : 0);
     static constexpr int kItems = (kBars + kNumBars * 8 + 15) / 16 * 16;
     static constexpr int kMisc = kItems + kItemSlots * kItemInts * 4;
@@ -444,6 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 {
     using C = Cfg<D, FP4>;
     constexpr bool TURN_Q = FP16 != OUT16;
+    // pages in 4 bits: a warp of its own copies them, the turning warps say what has landed
+    constexpr bool kPager = FP4 && !SEL;
     constexpr int S = C::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_addr(smem);
@@ -458,7 +468,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sfull0 = qempty0 + 16u, pvdone0 = sfull0 + 16u,
                    group0 = pvdone0 + 16u, oempty = group0 + 16u, altbar = oempty + 8u,
                    itfull0 = altbar + 8u, itempty0 = itfull0 + 8u * kItemSlots, drain = itempty0 + 8u * kItemSlots,
-                   qready0 = drain + 8u, rawfull0 = qready0 + 16u;
+                   qready0 = drain + 8u, rawfull0 = qready0 + 16u,
+                   rawempty0 = rawfull0 + 8u * C::kRawTiles;
     int* items = reinterpret_cast<int*>(smem + C::kItems);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMisc + 4);
@@ -480,13 +491,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort_flag = 0;
         *total_places = -1;
         st_release_shared(landed_word, 0);
+        st_release_shared(landed_word + 8, 0);
         for (int s = 0; s < S; ++s) {
             mbar_init(full_bar(s), SEL || FP4 ? 2 : 1);
             mbar_init(empty_bar(s), 1);
         }
         mbar_init(drain, 1);
-        if (FP4)
-            for (int i = 0; i < 2 * C::kRawTiles; ++i) mbar_init(rawfull0 + 8u * i, 1);
+        for (int i = 0; kPager && i < C::kRawTiles; ++i) {
+            mbar_init(rawfull0 + 8u * i, 33);       // the copying warp's lanes, and once more for TMA
+            mbar_init(rawempty0 + 8u * i, 2);
+        }
         for (int h = 0; h < 2; ++h) {
             mbar_init(qfull0 + 8u * h, 1);
             mbar_init(qempty0 + 8u * h, 1);
@@ -518,7 +532,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_dependency_wait();
     const int sel_tiles = SEL ? (a.sel_k + kAttnTileKeys - 1) / kAttnTileKeys : 0;
     Start start = {0, 0, 0, 0, 0};
-    const bool loads = warp == kLoadWarp || ((SEL || FP4) && warp == kGatherWarp);
+    const bool pager = kPager && warp == kLandWarp;
+    const bool loads = warp == kLoadWarp || ((SEL || FP4) && warp == kGatherWarp) || pager;
     const bool lead = warp == kLoadWarp;
     if (loads) {
         if constexpr (SEL) {
@@ -558,8 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int handed = 0;              // selected: those whose copies are complete
         int item = 0;
         uint32_t qcount = 0;         // Q halves filled so far
-        uint32_t raw_put = 0, raw_got = 0;       // 4 bits: this warp's raw tiles asked for and taken
-        const uint32_t raw_bar = rawfull0 + (lead ? 0u : 8u * C::kRawTiles);
+        uint32_t raw_put = 0, raw_got = 0;       // 4 bits: raw tiles asked for and taken
         bool ok = true;
         int tok0 = 0, nq = 0, kv = 0, tiles = 0, cur_b = -1;
         auto next_item = [&]() {
@@ -665,35 +679,84 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---- K and V tiles: K runs `ahead` tiles before V
             const int ahead = alt ? 2 : 1;
             if constexpr (FP4) {
-                // Codes to fp16 tiles: each of the two warps has half of a tile's
-                // rows, whose codes and scales it copies as they are, two tiles
-                // ahead, into its own memory; then a lane takes sixteen bytes of
+                // Codes to fp16 tiles: each of two warps has half of a tile's rows.
+                // Their codes and scales come as they are into a ring of their
+                // own: pages by a third warp, listed rows by the two
+                // themselves, two tiles ahead.  Then a lane takes sixteen bytes of
                 // a row (eight lanes side by side the same bytes of eight rows,
                 // whose chunks the swizzle puts into different banks) and turns
                 // them into 64 in the stage.  Rows that no row of the item may
-                // see have scales of zero.  Pages' codes come by TMA where rows
-                // are of 64 bytes (64 rows of q: 125 us against 135 with eight
-                // copies a lane); of 32 bytes it takes as long as the copies, and
-                // longer with 256 rows (131 against 122).
+                // see have scales of zero.
                 constexpr int CB = D / 2, SB = D / kNvGroup, kRowLanes = CB / 16, kInst = 32 / kRowLanes,
                               kIter = 64 / kInst;
-                constexpr bool kByTma = !SEL && D == 128;
                 const int r_in = (lane & 7) + 8 * (lane / (8 * kRowLanes)), chunk = (lane >> 3) % kRowLanes;
                 // (where a row's chunk lies: the same chunk of eight rows in eight places,
-                // which is TMA's 64-byte swizzle for rows of 64)
+                // which is TMA's swizzle for rows of 64 or 32 bytes)
                 const int place = (D == 128 ? chunk ^ ((lane >> 1) & 3) : chunk ^ ((lane >> 2) & 1)) * 16;
                 const int row0 = lead ? 0 : 64;
-                const uint32_t raw0 = base + C::kRaw + (lead ? 0 : C::kRawTiles * C::kRawBytes);
+                constexpr uint32_t kRawHalf = C::kRawTiles * C::kRawBytes;
+                const uint32_t raw0 = base + C::kRaw + (lead || pager ? 0 : kRawHalf);
                 const int32_t* table = a.block_table + (long long)req * a.bt_stride;
                 auto checked = [&](int page) {
                     const bool bad = page < 0 || page >= a.num_pages;
                     if (bad) atomicOr(a.status, kStatusBadBlock);
                     return bad ? 0 : page;
                 };
-                // dense: 32 table entries from page `win` on, one a lane; pages of
-                // the one or two tiles whose K is in and V is not
+                int nk = 0, nv = 0;          // tiles whose K, V has been asked for
+                // ---- pages: all of a tile's rows, K or V
                 const int page_begin = sp.lo / kBlockKeys, page_end = sp.hi > 0 ? (sp.hi - 1) / kBlockKeys + 1 : 0;
-                int win = -1, entry = 0, pg0 = 0, pg1 = 0;
+                const long long row_k = head * a.kc4.s_head + lane * a.kc4.s_slot,
+                                row_v = head * a.vc4.s_head + lane * a.vc4.s_slot;
+                auto copy_tile = [&](const NvCache& c, const CUtensorMap* map, long long row, int tile_at, int px, int py) {
+                    const uint32_t slot = raw_put % C::kRawTiles, full = rawfull0 + 8u * slot;
+                    const uint32_t to = raw0 + slot * C::kRawBytes;
+                    ok = warp_wait(rawempty0 + 8u * slot, ((raw_put / C::kRawTiles) & 1u) ^ 1u, abort_flag, a.status);
+                    if (!ok) return;
+                    if (lane == 0) mbar_arrive_expect_tx(full, 2 * 64 * CB);
+                    __syncwarp();
+                    if (lane < 2) tma_load_4d(to + lane * kRawHalf, map, full, 0, 0, head, lane ? py : px);
+                    // the rows that some row of the item may see
+                    const int first_key = (j0 + tile_at) * kAttnTileKeys;
+                    const int lo = sp.lo - first_key, hi = sp.hi - first_key;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint8_t* src = c.scales + (x ? py : px) * c.s_page + row;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int r = 64 * x + 32 * i + lane;
+                            cp_async_small<SB>(to + x * kRawHalf + 64 * CB + (32 * i + lane) * SB, src + 32 * i * c.s_slot,
+                                               r >= lo && r < hi ? SB : 0);
+                        }
+                    }
+                    cp_async_arrive(full);
+                    ++raw_put;
+                };
+                if (kPager && pager) {
+                    // 32 table entries from page `win` on, one a lane; pages of the one
+                    // or two tiles whose K is in and V is not
+                    int win = -1, entry = 0, x0 = 0, y0 = 0, x1 = 0, y1 = 0;
+#pragma unroll 1
+                    while (nv < n && ok) {
+                        if (nk < n && nk - nv < ahead) {
+                            const int pg = 2 * (j0 + nk);
+                            if (win < 0 || pg >= win + 32) {
+                                win = pg;
+                                entry = pg + lane >= page_begin && pg + lane < page_end
+                                            ? checked(__ldg(table + pg + lane)) : 0;
+                            }
+                            const int x = __shfl_sync(0xffffffffu, entry, pg - win),
+                                      y = __shfl_sync(0xffffffffu, entry, pg - win + 1);
+                            if (nk == nv) { x0 = x; y0 = y; }
+                            else { x1 = x; y1 = y; }
+                            copy_tile(a.kc4, &kmap, row_k, nk, x, y);
+                            ++nk;
+                        } else {
+                            copy_tile(a.vc4, &vmap, row_v, nv, x0, y0);
+                            x0 = x1; y0 = y1;
+                            ++nv;
+                        }
+                    }
+                }
                 // selected: positions of this lane's two rows in the next tiles, and
                 // pages of the nearer ones
                 const int32_t* list = SEL ? a.selected + (long long)b * a.sel_stride : nullptr;
@@ -714,110 +777,62 @@ __global__ void __launch_bounds__(kThreads, 1)
                     g0 = pages(p0);
                     g1 = pages(p1);
                 }
-                int nk = 0, nv = 0;
-                // dense: a tile's codes and scales from a page, K or V
-                const long long row_k = head * a.kc4.s_head + lane * a.kc4.s_slot,
-                                row_v = head * a.vc4.s_head + lane * a.vc4.s_slot,
-                                code_k = head * a.kc4.head + r_in * a.kc4.slot + chunk * 16,
-                                code_v = head * a.vc4.head + r_in * a.vc4.slot + chunk * 16;
-                auto copy_page = [&](const NvCache& c, const CUtensorMap* map, long long row, long long code, int tile_at, int page) {
-                    const uint32_t slot = raw_put % C::kRawTiles, to = raw0 + slot * C::kRawBytes;
-                    if constexpr (kByTma) {
-                        if (lane == 0) {
-                            mbar_arrive_expect_tx(raw_bar + 8u * slot, 64 * CB);
-                            tma_load_4d(to, map, raw_bar + 8u * slot, 0, 0, head, page);
-                        }
-                    } else {
-                        const uint8_t* from = c.codes + page * c.page + code;
-#pragma unroll
-                        for (int i = 0; i < kIter; ++i) {
-                            cp_async16(to + (i * kInst + r_in) * CB + place, from, 16u);
-                            from += kInst * c.slot;
-                        }
-                    }
-                    // the page's rows that some row of the item may see
-                    const int first_key = (j0 + tile_at) * kAttnTileKeys + row0;
-                    const int lo = sp.lo - first_key, hi = sp.hi - first_key;
-                    uint32_t bytes0 = SB, bytes1 = SB;
-                    if (lo > 0 || hi < 64) {
-                        bytes0 = lane >= lo && lane < hi ? SB : 0;
-                        bytes1 = lane + 32 >= lo && lane + 32 < hi ? SB : 0;
-                    }
-                    const uint8_t* src = c.scales + page * c.s_page + row;
-                    cp_async_small<SB>(to + 64 * CB + lane * SB, src, bytes0);
-                    cp_async_small<SB>(to + 64 * CB + (lane + 32) * SB, src + 32 * c.s_slot, bytes1);
-                };
-                // Copies the next tile in order, K `ahead` tiles before V; nothing
-                // when none is left.
-                auto copy = [&]() {
+                // Copies the next tile's listed rows in order, K `ahead` tiles before
+                // V; nothing when none is left.
+                auto copy_listed = [&]() {
                     if (nv < n) {
                         const bool is_k = nk < n && nk - nv < ahead;
-                        if constexpr (SEL) {
-                            const NvCache& c = is_k ? a.kc4 : a.vc4;
-                            const uint8_t* ssrc = c.scales + head * c.s_head;
-                            const uint32_t to = raw0 + raw_put % C::kRawTiles * C::kRawBytes;
-                            int2 p = vp0, g = vg0;
-                            if (is_k) {
-                                p = p0;
-                                g = make_int2(checked(g0.x), checked(g0.y));
-                                if (nk == nv) { vp0 = p; vg0 = g; }
-                                else { vp1 = p; vg1 = g; }
-                                ++nk;
-                                p0 = p1; g0 = g1;
-                                p1 = p2; g1 = pages(p1);
-                                p2 = positions(nk + 2);
-                            } else {
-                                vp0 = vp1; vg0 = vg1;
-                                ++nv;
-                            }
-                            const uint8_t* src = c.codes + head * c.head + chunk * 16;
-                            const long long at[2] = {p.x < 0 ? -1 : g.x * c.page + (p.x & 63) * c.slot,
-                                                     p.y < 0 ? -1 : g.y * c.page + (p.y & 63) * c.slot};
-#pragma unroll
-                            for (int i = 0; i < kIter; ++i) {
-                                const long long o = __shfl_sync(0xffffffffu, at[i * kInst / 32], (i * kInst + r_in) & 31);
-                                cp_async16(to + (i * kInst + r_in) * CB + place, src + max(o, 0ll), o < 0 ? 0u : 16u);
-                            }
-                            cp_async_small<SB>(to + 64 * CB + lane * SB, ssrc + g.x * c.s_page + (p.x & 63) * c.s_slot,
-                                               p.x < 0 ? 0u : SB);
-                            cp_async_small<SB>(to + 64 * CB + (lane + 32) * SB, ssrc + g.y * c.s_page + (p.y & 63) * c.s_slot,
-                                               p.y < 0 ? 0u : SB);
-                        } else if (is_k) {
-                            const int pg = 2 * (j0 + nk) + (lead ? 0 : 1);
-                            if (win < 0 || pg >= win + 32) {
-                                win = pg;
-                                entry = pg + lane >= page_begin && pg + lane < page_end
-                                            ? checked(__ldg(table + pg + lane)) : 0;
-                            }
-                            const int page = __shfl_sync(0xffffffffu, entry, pg - win);
-                            if (nk == nv) pg0 = page;
-                            else pg1 = page;
-                            copy_page(a.kc4, &kmap, row_k, code_k, nk, page);
+                        const NvCache& c = is_k ? a.kc4 : a.vc4;
+                        const uint8_t* ssrc = c.scales + head * c.s_head;
+                        const uint32_t to = raw0 + raw_put % C::kRawTiles * C::kRawBytes;
+                        int2 p = vp0, g = vg0;
+                        if (is_k) {
+                            p = p0;
+                            g = make_int2(checked(g0.x), checked(g0.y));
+                            if (nk == nv) { vp0 = p; vg0 = g; }
+                            else { vp1 = p; vg1 = g; }
                             ++nk;
+                            p0 = p1; g0 = g1;
+                            p1 = p2; g1 = pages(p1);
+                            p2 = positions(nk + 2);
                         } else {
-                            copy_page(a.vc4, &vmap, row_v, code_v, nv, pg0);
-                            pg0 = pg1;
+                            vp0 = vp1; vg0 = vg1;
                             ++nv;
                         }
+                        const uint8_t* src = c.codes + head * c.head + chunk * 16;
+                        const long long at[2] = {p.x < 0 ? -1 : g.x * c.page + (p.x & 63) * c.slot,
+                                                 p.y < 0 ? -1 : g.y * c.page + (p.y & 63) * c.slot};
+#pragma unroll
+                        for (int i = 0; i < kIter; ++i) {
+                            const long long o = __shfl_sync(0xffffffffu, at[i * kInst / 32], (i * kInst + r_in) & 31);
+                            cp_async16(to + (i * kInst + r_in) * CB + place, src + max(o, 0ll), o < 0 ? 0u : 16u);
+                        }
+                        cp_async_small<SB>(to + 64 * CB + lane * SB, ssrc + g.x * c.s_page + (p.x & 63) * c.s_slot,
+                                           p.x < 0 ? 0u : SB);
+                        cp_async_small<SB>(to + 64 * CB + (lane + 32) * SB, ssrc + g.y * c.s_page + (p.y & 63) * c.s_slot,
+                                           p.y < 0 ? 0u : SB);
                         ++raw_put;
                     }
                     cp_async_commit();
                 };
+                // ---- turned
 #pragma unroll 1
-                for (int tile_op = 1 - C::kRawTiles; tile_op < 2 * n && ok; ++tile_op) {
-                    copy();
-                    if (tile_op < 0) continue;
+                for (int tile_op = SEL ? 1 - C::kRawTiles : 0; tile_op < 2 * n && ok && !pager; ++tile_op) {
+                    if constexpr (SEL) {
+                        copy_listed();
+                        if (tile_op < 0) continue;
+                        cp_async_wait<C::kRawTiles - 1>();
+                        __syncwarp();
+                    }
                     const int st = pos % S;
-                    cp_async_wait<C::kRawTiles - 1>();
-                    __syncwarp();
                     const uint32_t slot = raw_got % C::kRawTiles, raw = raw0 + slot * C::kRawBytes;
                     const uint32_t raw_parity = (raw_got / C::kRawTiles) & 1u, parity = ((pos / S) & 1) ^ 1u;
                     if constexpr (SEL) {
                         ok = warp_wait(empty_bar(st), parity, abort_flag, a.status);
                     } else {                      // (mostly both are: one vote)
-                        const bool raw_there = !kByTma || mbar_try_wait(raw_bar + 8u * slot, raw_parity);
+                        const bool raw_there = mbar_try_wait(rawfull0 + 8u * slot, raw_parity);
                         ok = __all_sync(0xffffffffu, mbar_try_wait(empty_bar(st), parity) && raw_there) ||
-                             ((!kByTma || warp_wait(raw_bar + 8u * slot, raw_parity, abort_flag, a.status)) &&
+                             (warp_wait(rawfull0 + 8u * slot, raw_parity, abort_flag, a.status) &&
                               warp_wait(empty_bar(st), parity, abort_flag, a.status));
                     }
                     if (!ok) break;
@@ -826,8 +841,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                          (row0 + r_in) * 128;
                     // (a short loop: the softmax's long straight code on the same
                     // scheduler leaves few instructions where they can be had at
-                    // once.  Unrolled 140 us with 64 rows of q, 179 with 256; two
-                    // rows at a time 125 and 145, one 154 and 172)
+                    // once.  Unrolled 140 us with 64 rows of q, 179 with 256, when
+                    // two rows at a time took 125 and 145, and one 154 and 172)
                     constexpr int kRows = 2;
 #pragma unroll 1
                     for (int i0 = 0; i0 < kIter; i0 += kRows) {
@@ -861,12 +876,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     fence_proxy_async_smem();     // the tensor core reads what this lane has written
                     __syncwarp();                 // (and the codes' place is free)
-                    if (lane == 0) mbar_arrive(full_bar(st));
                     ++pos;
+                    if (lane == 0) {
+                        if constexpr (kPager) st_release_shared(landed_word + (lead ? 0 : 8), (uint32_t)pos);
+                        mbar_arrive(full_bar(st));
+                        if constexpr (kPager) mbar_arrive(rawempty0 + 8u * slot);
+                    }
                 }
-                cp_async_wait<0>();
-                __syncwarp();
-                handed = pos;
+                if constexpr (SEL) {
+                    cp_async_wait<0>();
+                    __syncwarp();
+                    handed = pos;
+                }
             } else if constexpr (SEL) {
                 const int32_t* list = a.selected + (long long)b * a.sel_stride;
                 const int32_t* table = a.block_table + (long long)req * a.bt_stride;
@@ -1033,9 +1054,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(full_bar(handed % S));
             }
         }
-        if constexpr (FP4 && !SEL && D == 128)              // copies in flight land before the CTA may leave
-            for (; raw_got < raw_put; ++raw_got)
-                mbar_wait_drain<false>(raw_bar + 8u * (raw_got % C::kRawTiles), (raw_got / C::kRawTiles) & 1u);
+        if (kPager && pager) {               // copies in flight land before the CTA may leave
+            cp_async_wait<0>();
+            for (uint32_t k = raw_put > C::kRawTiles ? raw_put - C::kRawTiles : 0; k < raw_put; ++k)
+                mbar_wait_drain<false>(rawfull0 + 8u * (k % C::kRawTiles), (k / C::kRawTiles) & 1u);
+        }
         if (lead) {
             if (ok) {
                 const int is = item % kItemSlots;
@@ -1104,7 +1127,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             // places below `place` have landed, and (words != 0) a half's P number `count`
             auto wait_words = [&](uint32_t words, uint32_t count) {
-                return words_ready(landed_word, place, words, count, skip, abort_flag, a.status);
+                return words_ready<kPager>(landed_word, place, words, count, skip, abort_flag, a.status);
             };
             for (int item = 0; ok; ++item) {
                 const int is = item % kItemSlots;

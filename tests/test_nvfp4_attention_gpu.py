@@ -3,8 +3,8 @@ the definitions in 64 bits over the values that the caches stand for: single
 tokens, drafts, chunks and mixed batches; head groups from 1 to 300; causal,
 windows, neither; empty requests and rows without a key; layouts; stale slots
 and NaN scales in masked places; large logits; bad pages, requests and lists.
-Up to 48 rows ((token, head) pairs of a kv head) to a request on average run
-warp by warp, more by tiles: both ways are tested throughout."""
+Up to 32 rows ((token, head) pairs of a kv head) to a request on average, or 127
+in all, run warp by warp, more by tiles: both ways are tested throughout."""
 import math
 
 import pytest
@@ -136,7 +136,7 @@ def test_single_tokens(dim, dtype, kvn):
 
 @pytest.mark.parametrize("hq,hkv", [(1, 1), (3, 1), (4, 4), (10, 2), (7, 1), (8, 1), (9, 1), (16, 1), (17, 1), (33, 1),
                                     (64, 1), (65, 1), (128, 1), (300, 1), (48, 2)])
-@pytest.mark.parametrize("q", [1, 3])
+@pytest.mark.parametrize("q", [1, 3, 11])
 def test_head_groups(hq, hkv, q):
     p = Problem([q, q], [200, 77], hq, hkv, 64, BF, seed=hq).stale()
     check(p, *p.run(cu=False))
@@ -315,8 +315,9 @@ def test_masked_places_of_few_tokens(dim, hq):
     check(p, out, lse, window=40)
 
 
-def test_masked_keys_of_nan():
-    p = Problem([40], [200], 2, 1, 64, BF, seed=7).stale()
+@pytest.mark.parametrize("hq", [2, 6])
+def test_masked_keys_of_nan(hq):
+    p = Problem([40], [200], hq, 1, 64, BF, seed=7).stale()
     p.set_scale("k", 0, 199, 0, 2, NAN_SCALE | 128)       # the last token's key
     out, lse = p.run()
     got = out.cpu()
@@ -381,7 +382,7 @@ def test_long_lists_of_few_tokens(dim, hq, hkv):
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
-@pytest.mark.parametrize("hq", [2, 64])
+@pytest.mark.parametrize("hq", [2, 64, 128])
 def test_small_weights_beside_a_large_one(dtype, hq):
     """30000 keys whose weights are e^-8 of the best one's."""
     p = Problem([1], [30000], hq, 1, 64, dtype, seed=10).stale()
@@ -638,7 +639,7 @@ def test_no_tokens():
 
 
 @pytest.mark.parametrize("dim", [64, 128])
-@pytest.mark.parametrize("hq", [4, 32])
+@pytest.mark.parametrize("hq", [4, 32, 64])
 def test_positions_up_to_the_last(dim, hq):
     """A table as wide as positions go, one page behind all its entries, and a
     window that leaves the end of it."""
