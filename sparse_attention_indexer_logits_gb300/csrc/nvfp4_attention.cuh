@@ -1065,7 +1065,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         const int c_heads = p[kPcHeads];
         if (row >= p[kPcNtok] * c_heads) continue;
         Joined<N> x;
-        auto add = [&](int w, bool here) {
+        // (what an item begins with is its warp's last piece)
+        const unsigned own = led ? 0u : 1u << w0;
+        members |= own;
+#pragma unroll 1
+        for (; members; members &= members - 1) {
+            const int w = __ffs(members) - 1;
+            const bool here = ((kept | own) >> w) & 1;
             const long long q = (blockIdx.x * (long long)C::kWarps + w) * C::kRows;
             const float* part = here ? reinterpret_cast<const float*>(smem + w * C::kRing) : wp.part + q * D;
             const float2* stats = here ? reinterpret_cast<const float2*>(smem + w * C::kRing + C::kRows * D * 4)
@@ -1074,11 +1080,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             float y[N];
             load_cols<N>(part + row * D + col, y);
             x.add(st.x, st.y, y, a.scale_log2);
-        };
-        if (!led) add(w0, true);            // (what an item begins with is its warp's last piece)
-        for (; members; members &= members - 1) {
-            const int w = __ffs(members) - 1;
-            add(w, (kept >> w) & 1);
         }
         if (!led && ends) {
             write_joined<FP16, N>(a, x, p[kPcTok0], p[kPcHead], c_heads, row, col);
