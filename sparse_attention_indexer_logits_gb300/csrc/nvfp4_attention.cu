@@ -11,13 +11,24 @@ extern template cudaError_t launch_nvfp4_attention_dim<64>(bool, int, const NvAt
                                                            const nvattn::Pieces&, int, cudaStream_t);
 extern template cudaError_t launch_nvfp4_attention_dim<128>(bool, int, const NvAttnArgs&, const nvattn::Pieces&,
                                                             const nvattn::Pieces&, int, cudaStream_t);
+template <int D>
+int nvfp4_clusters_dim(bool select, int tiles, int size);
+extern template int nvfp4_clusters_dim<64>(bool, int, int);
+extern template int nvfp4_clusters_dim<128>(bool, int, int);
 
 namespace {
 
 using namespace nvattn;
 
 constexpr int kJoinWarps = 8, kJoinRows = 4;
-constexpr int kJoinSteps = 3;     // the join's time in steps of a warp
+constexpr int kMaxCluster = 8;    // portable (of 16 the device runs 7 at a time)
+// The joins' times in steps of a warp: by the second kernel, within a cluster.  One
+// token over 4000 keys, 32 / 8 heads of 128, takes 15.2 us cut over all CTAs and
+// 12.2 by clusters of eight; over 500 keys 13.5 and 11.4; 16 lists of 2048 for 64
+// heads 22.6 whole and 18.1 by clusters of two; 7 lists of 500 for 16 / 2 heads of
+// 64 8.3 whole and 9.6 by clusters; one token over 32768 keys 23.6 cut: clusters
+// of eight would be of 64 CTAs alone.
+constexpr int kJoinSteps = 3, kClusterSteps = 2;
 
 // A CTA whose pieces ended with an item that it had begun (slot 1) owns the
 // join: the item's other pieces are slot 0 of the following CTAs, up to the one
@@ -139,22 +150,40 @@ cudaError_t launch_nvfp4_attention(int head_dim, bool fp16, NvAttnArgs& a, int n
     a.block_heads = (a.group + a.head_blocks - 1) / a.head_blocks;
     a.tile_tokens = a.selected || a.group > rows ? 1 : rows / a.group;
     const int warps = tiles == 1 ? Cfg<128, 1>::kWarps : Cfg<128, 2>::kWarps;
-    if (a.selected) {
-        // Items of the same number of steps: where leaving them whole costs a warp no
-        // more than kJoinSteps further steps, no CTA shares one and nothing is left
-        // to join.
-        const long long items = (long long)a.tokens * a.kv_heads * a.head_blocks;
-        const long long steps = (a.sel_k + kStepKeys - 1) / kStepKeys + kItemUnits;
-        const long long whole = (items + num_ctas - 1) / num_ctas * steps / warps;
-        a.whole_items = whole <= items * steps / ((long long)num_ctas * warps) + kJoinSteps;
+    // Whether the steps are cut without regard to items, which a second kernel joins,
+    // or an item is one CTA's or one cluster's, by a warp's most steps and the join.
+    // Lists have equally many each; of one request the longest its table allows
+    // counts; several requests may differ by any factor and are cut.
+    const long long items = a.selected ? (long long)a.tokens * a.kv_heads * a.head_blocks
+                                       : (long long)((a.tokens + a.tile_tokens - 1) / a.tile_tokens) * a.kv_heads * a.head_blocks;
+    const long long steps = (a.selected ? (a.sel_k + kStepKeys - 1) / kStepKeys : 2LL * a.bt_width) + kItemUnits;
+    int grid = num_ctas;
+    if (a.selected || a.batch == 1) {
+        double best = (double)items * steps / ((double)num_ctas * warps) + kJoinSteps;
+        if (a.selected) {
+            const double whole = (double)((items + num_ctas - 1) / num_ctas * steps) / warps;
+            a.whole_items = whole <= best;
+            if (a.whole_items) best = whole;
+        }
+        for (int size = 2; size <= kMaxCluster && items * size <= num_ctas; size *= 2) {
+            const double mine = (double)steps / (size * warps) + kClusterSteps;
+            if (mine >= best) continue;
+            if ((head_dim == 128 ? nvfp4_clusters_dim<128>(a.selected, tiles, size)
+                                 : nvfp4_clusters_dim<64>(a.selected, tiles, size)) < items)
+                continue;
+            best = mine;
+            a.cluster = size;
+            a.whole_items = 0;
+            grid = (int)items * size;
+        }
     }
     uint8_t* at = static_cast<uint8_t*>(workspace);
     const Pieces wp = take(at, (int64_t)num_ctas * warps, 1, rows, head_dim);
     const Pieces cp = take(at, num_ctas, 2, rows, head_dim);
     if (at - static_cast<uint8_t*>(workspace) > workspace_bytes) return cudaErrorInvalidValue;    // never
-    cudaError_t e = head_dim == 128 ? launch_nvfp4_attention_dim<128>(fp16, tiles, a, wp, cp, num_ctas, stream)
-                                    : launch_nvfp4_attention_dim<64>(fp16, tiles, a, wp, cp, num_ctas, stream);
-    if (e != cudaSuccess || a.whole_items) return e;
+    cudaError_t e = head_dim == 128 ? launch_nvfp4_attention_dim<128>(fp16, tiles, a, wp, cp, grid, stream)
+                                    : launch_nvfp4_attention_dim<64>(fp16, tiles, a, wp, cp, grid, stream);
+    if (e != cudaSuccess || a.whole_items || a.cluster > 1) return e;
     return head_dim == 128 ? launch_join_dim<128>(fp16, tiles, a, cp, num_ctas, stream)
                            : launch_join_dim<64>(fp16, tiles, a, cp, num_ctas, stream);
 }

@@ -25,7 +25,8 @@
 // codes and scales into a ring of its own (cp.async, a few steps ahead) and
 // waits for nobody.  Pieces of items that several warps of a CTA shared are
 // joined at the CTA's end, those of several CTAs by a second kernel; all in a
-// fixed order.
+// fixed order.  One request, or lists, which are equally long, may have a
+// cluster of CTAs for each item instead, which joins its pieces itself.
 //
 // Operands (m16n8k16; g = lane / 4, t = lane % 4), eight rows of Q at a time:
 //   S^T = K Q^T   K is A, 16 keys.  The order of the summed elements is free, so
@@ -62,8 +63,8 @@
 //   64 tokens x 500 listed positions, 64 heads over 1: 17.7 us, a floor of 0.8; two
 //       steps a warp after a fixed part of 10 us
 //   one token, 4000 keys, 32 heads over 8
-//       15 us: a launch, where a range begins 2, first copies and Q 3, joined in
-//       the CTA 3-5, joined between CTAs 4
+//       12.2 us, eight CTAs to a kv head (15.2 cut over all, with the second
+//       kernel): a launch, first copies and Q 3, joined in the CTA 3-5
 // Steps are of 32 keys, a whole number of times in a page: an item's end costs
 // half of what steps of 64 would waste.
 #pragma once
@@ -421,6 +422,35 @@ __device__ __forceinline__ void write_joined(const NvAttnArgs& a, const Joined<N
         a.lse[token * a.kv_heads * a.group + head] = log_sum_of(x.top * a.scale_log2, x.sum);
 }
 
+// The pieces of a cluster's item, when all of its CTAs are through: a row to a warp.
+template <int D, bool FP16, int NT>
+__device__ __forceinline__ void join_cluster(const NvAttnArgs& a, const Pieces& cp)
+{
+    constexpr int N = D / 32, kRows = 8 * NT;
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = blockIdx.x % a.cluster, row = warp * a.cluster + rank, col = lane * N;
+    const long long q0 = (blockIdx.x - rank) * 2LL;
+    const int* r = cp.rec + (q0 + 1) * kPcInts;
+    if (!r[kPcUsed] || row >= r[kPcNtok] * r[kPcHeads]) return;
+    Joined<N> x;
+#pragma unroll 4
+    for (int p = 0; p < a.cluster; ++p) {
+        const long long q = q0 + 2 * p + (p == 0 ? 1 : 0);
+        const bool used = cp.rec[q * kPcInts + kPcUsed];       // (a range without a step left none)
+        float2 st = cp.stats[q * kRows + row];
+        float v[N];
+        load_cols<N>(cp.part + (q * kRows + row) * D + col, v);
+        if (!used) {
+            st = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] = 0.0f;
+        }
+        x.add(st.x, st.y, v, a.scale_log2);
+    }
+    write_joined<FP16, N>(a, x, r[kPcTok0], r[kPcHead], r[kPcHeads], row, col);
+}
+
 // ------------------------------------------------------------------ the kernel
 
 template <int D, bool FP16, bool SEL, int NT>
@@ -444,7 +474,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         const int per = sel_n + kItemUnits;
         const long long items = (long long)a.tokens * heads;
         long long s0, s1;
-        if (a.whole_items) {               // a CTA's items, shared out over its warps
+        if (a.cluster > 1) {
+            const long long i0 = blockIdx.x / a.cluster;
+            const int workers = a.cluster * C::kWarps, me = blockIdx.x % a.cluster * C::kWarps + warp;
+            s0 = i0 * per + range_start(per, workers, me);
+            s1 = i0 * per + range_start(per, workers, me + 1);
+        } else if (a.whole_items) {        // a CTA's items, shared out over its warps
             const long long i0 = range_start(items, gridDim.x, blockIdx.x);
             const long long units = (range_start(items, gridDim.x, blockIdx.x + 1) - i0) * per;
             s0 = i0 * per + range_start(units, C::kWarps, warp);
@@ -461,8 +496,21 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         start.head = (int)(item - (long long)start.b * heads);
         start.tile = 0;
     } else {
-        start = find_start<D, NT>(a, smem);
-        __syncthreads();                   // (the numbers lie in the ring)
+        if (a.cluster > 1) {               // one request
+            const int item = blockIdx.x / a.cluster;
+            start = {0, item / heads, item % heads, 0, 0};
+            int tok0, nq, kv;
+            request_of(a, 0, tok0, nq, kv);
+            if (start.tile < tiles_of(a, nq)) {
+                const int per = kItemUnits + span_of(a, nq, kv, start.tile).n;
+                const int workers = a.cluster * C::kWarps, me = blockIdx.x % a.cluster * C::kWarps + warp;
+                start.at = (int)range_start(per, workers, me);
+                start.left = range_start(per, workers, me + 1) - start.at;
+            }
+        } else {
+            start = find_start<D, NT>(a, smem);
+            __syncthreads();               // (the numbers lie in the ring)
+        }
     }
 
     const uint32_t ring = smem_addr(smem) + warp * C::kRing;
@@ -1090,6 +1138,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             for (int e = 0; e < N; ++e) cp.part[q * D + col + e] = x.acc[e];
         }
     }
+    if (a.cluster > 1) join_cluster<D, FP16, NT>(a, cp);
 }
 
 }  // namespace nvattn

@@ -21,7 +21,47 @@ cudaError_t launch_nvfp4_one(const NvAttnArgs& a, const nvattn::Pieces& wp, cons
         if (e != cudaSuccess) return e;
         configured_device = dev;
     }
+    if (a.cluster > 1)
+        return launch_dependent_clusters(kernel, dim3((unsigned)num_ctas), a.cluster, C::kThreads, C::kTotal, stream, a,
+                                         wp, cp);
     return launch_dependent(kernel, dim3((unsigned)num_ctas), C::kThreads, C::kTotal, stream, a, wp, cp);
+}
+
+// Clusters of `size` CTAs that the device runs at a time, 0 if it cannot say.
+template <int D, bool SEL, int NT>
+int nvfp4_clusters(int size)
+{
+    using C = nvattn::Cfg<D, NT>;
+    auto kernel = nvattn::nvfp4_attention_kernel<D, true, SEL, NT>;
+    static int known_device = -1, known[9];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (known_device != dev) {
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kTotal);
+        for (int s = 2; s <= 8; s *= 2) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)s);
+            cfg.blockDim = dim3((unsigned)C::kThreads);
+            cfg.dynamicSmemBytes = C::kTotal;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim = {(unsigned)s, 1, 1};
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            known[s] = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
+        }
+        cudaGetLastError();
+        known_device = dev;
+    }
+    return known[size];
+}
+
+template <int D>
+int nvfp4_clusters_dim(bool select, int tiles, int size)
+{
+    if (select) return tiles == 1 ? nvfp4_clusters<D, true, 1>(size) : nvfp4_clusters<D, true, 2>(size);
+    return tiles == 1 ? nvfp4_clusters<D, false, 1>(size) : nvfp4_clusters<D, false, 2>(size);
 }
 
 template <int D, bool FP16>

@@ -73,6 +73,7 @@ struct NvAttnArgs {
     int block_heads;               // query heads of one
     int sel_k;                     // selected: entries per token
     int whole_items;               // selected: no item is split between CTAs
+    int cluster;                   // > 1: each item is one cluster's of so many CTAs
     int causal;
     int window;                    // > 0: only keys past position - window
     float scale;                   // softmax scale times the keys' scale

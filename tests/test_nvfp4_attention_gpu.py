@@ -251,6 +251,34 @@ def test_one_long_request():
     check(p, *p.run())
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("hq,hkv,q", [(1, 1, 1), (4, 1, 1), (8, 8, 1), (19, 19, 1), (32, 8, 1), (7, 1, 4), (16, 2, 3),
+                                      (12, 4, 5), (76, 76, 1), (9, 1, 1)])
+@pytest.mark.parametrize("kv,window", [(5, 0), (6, 2), (33, 0), (257, 0), (4000, 0), (5000, 900), (0, 0)])
+def test_one_request(dim, hq, hkv, q, kv, window):
+    """Few items, each with CTAs of its own; more units than warps, fewer, none."""
+    p = Problem([q], [kv], hq, hkv, dim, BF if kv % 2 else FP, seed=kv + hq).stale()
+    out, lse = p.run(window=window)
+    check(p, out, lse, window=window, heads=range(0, hq, 1 + hq // 10))
+    for cu in (True, False):
+        again, lse2 = p.run(cu=cu, window=window)
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("hq", [4, 24])
+def test_one_request_of_fewer_tokens_than_rows(hq):
+    p = Problem([3], [700], hq, 1, 128, BF, seed=4).stale()
+    p.q = torch.cat([p.q, p.q, p.q])
+    args = p.device()
+    out, lse = torch.full_like(args[0], 9.0), torch.full((9, hq), 9.0, device="cuda")
+    pml.pml_paged_attention_nvfp4(*args, p.cu.cuda(), out, lse=lse)
+    check(p, out[:3], lse[:3])
+    assert (out[3:] == 9.0).all() and (lse[3:] == 9.0).all()
+    pml.pml_paged_attention_nvfp4(*args, torch.tensor([4, 7], dtype=torch.int32, device="cuda"), out, lse=lse)
+    p.q = p.q[4:7]
+    check(p, out[4:7], lse[4:7])
+
+
 @pytest.mark.parametrize("layout", ["pages", "gaps"])
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("qn", [[5, 60], [4, 3]])
@@ -369,13 +397,14 @@ def test_equal_logits_far_from_zero(size, hq):
 
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("hq,hkv", [(4, 2), (24, 1)])
-def test_long_lists_of_few_tokens(dim, hq, hkv):
+@pytest.mark.parametrize("tokens,k", [(1, 4000), (2, 4000), (9, 1500), (20, 700), (37, 900)])
+def test_long_lists_of_few_tokens(dim, hq, hkv, tokens, k):
     """Lists long enough to be split between CTAs."""
     g = R.gen(hq)
-    p = Problem([1, 1], [5000, 3000], hq, hkv, dim, FP, seed=12).stale()
-    sel = torch.randint(-100, 5000, (2, 4000), generator=g, dtype=torch.int32)
-    req = torch.tensor([0, 1], dtype=torch.int32)
-    lse = torch.empty((2, hq), device="cuda")
+    p = Problem([1] * tokens, [5000, 3000, 1, 0] * 9 + [200], hq, hkv, dim, FP, seed=12).stale()
+    sel = torch.randint(-100, 5000, (tokens, k), generator=g, dtype=torch.int32)
+    req = torch.arange(tokens, dtype=torch.int32)
+    lse = torch.empty((tokens, hq), device="cuda")
     out = pml.pml_sparse_attention_nvfp4(*p.device(), req.cuda(), sel.cuda(), lse=lse)
     assert pml.pml_device_status(clear=True) == 0
     check_selected(p, req, sel, out, lse, heads=range(0, hq, 3))
@@ -603,6 +632,29 @@ def test_same_result_every_time_and_captured(chunk):
     lse = torch.empty((chunk + 2, 8), device="cuda")
     check(p, pml.pml_paged_attention_nvfp4(*args, cu, lse=lse), lse)
     assert torch.equal(out, pml.pml_paged_attention_nvfp4(*args, cu))
+
+
+def test_one_request_captured():
+    p = Problem([2], [3000], 16, 4, 128, BF, seed=25).stale()
+    args, cu = p.device(), p.cu.cuda()
+    out, ws = torch.empty_like(args[0]), pml.pml_attention_workspace(128)
+    pml.pml_paged_attention_nvfp4(*args, cu, out, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(3):
+            pml.pml_paged_attention_nvfp4(*args, cu, out, workspace=ws)
+    for n in (2999, 1, 40, 3000):
+        args[-1].fill_(n)
+        out.fill_(9.0)
+        ws.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        lse = torch.empty((2, 16), device="cuda")
+        assert torch.equal(out, pml.pml_paged_attention_nvfp4(*args, cu, lse=lse))
+        if n != 3000:                  # (its last page holds stale slots)
+            p.kvn = [n]
+            check(p, out, lse)
 
 
 def test_memory_of_a_call_on_another_stream():
