@@ -652,9 +652,8 @@ def test_one_request_captured():
         torch.cuda.synchronize()
         lse = torch.empty((2, 16), device="cuda")
         assert torch.equal(out, pml.pml_paged_attention_nvfp4(*args, cu, lse=lse))
-        if n != 3000:                  # (its last page holds stale slots)
-            p.kvn = [n]
-            check(p, out, lse)
+        p.kvn = [n]
+        check(p, out, lse)
 
 
 def test_memory_of_a_call_on_another_stream():
