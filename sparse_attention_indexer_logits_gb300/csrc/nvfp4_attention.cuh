@@ -90,7 +90,6 @@ constexpr float kPLog2 = 7.0f, kPMost = 15.0f;
 // c S - c m is one fused product and sum while |c m| is below this (c m is
 // rounded once, to 2^-14); past it the difference is taken first.
 constexpr float kFar = 1024.0f;
-constexpr float kFresh = 3e38f;        // 7 - c m of a row that has seen no key: any score is too large
 
 // a piece's record
 enum { kPcUsed, kPcTok0, kPcNtok, kPcHead, kPcHeads, kPcLast };
@@ -774,6 +773,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[x][i][e] = 0.0f;
 
+        // whether a row of this lane's has seen no key yet, or its exponents are large
+        bool far = true;
         // ---- one step's keys in stage `st`
         auto compute = [&](int s, int st) {
             const uint32_t from = ring + st * C::kStageBytes;
@@ -854,16 +855,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             }
             // exponents of P, unless one is too large
             float most = -INFINITY;
-            bool far = false;
             float z[NT][2][4];
 #pragma unroll
             for (int x = 0; x < NT; ++x) {
                 float off[2];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    off[c] = ref[x][c] == -INFINITY ? kFresh : fmaf(-ref[x][c], f[x][c], kPLog2);
-                    far = far || fabsf(off[c]) > kFar;
-                }
+                for (int c = 0; c < 2; ++c) off[c] = fmaf(-ref[x][c], f[x][c], kPLog2);
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
 #pragma unroll
@@ -873,6 +870,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                 }
             }
             if (__any_sync(0xffffffffu, far || most > kPMost)) {
+                far = false;
 #pragma unroll
                 for (int x = 0; x < NT; ++x) {
                     float down[2], from_ref[2];
@@ -886,6 +884,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                         down[c] = ref[x][c] == -INFINITY ? 0.0f : exp2_approx((ref[x][c] - next) * f[x][c]);
                         ref[x][c] = next;
                         from_ref[c] = next == -INFINITY ? 0.0f : next;
+                        far = far || fabsf(next) * f[x][c] > kFar;      // (-inf too)
                         l[x][c] *= down[c];
                     }
 #pragma unroll
