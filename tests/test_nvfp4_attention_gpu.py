@@ -73,7 +73,7 @@ class Problem:
         return out, lse
 
 
-def judge(p, q, k, v, allowed, scale, got, got_lse, where):
+def compare_rows(p, q, k, v, allowed, scale, got, got_lse, where):
     """A score is a sum of products that are exact in fp32, each further one a
     rounding of 2^-23 of their magnitudes' sum (the tensor core may cut off),
     after q's own rounding: fp16 at most 2^-25 of the row's largest element.  A
@@ -121,7 +121,7 @@ def check(p, out, lse, causal=True, window=0, scale=None, requests=None, heads=N
         if window:
             allowed = allowed & (at > here - window)
         for h in range(p.hq) if heads is None else heads:
-            judge(p, p.q[lo:hi, h], k[:, h // group], v[:, h // group], allowed, scale, out[lo:hi, h], lse[lo:hi, h],
+            compare_rows(p, p.q[lo:hi, h], k[:, h // group], v[:, h // group], allowed, scale, out[lo:hi, h], lse[lo:hi, h],
                   f"request {b} head {h}")
     assert pml.pml_device_status(clear=True) == 0
 
@@ -351,7 +351,7 @@ def test_masked_keys_of_nan(hq):
     got = out.cpu()
     assert torch.isfinite(got[:39]).all() and torch.isnan(got[39]).all()
     k, v = p.rows(0, torch.arange(199))
-    judge(p, p.q[:39, 0], k[:, 0], v[:, 0], torch.arange(199) <= torch.arange(160, 199)[:, None], 0.125, out[:39, 0],
+    compare_rows(p, p.q[:39, 0], k[:, 0], v[:, 0], torch.arange(199) <= torch.arange(160, 199)[:, None], 0.125, out[:39, 0],
           lse[:39, 0], "rows before")
 
 
@@ -481,7 +481,7 @@ def check_selected(p, req, sel, out, lse, scale=None, heads=None):
         at = sel[t][(sel[t] >= 0) & (sel[t] < n)].long()
         k, v = p.rows(max(0, min(b, len(p.kvn) - 1)), at)
         for h in range(p.hq) if heads is None else heads:
-            judge(p, p.q[t:t + 1, h], k[:, h // group], v[:, h // group], torch.ones((1, len(at)), dtype=torch.bool),
+            compare_rows(p, p.q[t:t + 1, h], k[:, h // group], v[:, h // group], torch.ones((1, len(at)), dtype=torch.bool),
                   scale, out[t:t + 1, h], lse[t:t + 1, h], f"token {t} head {h}")
 
 
@@ -581,7 +581,7 @@ def test_selected_bad_places_and_nan(hq, copies):
                                              lse=lse)
         return out, lse
 
-    def judge_all(out, lse):
+    def check_all(out, lse):
         for i in {0, 2 * (copies // 2), 2 * copies - 2}:
             check_selected(p, req, sel, out[i:i + 2], lse[i:i + 2], heads=heads)
 
@@ -596,11 +596,11 @@ def test_selected_bad_places_and_nan(hq, copies):
     pos = int(sel[0, 17])
     p.set_scale("v", 0, pos, 0, 1, NAN_SCALE)
     out, lse = run()
-    judge_all(out, lse)
+    check_all(out, lse)
     assert torch.isnan(out[::2, :hq // 2, 16:32]).all()
     sel[0, 17] = -1
     out, lse = run()
-    judge_all(out, lse)
+    check_all(out, lse)
     assert torch.isfinite(out).all()
 
 
@@ -707,7 +707,7 @@ def test_positions_up_to_the_last(dim, hq):
         at = torch.arange(64 * width - 2 + i - 149, 64 * width - 1 + i) % 64
         k, v = (N.values(p.parts[c][page, at], p.parts[c + 1][page, at], 1.0) for c in (0, 2))
         for h in range(hq):
-            judge(p, p.q[i:i + 1, h], k[:, 0], v[:, 0], torch.ones((1, 150), dtype=torch.bool), dim ** -0.5,
+            compare_rows(p, p.q[i:i + 1, h], k[:, 0], v[:, 0], torch.ones((1, 150), dtype=torch.bool), dim ** -0.5,
                   out[i:i + 1, h], lse[i:i + 1, h], f"token {i}")
 
 
