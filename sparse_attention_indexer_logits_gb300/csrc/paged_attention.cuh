@@ -1274,9 +1274,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             if constexpr (TURN_Q) {
                 // Q's rows to fp16, each times a power of two that makes its
-                // largest element 1 to 2: bf16's 8 bits stay for those down to
-                // 2^-17 of it.  A half's group does it, half 0's where both
-                // halves hold the same rows.
+                // largest element 1 to 2 (of any size: a row of 2^-100 has
+                // ordinary logits under a scale of 2^97): bf16's 8 bits stay for
+                // those down to 2^-17 of it.  A half's group does it, half 0's
+                // where both halves hold the same rows.
                 if (!alt || h == 0) {
                     ok = warp_wait(qfull0 + 8u * q_slot, ((qcount + (alt ? 0u : (uint32_t)h)) >> 1) & 1u, abort_flag,
                                    a.status);
@@ -1290,7 +1291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         constexpr uint32_t k = 0x7fff7fffu;
                         top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[e].x & k, w[e].y & k), __vmaxu2(w[e].z & k, w[e].w & k)));
                     }
-                    top = min(max(max(top & 0xffffu, top >> 16) >> 7, 64u), 253u);
+                    top = min(max(max(top & 0xffffu, top >> 16) >> 7, 1u), 253u);
                     const float inv = __uint_as_float((254u - top) << 23);
                     auto half = [&](uint32_t v) {
                         return pack16<true>(__uint_as_float(v << 16) * inv, __uint_as_float(v & 0xffff0000u) * inv);
