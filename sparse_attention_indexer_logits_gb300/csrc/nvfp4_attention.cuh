@@ -744,7 +744,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                     st_shared_v4(q_at + (x * (KS / 2) + c) * 512, w[c].x, w[c].y, w[c].z, w[c].w);
                 }
             }
-            scale = fmaxf(scale, 1.2e-38f);        // (times -inf it stays -inf)
+            scale = fminf(fmaxf(scale, 1.2e-38f), 3.4e38f);    // (times -inf it stays -inf, times 0 it is 0)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 f[x][c] = __shfl_sync(0xffffffffu, scale, 8 * t + 4 * c);

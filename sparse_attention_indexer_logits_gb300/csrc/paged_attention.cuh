@@ -1270,7 +1270,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t q_slot = (qcount + (alt ? 0u : (uint32_t)h)) & 1u;
             auto take_factor = [&]() {
                 factor = factors[q_slot * 128 + row];
-                c = fmaxf(a.scale_log2 * factor, 1.2e-38f);      // (times -inf it stays -inf)
+                // (times -inf it stays -inf, times 0 it is 0)
+                c = fminf(fmaxf(a.scale_log2 * factor, 1.2e-38f), 3.4e38f);
             };
             if constexpr (TURN_Q) {
                 // Q's rows to fp16, each times a power of two that makes its
