@@ -38,7 +38,8 @@ constexpr int kMxfp4BlockBytes = kBlockKeys * (kHeadDim / 2 + kHeadDim / 32);   
 
 __host__ __device__ __forceinline__ int blocks_of(int32_t len)
 {
-    return len > 0 ? (len + kBlockKeys - 1) / kBlockKeys : 0;
+    // (unsigned: the sum passes the last int for lengths near it)
+    return len > 0 ? (int)(((unsigned)len + kBlockKeys - 1) / kBlockKeys) : 0;
 }
 
 // Start of range `cta` in the flattened block order: cta*floor(T/G) + min(cta, T mod G).
