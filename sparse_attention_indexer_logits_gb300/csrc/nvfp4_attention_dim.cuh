@@ -2,6 +2,7 @@
 // unit each, compiled side by side).
 #pragma once
 
+#include "cluster_counts.h"
 #include "nvfp4_attention.cuh"
 
 namespace pml {
@@ -32,29 +33,27 @@ template <int D, bool SEL, int NT>
 int nvfp4_clusters(int size)
 {
     using C = nvattn::Cfg<D, NT>;
-    auto kernel = nvattn::nvfp4_attention_kernel<D, true, SEL, NT>;
-    static int known_device = -1, known[9];
+    static ClusterCounts counts;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    if (known_device != dev) {
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kTotal);
-        for (int s = 2; s <= 8; s *= 2) {
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3((unsigned)s);
-            cfg.blockDim = dim3((unsigned)C::kThreads);
-            cfg.dynamicSmemBytes = C::kTotal;
-            cudaLaunchAttribute attr[1];
-            attr[0].id = cudaLaunchAttributeClusterDimension;
-            attr[0].val.clusterDim = {(unsigned)s, 1, 1};
-            cfg.attrs = attr;
-            cfg.numAttrs = 1;
-            int n = 0;
-            known[s] = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
-        }
+    return counts.get(dev, size, [](int s) {
+        auto kernel = nvattn::nvfp4_attention_kernel<D, true, SEL, NT>;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)s);
+        cfg.blockDim = dim3((unsigned)C::kThreads);
+        cfg.dynamicSmemBytes = C::kTotal;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim = {(unsigned)s, 1, 1};
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kTotal) == cudaSuccess &&
+            cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess)
+            return n;
         cudaGetLastError();
-        known_device = dev;
-    }
-    return known[size];
+        return 0;
+    });
 }
 
 template <int D>
