@@ -620,9 +620,12 @@ int pml_read_nvfp4(const pml_nvfp4_cache* k_cache, const pml_nvfp4_cache* v_cach
  * softmax_scale * k_cache->scale is in 1e-30 .. 1e30 (else
  * PML_ERR_INVALID_ARG); a row of q that is not finite, or whose scores fp32
  * does not hold, gives a row without meaning.
- * Up to 32 rows of q to a kv head (tokens of a request, on average, times
- * num_heads / kv_heads), or 127 in all, are taken warp by warp, more in tiles of
- * 128, with different roundings.
+ * Which way a call goes, and with it its roundings, follows from its sizes.  A
+ * request's rows of q to a kv head, its tokens (taken as tokens / batch each, or one
+ * more for tokens % batch of them) times num_heads / kv_heads, are items of 16:
+ * whole tokens, or some of one's heads.  Calls of up to 19/8 items a request, of
+ * fewer than 128 rows in all, and of more than 128 heads to a kv head are taken warp
+ * by warp, others in tiles of 128.
  */
 int pml_paged_attention_nvfp4(const void* q, int64_t q_token_stride, int64_t q_head_stride, int dtype,
                               const pml_nvfp4_cache* k_cache, const pml_nvfp4_cache* v_cache,
@@ -635,7 +638,9 @@ int pml_paged_attention_nvfp4(const void* q, int64_t q_token_stride, int64_t q_h
 
 /*
  * pml_sparse_attention_nvfp4 -- pml_sparse_attention over caches held in 4
- * bits, with the differences above.
+ * bits, with the differences above.  Groups of 33 to 128 heads to a kv head go in
+ * tiles once there is more to do than eight steps (32 positions for 16 heads) for
+ * each of 12 warps an SM; all else goes warp by warp.
  */
 int pml_sparse_attention_nvfp4(const void* q, int64_t q_token_stride, int64_t q_head_stride, int dtype,
                                const pml_nvfp4_cache* k_cache, const pml_nvfp4_cache* v_cache,

@@ -16,20 +16,6 @@ using namespace pml;
 constexpr int kMaxListed = 0x7fffff00; // entries of a list, so that their tiles' ends fit an int
 constexpr int kMaxHeads = 8192;
 constexpr int kMaxScaleExponent = 32;
-// Rows ((token, head) pairs of a kv head) of a request up to which its attention
-// is left to warps alone.  128 request-heads of 8500 keys, heads of 128 (64): 32
-// rows take 91 (61) us that way and 108 (76) by tiles, 40 rows 127 (84) and 107
-// (77), 64 rows 162 (106) and 107 (77), 256 rows 568 and 145.
-constexpr int kNvWarpRows = 32;
-// So is a call of fewer rows in all, of which a warp has no more than a step or
-// two: one request-head of 40 or 64 rows 21 us that way and 31 by tiles, 4 of them
-// 23 and 26, 16 of 40 rows 32 and 28.
-constexpr int kNvTileRows = 128;
-// Lists are, whatever the rows, while a warp has no more than so many steps: 64
-// heads over 1, 64 tokens of 64 positions 9.2 us that way and 13.9 by tiles, of 500
-// 17.7 and 20.3, of 1500 28.8 and 30.1, of 2048 34.4 and 32.7; 200 tokens of 2048
-// 132 and 83.
-constexpr int kNvWarpSteps = 8;
 
 // Strides of a dimension of one element are never used: any valid one will do.
 int64_t used(int64_t stride, int64_t size, int64_t other) { return size > 1 ? stride : other; }
@@ -99,11 +85,8 @@ int attention_call(NvAttnArgs& a, const void* q, int64_t q_token, int64_t q_head
     if (workspace_bytes < pml_attention_workspace_bytes(dev.sm_count, head_dim)) return PML_ERR_INVALID_ARG;
     const int group = num_heads / kv_heads;
     const bool fp16 = dtype == PML_DTYPE_FLOAT16;
-    const long long per_request = a.selected ? 1 : (tokens + a.batch - 1) / a.batch;
-    bool by_tiles = per_request * group > kNvWarpRows && group <= kAttnHalfRows;
-    if (by_tiles && !a.selected) by_tiles = per_request * a.batch * num_heads >= kNvTileRows;
-    if (by_tiles && a.selected)
-        by_tiles = nvfp4_list_steps(a.sel_k, group, (long long)tokens * kv_heads) > (long long)kNvWarpSteps * nvfp4_list_warps(dev.sm_count);
+    const bool by_tiles = a.selected ? nvfp4_lists_by_tiles(tokens, num_heads, group, a.sel_k, dev.sm_count)
+                                     : nvfp4_by_tiles(tokens, a.batch, num_heads, group);
     if (by_tiles) {
         AttnArgs w = {};
         attention_workspace(w, workspace, dev.sm_count, head_dim);

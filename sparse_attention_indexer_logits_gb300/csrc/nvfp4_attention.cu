@@ -132,20 +132,14 @@ Pieces take(uint8_t*& at, int64_t n, int slots, int rows, int dim)
 
 }  // namespace
 
-long long nvfp4_list_steps(int k, int group, long long lists)
-{
-    constexpr int rows = Cfg<128, 2>::kRows;
-    return lists * ((group + rows - 1) / rows) * ((k + kStepKeys - 1) / kStepKeys);
-}
-
-int nvfp4_list_warps(int num_ctas) { return num_ctas * Cfg<128, 2>::kWarps; }
+// (what the choice of the way counts with)
+static_assert(Cfg<128, 2>::kWarps == 12 && Cfg<128, 2>::kRows == 16 && kStepKeys == 32, "steps of a warp");
 
 cudaError_t launch_nvfp4_attention(int head_dim, bool fp16, NvAttnArgs& a, int num_ctas, void* workspace,
                                    int64_t workspace_bytes, cudaStream_t stream)
 {
-    // Items of 8 or of 16 rows: the larger ones where a request's tokens fill them.
-    const long long per_request = a.selected ? 1 : (a.tokens + a.batch - 1) / a.batch;
-    const int tiles = per_request * a.group > 8 ? 2 : 1, rows = 8 * tiles;
+    const bool large = a.selected ? a.group > 8 : nvfp4_large_items(a.tokens, a.batch, a.group);
+    const int tiles = large ? 2 : 1, rows = 8 * tiles;
     a.head_blocks = (a.group + rows - 1) / rows;
     a.block_heads = (a.group + a.head_blocks - 1) / a.head_blocks;
     a.tile_tokens = a.selected || a.group > rows ? 1 : rows / a.group;

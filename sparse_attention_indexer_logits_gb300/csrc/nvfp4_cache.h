@@ -82,10 +82,46 @@ struct NvAttnArgs {
 
 cudaError_t launch_nvfp4_append(const NvAppendArgs& a, cudaStream_t stream);
 cudaError_t launch_nvfp4_read(const NvReadArgs& a, int sm_count, cudaStream_t stream);
-// Lists of k positions for groups of more than eight heads: steps of all warps,
-// and the warps.
-long long nvfp4_list_steps(int k, int group, long long lists);
-int nvfp4_list_warps(int num_ctas);
+// Items of `rows` rows ((token, head) pairs of a kv head: whole tokens, or some of
+// one's heads) for each kv head, the tokens shared out evenly over the requests.
+inline long long nvfp4_items(long long tokens, long long batch, int group, int rows)
+{
+    const long long per = group > rows ? 1 : rows / group, blocks = (group + rows - 1) / rows;
+    const long long full = tokens / batch, more = tokens % batch;      // (`more` requests have one more)
+    return blocks * ((batch - more) * ((full + per - 1) / per) + more * ((full + per) / per));
+}
+
+// Whether warps alone take items of 16 rows, else of 8.  One of 16 takes 1.2 to 1.4
+// times as long: 128 request-heads of 8500 keys, heads of 128, 54 and 44 us; 512 of
+// them, 8 heads to each, 166-172 us for 65 to 128 tokens in items of 16, 121 for 64
+// in items of 8.
+inline bool nvfp4_large_items(long long tokens, long long batch, int group)
+{
+    return 4 * nvfp4_items(tokens, batch, group, 16) < 3 * nvfp4_items(tokens, batch, group, 8);
+}
+
+// Whether a call goes by tiles.  By warps its time is that of its items of 16 rows,
+// by tiles that of a tile for every 128 rows: the same 64 requests with 12 heads,
+// one item a token, 169 us for 64 tokens, 230 for 90, 281 for 110, 317 for 128; by
+// tiles 378-386 for any of them, which is 19/8 items a request.  A call of fewer
+// than 128 rows in all, of which a warp has no more than a step or two, is left to
+// warps: one request-head of 40 or 64 rows 21 us that way and 31 by tiles, 4 of them
+// 23 and 26, 16 of 40 rows 32 and 28.
+inline bool nvfp4_by_tiles(long long tokens, long long batch, int num_heads, int group)
+{
+    return group <= kAttnHalfRows && tokens * num_heads >= 128 && 8 * nvfp4_items(tokens, batch, group, 16) > 19 * batch;
+}
+
+// Lists for groups of more than eight heads, of which 12 warps a CTA take 32
+// positions for 16 heads a step.  Up to 32 heads go that way, and others while a
+// warp has no more than eight steps: 64 heads over 1, 64 tokens of 64 positions 9.2
+// us by warps and 13.9 by tiles, of 500 17.7 and 20.3, of 1500 28.8 and 30.1, of
+// 2048 37.3 and 34.6; 200 tokens of 2048 132 and 83.
+inline bool nvfp4_lists_by_tiles(long long tokens, int num_heads, int group, int k, int num_ctas)
+{
+    const long long steps = tokens * (num_heads / group) * nvfp4_items(1, 1, group, 16) * ((k + 31LL) / 32);
+    return group > 32 && group <= kAttnHalfRows && steps > 8LL * 12 * num_ctas;
+}
 
 // Fills in the items' shape.  `workspace` holds pml_attention_workspace_bytes.
 cudaError_t launch_nvfp4_attention(int head_dim, bool fp16, NvAttnArgs& a, int num_ctas, void* workspace,
