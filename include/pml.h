@@ -535,7 +535,7 @@ int pml_sparse_attention(const void* q, int64_t q_token_stride, int64_t q_head_s
                          void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
- * K/V caches held in 4 bits: a quarter of the memory and traffic of 16 bits.
+ * K/V caches held in 4 bits: 9/32 of the memory and traffic of 16 bits.
  * A row (a token's head of head_dim values, 64 or 128) is head_dim / 2 bytes
  * of E2M1 codes, element d in byte d / 2, the low nibble the even one, and
  * head_dim / 16 E4M3 scales, each of sixteen values, as the rows of

@@ -156,7 +156,6 @@ int attention_call(NvAttnArgs& a, const void* q, int64_t q_token, int64_t q_head
     a.tokens = tokens;
     a.kv_heads = kv_heads;
     a.group = group;
-    a.scale = scale;
     a.scale_log2 = scale * 1.4426950408889634f;
     e = launch_nvfp4_attention(head_dim, fp16, a, dev.sm_count, workspace, workspace_bytes,
                                static_cast<cudaStream_t>(stream));

@@ -76,8 +76,7 @@ struct NvAttnArgs {
     int cluster;                   // > 1: each item is one cluster's of so many CTAs
     int causal;
     int window;                    // > 0: only keys past position - window
-    float scale;                   // softmax scale times the keys' scale
-    float scale_log2;              // the same times log2(e)
+    float scale_log2;              // softmax scale times the keys' scale, times log2(e)
 };
 
 cudaError_t launch_nvfp4_append(const NvAppendArgs& a, cudaStream_t stream);
