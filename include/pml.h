@@ -621,11 +621,11 @@ int pml_read_nvfp4(const pml_nvfp4_cache* k_cache, const pml_nvfp4_cache* v_cach
  * PML_ERR_INVALID_ARG); a row of q that is not finite, or whose scores fp32
  * does not hold, gives a row without meaning.
  * Which way a call goes, and with it its roundings, follows from its sizes.  A
- * request's rows of q to a kv head, its tokens (taken as tokens / batch each, or one
- * more for tokens % batch of them) times num_heads / kv_heads, are items of 16:
- * whole tokens, or some of one's heads.  Calls of up to 19/8 items a request, of
- * fewer than 128 rows in all, and of more than 128 heads to a kv head are taken warp
- * by warp, others in tiles of 128.
+ * request's rows of q to a kv head are its tokens (taken as tokens / batch each, one
+ * more for tokens % batch of them) times num_heads / kv_heads; items are 16 of them:
+ * whole tokens, or some of one's heads.  Calls of up to 32 rows to each request, or
+ * of up to 19/8 items a request, or of fewer than 128 rows in all, and those of more
+ * than 128 heads to a kv head are taken warp by warp, others in tiles of 128.
  */
 int pml_paged_attention_nvfp4(const void* q, int64_t q_token_stride, int64_t q_head_stride, int dtype,
                               const pml_nvfp4_cache* k_cache, const pml_nvfp4_cache* v_cache,

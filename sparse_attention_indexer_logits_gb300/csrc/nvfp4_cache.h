@@ -99,16 +99,20 @@ inline bool nvfp4_large_items(long long tokens, long long batch, int group)
     return 4 * nvfp4_items(tokens, batch, group, 16) < 3 * nvfp4_items(tokens, batch, group, 8);
 }
 
-// Whether a call goes by tiles.  By warps its time is that of its items of 16 rows,
-// by tiles that of a tile for every 128 rows: the same 64 requests with 12 heads,
-// one item a token, 169 us for 64 tokens, 230 for 90, 281 for 110, 317 for 128; by
-// tiles 378-386 for any of them, which is 19/8 items a request.  A call of fewer
-// than 128 rows in all, of which a warp has no more than a step or two, is left to
-// warps: one request-head of 40 or 64 rows 21 us that way and 31 by tiles, 4 of them
-// 23 and 26, 16 of 40 rows 32 and 28.
+// Whether a call goes by tiles: where some request, the tokens shared out evenly,
+// has more than 32 rows, and all of them together more than 19/8 items each.  By
+// warps a call's time is that of its items of 16 rows, by tiles that of a tile for
+// every 128 rows: the same 64 requests with 12 heads, one item a token, 169 us for
+// 64 tokens, 230 for 90, 281 for 110, 317 for 128; by tiles 378-386 for any of them,
+// which is 19/8 items a request.  (Up to 32 rows may be three items too, 5 tokens of
+// 6 heads: 64 requests 485 us and 386, but one over 500 keys 11.5 and 15.2, over
+// 2000 14.0 and 18.1.)  A call of fewer than 128 rows in all, of which a warp has no
+// more than a step or two, is left to warps: one request-head of 40 or 64 rows 21 us
+// that way and 31 by tiles, 4 of them 23 and 26, 16 of 40 rows 32 and 28.
 inline bool nvfp4_by_tiles(long long tokens, long long batch, int num_heads, int group)
 {
-    return group <= kAttnHalfRows && tokens * num_heads >= 128 && 8 * nvfp4_items(tokens, batch, group, 16) > 19 * batch;
+    return group <= kAttnHalfRows && tokens * num_heads >= 128 && (tokens + batch - 1) / batch * group > 32 &&
+           8 * nvfp4_items(tokens, batch, group, 16) > 19 * batch;
 }
 
 // Lists for groups of more than eight heads, of which 12 warps a CTA take 32

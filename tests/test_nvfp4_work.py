@@ -62,22 +62,23 @@ def test_a_few_more_tokens_keep_the_way(W, group, batch, more):
 
 
 def test_equal_batches(W):
-    """Items of 16 for more than 8 rows; warps for one or two of them a request, tiles for three or more."""
+    """Items of 16 for more than 8 rows, tiles for more than 32."""
     for group in range(1, 200):
         for q in (1, 2, 3, 4, 5, 8, 30):
-            n = items(q, 1, group, 16)
-            assert W.by_tiles(64 * q, 64, 8 * group, group) == (n > 2 and group <= 128)
-            assert n <= 2 or q * group > 24
-            if n <= 2 or group > 128:                   # (others go by tiles)
+            tiles = q * group > 32 and group <= 128
+            assert W.by_tiles(64 * q, 64, 8 * group, group) == tiles
+            if not tiles:
                 assert W.large_items(64 * q, 64, group) == (q * group > 8)
 
 
 def test_unequal_batches(W):
     """Where a part of the requests has one more token: items of 16 once they are less
-    than three quarters of those of 8, tiles past 19/8 items a request."""
+    than three quarters of those of 8, tiles past 19/8 items a request and where the
+    longer ones have more than 32 rows."""
     assert [W.large_items(n, 64, 8) for n in (64, 85, 86, 100)] == [0, 0, 1, 1]
     assert [W.by_tiles(n, 64, 160, 20) for n in (64, 65, 76, 77, 100)] == [0, 0, 0, 1, 1]
     assert [W.by_tiles(n, 64, 96, 12) for n in (64, 100, 128, 152, 153)] == [0, 0, 0, 0, 1]
+    assert [W.by_tiles(n, 64, 48, 6) for n in (280, 320, 321)] == [0, 0, 1]
 
 
 def test_calls_of_few_rows(W):
