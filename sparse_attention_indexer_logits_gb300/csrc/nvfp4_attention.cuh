@@ -57,14 +57,16 @@
 //       rows a scheduler has three warps, issues in 46 % of the cycles, and its
 //       matrix unit is as busy: latencies within a step, which more warps (of 128
 //       registers: spills) or items of 32 rows (255 registers, two warps a
-//       scheduler: 88 -> 91) do not shorten
+//       scheduler: 88 -> 91) do not shorten.  (168 registers are all in use then:
+//       64 bytes of stack, 196 of spill stores; lists 56 and 68)
 //   31 requests of 4 tokens over up to 16000 keys, 28 / 4 heads: 85 us, a floor of
 //       21, two items of 14 rows to a key.  (Fourteen warps: 114)
 //   64 tokens x 500 listed positions, 64 heads over 1: 17.7 us, a floor of 0.8; two
 //       steps a warp after a fixed part of 10 us
 //   one token, 4000 keys, 32 heads over 8
 //       12.2 us, eight CTAs to a kv head (15.2 cut over all, with the second
-//       kernel): a launch, first copies and Q 3, joined in the CTA 3-5
+//       kernel, as it also is under a table of more than about 110 pages): a
+//       launch, first copies and Q 3, joined in the CTA 3-5
 // Steps are of 32 keys, a whole number of times in a page: an item's end costs
 // half of what steps of 64 would waste.
 #pragma once
